@@ -200,8 +200,8 @@ def run(s):
 
 
 def _from_pool(t, pool):
-    """The tables with the pointers counted from the pool's start (its address differs from process to process)."""
-    return {**t, "h_table": t["h_table"] - pool.data_ptr()}
+    """The tables with the pointers counted from the pool's start (its address differs from process to process), -1 for none."""
+    return {**t, "h_table": t["h_table"].clamp_min(pool.data_ptr() - 1) - pool.data_ptr()}
 
 
 def _decode(s):
