@@ -331,6 +331,120 @@ int gdn_fold(float* const* h_table, const float* stash, const int32_t* na_tab,
 int gdn_flag_clear(uint32_t* engaged_flag, gdn_stream_t stream);
 
 /* --------------------------------------------------------------------------
+ * gdn_decode -- the recurrent form: new rows of each sequence, state in place.
+ * The token recurrence itself, for callers that add one or a few rows per
+ * sequence and keep every state (a decode step; gdn_verify_woa is the K = 4
+ * form that writes no state).  For each row, with H the live state,
+ *     H <- exp(g) H,  H <- H + beta k (v - H^T k)^T,  o = scale H^T q.
+ * Every state element is read and written once per call, whatever the number
+ * of rows, and the arithmetic is f32.  A call costs about one reduction per
+ * row on top of the state traffic: gdn_chunk_prefill is the form for prompts.
+ *
+ *   h_table    [batch] as for gdn_verify_woa; states 16-byte aligned and
+ *              distinct; a NULL entry marks a padding sequence (its o rows are
+ *              written as zeros, nothing else)
+ *   cu_seqlens [batch + 1] int32 DEVICE array: sequence b owns rows
+ *              cu[b] .. cu[b+1]-1, any number from 0 (the state is then not
+ *              touched); or NULL: one row per sequence (total_rows == batch).
+ *              Offsets are clamped to 0..total_rows on the device; o rows that
+ *              belong to no sequence are left as they were
+ *   q, k       [total_rows, qk_stride] bf16; v [total_rows, v_stride] bf16;
+ *              g, beta [total_rows, gb_stride] f32 (g = -inf forgets the state)
+ *   o          [total_rows, H_v, d_v] bf16 contiguous
+ * Supported: d_k == d_v in {64, 128}, H_v % H_k == 0.
+ * Errors: GDN_ERR_NULL (h_table, q, k, v, g, beta or o NULL; a call without
+ * sequences or rows may leave theirs out), GDN_ERR_SHAPE (also batch < 0, total_rows < 0, no cu_seqlens with total_rows != batch, or
+ * more than 2^31 - 1 CTAs: batch * H_v * d / 32), GDN_ERR_STRIDE,
+ * GDN_ERR_ALIGN (q, k, v or o not 16-byte aligned, or qk_stride, v_stride not
+ * multiples of 8), GDN_ERR_CUDA.  batch == 0 or total_rows == 0 launches
+ * nothing.
+ * ------------------------------------------------------------------------ */
+int gdn_decode(float* const* h_table, const uint16_t* q, const uint16_t* k, int qk_stride,
+               const uint16_t* v, int v_stride, const float* g, const float* beta,
+               int gb_stride, const int32_t* cu_seqlens, uint16_t* o, int batch, int total_rows,
+               int H_k, int H_v, int d_k, int d_v, float scale, gdn_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * gdn_state_tables -- the tables of one engine step, built on the device.
+ * From the new rows of each request and the pool slot of its state: the packed
+ * row offsets that prefill, decode and backward read, the pointer table that
+ * verify, fold and decode read, and maps from rows and 64-row chunks back to
+ * their sequence.  One launch, capturable; the same lengths give the same
+ * tables.
+ *
+ *   lens       [num_seqs] int32, rows of each sequence, >= 0 (a negative length
+ *              counts as 0 and sets GDN_FLAG_ERROR)
+ *   slots      [num_seqs] int32, state slot of each sequence; negative: none
+ *              (its h_table entry is NULL); >= num_slots: NULL and
+ *              GDN_FLAG_ERROR.  NULL array: h_table is not written and
+ *              row_slot must be NULL
+ *   pool       state pool; slot i starts at pool + i * slot_floats
+ *   cu_seqlens [num_seqs + 1] int32: 0, then the running sum of lens
+ *   h_table    [num_seqs] device pointers
+ *   row_seq    [row_capacity] int32: the sequence of each row
+ *   row_slot   [row_capacity] int32: the slot of each row (-1 for none)
+ *   cu_chunks  [num_seqs + 1] int32: 0, then the running sum of ceil(lens / 64)
+ *   chunk_seq  [chunk_capacity] int32: the sequence of each chunk; chunk c of
+ *              sequence b starts at row cu_seqlens[b] + 64 (c - cu_chunks[b])
+ *   flag       u32, GDN_FLAG_ERROR is OR-ed in on the conditions above and
+ *              where the rows or chunks exceed their capacity; or NULL
+ * cu_seqlens, row_seq, row_slot, cu_chunks and chunk_seq may each be NULL (not
+ * written).  Positions of the maps behind the last row or chunk are left as
+ * they were.  Offsets are clamped to row_capacity (cu_chunks to
+ * chunk_capacity), so no later call reads behind the rows; give the capacity
+ * also when the map itself is not wanted.
+ * Errors: GDN_ERR_NULL (lens NULL with num_seqs > 0; slots without pool or
+ * h_table; row_slot without slots), GDN_ERR_SHAPE (num_seqs, num_slots or
+ * slot_floats < 0, a capacity outside 0..2^31-2), GDN_ERR_ALIGN (pool not
+ * 16-byte aligned or slot_floats % 4 != 0), GDN_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+int gdn_state_tables(const int32_t* lens, const int32_t* slots, int num_seqs, float* pool,
+                     long long slot_floats, int num_slots, int32_t* cu_seqlens,
+                     float** h_table, int32_t* row_seq, int32_t* row_slot, int row_capacity,
+                     int32_t* cu_chunks, int32_t* chunk_seq, int chunk_capacity,
+                     uint32_t* flag, gdn_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * gdn_chunk_backward -- gradients of the chunk-parallel prefill.
+ * Given the gradients dout of the outputs and dhT of the final states of
+ *     (o, hT) = gdn_chunk_prefill(q, k, v, g, beta, h0),
+ * the gradients of every input.  Nothing of the forward call is kept: the
+ * chunk states are recomputed here, to f32 accuracy (dg, dbeta and dh0 are
+ * the exact function's gradients to about 1e-6 relative, dq, dk and dv are
+ * rounded once, to bf16).  No atomics: the same inputs give the same bits.
+ *
+ *   q, k, v, g, beta, strides, cu_seqlens, num_seqs, total_tokens, h0, heads,
+ *   scale      as for gdn_chunk_prefill (h0 NULL = zeros); the same bound on
+ *              positive gates (a cumulative rise above 80 within a chunk
+ *              overflows)
+ *   dout       [T, H_v, d_v] bf16 contiguous
+ *   dhT        [num_seqs, H_v, d_k, d_v] f32, or NULL = zeros
+ *   dq, dk     [T, H_k, d_k] bf16 contiguous; summed (in f32) over the value
+ *              heads that share a key head
+ *   dv         [T, H_v, d_v] bf16 contiguous
+ *   dg, dbeta  [T, H_v] f32 contiguous
+ *   dh0        [num_seqs, H_v, d_k, d_v] f32, or NULL (not wanted); may equal
+ *              dhT.  An empty sequence's dh0 is its dhT
+ *   workspace  >= gdn_chunk_backward_workspace_bytes() bytes, 256-byte aligned,
+ *              no two calls in flight at once may share it
+ * Rows that belong to no sequence (behind cu[num_seqs]) are left as they were.
+ * Supported: d_k == d_v in {64, 128}; H_v % H_k == 0, H_v <= 65535.
+ * Errors: as for gdn_chunk_prefill, over the buffers above (GDN_ERR_NULL: q, k,
+ * v, g, beta, cu_seqlens, dout, dq, dk, dv, dg or dbeta NULL; with
+ * total_tokens == 0 only cu_seqlens).  total_tokens == 0 launches nothing
+ * except the copy dhT -> dh0 (zeros without dhT).
+ * ------------------------------------------------------------------------ */
+size_t gdn_chunk_backward_workspace_bytes(int total_tokens, int num_seqs, int H_k, int H_v,
+                                          int d_k, int d_v);
+int gdn_chunk_backward(const uint16_t* q, const uint16_t* k, int qk_stride, const uint16_t* v,
+                       int v_stride, const float* g, const float* beta, int gb_stride,
+                       const int32_t* cu_seqlens, int num_seqs, int total_tokens,
+                       const float* h0, const uint16_t* dout, const float* dhT, uint16_t* dq,
+                       uint16_t* dk, uint16_t* dv, float* dg, float* dbeta, float* dh0, int H_k,
+                       int H_v, int d_k, int d_v, float scale, void* workspace,
+                       size_t workspace_bytes, gdn_stream_t stream);
+
+/* --------------------------------------------------------------------------
  * gdn_debug_device_errors -- diagnostics, not part of the hot path.
  * Copies the library's four device-side error words (BA gates, prefill,
  * verify/fold, reserved) into host memory `out4` and clears them.  Bit 64 of

@@ -9,11 +9,15 @@ from .gdn import (  # noqa: F401
     debug_device_errors,
     debug_set_spin_limit,
     gdn_ba_gates,
+    gdn_chunk_backward,
+    gdn_chunk_backward_workspace_bytes,
     gdn_chunk_prefill,
     gdn_chunk_prefill_workspace_bytes,
+    gdn_decode,
     gdn_flag_clear,
     gdn_fold,
     gdn_stash_seq_floats,
+    gdn_state_tables,
     gdn_verify_parent,
     gdn_verify_woa,
     version,

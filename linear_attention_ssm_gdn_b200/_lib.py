@@ -53,6 +53,13 @@ SIGNATURES = {
                                _I, _F, _P]),
     "gdn_fold": (_I, [_P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "gdn_flag_clear": (_I, [_P, _P]),
+    "gdn_decode": (_I, [_P, _P, _P, _I, _P, _I, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _F,
+                        _P]),
+    "gdn_state_tables": (_I, [_P, _P, _I, _P, ctypes.c_longlong, _I, _P, _P, _P, _P, _I, _P, _P,
+                              _I, _P, _P]),
+    "gdn_chunk_backward_workspace_bytes": (_S, [_I, _I, _I, _I, _I, _I]),
+    "gdn_chunk_backward": (_I, [_P, _P, _I, _P, _I, _P, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P,
+                                _P, _P, _P, _P, _I, _I, _I, _I, _F, _P, _S, _P]),
     "gdn_debug_device_errors": (_I, [_P]),
     "gdn_debug_set_spin_limit": (_I, [ctypes.c_longlong]),
 }

@@ -418,6 +418,158 @@ int gdn_flag_clear(uint32_t* engaged_flag, gdn_stream_t stream) {
                      "gdn_flag_clear");
 }
 
+int gdn_decode(float* const* h_table, const uint16_t* q, const uint16_t* k, int qk_stride,
+               const uint16_t* v, int v_stride, const float* g, const float* beta,
+               int gb_stride, const int32_t* cu_seqlens, uint16_t* o, int batch, int total_rows,
+               int H_k, int H_v, int d_k, int d_v, float scale, gdn_stream_t stream) {
+  const char* fn = "gdn_decode";
+  if (!h_table && batch > 0) return fail(GDN_ERR_NULL, "gdn_decode: null table");
+  if ((!q || !k || !v || !g || !beta || !o) && total_rows > 0)
+    return fail(GDN_ERR_NULL, "gdn_decode: null q/k/v/g/beta/o");
+  int rc = check_heads(fn, H_k, H_v, d_k, d_v);
+  if (rc != GDN_OK) return rc;
+  if (batch < 0 || total_rows < 0)
+    return fail(GDN_ERR_SHAPE, "gdn_decode: batch < 0 or total_rows < 0");
+  if (!cu_seqlens && total_rows != batch)
+    return fail(GDN_ERR_SHAPE, "gdn_decode: total_rows != batch without cu_seqlens");
+  if ((long long)batch * H_v > 0x7fffffffLL / (d_k / 32))
+    return fail(GDN_ERR_SHAPE, "gdn_decode: batch * H_v is too large for one launch");
+  if (qk_stride < H_k * d_k || v_stride < H_v * d_v || gb_stride < H_v)
+    return fail(GDN_ERR_STRIDE, "gdn_decode: a stride is shorter than its row");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o))
+    return fail(GDN_ERR_ALIGN, "gdn_decode: q/k/v/o not 16-byte aligned");
+  if (qk_stride % 8 != 0 || v_stride % 8 != 0)
+    return fail(GDN_ERR_ALIGN, "gdn_decode: qk_stride and v_stride must be multiples of 8");
+  if (batch == 0 || total_rows == 0) {
+    gdn::clear_error();
+    return GDN_OK;
+  }
+  return cuda_status(gdn::launch_decode(h_table, q, k, qk_stride, v, v_stride, g, beta, gb_stride,
+                                        cu_seqlens, o, batch, total_rows, H_k, H_v, d_k, scale,
+                                        reinterpret_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+int gdn_state_tables(const int32_t* lens, const int32_t* slots, int num_seqs, float* pool,
+                     long long slot_floats, int num_slots, int32_t* cu_seqlens,
+                     float** h_table, int32_t* row_seq, int32_t* row_slot, int row_capacity,
+                     int32_t* cu_chunks, int32_t* chunk_seq, int chunk_capacity,
+                     uint32_t* flag, gdn_stream_t stream) {
+  if (num_seqs < 0 || num_slots < 0 || slot_floats < 0)
+    return fail(GDN_ERR_SHAPE, "gdn_state_tables: num_seqs, num_slots or slot_floats < 0");
+  if (row_capacity < 0 || chunk_capacity < 0 || row_capacity == 0x7fffffff ||
+      chunk_capacity == 0x7fffffff)
+    return fail(GDN_ERR_SHAPE, "gdn_state_tables: a capacity is outside 0..2^31-2");
+  if (!lens && num_seqs > 0) return fail(GDN_ERR_NULL, "gdn_state_tables: null lens");
+  if (slots && (!pool || !h_table))
+    return fail(GDN_ERR_NULL, "gdn_state_tables: slots without pool or h_table");
+  if (row_slot && !slots && num_seqs > 0)
+    return fail(GDN_ERR_NULL, "gdn_state_tables: row_slot without slots");
+  if (slots && (!aligned16(pool) || slot_floats % 4 != 0))
+    return fail(GDN_ERR_ALIGN,
+                "gdn_state_tables: pool not 16-byte aligned or slot_floats % 4 != 0");
+  gdn::TablesCall c = {};
+  c.lens = lens;
+  c.slots = slots;
+  c.num_seqs = num_seqs;
+  c.pool = pool;
+  c.slot_floats = slot_floats;
+  c.num_slots = num_slots;
+  c.cu_seqlens = cu_seqlens;
+  c.h_table = h_table;
+  c.row_seq = row_seq;
+  c.row_slot = row_slot;
+  c.row_capacity = row_capacity;
+  c.cu_chunks = cu_chunks;
+  c.chunk_seq = chunk_seq;
+  c.chunk_capacity = chunk_capacity;
+  c.flag = flag;
+  return cuda_status(gdn::launch_tables(c, reinterpret_cast<cudaStream_t>(stream)),
+                     "gdn_state_tables");
+}
+
+size_t gdn_chunk_backward_workspace_bytes(int total_tokens, int num_seqs, int H_k, int H_v,
+                                          int d_k, int d_v) {
+  (void)H_k;
+  (void)d_v;
+  if (total_tokens <= 0 || num_seqs <= 0 || H_v <= 0 || d_k <= 0) return 0;
+  return gdn::backward_workspace_bytes(total_tokens, num_seqs, H_v, d_k);
+}
+
+int gdn_chunk_backward(const uint16_t* q, const uint16_t* k, int qk_stride, const uint16_t* v,
+                       int v_stride, const float* g, const float* beta, int gb_stride,
+                       const int32_t* cu_seqlens, int num_seqs, int total_tokens,
+                       const float* h0, const uint16_t* dout, const float* dhT, uint16_t* dq,
+                       uint16_t* dk, uint16_t* dv, float* dg, float* dbeta, float* dh0, int H_k,
+                       int H_v, int d_k, int d_v, float scale, void* workspace,
+                       size_t workspace_bytes, gdn_stream_t stream) {
+  const char* fn = "gdn_chunk_backward";
+  const std::string f(fn);
+  if (!cu_seqlens) return fail(GDN_ERR_NULL, f + ": null cu_seqlens");
+  if ((!q || !k || !v || !g || !beta || !dout) && total_tokens > 0)
+    return fail(GDN_ERR_NULL, f + ": null q/k/v/g/beta/dout");
+  if ((!dq || !dk || !dv || !dg || !dbeta) && total_tokens > 0)
+    return fail(GDN_ERR_NULL, f + ": null dq/dk/dv/dg/dbeta");
+  int rc = check_heads(fn, H_k, H_v, d_k, d_v);
+  if (rc != GDN_OK) return rc;
+  if (H_v > 65535) return fail(GDN_ERR_SHAPE, f + ": H_v > 65535");
+  if (num_seqs <= 0) return fail(GDN_ERR_SHAPE, f + ": num_seqs must be >= 1");
+  if (total_tokens < 0) return fail(GDN_ERR_SHAPE, f + ": total_tokens < 0");
+  if ((long long)num_seqs * H_v > 0x7fffffffLL / 16)
+    return fail(GDN_ERR_SHAPE, f + ": num_seqs * H_v is too large for one launch");
+  if (qk_stride < H_k * d_k) return fail(GDN_ERR_STRIDE, f + ": qk_stride < H_k*d_k");
+  if (v_stride < H_v * d_v) return fail(GDN_ERR_STRIDE, f + ": v_stride < H_v*d_v");
+  if (gb_stride < H_v) return fail(GDN_ERR_STRIDE, f + ": gb_stride < H_v");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dout) || !aligned16(h0) ||
+      !aligned16(dhT) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(dh0))
+    return fail(GDN_ERR_ALIGN, f + ": q/k/v/dout/h0/dhT/dq/dk/dv/dh0 not 16-byte aligned");
+  if (qk_stride % 8 != 0 || v_stride % 8 != 0)
+    return fail(GDN_ERR_ALIGN, f + ": qk_stride and v_stride must be multiples of 8");
+  const size_t need =
+      gdn_chunk_backward_workspace_bytes(total_tokens, num_seqs, H_k, H_v, d_k, d_v);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
+                   (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+    return fail(GDN_ERR_WORKSPACE, f + ": workspace missing, small or unaligned");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (total_tokens == 0) {
+    if (dh0 != nullptr && dh0 != dhT) {
+      const size_t bytes = size_t(num_seqs) * H_v * d_k * d_v * sizeof(float);
+      return cuda_status(dhT ? cudaMemcpyAsync(dh0, dhT, bytes, cudaMemcpyDeviceToDevice, s)
+                             : cudaMemsetAsync(dh0, 0, bytes, s),
+                         fn);
+    }
+    gdn::clear_error();
+    return GDN_OK;
+  }
+  gdn::BackwardCall c = {};
+  c.q = q;
+  c.k = k;
+  c.v = v;
+  c.dout = dout;
+  c.qk_stride = qk_stride;
+  c.v_stride = v_stride;
+  c.g = g;
+  c.beta = beta;
+  c.gb_stride = gb_stride;
+  c.cu_seqlens = cu_seqlens;
+  c.num_seqs = num_seqs;
+  c.total_tokens = total_tokens;
+  c.h0 = h0;
+  c.dhT = dhT;
+  c.dq = dq;
+  c.dk = dk;
+  c.dv = dv;
+  c.dg = dg;
+  c.dbeta = dbeta;
+  c.dh0 = dh0;
+  c.H_k = H_k;
+  c.H_v = H_v;
+  c.D = d_k;
+  c.scale = scale;
+  c.workspace = workspace;
+  return cuda_status(gdn::launch_backward(c, s), fn);
+}
+
 int gdn_debug_set_spin_limit(long long cycles) {
   if (cycles < 0) return fail(GDN_ERR_SHAPE, "gdn_debug_set_spin_limit: cycles < 0");
   gdn::set_prefill_spin_limit(cycles);

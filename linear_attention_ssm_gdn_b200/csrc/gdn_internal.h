@@ -55,6 +55,35 @@ cudaError_t launch_verify_parent(float* const* h_table, const uint16_t* q, const
                                  float* const* hi_tables, int slab_entries, int batch, int H_k,
                                  int H_v, int D, float scale, cudaStream_t s);
 
+cudaError_t launch_decode(float* const* h_table, const uint16_t* q, const uint16_t* k,
+                          int qk_stride, const uint16_t* v, int v_stride, const float* g,
+                          const float* beta, int gb_stride, const int32_t* cu_seqlens,
+                          uint16_t* o, int batch, int total_rows, int H_k, int H_v, int D,
+                          float scale, cudaStream_t s);
+
+// The step tables (gdn_tables.cu).  Lengths come from `lens`, or from the
+// differences of `cu_in` where lens is NULL; every output may be NULL except
+// h_table when slots is given.
+struct TablesCall {
+  const int32_t* lens;
+  const int32_t* cu_in;     // [num_seqs + 1]
+  const int32_t* slots;     // [num_seqs], or NULL
+  int num_seqs;
+  float* pool;
+  long long slot_floats;
+  int num_slots;
+  int32_t* cu_seqlens;      // [num_seqs + 1]
+  float** h_table;          // [num_seqs]
+  int32_t* row_seq;         // [row_capacity]
+  int32_t* row_slot;        // [row_capacity]
+  int row_capacity;
+  int32_t* cu_chunks;       // [num_seqs + 1]
+  int32_t* chunk_seq;       // [chunk_capacity]
+  int chunk_capacity;
+  uint32_t* flag;
+};
+cudaError_t launch_tables(const TablesCall& c, cudaStream_t s);
+
 // One launch of the chunk-parallel prefill kernel.  The optional per-sequence
 // overrides (seg, h0_tab, hT_tab, v_zero) let the segment-parallel scan run it
 // over segments of the caller's sequences; plain calls leave them NULL / 0.
@@ -97,6 +126,24 @@ cudaError_t launch_prefill_segmented(const PrefillCall& c, int segments, void* w
                                      cudaStream_t s);
 // Segments the library picks on its own for a call (1: the single-level path).
 int prefill_auto_segments(int total_tokens, int num_seqs, int H_v);
+
+// The chunk form's backward pass (gdn_backward.cu).
+struct BackwardCall {
+  const uint16_t *q, *k, *v, *dout;
+  int qk_stride, v_stride;
+  const float *g, *beta;
+  int gb_stride;
+  const int32_t* cu_seqlens;
+  int num_seqs, total_tokens;
+  const float *h0, *dhT;    // [num_seqs, H_v, D, D] or NULL (zeros)
+  uint16_t *dq, *dk, *dv;
+  float *dg, *dbeta, *dh0;  // dh0 may be NULL (not stored)
+  int H_k, H_v, D;
+  float scale;
+  void* workspace;          // >= backward_workspace_bytes(), 256-byte aligned
+};
+size_t backward_workspace_bytes(int total_tokens, int num_seqs, int H_v, int D);
+cudaError_t launch_backward(const BackwardCall& c, cudaStream_t s);
 
 // Device error words (one per kernel family): read and clear (synchronous).
 cudaError_t take_err_ba_gates(uint32_t* out);
