@@ -490,10 +490,9 @@ int gdn_state_tables(const int32_t* lens, const int32_t* slots, int num_seqs, fl
 
 size_t gdn_chunk_backward_workspace_bytes(int total_tokens, int num_seqs, int H_k, int H_v,
                                           int d_k, int d_v) {
-  (void)H_k;
   (void)d_v;
-  if (total_tokens <= 0 || num_seqs <= 0 || H_v <= 0 || d_k <= 0) return 0;
-  return gdn::backward_workspace_bytes(total_tokens, num_seqs, H_v, d_k);
+  if (total_tokens <= 0 || num_seqs <= 0 || H_k <= 0 || H_v <= 0 || d_k <= 0) return 0;
+  return gdn::backward_workspace_bytes(total_tokens, num_seqs, H_k, H_v, d_k);
 }
 
 int gdn_chunk_backward(const uint16_t* q, const uint16_t* k, int qk_stride, const uint16_t* v,

@@ -19,7 +19,25 @@
 //
 // Gates reach the exponentials as differences of 64-bit cumulative sums, kept
 // as two floats: a strong decay early in the chunk costs later rows nothing.
+//
+// Arithmetic.  dg, dbeta and dh0 are f32, so everything they depend on is kept
+// to f32 accuracy; a single bf16 or f16 operand would cost three digits.  Every
+// product runs on the tensor cores in f16 with f32 sums, each f32 operand as
+// two f16 limbs (hi = f16(x s), lo = f16(x s - hi)) under a power-of-two scale s
+// that puts the largest value of its row or tile just below 2^15: 22 bits, or
+// 2^-40 of the largest value, whichever is coarser.  bf16 inputs are exact in
+// one limb under such a scale.  exact x f32 takes 2 MMAs, f32 x f32 takes 3
+// (lo x lo is below the f32 rounding).  What reaches only dq or dk, which are
+// rounded to bf16 (2^-9), takes one limb (2^-12).
+//
+// The MMAs are warp-level (mma.sync m16n8k16).  tcgen05 has four times their
+// rate, but the scans' chains are register-resident here: the state's
+// accumulator fragment is the next product's A fragment, so nothing of the
+// chain passes through tensor or shared memory and no warp waits for another
+// one's product; and splitting a head's value columns over 16-column warps
+// costs no efficiency (M = 16, where tcgen05 wants 128).
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "gdn_device.cuh"
@@ -27,11 +45,13 @@
 
 namespace gdn {
 
-constexpr int kBC = 64;         // rows of a chunk
-constexpr int kScanCols = 32;   // state columns of a scan CTA
+constexpr int kBC = 64;              // rows of a chunk
+constexpr int kBlk = 8192;           // bytes of a [64 rows][64 columns] 16-bit tile block
 constexpr float kGateFloor = -1e4f;  // e^x is 0 in f32 far above it; keeps sums finite
 
-// Where everything is in the workspace (element offsets are 64-bit).
+// Where everything is in the workspace.  16-bit tiles are blocks of 64 columns,
+// rows of 128 bytes, 16-byte pieces XOR-swizzled by row (sw128_offset): a copy
+// brings them into shared memory as the matrix loads want them.
 struct BwdArgs {
   const uint16_t *q, *k, *v, *dout;
   const float *g, *beta;
@@ -43,17 +63,24 @@ struct BwdArgs {
   float *dg, *dbeta, *dh0;
   float scale;
   // workspace
-  int32_t* cu_chunks;   // [num_seqs + 1]
-  int32_t* chunk_seq;   // [max_chunks]
+  int32_t* cu_chunks;  // [num_seqs + 1]
+  int32_t* chunk_seq;  // [max_chunks]
   int max_chunks;
-  float2* G;            // [chunk][H_v][64] cumulative gates, high and low part
-  float* S;             // [chunk][H_v][64][64]
-  float* M;             // [chunk][H_v][64][64]  Q K^T * D, lower with the diagonal
-  float* u;             // [chunk][H_v][64][D]
-  float* E;             // [chunk][H_v][64][D]
-  float* H;             // [chunk + sequence][H_v][D][D] entry states, then the final state
-  float* dH;            // [chunk][H_v][D][D] gradient of the exit state
+  uint8_t* KQ;         // [chunk][H_k] f16 tiles of K, then of Q
+  uint8_t* O;          // [chunk][H_v] f16 tile of dO
+  uint8_t* SM;         // [chunk][H_v] S high, S low, M high, M low (M = Q K^T * D)
+  float* fac;          // [chunk][H_v][kFac]
+  float2* G;           // [chunk][H_v][64] cumulative gates, high and low part
+  float* u;            // [chunk][H_v][64][D]
+  float* E;            // [chunk][H_v][64][D]
+  float* H;            // [chunk + sequence][H_v][D][D] entry states, then the final state
+  float* dH;           // [chunk][H_v][D][D] gradient of the exit state
+  float* Hmax;         // [chunk][H_v][2][D / 16] largest |H| and |dH| of each 16 columns
 };
+
+// Per-unit factors: e^G, e^{G_C - G}, beta of each row, then scalars.
+constexpr int kFac = 3 * kBC + 8;
+enum { kFeC = 3 * kBC, kFinvK, kFinvQ, kFinvO, kFinvS, kFinvM };
 
 __device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(uint32_t(x) << 16); }
 __device__ __forceinline__ float expdiff(float2 a, float2 b) {
@@ -75,334 +102,1107 @@ __device__ __forceinline__ ChunkRows chunk_rows(const BwdArgs& a, int i) {
 }
 
 // ---------------------------------------------------------------------------
-// Prep: per (chunk, value head) G, M and S.
+// Limbs, fragments, MMAs
 // ---------------------------------------------------------------------------
+
+// Power-of-two scale that brings `largest` (>= 0) into [2^14, 2^15), and its
+// inverse.  Zero and what is below 2^-111 take the largest scale; infinity and
+// NaN stay what they are through the split.
+__device__ __forceinline__ float pow2_scale(float largest, float* inverse) {
+  const uint32_t e = max(__float_as_uint(largest) >> 23, 16u);
+  *inverse = __uint_as_float((e - 14u) << 23);
+  return __uint_as_float((268u - e) << 23);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack_f16(a, b);
+  const float2 f = unpack_f16(hi);
+  lo = pack_f16(a - f.x, b - f.y);
+}
+
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                      uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+// Lane address of a 16 x 16 piece at (row, col) of a swizzled tile.  order_rc:
+// the four 8 x 8 matrices run (0,0), (0,8), (8,0), (8,8) -- B fragments of two
+// n-tiles from rows n, columns k (plain) -- else (0,0), (8,0), (0,8), (8,8):
+// A fragments from rows m, columns k (plain), and B fragments of two n-tiles
+// from rows k, columns n (transposed).  An A fragment from rows k, columns m
+// (transposed) takes order_rc.
+template <bool order_rc>
+__device__ __forceinline__ uint32_t piece(uint32_t tile, int row, int col) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  const int r = row + (lane & 7) + (order_rc ? (m >> 1) * 8 : (m & 1) * 8);
+  const int c = col + (order_rc ? (m & 1) * 8 : (m >> 1) * 8);
+  return tile + (c >> 6) * kBlk + sw128_offset(r, (c & 63) * 2);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on = true) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// `bytes` (a multiple of 16 x threads) from global to shared memory.
+template <int THREADS>
+__device__ __forceinline__ void cp_async_block(uint32_t dst, const uint8_t* src, int bytes) {
+  for (int x = threadIdx.x * 16; x < bytes; x += THREADS * 16) cp_async16(dst + x, src + x);
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
+}
+// The larger, NaN if either is (so that a NaN reaches the outputs).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// Prep: per (chunk, value head), what neither scan's state enters: the f16
+// tiles of K, Q and dO, the gate factors, M and S.
+//
+// K K^T and Q K^T are one pass of MMAs each (exact operands).  S is solved in
+// f32 on the CUDA cores: 16-row blocks, the part left of the diagonal block by
+// all 256 threads (column x 4 rows), the diagonal block by one thread per
+// column.  Bound by latency and by the 64-step chain of that solve; several
+// CTAs per SM hide it.
+// ---------------------------------------------------------------------------
+
+// 64 x D bf16 rows (row stride in elements) as an f16 tile: loads, finds the
+// largest value of the tile (into *most, a shared word that was zero) ...
+template <int D>
+struct TileIn {
+  uint4 x[D / 32];
+  __device__ __forceinline__ void load(const uint16_t* src, size_t stride, int rows,
+                                       uint32_t* most) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int p = threadIdx.x + 256 * i, r = p / (D / 8), c = p % (D / 8);
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows) x[i] = *reinterpret_cast<const uint4*>(src + size_t(r) * stride + 8 * c);
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                               __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+    }
+    m = max(m >> 16, m & 0xffffu);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) atomicMax(most, m << 16);
+  }
+  // ... and stores the scaled tile to shared (0: not) and global memory (NULL: not).
+  __device__ __forceinline__ void store(float s, uint32_t tile, uint8_t* out) const {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int p = threadIdx.x + 256 * i, r = p / (D / 8), c = 8 * (p % (D / 8));
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        h[j] = pack_f16(__uint_as_float(w[j] << 16) * s,
+                        __uint_as_float(w[j] & 0xffff0000u) * s);
+      const uint32_t at = (c >> 6) * kBlk + sw128_offset(r, (c & 63) * 2);
+      if (tile != 0) st_shared_v4(tile + at, h[0], h[1], h[2], h[3]);
+      if (out != nullptr) *reinterpret_cast<uint4*>(out + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+};
+
+constexpr int kBT = 68;  // row length of the f32 triangles (16-byte rows)
+
+template <int D>
+struct PrepSmem {
+  static constexpr int kTile = D / 64 * kBlk;
+  static constexpr int K = 0, Q = kTile;       // f16 tiles; later the staged limbs
+  static constexpr int BT = 2 * kTile > 4 * kBlk ? 2 * kTile : 4 * kBlk;  // B transposed
+  static constexpr int S = BT + kBC * kBT * 4;   // S
+  static constexpr int SB = S + kBC * kBT * 4;   // diag(beta) S
+  static constexpr int kBytes = SB + kBC * kBT * 4;
+};
+
 template <int D>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
-  extern __shared__ float sm[];
-  float* Ks = sm;                    // [64][D + 1]
-  float* Qs = Ks + kBC * (D + 1);    // [64][D + 1]
-  float* Bs = Qs + kBC * (D + 1);    // [64][65]
-  float* Ss = Bs + kBC * 65;         // [64][65]
+  using L = PrepSmem<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float2 Gs[kBC];
   __shared__ float bs[kBC];
-  const int i = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  __shared__ uint32_t most[5];  // K, Q, dO, M, S
+  const int i = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
-  const int hk = h / (a.H_v / a.H_k);
+  const int vpg = a.H_v / a.H_k, hk = h / vpg;
   const size_t unit = size_t(i) * a.H_v + h;
-  for (int x = tid; x < kBC * D; x += 256) {
-    const int r = x / D, j = x % D;
-    const size_t at = size_t(c.row0 + r) * a.qk_stride + hk * D + j;
-    Ks[r * (D + 1) + j] = r < c.rows ? bf16f(a.k[at]) : 0.f;
-    Qs[r * (D + 1) + j] = r < c.rows ? bf16f(a.q[at]) : 0.f;
-  }
-  if (tid < kBC) bs[tid] = tid < c.rows ? a.beta[size_t(c.row0 + tid) * a.gb_stride + h] : 0.f;
-  if (tid == 0) {
-    double run = 0.0;
-    for (int r = 0; r < kBC; ++r) {
-      if (r < c.rows) {
-        const float x = a.g[size_t(c.row0 + r) * a.gb_stride + h];
-        run += x < kGateFloor ? kGateFloor : x;
+  const uint32_t base = smem_u32(smem);
+  float* fac = a.fac + unit * kFac;
+  uint8_t* kq = h % vpg == 0 ? a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile : nullptr;
+  if (tid < 5) most[tid] = 0;
+  __syncthreads();
+  {
+    TileIn<D> kt, qt, ot;
+    kt.load(a.k + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows, &most[0]);
+    qt.load(a.q + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows, &most[1]);
+    ot.load(a.dout + (size_t(c.row0) * a.H_v + h) * D, size_t(a.H_v) * D, c.rows, &most[2]);
+    if (warp == 0) {  // two rows per lane; 64-bit sums
+      double x[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 2 * lane + e;
+        float gv = 0.f, bv = 0.f;
+        if (r < c.rows) {
+          gv = a.g[size_t(c.row0 + r) * a.gb_stride + h];
+          bv = a.beta[size_t(c.row0 + r) * a.gb_stride + h];
+        }
+        x[e] = gv < kGateFloor ? kGateFloor : gv;
+        bs[r] = bv;
+        fac[2 * kBC + r] = bv;
       }
-      const float hi = float(run);
-      Gs[r] = make_float2(hi, float(run - double(hi)));
-      a.G[unit * kBC + r] = Gs[r];
-    }
-  }
-  __syncthreads();
-  for (int x = tid; x < kBC * kBC; x += 256) {
-    const int r = x / kBC, s = x % kBC;
-    float kk = 0.f, qk = 0.f;
-    if (s <= r) {
-      for (int j = 0; j < D; ++j) {
-        kk = fmaf(Ks[r * (D + 1) + j], Ks[s * (D + 1) + j], kk);
-        qk = fmaf(Qs[r * (D + 1) + j], Ks[s * (D + 1) + j], qk);
+      x[1] += x[0];
+      double run = x[1];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, run, off);
+        if (lane >= off) run += y;
       }
-      const float e = expdiff(Gs[r], Gs[s]);
-      kk *= e;
-      qk *= e;
+      const double total = __shfl_sync(0xffffffffu, run, 31);
+      x[0] += run - x[1];
+      x[1] = run;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float hi = float(x[e]);
+        const float2 G = make_float2(hi, float(x[e] - double(hi)));
+        Gs[2 * lane + e] = G;
+        a.G[unit * kBC + 2 * lane + e] = G;
+        fac[2 * lane + e] = expf(G.x + G.y);
+        fac[kBC + 2 * lane + e] = expf(float(total - x[e]));
+      }
+      if (lane == 0) fac[kFeC] = expf(float(total));
     }
-    a.M[unit * kBC * kBC + x] = qk;
-    Bs[r * 65 + s] = s < r ? kk : 0.f;
+    __syncthreads();
+    float inv;
+    float s = pow2_scale(__uint_as_float(most[0]), &inv);
+    if (tid == 0) fac[kFinvK] = inv;
+    kt.store(s, base + L::K, kq);
+    s = pow2_scale(__uint_as_float(most[1]), &inv);
+    if (tid == 0) fac[kFinvQ] = inv;
+    qt.store(s, base + L::Q, kq != nullptr ? kq + L::kTile : nullptr);
+    s = pow2_scale(__uint_as_float(most[2]), &inv);
+    if (tid == 0) fac[kFinvO] = inv;
+    ot.store(s, 0, a.O + unit * L::kTile);
   }
   __syncthreads();
-  // S = B - B diag(beta) S, row by row; thread = column
-  if (tid < kBC) {
-    const int j = tid;
-    for (int r = 0; r < kBC; ++r) {
-      float x = Bs[r * 65 + j];
-      for (int s = 0; s < r; ++s) x = fmaf(-Bs[r * 65 + s] * bs[s], Ss[s * 65 + j], x);
-      Ss[r * 65 + j] = x;
+  // Warps 0-3: 16 rows of K K^T each; warps 4-7: of Q K^T.  Lower blocks only.
+  const int rb = warp & 3, g8 = lane >> 2, t2 = 2 * (lane & 3);
+  const bool isq = warp >= 4;
+  float acc[8][4] = {};
+  {
+    const uint32_t ta = base + (isq ? L::Q : L::K);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t av[4];
+      ldsm4(av, piece<false>(ta, 16 * rb, 16 * kk));
+#pragma unroll
+      for (int np = 0; np < 4; ++np)
+        if (np <= rb) {
+          uint32_t bv[4];
+          ldsm4(bv, piece<true>(base + L::K, 16 * np, 16 * kk));
+          mma16(acc[2 * np], av, bv[0], bv[1]);
+          mma16(acc[2 * np + 1], av, bv[2], bv[3]);
+        }
+    }
+  }
+  float* BT = reinterpret_cast<float*>(smem + L::BT);
+  float* S = reinterpret_cast<float*>(smem + L::S);
+  float* SB = reinterpret_cast<float*>(smem + L::SB);
+  float invk, invq;
+  pow2_scale(__uint_as_float(most[0]), &invk);
+  pow2_scale(__uint_as_float(most[1]), &invq);
+  float big = 0.f;
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = 16 * rb + g8 + (e >> 1) * 8, s = 8 * n + t2 + (e & 1);
+      float x = 0.f;
+      if (s <= r) x = acc[n][e] * invk * (isq ? invq : invk) * expdiff(Gs[r], Gs[s]);
+      if (!isq) {
+        if (s >= r) x = 0.f;
+        BT[s * kBT + r] = x;
+        S[r * kBT + s] = x;  // the substitution starts from B
+      }
+      acc[n][e] = x;
+      big = max_nan(big, fabsf(x));
+    }
+  if (isq) {
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    if (lane == 0) atomicMax(&most[3], __float_as_uint(big));
+  }
+  __syncthreads();  // K and Q tiles are free from here
+  if (isq) {
+    float inv;
+    const float s = pow2_scale(__uint_as_float(most[3]), &inv);
+    if (tid == 128) fac[kFinvM] = inv;
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const int r = 16 * rb + g8 + (e >> 1) * 8;
+        uint32_t hi, lo;
+        split_f16(acc[n][e] * s, acc[n][e + 1] * s, hi, lo);
+        const uint32_t at = sw128_offset(r, (8 * n + t2) * 2);
+        *reinterpret_cast<uint32_t*>(smem + 2 * kBlk + at) = hi;
+        *reinterpret_cast<uint32_t*>(smem + 3 * kBlk + at) = lo;
+      }
+  }
+  // S = B - B (diag(beta) S), 16 rows at a time
+  {
+    const int j = tid & 63, p = tid >> 6;
+    for (int b = 0; b < 4; ++b) {
+      if (b > 0) {
+        float x[4];
+        const int r = 16 * b + 4 * p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = S[(r + e) * kBT + j];
+#pragma unroll 8
+        for (int s = 0; s < 16 * b; ++s) {
+          const float sv = SB[s * kBT + j];
+          const float4 b4 = *reinterpret_cast<const float4*>(&BT[s * kBT + r]);
+          x[0] = fmaf(-b4.x, sv, x[0]);
+          x[1] = fmaf(-b4.y, sv, x[1]);
+          x[2] = fmaf(-b4.z, sv, x[2]);
+          x[3] = fmaf(-b4.w, sv, x[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[(r + e) * kBT + j] = x[e];
+        __syncthreads();
+      }
+      if (p == 0) {
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = S[(16 * b + e) * kBT + j];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float sb = bs[16 * b + e] * x[e];
+          SB[(16 * b + e) * kBT + j] = sb;
+#pragma unroll
+          for (int f = e + 1; f < 16; ++f)
+            x[f] = fmaf(-BT[(16 * b + e) * kBT + 16 * b + f], sb, x[f]);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[(16 * b + e) * kBT + j] = x[e];
+      }
+      __syncthreads();
+    }
+  }
+  // S as limbs: 8 pairs a thread
+  float2 sv[8];
+  big = 0.f;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    const int x = tid + 256 * m;
+    sv[m] = *reinterpret_cast<const float2*>(&S[(x >> 5) * kBT + 2 * (x & 31)]);
+    big = max_nan(big, max_nan(fabsf(sv[m].x), fabsf(sv[m].y)));
+  }
+  big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+  if (lane == 0) atomicMax(&most[4], __float_as_uint(big));
+  __syncthreads();
+  {
+    float inv;
+    const float s = pow2_scale(__uint_as_float(most[4]), &inv);
+    if (tid == 0) fac[kFinvS] = inv;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const int x = tid + 256 * m;
+      uint32_t hi, lo;
+      split_f16(sv[m].x * s, sv[m].y * s, hi, lo);
+      const uint32_t at = sw128_offset(x >> 5, 4 * (x & 31));
+      *reinterpret_cast<uint32_t*>(smem + at) = hi;
+      *reinterpret_cast<uint32_t*>(smem + kBlk + at) = lo;
     }
   }
   __syncthreads();
-  for (int x = tid; x < kBC * kBC; x += 256)
-    a.S[unit * kBC * kBC + x] = Ss[(x / kBC) * 65 + x % kBC];
+  uint4* out = reinterpret_cast<uint4*>(a.SM + unit * 4 * kBlk);
+#pragma unroll
+  for (int x = tid; x < 4 * kBlk / 16; x += 256) out[x] = reinterpret_cast<const uint4*>(smem)[x];
 }
 
 // ---------------------------------------------------------------------------
-// Scans: one CTA per (sequence, value head, 32 state columns, direction).
+// Scans: one CTA of 4 warps per (sequence, value head, 64 state columns,
+// direction).  A warp owns 16 columns of H (rows of H^T) for the whole
+// sequence: 16 x D f32 in accumulator fragments, which are also the A fragments
+// of the next chunk's product with K.  Warps share only the chunk's tiles
+// (two cp.async stages); no product crosses a warp.
+//
+// Per chunk and warp 316 (forward) or 484 (backward) MMAs of 8.65 cycles each
+// (measured, m16n8k16 at f32 sums): the chain is bound by its warp's tensor
+// pipe share.
 // ---------------------------------------------------------------------------
+
+// acc[n] (8 tiles of 8 rows r) = sum over d_k of st[dv][dk] K[r][dk], scaled;
+// inv0 / inv1 undo the state rows' scales.  `most` gets the largest |state|.
 template <int D>
-__global__ void __launch_bounds__(128) bwd_scan_kernel(BwdArgs a) {
-  extern __shared__ float sm[];
-  float* Hs = sm;                      // [D][32]
-  float* Ks = Hs + D * kScanCols;      // [64][D]
-  float* Qs = Ks + kBC * D;            // [64][D]
-  float* Xs = Qs + kBC * D;            // [64][32]
-  float* Ss = Xs + kBC * kScanCols;    // [64][64]
-  float* Ms = Ss + kBC * kBC;          // [64][64]
-  float* Os = Ms + kBC * kBC;          // [64][32]
-  __shared__ float eG[kBC], eT[kBC], bs[kBC], eCs;
-  constexpr int SL = D / kScanCols;
-  const int slice = blockIdx.x % SL, h = blockIdx.x / SL % a.H_v, b = blockIdx.x / SL / a.H_v;
-  const bool back = blockIdx.y != 0;
-  const int tid = threadIdx.x, j = tid % 32, w = tid / 32, col = slice * kScanCols + j;
+__device__ __forceinline__ void times_k(const float (&st)[D / 8][4], uint32_t tile,
+                                        float (&acc)[8][4], float* inv0, float* inv1,
+                                        float* most) {
+  float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n) {
+    m0 = max_nan(m0, max_nan(fabsf(st[n][0]), fabsf(st[n][1])));
+    m1 = max_nan(m1, max_nan(fabsf(st[n][2]), fabsf(st[n][3])));
+  }
+  m0 = quad_max(m0), m1 = quad_max(m1);
+  *most = max_nan(m0, m1);
+  const float s0 = pow2_scale(m0, inv0), s1 = pow2_scale(m1, inv1);
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    uint32_t hi[4], lo[4];
+    split_f16(st[2 * kk][0] * s0, st[2 * kk][1] * s0, hi[0], lo[0]);
+    split_f16(st[2 * kk][2] * s1, st[2 * kk][3] * s1, hi[1], lo[1]);
+    split_f16(st[2 * kk + 1][0] * s0, st[2 * kk + 1][1] * s0, hi[2], lo[2]);
+    split_f16(st[2 * kk + 1][2] * s1, st[2 * kk + 1][3] * s1, hi[3], lo[3]);
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      uint32_t b[4];
+      ldsm4(b, piece<true>(tile, 16 * np, 16 * kk));
+      mma16(acc[2 * np], hi, b[0], b[1]);
+      mma16(acc[2 * np + 1], hi, b[2], b[3]);
+      mma16(acc[2 * np], lo, b[0], b[1]);
+      mma16(acc[2 * np + 1], lo, b[2], b[3]);
+    }
+  }
+}
+
+// x[n][e] (columns r = 8 n + ...) times the column factors f, as A limbs of the
+// four 16-row k-steps; the inverse row scales come back in inv0 / inv1.
+__device__ __forceinline__ void limbs_of(const float (&x)[8][4], const float* f,
+                                         uint32_t (&hi)[4][4], uint32_t (&lo)[4][4], float* inv0,
+                                         float* inv1) {
+  const int t2 = 2 * (threadIdx.x & 3);
+  float y[8][4], m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const float2 fv = *reinterpret_cast<const float2*>(f + 8 * n + t2);
+    y[n][0] = x[n][0] * fv.x, y[n][1] = x[n][1] * fv.y;
+    y[n][2] = x[n][2] * fv.x, y[n][3] = x[n][3] * fv.y;
+    m0 = max_nan(m0, max_nan(fabsf(y[n][0]), fabsf(y[n][1])));
+    m1 = max_nan(m1, max_nan(fabsf(y[n][2]), fabsf(y[n][3])));
+  }
+  const float s0 = pow2_scale(quad_max(m0), inv0), s1 = pow2_scale(quad_max(m1), inv1);
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    split_f16(y[2 * kk][0] * s0, y[2 * kk][1] * s0, hi[kk][0], lo[kk][0]);
+    split_f16(y[2 * kk][2] * s1, y[2 * kk][3] * s1, hi[kk][1], lo[kk][1]);
+    split_f16(y[2 * kk + 1][0] * s0, y[2 * kk + 1][1] * s0, hi[kk][2], lo[kk][2]);
+    split_f16(y[2 * kk + 1][2] * s1, y[2 * kk + 1][3] * s1, hi[kk][3], lo[kk][3]);
+  }
+}
+
+// Writes a state (C fragments, rows dv0 + g / g + 8) to the workspace, whose rows
+// hold each 16 columns as four quads (2t, 2t+1, 2t+8, 2t+9): the B fragment of
+// the products that read it.  Lanes g and g ^ 1 trade halves for 16-byte stores.
+template <int D>
+__device__ __forceinline__ void store_state(const float (&st)[D / 8][4], float* out, int dv0) {
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, t2 = 2 * (lane & 3), odd = g8 & 1;
+  float* p = out + size_t(t2 + odd) * D + dv0 + 4 * (g8 >> 1);
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n) {
+    const float x = __shfl_xor_sync(0xffffffffu, odd ? st[n][0] : st[n][1], 4);
+    const float y = __shfl_xor_sync(0xffffffffu, odd ? st[n][2] : st[n][3], 4);
+    *reinterpret_cast<float4*>(p + size_t(8 * n) * D) =
+        odd ? make_float4(x, st[n][1], y, st[n][3]) : make_float4(st[n][0], x, st[n][2], y);
+  }
+}
+
+template <int D, bool back>
+struct ScanSmem {
+  static constexpr int kTile = D / 64 * kBlk;
+  static constexpr int K = 0, Q = kTile;
+  static constexpr int S = back ? 2 * kTile : kTile;  // S high, low (then M high, low)
+  static constexpr int V = S + (back ? 4 : 2) * kBlk;  // V (bf16) or dO (f16), 64 columns
+  static constexpr int kStage = V + kBlk;
+  static constexpr int Fac = 2 * kStage;
+  static constexpr int kBytes = Fac + (3 * kBC + 8 + 2 * kBC) * 4;
+};
+
+template <int D, bool back>
+__device__ __forceinline__ void scan(const BwdArgs& a, int b, int h, int slice, uint8_t* smem) {
+  using L = ScanSmem<D, back>;
+  constexpr int NT = D / 8;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2,
+            t2 = 2 * (lane & 3);
   const int hk = h / (a.H_v / a.H_k);
   const int c0 = a.cu_chunks[b], n = a.cu_chunks[b + 1] - c0;
-  const float* init = back ? a.dhT : a.h0;
+  const int seq_lo = max(a.cu[b], 0), seq_hi = min(a.cu[b + 1], a.total_tokens);
+  const uint32_t base = smem_u32(smem);
+  float* fac = reinterpret_cast<float*>(smem + L::Fac);  // the unit's factors
+  float* mul = fac + kFac;                               // two products of them
+  const int dv0 = 64 * slice + 16 * warp;                // this warp's columns
   const size_t seq_state = (size_t(b) * a.H_v + h) * D * D;
-  for (int x = w; x < D; x += 4)
-    Hs[x * 32 + j] = init != nullptr ? init[seq_state + size_t(x) * D + col] : 0.f;
+
+  auto load = [&](int t) {  // chunk t of this scan into stage t & 1
+    const int i = c0 + (back ? n - 1 - t : t);
+    const size_t unit = size_t(i) * a.H_v + h;
+    const uint32_t st = base + (t & 1) * L::kStage;
+    cp_async_block<128>(st + L::K, a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile,
+                        (back ? 2 : 1) * L::kTile);
+    cp_async_block<128>(st + L::S, a.SM + unit * 4 * kBlk, (back ? 4 : 2) * kBlk);
+    if (back) {
+      cp_async_block<128>(st + L::V, a.O + unit * L::kTile + slice * kBlk, kBlk);
+    } else {
+      const int row0 = seq_lo + kBC * t, rows = max(0, min(kBC, seq_hi - row0));
+      for (int x = tid; x < kBC * 8; x += 128) {
+        const int r = x >> 3, p = x & 7;
+        const uint16_t* src = a.v + h * D + 64 * slice + 8 * p;
+        cp_async16(st + L::V + sw128_offset(r, 16 * p),
+                   r < rows ? src + size_t(row0 + r) * a.v_stride : src, r < rows);
+      }
+    }
+    cp_async_commit();
+  };
+
+  float st[NT][4];
+  const float* init = back ? a.dhT : a.h0;
+#pragma unroll
+  for (int m = 0; m < NT; ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      st[m][e] = init == nullptr ? 0.f
+          : init[seq_state + size_t(8 * m + t2 + (e & 1)) * D + dv0 + g8 + (e >> 1) * 8];
+  if (n > 0) load(0);
   for (int t = 0; t < n; ++t) {
     const int i = c0 + (back ? n - 1 - t : t);
-    const ChunkRows c = chunk_rows(a, i);
     const size_t unit = size_t(i) * a.H_v + h;
-    float* state = back ? a.dH + unit * D * D : a.H + (size_t(i + b) * a.H_v + h) * D * D;
+    if (t + 1 < n)
+      load(t + 1);
+    else
+      cp_async_commit();
+    for (int x = tid; x < kFac; x += 128) fac[x] = a.fac[unit * kFac + x];
+    store_state<D>(st, back ? a.dH + unit * D * D
+                            : a.H + (size_t(i + b) * a.H_v + h) * D * D, dv0);
+    cp_async_wait<1>();
     __syncthreads();
-    for (int x = tid; x < kBC * D; x += 128) {
-      const int r = x / D, d = x % D;
-      const size_t at = size_t(c.row0 + r) * a.qk_stride + hk * D + d;
-      Ks[x] = r < c.rows ? bf16f(a.k[at]) : 0.f;
-      if (back) Qs[x] = r < c.rows ? bf16f(a.q[at]) : 0.f;
-    }
-    for (int x = tid; x < kBC * kBC; x += 128) {
-      Ss[x] = a.S[unit * kBC * kBC + x];
-      if (back) Ms[x] = a.M[unit * kBC * kBC + x];
-    }
-    if (back)
-      for (int r = w; r < kBC; r += 4)
-        Os[r * 32 + j] = r < c.rows
-            ? a.scale * bf16f(a.dout[(size_t(c.row0 + r) * a.H_v + h) * D + col]) : 0.f;
     if (tid < kBC) {
-      const float2 G = a.G[unit * kBC + tid], GC = a.G[unit * kBC + kBC - 1];
-      eG[tid] = expf(G.x + G.y);
-      eT[tid] = expdiff(GC, G);
-      bs[tid] = tid < c.rows ? a.beta[size_t(c.row0 + tid) * a.gb_stride + h] : 0.f;
-      if (tid == 0) eCs = expf(GC.x + GC.y);
+      mul[tid] = fac[2 * kBC + tid] * (back ? fac[tid] : fac[kBC + tid]);  // beta e^G | beta e^T
+      if (back) mul[kBC + tid] = a.scale * fac[tid];
     }
-    for (int x = w; x < D; x += 4) state[size_t(x) * D + col] = Hs[x * 32 + j];
-    __syncthreads();
-    float y[16];
+    const uint32_t stage = base + (t & 1) * L::kStage;
+    float x[8][4], inv0, inv1, most;
+    times_k<D>(st, stage + L::K, x, &inv0, &inv1, &most);
+    most = warp_max(most);
+    if (lane == 0) a.Hmax[(unit * 2 + back) * (D / 16) + dv0 / 16] = most;
+    inv0 *= fac[kFinvK], inv1 *= fac[kFinvK];
+    uint32_t oa[back ? 4 : 1][4];  // backward: dO^T as A fragments
+    if constexpr (!back) {
 #pragma unroll
-    for (int m = 0; m < 16; ++m) {
-      const int r = w * 16 + m;
-      float kh = 0.f;
-      for (int d = 0; d < D; ++d) kh = fmaf(Ks[r * D + d], Hs[d * 32 + j], kh);
-      if (!back) {
-        const float vv = r < c.rows
-            ? bf16f(a.v[size_t(c.row0 + r) * a.v_stride + h * D + col]) : 0.f;
-        y[m] = vv - eG[r] * kh;
-      } else {
-        float acc = eT[r] * kh;
-        for (int s = r; s < kBC; ++s) acc = fmaf(Ms[s * kBC + r], Os[s * 32 + j], acc);
-        y[m] = acc;
+      for (int np = 0; np < 4; ++np) {
+        uint32_t v[4];  // V^T: (dv 0-7, r 0-7), (dv 0-7, r 8-15), (dv 8-15, r 0-7), ...
+        ldsm4t(v, piece<false>(stage + L::V, 16 * np, 16 * warp));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 eg = *reinterpret_cast<const float2*>(fac + 16 * np + 8 * e + t2);
+          float(&y)[4] = x[2 * np + e];
+          const uint32_t v0 = v[e], v1 = v[2 + e];
+          y[0] = fmaf(-eg.x, y[0] * inv0, __uint_as_float(v0 << 16));
+          y[1] = fmaf(-eg.y, y[1] * inv0, __uint_as_float(v0 & 0xffff0000u));
+          y[2] = fmaf(-eg.x, y[2] * inv1, __uint_as_float(v1 << 16));
+          y[3] = fmaf(-eg.y, y[3] * inv1, __uint_as_float(v1 & 0xffff0000u));
+        }
       }
-      Xs[r * 32 + j] = bs[r] * y[m];
-    }
-    __syncthreads();
+    } else {
+      float ma[8][4] = {};
 #pragma unroll
-    for (int m = 0; m < 16; ++m) {
-      const int r = w * 16 + m;
-      if (!back)
-        for (int s = 0; s < r; ++s) y[m] = fmaf(-Ss[r * kBC + s], Xs[s * 32 + j], y[m]);
-      else
-        for (int s = r + 1; s < kBC; ++s) y[m] = fmaf(-Ss[s * kBC + r], Xs[s * 32 + j], y[m]);
-    }
-    __syncthreads();
+      for (int kk = 0; kk < 4; ++kk)
+        ldsm4t(oa[kk], piece<true>(stage + L::V, 16 * kk, 16 * warp));
 #pragma unroll
-    for (int m = 0; m < 16; ++m) {
-      const int r = w * 16 + m;
-      (back ? a.E : a.u)[(unit * kBC + r) * D + col] = y[m];
-      Xs[r * 32 + j] = bs[r] * y[m];
-    }
-    __syncthreads();
-    for (int d = w; d < D; d += 4) {
-      float acc = eCs * Hs[d * 32 + j];
-      for (int r = 0; r < kBC; ++r) {
-        if (!back)
-          acc = fmaf(eT[r] * Ks[r * D + d], Xs[r * 32 + j], acc);
-        else
-          acc = fmaf(eG[r] * Qs[r * D + d], Os[r * 32 + j],
-                     fmaf(-eG[r] * Ks[r * D + d], Xs[r * 32 + j], acc));
+      for (int np = 0; np < 4; ++np)
+#pragma unroll
+        for (int kk = np; kk < 4; ++kk) {
+          uint32_t bh[4], bl[4];
+          ldsm4t(bh, piece<false>(stage + L::S + 2 * kBlk, 16 * kk, 16 * np));
+          ldsm4t(bl, piece<false>(stage + L::S + 3 * kBlk, 16 * kk, 16 * np));
+          mma16(ma[2 * np], oa[kk], bh[0], bh[1]);
+          mma16(ma[2 * np + 1], oa[kk], bh[2], bh[3]);
+          mma16(ma[2 * np], oa[kk], bl[0], bl[1]);
+          mma16(ma[2 * np + 1], oa[kk], bl[2], bl[3]);
+        }
+      const float im = a.scale * fac[kFinvO] * fac[kFinvM];
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const float2 et = *reinterpret_cast<const float2*>(fac + kBC + 8 * m + t2);
+        x[m][0] = fmaf(et.x, x[m][0] * inv0, ma[m][0] * im);
+        x[m][1] = fmaf(et.y, x[m][1] * inv0, ma[m][1] * im);
+        x[m][2] = fmaf(et.x, x[m][2] * inv1, ma[m][2] * im);
+        x[m][3] = fmaf(et.y, x[m][3] * inv1, ma[m][3] * im);
       }
-      Hs[d * 32 + j] = acc;
     }
+    uint32_t hi[4][4], lo[4][4];
+    {
+      // x -= (beta x) S^T (forward) or (beta x) S (backward); S is strictly lower
+      limbs_of(x, fac + 2 * kBC, hi, lo, &inv0, &inv1);
+      inv0 *= fac[kFinvS], inv1 *= fac[kFinvS];
+      float y[8][4] = {};
+#pragma unroll
+      for (int np = 0; np < 4; ++np)
+#pragma unroll
+        for (int kk = back ? np : 0; kk < (back ? 4 : np + 1); ++kk) {
+          uint32_t bh[4], bl[4];
+          if constexpr (back) {
+            ldsm4t(bh, piece<false>(stage + L::S, 16 * kk, 16 * np));
+            ldsm4t(bl, piece<false>(stage + L::S + kBlk, 16 * kk, 16 * np));
+          } else {
+            ldsm4(bh, piece<true>(stage + L::S, 16 * np, 16 * kk));
+            ldsm4(bl, piece<true>(stage + L::S + kBlk, 16 * np, 16 * kk));
+          }
+          mma16(y[2 * np], hi[kk], bh[0], bh[1]);
+          mma16(y[2 * np + 1], hi[kk], bh[2], bh[3]);
+          mma16(y[2 * np], lo[kk], bh[0], bh[1]);
+          mma16(y[2 * np + 1], lo[kk], bh[2], bh[3]);
+          mma16(y[2 * np], hi[kk], bl[0], bl[1]);
+          mma16(y[2 * np + 1], hi[kk], bl[2], bl[3]);
+        }
+      float* out = (back ? a.E : a.u) + unit * kBC * D + dv0 + g8;
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[m][e] = fmaf(-(e < 2 ? inv0 : inv1), y[m][e], x[m][e]);
+          out[size_t(8 * m + t2 + (e & 1)) * D + (e >> 1) * 8] = x[m][e];
+        }
+    }
+    __syncthreads();  // mul
+    limbs_of(x, mul, hi, lo, &inv0, &inv1);
+    inv0 *= fac[kFinvK], inv1 *= fac[kFinvK];
+    uint32_t oh[back ? 4 : 1][4], ol[back ? 4 : 1][4];
+    float jnv0 = 0.f, jnv1 = 0.f;
+    if constexpr (back) {  // e^G scale dO as limbs
+      float y[8][4];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack_f16(oa[kk][e]);
+          y[2 * kk + (e >> 1)][2 * (e & 1)] = f.x;
+          y[2 * kk + (e >> 1)][2 * (e & 1) + 1] = f.y;
+        }
+      limbs_of(y, mul + kBC, oh, ol, &jnv0, &jnv1);
+      jnv0 *= fac[kFinvO], jnv1 *= fac[kFinvO];
+      jnv0 *= fac[kFinvQ], jnv1 *= fac[kFinvQ];
+    }
+    const float eC = fac[kFeC];
+#pragma unroll
+    for (int np = 0; np < D / 16; ++np) {
+      float y[2][4] = {}, z[2][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t bv[4];
+        ldsm4t(bv, piece<false>(stage + L::K, 16 * kk, 16 * np));
+        mma16(y[0], hi[kk], bv[0], bv[1]);
+        mma16(y[1], hi[kk], bv[2], bv[3]);
+        mma16(y[0], lo[kk], bv[0], bv[1]);
+        mma16(y[1], lo[kk], bv[2], bv[3]);
+        if constexpr (back) {
+          ldsm4t(bv, piece<false>(stage + L::Q, 16 * kk, 16 * np));
+          mma16(z[0], oh[kk], bv[0], bv[1]);
+          mma16(z[1], oh[kk], bv[2], bv[3]);
+          mma16(z[0], ol[kk], bv[0], bv[1]);
+          mma16(z[1], ol[kk], bv[2], bv[3]);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float& s = st[2 * np + m][e];
+          s *= eC;
+          s = fmaf(back ? -(e < 2 ? inv0 : inv1) : (e < 2 ? inv0 : inv1), y[m][e], s);
+          if constexpr (back) s = fmaf(e < 2 ? jnv0 : jnv1, z[m][e], s);
+        }
+    }
+    __syncthreads();  // the stage and the factors are free
   }
-  float* last = back ? (a.dh0 != nullptr ? a.dh0 + seq_state : nullptr)
-                     : a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D;
-  if (last != nullptr)
-    for (int x = w; x < D; x += 4) last[size_t(x) * D + col] = Hs[x * 32 + j];
-}
-
-// ---------------------------------------------------------------------------
-// Grads: per (chunk, key head), the value heads of the group one after another.
-// ---------------------------------------------------------------------------
-
-// acc[4][NT] += A[64][K] B[N][K]^T, operands fetched element by element; thread
-// (ty, tx) of 16 x 16 owns rows ty + 16 m and columns tx + 16 n.
-template <int NT, class FA, class FB>
-__device__ __forceinline__ void block_nt(float (&acc)[4][NT], int K, FA fa, FB fb, float* As,
-                                         float* Bt) {
-  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-  for (int k0 = 0; k0 < K; k0 += 32) {
-    __syncthreads();
-    for (int x = tid; x < 64 * 32; x += 256) As[(x / 32) * 33 + x % 32] = fa(x / 32, k0 + x % 32);
-    for (int x = tid; x < 16 * NT * 32; x += 256)
-      Bt[(x / 32) * 33 + x % 32] = fb(x / 32, k0 + x % 32);
-    __syncthreads();
-    for (int kk = 0; kk < 32; ++kk) {
-      float av[4], bv[NT];
+  if (!back) {
+    store_state<D>(st, a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D, dv0);
+  } else if (a.dh0 != nullptr) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) av[m] = As[(ty + 16 * m) * 33 + kk];
+    for (int m = 0; m < NT; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) bv[n] = Bt[(tx + 16 * n) * 33 + kk];
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[m][n] = fmaf(av[m], bv[n], acc[m][n]);
-    }
+      for (int e = 0; e < 4; ++e)
+        a.dh0[seq_state + size_t(8 * m + t2 + (e & 1)) * D + dv0 + g8 + (e >> 1) * 8] = st[m][e];
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) bwd_grads_kernel(BwdArgs a) {
-  constexpr int NT = D / 16;
-  extern __shared__ float sm[];
-  float* As = sm;                 // [64][33]
-  float* Bt = As + 64 * 33;       // [D][33]
-  float* Ps = Bt + D * 33;        // [64][65]
-  float* Ns = Ps + 64 * 65;       // [64][65]
-  __shared__ float eG[kBC], eT[kBC], bs[kBC], dG[kBC];
-  __shared__ float2 Gs[kBC];
-  __shared__ float red[8];
-  const int i = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+__global__ void __launch_bounds__(128) bwd_scan_kernel(BwdArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int SL = D / 64;
+  const int slice = blockIdx.x % SL, h = blockIdx.x / SL % a.H_v, b = blockIdx.x / SL / a.H_v;
+  scan<D, false>(a, b, h, slice, smem);
+}
+template <int D>
+__global__ void __launch_bounds__(128) bwd_scan_back_kernel(BwdArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int SL = D / 64;
+  const int slice = blockIdx.x % SL, h = blockIdx.x / SL % a.H_v, b = blockIdx.x / SL / a.H_v;
+  scan<D, true>(a, b, h, slice, smem);
+}
+
+// ---------------------------------------------------------------------------
+// Grads: one CTA of 8 warps per (chunk, key head), the value heads of the group
+// one after another, so that the shared dq and dk are summed in registers, in
+// one order.
+//
+// A warp owns 16 columns of dq and dk (D = 64: and half of the rows).  The
+// states are its B operand: they are read straight from global memory, once,
+// as the fragments that the scans stored, and split in registers; the row
+// operands (dO, u, E and their scaled forms) are f16 tiles in shared memory.
+// ---------------------------------------------------------------------------
+
+template <int D>
+struct GradsSmem {
+  static constexpr int kTile = D / 64 * kBlk;
+  static constexpr int K = 0, Q = kTile;   // f16 tiles of the chunk
+  static constexpr int O = 2 * kTile;      // dO
+  static constexpr int UH = 3 * kTile, UL = 4 * kTile;  // beta u, two limbs
+  static constexpr int E = 5 * kTile;      // beta E
+  static constexpr int GE = 6 * kTile;     // -e^G beta E
+  static constexpr int DU = 7 * kTile;     // e^{G_C - G} beta u
+  static constexpr int PH = 8 * kTile, PL = PH + kBlk, N = PL + kBlk;
+  static constexpr int F = N + kBlk;       // floats from here
+  static constexpr int kFloats = kFac + 4 * kBC + (D / 16) * kBC + kBC + 16;
+  static constexpr int kBytes = F + kFloats * 4 + kBC * 8;
+};
+
+// A fragments of MT 16-row tiles times two 8-column B tiles.
+template <int MT>
+__device__ __forceinline__ void mma_rows(float (&acc)[MT][2][4], const uint32_t (&av)[MT][4],
+                                         const uint32_t (&b)[4]) {
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    mma16(acc[m][0], av[m], b[0], b[1]);
+    mma16(acc[m][1], av[m], b[2], b[3]);
+  }
+}
+
+// total += f(row) * acc, acc = 0; f gives the factor of a row.
+template <int MT, class F>
+__device__ __forceinline__ void fold_in(float (&total)[MT][2][4], float (&acc)[MT][2][4], F f) {
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float x = f(16 * m + 8 * e);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          total[m][n][2 * e + c] = fmaf(x, acc[m][n][2 * e + c], total[m][n][2 * e + c]);
+          acc[m][n][2 * e + c] = 0.f;
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256, 1) bwd_grads_kernel(BwdArgs a) {
+  using L = GradsSmem<D>;
+  constexpr int CG = D / 16;        // column groups
+  constexpr int MT = D / 32;        // 16-row tiles of a warp: all four, or two
+  constexpr int V = D / 32;         // values of a row per lane in the row pass
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint32_t most[2];      // P, N
+  const uint32_t base = smem_u32(smem);
+  float* fac = reinterpret_cast<float*>(smem + L::F);
+  float *invU = fac + kFac, *invE = invU + kBC, *invGE = invE + kBC, *invDU = invGE + kBC;
+  float* part = invDU + kBC;        // [CG][64] row sums q . dq
+  float* vd = part + CG * kBC;      // [64] v . dv
+  float* red = vd + kBC;            // [8] <H', dH'>
+  float2* Gs = reinterpret_cast<float2*>(red + 16);
+  const int i = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5,
+            lane = tid & 31, g8 = lane >> 2, t2 = 2 * (lane & 3);
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
   const int vpg = a.H_v / a.H_k;
-  auto Kf = [&](int r, int d) {
-    return r < c.rows ? bf16f(a.k[size_t(c.row0 + r) * a.qk_stride + hk * D + d]) : 0.f;
-  };
-  auto Qf = [&](int r, int d) {
-    return r < c.rows ? bf16f(a.q[size_t(c.row0 + r) * a.qk_stride + hk * D + d]) : 0.f;
-  };
-  float dqs[4][NT] = {}, dks[4][NT] = {};
+  const int cg = warp % CG, r0 = (warp / CG) * MT * 16;  // this warp's columns and rows
+  cp_async_block<256>(base + L::K, a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile, 2 * L::kTile);
+  float dqs[MT][2][4] = {}, dks[MT][2][4] = {};
   for (int h = hk * vpg; h < (hk + 1) * vpg; ++h) {
     const size_t unit = size_t(i) * a.H_v + h;
     const float* H = a.H + (size_t(i + c.seq) * a.H_v + h) * D * D;
     const float* H1 = H + size_t(a.H_v) * D * D;
     const float* dH = a.dH + unit * D * D;
-    const float *u = a.u + unit * kBC * D, *E = a.E + unit * kBC * D;
+    cp_async_block<256>(base + L::O, a.O + unit * L::kTile, L::kTile);
+    cp_async_commit();
+    for (int x = tid; x < kFac; x += 256) fac[x] = a.fac[unit * kFac + x];
+    if (tid < kBC) Gs[tid] = a.G[unit * kBC + tid];
+    if (tid < 2) most[tid] = 0;
     __syncthreads();
-    if (tid < kBC) {
-      Gs[tid] = a.G[unit * kBC + tid];
-      const float2 GC = a.G[unit * kBC + kBC - 1];
-      eG[tid] = expf(Gs[tid].x + Gs[tid].y);
-      eT[tid] = expdiff(GC, Gs[tid]);
-      bs[tid] = tid < c.rows ? a.beta[size_t(c.row0 + tid) * a.gb_stride + h] : 0.f;
+    // Rows 8 w .. 8 w + 7: dv, dbeta, v . dv, and the f16 tiles of u and E.
+#pragma unroll 2
+    for (int m = 0; m < 8; ++m) {
+      const int r = 8 * warp + m;
+      float u[V], e[V];
+      const float* up = a.u + (unit * kBC + r) * D + V * lane;
+      const float* ep = a.E + (unit * kBC + r) * D + V * lane;
+      if constexpr (V == 4) {
+        *reinterpret_cast<float4*>(u) = *reinterpret_cast<const float4*>(up);
+        *reinterpret_cast<float4*>(e) = *reinterpret_cast<const float4*>(ep);
+      } else {
+        *reinterpret_cast<float2*>(u) = *reinterpret_cast<const float2*>(up);
+        *reinterpret_cast<float2*>(e) = *reinterpret_cast<const float2*>(ep);
+      }
+      const float bt = fac[2 * kBC + r], eG = fac[r], eT = fac[kBC + r];
+      float db = 0.f, vs = 0.f, mu = 0.f, me = 0.f;
+      uint32_t vw[V / 2] = {};
+      if (r < c.rows) {
+        const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + h * D + V * lane;
+        if constexpr (V == 4)
+          *reinterpret_cast<uint2*>(vw) = *reinterpret_cast<const uint2*>(vp);
+        else
+          vw[0] = *reinterpret_cast<const uint32_t*>(vp);
+      }
+#pragma unroll
+      for (int x = 0; x < V; ++x) {
+        db = fmaf(e[x], u[x], db);
+        u[x] *= bt, e[x] *= bt;
+        vs = fmaf(__uint_as_float(x & 1 ? vw[x / 2] & 0xffff0000u : vw[x / 2] << 16), e[x], vs);
+        mu = max_nan(mu, fabsf(u[x])), me = max_nan(me, fabsf(e[x]));
+      }
+      db = warp_sum(db), vs = warp_sum(vs), mu = warp_max(mu), me = warp_max(me);
+      if (r < c.rows) {
+        uint16_t* dv = a.dv + (size_t(c.row0 + r) * a.H_v + h) * D + V * lane;
+        if constexpr (V == 4)
+          *reinterpret_cast<uint2*>(dv) =
+              make_uint2(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]));
+        else
+          *reinterpret_cast<uint32_t*>(dv) = pack_bf16x2(e[0], e[1]);
+      }
+      float iu, ie, ig, id;
+      const float su = pow2_scale(mu, &iu), se = pow2_scale(me, &ie);
+      const float sg = pow2_scale(eG * me, &ig), sd = pow2_scale(eT * mu, &id);
+      if (lane == 0) {
+        if (r < c.rows) a.dbeta[size_t(c.row0 + r) * a.H_v + h] = db;
+        vd[r] = vs;
+        invU[r] = iu, invE[r] = ie, invGE[r] = ig, invDU[r] = id;
+      }
+      uint32_t uh[V / 2], ul[V / 2], eh[V / 2], gh[V / 2], dh[V / 2];
+#pragma unroll
+      for (int x = 0; x < V / 2; ++x) {
+        const float u0 = u[2 * x], u1 = u[2 * x + 1], e0 = e[2 * x], e1 = e[2 * x + 1];
+        split_f16(u0 * su, u1 * su, uh[x], ul[x]);
+        eh[x] = pack_f16(e0 * se, e1 * se);
+        gh[x] = pack_f16(-eG * e0 * sg, -eG * e1 * sg);
+        dh[x] = pack_f16(eT * u0 * sd, eT * u1 * sd);
+      }
+      const int col = V * lane;
+      uint8_t* at = smem + (col >> 6) * kBlk + sw128_offset(r, (col & 63) * 2);
+      if constexpr (V == 4) {
+        *reinterpret_cast<uint2*>(at + L::UH) = make_uint2(uh[0], uh[1]);
+        *reinterpret_cast<uint2*>(at + L::UL) = make_uint2(ul[0], ul[1]);
+        *reinterpret_cast<uint2*>(at + L::E) = make_uint2(eh[0], eh[1]);
+        *reinterpret_cast<uint2*>(at + L::GE) = make_uint2(gh[0], gh[1]);
+        *reinterpret_cast<uint2*>(at + L::DU) = make_uint2(dh[0], dh[1]);
+      } else {
+        *reinterpret_cast<uint32_t*>(at + L::UH) = uh[0];
+        *reinterpret_cast<uint32_t*>(at + L::UL) = ul[0];
+        *reinterpret_cast<uint32_t*>(at + L::E) = eh[0];
+        *reinterpret_cast<uint32_t*>(at + L::GE) = gh[0];
+        *reinterpret_cast<uint32_t*>(at + L::DU) = dh[0];
+      }
     }
+    cp_async_wait<0>();
     __syncthreads();
-    auto dOf = [&](int r, int d) {
-      return r < c.rows ? bf16f(a.dout[(size_t(c.row0 + r) * a.H_v + h) * D + d]) : 0.f;
-    };
-    auto uf = [&](int r, int d) { return bs[r] * u[r * D + d]; };
-    auto Ef = [&](int r, int d) { return bs[r] * E[r * D + d]; };
+    // P and N: rows 16 (w / 2), columns 32 (w % 2), the lower 16-column blocks
     {
-      float p[4][4] = {}, nn[4][4] = {};
-      block_nt<4>(p, D, dOf, uf, As, Bt);
-      block_nt<4>(nn, D, Ef, uf, As, Bt);
+      const int rb = warp >> 1, ch = warp & 1;
+      float pa[4][4] = {}, na[4][4] = {};
+      if (2 * ch <= rb) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t ao[4], ae[4];
+          ldsm4(ao, piece<false>(base + L::O, 16 * rb, 16 * kk));
+          ldsm4(ae, piece<false>(base + L::E, 16 * rb, 16 * kk));
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int r = ty + 16 * m, s = tx + 16 * n;
-          const float e = s <= r ? expdiff(Gs[r], Gs[s]) : 0.f;
-          Ps[r * 65 + s] = a.scale * p[m][n] * e;
-          Ns[r * 65 + s] = s < r ? -nn[m][n] * e : 0.f;
+          for (int np = 0; np < 2; ++np)
+            if (2 * ch + np <= rb) {
+              uint32_t bh[4], bl[4];
+              ldsm4(bh, piece<true>(base + L::UH, 32 * ch + 16 * np, 16 * kk));
+              ldsm4(bl, piece<true>(base + L::UL, 32 * ch + 16 * np, 16 * kk));
+              mma16(pa[2 * np], ao, bh[0], bh[1]);
+              mma16(pa[2 * np + 1], ao, bh[2], bh[3]);
+              mma16(na[2 * np], ae, bh[0], bh[1]);
+              mma16(na[2 * np + 1], ae, bh[2], bh[3]);
+              mma16(pa[2 * np], ao, bl[0], bl[1]);
+              mma16(pa[2 * np + 1], ao, bl[2], bl[3]);
+            }
+        }
+      }
+      const float io = a.scale * fac[kFinvO];
+      float mp = 0.f, mn = 0.f;
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * rb + g8 + (e >> 1) * 8, s = 32 * ch + 8 * n + t2 + (e & 1);
+          const float d = s <= r ? expdiff(Gs[r], Gs[s]) * invU[s] : 0.f;
+          pa[n][e] = s <= r ? pa[n][e] * io * d : 0.f;
+          na[n][e] = s < r ? -na[n][e] * invE[r] * d : 0.f;
+          mp = max_nan(mp, fabsf(pa[n][e])), mn = max_nan(mn, fabsf(na[n][e]));
+        }
+      const uint32_t up = __reduce_max_sync(0xffffffffu, __float_as_uint(mp));
+      const uint32_t un = __reduce_max_sync(0xffffffffu, __float_as_uint(mn));
+      if (lane == 0) {
+        atomicMax(&most[0], up);
+        atomicMax(&most[1], un);
+      }
+      __syncthreads();
+      float ip, in;
+      const float sp = pow2_scale(__uint_as_float(most[0]), &ip);
+      const float sn = pow2_scale(__uint_as_float(most[1]), &in);
+      if (2 * ch <= rb)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const int r = 16 * rb + g8 + (e >> 1) * 8, s = 32 * ch + 8 * n + t2;
+            uint32_t hi, lo;
+            split_f16(pa[n][e] * sp, pa[n][e + 1] * sp, hi, lo);
+            const uint32_t at = sw128_offset(r, s * 2);
+            *reinterpret_cast<uint32_t*>(smem + L::PH + at) = hi;
+            *reinterpret_cast<uint32_t*>(smem + L::PL + at) = lo;
+            *reinterpret_cast<uint32_t*>(smem + L::N + at) = pack_f16(na[n][e] * sn,
+                                                                      na[n][e + 1] * sn);
+          }
+    }
+    float dq[MT][2][4] = {}, acc[MT][2][4] = {};
+    // dO H^T and -(e^G beta E) H^T
+    {
+      const float* p = a.Hmax + unit * 2 * CG;
+      float m0 = 0.f, m1 = 0.f, ih, id;
+#pragma unroll
+      for (int x = 0; x < CG; ++x) m0 = max_nan(m0, p[x]), m1 = max_nan(m1, p[CG + x]);
+      const float sh = pow2_scale(m0, &ih), sd = pow2_scale(m1, &id);
+      const float* Hp = H + size_t(16 * cg + g8) * D + 2 * t2;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t bh[4], bl[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float4 x = *reinterpret_cast<const float4*>(Hp + size_t(8 * n) * D + 16 * kk);
+          split_f16(x.x * sh, x.y * sh, bh[2 * n], bl[2 * n]);
+          split_f16(x.z * sh, x.w * sh, bh[2 * n + 1], bl[2 * n + 1]);
+        }
+        uint32_t av[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          ldsm4(av[m], piece<false>(base + L::O, r0 + 16 * m, 16 * kk));
+        mma_rows(dq, av, bh);
+        mma_rows(dq, av, bl);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          ldsm4(av[m], piece<false>(base + L::GE, r0 + 16 * m, 16 * kk));
+        mma_rows(acc, av, bh);
+      }
+      fold_in(dks, acc, [&](int r) { return invGE[r0 + r + g8] * ih; });
+      const float f = a.scale * fac[kFinvO] * ih;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dq[m][n][e] *= f * fac[r0 + 16 * m + g8 + (e >> 1) * 8];
+      // (e^{G_C - G} beta u) dH'^T, and <H', dH'> on the way (each value once)
+      const float* Dp = dH + size_t(16 * cg + g8) * D + 2 * t2;
+      const float* H1p = H1 + size_t(16 * cg + g8) * D + 2 * t2;
+      float hh = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t bh[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float4 x = *reinterpret_cast<const float4*>(Dp + size_t(8 * n) * D + 16 * kk);
+          bh[2 * n] = pack_f16(x.x * sd, x.y * sd);
+          bh[2 * n + 1] = pack_f16(x.z * sd, x.w * sd);
+          if (r0 == 0) {
+            const float4 y = *reinterpret_cast<const float4*>(H1p + size_t(8 * n) * D + 16 * kk);
+            hh += fmaf(x.x, y.x, x.y * y.y) + fmaf(x.z, y.z, x.w * y.w);
+          }
+        }
+        uint32_t av[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          ldsm4(av[m], piece<false>(base + L::DU, r0 + 16 * m, 16 * kk));
+        mma_rows(acc, av, bh);
+      }
+      fold_in(dks, acc, [&](int r) { return invDU[r0 + r + g8] * id; });
+      hh = warp_sum(hh);
+      if (lane == 0) red[warp] = hh;
+    }
+    __syncthreads();  // P, N and red
+    {
+      float ip, in;
+      pow2_scale(__uint_as_float(most[0]), &ip);
+      pow2_scale(__uint_as_float(most[1]), &in);
+      const int mt0 = r0 / 16;
+      float ac2[MT][2][4] = {};
+      // P K (two limbs, k-steps up to the diagonal)
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t b[4];
+        ldsm4t(b, piece<false>(base + L::K, 16 * kk, 16 * cg));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          if (kk <= mt0 + m) {
+            uint32_t av[4];
+            ldsm4(av, piece<false>(base + L::PH, r0 + 16 * m, 16 * kk));
+            mma16(acc[m][0], av, b[0], b[1]);
+            mma16(acc[m][1], av, b[2], b[3]);
+            ldsm4(av, piece<false>(base + L::PL, r0 + 16 * m, 16 * kk));
+            mma16(acc[m][0], av, b[0], b[1]);
+            mma16(acc[m][1], av, b[2], b[3]);
+            ldsm4(av, piece<false>(base + L::N, r0 + 16 * m, 16 * kk));
+            mma16(ac2[m][0], av, b[0], b[1]);
+            mma16(ac2[m][1], av, b[2], b[3]);
+          }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          if (kk >= mt0 + m) {  // N^T K
+            uint32_t av[4];
+            ldsm4t(av, piece<true>(base + L::N, 16 * kk, r0 + 16 * m));
+            mma16(ac2[m][0], av, b[0], b[1]);
+            mma16(ac2[m][1], av, b[2], b[3]);
+          }
+      }
+      const float fp = ip * fac[kFinvK], fn = in * fac[kFinvK], fq = ip * fac[kFinvQ];
+      fold_in(dq, acc, [&](int) { return fp; });
+      fold_in(dks, ac2, [&](int) { return fn; });
+      // P^T Q
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t b[4];
+        ldsm4t(b, piece<false>(base + L::Q, 16 * kk, 16 * cg));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          if (kk >= mt0 + m) {
+            uint32_t av[4];
+            ldsm4t(av, piece<true>(base + L::PH, 16 * kk, r0 + 16 * m));
+            mma16(acc[m][0], av, b[0], b[1]);
+            mma16(acc[m][1], av, b[2], b[3]);
+          }
+      }
+      fold_in(dks, acc, [&](int) { return fq; });
+    }
+    // q . dq of this warp's columns, and the group's sum
+    {
+      const float iq = fac[kFinvQ];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = r0 + 16 * m + 8 * e + g8;
+          float x = 0.f;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int col = 16 * cg + 8 * n + t2;
+            const float2 q = unpack_f16(*reinterpret_cast<const uint32_t*>(
+                smem + L::Q + (col >> 6) * kBlk + sw128_offset(r, (col & 63) * 2)));
+            x = fmaf(q.x, dq[m][n][2 * e], fmaf(q.y, dq[m][n][2 * e + 1], x));
+            dqs[m][n][2 * e] += dq[m][n][2 * e];
+            dqs[m][n][2 * e + 1] += dq[m][n][2 * e + 1];
+          }
+          x += __shfl_xor_sync(0xffffffffu, x, 1);
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+          if ((lane & 3) == 0) part[cg * kBC + r] = x * iq;
         }
     }
-    float dq[4][NT] = {};
-    block_nt<NT>(dq, D, dOf, [&](int x, int d) { return H[x * D + d]; }, As, Bt);
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) dq[m][n] *= a.scale * eG[ty + 16 * m];
-    block_nt<NT>(dq, kBC, [&](int r, int s) { return Ps[r * 65 + s]; },
-                 [&](int x, int s) { return Kf(s, x); }, As, Bt);
-    block_nt<NT>(dks, kBC, [&](int r, int s) { return Ps[s * 65 + r]; },
-                 [&](int x, int s) { return Qf(s, x); }, As, Bt);
-    block_nt<NT>(dks, kBC, [&](int r, int s) { return Ns[r * 65 + s] + Ns[s * 65 + r]; },
-                 [&](int x, int s) { return Kf(s, x); }, As, Bt);
-    block_nt<NT>(dks, D, [&](int r, int d) { return -eG[r] * Ef(r, d); },
-                 [&](int x, int d) { return H[x * D + d]; }, As, Bt);
-    block_nt<NT>(dks, D, [&](int r, int d) { return eT[r] * uf(r, d); },
-                 [&](int x, int d) { return dH[x * D + d]; }, As, Bt);
-    // dv, dbeta and dG: a row per warp at a time for the value columns
-    for (int r = tid / 32; r < c.rows; r += 8) {
-      float db = 0.f, vd = 0.f;
-      for (int d = tid % 32; d < D; d += 32) {
-        const float e = E[r * D + d], dv = bs[r] * e;
-        db = fmaf(e, u[r * D + d], db);
-        vd = fmaf(bf16f(a.v[size_t(c.row0 + r) * a.v_stride + h * D + d]), dv, vd);
-        a.dv[(size_t(c.row0 + r) * a.H_v + h) * D + d] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(dv));
-      }
-      for (int off = 16; off > 0; off >>= 1) {
-        db += __shfl_xor_sync(0xffffffffu, db, off);
-        vd += __shfl_xor_sync(0xffffffffu, vd, off);
-      }
-      if (tid % 32 == 0) {
-        a.dbeta[size_t(c.row0 + r) * a.H_v + h] = db;
-        dG[r] = -vd;
-      }
-    }
-    float hh = 0.f;
-    for (int x = tid; x < D * D; x += 256) hh = fmaf(H1[x], dH[x], hh);
-    for (int off = 16; off > 0; off >>= 1) hh += __shfl_xor_sync(0xffffffffu, hh, off);
-    if (tid % 32 == 0) red[tid / 32] = hh;
     __syncthreads();
+    // dg: suffix sums over the rows, two per lane, on top of <H', dH'>
+    if (warp == 0) {
+      double x[2], run;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int r = ty + 16 * m;
-      float x = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        const int r = 63 - (2 * lane + e);
+        float s = 0.f;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        x = fmaf(Qf(r, tx + 16 * n), dq[m][n], x);
-        dqs[m][n] += dq[m][n];
+        for (int w = 0; w < CG; ++w) s += part[w * kBC + r];
+        x[e] = r < c.rows ? double(s) - double(vd[r]) : 0.0;
       }
-      for (int off = 8; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-      if (tx == 0 && r < c.rows) dG[r] += x;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      float run = 0.f;
-      for (int w = 0; w < 8; ++w) run += red[w];
-      for (int r = c.rows - 1; r >= 0; --r) {
-        run += dG[r];
-        a.dg[size_t(c.row0 + r) * a.H_v + h] = run;
+      x[1] += x[0];
+      run = x[1];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, run, off);
+        if (lane >= off) run += y;
+      }
+      double hh = 0.0;
+#pragma unroll
+      for (int w = 0; w < CG; ++w) hh += red[w];
+      x[0] += run - x[1];
+      x[1] = run;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 63 - (2 * lane + e);
+        if (r < c.rows) a.dg[size_t(c.row0 + r) * a.H_v + h] = float(x[e] + hh);
       }
     }
+    __syncthreads();  // the tiles and factors are rewritten for the next head
   }
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = ty + 16 * m;
+    for (int e = 0; e < 2; ++e) {
+      const int r = r0 + 16 * m + 8 * e + g8;
       if (r >= c.rows) continue;
-      const size_t at = (size_t(c.row0 + r) * a.H_k + hk) * D + tx + 16 * n;
-      a.dq[at] = __bfloat16_as_ushort(__float2bfloat16_rn(dqs[m][n]));
-      a.dk[at] = __bfloat16_as_ushort(__float2bfloat16_rn(dks[m][n]));
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const size_t at = (size_t(c.row0 + r) * a.H_k + hk) * D + 16 * cg + 8 * n + t2;
+        *reinterpret_cast<uint32_t*>(a.dq + at) =
+            pack_bf16x2(dqs[m][n][2 * e], dqs[m][n][2 * e + 1]);
+        *reinterpret_cast<uint32_t*>(a.dk + at) =
+            pack_bf16x2(dks[m][n][2 * e], dks[m][n][2 * e + 1]);
+      }
     }
 }
 
@@ -415,9 +1215,9 @@ namespace {
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Lays the workspace out behind `base` (which may be null) and returns its size.
-size_t layout(BwdArgs* a, char* base, int total_tokens, int num_seqs, int H_v, int D) {
+size_t layout(BwdArgs* a, char* base, int total_tokens, int num_seqs, int H_k, int H_v, int D) {
   const size_t mc = size_t(total_tokens / kBC) + size_t(num_seqs);
-  const size_t units = mc * H_v;
+  const size_t units = mc * H_v, tile = size_t(D) / 64 * kBlk;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     char* p = base + at;
@@ -427,44 +1227,50 @@ size_t layout(BwdArgs* a, char* base, int total_tokens, int num_seqs, int H_v, i
   a->max_chunks = int(mc);
   a->cu_chunks = reinterpret_cast<int32_t*>(take((size_t(num_seqs) + 1) * 4));
   a->chunk_seq = reinterpret_cast<int32_t*>(take(mc * 4));
+  a->KQ = reinterpret_cast<uint8_t*>(take(mc * H_k * 2 * tile));
+  a->O = reinterpret_cast<uint8_t*>(take(units * tile));
+  a->SM = reinterpret_cast<uint8_t*>(take(units * 4 * kBlk));
+  a->fac = reinterpret_cast<float*>(take(units * kFac * 4));
   a->G = reinterpret_cast<float2*>(take(units * kBC * 8));
-  a->S = reinterpret_cast<float*>(take(units * kBC * kBC * 4));
-  a->M = reinterpret_cast<float*>(take(units * kBC * kBC * 4));
   a->u = reinterpret_cast<float*>(take(units * kBC * D * 4));
   a->E = reinterpret_cast<float*>(take(units * kBC * D * 4));
   a->H = reinterpret_cast<float*>(take((mc + num_seqs) * size_t(H_v) * D * D * 4));
   a->dH = reinterpret_cast<float*>(take(units * D * D * 4));
+  a->Hmax = reinterpret_cast<float*>(take(units * 2 * (D / 16) * 4));
   return at;
 }
 
 template <int D>
 cudaError_t run(const BwdArgs& a, cudaStream_t s) {
-  const int prep_smem = (2 * kBC * (D + 1) + 2 * kBC * 65) * 4;
-  const int scan_smem = (D * kScanCols + 2 * kBC * D + 2 * kBC * kScanCols + 2 * kBC * kBC) * 4;
-  const int grads_smem = (64 * 33 + D * 33 + 2 * 64 * 65) * 4;
+  constexpr int prep = PrepSmem<D>::kBytes, fwd = ScanSmem<D, false>::kBytes,
+                back = ScanSmem<D, true>::kBytes, grads = GradsSmem<D>::kBytes;
   cudaError_t e;
   const auto kMax = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  if ((e = cudaFuncSetAttribute(bwd_prep_kernel<D>, kMax, prep_smem)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D>, kMax, scan_smem)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(bwd_grads_kernel<D>, kMax, grads_smem)) != cudaSuccess) return e;
-  bwd_prep_kernel<D><<<dim3(a.max_chunks, a.H_v), 256, prep_smem, s>>>(a);
+  if ((e = cudaFuncSetAttribute(bwd_prep_kernel<D>, kMax, prep)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D>, kMax, fwd)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(bwd_scan_back_kernel<D>, kMax, back)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(bwd_grads_kernel<D>, kMax, grads)) != cudaSuccess) return e;
+  bwd_prep_kernel<D><<<dim3(a.max_chunks, a.H_v), 256, prep, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  bwd_scan_kernel<D><<<dim3(a.num_seqs * a.H_v * (D / kScanCols), 2), 128, scan_smem, s>>>(a);
+  const int scans = a.num_seqs * a.H_v * (D / 64);
+  bwd_scan_back_kernel<D><<<scans, 128, back, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  bwd_grads_kernel<D><<<dim3(a.max_chunks, a.H_k), 256, grads_smem, s>>>(a);
+  bwd_scan_kernel<D><<<scans, 128, fwd, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  bwd_grads_kernel<D><<<dim3(a.max_chunks, a.H_k), 256, grads, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t backward_workspace_bytes(int total_tokens, int num_seqs, int H_v, int D) {
+size_t backward_workspace_bytes(int total_tokens, int num_seqs, int H_k, int H_v, int D) {
   BwdArgs a;
-  return layout(&a, nullptr, total_tokens, num_seqs, H_v, D);
+  return layout(&a, nullptr, total_tokens, num_seqs, H_k, H_v, D);
 }
 
 cudaError_t launch_backward(const BackwardCall& c, cudaStream_t s) {
   BwdArgs a;
-  layout(&a, static_cast<char*>(c.workspace), c.total_tokens, c.num_seqs, c.H_v, c.D);
+  layout(&a, static_cast<char*>(c.workspace), c.total_tokens, c.num_seqs, c.H_k, c.H_v, c.D);
   a.q = c.q, a.k = c.k, a.v = c.v, a.dout = c.dout;
   a.g = c.g, a.beta = c.beta;
   a.qk_stride = c.qk_stride, a.v_stride = c.v_stride, a.gb_stride = c.gb_stride;

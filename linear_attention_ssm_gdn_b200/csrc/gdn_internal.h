@@ -142,7 +142,7 @@ struct BackwardCall {
   float scale;
   void* workspace;          // >= backward_workspace_bytes(), 256-byte aligned
 };
-size_t backward_workspace_bytes(int total_tokens, int num_seqs, int H_v, int D);
+size_t backward_workspace_bytes(int total_tokens, int num_seqs, int H_k, int H_v, int D);
 cudaError_t launch_backward(const BackwardCall& c, cudaStream_t s);
 
 // Device error words (one per kernel family): read and clear (synchronous).
