@@ -75,12 +75,14 @@ struct BwdArgs {
   float* E;            // [chunk][H_v][64][D]
   float* H;            // [chunk + sequence][H_v][D][D] entry states, then the final state
   float* dH;           // [chunk][H_v][D][D] gradient of the exit state
-  float* Hmax;         // [chunk][H_v][2][D / 16] largest |H| and |dH| of each 16 columns
+  float* Hmax;         // [chunk][H_v][2][D / 8] largest |H| and |dH| of each scan warp's part
 };
 
-// Per-unit factors: e^G, e^{G_C - G}, beta of each row, then scalars.
-constexpr int kFac = 3 * kBC + 8;
-enum { kFeC = 3 * kBC, kFinvK, kFinvQ, kFinvO, kFinvS, kFinvM };
+// Per-unit factors: of each row e^G, e^{G_C - G}, beta and the products beta
+// e^{G_C - G} and beta e^G, then scalars.
+enum { kFeG = 0, kFeT = kBC, kFbeta = 2 * kBC, kFbT = 3 * kBC, kFbG = 4 * kBC,
+       kFeC = 5 * kBC, kFinvK, kFinvQ, kFinvO, kFinvS, kFinvM };
+constexpr int kFac = 5 * kBC + 8;
 
 __device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(uint32_t(x) << 16); }
 __device__ __forceinline__ float expdiff(float2 a, float2 b) {
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
         }
         x[e] = gv < kGateFloor ? kGateFloor : gv;
         bs[r] = bv;
-        fac[2 * kBC + r] = bv;
+        fac[kFbeta + r] = bv;
       }
       x[1] += x[0];
       double run = x[1];
@@ -312,8 +314,12 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
         const float2 G = make_float2(hi, float(x[e] - double(hi)));
         Gs[2 * lane + e] = G;
         a.G[unit * kBC + 2 * lane + e] = G;
-        fac[2 * lane + e] = expf(G.x + G.y);
-        fac[kBC + 2 * lane + e] = expf(float(total - x[e]));
+        const float eG = expf(G.x + G.y), eT = expf(float(total - x[e]));
+        const float bt = bs[2 * lane + e];
+        fac[kFeG + 2 * lane + e] = eG;
+        fac[kFeT + 2 * lane + e] = eT;
+        fac[kFbT + 2 * lane + e] = bt * eT;
+        fac[kFbG + 2 * lane + e] = bt * eG;
       }
       if (lane == 0) fac[kFeC] = expf(float(total));
     }
@@ -466,38 +472,42 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Scans: one CTA of 4 warps per (sequence, value head, 64 state columns,
-// direction).  A warp owns 16 columns of H (rows of H^T) for the whole
-// sequence: 16 x D f32 in accumulator fragments, which are also the A fragments
-// of the next chunk's product with K.  Warps share only the chunk's tiles
-// (two cp.async stages); no product crosses a warp.
+// Scans: one CTA of 8 warps per (sequence, value head, 64 state columns,
+// direction).  Two warps own 16 columns of H (rows of H^T), each for half of the
+// key rows d_k, for the whole sequence: 8 D f32 in accumulator fragments, which
+// are also the A fragments of the next chunk's product with K.
 //
-// Per chunk and warp 316 (forward) or 484 (backward) MMAs of 8.65 cycles each
-// (measured, m16n8k16 at f32 sums): the chain is bound by its warp's tensor
-// pipe share.
+// A chain of one warp per scheduler was bound by its own latencies (tensor pipe
+// 32 % busy, 6.9 us a chunk backward); two warps a chain halve it.  The pair
+// meets twice a chunk, through shared memory: to add its two halves of K H, and
+// to trade its shares of u (the S product is split by 16-row column blocks 0, 3
+// and 1, 2, which have equal work).  Per chunk and warp 158 (forward) or 242
+// (backward) MMAs of 8.65 cycles (measured, m16n8k16 with f32 sums).
+//
+// The two scans are two kernels that run at the same time (programmatic
+// dependent launch): the backward one, with the longer chain, first.
 // ---------------------------------------------------------------------------
 
-// acc[n] (8 tiles of 8 rows r) = sum over d_k of st[dv][dk] K[r][dk], scaled;
-// inv0 / inv1 undo the state rows' scales.  `most` gets the largest |state|.
-template <int D>
-__device__ __forceinline__ void times_k(const float (&st)[D / 8][4], uint32_t tile,
-                                        float (&acc)[8][4], float* inv0, float* inv1,
-                                        float* most) {
+// acc[n] (8 tiles of 8 rows r) = sum over this warp's d_k of st[dv][dk] K[r][dk],
+// scaled; inv0 / inv1 undo the state rows' scales.  Returns the largest |state|
+// of the thread.
+template <int NT>
+__device__ __forceinline__ float times_k(const float (&st)[NT][4], uint32_t tile, int dk0,
+                                         float (&acc)[8][4], float* inv0, float* inv1) {
   float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-  for (int n = 0; n < D / 8; ++n) {
+  for (int n = 0; n < NT; ++n) {
     m0 = max_nan(m0, max_nan(fabsf(st[n][0]), fabsf(st[n][1])));
     m1 = max_nan(m1, max_nan(fabsf(st[n][2]), fabsf(st[n][3])));
   }
   m0 = quad_max(m0), m1 = quad_max(m1);
-  *most = max_nan(m0, m1);
   const float s0 = pow2_scale(m0, inv0), s1 = pow2_scale(m1, inv1);
 #pragma unroll
   for (int n = 0; n < 8; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
+  for (int kk = 0; kk < NT / 2; ++kk) {
     uint32_t hi[4], lo[4];
     split_f16(st[2 * kk][0] * s0, st[2 * kk][1] * s0, hi[0], lo[0]);
     split_f16(st[2 * kk][2] * s1, st[2 * kk][3] * s1, hi[1], lo[1]);
@@ -506,27 +516,27 @@ __device__ __forceinline__ void times_k(const float (&st)[D / 8][4], uint32_t ti
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       uint32_t b[4];
-      ldsm4(b, piece<true>(tile, 16 * np, 16 * kk));
+      ldsm4(b, piece<true>(tile, 16 * np, dk0 + 16 * kk));
       mma16(acc[2 * np], hi, b[0], b[1]);
       mma16(acc[2 * np + 1], hi, b[2], b[3]);
       mma16(acc[2 * np], lo, b[0], b[1]);
       mma16(acc[2 * np + 1], lo, b[2], b[3]);
     }
   }
+  return max_nan(m0, m1);
 }
 
 // x[n][e] (columns r = 8 n + ...) times the column factors f, as A limbs of the
 // four 16-row k-steps; the inverse row scales come back in inv0 / inv1.
-__device__ __forceinline__ void limbs_of(const float (&x)[8][4], const float* f,
-                                         uint32_t (&hi)[4][4], uint32_t (&lo)[4][4], float* inv0,
-                                         float* inv1) {
+__device__ __forceinline__ void limbs_of(float (&y)[8][4], const float* f, uint32_t (&hi)[4][4],
+                                         uint32_t (&lo)[4][4], float* inv0, float* inv1) {
   const int t2 = 2 * (threadIdx.x & 3);
-  float y[8][4], m0 = 0.f, m1 = 0.f;
+  float m0 = 0.f, m1 = 0.f;
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
     const float2 fv = *reinterpret_cast<const float2*>(f + 8 * n + t2);
-    y[n][0] = x[n][0] * fv.x, y[n][1] = x[n][1] * fv.y;
-    y[n][2] = x[n][2] * fv.x, y[n][3] = x[n][3] * fv.y;
+    y[n][0] *= fv.x, y[n][1] *= fv.y;
+    y[n][2] *= fv.x, y[n][3] *= fv.y;
     m0 = max_nan(m0, max_nan(fabsf(y[n][0]), fabsf(y[n][1])));
     m1 = max_nan(m1, max_nan(fabsf(y[n][2]), fabsf(y[n][3])));
   }
@@ -540,15 +550,42 @@ __device__ __forceinline__ void limbs_of(const float (&x)[8][4], const float* f,
   }
 }
 
+// st = decay st + sign (limbs x the tile's columns dk0 ...), the limbs' rows
+// unscaled by inv0 / inv1.
+template <int NT>
+__device__ __forceinline__ void add_product(float (&st)[NT][4], float decay, float inv0,
+                                            float inv1, const uint32_t (&hi)[4][4],
+                                            const uint32_t (&lo)[4][4], uint32_t tile, int dk0) {
+#pragma unroll
+  for (int np = 0; np < NT / 2; ++np) {
+    float y[2][4] = {};
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t b[4];
+      ldsm4t(b, piece<false>(tile, 16 * kk, dk0 + 16 * np));
+      mma16(y[0], hi[kk], b[0], b[1]);
+      mma16(y[1], hi[kk], b[2], b[3]);
+      mma16(y[0], lo[kk], b[0], b[1]);
+      mma16(y[1], lo[kk], b[2], b[3]);
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        st[2 * np + m][e] = fmaf(e < 2 ? inv0 : inv1, y[m][e], decay * st[2 * np + m][e]);
+  }
+}
+
 // Writes a state (C fragments, rows dv0 + g / g + 8) to the workspace, whose rows
 // hold each 16 columns as four quads (2t, 2t+1, 2t+8, 2t+9): the B fragment of
 // the products that read it.  Lanes g and g ^ 1 trade halves for 16-byte stores.
-template <int D>
-__device__ __forceinline__ void store_state(const float (&st)[D / 8][4], float* out, int dv0) {
+template <int D, int NT>
+__device__ __forceinline__ void store_state(const float (&st)[NT][4], float* out, int dk0,
+                                            int dv0) {
   const int lane = threadIdx.x & 31, g8 = lane >> 2, t2 = 2 * (lane & 3), odd = g8 & 1;
-  float* p = out + size_t(t2 + odd) * D + dv0 + 4 * (g8 >> 1);
+  float* p = out + size_t(dk0 + t2 + odd) * D + dv0 + 4 * (g8 >> 1);
 #pragma unroll
-  for (int n = 0; n < D / 8; ++n) {
+  for (int n = 0; n < NT; ++n) {
     const float x = __shfl_xor_sync(0xffffffffu, odd ? st[n][0] : st[n][1], 4);
     const float y = __shfl_xor_sync(0xffffffffu, odd ? st[n][2] : st[n][3], 4);
     *reinterpret_cast<float4*>(p + size_t(8 * n) * D) =
@@ -556,47 +593,72 @@ __device__ __forceinline__ void store_state(const float (&st)[D / 8][4], float* 
   }
 }
 
+// Shared memory of a scan CTA.  K is needed at both ends of a chunk and has two
+// buffers; what is needed in the middle is loaded over its last use.
 template <int D, bool back>
 struct ScanSmem {
   static constexpr int kTile = D / 64 * kBlk;
-  static constexpr int K = 0, Q = kTile;
-  static constexpr int S = back ? 2 * kTile : kTile;  // S high, low (then M high, low)
-  static constexpr int V = S + (back ? 4 : 2) * kBlk;  // V (bf16) or dO (f16), 64 columns
-  static constexpr int kStage = V + kBlk;
-  static constexpr int Fac = 2 * kStage;
-  static constexpr int kBytes = Fac + (3 * kBC + 8 + 2 * kBC) * 4;
+  static constexpr int K = 0;                      // two buffers
+  static constexpr int S = 2 * kTile;              // S high, low
+  static constexpr int V = S + 2 * kBlk;           // V (bf16) or dO (f16), 64 columns
+  static constexpr int M = V + kBlk;               // backward: M high, low
+  static constexpr int Q = M + (back ? 2 * kBlk : 0);
+  static constexpr int X = Q + (back ? kTile : 0);  // 8 x 4 KB: what the warp pairs trade
+  static constexpr int Fac = X + 8 * 4096;          // two buffers
+  static constexpr int kBytes = Fac + 2 * kFac * 4;
 };
 
 template <int D, bool back>
-__device__ __forceinline__ void scan(const BwdArgs& a, int b, int h, int slice, uint8_t* smem) {
+__global__ void __launch_bounds__(256, 2) bwd_scan_kernel(BwdArgs a) {
   using L = ScanSmem<D, back>;
-  constexpr int NT = D / 8;
+  constexpr int NT = D / 16;  // 8-row tiles of d_k of a warp
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int slice = blockIdx.x % (D / 64), h = blockIdx.x / (D / 64) % a.H_v,
+            b = blockIdx.x / (D / 64) / a.H_v;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2,
             t2 = 2 * (lane & 3);
+  const int rg = warp & 3, hf = warp >> 2;  // 16 columns; half of d_k
   const int hk = h / (a.H_v / a.H_k);
   const int c0 = a.cu_chunks[b], n = a.cu_chunks[b + 1] - c0;
   const int seq_lo = max(a.cu[b], 0), seq_hi = min(a.cu[b + 1], a.total_tokens);
   const uint32_t base = smem_u32(smem);
-  float* fac = reinterpret_cast<float*>(smem + L::Fac);  // the unit's factors
-  float* mul = fac + kFac;                               // two products of them
-  const int dv0 = 64 * slice + 16 * warp;                // this warp's columns
+  const int dv0 = 64 * slice + 16 * rg, dk0 = hf * (D / 2);
   const size_t seq_state = (size_t(b) * a.H_v + h) * D * D;
+  float4* mine = reinterpret_cast<float4*>(smem + L::X + warp * 4096) + lane;
+  float4* other = reinterpret_cast<float4*>(smem + L::X + (warp ^ 4) * 4096) + lane;
+  if constexpr (back) asm volatile("griddepcontrol.launch_dependents;");
 
-  auto load = [&](int t) {  // chunk t of this scan into stage t & 1
-    const int i = c0 + (back ? n - 1 - t : t);
-    const size_t unit = size_t(i) * a.H_v + h;
-    const uint32_t st = base + (t & 1) * L::kStage;
-    cp_async_block<128>(st + L::K, a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile,
-                        (back ? 2 : 1) * L::kTile);
-    cp_async_block<128>(st + L::S, a.SM + unit * 4 * kBlk, (back ? 4 : 2) * kBlk);
-    if (back) {
-      cp_async_block<128>(st + L::V, a.O + unit * L::kTile + slice * kBlk, kBlk);
-    } else {
+  auto chunk_of = [&](int t) { return c0 + (back ? n - 1 - t : t); };
+  auto load_k = [&](int t) {  // K and the factors
+    const int i = chunk_of(t);
+    cp_async_block<256>(base + L::K + (t & 1) * L::kTile,
+                        a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile, L::kTile);
+    if (tid < kFac / 4)
+      cp_async16(base + L::Fac + (t & 1) * kFac * 4 + tid * 16,
+                 a.fac + (size_t(i) * a.H_v + h) * kFac + tid * 4);
+    cp_async_commit();
+  };
+  auto load_early = [&](int t) {  // backward: what is read before the first meeting
+    if constexpr (back) {
+      const int i = chunk_of(t);
+      const size_t unit = size_t(i) * a.H_v + h;
+      cp_async_block<256>(base + L::Q, a.KQ + ((size_t(i) * a.H_k + hk) * 2 + 1) * L::kTile,
+                          L::kTile);
+      cp_async_block<256>(base + L::M, a.SM + (unit * 4 + 2) * kBlk, 2 * kBlk);
+      cp_async_block<256>(base + L::V, a.O + unit * L::kTile + slice * kBlk, kBlk);
+    }
+    cp_async_commit();
+  };
+  auto load_late = [&](int t) {  // what is read between the meetings
+    const size_t unit = size_t(chunk_of(t)) * a.H_v + h;
+    cp_async_block<256>(base + L::S, a.SM + unit * 4 * kBlk, 2 * kBlk);
+    if constexpr (!back) {
       const int row0 = seq_lo + kBC * t, rows = max(0, min(kBC, seq_hi - row0));
-      for (int x = tid; x < kBC * 8; x += 128) {
-        const int r = x >> 3, p = x & 7;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int r = (tid >> 3) + 32 * m, p = tid & 7;
         const uint16_t* src = a.v + h * D + 64 * slice + 8 * p;
-        cp_async16(st + L::V + sw128_offset(r, 16 * p),
+        cp_async16(base + L::V + sw128_offset(r, 16 * p),
                    r < rows ? src + size_t(row0 + r) * a.v_stride : src, r < rows);
       }
     }
@@ -610,183 +672,187 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int b, int h, int slice, 
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       st[m][e] = init == nullptr ? 0.f
-          : init[seq_state + size_t(8 * m + t2 + (e & 1)) * D + dv0 + g8 + (e >> 1) * 8];
-  if (n > 0) load(0);
-  for (int t = 0; t < n; ++t) {
-    const int i = c0 + (back ? n - 1 - t : t);
-    const size_t unit = size_t(i) * a.H_v + h;
-    if (t + 1 < n)
-      load(t + 1);
-    else
-      cp_async_commit();
-    for (int x = tid; x < kFac; x += 128) fac[x] = a.fac[unit * kFac + x];
-    store_state<D>(st, back ? a.dH + unit * D * D
-                            : a.H + (size_t(i + b) * a.H_v + h) * D * D, dv0);
+          : init[seq_state + size_t(dk0 + 8 * m + t2 + (e & 1)) * D + dv0 + g8 + (e >> 1) * 8];
+  if (n > 0) {
+    load_k(0);
+    load_early(0);
+    load_late(0);
     cp_async_wait<1>();
     __syncthreads();
-    if (tid < kBC) {
-      mul[tid] = fac[2 * kBC + tid] * (back ? fac[tid] : fac[kBC + tid]);  // beta e^G | beta e^T
-      if (back) mul[kBC + tid] = a.scale * fac[tid];
-    }
-    const uint32_t stage = base + (t & 1) * L::kStage;
-    float x[8][4], inv0, inv1, most;
-    times_k<D>(st, stage + L::K, x, &inv0, &inv1, &most);
-    most = warp_max(most);
-    if (lane == 0) a.Hmax[(unit * 2 + back) * (D / 16) + dv0 / 16] = most;
+  }
+  for (int t = 0; t < n; ++t) {
+    const int i = chunk_of(t);
+    const size_t unit = size_t(i) * a.H_v + h;
+    const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (t & 1) * kFac;
+    const uint32_t tk = base + L::K + (t & 1) * L::kTile;
+    if (t + 1 < n)
+      load_k(t + 1);
+    else
+      cp_async_commit();
+    const float eC = fac[kFeC];
+    float x[8][4], inv0, inv1;
+    float most = times_k<NT>(st, tk, dk0, x, &inv0, &inv1);
     inv0 *= fac[kFinvK], inv1 *= fac[kFinvK];
-    uint32_t oa[back ? 4 : 1][4];  // backward: dO^T as A fragments
+    uint32_t hi[4][4], lo[4][4];
     if constexpr (!back) {
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t v[4];  // V^T: (dv 0-7, r 0-7), (dv 0-7, r 8-15), (dv 8-15, r 0-7), ...
-        ldsm4t(v, piece<false>(stage + L::V, 16 * np, 16 * warp));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 eg = *reinterpret_cast<const float2*>(fac + 16 * np + 8 * e + t2);
-          float(&y)[4] = x[2 * np + e];
-          const uint32_t v0 = v[e], v1 = v[2 + e];
-          y[0] = fmaf(-eg.x, y[0] * inv0, __uint_as_float(v0 << 16));
-          y[1] = fmaf(-eg.y, y[1] * inv0, __uint_as_float(v0 & 0xffff0000u));
-          y[2] = fmaf(-eg.x, y[2] * inv1, __uint_as_float(v1 << 16));
-          y[3] = fmaf(-eg.y, y[3] * inv1, __uint_as_float(v1 & 0xffff0000u));
-        }
-      }
+      for (int m = 0; m < 8; ++m)
+        mine[32 * m] = make_float4(x[m][0] * inv0, x[m][1] * inv0, x[m][2] * inv1, x[m][3] * inv1);
+      store_state<D, NT>(st, a.H + (size_t(i + b) * a.H_v + h) * D * D, dk0, dv0);
     } else {
-      float ma[8][4] = {};
+      uint32_t oa[4][4];  // dO^T as A fragments
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        ldsm4t(oa[kk], piece<true>(stage + L::V, 16 * kk, 16 * warp));
+      for (int kk = 0; kk < 4; ++kk) ldsm4t(oa[kk], piece<true>(base + L::V, 16 * kk, 16 * rg));
+      float ma[4][4] = {};  // this warp's two 16-row blocks of M^T dO
 #pragma unroll
-      for (int np = 0; np < 4; ++np)
+      for (int j = 0; j < 2; ++j) {
+        const int np = hf ? 1 + j : 3 * j;
 #pragma unroll
-        for (int kk = np; kk < 4; ++kk) {
-          uint32_t bh[4], bl[4];
-          ldsm4t(bh, piece<false>(stage + L::S + 2 * kBlk, 16 * kk, 16 * np));
-          ldsm4t(bl, piece<false>(stage + L::S + 3 * kBlk, 16 * kk, 16 * np));
-          mma16(ma[2 * np], oa[kk], bh[0], bh[1]);
-          mma16(ma[2 * np + 1], oa[kk], bh[2], bh[3]);
-          mma16(ma[2 * np], oa[kk], bl[0], bl[1]);
-          mma16(ma[2 * np + 1], oa[kk], bl[2], bl[3]);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk >= np) {
+            uint32_t bh[4], bl[4];
+            ldsm4t(bh, piece<false>(base + L::M, 16 * kk, 16 * np));
+            ldsm4t(bl, piece<false>(base + L::M + kBlk, 16 * kk, 16 * np));
+            mma16(ma[2 * j], oa[kk], bh[0], bh[1]);
+            mma16(ma[2 * j + 1], oa[kk], bh[2], bh[3]);
+            mma16(ma[2 * j], oa[kk], bl[0], bl[1]);
+            mma16(ma[2 * j + 1], oa[kk], bl[2], bl[3]);
+          }
+      }
       const float im = a.scale * fac[kFinvO] * fac[kFinvM];
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
-        const float2 et = *reinterpret_cast<const float2*>(fac + kBC + 8 * m + t2);
-        x[m][0] = fmaf(et.x, x[m][0] * inv0, ma[m][0] * im);
-        x[m][1] = fmaf(et.y, x[m][1] * inv0, ma[m][1] * im);
-        x[m][2] = fmaf(et.x, x[m][2] * inv1, ma[m][2] * im);
-        x[m][3] = fmaf(et.y, x[m][3] * inv1, ma[m][3] * im);
+        const float2 et = *reinterpret_cast<const float2*>(fac + kFeT + 8 * m + t2);
+        const int j = m < 2 || m >= 6 ? (m & 1) + (m >= 6 ? 2 : 0) : m - 2;
+        const float f = ((m < 2 || m >= 6) == (hf == 0)) ? im : 0.f;
+        mine[32 * m] = make_float4(
+            fmaf(et.x, x[m][0] * inv0, ma[j][0] * f), fmaf(et.y, x[m][1] * inv0, ma[j][1] * f),
+            fmaf(et.x, x[m][2] * inv1, ma[j][2] * f), fmaf(et.y, x[m][3] * inv1, ma[j][3] * f));
       }
-    }
-    uint32_t hi[4][4], lo[4][4];
-    {
-      // x -= (beta x) S^T (forward) or (beta x) S (backward); S is strictly lower
-      limbs_of(x, fac + 2 * kBC, hi, lo, &inv0, &inv1);
-      inv0 *= fac[kFinvS], inv1 *= fac[kFinvS];
-      float y[8][4] = {};
-#pragma unroll
-      for (int np = 0; np < 4; ++np)
-#pragma unroll
-        for (int kk = back ? np : 0; kk < (back ? 4 : np + 1); ++kk) {
-          uint32_t bh[4], bl[4];
-          if constexpr (back) {
-            ldsm4t(bh, piece<false>(stage + L::S, 16 * kk, 16 * np));
-            ldsm4t(bl, piece<false>(stage + L::S + kBlk, 16 * kk, 16 * np));
-          } else {
-            ldsm4(bh, piece<true>(stage + L::S, 16 * np, 16 * kk));
-            ldsm4(bl, piece<true>(stage + L::S + kBlk, 16 * np, 16 * kk));
-          }
-          mma16(y[2 * np], hi[kk], bh[0], bh[1]);
-          mma16(y[2 * np + 1], hi[kk], bh[2], bh[3]);
-          mma16(y[2 * np], lo[kk], bh[0], bh[1]);
-          mma16(y[2 * np + 1], lo[kk], bh[2], bh[3]);
-          mma16(y[2 * np], hi[kk], bl[0], bl[1]);
-          mma16(y[2 * np + 1], hi[kk], bl[2], bl[3]);
-        }
-      float* out = (back ? a.E : a.u) + unit * kBC * D + dv0 + g8;
-#pragma unroll
-      for (int m = 0; m < 8; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[m][e] = fmaf(-(e < 2 ? inv0 : inv1), y[m][e], x[m][e]);
-          out[size_t(8 * m + t2 + (e & 1)) * D + (e >> 1) * 8] = x[m][e];
-        }
-    }
-    __syncthreads();  // mul
-    limbs_of(x, mul, hi, lo, &inv0, &inv1);
-    inv0 *= fac[kFinvK], inv1 *= fac[kFinvK];
-    uint32_t oh[back ? 4 : 1][4], ol[back ? 4 : 1][4];
-    float jnv0 = 0.f, jnv1 = 0.f;
-    if constexpr (back) {  // e^G scale dO as limbs
-      float y[8][4];
+      store_state<D, NT>(st, a.dH + unit * D * D, dk0, dv0);
+      // e^{G_C} dH' + scale (e^G Q)^T dO, while the other warps arrive
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f = unpack_f16(oa[kk][e]);
-          y[2 * kk + (e >> 1)][2 * (e & 1)] = f.x;
-          y[2 * kk + (e >> 1)][2 * (e & 1) + 1] = f.y;
+          x[2 * kk + (e >> 1)][2 * (e & 1)] = f.x;
+          x[2 * kk + (e >> 1)][2 * (e & 1) + 1] = f.y;
         }
-      limbs_of(y, mul + kBC, oh, ol, &jnv0, &jnv1);
-      jnv0 *= fac[kFinvO], jnv1 *= fac[kFinvO];
-      jnv0 *= fac[kFinvQ], jnv1 *= fac[kFinvQ];
+      limbs_of(x, fac + kFeG, hi, lo, &inv0, &inv1);
+      const float f = a.scale * fac[kFinvO];
+      inv0 *= f, inv1 *= f;
+      inv0 *= fac[kFinvQ], inv1 *= fac[kFinvQ];
+      add_product<NT>(st, eC, inv0, inv1, hi, lo, base + L::Q, dk0);
     }
-    const float eC = fac[kFeC];
+    most = warp_max(most);
+    if (lane == 0) a.Hmax[(unit * 2 + back) * (D / 8) + 2 * (dv0 / 16) + hf] = most;
+    cp_async_wait<1>();  // S (and V) of this chunk
+    __syncthreads();
+    if (t + 1 < n)
+      load_early(t + 1);
+    else
+      cp_async_commit();
 #pragma unroll
-    for (int np = 0; np < D / 16; ++np) {
-      float y[2][4] = {}, z[2][4] = {};
+    for (int m = 0; m < 8; ++m) {
+      const float4 p = mine[32 * m], q = other[32 * m];
+      x[m][0] = p.x + q.x, x[m][1] = p.y + q.y, x[m][2] = p.z + q.z, x[m][3] = p.w + q.w;
+    }
+    named_sync(1 + rg, 64);  // both have read both slots: they are free for u
+    if constexpr (!back) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        uint32_t bv[4];
-        ldsm4t(bv, piece<false>(stage + L::K, 16 * kk, 16 * np));
-        mma16(y[0], hi[kk], bv[0], bv[1]);
-        mma16(y[1], hi[kk], bv[2], bv[3]);
-        mma16(y[0], lo[kk], bv[0], bv[1]);
-        mma16(y[1], lo[kk], bv[2], bv[3]);
-        if constexpr (back) {
-          ldsm4t(bv, piece<false>(stage + L::Q, 16 * kk, 16 * np));
-          mma16(z[0], oh[kk], bv[0], bv[1]);
-          mma16(z[1], oh[kk], bv[2], bv[3]);
-          mma16(z[0], ol[kk], bv[0], bv[1]);
-          mma16(z[1], ol[kk], bv[2], bv[3]);
+      for (int np = 0; np < 4; ++np) {
+        uint32_t v[4];  // V^T: (dv 0-7, r 0-7), (dv 0-7, r 8-15), (dv 8-15, r 0-7), ...
+        ldsm4t(v, piece<false>(base + L::V, 16 * np, 16 * rg));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 eg = *reinterpret_cast<const float2*>(fac + kFeG + 16 * np + 8 * e + t2);
+          float(&y)[4] = x[2 * np + e];
+          const uint32_t v0 = v[e], v1 = v[2 + e];
+          y[0] = fmaf(-eg.x, y[0], __uint_as_float(v0 << 16));
+          y[1] = fmaf(-eg.y, y[1], __uint_as_float(v0 & 0xffff0000u));
+          y[2] = fmaf(-eg.x, y[2], __uint_as_float(v1 << 16));
+          y[3] = fmaf(-eg.y, y[3], __uint_as_float(v1 & 0xffff0000u));
         }
       }
+    }
+    {
+      // u = X - (beta X) S^T, E = Y - (beta Y) S: this warp's two 16-row blocks
+      float w[4][4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[j][e] = hf ? x[2 + j][e] : x[j < 2 ? j : 4 + j][e];
+      limbs_of(x, fac + kFbeta, hi, lo, &inv0, &inv1);
+      inv0 *= fac[kFinvS], inv1 *= fac[kFinvS];
+      float y[4][4] = {};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int np = hf ? 1 + j : 3 * j;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (back ? kk >= np : kk <= np) {
+            uint32_t bh[4], bl[4];
+            if constexpr (back) {
+              ldsm4t(bh, piece<false>(base + L::S, 16 * kk, 16 * np));
+              ldsm4t(bl, piece<false>(base + L::S + kBlk, 16 * kk, 16 * np));
+            } else {
+              ldsm4(bh, piece<true>(base + L::S, 16 * np, 16 * kk));
+              ldsm4(bl, piece<true>(base + L::S + kBlk, 16 * np, 16 * kk));
+            }
+            mma16(y[2 * j], hi[kk], bh[0], bh[1]);
+            mma16(y[2 * j + 1], hi[kk], bh[2], bh[3]);
+            mma16(y[2 * j], lo[kk], bh[0], bh[1]);
+            mma16(y[2 * j + 1], lo[kk], bh[2], bh[3]);
+            mma16(y[2 * j], hi[kk], bl[0], bl[1]);
+            mma16(y[2 * j + 1], hi[kk], bl[2], bl[3]);
+          }
+      }
+      float* out = (back ? a.E : a.u) + unit * kBC * D + dv0 + g8;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int m = hf ? 2 + j : j < 2 ? j : 4 + j;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float& s = st[2 * np + m][e];
-          s *= eC;
-          s = fmaf(back ? -(e < 2 ? inv0 : inv1) : (e < 2 ? inv0 : inv1), y[m][e], s);
-          if constexpr (back) s = fmaf(e < 2 ? jnv0 : jnv1, z[m][e], s);
+          w[j][e] = fmaf(-(e < 2 ? inv0 : inv1), y[j][e], w[j][e]);
+          out[size_t(8 * m + t2 + (e & 1)) * D + (e >> 1) * 8] = w[j][e];
         }
+        other[32 * j] = make_float4(w[j][0], w[j][1], w[j][2], w[j][3]);
+      }
     }
-    __syncthreads();  // the stage and the factors are free
+    __syncthreads();
+    if (t + 1 < n)
+      load_late(t + 1);
+    else
+      cp_async_commit();
+    {
+      // blocks 0 and 3 are warp rg's (in slot rg + 4), 1 and 2 warp rg + 4's
+      const float4* s0 = hf ? mine : other;
+      const float4* s1 = hf ? other : mine;
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const float4 p = m < 2 ? s0[32 * m] : m >= 6 ? s0[32 * (m - 4)] : s1[32 * (m - 2)];
+        x[m][0] = p.x, x[m][1] = p.y, x[m][2] = p.z, x[m][3] = p.w;
+      }
+    }
+    limbs_of(x, fac + (back ? kFbG : kFbT), hi, lo, &inv0, &inv1);
+    const float f = back ? -fac[kFinvK] : fac[kFinvK];
+    add_product<NT>(st, back ? 1.f : eC, inv0 * f, inv1 * f, hi, lo, tk, dk0);
+    cp_async_wait<1>();  // all but S (and V) of the next chunk
+    __syncthreads();
   }
-  if (!back) {
-    store_state<D>(st, a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D, dv0);
+  if constexpr (!back) {
+    store_state<D, NT>(st, a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D, dk0, dv0);
+    // This grid ends after the other scan's: what follows reads both.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
   } else if (a.dh0 != nullptr) {
 #pragma unroll
     for (int m = 0; m < NT; ++m)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        a.dh0[seq_state + size_t(8 * m + t2 + (e & 1)) * D + dv0 + g8 + (e >> 1) * 8] = st[m][e];
+        a.dh0[seq_state + size_t(dk0 + 8 * m + t2 + (e & 1)) * D + dv0 + g8 + (e >> 1) * 8] =
+            st[m][e];
   }
-}
-
-template <int D>
-__global__ void __launch_bounds__(128) bwd_scan_kernel(BwdArgs a) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int SL = D / 64;
-  const int slice = blockIdx.x % SL, h = blockIdx.x / SL % a.H_v, b = blockIdx.x / SL / a.H_v;
-  scan<D, false>(a, b, h, slice, smem);
-}
-template <int D>
-__global__ void __launch_bounds__(128) bwd_scan_back_kernel(BwdArgs a) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int SL = D / 64;
-  const int slice = blockIdx.x % SL, h = blockIdx.x / SL % a.H_v, b = blockIdx.x / SL / a.H_v;
-  scan<D, true>(a, b, h, slice, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -892,7 +958,7 @@ __global__ void __launch_bounds__(256, 1) bwd_grads_kernel(BwdArgs a) {
         *reinterpret_cast<float2*>(u) = *reinterpret_cast<const float2*>(up);
         *reinterpret_cast<float2*>(e) = *reinterpret_cast<const float2*>(ep);
       }
-      const float bt = fac[2 * kBC + r], eG = fac[r], eT = fac[kBC + r];
+      const float bt = fac[kFbeta + r], eG = fac[kFeG + r], eT = fac[kFeT + r];
       float db = 0.f, vs = 0.f, mu = 0.f, me = 0.f;
       uint32_t vw[V / 2] = {};
       if (r < c.rows) {
@@ -1018,10 +1084,10 @@ __global__ void __launch_bounds__(256, 1) bwd_grads_kernel(BwdArgs a) {
     float dq[MT][2][4] = {}, acc[MT][2][4] = {};
     // dO H^T and -(e^G beta E) H^T
     {
-      const float* p = a.Hmax + unit * 2 * CG;
+      const float* p = a.Hmax + unit * 4 * CG;
       float m0 = 0.f, m1 = 0.f, ih, id;
 #pragma unroll
-      for (int x = 0; x < CG; ++x) m0 = max_nan(m0, p[x]), m1 = max_nan(m1, p[CG + x]);
+      for (int x = 0; x < 2 * CG; ++x) m0 = max_nan(m0, p[x]), m1 = max_nan(m1, p[2 * CG + x]);
       const float sh = pow2_scale(m0, &ih), sd = pow2_scale(m1, &id);
       const float* Hp = H + size_t(16 * cg + g8) * D + 2 * t2;
 #pragma unroll
@@ -1236,7 +1302,7 @@ size_t layout(BwdArgs* a, char* base, int total_tokens, int num_seqs, int H_k, i
   a->E = reinterpret_cast<float*>(take(units * kBC * D * 4));
   a->H = reinterpret_cast<float*>(take((mc + num_seqs) * size_t(H_v) * D * D * 4));
   a->dH = reinterpret_cast<float*>(take(units * D * D * 4));
-  a->Hmax = reinterpret_cast<float*>(take(units * 2 * (D / 16) * 4));
+  a->Hmax = reinterpret_cast<float*>(take(units * 2 * (D / 8) * 4));
   return at;
 }
 
@@ -1247,16 +1313,25 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   cudaError_t e;
   const auto kMax = cudaFuncAttributeMaxDynamicSharedMemorySize;
   if ((e = cudaFuncSetAttribute(bwd_prep_kernel<D>, kMax, prep)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D>, kMax, fwd)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(bwd_scan_back_kernel<D>, kMax, back)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D, false>, kMax, fwd)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D, true>, kMax, back)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(bwd_grads_kernel<D>, kMax, grads)) != cudaSuccess) return e;
   bwd_prep_kernel<D><<<dim3(a.max_chunks, a.H_v), 256, prep, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int scans = a.num_seqs * a.H_v * (D / 64);
-  bwd_scan_back_kernel<D><<<scans, 128, back, s>>>(a);
+  const unsigned scans = unsigned(a.num_seqs) * a.H_v * (D / 64);
+  bwd_scan_kernel<D, true><<<scans, 256, back, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  bwd_scan_kernel<D><<<scans, 128, fwd, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchAttribute beside;
+  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  beside.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(scans);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = fwd;
+  cfg.stream = s;
+  cfg.attrs = &beside;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, bwd_scan_kernel<D, false>, a)) != cudaSuccess) return e;
   bwd_grads_kernel<D><<<dim3(a.max_chunks, a.H_k), 256, grads, s>>>(a);
   return cudaGetLastError();
 }
