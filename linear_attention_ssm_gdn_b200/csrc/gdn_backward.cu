@@ -856,13 +856,13 @@ __global__ void __launch_bounds__(256, 2) bwd_scan_kernel(BwdArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Grads: one CTA of 8 warps per (chunk, key head), the value heads of the group
+// Grads: one CTA of 16 warps per (chunk, key head), the value heads of the group
 // one after another, so that the shared dq and dk are summed in registers, in
 // one order.
 //
-// A warp owns 16 columns of dq and dk (D = 64: and half of the rows).  The
-// states are its B operand: they are read straight from global memory, once,
-// as the fragments that the scans stored, and split in registers; the row
+// Warps 0-7 make dq, warps 8-15 dk: a warp owns 16 of its columns (D = 64: and
+// half of the rows).  The states are its B operand: read straight from global
+// memory as the fragments that the scans stored, and split in registers; the row
 // operands (dO, u, E and their scaled forms) are f16 tiles in shared memory.
 // ---------------------------------------------------------------------------
 
@@ -876,21 +876,12 @@ struct GradsSmem {
   static constexpr int GE = 6 * kTile;     // -e^G beta E
   static constexpr int DU = 7 * kTile;     // e^{G_C - G} beta u
   static constexpr int PH = 8 * kTile, PL = PH + kBlk, N = PL + kBlk;
-  static constexpr int F = N + kBlk;       // floats from here
-  static constexpr int kFloats = kFac + 4 * kBC + (D / 16) * kBC + kBC + 16;
-  static constexpr int kBytes = F + kFloats * 4 + kBC * 8;
+  static constexpr int Fac = N + kBlk;           // two buffers of the unit's factors
+  static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
+  static constexpr int F = G + 2 * kBC * 8;      // floats from here
+  static constexpr int kFloats = 4 * kBC + (D / 16) * kBC + kBC + 16;
+  static constexpr int kBytes = F + kFloats * 4;
 };
-
-// A fragments of MT 16-row tiles times two 8-column B tiles.
-template <int MT>
-__device__ __forceinline__ void mma_rows(float (&acc)[MT][2][4], const uint32_t (&av)[MT][4],
-                                         const uint32_t (&b)[4]) {
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    mma16(acc[m][0], av[m], b[0], b[1]);
-    mma16(acc[m][1], av[m], b[2], b[3]);
-  }
-}
 
 // total += f(row) * acc, acc = 0; f gives the factor of a row.
 template <int MT, class F>
@@ -910,186 +901,224 @@ __device__ __forceinline__ void fold_in(float (&total)[MT][2][4], float (&acc)[M
     }
 }
 
+// acc += A (MT 16-row tiles of a tile, k-step kk) x two 8-column B tiles, one limb or two.
+template <int MT, bool two>
+__device__ __forceinline__ void rows_times(float (&acc)[MT][2][4], uint32_t tile, int r0, int kk,
+                                           const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    uint32_t av[4];
+    ldsm4(av, piece<false>(tile, r0 + 16 * m, 16 * kk));
+    mma16(acc[m][0], av, bh[0], bh[1]);
+    mma16(acc[m][1], av, bh[2], bh[3]);
+    if constexpr (two) {
+      mma16(acc[m][0], av, bl[0], bl[1]);
+      mma16(acc[m][1], av, bl[2], bl[3]);
+    }
+  }
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 template <int D>
-__global__ void __launch_bounds__(256, 1) bwd_grads_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
   using L = GradsSmem<D>;
   constexpr int CG = D / 16;        // column groups
   constexpr int MT = D / 32;        // 16-row tiles of a warp: all four, or two
-  constexpr int V = D / 32;         // values of a row per lane in the row pass
+  constexpr int J = D / 32;         // quads of a row per lane in the row pass
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint32_t most[2];      // P, N
   const uint32_t base = smem_u32(smem);
-  float* fac = reinterpret_cast<float*>(smem + L::F);
-  float *invU = fac + kFac, *invE = invU + kBC, *invGE = invE + kBC, *invDU = invGE + kBC;
+  float* invU = reinterpret_cast<float*>(smem + L::F);
+  float *invE = invU + kBC, *invGE = invE + kBC, *invDU = invGE + kBC;
   float* part = invDU + kBC;        // [CG][64] row sums q . dq
   float* vd = part + CG * kBC;      // [64] v . dv
   float* red = vd + kBC;            // [8] <H', dH'>
-  float2* Gs = reinterpret_cast<float2*>(red + 16);
   const int i = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5,
             lane = tid & 31, g8 = lane >> 2, t2 = 2 * (lane & 3);
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
   const int vpg = a.H_v / a.H_k;
-  const int cg = warp % CG, r0 = (warp / CG) * MT * 16;  // this warp's columns and rows
-  cp_async_block<256>(base + L::K, a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile, 2 * L::kTile);
-  float dqs[MT][2][4] = {}, dks[MT][2][4] = {};
+  const bool kside = warp >= 8;
+  const int w8 = warp & 7;
+  const int cg = w8 % CG, r0 = (w8 / CG) * MT * 16;  // this warp's columns and rows
+  // dO, factors and gates of head h, into the buffer of its parity
+  auto load_head = [&](int h) {
+    const size_t unit = size_t(i) * a.H_v + h;
+    const int p = h & 1;
+    if (tid < kFac / 4)
+      cp_async16(base + L::Fac + p * kFac * 4 + tid * 16, a.fac + unit * kFac + tid * 4);
+    else if (tid >= 128 && tid < 128 + kBC / 2)
+      cp_async16(base + L::G + p * kBC * 8 + (tid - 128) * 16, a.G + unit * kBC + (tid - 128) * 2);
+  };
+  cp_async_block<512>(base + L::K, a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile, 2 * L::kTile);
+  load_head(hk * vpg);
+  cp_async_commit();
+  float total[MT][2][4] = {};  // dq or dk of the group
   for (int h = hk * vpg; h < (hk + 1) * vpg; ++h) {
     const size_t unit = size_t(i) * a.H_v + h;
+    const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (h & 1) * kFac;
+    const float2* Gs = reinterpret_cast<const float2*>(smem + L::G) + (h & 1) * kBC;
     const float* H = a.H + (size_t(i + c.seq) * a.H_v + h) * D * D;
     const float* H1 = H + size_t(a.H_v) * D * D;
     const float* dH = a.dH + unit * D * D;
-    cp_async_block<256>(base + L::O, a.O + unit * L::kTile, L::kTile);
+    cp_async_block<512>(base + L::O, a.O + unit * L::kTile, L::kTile);
     cp_async_commit();
-    for (int x = tid; x < kFac; x += 256) fac[x] = a.fac[unit * kFac + x];
-    if (tid < kBC) Gs[tid] = a.G[unit * kBC + tid];
-    if (tid < 2) most[tid] = 0;
-    __syncthreads();
-    // Rows 8 w .. 8 w + 7: dv, dbeta, v . dv, and the f16 tiles of u and E.
-#pragma unroll 2
-    for (int m = 0; m < 8; ++m) {
-      const int r = 8 * warp + m;
-      float u[V], e[V];
-      const float* up = a.u + (unit * kBC + r) * D + V * lane;
-      const float* ep = a.E + (unit * kBC + r) * D + V * lane;
-      if constexpr (V == 4) {
-        *reinterpret_cast<float4*>(u) = *reinterpret_cast<const float4*>(up);
-        *reinterpret_cast<float4*>(e) = *reinterpret_cast<const float4*>(ep);
-      } else {
-        *reinterpret_cast<float2*>(u) = *reinterpret_cast<const float2*>(up);
-        *reinterpret_cast<float2*>(e) = *reinterpret_cast<const float2*>(ep);
+    // Rows 4 w .. 4 w + 3, 8 lanes a row, 4 J columns a lane.
+    const int r = 4 * warp + (lane >> 3), l8 = lane & 7;
+    float u[4 * J], e[4 * J];
+    uint2 vw[J];
+    {
+      const float* up = a.u + (unit * kBC + r) * D + 4 * l8;
+      const float* ep = a.E + (unit * kBC + r) * D + 4 * l8;
+      const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + h * D + 4 * l8;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        *reinterpret_cast<float4*>(u + 4 * j) = *reinterpret_cast<const float4*>(up + 32 * j);
+        *reinterpret_cast<float4*>(e + 4 * j) = *reinterpret_cast<const float4*>(ep + 32 * j);
+        vw[j] = make_uint2(0u, 0u);
+        if (r < c.rows) vw[j] = *reinterpret_cast<const uint2*>(vp + 32 * j);
       }
+    }
+    if (tid < 2) most[tid] = 0;
+    if (tid == 0) {  // this head's states, and the next head's, on their way to L2
+      prefetch_l2(H, D * D * 4);
+      prefetch_l2(dH, D * D * 4);
+      prefetch_l2(H1, D * D * 4);
+      if (h + 1 < (hk + 1) * vpg) {
+        prefetch_l2(a.u + (unit + 1) * kBC * D, kBC * D * 4);
+        prefetch_l2(a.E + (unit + 1) * kBC * D, kBC * D * 4);
+        prefetch_l2(a.O + (unit + 1) * L::kTile, L::kTile);
+      }
+    }
+    cp_async_wait<1>();  // the factors
+    __syncthreads();
+    // dv, dbeta, v . dv, and the f16 tiles of u and E
+    {
       const float bt = fac[kFbeta + r], eG = fac[kFeG + r], eT = fac[kFeT + r];
       float db = 0.f, vs = 0.f, mu = 0.f, me = 0.f;
-      uint32_t vw[V / 2] = {};
-      if (r < c.rows) {
-        const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + h * D + V * lane;
-        if constexpr (V == 4)
-          *reinterpret_cast<uint2*>(vw) = *reinterpret_cast<const uint2*>(vp);
-        else
-          vw[0] = *reinterpret_cast<const uint32_t*>(vp);
-      }
 #pragma unroll
-      for (int x = 0; x < V; ++x) {
+      for (int x = 0; x < 4 * J; ++x) {
+        const uint32_t w = x & 2 ? vw[x / 4].y : vw[x / 4].x;
         db = fmaf(e[x], u[x], db);
         u[x] *= bt, e[x] *= bt;
-        vs = fmaf(__uint_as_float(x & 1 ? vw[x / 2] & 0xffff0000u : vw[x / 2] << 16), e[x], vs);
+        vs = fmaf(__uint_as_float(x & 1 ? w & 0xffff0000u : w << 16), e[x], vs);
         mu = max_nan(mu, fabsf(u[x])), me = max_nan(me, fabsf(e[x]));
       }
-      db = warp_sum(db), vs = warp_sum(vs), mu = warp_max(mu), me = warp_max(me);
-      if (r < c.rows) {
-        uint16_t* dv = a.dv + (size_t(c.row0 + r) * a.H_v + h) * D + V * lane;
-        if constexpr (V == 4)
-          *reinterpret_cast<uint2*>(dv) =
-              make_uint2(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]));
-        else
-          *reinterpret_cast<uint32_t*>(dv) = pack_bf16x2(e[0], e[1]);
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1) {
+        db += __shfl_xor_sync(0xffffffffu, db, off);
+        vs += __shfl_xor_sync(0xffffffffu, vs, off);
+        mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
+        me = fmaxf(me, __shfl_xor_sync(0xffffffffu, me, off));
       }
       float iu, ie, ig, id;
       const float su = pow2_scale(mu, &iu), se = pow2_scale(me, &ie);
-      const float sg = pow2_scale(eG * me, &ig), sd = pow2_scale(eT * mu, &id);
-      if (lane == 0) {
+      const float sg = -eG * pow2_scale(eG * me, &ig), sd = eT * pow2_scale(eT * mu, &id);
+      if (l8 == 0) {
         if (r < c.rows) a.dbeta[size_t(c.row0 + r) * a.H_v + h] = db;
         vd[r] = vs;
         invU[r] = iu, invE[r] = ie, invGE[r] = ig, invDU[r] = id;
       }
-      uint32_t uh[V / 2], ul[V / 2], eh[V / 2], gh[V / 2], dh[V / 2];
+      uint16_t* dv = a.dv + (size_t(c.row0 + r) * a.H_v + h) * D + 4 * l8;
 #pragma unroll
-      for (int x = 0; x < V / 2; ++x) {
-        const float u0 = u[2 * x], u1 = u[2 * x + 1], e0 = e[2 * x], e1 = e[2 * x + 1];
-        split_f16(u0 * su, u1 * su, uh[x], ul[x]);
-        eh[x] = pack_f16(e0 * se, e1 * se);
-        gh[x] = pack_f16(-eG * e0 * sg, -eG * e1 * sg);
-        dh[x] = pack_f16(eT * u0 * sd, eT * u1 * sd);
-      }
-      const int col = V * lane;
-      uint8_t* at = smem + (col >> 6) * kBlk + sw128_offset(r, (col & 63) * 2);
-      if constexpr (V == 4) {
-        *reinterpret_cast<uint2*>(at + L::UH) = make_uint2(uh[0], uh[1]);
-        *reinterpret_cast<uint2*>(at + L::UL) = make_uint2(ul[0], ul[1]);
-        *reinterpret_cast<uint2*>(at + L::E) = make_uint2(eh[0], eh[1]);
-        *reinterpret_cast<uint2*>(at + L::GE) = make_uint2(gh[0], gh[1]);
-        *reinterpret_cast<uint2*>(at + L::DU) = make_uint2(dh[0], dh[1]);
-      } else {
-        *reinterpret_cast<uint32_t*>(at + L::UH) = uh[0];
-        *reinterpret_cast<uint32_t*>(at + L::UL) = ul[0];
-        *reinterpret_cast<uint32_t*>(at + L::E) = eh[0];
-        *reinterpret_cast<uint32_t*>(at + L::GE) = gh[0];
-        *reinterpret_cast<uint32_t*>(at + L::DU) = dh[0];
+      for (int j = 0; j < J; ++j) {
+        const float *up = u + 4 * j, *ep = e + 4 * j;
+        if (r < c.rows)
+          *reinterpret_cast<uint2*>(dv + 32 * j) =
+              make_uint2(pack_bf16x2(ep[0], ep[1]), pack_bf16x2(ep[2], ep[3]));
+        const int col = 4 * l8 + 32 * j;
+        uint8_t* at = smem + (col >> 6) * kBlk + sw128_offset(r, (col & 63) * 2);
+        uint2 uh, ul;
+        split_f16(up[0] * su, up[1] * su, uh.x, ul.x);
+        split_f16(up[2] * su, up[3] * su, uh.y, ul.y);
+        *reinterpret_cast<uint2*>(at + L::UH) = uh;
+        *reinterpret_cast<uint2*>(at + L::UL) = ul;
+        *reinterpret_cast<uint2*>(at + L::E) =
+            make_uint2(pack_f16(ep[0] * se, ep[1] * se), pack_f16(ep[2] * se, ep[3] * se));
+        *reinterpret_cast<uint2*>(at + L::GE) =
+            make_uint2(pack_f16(ep[0] * sg, ep[1] * sg), pack_f16(ep[2] * sg, ep[3] * sg));
+        *reinterpret_cast<uint2*>(at + L::DU) =
+            make_uint2(pack_f16(up[0] * sd, up[1] * sd), pack_f16(up[2] * sd, up[3] * sd));
       }
     }
     cp_async_wait<0>();
     __syncthreads();
-    // P and N: rows 16 (w / 2), columns 32 (w % 2), the lower 16-column blocks
+    if (h + 1 < (hk + 1) * vpg) load_head(h + 1);
+    cp_async_commit();
+    // P (warps 0-7) and N (8-15): rows 16 (w / 2), columns 32 (w % 2), the lower
+    // 16-column blocks
     {
-      const int rb = warp >> 1, ch = warp & 1;
-      float pa[4][4] = {}, na[4][4] = {};
+      const int rb = w8 >> 1, ch = w8 & 1;
+      float x[4][4] = {};
       if (2 * ch <= rb) {
+        const uint32_t ta = base + (kside ? L::E : L::O);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t ao[4], ae[4];
-          ldsm4(ao, piece<false>(base + L::O, 16 * rb, 16 * kk));
-          ldsm4(ae, piece<false>(base + L::E, 16 * rb, 16 * kk));
+          uint32_t av[4];
+          ldsm4(av, piece<false>(ta, 16 * rb, 16 * kk));
 #pragma unroll
           for (int np = 0; np < 2; ++np)
             if (2 * ch + np <= rb) {
-              uint32_t bh[4], bl[4];
-              ldsm4(bh, piece<true>(base + L::UH, 32 * ch + 16 * np, 16 * kk));
-              ldsm4(bl, piece<true>(base + L::UL, 32 * ch + 16 * np, 16 * kk));
-              mma16(pa[2 * np], ao, bh[0], bh[1]);
-              mma16(pa[2 * np + 1], ao, bh[2], bh[3]);
-              mma16(na[2 * np], ae, bh[0], bh[1]);
-              mma16(na[2 * np + 1], ae, bh[2], bh[3]);
-              mma16(pa[2 * np], ao, bl[0], bl[1]);
-              mma16(pa[2 * np + 1], ao, bl[2], bl[3]);
+              uint32_t bv[4];
+              ldsm4(bv, piece<true>(base + L::UH, 32 * ch + 16 * np, 16 * kk));
+              mma16(x[2 * np], av, bv[0], bv[1]);
+              mma16(x[2 * np + 1], av, bv[2], bv[3]);
+              if (!kside) {
+                ldsm4(bv, piece<true>(base + L::UL, 32 * ch + 16 * np, 16 * kk));
+                mma16(x[2 * np], av, bv[0], bv[1]);
+                mma16(x[2 * np + 1], av, bv[2], bv[3]);
+              }
             }
         }
       }
-      const float io = a.scale * fac[kFinvO];
-      float mp = 0.f, mn = 0.f;
+      float m = 0.f;
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 16 * rb + g8 + (e >> 1) * 8, s = 32 * ch + 8 * n + t2 + (e & 1);
-          const float d = s <= r ? expdiff(Gs[r], Gs[s]) * invU[s] : 0.f;
-          pa[n][e] = s <= r ? pa[n][e] * io * d : 0.f;
-          na[n][e] = s < r ? -na[n][e] * invE[r] * d : 0.f;
-          mp = max_nan(mp, fabsf(pa[n][e])), mn = max_nan(mn, fabsf(na[n][e]));
+        for (int k = 0; k < 4; ++k) {
+          const int pr = 16 * rb + g8 + (k >> 1) * 8, ps = 32 * ch + 8 * n + t2 + (k & 1);
+          float f = 0.f;
+          if (ps < pr || (ps == pr && !kside))
+            f = expdiff(Gs[pr], Gs[ps]) * invU[ps] *
+                (kside ? -invE[pr] : a.scale * fac[kFinvO]);
+          x[n][k] = f == 0.f ? 0.f : x[n][k] * f;
+          m = max_nan(m, fabsf(x[n][k]));
         }
-      const uint32_t up = __reduce_max_sync(0xffffffffu, __float_as_uint(mp));
-      const uint32_t un = __reduce_max_sync(0xffffffffu, __float_as_uint(mn));
-      if (lane == 0) {
-        atomicMax(&most[0], up);
-        atomicMax(&most[1], un);
-      }
-      __syncthreads();
-      float ip, in;
-      const float sp = pow2_scale(__uint_as_float(most[0]), &ip);
-      const float sn = pow2_scale(__uint_as_float(most[1]), &in);
+      const uint32_t um = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+      if (lane == 0) atomicMax(&most[kside], um);
+      named_sync(1 + kside, 256);
+      float inv;
+      const float sc = pow2_scale(__uint_as_float(most[kside]), &inv);
       if (2 * ch <= rb)
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const int r = 16 * rb + g8 + (e >> 1) * 8, s = 32 * ch + 8 * n + t2;
+          for (int k = 0; k < 4; k += 2) {
+            const int pr = 16 * rb + g8 + (k >> 1) * 8, ps = 32 * ch + 8 * n + t2;
             uint32_t hi, lo;
-            split_f16(pa[n][e] * sp, pa[n][e + 1] * sp, hi, lo);
-            const uint32_t at = sw128_offset(r, s * 2);
-            *reinterpret_cast<uint32_t*>(smem + L::PH + at) = hi;
-            *reinterpret_cast<uint32_t*>(smem + L::PL + at) = lo;
-            *reinterpret_cast<uint32_t*>(smem + L::N + at) = pack_f16(na[n][e] * sn,
-                                                                      na[n][e + 1] * sn);
+            split_f16(x[n][k] * sc, x[n][k + 1] * sc, hi, lo);
+            const uint32_t at = sw128_offset(pr, ps * 2);
+            if (kside) {
+              *reinterpret_cast<uint32_t*>(smem + L::N + at) = hi;
+            } else {
+              *reinterpret_cast<uint32_t*>(smem + L::PH + at) = hi;
+              *reinterpret_cast<uint32_t*>(smem + L::PL + at) = lo;
+            }
           }
     }
-    float dq[MT][2][4] = {}, acc[MT][2][4] = {};
-    // dO H^T and -(e^G beta E) H^T
-    {
-      const float* p = a.Hmax + unit * 4 * CG;
-      float m0 = 0.f, m1 = 0.f, ih, id;
+    const float* hm = a.Hmax + unit * 4 * CG;
+    float m0 = 0.f, ih;
 #pragma unroll
-      for (int x = 0; x < 2 * CG; ++x) m0 = max_nan(m0, p[x]), m1 = max_nan(m1, p[2 * CG + x]);
-      const float sh = pow2_scale(m0, &ih), sd = pow2_scale(m1, &id);
-      const float* Hp = H + size_t(16 * cg + g8) * D + 2 * t2;
+    for (int x = 0; x < 2 * CG; ++x) m0 = max_nan(m0, hm[x]);
+    const float sh = pow2_scale(m0, &ih);
+    const float* Hp = H + size_t(16 * cg + g8) * D + 2 * t2;
+    float acc[MT][2][4] = {};
+    if (!kside) {
+      float dq[MT][2][4] = {};
+      // dO H^T
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         uint32_t bh[4], bl[4];
@@ -1099,30 +1128,80 @@ __global__ void __launch_bounds__(256, 1) bwd_grads_kernel(BwdArgs a) {
           split_f16(x.x * sh, x.y * sh, bh[2 * n], bl[2 * n]);
           split_f16(x.z * sh, x.w * sh, bh[2 * n + 1], bl[2 * n + 1]);
         }
-        uint32_t av[MT][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          ldsm4(av[m], piece<false>(base + L::O, r0 + 16 * m, 16 * kk));
-        mma_rows(dq, av, bh);
-        mma_rows(dq, av, bl);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          ldsm4(av[m], piece<false>(base + L::GE, r0 + 16 * m, 16 * kk));
-        mma_rows(acc, av, bh);
+        rows_times<MT, true>(dq, base + L::O, r0, kk, bh, bl);
       }
-      fold_in(dks, acc, [&](int r) { return invGE[r0 + r + g8] * ih; });
       const float f = a.scale * fac[kFinvO] * ih;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dq[m][n][e] *= f * fac[r0 + 16 * m + g8 + (e >> 1) * 8];
+          for (int k = 0; k < 4; ++k)
+            dq[m][n][k] *= f * fac[kFeG + r0 + 16 * m + g8 + (k >> 1) * 8];
+      named_sync(1, 256);  // P
+      // P K (two limbs, k-steps up to the diagonal)
+      float ip;
+      pow2_scale(__uint_as_float(most[0]), &ip);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t bv[4];
+        ldsm4t(bv, piece<false>(base + L::K, 16 * kk, 16 * cg));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          if (kk <= r0 / 16 + m) {
+            uint32_t av[4];
+            ldsm4(av, piece<false>(base + L::PH, r0 + 16 * m, 16 * kk));
+            mma16(acc[m][0], av, bv[0], bv[1]);
+            mma16(acc[m][1], av, bv[2], bv[3]);
+            ldsm4(av, piece<false>(base + L::PL, r0 + 16 * m, 16 * kk));
+            mma16(acc[m][0], av, bv[0], bv[1]);
+            mma16(acc[m][1], av, bv[2], bv[3]);
+          }
+      }
+      const float fp = ip * fac[kFinvK];
+      fold_in(dq, acc, [&](int) { return fp; });
+      // q . dq of this warp's columns, and the group's sum
+      const float iq = fac[kFinvQ];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int rr = r0 + 16 * m + 8 * k + g8;
+          float x = 0.f;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int col = 16 * cg + 8 * n + t2;
+            const float2 q = unpack_f16(*reinterpret_cast<const uint32_t*>(
+                smem + L::Q + (col >> 6) * kBlk + sw128_offset(rr, (col & 63) * 2)));
+            x = fmaf(q.x, dq[m][n][2 * k], fmaf(q.y, dq[m][n][2 * k + 1], x));
+            total[m][n][2 * k] += dq[m][n][2 * k];
+            total[m][n][2 * k + 1] += dq[m][n][2 * k + 1];
+          }
+          x += __shfl_xor_sync(0xffffffffu, x, 1);
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+          if ((lane & 3) == 0) part[cg * kBC + rr] = x * iq;
+        }
+    } else {
+      // -(e^G beta E) H^T
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t bh[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float4 x = *reinterpret_cast<const float4*>(Hp + size_t(8 * n) * D + 16 * kk);
+          bh[2 * n] = pack_f16(x.x * sh, x.y * sh);
+          bh[2 * n + 1] = pack_f16(x.z * sh, x.w * sh);
+        }
+        rows_times<MT, false>(acc, base + L::GE, r0, kk, bh, bh);
+      }
+      fold_in(total, acc, [&](int x) { return invGE[r0 + x + g8] * ih; });
       // (e^{G_C - G} beta u) dH'^T, and <H', dH'> on the way (each value once)
+      float m1 = 0.f, id, hh = 0.f;
+#pragma unroll
+      for (int x = 0; x < 2 * CG; ++x) m1 = max_nan(m1, hm[2 * CG + x]);
+      const float sd = pow2_scale(m1, &id);
       const float* Dp = dH + size_t(16 * cg + g8) * D + 2 * t2;
       const float* H1p = H1 + size_t(16 * cg + g8) * D + 2 * t2;
-      float hh = 0.f;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         uint32_t bh[4];
@@ -1136,104 +1215,67 @@ __global__ void __launch_bounds__(256, 1) bwd_grads_kernel(BwdArgs a) {
             hh += fmaf(x.x, y.x, x.y * y.y) + fmaf(x.z, y.z, x.w * y.w);
           }
         }
-        uint32_t av[MT][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          ldsm4(av[m], piece<false>(base + L::DU, r0 + 16 * m, 16 * kk));
-        mma_rows(acc, av, bh);
+        rows_times<MT, false>(acc, base + L::DU, r0, kk, bh, bh);
       }
-      fold_in(dks, acc, [&](int r) { return invDU[r0 + r + g8] * id; });
+      fold_in(total, acc, [&](int x) { return invDU[r0 + x + g8] * id; });
       hh = warp_sum(hh);
-      if (lane == 0) red[warp] = hh;
-    }
-    __syncthreads();  // P, N and red
-    {
-      float ip, in;
-      pow2_scale(__uint_as_float(most[0]), &ip);
-      pow2_scale(__uint_as_float(most[1]), &in);
-      const int mt0 = r0 / 16;
-      float ac2[MT][2][4] = {};
-      // P K (two limbs, k-steps up to the diagonal)
+      if (lane == 0) red[w8] = hh;
+      named_sync(2, 256);  // N
+      // N K and N^T K
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        uint32_t b[4];
-        ldsm4t(b, piece<false>(base + L::K, 16 * kk, 16 * cg));
+        uint32_t bv[4];
+        ldsm4t(bv, piece<false>(base + L::K, 16 * kk, 16 * cg));
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-          if (kk <= mt0 + m) {
-            uint32_t av[4];
-            ldsm4(av, piece<false>(base + L::PH, r0 + 16 * m, 16 * kk));
-            mma16(acc[m][0], av, b[0], b[1]);
-            mma16(acc[m][1], av, b[2], b[3]);
-            ldsm4(av, piece<false>(base + L::PL, r0 + 16 * m, 16 * kk));
-            mma16(acc[m][0], av, b[0], b[1]);
-            mma16(acc[m][1], av, b[2], b[3]);
+        for (int m = 0; m < MT; ++m) {
+          uint32_t av[4];
+          if (kk <= r0 / 16 + m) {
             ldsm4(av, piece<false>(base + L::N, r0 + 16 * m, 16 * kk));
-            mma16(ac2[m][0], av, b[0], b[1]);
-            mma16(ac2[m][1], av, b[2], b[3]);
+            mma16(acc[m][0], av, bv[0], bv[1]);
+            mma16(acc[m][1], av, bv[2], bv[3]);
           }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          if (kk >= mt0 + m) {  // N^T K
-            uint32_t av[4];
+          if (kk >= r0 / 16 + m) {
             ldsm4t(av, piece<true>(base + L::N, 16 * kk, r0 + 16 * m));
-            mma16(ac2[m][0], av, b[0], b[1]);
-            mma16(ac2[m][1], av, b[2], b[3]);
+            mma16(acc[m][0], av, bv[0], bv[1]);
+            mma16(acc[m][1], av, bv[2], bv[3]);
           }
+        }
       }
-      const float fp = ip * fac[kFinvK], fn = in * fac[kFinvK], fq = ip * fac[kFinvQ];
-      fold_in(dq, acc, [&](int) { return fp; });
-      fold_in(dks, ac2, [&](int) { return fn; });
+      float in;
+      pow2_scale(__uint_as_float(most[1]), &in);
+      const float fn = in * fac[kFinvK];
+      fold_in(total, acc, [&](int) { return fn; });
+    }
+    __syncthreads();  // P, part, red
+    if (kside) {
       // P^T Q
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        uint32_t b[4];
-        ldsm4t(b, piece<false>(base + L::Q, 16 * kk, 16 * cg));
+        uint32_t bv[4];
+        ldsm4t(bv, piece<false>(base + L::Q, 16 * kk, 16 * cg));
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          if (kk >= mt0 + m) {
+          if (kk >= r0 / 16 + m) {
             uint32_t av[4];
             ldsm4t(av, piece<true>(base + L::PH, 16 * kk, r0 + 16 * m));
-            mma16(acc[m][0], av, b[0], b[1]);
-            mma16(acc[m][1], av, b[2], b[3]);
+            mma16(acc[m][0], av, bv[0], bv[1]);
+            mma16(acc[m][1], av, bv[2], bv[3]);
           }
       }
-      fold_in(dks, acc, [&](int) { return fq; });
-    }
-    // q . dq of this warp's columns, and the group's sum
-    {
-      const float iq = fac[kFinvQ];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = r0 + 16 * m + 8 * e + g8;
-          float x = 0.f;
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int col = 16 * cg + 8 * n + t2;
-            const float2 q = unpack_f16(*reinterpret_cast<const uint32_t*>(
-                smem + L::Q + (col >> 6) * kBlk + sw128_offset(r, (col & 63) * 2)));
-            x = fmaf(q.x, dq[m][n][2 * e], fmaf(q.y, dq[m][n][2 * e + 1], x));
-            dqs[m][n][2 * e] += dq[m][n][2 * e];
-            dqs[m][n][2 * e + 1] += dq[m][n][2 * e + 1];
-          }
-          x += __shfl_xor_sync(0xffffffffu, x, 1);
-          x += __shfl_xor_sync(0xffffffffu, x, 2);
-          if ((lane & 3) == 0) part[cg * kBC + r] = x * iq;
-        }
-    }
-    __syncthreads();
-    // dg: suffix sums over the rows, two per lane, on top of <H', dH'>
-    if (warp == 0) {
+      float ip;
+      pow2_scale(__uint_as_float(most[0]), &ip);
+      const float fq = ip * fac[kFinvQ];
+      fold_in(total, acc, [&](int) { return fq; });
+    } else if (warp == 0) {
+      // dg: suffix sums over the rows, two per lane, on top of <H', dH'>
       double x[2], run;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 63 - (2 * lane + e);
-        float s = 0.f;
+      for (int k = 0; k < 2; ++k) {
+        const int rr = 63 - (2 * lane + k);
+        float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < CG; ++w) s += part[w * kBC + r];
-        x[e] = r < c.rows ? double(s) - double(vd[r]) : 0.0;
+        for (int w = 0; w < CG; ++w) sum += part[w * kBC + rr];
+        x[k] = rr < c.rows ? double(sum) - double(vd[rr]) : 0.0;
       }
       x[1] += x[0];
       run = x[1];
@@ -1248,13 +1290,14 @@ __global__ void __launch_bounds__(256, 1) bwd_grads_kernel(BwdArgs a) {
       x[0] += run - x[1];
       x[1] = run;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 63 - (2 * lane + e);
-        if (r < c.rows) a.dg[size_t(c.row0 + r) * a.H_v + h] = float(x[e] + hh);
+      for (int k = 0; k < 2; ++k) {
+        const int rr = 63 - (2 * lane + k);
+        if (rr < c.rows) a.dg[size_t(c.row0 + rr) * a.H_v + h] = float(x[k] + hh);
       }
     }
     __syncthreads();  // the tiles and factors are rewritten for the next head
   }
+  uint16_t* out = kside ? a.dk : a.dq;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -1262,13 +1305,10 @@ __global__ void __launch_bounds__(256, 1) bwd_grads_kernel(BwdArgs a) {
       const int r = r0 + 16 * m + 8 * e + g8;
       if (r >= c.rows) continue;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const size_t at = (size_t(c.row0 + r) * a.H_k + hk) * D + 16 * cg + 8 * n + t2;
-        *reinterpret_cast<uint32_t*>(a.dq + at) =
-            pack_bf16x2(dqs[m][n][2 * e], dqs[m][n][2 * e + 1]);
-        *reinterpret_cast<uint32_t*>(a.dk + at) =
-            pack_bf16x2(dks[m][n][2 * e], dks[m][n][2 * e + 1]);
-      }
+      for (int n = 0; n < 2; ++n)
+        *reinterpret_cast<uint32_t*>(out + (size_t(c.row0 + r) * a.H_k + hk) * D + 16 * cg +
+                                     8 * n + t2) =
+            pack_bf16x2(total[m][n][2 * e], total[m][n][2 * e + 1]);
     }
 }
 
@@ -1332,7 +1372,7 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   cfg.attrs = &beside;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, bwd_scan_kernel<D, false>, a)) != cudaSuccess) return e;
-  bwd_grads_kernel<D><<<dim3(a.max_chunks, a.H_k), 256, grads, s>>>(a);
+  bwd_grads_kernel<D><<<dim3(a.max_chunks, a.H_k), 512, grads, s>>>(a);
   return cudaGetLastError();
 }
 
