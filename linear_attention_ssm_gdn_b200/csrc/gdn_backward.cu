@@ -73,8 +73,8 @@ struct BwdArgs {
   float2* G;           // [chunk][H_v][64] cumulative gates, high and low part
   float* u;            // [chunk][H_v][64][D]
   float* E;            // [chunk][H_v][64][D]
-  float* H;            // [chunk + sequence][H_v][D][D] entry states, then the final state
-  float* dH;           // [chunk][H_v][D][D] gradient of the exit state
+  float* H;            // [chunk + sequence][H_v][D / 16][D][16] entry states, then the final one
+  float* dH;           // [chunk][H_v][D / 16][D][16] gradient of the exit state
   float* Hmax;         // [chunk][H_v][2][D / 8] largest |H| and |dH| of each scan warp's part
 };
 
@@ -576,19 +576,19 @@ __device__ __forceinline__ void add_product(float (&st)[NT][4], float decay, flo
   }
 }
 
-// Writes a state (C fragments, rows dv0 + g / g + 8) to the workspace, whose rows
-// hold each 16 columns as four quads (2t, 2t+1, 2t+8, 2t+9): the B fragment of
-// the products that read it.  Lanes g and g ^ 1 trade halves for 16-byte stores.
+// Writes a state (C fragments, rows dv0 + g / g + 8) to the workspace: slices of 16
+// columns, [d_k][16], each row as four quads (2t, 2t+1, 2t+8, 2t+9), the B fragment
+// of the products that read it.  Lanes g and g ^ 1 trade halves for 16-byte stores.
 template <int D, int NT>
 __device__ __forceinline__ void store_state(const float (&st)[NT][4], float* out, int dk0,
                                             int dv0) {
   const int lane = threadIdx.x & 31, g8 = lane >> 2, t2 = 2 * (lane & 3), odd = g8 & 1;
-  float* p = out + size_t(dk0 + t2 + odd) * D + dv0 + 4 * (g8 >> 1);
+  float* p = out + dv0 * D + (dk0 + t2 + odd) * 16 + 4 * (g8 >> 1);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const float x = __shfl_xor_sync(0xffffffffu, odd ? st[n][0] : st[n][1], 4);
     const float y = __shfl_xor_sync(0xffffffffu, odd ? st[n][2] : st[n][3], 4);
-    *reinterpret_cast<float4*>(p + size_t(8 * n) * D) =
+    *reinterpret_cast<float4*>(p + 8 * n * 16) =
         odd ? make_float4(x, st[n][1], y, st[n][3]) : make_float4(st[n][0], x, st[n][2], y);
   }
 }
@@ -873,14 +873,22 @@ struct GradsSmem {
   static constexpr int O = 2 * kTile;      // dO
   static constexpr int UH = 3 * kTile, UL = 4 * kTile;  // beta u, two limbs
   static constexpr int E = 5 * kTile;      // beta E
-  static constexpr int GE = 6 * kTile;     // -e^G beta E
-  static constexpr int DU = 7 * kTile;     // e^{G_C - G} beta u
-  static constexpr int PH = 8 * kTile, PL = PH + kBlk, N = PL + kBlk;
-  static constexpr int Fac = N + kBlk;           // two buffers of the unit's factors
+  static constexpr int PH = 6 * kTile, PL = PH + kBlk, N = PL + kBlk;
+  static constexpr int kSlice = D * 64;    // 16 state columns in f32
+  static constexpr int H = N + kBlk;       // all slices of H; two of them, later, of dH'
+  static constexpr int DH = H + D / 16 * kSlice;  // the first D / 16 - 4 slices of dH'
+  static constexpr int Fac = DH + (D / 16 - 4) * kSlice;  // two buffers of the unit's factors
   static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
   static constexpr int F = G + 2 * kBC * 8;      // floats from here
-  static constexpr int kFloats = 4 * kBC + (D / 16) * kBC + kBC + 16;
+  static constexpr int kFloats = 2 * kBC + (D / 16) * kBC + kBC + 16;
   static constexpr int kBytes = F + kFloats * 4;
+  // Where slice x of dH' is: the last four go where beta u's low limb was (its
+  // kTile holds two) and over the first two slices of H.
+  __device__ static constexpr int dh_slice(int x) {
+    constexpr int n = D / 16;
+    return x < n - 4 ? DH + x * kSlice : x < n - 2 ? UL + (x - (n - 4)) * kSlice
+                                                   : H + (x - (n - 2)) * kSlice;
+  }
 };
 
 // total += f(row) * acc, acc = 0; f gives the factor of a row.
@@ -918,6 +926,10 @@ __device__ __forceinline__ void rows_times(float (&acc)[MT][2][4], uint32_t tile
   }
 }
 
+__device__ __forceinline__ void named_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
@@ -932,8 +944,8 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
   __shared__ uint32_t most[2];      // P, N
   const uint32_t base = smem_u32(smem);
   float* invU = reinterpret_cast<float*>(smem + L::F);
-  float *invE = invU + kBC, *invGE = invE + kBC, *invDU = invGE + kBC;
-  float* part = invDU + kBC;        // [CG][64] row sums q . dq
+  float* invE = invU + kBC;
+  float* part = invE + kBC;         // [CG][64] row sums q . dq
   float* vd = part + CG * kBC;      // [64] v . dv
   float* red = vd + kBC;            // [8] <H', dH'>
   const int i = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5,
@@ -953,6 +965,11 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
     else if (tid >= 128 && tid < 128 + kBC / 2)
       cp_async16(base + L::G + p * kBC * 8 + (tid - 128) * 16, a.G + unit * kBC + (tid - 128) * 2);
   };
+  // two slices of a state from slice x, by warps 8-15, whose own waits cover them
+  auto load_slices = [&](uint32_t dst, const float* state, int x) {
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(state) + x * L::kSlice;
+    for (int y = (tid - 256) * 16; y < 2 * L::kSlice; y += 256 * 16) cp_async16(dst + y, src + y);
+  };
   cp_async_block<512>(base + L::K, a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile, 2 * L::kTile);
   load_head(hk * vpg);
   cp_async_commit();
@@ -965,6 +982,10 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
     const float* H1 = H + size_t(a.H_v) * D * D;
     const float* dH = a.dH + unit * D * D;
     cp_async_block<512>(base + L::O, a.O + unit * L::kTile, L::kTile);
+    cp_async_commit();
+    cp_async_block<512>(base + L::H, reinterpret_cast<const uint8_t*>(H), D * D * 4);
+    cp_async_block<512>(base + L::DH, reinterpret_cast<const uint8_t*>(dH),
+                        (CG - 4) * L::kSlice);
     cp_async_commit();
     // Rows 4 w .. 4 w + 3, 8 lanes a row, 4 J columns a lane.
     const int r = 4 * warp + (lane >> 3), l8 = lane & 7;
@@ -983,21 +1004,22 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
       }
     }
     if (tid < 2) most[tid] = 0;
-    if (tid == 0) {  // this head's states, and the next head's, on their way to L2
-      prefetch_l2(H, D * D * 4);
-      prefetch_l2(dH, D * D * 4);
+    if (tid == 0) {  // to L2: what this head reads later, and all of the next one
+      if (h == hk * vpg) prefetch_l2(dH + (CG - 4) * D * 16, 4 * L::kSlice);
       prefetch_l2(H1, D * D * 4);
       if (h + 1 < (hk + 1) * vpg) {
         prefetch_l2(a.u + (unit + 1) * kBC * D, kBC * D * 4);
         prefetch_l2(a.E + (unit + 1) * kBC * D, kBC * D * 4);
         prefetch_l2(a.O + (unit + 1) * L::kTile, L::kTile);
+        prefetch_l2(H + D * D, D * D * 4);
+        prefetch_l2(dH + D * D, D * D * 4);
       }
     }
-    cp_async_wait<1>();  // the factors
+    cp_async_wait<2>();  // the factors
     __syncthreads();
     // dv, dbeta, v . dv, and the f16 tiles of u and E
     {
-      const float bt = fac[kFbeta + r], eG = fac[kFeG + r], eT = fac[kFeT + r];
+      const float bt = fac[kFbeta + r];
       float db = 0.f, vs = 0.f, mu = 0.f, me = 0.f;
 #pragma unroll
       for (int x = 0; x < 4 * J; ++x) {
@@ -1014,13 +1036,12 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
         mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
         me = fmaxf(me, __shfl_xor_sync(0xffffffffu, me, off));
       }
-      float iu, ie, ig, id;
+      float iu, ie;
       const float su = pow2_scale(mu, &iu), se = pow2_scale(me, &ie);
-      const float sg = -eG * pow2_scale(eG * me, &ig), sd = eT * pow2_scale(eT * mu, &id);
       if (l8 == 0) {
         if (r < c.rows) a.dbeta[size_t(c.row0 + r) * a.H_v + h] = db;
         vd[r] = vs;
-        invU[r] = iu, invE[r] = ie, invGE[r] = ig, invDU[r] = id;
+        invU[r] = iu, invE[r] = ie;
       }
       uint16_t* dv = a.dv + (size_t(c.row0 + r) * a.H_v + h) * D + 4 * l8;
 #pragma unroll
@@ -1038,16 +1059,10 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
         *reinterpret_cast<uint2*>(at + L::UL) = ul;
         *reinterpret_cast<uint2*>(at + L::E) =
             make_uint2(pack_f16(ep[0] * se, ep[1] * se), pack_f16(ep[2] * se, ep[3] * se));
-        *reinterpret_cast<uint2*>(at + L::GE) =
-            make_uint2(pack_f16(ep[0] * sg, ep[1] * sg), pack_f16(ep[2] * sg, ep[3] * sg));
-        *reinterpret_cast<uint2*>(at + L::DU) =
-            make_uint2(pack_f16(up[0] * sd, up[1] * sd), pack_f16(up[2] * sd, up[3] * sd));
       }
     }
-    cp_async_wait<0>();
+    cp_async_wait<1>();  // dO
     __syncthreads();
-    if (h + 1 < (hk + 1) * vpg) load_head(h + 1);
-    cp_async_commit();
     // P (warps 0-7) and N (8-15): rows 16 (w / 2), columns 32 (w % 2), the lower
     // 16-column blocks
     {
@@ -1089,7 +1104,12 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
         }
       const uint32_t um = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
       if (lane == 0) atomicMax(&most[kside], um);
-      named_sync(1 + kside, 256);
+      cp_async_wait<0>();  // H and the first slices of dH'
+      __syncthreads();
+      // beta u's low limb is done with: two more slices of dH'
+      if (kside) load_slices(base + L::UL, dH, CG - 4);
+      if (h + 1 < (hk + 1) * vpg) load_head(h + 1);
+      cp_async_commit();
       float inv;
       const float sc = pow2_scale(__uint_as_float(most[kside]), &inv);
       if (2 * ch <= rb)
@@ -1114,7 +1134,7 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
 #pragma unroll
     for (int x = 0; x < 2 * CG; ++x) m0 = max_nan(m0, hm[x]);
     const float sh = pow2_scale(m0, &ih);
-    const float* Hp = H + size_t(16 * cg + g8) * D + 2 * t2;
+    const int at = (16 * cg + g8) * 64 + 8 * t2;  // this lane's quads of a slice
     float acc[MT][2][4] = {};
     if (!kside) {
       float dq[MT][2][4] = {};
@@ -1124,11 +1144,13 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
         uint32_t bh[4], bl[4];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float4 x = *reinterpret_cast<const float4*>(Hp + size_t(8 * n) * D + 16 * kk);
+          const float4 x = *reinterpret_cast<const float4*>(smem + L::H + kk * L::kSlice + at +
+                                                            512 * n);
           split_f16(x.x * sh, x.y * sh, bh[2 * n], bl[2 * n]);
           split_f16(x.z * sh, x.w * sh, bh[2 * n + 1], bl[2 * n + 1]);
         }
         rows_times<MT, true>(dq, base + L::O, r0, kk, bh, bl);
+        if (kk == 1) named_arrive(3, 512);  // the first two slices of H may go
       }
       const float f = a.scale * fac[kFinvO] * ih;
 #pragma unroll
@@ -1188,36 +1210,51 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
         uint32_t bh[4];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float4 x = *reinterpret_cast<const float4*>(Hp + size_t(8 * n) * D + 16 * kk);
+          const float4 x = *reinterpret_cast<const float4*>(smem + L::H + kk * L::kSlice + at +
+                                                            512 * n);
           bh[2 * n] = pack_f16(x.x * sh, x.y * sh);
           bh[2 * n + 1] = pack_f16(x.z * sh, x.w * sh);
         }
-        rows_times<MT, false>(acc, base + L::GE, r0, kk, bh, bh);
+        rows_times<MT, false>(acc, base + L::E, r0, kk, bh, bh);
       }
-      fold_in(total, acc, [&](int x) { return invGE[r0 + x + g8] * ih; });
+      fold_in(total, acc, [&](int x) {
+        return -fac[kFeG + r0 + x + g8] * (invE[r0 + x + g8] * ih);
+      });
+      named_sync(3, 512);  // everybody is past the first two slices of H
+      load_slices(base + L::H, dH, CG - 2);
+      cp_async_commit();
+      cp_async_wait<1>();  // the two slices before them
+      named_sync(2, 256);
       // (e^{G_C - G} beta u) dH'^T, and <H', dH'> on the way (each value once)
       float m1 = 0.f, id, hh = 0.f;
 #pragma unroll
       for (int x = 0; x < 2 * CG; ++x) m1 = max_nan(m1, hm[2 * CG + x]);
       const float sd = pow2_scale(m1, &id);
-      const float* Dp = dH + size_t(16 * cg + g8) * D + 2 * t2;
-      const float* H1p = H1 + size_t(16 * cg + g8) * D + 2 * t2;
+      const float* H1p = H1 + at / 4;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
+        if (kk == D / 16 - 2) {
+          cp_async_wait<0>();
+          named_sync(2, 256);
+        }
         uint32_t bh[4];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float4 x = *reinterpret_cast<const float4*>(Dp + size_t(8 * n) * D + 16 * kk);
+          const float4 x =
+              *reinterpret_cast<const float4*>(smem + L::dh_slice(kk) + at + 512 * n);
           bh[2 * n] = pack_f16(x.x * sd, x.y * sd);
           bh[2 * n + 1] = pack_f16(x.z * sd, x.w * sd);
           if (r0 == 0) {
-            const float4 y = *reinterpret_cast<const float4*>(H1p + size_t(8 * n) * D + 16 * kk);
+            const float4 y =
+                *reinterpret_cast<const float4*>(H1p + kk * (L::kSlice / 4) + 128 * n);
             hh += fmaf(x.x, y.x, x.y * y.y) + fmaf(x.z, y.z, x.w * y.w);
           }
         }
-        rows_times<MT, false>(acc, base + L::DU, r0, kk, bh, bh);
+        rows_times<MT, false>(acc, base + L::UH, r0, kk, bh, bh);
       }
-      fold_in(total, acc, [&](int x) { return invDU[r0 + x + g8] * id; });
+      fold_in(total, acc, [&](int x) {
+        return fac[kFeT + r0 + x + g8] * (invU[r0 + x + g8] * id);
+      });
       hh = warp_sum(hh);
       if (lane == 0) red[w8] = hh;
       named_sync(2, 256);  // N
