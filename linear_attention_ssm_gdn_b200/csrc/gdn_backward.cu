@@ -17,8 +17,9 @@
 //   dg_r = <H', dH'> + sum_{s >= r} (q_s . dq_s - v_s . dv_s),
 // the last because e^{G_r} enters only by scaling q_r up and v_r down.
 //
-// Gates reach the exponentials as differences of 64-bit cumulative sums, kept
-// as two floats: a strong decay early in the chunk costs later rows nothing.
+// Gates reach the exponentials as differences of 64-bit cumulative sums (in base
+// 2: exp2f is the shorter function), kept as two floats: a strong decay early in
+// the chunk costs later rows nothing.
 //
 // Arithmetic.  dg, dbeta and dh0 are f32, so everything they depend on is kept
 // to f32 accuracy; a single bf16 or f16 operand would cost three digits.  Every
@@ -70,7 +71,7 @@ struct BwdArgs {
   uint8_t* O;          // [chunk][H_v] f16 tile of dO
   uint8_t* SM;         // [chunk][H_v] S high, S low, M high, M low (M = Q K^T * D)
   float* fac;          // [chunk][H_v][kFac]
-  float2* G;           // [chunk][H_v][64] cumulative gates, high and low part
+  float2* G;           // [chunk][H_v][64] cumulative gates / ln 2, high and low part
   float* u;            // [chunk][H_v][64][D]
   float* E;            // [chunk][H_v][64][D]
   float* H;            // [chunk + sequence][H_v][D / 16][D][16] entry states, then the final one
@@ -86,7 +87,7 @@ constexpr int kFac = 5 * kBC + 8;
 
 __device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(uint32_t(x) << 16); }
 __device__ __forceinline__ float expdiff(float2 a, float2 b) {
-  return expf((a.x - b.x) + (a.y - b.y));
+  return exp2f((a.x - b.x) + (a.y - b.y));
 }
 
 // The rows of chunk i: sequence, first row, number of rows (0 where the row
@@ -205,11 +206,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // Prep: per (chunk, value head), what neither scan's state enters: the f16
 // tiles of K, Q and dO, the gate factors, M and S.
 //
-// K K^T and Q K^T are one pass of MMAs each (exact operands).  S is solved in
-// f32 on the CUDA cores: 16-row blocks, the part left of the diagonal block by
-// all 256 threads (column x 4 rows), the diagonal block by one thread per
-// column.  Bound by latency and by the 64-step chain of that solve; several
-// CTAs per SM hide it.
+// K K^T and Q K^T are one pass of MMAs each (exact operands).  With L_b the
+// diagonal 16 x 16 blocks of B diag(beta), S by block rows:
+//   S_bj = (I + L_b)^-1 (B_bj - sum over j <= c < b of B_bc (diag(beta) S)_cj).
+// The four inverses are solved side by side in f32 on the CUDA cores (a thread a
+// column); the block products are TF32 MMAs in two limbs each (22 bits).  Bound
+// by latency: several CTAs per SM hide it.
 // ---------------------------------------------------------------------------
 
 // 64 x D bf16 rows (row stride in elements) as an f16 tile: loads, finds the
@@ -250,17 +252,55 @@ struct TileIn {
   }
 };
 
-constexpr int kBT = 68;  // row length of the f32 triangles (16-byte rows)
+constexpr int kBT = 68;  // row length of the f32 squares (16-byte rows, 4 banks apart)
 
 template <int D>
 struct PrepSmem {
   static constexpr int kTile = D / 64 * kBlk;
-  static constexpr int K = 0, Q = kTile;       // f16 tiles; later the staged limbs
-  static constexpr int BT = 2 * kTile > 4 * kBlk ? 2 * kTile : 4 * kBlk;  // B transposed
-  static constexpr int S = BT + kBC * kBT * 4;   // S
-  static constexpr int SB = S + kBC * kBT * 4;   // diag(beta) S
-  static constexpr int kBytes = SB + kBC * kBT * 4;
+  static constexpr int K = 0, Q = kTile;       // f16 tiles; later the limbs of S and M
+  static constexpr int B = 2 * kTile > 4 * kBlk ? 2 * kTile : 4 * kBlk;
+  static constexpr int S = B + kBC * kBT * 4;
+  static constexpr int T = S + kBC * kBT * 4;  // [4][16][20] the diagonal blocks' inverses
+  static constexpr int kBytes = T + 4 * 16 * 20 * 4;
 };
+
+// x as two TF32 limbs.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  const float rest = x - __uint_as_float(hi);
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
+}
+__device__ __forceinline__ void mma8_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// acc (16 x 16, two tiles) += A (16 x 16, row length la) diag(f) B (16 x 16, row length kBT),
+// with `negate` minus it; f may be NULL (ones).
+__device__ __forceinline__ void block_product(float (&acc)[2][4], const float* A, int la,
+                                              const float* f, const float* Bm, bool negate) {
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int k0 = 0; k0 < 16; k0 += 8) {
+    float x[4] = {A[g8 * la + k0 + t], A[(g8 + 8) * la + k0 + t], A[g8 * la + k0 + t + 4],
+                  A[(g8 + 8) * la + k0 + t + 4]};
+    if (f != nullptr) x[0] *= f[k0 + t], x[1] *= f[k0 + t], x[2] *= f[k0 + t + 4], x[3] *= f[k0 + t + 4];
+    uint32_t ah[4], al[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_tf32(negate ? -x[e] : x[e], ah[e], al[e]);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      uint32_t h0, l0, h1, l1;
+      split_tf32(Bm[(k0 + t) * kBT + 8 * n + g8], h0, l0);
+      split_tf32(Bm[(k0 + t + 4) * kBT + 8 * n + g8], h1, l1);
+      mma8_tf32(acc[n], al, h0, h1);
+      mma8_tf32(acc[n], ah, l0, l1);
+      mma8_tf32(acc[n], ah, h0, h1);
+    }
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
@@ -286,17 +326,18 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
     ot.load(a.dout + (size_t(c.row0) * a.H_v + h) * D, size_t(a.H_v) * D, c.rows, &most[2]);
     if (warp == 0) {  // two rows per lane; 64-bit sums
       double x[2];
+      float bt[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 2 * lane + e;
-        float gv = 0.f, bv = 0.f;
+        float gv = 0.f;
+        bt[e] = 0.f;
         if (r < c.rows) {
           gv = a.g[size_t(c.row0 + r) * a.gb_stride + h];
-          bv = a.beta[size_t(c.row0 + r) * a.gb_stride + h];
+          bt[e] = a.beta[size_t(c.row0 + r) * a.gb_stride + h];
         }
-        x[e] = gv < kGateFloor ? kGateFloor : gv;
-        bs[r] = bv;
-        fac[kFbeta + r] = bv;
+        x[e] = (gv < kGateFloor ? kGateFloor : gv) * 1.4426950408889634;
+        bs[r] = bt[e];
       }
       x[1] += x[0];
       double run = x[1];
@@ -314,14 +355,14 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
         const float2 G = make_float2(hi, float(x[e] - double(hi)));
         Gs[2 * lane + e] = G;
         a.G[unit * kBC + 2 * lane + e] = G;
-        const float eG = expf(G.x + G.y), eT = expf(float(total - x[e]));
-        const float bt = bs[2 * lane + e];
+        const float eG = exp2f(G.x + G.y), eT = exp2f(float(total - x[e]));
         fac[kFeG + 2 * lane + e] = eG;
         fac[kFeT + 2 * lane + e] = eT;
-        fac[kFbT + 2 * lane + e] = bt * eT;
-        fac[kFbG + 2 * lane + e] = bt * eG;
+        fac[kFbeta + 2 * lane + e] = bt[e];
+        fac[kFbT + 2 * lane + e] = bt[e] * eT;
+        fac[kFbG + 2 * lane + e] = bt[e] * eG;
       }
-      if (lane == 0) fac[kFeC] = expf(float(total));
+      if (lane == 0) fac[kFeC] = exp2f(float(total));
     }
     __syncthreads();
     float inv;
@@ -336,116 +377,130 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
     ot.store(s, 0, a.O + unit * L::kTile);
   }
   __syncthreads();
-  // Warps 0-3: 16 rows of K K^T each; warps 4-7: of Q K^T.  Lower blocks only.
-  const int rb = warp & 3, g8 = lane >> 2, t2 = 2 * (lane & 3);
-  const bool isq = warp >= 4;
-  float acc[8][4] = {};
-  {
-    const uint32_t ta = base + (isq ? L::Q : L::K);
+  // K K^T and Q K^T: warp = 16 rows, every other 16-column block up to the diagonal
+  const int rb = warp >> 1, par = warp & 1, g8 = lane >> 2, t2 = 2 * (lane & 3);
+  float kk_[4][4] = {}, qk[4][4] = {};
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      uint32_t av[4];
-      ldsm4(av, piece<false>(ta, 16 * rb, 16 * kk));
+  for (int kk = 0; kk < D / 16; ++kk) {
+    uint32_t ak[4], aq[4];
+    ldsm4(ak, piece<false>(base + L::K, 16 * rb, 16 * kk));
+    ldsm4(aq, piece<false>(base + L::Q, 16 * rb, 16 * kk));
 #pragma unroll
-      for (int np = 0; np < 4; ++np)
-        if (np <= rb) {
-          uint32_t bv[4];
-          ldsm4(bv, piece<true>(base + L::K, 16 * np, 16 * kk));
-          mma16(acc[2 * np], av, bv[0], bv[1]);
-          mma16(acc[2 * np + 1], av, bv[2], bv[3]);
-        }
-    }
+    for (int j = 0; j < 2; ++j)
+      if (2 * j + par <= rb) {
+        uint32_t bv[4];
+        ldsm4(bv, piece<true>(base + L::K, 16 * (2 * j + par), 16 * kk));
+        mma16(kk_[2 * j], ak, bv[0], bv[1]);
+        mma16(kk_[2 * j + 1], ak, bv[2], bv[3]);
+        mma16(qk[2 * j], aq, bv[0], bv[1]);
+        mma16(qk[2 * j + 1], aq, bv[2], bv[3]);
+      }
   }
-  float* BT = reinterpret_cast<float*>(smem + L::BT);
+  float* B = reinterpret_cast<float*>(smem + L::B);
   float* S = reinterpret_cast<float*>(smem + L::S);
-  float* SB = reinterpret_cast<float*>(smem + L::SB);
+  float* T = reinterpret_cast<float*>(smem + L::T);
   float invk, invq;
   pow2_scale(__uint_as_float(most[0]), &invk);
   pow2_scale(__uint_as_float(most[1]), &invq);
   float big = 0.f;
 #pragma unroll
-  for (int n = 0; n < 8; ++n)
+  for (int j = 0; j < 4; ++j) {
+    const int s0 = 32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2;
+    if (2 * (j >> 1) + par <= rb) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = 16 * rb + g8 + (e >> 1) * 8, s = 8 * n + t2 + (e & 1);
-      float x = 0.f;
-      if (s <= r) x = acc[n][e] * invk * (isq ? invq : invk) * expdiff(Gs[r], Gs[s]);
-      if (!isq) {
-        if (s >= r) x = 0.f;
-        BT[s * kBT + r] = x;
-        S[r * kBT + s] = x;  // the substitution starts from B
+      for (int e = 0; e < 4; ++e) {
+        const int r = 16 * rb + g8 + (e >> 1) * 8, s = s0 + (e & 1);
+        const float d = s <= r ? expdiff(Gs[r], Gs[s]) * invk : 0.f;
+        kk_[j][e] = s < r ? kk_[j][e] * invk * d : 0.f;
+        qk[j][e] = s <= r ? qk[j][e] * invq * d : 0.f;
+        big = max_nan(big, fabsf(qk[j][e]));
       }
-      acc[n][e] = x;
-      big = max_nan(big, fabsf(x));
+#pragma unroll
+      for (int e = 0; e < 4; e += 2)
+        *reinterpret_cast<float2*>(&B[(16 * rb + g8 + (e >> 1) * 8) * kBT + s0]) =
+            make_float2(kk_[j][e], kk_[j][e + 1]);
     }
-  if (isq) {
-    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-    if (lane == 0) atomicMax(&most[3], __float_as_uint(big));
   }
-  __syncthreads();  // K and Q tiles are free from here
-  if (isq) {
-    float inv;
-    const float s = pow2_scale(__uint_as_float(most[3]), &inv);
-    if (tid == 128) fac[kFinvM] = inv;
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const int r = 16 * rb + g8 + (e >> 1) * 8;
-        uint32_t hi, lo;
-        split_f16(acc[n][e] * s, acc[n][e + 1] * s, hi, lo);
-        const uint32_t at = sw128_offset(r, (8 * n + t2) * 2);
-        *reinterpret_cast<uint32_t*>(smem + 2 * kBlk + at) = hi;
-        *reinterpret_cast<uint32_t*>(smem + 3 * kBlk + at) = lo;
-      }
-  }
-  // S = B - B (diag(beta) S), 16 rows at a time
+  big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+  if (lane == 0) atomicMax(&most[3], __float_as_uint(big));
+  __syncthreads();  // B; the K and Q tiles are free from here
   {
-    const int j = tid & 63, p = tid >> 6;
-    for (int b = 0; b < 4; ++b) {
-      if (b > 0) {
-        float x[4];
-        const int r = 16 * b + 4 * p;
+    float inv;
+    const float sc = pow2_scale(__uint_as_float(most[3]), &inv);
+    if (tid == 0) fac[kFinvM] = inv;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = S[(r + e) * kBT + j];
-#pragma unroll 8
-        for (int s = 0; s < 16 * b; ++s) {
-          const float sv = SB[s * kBT + j];
-          const float4 b4 = *reinterpret_cast<const float4*>(&BT[s * kBT + r]);
-          x[0] = fmaf(-b4.x, sv, x[0]);
-          x[1] = fmaf(-b4.y, sv, x[1]);
-          x[2] = fmaf(-b4.z, sv, x[2]);
-          x[3] = fmaf(-b4.w, sv, x[3]);
+    for (int j = 0; j < 4; ++j)
+      if (2 * (j >> 1) + par <= rb)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          uint32_t hi, lo;
+          split_f16(qk[j][e] * sc, qk[j][e + 1] * sc, hi, lo);
+          const uint32_t at = sw128_offset(16 * rb + g8 + (e >> 1) * 8,
+                                           (32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2) * 2);
+          *reinterpret_cast<uint32_t*>(smem + 2 * kBlk + at) = hi;
+          *reinterpret_cast<uint32_t*>(smem + 3 * kBlk + at) = lo;
         }
+  }
+  // The inverses of I + L_b: thread = (block, column), forward substitution
+  if (tid < kBC) {
+    const int b = tid >> 4, j = tid & 15;
+    float x[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[(r + e) * kBT + j] = x[e];
-        __syncthreads();
-      }
-      if (p == 0) {
-        float x[16];
+    for (int r = 0; r < 16; ++r) {
+      float y = r == j ? 1.f : 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = S[(16 * b + e) * kBT + j];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float sb = bs[16 * b + e] * x[e];
-          SB[(16 * b + e) * kBT + j] = sb;
-#pragma unroll
-          for (int f = e + 1; f < 16; ++f)
-            x[f] = fmaf(-BT[(16 * b + e) * kBT + 16 * b + f], sb, x[f]);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) S[(16 * b + e) * kBT + j] = x[e];
-      }
-      __syncthreads();
+      for (int q = 0; q < r; ++q)
+        y = fmaf(-B[(16 * b + r) * kBT + 16 * b + q], x[q], y);
+      T[(b * 16 + r) * 20 + j] = y;
+      x[r] = y * bs[16 * b + r];  // L_b's columns carry beta
     }
   }
-  // S as limbs: 8 pairs a thread
+  __syncthreads();
+  for (int b = 0; b < 4; ++b) {
+    if (warp <= b) {  // block (b, j = warp)
+      const int j = warp;
+      float acc[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[n][e] = B[(16 * b + g8 + (e >> 1) * 8) * kBT + 16 * j + 8 * n + t2 + (e & 1)];
+      for (int cc = j; cc < b; ++cc)
+        block_product(acc, B + 16 * b * kBT + 16 * cc, kBT, bs + 16 * cc,
+                      S + 16 * cc * kBT + 16 * j, true);
+      // the right-hand side, then (I + L_b)^-1 times it, both in this block's place
+      float* out = S + 16 * b * kBT + 16 * j;
+#pragma unroll
+      for (int round = 0; round < 2; ++round) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2)
+            *reinterpret_cast<float2*>(&out[(g8 + (e >> 1) * 8) * kBT + 8 * n + t2]) =
+                make_float2(acc[n][e], acc[n][e + 1]);
+        __syncwarp();
+        if (round == 0) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+          block_product(acc, T + b * 16 * 20, 20, nullptr, out, false);
+          __syncwarp();
+        }
+      }
+    }
+    __syncthreads();
+  }
+  // S as limbs: warp = 16 rows, half of the columns up to the diagonal block
   float2 sv[8];
+  const int cols = 8 * (rb + 1);  // this warp's share of 16 (rb + 1) columns
   big = 0.f;
 #pragma unroll
   for (int m = 0; m < 8; ++m) {
-    const int x = tid + 256 * m;
-    sv[m] = *reinterpret_cast<const float2*>(&S[(x >> 5) * kBT + 2 * (x & 31)]);
+    // 16 rows x cols / 2 pairs; lane = (row of 8, pair of 4)
+    const int r = 16 * rb + g8 + 8 * (m & 1), s = par * cols + 8 * (m >> 1) + t2;
+    sv[m] = make_float2(0.f, 0.f);
+    if ((m >> 1) <= rb) sv[m] = *reinterpret_cast<const float2*>(&S[r * kBT + s]);
     big = max_nan(big, max_nan(fabsf(sv[m].x), fabsf(sv[m].y)));
   }
   big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
@@ -453,19 +508,21 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
   __syncthreads();
   {
     float inv;
-    const float s = pow2_scale(__uint_as_float(most[4]), &inv);
+    const float sc = pow2_scale(__uint_as_float(most[4]), &inv);
     if (tid == 0) fac[kFinvS] = inv;
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const int x = tid + 256 * m;
-      uint32_t hi, lo;
-      split_f16(sv[m].x * s, sv[m].y * s, hi, lo);
-      const uint32_t at = sw128_offset(x >> 5, 4 * (x & 31));
-      *reinterpret_cast<uint32_t*>(smem + at) = hi;
-      *reinterpret_cast<uint32_t*>(smem + kBlk + at) = lo;
-    }
+    for (int m = 0; m < 8; ++m)
+      if ((m >> 1) <= rb) {
+        const int r = 16 * rb + g8 + 8 * (m & 1), s = par * cols + 8 * (m >> 1) + t2;
+        uint32_t hi, lo;
+        split_f16(sv[m].x * sc, sv[m].y * sc, hi, lo);
+        const uint32_t at = sw128_offset(r, 2 * s);
+        *reinterpret_cast<uint32_t*>(smem + at) = hi;
+        *reinterpret_cast<uint32_t*>(smem + kBlk + at) = lo;
+      }
   }
   __syncthreads();
+  // (blocks above the diagonal are never read: whatever they hold goes along)
   uint4* out = reinterpret_cast<uint4*>(a.SM + unit * 4 * kBlk);
 #pragma unroll
   for (int x = tid; x < 4 * kBlk / 16; x += 256) out[x] = reinterpret_cast<const uint4*>(smem)[x];
@@ -879,7 +936,8 @@ struct GradsSmem {
   static constexpr int DH = H + D / 16 * kSlice;  // the first D / 16 - 4 slices of dH'
   static constexpr int Fac = DH + (D / 16 - 4) * kSlice;  // two buffers of the unit's factors
   static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
-  static constexpr int F = G + 2 * kBC * 8;      // floats from here
+  static constexpr int M = G + 2 * kBC * 8;      // two buffers of the states' largest values
+  static constexpr int F = M + 2 * D / 4 * 4;    // floats from here
   static constexpr int kFloats = 2 * kBC + (D / 16) * kBC + kBC + 16;
   static constexpr int kBytes = F + kFloats * 4;
   // Where slice x of dH' is: the last four go where beta u's low limb was (its
@@ -964,6 +1022,8 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
       cp_async16(base + L::Fac + p * kFac * 4 + tid * 16, a.fac + unit * kFac + tid * 4);
     else if (tid >= 128 && tid < 128 + kBC / 2)
       cp_async16(base + L::G + p * kBC * 8 + (tid - 128) * 16, a.G + unit * kBC + (tid - 128) * 2);
+    else if (tid >= 192 && tid < 192 + D / 16)
+      cp_async16(base + L::M + p * D + (tid - 192) * 16, a.Hmax + unit * (D / 4) + (tid - 192) * 4);
   };
   // two slices of a state from slice x, by warps 8-15, whose own waits cover them
   auto load_slices = [&](uint32_t dst, const float* state, int x) {
@@ -1129,7 +1189,7 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
             }
           }
     }
-    const float* hm = a.Hmax + unit * 4 * CG;
+    const float* hm = reinterpret_cast<const float*>(smem + L::M) + (h & 1) * (D / 4);
     float m0 = 0.f, ih;
 #pragma unroll
     for (int x = 0; x < 2 * CG; ++x) m0 = max_nan(m0, hm[x]);
@@ -1203,6 +1263,16 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
           x += __shfl_xor_sync(0xffffffffu, x, 2);
           if ((lane & 3) == 0) part[cg * kBC + rr] = x * iq;
         }
+      // <H', dH'>, while the other half is at its longer products
+      float hh = 0.f;
+#pragma unroll 4
+      for (int x = 4 * tid; x < D * D; x += 1024) {
+        const float4 y = *reinterpret_cast<const float4*>(H1 + x);
+        const float4 z = *reinterpret_cast<const float4*>(dH + x);
+        hh += fmaf(y.x, z.x, y.y * z.y) + fmaf(y.z, z.z, y.w * z.w);
+      }
+      hh = warp_sum(hh);
+      if (lane == 0) red[w8] = hh;
     } else {
       // -(e^G beta E) H^T
 #pragma unroll
@@ -1225,12 +1295,11 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
       cp_async_commit();
       cp_async_wait<1>();  // the two slices before them
       named_sync(2, 256);
-      // (e^{G_C - G} beta u) dH'^T, and <H', dH'> on the way (each value once)
-      float m1 = 0.f, id, hh = 0.f;
+      // (e^{G_C - G} beta u) dH'^T
+      float m1 = 0.f, id;
 #pragma unroll
       for (int x = 0; x < 2 * CG; ++x) m1 = max_nan(m1, hm[2 * CG + x]);
       const float sd = pow2_scale(m1, &id);
-      const float* H1p = H1 + at / 4;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         if (kk == D / 16 - 2) {
@@ -1244,19 +1313,12 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
               *reinterpret_cast<const float4*>(smem + L::dh_slice(kk) + at + 512 * n);
           bh[2 * n] = pack_f16(x.x * sd, x.y * sd);
           bh[2 * n + 1] = pack_f16(x.z * sd, x.w * sd);
-          if (r0 == 0) {
-            const float4 y =
-                *reinterpret_cast<const float4*>(H1p + kk * (L::kSlice / 4) + 128 * n);
-            hh += fmaf(x.x, y.x, x.y * y.y) + fmaf(x.z, y.z, x.w * y.w);
-          }
         }
         rows_times<MT, false>(acc, base + L::UH, r0, kk, bh, bh);
       }
       fold_in(total, acc, [&](int x) {
         return fac[kFeT + r0 + x + g8] * (invU[r0 + x + g8] * id);
       });
-      hh = warp_sum(hh);
-      if (lane == 0) red[w8] = hh;
       named_sync(2, 256);  // N
       // N K and N^T K
 #pragma unroll
@@ -1323,7 +1385,7 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
       }
       double hh = 0.0;
 #pragma unroll
-      for (int w = 0; w < CG; ++w) hh += red[w];
+      for (int w = 0; w < 8; ++w) hh += red[w];
       x[0] += run - x[1];
       x[1] = run;
 #pragma unroll
