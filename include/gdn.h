@@ -447,7 +447,7 @@ int gdn_chunk_backward(const uint16_t* q, const uint16_t* k, int qk_stride, cons
 /* --------------------------------------------------------------------------
  * gdn_debug_device_errors -- diagnostics, not part of the hot path.
  * Copies the library's four device-side error words (BA gates, prefill,
- * verify/fold, reserved) into host memory `out4` and clears them.  Bit 64 of
+ * verify/fold, backward) into host memory `out4` and clears them.  Bit 64 of
  * the prefill word means a gate rise beyond the documented bound (see
  * gdn_chunk_prefill); every other set bit means a bounded wait inside a kernel
  * gave up (the kernel then returned early instead of hanging).  This call

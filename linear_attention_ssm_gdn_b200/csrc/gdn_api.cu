@@ -77,10 +77,10 @@ int sm_count() {
 static cudaError_t read_device_errors(uint32_t* out4) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return e;
-  out4[3] = 0;
   if ((e = take_err_ba_gates(&out4[0])) != cudaSuccess) return e;
   if ((e = take_err_prefill(&out4[1])) != cudaSuccess) return e;
-  return take_err_verify(&out4[2]);
+  if ((e = take_err_verify(&out4[2])) != cudaSuccess) return e;
+  return take_err_backward(&out4[3]);
 }
 
 }  // namespace gdn

@@ -31,12 +31,10 @@
 // (lo x lo is below the f32 rounding).  What reaches only dq or dk, which are
 // rounded to bf16 (2^-9), takes one limb (2^-12).
 //
-// The MMAs are warp-level (mma.sync m16n8k16).  tcgen05 has four times their
-// rate, but the scans' chains are register-resident here: the state's
-// accumulator fragment is the next product's A fragment, so nothing of the
-// chain passes through tensor or shared memory and no warp waits for another
-// one's product; and splitting a head's value columns over 16-column warps
-// costs no efficiency (M = 16, where tcgen05 wants 128).
+// The scans, a chain of three dependent products a chunk, run on tcgen05 with the
+// state in registers and its limbs in tensor memory.  The chunk-parallel kernels
+// before and after them use warp-level MMAs: their operands change shape and
+// precision from product to product, and many warps hide the latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -69,20 +67,22 @@ struct BwdArgs {
   int max_chunks;
   uint8_t* KQ;         // [chunk][H_k] f16 tiles of K, then of Q
   uint8_t* O;          // [chunk][H_v] f16 tile of dO
-  uint8_t* SM;         // [chunk][H_v] S high, S low, M high, M low (M = Q K^T * D)
+  uint8_t* GO;         // [chunk][H_v] scale e^G dO, high and low tile
+  uint8_t* S;          // [chunk][H_v] S, high and low block
+  float* Y0;           // [chunk][H_v][64][D] scale (Q K^T * D)^T dO
   float* fac;          // [chunk][H_v][kFac]
   float2* G;           // [chunk][H_v][64] cumulative gates / ln 2, high and low part
   float* u;            // [chunk][H_v][64][D]
   float* E;            // [chunk][H_v][64][D]
   float* H;            // [chunk + sequence][H_v][D / 16][D][16] entry states, then the final one
   float* dH;           // [chunk][H_v][D / 16][D][16] gradient of the exit state
-  float* Hmax;         // [chunk][H_v][2][D / 8] largest |H| and |dH| of each scan warp's part
+  float* Hmax;         // [chunk][H_v][2][8] largest |H| and |dH| of each scan warp's part
 };
 
 // Per-unit factors: of each row e^G, e^{G_C - G}, beta and the products beta
 // e^{G_C - G} and beta e^G, then scalars.
 enum { kFeG = 0, kFeT = kBC, kFbeta = 2 * kBC, kFbT = 3 * kBC, kFbG = 4 * kBC,
-       kFeC = 5 * kBC, kFinvK, kFinvQ, kFinvO, kFinvS, kFinvM };
+       kFeC = 5 * kBC, kFinvK, kFinvQ, kFinvO, kFinvS, kFinvGO };
 constexpr int kFac = 5 * kBC + 8;
 
 __device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(uint32_t(x) << 16); }
@@ -124,10 +124,18 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 __device__ __forceinline__ float2 unpack_f16(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
+// a and b as two limbs: hi = f16(x), lo = f16(x - hi).
 __device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = pack_f16(a, b);
-  const float2 f = unpack_f16(hi);
-  lo = pack_f16(a - f.x, b - f.y);
+  float x, y;  // x - hi with hi read as f16 (exact: it is below half a step of hi)
+  asm("{\n\t.reg .b16 l, h, m;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "mov.b16 m, 0xBC00;\n\t"
+      "fma.rn.f32.f16 %0, l, m, %3;\n\t"
+      "fma.rn.f32.f16 %1, h, m, %4;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "r"(hi), "f"(a), "f"(b));
+  lo = pack_f16(x, y);
 }
 
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -250,6 +258,37 @@ struct TileIn {
       if (out != nullptr) *reinterpret_cast<uint4*>(out + at) = make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
+  // The largest |f[row] x| of the tile, and f[row] x as two limb tiles.
+  __device__ __forceinline__ void most_scaled(const float* f, uint32_t* most) const {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const float fr = f[(threadIdx.x + 256 * i) / (D / 8)];
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        m = max_nan(m, max_nan(fabsf(__uint_as_float(w[j] << 16) * fr),
+                               fabsf(__uint_as_float(w[j] & 0xffff0000u) * fr)));
+    }
+    const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    if ((threadIdx.x & 31) == 0) atomicMax(most, u);
+  }
+  __device__ __forceinline__ void store_limbs(const float* f, float s, uint8_t* out) const {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int p = threadIdx.x + 256 * i, r = p / (D / 8), c = 8 * (p % (D / 8));
+      const float fr = f[r];
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        split_f16(__uint_as_float(w[j] << 16) * fr * s,
+                  __uint_as_float(w[j] & 0xffff0000u) * fr * s, h[j], l[j]);
+      const uint32_t at = (c >> 6) * kBlk + sw128_offset(r, (c & 63) * 2);
+      *reinterpret_cast<uint4*>(out + at) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(out + D / 64 * kBlk + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+  }
 };
 
 constexpr int kBT = 68;  // row length of the f32 squares (16-byte rows, 4 banks apart)
@@ -257,7 +296,8 @@ constexpr int kBT = 68;  // row length of the f32 squares (16-byte rows, 4 banks
 template <int D>
 struct PrepSmem {
   static constexpr int kTile = D / 64 * kBlk;
-  static constexpr int K = 0, Q = kTile;       // f16 tiles; later the limbs of S and M
+  static constexpr int K = 0, Q = kTile;       // f16 tiles; later dO, then the limbs of S
+  static constexpr int M = 2 * kBlk;           // later, over Q: the limbs of M
   static constexpr int B = 2 * kTile > 4 * kBlk ? 2 * kTile : 4 * kBlk;
   static constexpr int S = B + kBC * kBT * 4;
   static constexpr int T = S + kBC * kBT * 4;  // [4][16][20] the diagonal blocks' inverses
@@ -307,8 +347,8 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
   using L = PrepSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float2 Gs[kBC];
-  __shared__ float bs[kBC];
-  __shared__ uint32_t most[5];  // K, Q, dO, M, S
+  __shared__ float bs[kBC], eGs[kBC];
+  __shared__ uint32_t most[6];  // K, Q, dO, M, S, e^G dO
   const int i = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
@@ -317,10 +357,11 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
   const uint32_t base = smem_u32(smem);
   float* fac = a.fac + unit * kFac;
   uint8_t* kq = h % vpg == 0 ? a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile : nullptr;
-  if (tid < 5) most[tid] = 0;
+  if (tid < 6) most[tid] = 0;
   __syncthreads();
+  TileIn<D> ot;
   {
-    TileIn<D> kt, qt, ot;
+    TileIn<D> kt, qt;
     kt.load(a.k + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows, &most[0]);
     qt.load(a.q + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows, &most[1]);
     ot.load(a.dout + (size_t(c.row0) * a.H_v + h) * D, size_t(a.H_v) * D, c.rows, &most[2]);
@@ -357,6 +398,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
         a.G[unit * kBC + 2 * lane + e] = G;
         const float eG = exp2f(G.x + G.y), eT = exp2f(float(total - x[e]));
         fac[kFeG + 2 * lane + e] = eG;
+        eGs[2 * lane + e] = a.scale * eG;
         fac[kFeT + 2 * lane + e] = eT;
         fac[kFbeta + 2 * lane + e] = bt[e];
         fac[kFbT + 2 * lane + e] = bt[e] * eT;
@@ -375,8 +417,15 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
     s = pow2_scale(__uint_as_float(most[2]), &inv);
     if (tid == 0) fac[kFinvO] = inv;
     ot.store(s, 0, a.O + unit * L::kTile);
+    ot.most_scaled(eGs, &most[5]);
   }
   __syncthreads();
+  {
+    float inv;
+    const float s = pow2_scale(__uint_as_float(most[5]), &inv);
+    if (tid == 0) fac[kFinvGO] = inv;
+    ot.store_limbs(eGs, s, a.GO + unit * 2 * L::kTile);
+  }
   // K K^T and Q K^T: warp = 16 rows, every other 16-column block up to the diagonal
   const int rb = warp >> 1, par = warp & 1, g8 = lane >> 2, t2 = 2 * (lane & 3);
   float kk_[4][4] = {}, qk[4][4] = {};
@@ -424,10 +473,10 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
   big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
   if (lane == 0) atomicMax(&most[3], __float_as_uint(big));
   __syncthreads();  // B; the K and Q tiles are free from here
+  float invm, invo;
+  ot.store(pow2_scale(__uint_as_float(most[2]), &invo), base, nullptr);
   {
-    float inv;
-    const float sc = pow2_scale(__uint_as_float(most[3]), &inv);
-    if (tid == 0) fac[kFinvM] = inv;
+    const float sc = pow2_scale(__uint_as_float(most[3]), &invm);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (2 * (j >> 1) + par <= rb)
@@ -437,8 +486,8 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
           split_f16(qk[j][e] * sc, qk[j][e + 1] * sc, hi, lo);
           const uint32_t at = sw128_offset(16 * rb + g8 + (e >> 1) * 8,
                                            (32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2) * 2);
-          *reinterpret_cast<uint32_t*>(smem + 2 * kBlk + at) = hi;
-          *reinterpret_cast<uint32_t*>(smem + 3 * kBlk + at) = lo;
+          *reinterpret_cast<uint32_t*>(smem + L::M + at) = hi;
+          *reinterpret_cast<uint32_t*>(smem + L::M + kBlk + at) = lo;
         }
   }
   // The inverses of I + L_b: thread = (block, column), forward substitution
@@ -456,6 +505,35 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
     }
   }
   __syncthreads();
+  // Y0 = scale M^T dO: warp = 16 rows s, half of the columns; k-steps from the diagonal
+  {
+    const int mt = warp & 3, c0 = (warp >> 2) * (D / 2);
+    float y[D / 16][4] = {};
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+      if (kk >= mt) {
+        uint32_t ah[4], al[4];
+        ldsm4t(ah, piece<true>(base + L::M, 16 * kk, 16 * mt));
+        ldsm4t(al, piece<true>(base + L::M + kBlk, 16 * kk, 16 * mt));
+#pragma unroll
+        for (int np = 0; np < D / 32; ++np) {
+          uint32_t bv[4];
+          ldsm4t(bv, piece<false>(base, 16 * kk, c0 + 16 * np));
+          mma16(y[2 * np], al, bv[0], bv[1]);
+          mma16(y[2 * np + 1], al, bv[2], bv[3]);
+          mma16(y[2 * np], ah, bv[0], bv[1]);
+          mma16(y[2 * np + 1], ah, bv[2], bv[3]);
+        }
+      }
+    const float f = a.scale * invm * invo;
+    float* out = a.Y0 + (unit * kBC + 16 * mt + g8) * D + c0 + t2;
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2)
+        *reinterpret_cast<float2*>(out + (e >> 1) * 8 * D + 8 * n) =
+            make_float2(y[n][e] * f, y[n][e + 1] * f);
+  }
   for (int b = 0; b < 4; ++b) {
     if (warp <= b) {  // block (b, j = warp)
       const int j = warp;
@@ -491,16 +569,14 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
     }
     __syncthreads();
   }
-  // S as limbs: warp = 16 rows, half of the columns up to the diagonal block
+  // S as limbs: warp = 16 rows, half of the columns; zeros above the diagonal blocks
   float2 sv[8];
-  const int cols = 8 * (rb + 1);  // this warp's share of 16 (rb + 1) columns
   big = 0.f;
 #pragma unroll
   for (int m = 0; m < 8; ++m) {
-    // 16 rows x cols / 2 pairs; lane = (row of 8, pair of 4)
-    const int r = 16 * rb + g8 + 8 * (m & 1), s = par * cols + 8 * (m >> 1) + t2;
+    const int r = 16 * rb + g8 + 8 * (m & 1), s = 32 * par + 8 * (m >> 1) + t2;
     sv[m] = make_float2(0.f, 0.f);
-    if ((m >> 1) <= rb) sv[m] = *reinterpret_cast<const float2*>(&S[r * kBT + s]);
+    if (2 * par + (m >> 2) <= rb) sv[m] = *reinterpret_cast<const float2*>(&S[r * kBT + s]);
     big = max_nan(big, max_nan(fabsf(sv[m].x), fabsf(sv[m].y)));
   }
   big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
@@ -511,405 +587,470 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
     const float sc = pow2_scale(__uint_as_float(most[4]), &inv);
     if (tid == 0) fac[kFinvS] = inv;
 #pragma unroll
-    for (int m = 0; m < 8; ++m)
-      if ((m >> 1) <= rb) {
-        const int r = 16 * rb + g8 + 8 * (m & 1), s = par * cols + 8 * (m >> 1) + t2;
-        uint32_t hi, lo;
-        split_f16(sv[m].x * sc, sv[m].y * sc, hi, lo);
-        const uint32_t at = sw128_offset(r, 2 * s);
-        *reinterpret_cast<uint32_t*>(smem + at) = hi;
-        *reinterpret_cast<uint32_t*>(smem + kBlk + at) = lo;
-      }
+    for (int m = 0; m < 8; ++m) {
+      const int r = 16 * rb + g8 + 8 * (m & 1), s = 32 * par + 8 * (m >> 1) + t2;
+      uint32_t hi, lo;
+      split_f16(sv[m].x * sc, sv[m].y * sc, hi, lo);
+      const uint32_t at = sw128_offset(r, 2 * s);
+      *reinterpret_cast<uint32_t*>(smem + at) = hi;
+      *reinterpret_cast<uint32_t*>(smem + kBlk + at) = lo;
+    }
   }
   __syncthreads();
-  // (blocks above the diagonal are never read: whatever they hold goes along)
-  uint4* out = reinterpret_cast<uint4*>(a.SM + unit * 4 * kBlk);
+  uint4* out = reinterpret_cast<uint4*>(a.S + unit * 2 * kBlk);
 #pragma unroll
-  for (int x = tid; x < 4 * kBlk / 16; x += 256) out[x] = reinterpret_cast<const uint4*>(smem)[x];
+  for (int x = tid; x < 2 * kBlk / 16; x += 256) out[x] = reinterpret_cast<const uint4*>(smem)[x];
 }
 
 // ---------------------------------------------------------------------------
-// Scans: one CTA of 8 warps per (sequence, value head, 64 state columns,
-// direction).  Two warps own 16 columns of H (rows of H^T), each for half of the
-// key rows d_k, for the whole sequence: 8 D f32 in accumulator fragments, which
-// are also the A fragments of the next chunk's product with K.
+// Scans: one CTA per (sequence, value head, direction); the two directions are two
+// kernels that run at the same time (programmatic dependent launch, the backward
+// one, with the longer chain, first).
 //
-// A chain of one warp per scheduler was bound by its own latencies (tensor pipe
-// 32 % busy, 6.9 us a chunk backward); two warps a chain halve it.  The pair
-// meets twice a chunk, through shared memory: to add its two halves of K H, and
-// to trade its shares of u (the S product is split by 16-row column blocks 0, 3
-// and 1, 2, which have equal work).  Per chunk and warp 158 (forward) or 242
-// (backward) MMAs of 8.65 cycles (measured, m16n8k16 with f32 sums).
+// H^T [dv][dk] is held by 8 state warps, thread (dv, half of d_k), 64 f32
+// registers at D = 128.  Per chunk three products, M = 128 (dv), A from tensor
+// memory (the limbs that the state warps write), B the chunk's tiles:
+//   1. H^T K^T -> X (or Y), 2. (beta X)^T S^T -> u (or S: E), 3. (f u)^T K -> H'.
+// A row's limbs have one scale per half (its thread's own maximum), so no warp
+// waits for another one's maximum: the halves go to accumulators of their own,
+// summed when they are read.  The backward scan also has (scale e^G dO)^T Q, from
+// tiles made before, between products 1 and 2.
+//   warps 0-7: state; warp 8: loads (bulk copies into buffers freed by the
+//   products that read them); warp 9: one thread issues the MMAs after the state
+//   warps' barrier.
+// Low limbs are multiplied first: the f32 accumulator then rounds against small
+// sums while it holds them.  D = 64 runs the same code with half of the rows idle.
 //
-// The two scans are two kernels that run at the same time (programmatic
-// dependent launch): the backward one, with the longer chain, first.
+// Bound by the chain: per chunk 16 + 12 + 8 MMAs (55 to 68 cycles each), about
+// 1200 instructions a state warp between them, and three hand-overs each way.
+// The warp-level form of this scan (two warps per 16 columns, state fragments as A
+// operands) needed four times the instructions and 6.2 us a chunk.
 // ---------------------------------------------------------------------------
 
-// acc[n] (8 tiles of 8 rows r) = sum over this warp's d_k of st[dv][dk] K[r][dk],
-// scaled; inv0 / inv1 undo the state rows' scales.  Returns the largest |state|
-// of the thread.
-template <int NT>
-__device__ __forceinline__ float times_k(const float (&st)[NT][4], uint32_t tile, int dk0,
-                                         float (&acc)[8][4], float* inv0, float* inv1) {
-  float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    m0 = max_nan(m0, max_nan(fabsf(st[n][0]), fabsf(st[n][1])));
-    m1 = max_nan(m1, max_nan(fabsf(st[n][2]), fabsf(st[n][3])));
-  }
-  m0 = quad_max(m0), m1 = quad_max(m1);
-  const float s0 = pow2_scale(m0, inv0), s1 = pow2_scale(m1, inv1);
-#pragma unroll
-  for (int n = 0; n < 8; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-#pragma unroll
-  for (int kk = 0; kk < NT / 2; ++kk) {
-    uint32_t hi[4], lo[4];
-    split_f16(st[2 * kk][0] * s0, st[2 * kk][1] * s0, hi[0], lo[0]);
-    split_f16(st[2 * kk][2] * s1, st[2 * kk][3] * s1, hi[1], lo[1]);
-    split_f16(st[2 * kk + 1][0] * s0, st[2 * kk + 1][1] * s0, hi[2], lo[2]);
-    split_f16(st[2 * kk + 1][2] * s1, st[2 * kk + 1][3] * s1, hi[3], lo[3]);
-#pragma unroll
-    for (int np = 0; np < 4; ++np) {
-      uint32_t b[4];
-      ldsm4(b, piece<true>(tile, 16 * np, dk0 + 16 * kk));
-      mma16(acc[2 * np], hi, b[0], b[1]);
-      mma16(acc[2 * np + 1], hi, b[2], b[3]);
-      mma16(acc[2 * np], lo, b[0], b[1]);
-      mma16(acc[2 * np + 1], lo, b[2], b[3]);
-    }
-  }
-  return max_nan(m0, m1);
+constexpr int kScanThreads = 320;
+constexpr int kScanSync = 288;  // the state warps and the issuer
+
+__device__ uint32_t g_err_backward;
+
+// Instruction descriptor as make_idesc_bf16, with f16 operands.
+__host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, int a_mn, int b_mn) {
+  return make_idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
-// x[n][e] (columns r = 8 n + ...) times the column factors f, as A limbs of the
-// four 16-row k-steps; the inverse row scales come back in inv0 / inv1.
-__device__ __forceinline__ void limbs_of(float (&y)[8][4], const float* f, uint32_t (&hi)[4][4],
-                                         uint32_t (&lo)[4][4], float* inv0, float* inv1) {
-  const int t2 = 2 * (threadIdx.x & 3);
-  float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-  for (int n = 0; n < 8; ++n) {
-    const float2 fv = *reinterpret_cast<const float2*>(f + 8 * n + t2);
-    y[n][0] *= fv.x, y[n][1] *= fv.y;
-    y[n][2] *= fv.x, y[n][3] *= fv.y;
-    m0 = max_nan(m0, max_nan(fabsf(y[n][0]), fabsf(y[n][1])));
-    m1 = max_nan(m1, max_nan(fabsf(y[n][2]), fabsf(y[n][3])));
-  }
-  const float s0 = pow2_scale(quad_max(m0), inv0), s1 = pow2_scale(quad_max(m1), inv1);
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) {
-    split_f16(y[2 * kk][0] * s0, y[2 * kk][1] * s0, hi[kk][0], lo[kk][0]);
-    split_f16(y[2 * kk][2] * s1, y[2 * kk][3] * s1, hi[kk][1], lo[kk][1]);
-    split_f16(y[2 * kk + 1][0] * s0, y[2 * kk + 1][1] * s0, hi[kk][2], lo[kk][2]);
-    split_f16(y[2 * kk + 1][2] * s1, y[2 * kk + 1][3] * s1, hi[kk][3], lo[kk][3]);
-  }
-}
+enum { kTX0 = 0, kTX1 = 64, kTH0 = 128, kTH1 = 256, kTA = 384 };  // tensor memory columns
+enum { bKF = 0, bKE = 2, bEF = 4, bQE, bYF, bYE, bSF, bSE, bX, bQ, bS, bH, bDrain, kBars };
 
-// st = decay st + sign (limbs x the tile's columns dk0 ...), the limbs' rows
-// unscaled by inv0 / inv1.
-template <int NT>
-__device__ __forceinline__ void add_product(float (&st)[NT][4], float decay, float inv0,
-                                            float inv1, const uint32_t (&hi)[4][4],
-                                            const uint32_t (&lo)[4][4], uint32_t tile, int dk0) {
-#pragma unroll
-  for (int np = 0; np < NT / 2; ++np) {
-    float y[2][4] = {};
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      uint32_t b[4];
-      ldsm4t(b, piece<false>(tile, 16 * kk, dk0 + 16 * np));
-      mma16(y[0], hi[kk], b[0], b[1]);
-      mma16(y[1], hi[kk], b[2], b[3]);
-      mma16(y[0], lo[kk], b[0], b[1]);
-      mma16(y[1], lo[kk], b[2], b[3]);
-    }
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        st[2 * np + m][e] = fmaf(e < 2 ? inv0 : inv1, y[m][e], decay * st[2 * np + m][e]);
-  }
-}
-
-// Writes a state (C fragments, rows dv0 + g / g + 8) to the workspace: slices of 16
-// columns, [d_k][16], each row as four quads (2t, 2t+1, 2t+8, 2t+9), the B fragment
-// of the products that read it.  Lanes g and g ^ 1 trade halves for 16-byte stores.
-template <int D, int NT>
-__device__ __forceinline__ void store_state(const float (&st)[NT][4], float* out, int dk0,
-                                            int dv0) {
-  const int lane = threadIdx.x & 31, g8 = lane >> 2, t2 = 2 * (lane & 3), odd = g8 & 1;
-  float* p = out + dv0 * D + (dk0 + t2 + odd) * 16 + 4 * (g8 >> 1);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const float x = __shfl_xor_sync(0xffffffffu, odd ? st[n][0] : st[n][1], 4);
-    const float y = __shfl_xor_sync(0xffffffffu, odd ? st[n][2] : st[n][3], 4);
-    *reinterpret_cast<float4*>(p + 8 * n * 16) =
-        odd ? make_float4(x, st[n][1], y, st[n][3]) : make_float4(st[n][0], x, st[n][2], y);
-  }
-}
-
-// Shared memory of a scan CTA.  K is needed at both ends of a chunk and has two
-// buffers; what is needed in the middle is loaded over its last use.
 template <int D, bool back>
 struct ScanSmem {
   static constexpr int kTile = D / 64 * kBlk;
   static constexpr int K = 0;                      // two buffers
   static constexpr int S = 2 * kTile;              // S high, low
-  static constexpr int V = S + 2 * kBlk;           // V (bf16) or dO (f16), 64 columns
-  static constexpr int M = V + kBlk;               // backward: M high, low
-  static constexpr int Q = M + (back ? 2 * kBlk : 0);
-  static constexpr int X = Q + (back ? kTile : 0);  // 8 x 4 KB: what the warp pairs trade
-  static constexpr int Fac = X + 8 * 4096;          // two buffers
-  static constexpr int kBytes = Fac + 2 * kFac * 4;
+  static constexpr int Y = S + 2 * kBlk;           // Y0 (f32) or V (bf16), [64][D]
+  static constexpr int Q = Y + kBC * D * (back ? 4 : 2);
+  static constexpr int GO = Q + (back ? kTile : 0);  // two limbs, M = 128 rows each
+  static constexpr int Fac = GO + (back ? 2 * kTile + (D == 64 ? kBlk : 0) : 0);  // two buffers
+  static constexpr int Inv = Fac + 2 * kFac * 4;   // [3][2][128] inverse row scales
+  static constexpr int Bars = Inv + 3 * 2 * 128 * 4;
+  static constexpr int kUsed = Bars + kBars * 8 + 16 + 1024;  // 1024: alignment of the base
+  // More than half of an SM's: all of its tensor memory goes to one CTA.
+  static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
 };
 
+// N floats times s as limbs: hi to TMEM columns `hi`, lo to `lo` (N / 2 each).
+template <int N>
+__device__ __forceinline__ void limbs_to_tmem(const float (&x)[N], float s, uint32_t hi,
+                                              uint32_t lo) {
+  uint32_t h[N / 2], l[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) split_f16(x[2 * i] * s, x[2 * i + 1] * s, h[i], l[i]);
+  if constexpr (N == 64) {
+    tmem_st32u(hi, h);
+    tmem_st32u(lo, l);
+  } else {
+    tmem_st16u(hi, h);
+    tmem_st16u(lo, l);
+  }
+  tmem_st_wait();
+}
+
+template <int N>
+__device__ __forceinline__ float max_abs_of(const float (&x)[N]) {
+  float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) m0 = max_nan(m0, fabsf(x[i])), m1 = max_nan(m1, fabsf(x[i + 1]));
+  return max_nan(m0, m1);
+}
+
 template <int D, bool back>
-__global__ void __launch_bounds__(256, 2) bwd_scan_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
   using L = ScanSmem<D, back>;
-  constexpr int NT = D / 16;  // 8-row tiles of d_k of a warp
-  extern __shared__ __align__(1024) uint8_t smem[];
-  const int slice = blockIdx.x % (D / 64), h = blockIdx.x / (D / 64) % a.H_v,
-            b = blockIdx.x / (D / 64) / a.H_v;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2,
-            t2 = 2 * (lane & 3);
-  const int rg = warp & 3, hf = warp >> 2;  // 16 columns; half of d_k
-  const int hk = h / (a.H_v / a.H_k);
-  const int c0 = a.cu_chunks[b], n = a.cu_chunks[b + 1] - c0;
-  const int seq_lo = max(a.cu[b], 0), seq_hi = min(a.cu[b + 1], a.total_tokens);
+  constexpr int NK = D / 2;   // d_k columns of a thread
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int seq_at;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem);
-  const int dv0 = 64 * slice + 16 * rg, dk0 = hf * (D / 2);
-  const size_t seq_state = (size_t(b) * a.H_v + h) * D * D;
-  float4* mine = reinterpret_cast<float4*>(smem + L::X + warp * 4096) + lane;
-  float4* other = reinterpret_cast<float4*>(smem + L::X + (warp ^ 4) * 4096) + lane;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::Bars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* err = &g_err_backward;
+  const int tid = threadIdx.x, warp = int(warp_id_sync()), lane = tid & 31;
+  const int h = blockIdx.x % a.H_v, order = blockIdx.x / a.H_v, hk = h / (a.H_v / a.H_k);
   if constexpr (back) asm volatile("griddepcontrol.launch_dependents;");
 
+  // Long sequences first: the order-th longest (for up to 64 of them).
+  if (tid == 0) {
+    seq_at = order;
+    for (int b = 0; b < kBars; ++b) mbar_init(&bars[b], b == bYF && !back ? 32u : 1u);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(tmem_slot, 512);
+  __syncthreads();
+  if (a.num_seqs <= 64 && tid < a.num_seqs) {
+    const int len = a.cu[tid + 1] - a.cu[tid];
+    int rank = 0;
+    for (int j = 0; j < a.num_seqs; ++j) {
+      const int other = a.cu[j + 1] - a.cu[j];
+      rank += other > len || (other == len && j < tid);
+    }
+    if (rank == order) seq_at = tid;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int b = seq_at;
+  const int c0 = a.cu_chunks[b], n = a.cu_chunks[b + 1] - c0;
   auto chunk_of = [&](int t) { return c0 + (back ? n - 1 - t : t); };
-  auto load_k = [&](int t) {  // K and the factors
-    const int i = chunk_of(t);
-    cp_async_block<256>(base + L::K + (t & 1) * L::kTile,
-                        a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile, L::kTile);
-    if (tid < kFac / 4)
-      cp_async16(base + L::Fac + (t & 1) * kFac * 4 + tid * 16,
-                 a.fac + (size_t(i) * a.H_v + h) * kFac + tid * 4);
-    cp_async_commit();
-  };
-  auto load_early = [&](int t) {  // backward: what is read before the first meeting
-    if constexpr (back) {
+
+  if (warp < 8) {
+    const int hh = warp >> 2, dv = 32 * (warp & 3) + lane;
+    const bool on = dv < D;
+    const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);  // this warp's TMEM lanes
+    float* inv_h = reinterpret_cast<float*>(smem + L::Inv);        // [2][128] each
+    float *inv_x = inv_h + 256, *inv_w = inv_x + 256;
+    const size_t head = (size_t(b) * a.H_v + h) * D * D;
+    // where (dv, dk = 0) is in a state of the workspace
+    const int ws = (dv >> 4) * D * 16 + 4 * ((dv & 7) >> 1) + (dv & 1) + 2 * ((dv >> 3) & 1);
+    float st[NK];
+    {
+      const float* init = back ? a.dhT : a.h0;
+#pragma unroll
+      for (int i = 0; i < NK; ++i)
+        st[i] = init != nullptr && on ? init[head + size_t(NK * hh + i) * D + dv] : 0.f;
+    }
+    bool ok = true;
+    int t = 0;
+    for (; t < n; ++t) {
       const int i = chunk_of(t);
       const size_t unit = size_t(i) * a.H_v + h;
-      cp_async_block<256>(base + L::Q, a.KQ + ((size_t(i) * a.H_k + hk) * 2 + 1) * L::kTile,
-                          L::kTile);
-      cp_async_block<256>(base + L::M, a.SM + (unit * 4 + 2) * kBlk, 2 * kBlk);
-      cp_async_block<256>(base + L::V, a.O + unit * L::kTile + slice * kBlk, kBlk);
-    }
-    cp_async_commit();
-  };
-  auto load_late = [&](int t) {  // what is read between the meetings
-    const size_t unit = size_t(chunk_of(t)) * a.H_v + h;
-    cp_async_block<256>(base + L::S, a.SM + unit * 4 * kBlk, 2 * kBlk);
-    if constexpr (!back) {
-      const int row0 = seq_lo + kBC * t, rows = max(0, min(kBC, seq_hi - row0));
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int r = (tid >> 3) + 32 * m, p = tid & 7;
-        const uint16_t* src = a.v + h * D + 64 * slice + 8 * p;
-        cp_async16(base + L::V + sw128_offset(r, 16 * p),
-                   r < rows ? src + size_t(row0 + r) * a.v_stride : src, r < rows);
+      const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (t & 1) * kFac;
+      // 1. the state's limbs
+      const float most = max_abs_of(st);
+      {
+        float inv;
+        const float s = pow2_scale(most, &inv);
+        inv_h[128 * hh + dv] = inv;
+        limbs_to_tmem(st, s, tl + kTA + NK / 2 * hh, tl + kTA + 64 + NK / 2 * hh);
       }
-    }
-    cp_async_commit();
-  };
-
-  float st[NT][4];
-  const float* init = back ? a.dhT : a.h0;
+      tc_fence_before();
+      if (!named_all(1, kScanSync, ok)) break;
+      {
+        float* out = back ? a.dH + unit * D * D : a.H + (size_t(i + b) * a.H_v + h) * D * D;
+        if (on) {
 #pragma unroll
-  for (int m = 0; m < NT; ++m)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      st[m][e] = init == nullptr ? 0.f
-          : init[seq_state + size_t(dk0 + 8 * m + t2 + (e & 1)) * D + dv0 + g8 + (e >> 1) * 8];
-  if (n > 0) {
-    load_k(0);
-    load_early(0);
-    load_late(0);
-    cp_async_wait<1>();
-    __syncthreads();
-  }
-  for (int t = 0; t < n; ++t) {
-    const int i = chunk_of(t);
-    const size_t unit = size_t(i) * a.H_v + h;
-    const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (t & 1) * kFac;
-    const uint32_t tk = base + L::K + (t & 1) * L::kTile;
-    if (t + 1 < n)
-      load_k(t + 1);
-    else
-      cp_async_commit();
-    const float eC = fac[kFeC];
-    float x[8][4], inv0, inv1;
-    float most = times_k<NT>(st, tk, dk0, x, &inv0, &inv1);
-    inv0 *= fac[kFinvK], inv1 *= fac[kFinvK];
-    uint32_t hi[4][4], lo[4][4];
-    if constexpr (!back) {
-#pragma unroll
-      for (int m = 0; m < 8; ++m)
-        mine[32 * m] = make_float4(x[m][0] * inv0, x[m][1] * inv0, x[m][2] * inv1, x[m][3] * inv1);
-      store_state<D, NT>(st, a.H + (size_t(i + b) * a.H_v + h) * D * D, dk0, dv0);
-    } else {
-      uint32_t oa[4][4];  // dO^T as A fragments
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) ldsm4t(oa[kk], piece<true>(base + L::V, 16 * kk, 16 * rg));
-      float ma[4][4] = {};  // this warp's two 16-row blocks of M^T dO
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int np = hf ? 1 + j : 3 * j;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          if (kk >= np) {
-            uint32_t bh[4], bl[4];
-            ldsm4t(bh, piece<false>(base + L::M, 16 * kk, 16 * np));
-            ldsm4t(bl, piece<false>(base + L::M + kBlk, 16 * kk, 16 * np));
-            mma16(ma[2 * j], oa[kk], bh[0], bh[1]);
-            mma16(ma[2 * j + 1], oa[kk], bh[2], bh[3]);
-            mma16(ma[2 * j], oa[kk], bl[0], bl[1]);
-            mma16(ma[2 * j + 1], oa[kk], bl[2], bl[3]);
-          }
-      }
-      const float im = a.scale * fac[kFinvO] * fac[kFinvM];
-#pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        const float2 et = *reinterpret_cast<const float2*>(fac + kFeT + 8 * m + t2);
-        const int j = m < 2 || m >= 6 ? (m & 1) + (m >= 6 ? 2 : 0) : m - 2;
-        const float f = ((m < 2 || m >= 6) == (hf == 0)) ? im : 0.f;
-        mine[32 * m] = make_float4(
-            fmaf(et.x, x[m][0] * inv0, ma[j][0] * f), fmaf(et.y, x[m][1] * inv0, ma[j][1] * f),
-            fmaf(et.x, x[m][2] * inv1, ma[j][2] * f), fmaf(et.y, x[m][3] * inv1, ma[j][3] * f));
-      }
-      store_state<D, NT>(st, a.dH + unit * D * D, dk0, dv0);
-      // e^{G_C} dH' + scale (e^G Q)^T dO, while the other warps arrive
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = unpack_f16(oa[kk][e]);
-          x[2 * kk + (e >> 1)][2 * (e & 1)] = f.x;
-          x[2 * kk + (e >> 1)][2 * (e & 1) + 1] = f.y;
+          for (int x = 0; x < NK; ++x) out[ws + (NK * hh + x) * 16] = st[x];
         }
-      limbs_of(x, fac + kFeG, hi, lo, &inv0, &inv1);
-      const float f = a.scale * fac[kFinvO];
-      inv0 *= f, inv1 *= f;
-      inv0 *= fac[kFinvQ], inv1 *= fac[kFinvQ];
-      add_product<NT>(st, eC, inv0, inv1, hi, lo, base + L::Q, dk0);
-    }
-    most = warp_max(most);
-    if (lane == 0) a.Hmax[(unit * 2 + back) * (D / 8) + 2 * (dv0 / 16) + hf] = most;
-    cp_async_wait<1>();  // S (and V) of this chunk
-    __syncthreads();
-    if (t + 1 < n)
-      load_early(t + 1);
-    else
-      cp_async_commit();
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const float4 p = mine[32 * m], q = other[32 * m];
-      x[m][0] = p.x + q.x, x[m][1] = p.y + q.y, x[m][2] = p.z + q.z, x[m][3] = p.w + q.w;
-    }
-    named_sync(1 + rg, 64);  // both have read both slots: they are free for u
-    if constexpr (!back) {
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t v[4];  // V^T: (dv 0-7, r 0-7), (dv 0-7, r 8-15), (dv 8-15, r 0-7), ...
-        ldsm4t(v, piece<false>(base + L::V, 16 * np, 16 * rg));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 eg = *reinterpret_cast<const float2*>(fac + kFeG + 16 * np + 8 * e + t2);
-          float(&y)[4] = x[2 * np + e];
-          const uint32_t v0 = v[e], v1 = v[2 + e];
-          y[0] = fmaf(-eg.x, y[0], __uint_as_float(v0 << 16));
-          y[1] = fmaf(-eg.y, y[1], __uint_as_float(v0 & 0xffff0000u));
-          y[2] = fmaf(-eg.x, y[2], __uint_as_float(v1 << 16));
-          y[3] = fmaf(-eg.y, y[3], __uint_as_float(v1 & 0xffff0000u));
-        }
+        const float wm = warp_max(on ? most : 0.f);
+        if (lane == 0) a.Hmax[(unit * 2 + back) * 8 + warp] = wm;
       }
-    }
-    {
-      // u = X - (beta X) S^T, E = Y - (beta Y) S: this warp's two 16-row blocks
-      float w[4][4];
+      // 2. X = V - e^G K H, or Y = Y0 + e^{G_C - G} K dH': rows 32 hh ..
+      ok = mbar_wait(&bars[bKF + (t & 1)], (t >> 1) & 1, abort_flag, err, 1u) && ok;
+      ok = mbar_wait(&bars[bYF], t & 1, abort_flag, err, 1u) && ok;
+      ok = mbar_wait(&bars[bX], t & 1, abort_flag, err, 2u) && ok;
+      tc_fence_after();
+      float x[32];
+      {
+        float y0[32], y1[32];
+        tmem_ld32(tl + kTX0 + 32 * hh, y0);
+        tmem_ld32(tl + kTX1 + 32 * hh, y1);
+        tmem_ld_wait();
+        const float ik = fac[kFinvK], i0 = inv_h[dv] * ik, i1 = inv_h[128 + dv] * ik;
+        const float* fr = fac + (back ? kFeT : kFeG) + 32 * hh;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+        for (int r = 0; r < 32; r += 4) {
+          const float4 f4 = *reinterpret_cast<const float4*>(fr + r);
+          const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[j][e] = hf ? x[2 + j][e] : x[j < 2 ? j : 4 + j][e];
-      limbs_of(x, fac + kFbeta, hi, lo, &inv0, &inv1);
-      inv0 *= fac[kFinvS], inv1 *= fac[kFinvS];
-      float y[4][4] = {};
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int np = hf ? 1 + j : 3 * j;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          if (back ? kk >= np : kk <= np) {
-            uint32_t bh[4], bl[4];
-            if constexpr (back) {
-              ldsm4t(bh, piece<false>(base + L::S, 16 * kk, 16 * np));
-              ldsm4t(bl, piece<false>(base + L::S + kBlk, 16 * kk, 16 * np));
+          for (int e = 0; e < 4; ++e) {
+            const float kh = fmaf(y0[r + e], i0, y1[r + e] * i1);
+            const int at = (32 * hh + r + e) * D + dv;
+            float v = 0.f;
+            if (back) {
+              if (on) v = reinterpret_cast<const float*>(smem + L::Y)[at];
+              x[r + e] = fmaf(f[e], kh, v);
             } else {
-              ldsm4(bh, piece<true>(base + L::S, 16 * np, 16 * kk));
-              ldsm4(bl, piece<true>(base + L::S + kBlk, 16 * np, 16 * kk));
+              if (on) v = bf16f(reinterpret_cast<const uint16_t*>(smem + L::Y)[at]);
+              x[r + e] = fmaf(-f[e], kh, v);
             }
-            mma16(y[2 * j], hi[kk], bh[0], bh[1]);
-            mma16(y[2 * j + 1], hi[kk], bh[2], bh[3]);
-            mma16(y[2 * j], lo[kk], bh[0], bh[1]);
-            mma16(y[2 * j + 1], lo[kk], bh[2], bh[3]);
-            mma16(y[2 * j], hi[kk], bl[0], bl[1]);
-            mma16(y[2 * j + 1], hi[kk], bl[2], bl[3]);
           }
-      }
-      float* out = (back ? a.E : a.u) + unit * kBC * D + dv0 + g8;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = hf ? 2 + j : j < 2 ? j : 4 + j;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[j][e] = fmaf(-(e < 2 ? inv0 : inv1), y[j][e], w[j][e]);
-          out[size_t(8 * m + t2 + (e & 1)) * D + (e >> 1) * 8] = w[j][e];
         }
-        other[32 * j] = make_float4(w[j][0], w[j][1], w[j][2], w[j][3]);
+      }
+      {
+        float z[32], inv;
+#pragma unroll
+        for (int r = 0; r < 32; r += 4) {
+          const float4 f4 = *reinterpret_cast<const float4*>(fac + kFbeta + 32 * hh + r);
+          z[r] = x[r] * f4.x, z[r + 1] = x[r + 1] * f4.y;
+          z[r + 2] = x[r + 2] * f4.z, z[r + 3] = x[r + 3] * f4.w;
+        }
+        const float s = pow2_scale(max_abs_of(z), &inv);
+        inv_x[128 * hh + dv] = inv;
+        limbs_to_tmem(z, s, tl + kTA + 16 * hh, tl + kTA + 32 + 16 * hh);
+      }
+      tc_fence_before();
+      if (!named_all(1, kScanSync, ok)) break;
+      if (tid == 0) mbar_arrive(&bars[bYE]);
+      const float eC = fac[kFeC];
+      if constexpr (back) {  // e^{G_C} dH' + (scale e^G dO)^T Q
+        ok = mbar_wait(&bars[bQ], t & 1, abort_flag, err, 2u) && ok;
+        tc_fence_after();
+        const float f = fac[kFinvGO] * fac[kFinvQ];
+#pragma unroll
+        for (int p = 0; p < NK; p += 32) {
+          float y[32];
+          tmem_ld32(tl + kTH0 + NK * hh + p, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) st[p + e] = fmaf(eC, st[p + e], y[e] * f);
+        }
+      }
+      // 3. u = X - (beta X) S^T, E = Y - (beta Y) S
+      ok = mbar_wait(&bars[bS], t & 1, abort_flag, err, 2u) && ok;
+      tc_fence_after();
+      {
+        float y0[32], y1[32];
+        tmem_ld32(tl + kTX0 + 32 * hh, y0);
+        tmem_ld32(tl + kTX1 + 32 * hh, y1);
+        tmem_ld_wait();
+        const float is = -fac[kFinvS], i0 = inv_x[dv] * is, i1 = inv_x[128 + dv] * is;
+        float* out = (back ? a.E : a.u) + (unit * kBC + 32 * hh) * D + dv;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+          x[r] += fmaf(y0[r], i0, y1[r] * i1);
+          if (on) out[r * D] = x[r];
+        }
+        const float* fr = fac + (back ? kFbG : kFbT) + 32 * hh;
+#pragma unroll
+        for (int r = 0; r < 32; r += 4) {
+          const float4 f4 = *reinterpret_cast<const float4*>(fr + r);
+          x[r] *= f4.x, x[r + 1] *= f4.y, x[r + 2] *= f4.z, x[r + 3] *= f4.w;
+        }
+        float inv;
+        const float s = pow2_scale(max_abs_of(x), &inv);
+        inv_w[128 * hh + dv] = inv;
+        limbs_to_tmem(x, s, tl + kTA + 64 + 16 * hh, tl + kTA + 96 + 16 * hh);
+      }
+      tc_fence_before();
+      const float ik = back ? -fac[kFinvK] : fac[kFinvK];  // (the factors go with K's buffer)
+      if (!named_all(1, kScanSync, ok)) break;
+      // 4. the next state
+      const float i0 = inv_w[dv] * ik, i1 = inv_w[128 + dv] * ik;
+      ok = mbar_wait(&bars[bH], t & 1, abort_flag, err, 2u) && ok;
+      tc_fence_after();
+#pragma unroll
+      for (int p = 0; p < NK; p += 32) {
+        float y0[32], y1[32];
+        tmem_ld32(tl + kTH0 + NK * hh + p, y0);
+        tmem_ld32(tl + kTH1 + NK * hh + p, y1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float d = fmaf(y0[e], i0, y1[e] * i1);
+          st[p + e] = back ? st[p + e] + d : fmaf(eC, st[p + e], d);
+        }
       }
     }
-    __syncthreads();
-    if (t + 1 < n)
-      load_late(t + 1);
-    else
-      cp_async_commit();
-    {
-      // blocks 0 and 3 are warp rg's (in slot rg + 4), 1 and 2 warp rg + 4's
-      const float4* s0 = hf ? mine : other;
-      const float4* s1 = hf ? other : mine;
+    float* last = nullptr;
+    if (!back) last = a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D;
+    if (on && last != nullptr) {
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        const float4 p = m < 2 ? s0[32 * m] : m >= 6 ? s0[32 * (m - 4)] : s1[32 * (m - 2)];
-        x[m][0] = p.x, x[m][1] = p.y, x[m][2] = p.z, x[m][3] = p.w;
-      }
+      for (int x = 0; x < NK; ++x) last[ws + (NK * hh + x) * 16] = st[x];
     }
-    limbs_of(x, fac + (back ? kFbG : kFbT), hi, lo, &inv0, &inv1);
-    const float f = back ? -fac[kFinvK] : fac[kFinvK];
-    add_product<NT>(st, back ? 1.f : eC, inv0 * f, inv1 * f, hi, lo, tk, dk0);
-    cp_async_wait<1>();  // all but S (and V) of the next chunk
-    __syncthreads();
-  }
-  if constexpr (!back) {
-    store_state<D, NT>(st, a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D, dk0, dv0);
-    // This grid ends after the other scan's: what follows reads both.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-  } else if (a.dh0 != nullptr) {
+    if (back && on && a.dh0 != nullptr) {
 #pragma unroll
-    for (int m = 0; m < NT; ++m)
+      for (int x = 0; x < NK; ++x) a.dh0[head + size_t(NK * hh + x) * D + dv] = st[x];
+    }
+    tc_fence_before();
+  } else if (warp == 8) {
+    // Loads, in the order in which the chain frees their buffers.
+    const int seq_lo = max(a.cu[b], 0), seq_hi = min(a.cu[b + 1], a.total_tokens);
+    bool ok = true;
+    int tk = -1, te = -1, ty = -1, ts = -1;  // the last chunk of each kind that was issued
+    for (int t = 0; t < n && ok; ++t) {
+      const int i = chunk_of(t);
+      const size_t unit = size_t(i) * a.H_v + h;
+      const uint8_t* kq = a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile;
+      if (t >= 2) ok = mbar_wait(&bars[bKE + (t & 1)], ((t >> 1) & 1) ^ 1, abort_flag, err, 4u);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars[bKF + (t & 1)], L::kTile + kFac * 4);
+        bulk_load_g2s(smem + L::K + (t & 1) * L::kTile, kq, L::kTile, &bars[bKF + (t & 1)]);
+        bulk_load_g2s(smem + L::Fac + (t & 1) * kFac * 4, a.fac + unit * kFac, kFac * 4,
+                      &bars[bKF + (t & 1)]);
+      }
+      tk = t;
+      if constexpr (back) {
+        if (t >= 1) ok = mbar_wait(&bars[bQE], (t - 1) & 1, abort_flag, err, 4u);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars[bEF], 3 * L::kTile);
+          bulk_load_g2s(smem + L::Q, kq + L::kTile, L::kTile, &bars[bEF]);
+          bulk_load_g2s(smem + L::GO, a.GO + unit * 2 * L::kTile, 2 * L::kTile, &bars[bEF]);
+        }
+        te = t;
+      }
+      if (t >= 1) ok = mbar_wait(&bars[bYE], (t - 1) & 1, abort_flag, err, 4u);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if constexpr (back) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars[bYF], kBC * D * 4);
+          bulk_load_g2s(smem + L::Y, a.Y0 + unit * kBC * D, kBC * D * 4, &bars[bYF]);
+        }
+      } else {
+        const int row0 = seq_lo + kBC * t, rows = max(0, min(kBC, seq_hi - row0));
+        for (int y = lane; y < kBC * D / 8; y += 32) {
+          const int r = y / (D / 8), p = y % (D / 8);
+          const uint16_t* src = a.v + h * D + 8 * p;
+          cp_async16(base + L::Y + y * 16, r < rows ? src + size_t(row0 + r) * a.v_stride : src,
+                     r < rows);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_u32(&bars[bYF]))
+                     : "memory");
+      }
+      ty = t;
+      if (t >= 1) ok = mbar_wait(&bars[bSE], (t - 1) & 1, abort_flag, err, 4u);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars[bSF], 2 * kBlk);
+        bulk_load_g2s(smem + L::S, a.S + unit * 2 * kBlk, 2 * kBlk, &bars[bSF]);
+      }
+      ts = t;
+    }
+    // nothing may still be landing in shared memory at exit
+    for (int t = tk - 1; t <= tk; ++t)
+      if (t >= 0) mbar_wait(&bars[bKF + (t & 1)], (t >> 1) & 1, nullptr, err, 8u);
+    if (te >= 0) mbar_wait(&bars[bEF], te & 1, nullptr, err, 8u);
+    if (ty >= 0) mbar_wait(&bars[bYF], ty & 1, nullptr, err, 8u);
+    if (ts >= 0) mbar_wait(&bars[bSF], ts & 1, nullptr, err, 8u);
+    cp_async_wait<0>();
+    __syncwarp();
+  } else {
+    const bool leader = lane == 0;
+    const uint64_t kmaj = make_sdesc_sw128(0, 16, 1024);    // K-major operands
+    const uint64_t mnmaj = make_sdesc_sw128(0, 8192, 1024);  // MN-major, 64-element blocks apart
+    constexpr uint32_t id_x = make_idesc_f16(128, 64, 0, 0);
+    constexpr uint32_t id_s = make_idesc_f16(128, 64, 0, back ? 1 : 0);
+    constexpr uint32_t id_h = make_idesc_f16(128, D, 0, 1);
+    constexpr uint32_t id_q = make_idesc_f16(128, D, 1, 1);
+    bool left = false;
+    for (int t = 0; t < n; ++t) {
+      const uint32_t k4 = (base + L::K + (t & 1) * L::kTile) >> 4;
+      bool ok = true;
+      if (leader) ok = mbar_wait(&bars[bKF + (t & 1)], (t >> 1) & 1, abort_flag, err, 16u);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!named_all(1, kScanSync, ok)) {
+        left = true;
+        break;
+      }
+      if (leader) {
+        tc_fence_after();
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        a.dh0[seq_state + size_t(dk0 + 8 * m + t2 + (e & 1)) * D + dv0 + g8 + (e >> 1) * 8] =
-            st[m][e];
+        for (int limb = 1; limb >= 0; --limb)
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int half = kk / (D / 32);
+            mma_bf16_ts(tmem + (half ? kTX1 : kTX0), tmem + kTA + 64 * limb + 8 * kk,
+                        kmaj + (k4 + (kk >> 2) * (kBlk >> 4) + (kk & 3) * 2), id_x,
+                        limb == 0 || kk % (D / 32) != 0);
+          }
+        mma_commit(&bars[bX]);
+        if constexpr (back) {
+          ok = mbar_wait(&bars[bEF], t & 1, abort_flag, err, 16u);
+          if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int limb = 1; limb >= 0; --limb)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16_ss(tmem + kTH0,
+                            mnmaj + (((base + L::GO + limb * L::kTile) >> 4) + 128 * kk),
+                            mnmaj + (((base + L::Q) >> 4) + 128 * kk), id_q,
+                            limb == 0 || kk != 0);
+          }
+          mma_commit(&bars[bQ]);
+          mma_commit(&bars[bQE]);
+        }
+        ok = mbar_wait(&bars[bSF], t & 1, abort_flag, err, 16u) && ok;
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!named_all(1, kScanSync, ok)) {
+        left = true;
+        break;
+      }
+      if (leader) {
+        tc_fence_after();
+        const uint32_t s4 = (base + L::S) >> 4;
+        // (x low) S high, (x high) S low, (x high) S high
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_ts(tmem + (kk >> 1 ? kTX1 : kTX0), tmem + kTA + (q == 0 ? 32 : 0) + 8 * kk,
+                        (back ? mnmaj + (s4 + (q == 1 ? kBlk >> 4 : 0) + 128 * kk)
+                              : kmaj + (s4 + (q == 1 ? kBlk >> 4 : 0) + 2 * kk)),
+                        id_s, q != 0 || (kk & 1) != 0);
+        mma_commit(&bars[bS]);
+        mma_commit(&bars[bSE]);
+      }
+      __syncwarp();
+      if (!named_all(1, kScanSync, true)) {
+        left = true;
+        break;
+      }
+      if (leader) {
+        tc_fence_after();
+#pragma unroll
+        for (int limb = 1; limb >= 0; --limb)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_ts(tmem + (kk >> 1 ? kTH1 : kTH0), tmem + kTA + 64 + 32 * limb + 8 * kk,
+                        mnmaj + (k4 + 128 * kk), id_h, limb == 0 || (kk & 1) != 0);
+        mma_commit(&bars[bH]);
+        mma_commit(&bars[bKE + (t & 1)]);
+      }
+      __syncwarp();
+    }
+    (void)left;
+    if (leader) {  // every MMA this thread issued has completed
+      mma_commit(&bars[bDrain]);
+      mbar_wait(&bars[bDrain], 0, nullptr, err, 32u);
+    }
+    __syncwarp();
   }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+  // This grid ends after the other scan's: what follows reads both.
+  if constexpr (!back) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+cudaError_t take_err_backward(uint32_t* out) {
+  uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_err_backward, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_err_backward, &zero, sizeof(uint32_t));
 }
 
 // ---------------------------------------------------------------------------
@@ -937,7 +1078,7 @@ struct GradsSmem {
   static constexpr int Fac = DH + (D / 16 - 4) * kSlice;  // two buffers of the unit's factors
   static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
   static constexpr int M = G + 2 * kBC * 8;      // two buffers of the states' largest values
-  static constexpr int F = M + 2 * D / 4 * 4;    // floats from here
+  static constexpr int F = M + 2 * 16 * 4;       // floats from here
   static constexpr int kFloats = 2 * kBC + (D / 16) * kBC + kBC + 16;
   static constexpr int kBytes = F + kFloats * 4;
   // Where slice x of dH' is: the last four go where beta u's low limb was (its
@@ -1022,8 +1163,8 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
       cp_async16(base + L::Fac + p * kFac * 4 + tid * 16, a.fac + unit * kFac + tid * 4);
     else if (tid >= 128 && tid < 128 + kBC / 2)
       cp_async16(base + L::G + p * kBC * 8 + (tid - 128) * 16, a.G + unit * kBC + (tid - 128) * 2);
-    else if (tid >= 192 && tid < 192 + D / 16)
-      cp_async16(base + L::M + p * D + (tid - 192) * 16, a.Hmax + unit * (D / 4) + (tid - 192) * 4);
+    else if (tid >= 192 && tid < 196)
+      cp_async16(base + L::M + p * 64 + (tid - 192) * 16, a.Hmax + unit * 16 + (tid - 192) * 4);
   };
   // two slices of a state from slice x, by warps 8-15, whose own waits cover them
   auto load_slices = [&](uint32_t dst, const float* state, int x) {
@@ -1189,10 +1330,10 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
             }
           }
     }
-    const float* hm = reinterpret_cast<const float*>(smem + L::M) + (h & 1) * (D / 4);
+    const float* hm = reinterpret_cast<const float*>(smem + L::M) + (h & 1) * 16;
     float m0 = 0.f, ih;
 #pragma unroll
-    for (int x = 0; x < 2 * CG; ++x) m0 = max_nan(m0, hm[x]);
+    for (int x = 0; x < 8; ++x) m0 = max_nan(m0, hm[x]);
     const float sh = pow2_scale(m0, &ih);
     const int at = (16 * cg + g8) * 64 + 8 * t2;  // this lane's quads of a slice
     float acc[MT][2][4] = {};
@@ -1298,7 +1439,7 @@ __global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
       // (e^{G_C - G} beta u) dH'^T
       float m1 = 0.f, id;
 #pragma unroll
-      for (int x = 0; x < 2 * CG; ++x) m1 = max_nan(m1, hm[2 * CG + x]);
+      for (int x = 0; x < 8; ++x) m1 = max_nan(m1, hm[8 + x]);
       const float sd = pow2_scale(m1, &id);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -1434,14 +1575,16 @@ size_t layout(BwdArgs* a, char* base, int total_tokens, int num_seqs, int H_k, i
   a->chunk_seq = reinterpret_cast<int32_t*>(take(mc * 4));
   a->KQ = reinterpret_cast<uint8_t*>(take(mc * H_k * 2 * tile));
   a->O = reinterpret_cast<uint8_t*>(take(units * tile));
-  a->SM = reinterpret_cast<uint8_t*>(take(units * 4 * kBlk));
+  a->GO = reinterpret_cast<uint8_t*>(take(units * 2 * tile));
+  a->S = reinterpret_cast<uint8_t*>(take(units * 2 * kBlk));
+  a->Y0 = reinterpret_cast<float*>(take(units * kBC * D * 4));
   a->fac = reinterpret_cast<float*>(take(units * kFac * 4));
   a->G = reinterpret_cast<float2*>(take(units * kBC * 8));
   a->u = reinterpret_cast<float*>(take(units * kBC * D * 4));
   a->E = reinterpret_cast<float*>(take(units * kBC * D * 4));
   a->H = reinterpret_cast<float*>(take((mc + num_seqs) * size_t(H_v) * D * D * 4));
   a->dH = reinterpret_cast<float*>(take(units * D * D * 4));
-  a->Hmax = reinterpret_cast<float*>(take(units * 2 * (D / 8) * 4));
+  a->Hmax = reinterpret_cast<float*>(take(units * 2 * 8 * 4));
   return at;
 }
 
@@ -1457,15 +1600,15 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   if ((e = cudaFuncSetAttribute(bwd_grads_kernel<D>, kMax, grads)) != cudaSuccess) return e;
   bwd_prep_kernel<D><<<dim3(a.max_chunks, a.H_v), 256, prep, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const unsigned scans = unsigned(a.num_seqs) * a.H_v * (D / 64);
-  bwd_scan_kernel<D, true><<<scans, 256, back, s>>>(a);
+  const unsigned scans = unsigned(a.num_seqs) * a.H_v;
+  bwd_scan_kernel<D, true><<<scans, kScanThreads, back, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchAttribute beside;
   beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   beside.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(scans);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kScanThreads);
   cfg.dynamicSmemBytes = fwd;
   cfg.stream = s;
   cfg.attrs = &beside;

@@ -149,5 +149,6 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t s);
 cudaError_t take_err_ba_gates(uint32_t* out);
 cudaError_t take_err_prefill(uint32_t* out);
 cudaError_t take_err_verify(uint32_t* out);
+cudaError_t take_err_backward(uint32_t* out);
 
 }  // namespace gdn
