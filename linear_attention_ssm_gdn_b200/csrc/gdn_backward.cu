@@ -648,7 +648,11 @@ struct ScanSmem {
   static constexpr int Y = S + 2 * kBlk;           // Y0 (f32) or V (bf16), [64][D]
   static constexpr int Q = Y + kBC * D * (back ? 4 : 2);
   static constexpr int GO = Q + (back ? kTile : 0);  // two limbs, M = 128 rows each
-  static constexpr int Fac = GO + (back ? 2 * kTile + (D == 64 ? kBlk : 0) : 0);  // two buffers
+  // The state on its way out: its slices, 64 bytes apart from a multiple of all
+  // banks, so that the two slices of a warp do not collide.
+  static constexpr int kSlice = D * 64, kStep = kSlice + 64;
+  static constexpr int St = GO + (back ? 2 * kTile + (D == 64 ? kBlk : 0) : 0);
+  static constexpr int Fac = St + D / 16 * kStep;  // two buffers
   static constexpr int Inv = Fac + 2 * kFac * 4;   // [3][2][128] inverse row scales
   static constexpr int Bars = Inv + 3 * 2 * 128 * 4;
   static constexpr int kUsed = Bars + kBars * 8 + 16 + 1024;  // 1024: alignment of the base
@@ -730,8 +734,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
     float* inv_h = reinterpret_cast<float*>(smem + L::Inv);        // [2][128] each
     float *inv_x = inv_h + 256, *inv_w = inv_x + 256;
     const size_t head = (size_t(b) * a.H_v + h) * D * D;
-    // where (dv, dk = 0) is in a state of the workspace
-    const int ws = (dv >> 4) * D * 16 + 4 * ((dv & 7) >> 1) + (dv & 1) + 2 * ((dv >> 3) & 1);
     float st[NK];
     {
       const float* init = back ? a.dhT : a.h0;
@@ -739,6 +741,21 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
       for (int i = 0; i < NK; ++i)
         st[i] = init != nullptr && on ? init[head + size_t(NK * hh + i) * D + dv] : 0.f;
     }
+    // where (dv, dk = NK hh) is in a state: slice, and place in its rows of 16
+    float* out_st = reinterpret_cast<float*>(smem + L::St + (dv >> 4) * L::kStep) + NK * hh * 16 +
+                    4 * ((dv & 7) >> 1) + (dv & 1) + 2 * ((dv >> 3) & 1);
+    auto stage_state = [&] {
+      if (on) {
+#pragma unroll
+        for (int x = 0; x < NK; ++x) out_st[x * 16] = st[x];
+      }
+      fence_proxy_async_smem();
+    };
+    auto send_state = [&](float* to) {  // one thread, once every warp has staged its part
+      for (int x = 0; x < D / 16; ++x)
+        bulk_store_s2g(to + x * D * 16, smem + L::St + x * L::kStep, L::kSlice);
+      tma_store_commit();
+    };
     bool ok = true;
     int t = 0;
     for (; t < n; ++t) {
@@ -754,13 +771,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
         limbs_to_tmem(st, s, tl + kTA + NK / 2 * hh, tl + kTA + 64 + NK / 2 * hh);
       }
       tc_fence_before();
+      if (tid == 0) tma_store_wait_read<0>();  // the last state has left its buffer
       if (!named_all(1, kScanSync, ok)) break;
       {
-        float* out = back ? a.dH + unit * D * D : a.H + (size_t(i + b) * a.H_v + h) * D * D;
-        if (on) {
-#pragma unroll
-          for (int x = 0; x < NK; ++x) out[ws + (NK * hh + x) * 16] = st[x];
-        }
+        stage_state();
         const float wm = warp_max(on ? most : 0.f);
         if (lane == 0) a.Hmax[(unit * 2 + back) * 8 + warp] = wm;
       }
@@ -810,7 +824,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
       }
       tc_fence_before();
       if (!named_all(1, kScanSync, ok)) break;
-      if (tid == 0) mbar_arrive(&bars[bYE]);
+      if (tid == 0) {
+        mbar_arrive(&bars[bYE]);
+        send_state(back ? a.dH + unit * D * D : a.H + (size_t(i + b) * a.H_v + h) * D * D);
+      }
       const float eC = fac[kFeC];
       if constexpr (back) {  // e^{G_C} dH' + (scale e^G dO)^T Q
         ok = mbar_wait(&bars[bQ], t & 1, abort_flag, err, 2u) && ok;
@@ -834,27 +851,31 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
         tmem_ld32(tl + kTX1 + 32 * hh, y1);
         tmem_ld_wait();
         const float is = -fac[kFinvS], i0 = inv_x[dv] * is, i1 = inv_x[128 + dv] * is;
-        float* out = (back ? a.E : a.u) + (unit * kBC + 32 * hh) * D + dv;
-#pragma unroll
-        for (int r = 0; r < 32; ++r) {
-          x[r] += fmaf(y0[r], i0, y1[r] * i1);
-          if (on) out[r * D] = x[r];
-        }
         const float* fr = fac + (back ? kFbG : kFbT) + 32 * hh;
 #pragma unroll
         for (int r = 0; r < 32; r += 4) {
           const float4 f4 = *reinterpret_cast<const float4*>(fr + r);
-          x[r] *= f4.x, x[r + 1] *= f4.y, x[r + 2] *= f4.z, x[r + 3] *= f4.w;
+          const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[r + e] += fmaf(y0[r + e], i0, y1[r + e] * i1);
+            y0[r + e] = x[r + e] * f[e];
+          }
         }
         float inv;
-        const float s = pow2_scale(max_abs_of(x), &inv);
+        const float s = pow2_scale(max_abs_of(y0), &inv);
         inv_w[128 * hh + dv] = inv;
-        limbs_to_tmem(x, s, tl + kTA + 64 + 16 * hh, tl + kTA + 96 + 16 * hh);
+        limbs_to_tmem(y0, s, tl + kTA + 64 + 16 * hh, tl + kTA + 96 + 16 * hh);
       }
       tc_fence_before();
       const float ik = back ? -fac[kFinvK] : fac[kFinvK];  // (the factors go with K's buffer)
       if (!named_all(1, kScanSync, ok)) break;
-      // 4. the next state
+      // 4. u or E out, while the product runs; the next state
+      if (on) {
+        float* out = (back ? a.E : a.u) + (unit * kBC + 32 * hh) * D + dv;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) out[r * D] = x[r];
+      }
       const float i0 = inv_w[dv] * ik, i1 = inv_w[128 + dv] * ik;
       ok = mbar_wait(&bars[bH], t & 1, abort_flag, err, 2u) && ok;
       tc_fence_after();
@@ -871,12 +892,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
         }
       }
     }
-    float* last = nullptr;
-    if (!back) last = a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D;
-    if (on && last != nullptr) {
-#pragma unroll
-      for (int x = 0; x < NK; ++x) last[ws + (NK * hh + x) * 16] = st[x];
+    if constexpr (!back) {  // the final state; the barrier is the state warps' own
+      if (tid == 0) tma_store_wait_read<0>();
+      named_sync(2, 256);
+      stage_state();
+      named_sync(2, 256);
+      if (tid == 0) send_state(a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D);
     }
+    if (tid == 0) tma_store_wait_all<0>();
     if (back && on && a.dh0 != nullptr) {
 #pragma unroll
       for (int x = 0; x < NK; ++x) a.dh0[head + size_t(NK * hh + x) * D + dv] = st[x];
