@@ -31,10 +31,8 @@
 // (lo x lo is below the f32 rounding).  What reaches only dq or dk, which are
 // rounded to bf16 (2^-9), takes one limb (2^-12).
 //
-// The scans, a chain of three dependent products a chunk, run on tcgen05 with the
-// state in registers and its limbs in tensor memory.  The chunk-parallel kernels
-// before and after them use warp-level MMAs: their operands change shape and
-// precision from product to product, and many warps hide the latency.
+// The scans and the gradients run on tcgen05; the first kernel, whose products are
+// small and triangular, on warp-level MMAs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -743,7 +741,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
     }
     // where (dv, dk = NK hh) is in a state: slice, and place in its rows of 16
     float* out_st = reinterpret_cast<float*>(smem + L::St + (dv >> 4) * L::kStep) + NK * hh * 16 +
-                    4 * ((dv & 7) >> 1) + (dv & 1) + 2 * ((dv >> 3) & 1);
+                    (dv & 15);
     auto stage_state = [&] {
       if (on) {
 #pragma unroll
@@ -1077,502 +1075,493 @@ cudaError_t take_err_backward(uint32_t* out) {
 }
 
 // ---------------------------------------------------------------------------
-// Grads: one CTA of 16 warps per (chunk, key head), the value heads of the group
-// one after another, so that the shared dq and dk are summed in registers, in
-// one order.
+// Grads: one CTA of 16 working warps and an issuing one per (chunk, key head), the
+// value heads of the group one after another, so that the shared dq and dk are
+// summed in registers, in one order.
 //
-// Warps 0-7 make dq, warps 8-15 dk: a warp owns 16 of its columns (D = 64: and
-// half of the rows).  The states are its B operand: read straight from global
-// memory as the fragments that the scans stored, and split in registers; the row
-// operands (dO, u, E and their scaled forms) are f16 tiles in shared memory.
+// All products are transposed, M = 128 rows d_k (or, for P and N, the rows of dO
+// above those of beta E), so that two of them share an MMA where they share an
+// operand:
+//   [P; N]       = [dO; beta E] (beta u)^T           K = d_v, two limbs of u
+//   [A1 | A2]    = H [dO; beta E]^T                  K = d_v, low limb of H for dO only
+//   A3           = P K (two limbs),  A4 = P^T Q,  A5 = N K + N^T K   K = 64
+//   A6           = dH' (beta u)^T                    K = d_v
+//   dq = scale e^G A1 + A3,  dk = A4 + A5 - e^G A2 + e^{G_C - G} A6.
+// The warps turn f32 rows and states into f16 tiles in shared memory while the
+// products of the tiles before run; row factors that differ within a product are
+// applied to its result.
 // ---------------------------------------------------------------------------
 
 template <int D>
 struct GradsSmem {
   static constexpr int kTile = D / 64 * kBlk;
-  static constexpr int K = 0, Q = kTile;   // f16 tiles of the chunk
-  static constexpr int O = 2 * kTile;      // dO
-  static constexpr int UH = 3 * kTile, UL = 4 * kTile;  // beta u, two limbs
-  static constexpr int E = 5 * kTile;      // beta E
-  static constexpr int PH = 6 * kTile, PL = PH + kBlk, N = PL + kBlk;
-  static constexpr int kSlice = D * 64;    // 16 state columns in f32
-  static constexpr int H = N + kBlk;       // all slices of H; two of them, later, of dH'
-  static constexpr int DH = H + D / 16 * kSlice;  // the first D / 16 - 4 slices of dH'
-  static constexpr int Fac = DH + (D / 16 - 4) * kSlice;  // two buffers of the unit's factors
+  static constexpr int kTall = 2 * kTile;        // 128 rows
+  static constexpr int K = 0, Q = kTile;         // f16 tiles of the chunk
+  static constexpr int OE = 2 * kTile + (D == 64 ? kBlk : 0);  // dO over beta E, 128 rows
+  static constexpr int UH = OE + kTall, UL = UH + kTile;       // beta u, two limbs
+  static constexpr int HH = UL + kTile, HL = HH + kTall;       // H, two limbs
+  static constexpr int DH = HL + kTall;          // dH'
+  static constexpr int PH = DH + kTall, PL = PH + kBlk, N = PL + kBlk;
+  static constexpr int Fac = N + kBlk;           // two buffers of the unit's factors
   static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
   static constexpr int M = G + 2 * kBC * 8;      // two buffers of the states' largest values
   static constexpr int F = M + 2 * 16 * 4;       // floats from here
-  static constexpr int kFloats = 2 * kBC + (D / 16) * kBC + kBC + 16;
-  static constexpr int kBytes = F + kFloats * 4;
-  // Where slice x of dH' is: the last four go where beta u's low limb was (its
-  // kTile holds two) and over the first two slices of H.
-  __device__ static constexpr int dh_slice(int x) {
-    constexpr int n = D / 16;
-    return x < n - 4 ? DH + x * kSlice : x < n - 2 ? UL + (x - (n - 4)) * kSlice
-                                                   : H + (x - (n - 2)) * kSlice;
-  }
+  static constexpr int kFloats = 2 * kBC + 4 * kBC + kBC + 16;
+  static constexpr int Bars = F + kFloats * 4;
+  static constexpr int kUsed = Bars + 16 * 8 + 16 + 1024;
+  // More than half of an SM's: all of its tensor memory goes to one CTA.
+  static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
 };
 
-// total += f(row) * acc, acc = 0; f gives the factor of a row.
-template <int MT, class F>
-__device__ __forceinline__ void fold_in(float (&total)[MT][2][4], float (&acc)[MT][2][4], F f) {
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float x = f(16 * m + 8 * e);
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          total[m][n][2 * e + c] = fmaf(x, acc[m][n][2 * e + c], total[m][n][2 * e + c]);
-          acc[m][n][2 * e + c] = 0.f;
-        }
-    }
-}
-
-// acc += A (MT 16-row tiles of a tile, k-step kk) x two 8-column B tiles, one limb or two.
-template <int MT, bool two>
-__device__ __forceinline__ void rows_times(float (&acc)[MT][2][4], uint32_t tile, int r0, int kk,
-                                           const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    uint32_t av[4];
-    ldsm4(av, piece<false>(tile, r0 + 16 * m, 16 * kk));
-    mma16(acc[m][0], av, bh[0], bh[1]);
-    mma16(acc[m][1], av, bh[2], bh[3]);
-    if constexpr (two) {
-      mma16(acc[m][0], av, bl[0], bl[1]);
-      mma16(acc[m][1], av, bl[2], bl[3]);
-    }
-  }
-}
-
-__device__ __forceinline__ void named_arrive(int id, int nthreads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
+constexpr int kGradsWork = 512, kGradsThreads = kGradsWork + 32;
+enum { gO = 0, gU, gH, gP, gD, gPN, gA12, gA345, gA6, gDrain, kGradsBars };
+enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA4 = 256, kTA5 = 320, kTA6 = 384 };
 
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// A state's slices into a tall f16 tile (and, with LO, its low limb into a second
+// one): eight values of one d_k row at a time, lanes along d_k.  f(values, offset
+// of the first in the state) sees them in f32.
+template <int D, bool LO, class F>
+__device__ __forceinline__ void state_tile(const float* st, float s, uint8_t* hi, uint8_t* lo,
+                                           F f) {
+#pragma unroll
+  for (int m = 0; m < D * D / 8 / kGradsWork; ++m) {
+    const int x = threadIdx.x + m * kGradsWork;
+    const int dk = x % D, half = x / D % 2, slice = x / (2 * D);
+    const int at = slice * D * 16 + dk * 16 + half * 8;
+    float v[8];
+    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(st + at);
+    *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(st + at + 4);
+    f(v, at);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (LO)
+        split_f16(v[2 * e] * s, v[2 * e + 1] * s, h[e], l[e]);
+      else
+        h[e] = pack_f16(v[2 * e] * s, v[2 * e + 1] * s);
+    }
+    const int col = slice * 16 + half * 8;
+    const uint32_t to = (col >> 6) * 2 * kBlk + sw128_offset(dk, (col & 63) * 2);
+    *reinterpret_cast<uint4*>(hi + to) = make_uint4(h[0], h[1], h[2], h[3]);
+    if constexpr (LO) *reinterpret_cast<uint4*>(lo + to) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+}
+
 template <int D>
-__global__ void __launch_bounds__(512, 1) bwd_grads_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) {
   using L = GradsSmem<D>;
-  constexpr int CG = D / 16;        // column groups
-  constexpr int MT = D / 32;        // 16-row tiles of a warp: all four, or two
   constexpr int J = D / 32;         // quads of a row per lane in the row pass
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t most[2];      // P, N
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem);
-  float* invU = reinterpret_cast<float*>(smem + L::F);
-  float* invE = invU + kBC;
-  float* part = invE + kBC;         // [CG][64] row sums q . dq
-  float* vd = part + CG * kBC;      // [64] v . dv
-  float* red = vd + kBC;            // [8] <H', dH'>
-  const int i = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5,
-            lane = tid & 31, g8 = lane >> 2, t2 = 2 * (lane & 3);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::Bars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kGradsBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* err = &g_err_backward;
+  const int i = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, warp = int(warp_id_sync()),
+            lane = tid & 31;
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
-  const int vpg = a.H_v / a.H_k;
-  const bool kside = warp >= 8;
-  const int w8 = warp & 7;
-  const int cg = w8 % CG, r0 = (w8 / CG) * MT * 16;  // this warp's columns and rows
-  // dO, factors and gates of head h, into the buffer of its parity
-  auto load_head = [&](int h) {
-    const size_t unit = size_t(i) * a.H_v + h;
-    const int p = h & 1;
-    if (tid < kFac / 4)
-      cp_async16(base + L::Fac + p * kFac * 4 + tid * 16, a.fac + unit * kFac + tid * 4);
-    else if (tid >= 128 && tid < 128 + kBC / 2)
-      cp_async16(base + L::G + p * kBC * 8 + (tid - 128) * 16, a.G + unit * kBC + (tid - 128) * 2);
-    else if (tid >= 192 && tid < 196)
-      cp_async16(base + L::M + p * 64 + (tid - 192) * 16, a.Hmax + unit * 16 + (tid - 192) * 4);
-  };
-  // two slices of a state from slice x, by warps 8-15, whose own waits cover them
-  auto load_slices = [&](uint32_t dst, const float* state, int x) {
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(state) + x * L::kSlice;
-    for (int y = (tid - 256) * 16; y < 2 * L::kSlice; y += 256 * 16) cp_async16(dst + y, src + y);
-  };
-  cp_async_block<512>(base + L::K, a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile, 2 * L::kTile);
-  load_head(hk * vpg);
-  cp_async_commit();
-  float total[MT][2][4] = {};  // dq or dk of the group
-  for (int h = hk * vpg; h < (hk + 1) * vpg; ++h) {
-    const size_t unit = size_t(i) * a.H_v + h;
-    const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (h & 1) * kFac;
-    const float2* Gs = reinterpret_cast<const float2*>(smem + L::G) + (h & 1) * kBC;
-    const float* H = a.H + (size_t(i + c.seq) * a.H_v + h) * D * D;
-    const float* H1 = H + size_t(a.H_v) * D * D;
-    const float* dH = a.dH + unit * D * D;
-    cp_async_block<512>(base + L::O, a.O + unit * L::kTile, L::kTile);
-    cp_async_commit();
-    cp_async_block<512>(base + L::H, reinterpret_cast<const uint8_t*>(H), D * D * 4);
-    cp_async_block<512>(base + L::DH, reinterpret_cast<const uint8_t*>(dH),
-                        (CG - 4) * L::kSlice);
-    cp_async_commit();
-    // Rows 4 w .. 4 w + 3, 8 lanes a row, 4 J columns a lane.
-    const int r = 4 * warp + (lane >> 3), l8 = lane & 7;
-    float u[4 * J], e[4 * J];
-    uint2 vw[J];
-    {
-      const float* up = a.u + (unit * kBC + r) * D + 4 * l8;
-      const float* ep = a.E + (unit * kBC + r) * D + 4 * l8;
-      const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + h * D + 4 * l8;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        *reinterpret_cast<float4*>(u + 4 * j) = *reinterpret_cast<const float4*>(up + 32 * j);
-        *reinterpret_cast<float4*>(e + 4 * j) = *reinterpret_cast<const float4*>(ep + 32 * j);
-        vw[j] = make_uint2(0u, 0u);
-        if (r < c.rows) vw[j] = *reinterpret_cast<const uint2*>(vp + 32 * j);
-      }
-    }
-    if (tid < 2) most[tid] = 0;
-    if (tid == 0) {  // to L2: what this head reads later, and all of the next one
-      if (h == hk * vpg) prefetch_l2(dH + (CG - 4) * D * 16, 4 * L::kSlice);
-      prefetch_l2(H1, D * D * 4);
-      if (h + 1 < (hk + 1) * vpg) {
-        prefetch_l2(a.u + (unit + 1) * kBC * D, kBC * D * 4);
-        prefetch_l2(a.E + (unit + 1) * kBC * D, kBC * D * 4);
-        prefetch_l2(a.O + (unit + 1) * L::kTile, L::kTile);
-        prefetch_l2(H + D * D, D * D * 4);
-        prefetch_l2(dH + D * D, D * D * 4);
-      }
-    }
-    cp_async_wait<2>();  // the factors
-    __syncthreads();
-    // dv, dbeta, v . dv, and the f16 tiles of u and E
-    {
-      const float bt = fac[kFbeta + r];
-      float db = 0.f, vs = 0.f, mu = 0.f, me = 0.f;
-#pragma unroll
-      for (int x = 0; x < 4 * J; ++x) {
-        const uint32_t w = x & 2 ? vw[x / 4].y : vw[x / 4].x;
-        db = fmaf(e[x], u[x], db);
-        u[x] *= bt, e[x] *= bt;
-        vs = fmaf(__uint_as_float(x & 1 ? w & 0xffff0000u : w << 16), e[x], vs);
-        mu = max_nan(mu, fabsf(u[x])), me = max_nan(me, fabsf(e[x]));
-      }
-#pragma unroll
-      for (int off = 1; off < 8; off <<= 1) {
-        db += __shfl_xor_sync(0xffffffffu, db, off);
-        vs += __shfl_xor_sync(0xffffffffu, vs, off);
-        mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
-        me = fmaxf(me, __shfl_xor_sync(0xffffffffu, me, off));
-      }
-      float iu, ie;
-      const float su = pow2_scale(mu, &iu), se = pow2_scale(me, &ie);
-      if (l8 == 0) {
-        if (r < c.rows) a.dbeta[size_t(c.row0 + r) * a.H_v + h] = db;
-        vd[r] = vs;
-        invU[r] = iu, invE[r] = ie;
-      }
-      uint16_t* dv = a.dv + (size_t(c.row0 + r) * a.H_v + h) * D + 4 * l8;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const float *up = u + 4 * j, *ep = e + 4 * j;
-        if (r < c.rows)
-          *reinterpret_cast<uint2*>(dv + 32 * j) =
-              make_uint2(pack_bf16x2(ep[0], ep[1]), pack_bf16x2(ep[2], ep[3]));
-        const int col = 4 * l8 + 32 * j;
-        uint8_t* at = smem + (col >> 6) * kBlk + sw128_offset(r, (col & 63) * 2);
-        uint2 uh, ul;
-        split_f16(up[0] * su, up[1] * su, uh.x, ul.x);
-        split_f16(up[2] * su, up[3] * su, uh.y, ul.y);
-        *reinterpret_cast<uint2*>(at + L::UH) = uh;
-        *reinterpret_cast<uint2*>(at + L::UL) = ul;
-        *reinterpret_cast<uint2*>(at + L::E) =
-            make_uint2(pack_f16(ep[0] * se, ep[1] * se), pack_f16(ep[2] * se, ep[3] * se));
-      }
-    }
-    cp_async_wait<1>();  // dO
-    __syncthreads();
-    // P (warps 0-7) and N (8-15): rows 16 (w / 2), columns 32 (w % 2), the lower
-    // 16-column blocks
-    {
-      const int rb = w8 >> 1, ch = w8 & 1;
-      float x[4][4] = {};
-      if (2 * ch <= rb) {
-        const uint32_t ta = base + (kside ? L::E : L::O);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t av[4];
-          ldsm4(av, piece<false>(ta, 16 * rb, 16 * kk));
-#pragma unroll
-          for (int np = 0; np < 2; ++np)
-            if (2 * ch + np <= rb) {
-              uint32_t bv[4];
-              ldsm4(bv, piece<true>(base + L::UH, 32 * ch + 16 * np, 16 * kk));
-              mma16(x[2 * np], av, bv[0], bv[1]);
-              mma16(x[2 * np + 1], av, bv[2], bv[3]);
-              if (!kside) {
-                ldsm4(bv, piece<true>(base + L::UL, 32 * ch + 16 * np, 16 * kk));
-                mma16(x[2 * np], av, bv[0], bv[1]);
-                mma16(x[2 * np + 1], av, bv[2], bv[3]);
-              }
-            }
-        }
-      }
-      float m = 0.f;
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int pr = 16 * rb + g8 + (k >> 1) * 8, ps = 32 * ch + 8 * n + t2 + (k & 1);
-          float f = 0.f;
-          if (ps < pr || (ps == pr && !kside))
-            f = expdiff(Gs[pr], Gs[ps]) * invU[ps] *
-                (kside ? -invE[pr] : a.scale * fac[kFinvO]);
-          x[n][k] = f == 0.f ? 0.f : x[n][k] * f;
-          m = max_nan(m, fabsf(x[n][k]));
-        }
-      const uint32_t um = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-      if (lane == 0) atomicMax(&most[kside], um);
-      cp_async_wait<0>();  // H and the first slices of dH'
-      __syncthreads();
-      // beta u's low limb is done with: two more slices of dH'
-      if (kside) load_slices(base + L::UL, dH, CG - 4);
-      if (h + 1 < (hk + 1) * vpg) load_head(h + 1);
+  const int vpg = a.H_v / a.H_k, h0 = hk * vpg;
+  if (tid == 0) {
+    for (int b = 0; b < kGradsBars; ++b)
+      mbar_init(&bars[b], b >= gU && b <= gD ? kGradsWork / 32 : 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < kGradsWork / 32) {
+    float* invU = reinterpret_cast<float*>(smem + L::F);
+    float* invE = invU + kBC;
+    float* part = invE + kBC;         // [4][64] q . dq of each 32 rows d_k
+    float* vd = part + 4 * kBC;       // [64] v . dv
+    float* red = vd + kBC;            // [16] <H', dH'>
+    const int qd = warp & 3, cq = warp >> 2;  // TMEM lanes 32 qd .., 16 columns 16 cq ..
+    const int dk = 32 * qd + lane;
+    const bool on = D == 128 || dk < D;
+    const uint32_t tl = tmem + (uint32_t(32 * qd) << 16) + 16 * cq;
+    // factors, gates and largest values of head h, into the buffer of its parity
+    auto load_head = [&](int h) {
+      const size_t unit = size_t(i) * a.H_v + h;
+      const int p = h & 1;
+      if (tid < kFac / 4)
+        cp_async16(base + L::Fac + p * kFac * 4 + tid * 16, a.fac + unit * kFac + tid * 4);
+      else if (tid >= 128 && tid < 128 + kBC / 2)
+        cp_async16(base + L::G + p * kBC * 8 + (tid - 128) * 16,
+                   a.G + unit * kBC + (tid - 128) * 2);
+      else if (tid >= 192 && tid < 196)
+        cp_async16(base + L::M + p * 64 + (tid - 192) * 16, a.Hmax + unit * 16 + (tid - 192) * 4);
       cp_async_commit();
-      float inv;
-      const float sc = pow2_scale(__uint_as_float(most[kside]), &inv);
-      if (2 * ch <= rb)
+    };
+    // this warp's part of a tile is written: the issuer may use it
+    auto ready = [&](int b) {
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[b]);
+    };
+    float dqs[16] = {}, dks[16] = {};
+    load_head(h0);
+    for (int h = h0; h < h0 + vpg; ++h) {
+      const uint32_t ph = (h - h0) & 1;
+      const size_t unit = size_t(i) * a.H_v + h;
+      const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (h & 1) * kFac;
+      const float2* Gs = reinterpret_cast<const float2*>(smem + L::G) + (h & 1) * kBC;
+      const float* hm = reinterpret_cast<const float*>(smem + L::M) + (h & 1) * 16;
+      const float* H = a.H + (size_t(i + c.seq) * a.H_v + h) * D * D;
+      const float* H1 = H + size_t(a.H_v) * D * D;
+      const float* dH = a.dH + unit * D * D;
+      // Rows 4 w .. 4 w + 3, 8 lanes a row, 4 J columns a lane.
+      const int r = 4 * warp + (lane >> 3), l8 = lane & 7;
+      float u[4 * J], e[4 * J];
+      uint2 vw[J];
+      {
+        const float* up = a.u + (unit * kBC + r) * D + 4 * l8;
+        const float* ep = a.E + (unit * kBC + r) * D + 4 * l8;
+        const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + h * D + 4 * l8;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            const int pr = 16 * rb + g8 + (k >> 1) * 8, ps = 32 * ch + 8 * n + t2;
-            uint32_t hi, lo;
-            split_f16(x[n][k] * sc, x[n][k + 1] * sc, hi, lo);
-            const uint32_t at = sw128_offset(pr, ps * 2);
-            if (kside) {
-              *reinterpret_cast<uint32_t*>(smem + L::N + at) = hi;
-            } else {
-              *reinterpret_cast<uint32_t*>(smem + L::PH + at) = hi;
-              *reinterpret_cast<uint32_t*>(smem + L::PL + at) = lo;
-            }
-          }
-    }
-    const float* hm = reinterpret_cast<const float*>(smem + L::M) + (h & 1) * 16;
-    float m0 = 0.f, ih;
-#pragma unroll
-    for (int x = 0; x < 8; ++x) m0 = max_nan(m0, hm[x]);
-    const float sh = pow2_scale(m0, &ih);
-    const int at = (16 * cg + g8) * 64 + 8 * t2;  // this lane's quads of a slice
-    float acc[MT][2][4] = {};
-    if (!kside) {
-      float dq[MT][2][4] = {};
-      // dO H^T
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t bh[4], bl[4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float4 x = *reinterpret_cast<const float4*>(smem + L::H + kk * L::kSlice + at +
-                                                            512 * n);
-          split_f16(x.x * sh, x.y * sh, bh[2 * n], bl[2 * n]);
-          split_f16(x.z * sh, x.w * sh, bh[2 * n + 1], bl[2 * n + 1]);
+        for (int j = 0; j < J; ++j) {
+          *reinterpret_cast<float4*>(u + 4 * j) = *reinterpret_cast<const float4*>(up + 32 * j);
+          *reinterpret_cast<float4*>(e + 4 * j) = *reinterpret_cast<const float4*>(ep + 32 * j);
+          vw[j] = make_uint2(0u, 0u);
+          if (r < c.rows) vw[j] = *reinterpret_cast<const uint2*>(vp + 32 * j);
         }
-        rows_times<MT, true>(dq, base + L::O, r0, kk, bh, bl);
-        if (kk == 1) named_arrive(3, 512);  // the first two slices of H may go
       }
-      const float f = a.scale * fac[kFinvO] * ih;
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dq[m][n][k] *= f * fac[kFeG + r0 + 16 * m + g8 + (k >> 1) * 8];
-      named_sync(1, 256);  // P
-      // P K (two limbs, k-steps up to the diagonal)
-      float ip;
-      pow2_scale(__uint_as_float(most[0]), &ip);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        uint32_t bv[4];
-        ldsm4t(bv, piece<false>(base + L::K, 16 * kk, 16 * cg));
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          if (kk <= r0 / 16 + m) {
-            uint32_t av[4];
-            ldsm4(av, piece<false>(base + L::PH, r0 + 16 * m, 16 * kk));
-            mma16(acc[m][0], av, bv[0], bv[1]);
-            mma16(acc[m][1], av, bv[2], bv[3]);
-            ldsm4(av, piece<false>(base + L::PL, r0 + 16 * m, 16 * kk));
-            mma16(acc[m][0], av, bv[0], bv[1]);
-            mma16(acc[m][1], av, bv[2], bv[3]);
-          }
+      if (tid < 2) most[tid] = 0;
+      if (tid == 0) {  // to L2: the states, then all of the next head
+        if (h == h0) {
+          prefetch_l2(H, D * D * 4);
+          prefetch_l2(dH, D * D * 4);
+        }
+        prefetch_l2(H1, D * D * 4);
+        if (h + 1 < h0 + vpg) {
+          prefetch_l2(a.u + (unit + 1) * kBC * D, kBC * D * 4);
+          prefetch_l2(a.E + (unit + 1) * kBC * D, kBC * D * 4);
+          prefetch_l2(H + D * D, D * D * 4);
+          prefetch_l2(dH + D * D, D * D * 4);
+        }
       }
-      const float fp = ip * fac[kFinvK];
-      fold_in(dq, acc, [&](int) { return fp; });
-      // q . dq of this warp's columns, and the group's sum
-      const float iq = fac[kFinvQ];
+      cp_async_wait<0>();  // the factors
+      named_sync(1, kGradsWork);
+      if (h + 1 < h0 + vpg) load_head(h + 1);
+      // dv, dbeta, v . dv, and the f16 tiles of u and E
+      {
+        const float bt = fac[kFbeta + r];
+        float db = 0.f, vs = 0.f, mu = 0.f, me = 0.f;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int x = 0; x < 4 * J; ++x) {
+          const uint32_t w = x & 2 ? vw[x / 4].y : vw[x / 4].x;
+          db = fmaf(e[x], u[x], db);
+          u[x] *= bt, e[x] *= bt;
+          vs = fmaf(__uint_as_float(x & 1 ? w & 0xffff0000u : w << 16), e[x], vs);
+          mu = max_nan(mu, fabsf(u[x])), me = max_nan(me, fabsf(e[x]));
+        }
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) {
+          db += __shfl_xor_sync(0xffffffffu, db, off);
+          vs += __shfl_xor_sync(0xffffffffu, vs, off);
+          mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
+          me = fmaxf(me, __shfl_xor_sync(0xffffffffu, me, off));
+        }
+        float iu, ie;
+        const float su = pow2_scale(mu, &iu), se = pow2_scale(me, &ie);
+        if (l8 == 0) {
+          if (r < c.rows) a.dbeta[size_t(c.row0 + r) * a.H_v + h] = db;
+          vd[r] = vs;
+          invU[r] = iu, invE[r] = ie;
+        }
+        uint16_t* dv = a.dv + (size_t(c.row0 + r) * a.H_v + h) * D + 4 * l8;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const float *up = u + 4 * j, *ep = e + 4 * j;
+          if (r < c.rows)
+            *reinterpret_cast<uint2*>(dv + 32 * j) =
+                make_uint2(pack_bf16x2(ep[0], ep[1]), pack_bf16x2(ep[2], ep[3]));
+          const int col = 4 * l8 + 32 * j;
+          const uint32_t at = sw128_offset(r, (col & 63) * 2);
+          uint2 uh, ul;
+          split_f16(up[0] * su, up[1] * su, uh.x, ul.x);
+          split_f16(up[2] * su, up[3] * su, uh.y, ul.y);
+          *reinterpret_cast<uint2*>(smem + L::UH + (col >> 6) * kBlk + at) = uh;
+          *reinterpret_cast<uint2*>(smem + L::UL + (col >> 6) * kBlk + at) = ul;
+          *reinterpret_cast<uint2*>(smem + L::OE + (col >> 6) * 2 * kBlk + kBlk + at) =
+              make_uint2(pack_f16(ep[0] * se, ep[1] * se), pack_f16(ep[2] * se, ep[3] * se));
+        }
+      }
+      ready(gU);
+      float ih, id, sd;
+      {
+        float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) m0 = max_nan(m0, hm[x]), m1 = max_nan(m1, hm[8 + x]);
+        const float sh = pow2_scale(m0, &ih);
+        sd = pow2_scale(m1, &id);
+        state_tile<D, true>(H, sh, smem + L::HH, smem + L::HL, [](const float (&)[8], int) {});
+      }
+      ready(gH);
+      // dH', and <H', dH'> on the way
+      {
+        float hh = 0.f;
+        state_tile<D, false>(dH, sd, smem + L::DH, nullptr, [&](const float (&v)[8], int at) {
+          const float4 x = *reinterpret_cast<const float4*>(H1 + at);
+          const float4 y = *reinterpret_cast<const float4*>(H1 + at + 4);
+          hh += fmaf(v[0], x.x, v[1] * x.y) + fmaf(v[2], x.z, v[3] * x.w);
+          hh += fmaf(v[4], y.x, v[5] * y.y) + fmaf(v[6], y.z, v[7] * y.w);
+        });
+        hh = warp_sum(hh);
+        if (lane == 0) red[warp] = hh;
+      }
+      ready(gD);
+      // P and N: lanes 0-63 are rows of P, 64-127 of N
+      float x[16], y[16];
+      mbar_wait(&bars[gPN], ph, abort_flag, err, 64u);
+      tc_fence_after();
+      tmem_ld16(tl + kTPN, x);
+      tmem_ld_wait();
+      float ip, in;
+      {
+        const bool isn = qd >= 2;
+        const int pr = dk & 63;
+        const float2 Gr = Gs[pr];
+        const float fr = isn ? -invE[pr] : a.scale * fac[kFinvO];
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int ps = 16 * cq + k;
+          float f = 0.f;
+          if (ps < pr || (ps == pr && !isn)) f = expdiff(Gr, Gs[ps]) * invU[ps] * fr;
+          x[k] = f == 0.f ? 0.f : x[k] * f;
+          m = max_nan(m, fabsf(x[k]));
+        }
+        const uint32_t um = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        if (lane == 0) atomicMax(&most[isn], um);
+        named_sync(1, kGradsWork);
+        const float sp = pow2_scale(__uint_as_float(most[0]), &ip);
+        const float sn = pow2_scale(__uint_as_float(most[1]), &in);
+        const float sc = isn ? sn : sp;
+        uint32_t ph_[8], pl_[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) split_f16(x[2 * k] * sc, x[2 * k + 1] * sc, ph_[k], pl_[k]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int rr = r0 + 16 * m + 8 * k + g8;
-          float x = 0.f;
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int col = 16 * cg + 8 * n + t2;
-            const float2 q = unpack_f16(*reinterpret_cast<const uint32_t*>(
-                smem + L::Q + (col >> 6) * kBlk + sw128_offset(rr, (col & 63) * 2)));
-            x = fmaf(q.x, dq[m][n][2 * k], fmaf(q.y, dq[m][n][2 * k + 1], x));
-            total[m][n][2 * k] += dq[m][n][2 * k];
-            total[m][n][2 * k + 1] += dq[m][n][2 * k + 1];
-          }
-          x += __shfl_xor_sync(0xffffffffu, x, 1);
-          x += __shfl_xor_sync(0xffffffffu, x, 2);
-          if ((lane & 3) == 0) part[cg * kBC + rr] = x * iq;
+          const uint32_t at = sw128_offset(pr, 32 * cq + 16 * k);
+          st_shared_v4(base + (isn ? L::N : L::PH) + at, ph_[4 * k], ph_[4 * k + 1],
+                       ph_[4 * k + 2], ph_[4 * k + 3]);
+          if (!isn)
+            st_shared_v4(base + L::PL + at, pl_[4 * k], pl_[4 * k + 1], pl_[4 * k + 2],
+                         pl_[4 * k + 3]);
         }
-      // <H', dH'>, while the other half is at its longer products
-      float hh = 0.f;
-#pragma unroll 4
-      for (int x = 4 * tid; x < D * D; x += 1024) {
-        const float4 y = *reinterpret_cast<const float4*>(H1 + x);
-        const float4 z = *reinterpret_cast<const float4*>(dH + x);
-        hh += fmaf(y.x, z.x, y.y * z.y) + fmaf(y.z, z.z, y.w * z.w);
       }
-      hh = warp_sum(hh);
-      if (lane == 0) red[w8] = hh;
-    } else {
-      // -(e^G beta E) H^T
+      ready(gP);
+      // dq and q . dq: row d_k of this thread, 16 chunk rows
+      mbar_wait(&bars[gA12], ph, abort_flag, err, 64u);
+      mbar_wait(&bars[gA345], ph, abort_flag, err, 64u);
+      tc_fence_after();
+      tmem_ld16(tl + kTA1, x);
+      tmem_ld16(tl + kTA3, y);
+      tmem_ld_wait();
+      {
+        const float f = a.scale * fac[kFinvO] * ih, fp = ip * fac[kFinvK], iq = fac[kFinvQ];
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t bh[4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float4 x = *reinterpret_cast<const float4*>(smem + L::H + kk * L::kSlice + at +
-                                                            512 * n);
-          bh[2 * n] = pack_f16(x.x * sh, x.y * sh);
-          bh[2 * n + 1] = pack_f16(x.z * sh, x.w * sh);
+        for (int k = 0; k < 16; ++k) {
+          const int rr = 16 * cq + k;
+          const float d = fmaf(x[k], f * fac[kFeG + rr], y[k] * fp);
+          dqs[k] += d;
+          float q = 0.f;
+          if (on)
+            q = __half2float(*reinterpret_cast<const __half*>(
+                    smem + L::Q + (dk >> 6) * kBlk + sw128_offset(rr, (dk & 63) * 2))) * d;
+          x[k] = q;
         }
-        rows_times<MT, false>(acc, base + L::E, r0, kk, bh, bh);
-      }
-      fold_in(total, acc, [&](int x) {
-        return -fac[kFeG + r0 + x + g8] * (invE[r0 + x + g8] * ih);
-      });
-      named_sync(3, 512);  // everybody is past the first two slices of H
-      load_slices(base + L::H, dH, CG - 2);
-      cp_async_commit();
-      cp_async_wait<1>();  // the two slices before them
-      named_sync(2, 256);
-      // (e^{G_C - G} beta u) dH'^T
-      float m1 = 0.f, id;
+        // sum over the 32 lanes, the 16 rows spread over them
 #pragma unroll
-      for (int x = 0; x < 8; ++x) m1 = max_nan(m1, hm[8 + x]);
-      const float sd = pow2_scale(m1, &id);
+        for (int w = 8; w >= 1; w >>= 1) {
+          const bool up = lane & (2 * w);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        if (kk == D / 16 - 2) {
-          cp_async_wait<0>();
-          named_sync(2, 256);
-        }
-        uint32_t bh[4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float4 x =
-              *reinterpret_cast<const float4*>(smem + L::dh_slice(kk) + at + 512 * n);
-          bh[2 * n] = pack_f16(x.x * sd, x.y * sd);
-          bh[2 * n + 1] = pack_f16(x.z * sd, x.w * sd);
-        }
-        rows_times<MT, false>(acc, base + L::UH, r0, kk, bh, bh);
-      }
-      fold_in(total, acc, [&](int x) {
-        return fac[kFeT + r0 + x + g8] * (invU[r0 + x + g8] * id);
-      });
-      named_sync(2, 256);  // N
-      // N K and N^T K
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        uint32_t bv[4];
-        ldsm4t(bv, piece<false>(base + L::K, 16 * kk, 16 * cg));
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint32_t av[4];
-          if (kk <= r0 / 16 + m) {
-            ldsm4(av, piece<false>(base + L::N, r0 + 16 * m, 16 * kk));
-            mma16(acc[m][0], av, bv[0], bv[1]);
-            mma16(acc[m][1], av, bv[2], bv[3]);
-          }
-          if (kk >= r0 / 16 + m) {
-            ldsm4t(av, piece<true>(base + L::N, 16 * kk, r0 + 16 * m));
-            mma16(acc[m][0], av, bv[0], bv[1]);
-            mma16(acc[m][1], av, bv[2], bv[3]);
+          for (int k = 0; k < w; ++k) {
+            const float send = up ? x[k] : x[k + w];
+            x[k] = (up ? x[k + w] : x[k]) + __shfl_xor_sync(0xffffffffu, send, 2 * w);
           }
         }
+        x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+        if ((lane & 1) == 0) part[qd * kBC + 16 * cq + (lane >> 1)] = x[0] * iq;
       }
-      float in;
-      pow2_scale(__uint_as_float(most[1]), &in);
-      const float fn = in * fac[kFinvK];
-      fold_in(total, acc, [&](int) { return fn; });
-    }
-    __syncthreads();  // P, part, red
-    if (kside) {
-      // P^T Q
+      // dk
+      tmem_ld16(tl + kTA2, x);
+      tmem_ld16(tl + kTA4, y);
+      tmem_ld_wait();
+      {
+        const float fq = ip * fac[kFinvQ];
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        uint32_t bv[4];
-        ldsm4t(bv, piece<false>(base + L::Q, 16 * kk, 16 * cg));
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          if (kk >= r0 / 16 + m) {
-            uint32_t av[4];
-            ldsm4t(av, piece<true>(base + L::PH, 16 * kk, r0 + 16 * m));
-            mma16(acc[m][0], av, bv[0], bv[1]);
-            mma16(acc[m][1], av, bv[2], bv[3]);
-          }
+        for (int k = 0; k < 16; ++k) {
+          const int rr = 16 * cq + k;
+          dks[k] += fmaf(y[k], fq, x[k] * (-fac[kFeG + rr] * (invE[rr] * ih)));
+        }
       }
-      float ip;
-      pow2_scale(__uint_as_float(most[0]), &ip);
-      const float fq = ip * fac[kFinvQ];
-      fold_in(total, acc, [&](int) { return fq; });
-    } else if (warp == 0) {
+      mbar_wait(&bars[gA6], ph, abort_flag, err, 64u);
+      tc_fence_after();
+      tmem_ld16(tl + kTA5, x);
+      tmem_ld16(tl + kTA6, y);
+      tmem_ld_wait();
+      {
+        const float fn = in * fac[kFinvK];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int rr = 16 * cq + k;
+          dks[k] += fmaf(x[k], fn, y[k] * (fac[kFeT + rr] * (invU[rr] * id)));
+        }
+      }
+      tc_fence_before();
+      named_sync(1, kGradsWork);  // part and red
       // dg: suffix sums over the rows, two per lane, on top of <H', dH'>
-      double x[2], run;
+      if (warp == 0) {
+        double z[2], run;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int rr = 63 - (2 * lane + k);
-        float sum = 0.f;
+        for (int k = 0; k < 2; ++k) {
+          const int rr = 63 - (2 * lane + k);
+          float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < CG; ++w) sum += part[w * kBC + rr];
-        x[k] = rr < c.rows ? double(sum) - double(vd[rr]) : 0.0;
+          for (int w = 0; w < D / 32; ++w) sum += part[w * kBC + rr];
+          z[k] = rr < c.rows ? double(sum) - double(vd[rr]) : 0.0;
+        }
+        z[1] += z[0];
+        run = z[1];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const double w = __shfl_up_sync(0xffffffffu, run, off);
+          if (lane >= off) run += w;
+        }
+        double hh = 0.0;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) hh += red[w];
+        z[0] += run - z[1];
+        z[1] = run;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int rr = 63 - (2 * lane + k);
+          if (rr < c.rows) a.dg[size_t(c.row0 + rr) * a.H_v + h] = float(z[k] + hh);
+        }
       }
-      x[1] += x[0];
-      run = x[1];
+      named_sync(1, kGradsWork);  // the tiles and factors are rewritten for the next head
+    }
+    if (on) {
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, run, off);
-        if (lane >= off) run += y;
-      }
-      double hh = 0.0;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) hh += red[w];
-      x[0] += run - x[1];
-      x[1] = run;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int rr = 63 - (2 * lane + k);
-        if (rr < c.rows) a.dg[size_t(c.row0 + rr) * a.H_v + h] = float(x[k] + hh);
+      for (int k = 0; k < 16; ++k) {
+        const int rr = 16 * cq + k;
+        if (rr < c.rows) {
+          const size_t at = (size_t(c.row0 + rr) * a.H_k + hk) * D + dk;
+          a.dq[at] = __bfloat16_as_ushort(__float2bfloat16_rn(dqs[k]));
+          a.dk[at] = __bfloat16_as_ushort(__float2bfloat16_rn(dks[k]));
+        }
       }
     }
-    __syncthreads();  // the tiles and factors are rewritten for the next head
+  } else {
+   if (lane == 0) {
+    // The issuer; it also loads K, Q and each head's dO.
+    const uint64_t kmaj = make_sdesc_sw128(0, 16, 1024);
+    const uint64_t mnmaj = make_sdesc_sw128(0, 8192, 1024);
+    constexpr uint32_t id64 = make_idesc_f16(128, 64, 0, 0), id128 = make_idesc_f16(128, 128, 0, 0);
+    constexpr uint32_t id_a = make_idesc_f16(128, 64, 1, 0);   // A MN-major
+    constexpr uint32_t id_ab = make_idesc_f16(128, 64, 1, 1);  // both MN-major
+    auto load_o = [&](int h) {
+      const uint8_t* src = a.O + (size_t(i) * a.H_v + h) * L::kTile;
+      for (int x = 0; x < D / 64; ++x)
+        bulk_load_g2s(smem + L::OE + x * 2 * kBlk, src + x * kBlk, kBlk, &bars[gO]);
+    };
+    mbar_arrive_expect_tx(&bars[gO], 3 * L::kTile);
+    bulk_load_g2s(smem + L::K, a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile, 2 * L::kTile,
+                  &bars[gO]);
+    load_o(h0);
+    int loads = 1;
+    const uint32_t oe = base + L::OE, uh = base + L::UH, ul = base + L::UL;
+    // descriptors: tall tiles (128 rows a block of 64 columns) and short ones
+    auto tall = [&](uint32_t tile, int kk) {
+      return kmaj + ((tile + (kk >> 2) * 2 * kBlk + (kk & 3) * 32) >> 4);
+    };
+    auto flat = [&](uint32_t tile, int kk) {
+      return kmaj + ((tile + (kk >> 2) * kBlk + (kk & 3) * 32) >> 4);
+    };
+    auto rows = [&](uint32_t tile, int kk) { return mnmaj + ((tile + kk * 2048) >> 4); };
+    bool ok = true;
+    for (int h = h0; h < h0 + vpg && ok; ++h) {
+      const uint32_t ph = (h - h0) & 1;
+      ok = mbar_wait(&bars[gO], ph, abort_flag, err, 128u) &&
+           mbar_wait(&bars[gU], ph, abort_flag, err, 128u);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_bf16_ss(tmem + kTPN, tall(oe, kk), flat(ul, kk), id64, kk != 0);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_bf16_ss(tmem + kTPN, tall(oe, kk), flat(uh, kk), id64, 1u);
+      mma_commit(&bars[gPN]);
+      ok = mbar_wait(&bars[gH], ph, abort_flag, err, 128u);
+      if (!ok) break;
+      tc_fence_after();
+      // the low limb first, for dO alone; then both, the second half of the columns fresh
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_bf16_ss(tmem + kTA1, tall(base + L::HL, kk), tall(oe, kk), id64, kk != 0);
+      mma_bf16_ss(tmem + kTA1, tall(base + L::HH, 0), tall(oe, 0), id64, 1u);
+      mma_bf16_ss(tmem + kTA2, tall(base + L::HH, 0), tall(oe + kBlk, 0), id64, 0u);
+#pragma unroll
+      for (int kk = 1; kk < D / 16; ++kk)
+        mma_bf16_ss(tmem + kTA1, tall(base + L::HH, kk), tall(oe, kk), id128, 1u);
+      mma_commit(&bars[gA12]);
+      ok = mbar_wait(&bars[gD], ph, abort_flag, err, 128u);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_bf16_ss(tmem + kTA6, tall(base + L::DH, kk), flat(uh, kk), id64, kk != 0);
+      mma_commit(&bars[gA6]);
+      ok = mbar_wait(&bars[gP], ph, abort_flag, err, 128u);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ss(tmem + kTA3, rows(base + L::K, kk), flat(base + L::PL, kk), id_a, kk != 0);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ss(tmem + kTA3, rows(base + L::K, kk), flat(base + L::PH, kk), id_a, 1u);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ss(tmem + kTA4, rows(base + L::Q, kk), rows(base + L::PH, kk), id_ab, kk != 0);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ss(tmem + kTA5, rows(base + L::K, kk), flat(base + L::N, kk), id_a, kk != 0);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ss(tmem + kTA5, rows(base + L::K, kk), rows(base + L::N, kk), id_ab, 1u);
+      mma_commit(&bars[gA345]);
+      if (h + 1 < h0 + vpg) {  // dO's last reader is done
+        ok = mbar_wait(&bars[gA12], ph, abort_flag, err, 128u);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&bars[gO], L::kTile);
+        load_o(h + 1);
+        ++loads;
+      }
+    }
+    mma_commit(&bars[gDrain]);
+    mbar_wait(&bars[gDrain], 0, nullptr, err, 32u);
+    mbar_wait(&bars[gO], (loads - 1) & 1, nullptr, err, 32u);
+   }
+   __syncwarp();
   }
-  uint16_t* out = kside ? a.dk : a.dq;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = r0 + 16 * m + 8 * e + g8;
-      if (r >= c.rows) continue;
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-        *reinterpret_cast<uint32_t*>(out + (size_t(c.row0 + r) * a.H_k + hk) * D + 16 * cg +
-                                     8 * n + t2) =
-            pack_bf16x2(total[m][n][2 * e], total[m][n][2 * e + 1]);
-    }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -1637,7 +1626,7 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   cfg.attrs = &beside;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, bwd_scan_kernel<D, false>, a)) != cudaSuccess) return e;
-  bwd_grads_kernel<D><<<dim3(a.max_chunks, a.H_k), 512, grads, s>>>(a);
+  bwd_grads_kernel<D><<<dim3(a.max_chunks, a.H_k), kGradsThreads, grads, s>>>(a);
   return cudaGetLastError();
 }
 
