@@ -77,11 +77,12 @@ struct BwdArgs {
   float* Hmax;         // [chunk][H_v][2][8] largest |H| and |dH| of each scan warp's part
 };
 
-// Per-unit factors: of each row e^G, e^{G_C - G}, beta and the products beta
-// e^{G_C - G} and beta e^G, then scalars.
+// Per-unit factors: of each row e^G, e^{G_C - G}, beta, the products beta
+// e^{G_C - G} and beta e^G, and e^{G_b - G} with b the last row of its 16-row
+// block; then scalars.
 enum { kFeG = 0, kFeT = kBC, kFbeta = 2 * kBC, kFbT = 3 * kBC, kFbG = 4 * kBC,
-       kFeC = 5 * kBC, kFinvK, kFinvQ, kFinvO, kFinvS, kFinvGO };
-constexpr int kFac = 5 * kBC + 8;
+       kFend = 5 * kBC, kFeC = 6 * kBC, kFinvK, kFinvQ, kFinvO, kFinvS, kFinvGO };
+constexpr int kFac = 6 * kBC + 8;
 
 __device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(uint32_t(x) << 16); }
 __device__ __forceinline__ float expdiff(float2 a, float2 b) {
@@ -394,6 +395,8 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
         const float2 G = make_float2(hi, float(x[e] - double(hi)));
         Gs[2 * lane + e] = G;
         a.G[unit * kBC + 2 * lane + e] = G;
+        const double end = __shfl_sync(0xffffffffu, x[1], lane | 7);
+        fac[kFend + 2 * lane + e] = exp2f(float(end - x[e]));
         const float eG = exp2f(G.x + G.y), eT = exp2f(float(total - x[e]));
         fac[kFeG + 2 * lane + e] = eG;
         eGs[2 * lane + e] = a.scale * eG;
@@ -1124,30 +1127,39 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
 // A state's slices into a tall f16 tile (and, with LO, its low limb into a second
 // one): eight values of one d_k row at a time, lanes along d_k.  f(values, offset
 // of the first in the state) sees them in f32.
-template <int D, bool LO, class F>
-__device__ __forceinline__ void state_tile(const float* st, float s, uint8_t* hi, uint8_t* lo,
+// The thread's pieces are loaded BATCH at a time, before any of them is stored.
+template <int D, bool LO, int BATCH, class F>
+__device__ __forceinline__ void state_tile(const float* st, float s, uint32_t hi, uint32_t lo,
                                            F f) {
+  constexpr int kPieces = D * D / 8 / kGradsWork, B = BATCH < kPieces ? BATCH : kPieces;
 #pragma unroll
-  for (int m = 0; m < D * D / 8 / kGradsWork; ++m) {
-    const int x = threadIdx.x + m * kGradsWork;
-    const int dk = x % D, half = x / D % 2, slice = x / (2 * D);
-    const int at = slice * D * 16 + dk * 16 + half * 8;
-    float v[8];
-    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(st + at);
-    *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(st + at + 4);
-    f(v, at);
-    uint32_t h[4], l[4];
+  for (int m0 = 0; m0 < kPieces; m0 += B) {
+    float v[B][8];
+    int at[B];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (LO)
-        split_f16(v[2 * e] * s, v[2 * e + 1] * s, h[e], l[e]);
-      else
-        h[e] = pack_f16(v[2 * e] * s, v[2 * e + 1] * s);
+    for (int m = 0; m < B; ++m) {
+      const int x = threadIdx.x + (m0 + m) * kGradsWork;
+      at[m] = x / (2 * D) * (D * 16) + x % D * 16 + x / D % 2 * 8;
+      *reinterpret_cast<float4*>(v[m]) = *reinterpret_cast<const float4*>(st + at[m]);
+      *reinterpret_cast<float4*>(v[m] + 4) = *reinterpret_cast<const float4*>(st + at[m] + 4);
     }
-    const int col = slice * 16 + half * 8;
-    const uint32_t to = (col >> 6) * 2 * kBlk + sw128_offset(dk, (col & 63) * 2);
-    *reinterpret_cast<uint4*>(hi + to) = make_uint4(h[0], h[1], h[2], h[3]);
-    if constexpr (LO) *reinterpret_cast<uint4*>(lo + to) = make_uint4(l[0], l[1], l[2], l[3]);
+    f(v, at);
+#pragma unroll
+    for (int m = 0; m < B; ++m) {
+      const int x = threadIdx.x + (m0 + m) * kGradsWork;
+      const int dk = x % D, col = x / (2 * D) * 16 + x / D % 2 * 8;
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (LO)
+          split_f16(v[m][2 * e] * s, v[m][2 * e + 1] * s, h[e], l[e]);
+        else
+          h[e] = pack_f16(v[m][2 * e] * s, v[m][2 * e + 1] * s);
+      }
+      const uint32_t to = (col >> 6) * 2 * kBlk + sw128_offset(dk, (col & 63) * 2);
+      st_shared_v4(hi + to, h[0], h[1], h[2], h[3]);
+      if constexpr (LO) st_shared_v4(lo + to, l[0], l[1], l[2], l[3]);
+    }
   }
 }
 
@@ -1203,6 +1215,15 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         cp_async16(base + L::M + p * 64 + (tid - 192) * 16, a.Hmax + unit * 16 + (tid - 192) * 4);
       cp_async_commit();
     };
+    // u and E of head h, into the place of H's limbs
+    auto load_rows = [&](int h) {
+      const size_t unit = size_t(i) * a.H_v + h;
+      cp_async_block<kGradsWork>(base + L::HL, reinterpret_cast<const uint8_t*>(a.u + unit * kBC * D),
+                                 kBC * D * 4);
+      cp_async_block<kGradsWork>(base + L::HH, reinterpret_cast<const uint8_t*>(a.E + unit * kBC * D),
+                                 kBC * D * 4);
+      cp_async_commit();
+    };
     // this warp's part of a tile is written: the issuer may use it
     auto ready = [&](int b) {
       fence_proxy_async_smem();
@@ -1212,6 +1233,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     };
     float dqs[16] = {}, dks[16] = {};
     load_head(h0);
+    load_rows(h0);
     for (int h = h0; h < h0 + vpg; ++h) {
       const uint32_t ph = (h - h0) & 1;
       const size_t unit = size_t(i) * a.H_v + h;
@@ -1223,16 +1245,11 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       const float* dH = a.dH + unit * D * D;
       // Rows 4 w .. 4 w + 3, 8 lanes a row, 4 J columns a lane.
       const int r = 4 * warp + (lane >> 3), l8 = lane & 7;
-      float u[4 * J], e[4 * J];
       uint2 vw[J];
       {
-        const float* up = a.u + (unit * kBC + r) * D + 4 * l8;
-        const float* ep = a.E + (unit * kBC + r) * D + 4 * l8;
         const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + h * D + 4 * l8;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          *reinterpret_cast<float4*>(u + 4 * j) = *reinterpret_cast<const float4*>(up + 32 * j);
-          *reinterpret_cast<float4*>(e + 4 * j) = *reinterpret_cast<const float4*>(ep + 32 * j);
           vw[j] = make_uint2(0u, 0u);
           if (r < c.rows) vw[j] = *reinterpret_cast<const uint2*>(vp + 32 * j);
         }
@@ -1245,17 +1262,22 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         }
         prefetch_l2(H1, D * D * 4);
         if (h + 1 < h0 + vpg) {
-          prefetch_l2(a.u + (unit + 1) * kBC * D, kBC * D * 4);
-          prefetch_l2(a.E + (unit + 1) * kBC * D, kBC * D * 4);
           prefetch_l2(H + D * D, D * D * 4);
           prefetch_l2(dH + D * D, D * D * 4);
         }
       }
-      cp_async_wait<0>();  // the factors
+      cp_async_wait<0>();  // the factors, u and E
       named_sync(1, kGradsWork);
       if (h + 1 < h0 + vpg) load_head(h + 1);
       // dv, dbeta, v . dv, and the f16 tiles of u and E
       {
+        float u[4 * J], e[4 * J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int at = (r * D + 4 * l8 + 32 * j) * 4;
+          *reinterpret_cast<float4*>(u + 4 * j) = *reinterpret_cast<const float4*>(smem + L::HL + at);
+          *reinterpret_cast<float4*>(e + 4 * j) = *reinterpret_cast<const float4*>(smem + L::HH + at);
+        }
         const float bt = fac[kFbeta + r];
         float db = 0.f, vs = 0.f, mu = 0.f, me = 0.f;
 #pragma unroll
@@ -1306,17 +1328,27 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         for (int x = 0; x < 8; ++x) m0 = max_nan(m0, hm[x]), m1 = max_nan(m1, hm[8 + x]);
         const float sh = pow2_scale(m0, &ih);
         sd = pow2_scale(m1, &id);
-        state_tile<D, true>(H, sh, smem + L::HH, smem + L::HL, [](const float (&)[8], int) {});
+        named_sync(1, kGradsWork);  // everybody has read the rows out of these tiles' place
+        state_tile<D, true, 4>(H, sh, base + L::HH, base + L::HL,
+                               [](const auto&, const auto&) {});
       }
       ready(gH);
       // dH', and <H', dH'> on the way
       {
         float hh = 0.f;
-        state_tile<D, false>(dH, sd, smem + L::DH, nullptr, [&](const float (&v)[8], int at) {
-          const float4 x = *reinterpret_cast<const float4*>(H1 + at);
-          const float4 y = *reinterpret_cast<const float4*>(H1 + at + 4);
-          hh += fmaf(v[0], x.x, v[1] * x.y) + fmaf(v[2], x.z, v[3] * x.w);
-          hh += fmaf(v[4], y.x, v[5] * y.y) + fmaf(v[6], y.z, v[7] * y.w);
+        state_tile<D, false, 2>(dH, sd, base + L::DH, 0u, [&](const auto& v, const auto& at) {
+          constexpr int B = sizeof(at) / sizeof(at[0]);
+          float4 x[B], y[B];
+#pragma unroll
+          for (int m = 0; m < B; ++m) {
+            x[m] = *reinterpret_cast<const float4*>(H1 + at[m]);
+            y[m] = *reinterpret_cast<const float4*>(H1 + at[m] + 4);
+          }
+#pragma unroll
+          for (int m = 0; m < B; ++m) {
+            hh += fmaf(v[m][0], x[m].x, v[m][1] * x[m].y) + fmaf(v[m][2], x[m].z, v[m][3] * x[m].w);
+            hh += fmaf(v[m][4], y[m].x, v[m][5] * y[m].y) + fmaf(v[m][6], y[m].z, v[m][7] * y[m].w);
+          }
         });
         hh = warp_sum(hh);
         if (lane == 0) red[warp] = hh;
@@ -1331,17 +1363,30 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       float ip, in;
       {
         const bool isn = qd >= 2;
-        const int pr = dk & 63;
+        const int pr = dk & 63, pb = pr >> 4;
         const float2 Gr = Gs[pr];
         const float fr = isn ? -invE[pr] : a.scale * fac[kFinvO];
         float m = 0.f;
+        if (pb > cq) {
+          // below the diagonal blocks: the decay in two factors, split at the end of the
+          // column block
+          const float fe = fr * expdiff(Gr, Gs[16 * cq + 15]);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int ps = 16 * cq + k;
-          float f = 0.f;
-          if (ps < pr || (ps == pr && !isn)) f = expdiff(Gr, Gs[ps]) * invU[ps] * fr;
-          x[k] = f == 0.f ? 0.f : x[k] * f;
-          m = max_nan(m, fabsf(x[k]));
+          for (int k = 0; k < 16; ++k) {
+            x[k] *= fe * (fac[kFend + 16 * cq + k] * invU[16 * cq + k]);
+            m = max_nan(m, fabsf(x[k]));
+          }
+        } else if (pb == cq) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int ps = 16 * cq + k;
+            const bool in_ = ps < pr || (ps == pr && !isn);
+            x[k] = in_ ? x[k] * (expdiff(Gr, Gs[ps]) * invU[ps] * fr) : 0.f;
+            m = max_nan(m, fabsf(x[k]));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = 0.f;
         }
         const uint32_t um = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
         if (lane == 0) atomicMax(&most[isn], um);
@@ -1365,6 +1410,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       ready(gP);
       // dq and q . dq: row d_k of this thread, 16 chunk rows
       mbar_wait(&bars[gA12], ph, abort_flag, err, 64u);
+      if (h + 1 < h0 + vpg) load_rows(h + 1);
       mbar_wait(&bars[gA345], ph, abort_flag, err, 64u);
       tc_fence_after();
       tmem_ld16(tl + kTA1, x);
