@@ -1125,40 +1125,35 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
 }
 
 // A state's slices into a tall f16 tile (and, with LO, its low limb into a second
-// one): eight values of one d_k row at a time, lanes along d_k.  f(values, offset
-// of the first in the state) sees them in f32.
-// The thread's pieces are loaded BATCH at a time, before any of them is stored.
+// one), a quad of one d_k row at a time: 512 contiguous bytes a warp and load.
+// f(quads, their places in the state) sees them in f32.  The thread's quads are
+// loaded BATCH at a time, before any of them is stored.
 template <int D, bool LO, int BATCH, class F>
 __device__ __forceinline__ void state_tile(const float* st, float s, uint32_t hi, uint32_t lo,
                                            F f) {
-  constexpr int kPieces = D * D / 8 / kGradsWork, B = BATCH < kPieces ? BATCH : kPieces;
+  constexpr int kQuads = D * D / 4 / kGradsWork, B = BATCH < kQuads ? BATCH : kQuads;
 #pragma unroll
-  for (int m0 = 0; m0 < kPieces; m0 += B) {
-    float v[B][8];
-    int at[B];
+  for (int m0 = 0; m0 < kQuads; m0 += B) {
+    float4 v[B];
 #pragma unroll
-    for (int m = 0; m < B; ++m) {
-      const int x = threadIdx.x + (m0 + m) * kGradsWork;
-      at[m] = x / (2 * D) * (D * 16) + x % D * 16 + x / D % 2 * 8;
-      *reinterpret_cast<float4*>(v[m]) = *reinterpret_cast<const float4*>(st + at[m]);
-      *reinterpret_cast<float4*>(v[m] + 4) = *reinterpret_cast<const float4*>(st + at[m] + 4);
-    }
-    f(v, at);
+    for (int m = 0; m < B; ++m)
+      v[m] = *reinterpret_cast<const float4*>(st + 4 * (threadIdx.x + (m0 + m) * kGradsWork));
+    f(v, 4 * (threadIdx.x + m0 * kGradsWork));
 #pragma unroll
     for (int m = 0; m < B; ++m) {
-      const int x = threadIdx.x + (m0 + m) * kGradsWork;
-      const int dk = x % D, col = x / (2 * D) * 16 + x / D % 2 * 8;
-      uint32_t h[4], l[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (LO)
-          split_f16(v[m][2 * e] * s, v[m][2 * e + 1] * s, h[e], l[e]);
-        else
-          h[e] = pack_f16(v[m][2 * e] * s, v[m][2 * e + 1] * s);
-      }
+      const int x = threadIdx.x + (m0 + m) * kGradsWork;  // slice, d_k, quad
+      const int dk = (x >> 2) % D, col = x / (4 * D) * 16 + (x & 3) * 4;
       const uint32_t to = (col >> 6) * 2 * kBlk + sw128_offset(dk, (col & 63) * 2);
-      st_shared_v4(hi + to, h[0], h[1], h[2], h[3]);
-      if constexpr (LO) st_shared_v4(lo + to, l[0], l[1], l[2], l[3]);
+      uint32_t h0, h1, l0, l1;
+      if constexpr (LO) {
+        split_f16(v[m].x * s, v[m].y * s, h0, l0);
+        split_f16(v[m].z * s, v[m].w * s, h1, l1);
+        st_shared_v2(lo + to, l0, l1);
+      } else {
+        h0 = pack_f16(v[m].x * s, v[m].y * s);
+        h1 = pack_f16(v[m].z * s, v[m].w * s);
+      }
+      st_shared_v2(hi + to, h0, h1);
     }
   }
 }
@@ -1329,26 +1324,21 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         const float sh = pow2_scale(m0, &ih);
         sd = pow2_scale(m1, &id);
         named_sync(1, kGradsWork);  // everybody has read the rows out of these tiles' place
-        state_tile<D, true, 4>(H, sh, base + L::HH, base + L::HL,
-                               [](const auto&, const auto&) {});
+        state_tile<D, true, 8>(H, sh, base + L::HH, base + L::HL, [](const auto&, int) {});
       }
       ready(gH);
       // dH', and <H', dH'> on the way
       {
         float hh = 0.f;
-        state_tile<D, false, 2>(dH, sd, base + L::DH, 0u, [&](const auto& v, const auto& at) {
-          constexpr int B = sizeof(at) / sizeof(at[0]);
-          float4 x[B], y[B];
+        state_tile<D, false, 4>(dH, sd, base + L::DH, 0u, [&](const auto& v, int at) {
+          constexpr int B = sizeof(v) / sizeof(v[0]);
+          float4 x[B];
 #pragma unroll
-          for (int m = 0; m < B; ++m) {
-            x[m] = *reinterpret_cast<const float4*>(H1 + at[m]);
-            y[m] = *reinterpret_cast<const float4*>(H1 + at[m] + 4);
-          }
+          for (int m = 0; m < B; ++m)
+            x[m] = *reinterpret_cast<const float4*>(H1 + at + 4 * m * kGradsWork);
 #pragma unroll
-          for (int m = 0; m < B; ++m) {
-            hh += fmaf(v[m][0], x[m].x, v[m][1] * x[m].y) + fmaf(v[m][2], x[m].z, v[m][3] * x[m].w);
-            hh += fmaf(v[m][4], y[m].x, v[m][5] * y[m].y) + fmaf(v[m][6], y[m].z, v[m][7] * y[m].w);
-          }
+          for (int m = 0; m < B; ++m)
+            hh += fmaf(v[m].x, x[m].x, v[m].y * x[m].y) + fmaf(v[m].z, x[m].z, v[m].w * x[m].w);
         });
         hh = warp_sum(hh);
         if (lane == 0) red[warp] = hh;

@@ -412,6 +412,10 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                : "memory");
 }
 
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
 // Four 8x8 b16 matrices, each stored transposed: thread t holds element
 // (t / 4, 2 (t % 4) + e) of matrix m in the e-th half of reg m; threads
 // 8 m .. 8 m + 7 give the addresses of the stored rows 0..7 of matrix m
