@@ -1078,9 +1078,8 @@ cudaError_t take_err_backward(uint32_t* out) {
 }
 
 // ---------------------------------------------------------------------------
-// Grads: one CTA of 16 working warps and an issuing one per (chunk, key head), the
-// value heads of the group one after another, so that the shared dq and dk are
-// summed in registers, in one order.
+// Grads: one CTA per (chunk, key head), the value heads of the group one after
+// another, so that the shared dq and dk are summed in registers, in one order.
 //
 // All products are transposed, M = 128 rows d_k (or, for P and N, the rows of dO
 // above those of beta E), so that two of them share an MMA where they share an
@@ -1090,9 +1089,13 @@ cudaError_t take_err_backward(uint32_t* out) {
 //   A3           = P K (two limbs),  A4 = P^T Q,  A5 = N K + N^T K   K = 64
 //   A6           = dH' (beta u)^T                    K = d_v
 //   dq = scale e^G A1 + A3,  dk = A4 + A5 - e^G A2 + e^{G_C - G} A6.
-// The warps turn f32 rows and states into f16 tiles in shared memory while the
-// products of the tiles before run; row factors that differ within a product are
-// applied to its result.
+// Row factors that differ within a product are applied to its result.
+//   warps 0-7: rows u and E to tiles, the masks of P and N, the sums dq, dk, dg;
+//   warps 8-11: states to tiles and <H', dH'>, as far as a head ahead;
+//   warp 12: one thread loads K, Q, dO and issues the MMAs.
+// Bound by the first eight warps' instructions and the latency of the states'
+// loads; the two groups overlap.  (All 16 warps in step took 320 us at 4576 rows,
+// 48 heads, the same products as warp-level MMAs 400 us.)
 // ---------------------------------------------------------------------------
 
 template <int D>
@@ -1107,16 +1110,17 @@ struct GradsSmem {
   static constexpr int PH = DH + kTall, PL = PH + kBlk, N = PL + kBlk;
   static constexpr int Fac = N + kBlk;           // two buffers of the unit's factors
   static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
-  static constexpr int M = G + 2 * kBC * 8;      // two buffers of the states' largest values
-  static constexpr int F = M + 2 * 16 * 4;       // floats from here
-  static constexpr int kFloats = 2 * kBC + 4 * kBC + kBC + 16;
+  static constexpr int F = G + 2 * kBC * 8;      // floats from here
+  static constexpr int kFloats = 3 * kBC + 4 * kBC + kBC + 24;
   static constexpr int Bars = F + kFloats * 4;
   static constexpr int kUsed = Bars + 16 * 8 + 16 + 1024;
   // More than half of an SM's: all of its tensor memory goes to one CTA.
   static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
 };
 
-constexpr int kGradsWork = 512, kGradsThreads = kGradsWork + 32;
+constexpr int kGradsRows = 256, kGradsStates = 128, kGradsThreads = 512;
+// Registers after re-allocation: 128 (2 x 176 + 112 + 48) is the launch's 512 x 128.
+constexpr uint32_t kRegsRows = 176, kRegsStates = 112, kRegsIssue = 48;
 enum { gO = 0, gU, gH, gP, gD, gPN, gA12, gA345, gA6, gDrain, kGradsBars };
 enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA4 = 256, kTA5 = 320, kTA6 = 384 };
 
@@ -1124,37 +1128,27 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-// A state's slices into a tall f16 tile (and, with LO, its low limb into a second
-// one), a quad of one d_k row at a time: 512 contiguous bytes a warp and load.
-// f(quads, their places in the state) sees them in f32.  The thread's quads are
-// loaded BATCH at a time, before any of them is stored.
-template <int D, bool LO, int BATCH, class F>
-__device__ __forceinline__ void state_tile(const float* st, float s, uint32_t hi, uint32_t lo,
-                                           F f) {
-  constexpr int kQuads = D * D / 4 / kGradsWork, B = BATCH < kQuads ? BATCH : kQuads;
+// B quads (float4) of a state into a tall f16 tile (and, with LO, their low limbs
+// into a second one): quad q of the state is thread q's, so a warp loads 512
+// contiguous bytes.
+template <int D, bool LO, int B>
+__device__ __forceinline__ void quads_to_tile(const float4 (&v)[B], int q0, float s, uint32_t hi,
+                                              uint32_t lo) {
 #pragma unroll
-  for (int m0 = 0; m0 < kQuads; m0 += B) {
-    float4 v[B];
-#pragma unroll
-    for (int m = 0; m < B; ++m)
-      v[m] = *reinterpret_cast<const float4*>(st + 4 * (threadIdx.x + (m0 + m) * kGradsWork));
-    f(v, 4 * (threadIdx.x + m0 * kGradsWork));
-#pragma unroll
-    for (int m = 0; m < B; ++m) {
-      const int x = threadIdx.x + (m0 + m) * kGradsWork;  // slice, d_k, quad
-      const int dk = (x >> 2) % D, col = x / (4 * D) * 16 + (x & 3) * 4;
-      const uint32_t to = (col >> 6) * 2 * kBlk + sw128_offset(dk, (col & 63) * 2);
-      uint32_t h0, h1, l0, l1;
-      if constexpr (LO) {
-        split_f16(v[m].x * s, v[m].y * s, h0, l0);
-        split_f16(v[m].z * s, v[m].w * s, h1, l1);
-        st_shared_v2(lo + to, l0, l1);
-      } else {
-        h0 = pack_f16(v[m].x * s, v[m].y * s);
-        h1 = pack_f16(v[m].z * s, v[m].w * s);
-      }
-      st_shared_v2(hi + to, h0, h1);
+  for (int m = 0; m < B; ++m) {
+    const int x = q0 + m * kGradsStates;  // slice, d_k, quad
+    const int dk = (x >> 2) % D, col = x / (4 * D) * 16 + (x & 3) * 4;
+    const uint32_t to = (col >> 6) * 2 * kBlk + sw128_offset(dk, (col & 63) * 2);
+    uint32_t h0, h1, l0, l1;
+    if constexpr (LO) {
+      split_f16(v[m].x * s, v[m].y * s, h0, l0);
+      split_f16(v[m].z * s, v[m].w * s, h1, l1);
+      st_shared_v2(lo + to, l0, l1);
+    } else {
+      h0 = pack_f16(v[m].x * s, v[m].y * s);
+      h1 = pack_f16(v[m].z * s, v[m].w * s);
     }
+    st_shared_v2(hi + to, h0, h1);
   }
 }
 
@@ -1177,7 +1171,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   const int vpg = a.H_v / a.H_k, h0 = hk * vpg;
   if (tid == 0) {
     for (int b = 0; b < kGradsBars; ++b)
-      mbar_init(&bars[b], b >= gU && b <= gD ? kGradsWork / 32 : 1);
+      mbar_init(&bars[b], b == gU || b == gP ? kGradsRows / 32 : b == gH || b == gD ? kGradsStates / 32 : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -1186,18 +1180,27 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  float* invU = reinterpret_cast<float*>(smem + L::F);
+  float* invE = invU + kBC;
+  float* endU = invE + kBC;         // invU e^{G_b - G}
+  float* part = endU + kBC;         // [4][64] q . dq of each 32 rows d_k
+  float* vd = part + 4 * kBC;       // [64] v . dv
+  float* red = vd + kBC;            // by the head's parity: [2][8] <H', dH'>, [2][2] 1 / scale of H, dH'
+  // this warp's part of a tile is written: the issuer may use it
+  auto ready = [&](int b) {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[b]);
+  };
 
-  if (warp < kGradsWork / 32) {
-    float* invU = reinterpret_cast<float*>(smem + L::F);
-    float* invE = invU + kBC;
-    float* part = invE + kBC;         // [4][64] q . dq of each 32 rows d_k
-    float* vd = part + 4 * kBC;       // [64] v . dv
-    float* red = vd + kBC;            // [16] <H', dH'>
-    const int qd = warp & 3, cq = warp >> 2;  // TMEM lanes 32 qd .., 16 columns 16 cq ..
+  if (warp < 8) {
+    setmaxnreg_inc<kRegsRows>();
+    const int qd = warp & 3, ch = warp >> 2;  // TMEM lanes 32 qd .., 32 columns 32 ch ..
     const int dk = 32 * qd + lane;
     const bool on = D == 128 || dk < D;
-    const uint32_t tl = tmem + (uint32_t(32 * qd) << 16) + 16 * cq;
-    // factors, gates and largest values of head h, into the buffer of its parity
+    const uint32_t tl = tmem + (uint32_t(32 * qd) << 16) + 32 * ch;
+    // factors and gates of head h, into the buffer of its parity
     auto load_head = [&](int h) {
       const size_t unit = size_t(i) * a.H_v + h;
       const int p = h & 1;
@@ -1206,82 +1209,60 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       else if (tid >= 128 && tid < 128 + kBC / 2)
         cp_async16(base + L::G + p * kBC * 8 + (tid - 128) * 16,
                    a.G + unit * kBC + (tid - 128) * 2);
-      else if (tid >= 192 && tid < 196)
-        cp_async16(base + L::M + p * 64 + (tid - 192) * 16, a.Hmax + unit * 16 + (tid - 192) * 4);
       cp_async_commit();
     };
-    // u and E of head h, into the place of H's limbs
-    auto load_rows = [&](int h) {
-      const size_t unit = size_t(i) * a.H_v + h;
-      cp_async_block<kGradsWork>(base + L::HL, reinterpret_cast<const uint8_t*>(a.u + unit * kBC * D),
-                                 kBC * D * 4);
-      cp_async_block<kGradsWork>(base + L::HH, reinterpret_cast<const uint8_t*>(a.E + unit * kBC * D),
-                                 kBC * D * 4);
-      cp_async_commit();
-    };
-    // this warp's part of a tile is written: the issuer may use it
-    auto ready = [&](int b) {
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[b]);
-    };
-    float dqs[16] = {}, dks[16] = {};
+    float dqs[32] = {}, dks[32] = {};
     load_head(h0);
-    load_rows(h0);
     for (int h = h0; h < h0 + vpg; ++h) {
       const uint32_t ph = (h - h0) & 1;
       const size_t unit = size_t(i) * a.H_v + h;
       const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (h & 1) * kFac;
       const float2* Gs = reinterpret_cast<const float2*>(smem + L::G) + (h & 1) * kBC;
-      const float* hm = reinterpret_cast<const float*>(smem + L::M) + (h & 1) * 16;
-      const float* H = a.H + (size_t(i + c.seq) * a.H_v + h) * D * D;
-      const float* H1 = H + size_t(a.H_v) * D * D;
-      const float* dH = a.dH + unit * D * D;
-      // Rows 4 w .. 4 w + 3, 8 lanes a row, 4 J columns a lane.
-      const int r = 4 * warp + (lane >> 3), l8 = lane & 7;
-      uint2 vw[J];
-      {
+      // Rows 8 w .. 8 w + 7 in two halves, 8 lanes a row, 4 J columns a lane.
+      const int l8 = lane & 7;
+      float4 u[2][J], e[2][J];
+      uint2 vw[2][J];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int r = 8 * warp + 4 * m + (lane >> 3);
+        const float* up = a.u + (unit * kBC + r) * D + 4 * l8;
+        const float* ep = a.E + (unit * kBC + r) * D + 4 * l8;
         const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + h * D + 4 * l8;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          vw[j] = make_uint2(0u, 0u);
-          if (r < c.rows) vw[j] = *reinterpret_cast<const uint2*>(vp + 32 * j);
+          u[m][j] = *reinterpret_cast<const float4*>(up + 32 * j);
+          e[m][j] = *reinterpret_cast<const float4*>(ep + 32 * j);
+          vw[m][j] = make_uint2(0u, 0u);
+          if (r < c.rows) vw[m][j] = *reinterpret_cast<const uint2*>(vp + 32 * j);
         }
       }
       if (tid < 2) most[tid] = 0;
-      if (tid == 0) {  // to L2: the states, then all of the next head
-        if (h == h0) {
-          prefetch_l2(H, D * D * 4);
-          prefetch_l2(dH, D * D * 4);
-        }
-        prefetch_l2(H1, D * D * 4);
-        if (h + 1 < h0 + vpg) {
-          prefetch_l2(H + D * D, D * D * 4);
-          prefetch_l2(dH + D * D, D * D * 4);
-        }
+      if (tid == 0 && h + 1 < h0 + vpg) {
+        prefetch_l2(a.u + (unit + 1) * kBC * D, kBC * D * 4);
+        prefetch_l2(a.E + (unit + 1) * kBC * D, kBC * D * 4);
       }
-      cp_async_wait<0>();  // the factors, u and E
-      named_sync(1, kGradsWork);
+      cp_async_wait<0>();  // the factors
+      named_sync(1, kGradsRows);
       if (h + 1 < h0 + vpg) load_head(h + 1);
       // dv, dbeta, v . dv, and the f16 tiles of u and E
-      {
-        float u[4 * J], e[4 * J];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const int at = (r * D + 4 * l8 + 32 * j) * 4;
-          *reinterpret_cast<float4*>(u + 4 * j) = *reinterpret_cast<const float4*>(smem + L::HL + at);
-          *reinterpret_cast<float4*>(e + 4 * j) = *reinterpret_cast<const float4*>(smem + L::HH + at);
-        }
+      for (int m = 0; m < 2; ++m) {
+        const int r = 8 * warp + 4 * m + (lane >> 3);
         const float bt = fac[kFbeta + r];
         float db = 0.f, vs = 0.f, mu = 0.f, me = 0.f;
 #pragma unroll
-        for (int x = 0; x < 4 * J; ++x) {
-          const uint32_t w = x & 2 ? vw[x / 4].y : vw[x / 4].x;
-          db = fmaf(e[x], u[x], db);
-          u[x] *= bt, e[x] *= bt;
-          vs = fmaf(__uint_as_float(x & 1 ? w & 0xffff0000u : w << 16), e[x], vs);
-          mu = max_nan(mu, fabsf(u[x])), me = max_nan(me, fabsf(e[x]));
+        for (int j = 0; j < J; ++j) {
+          float4 &x = u[m][j], &y = e[m][j];
+          const uint2 w = vw[m][j];
+          db = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, db))));
+          x.x *= bt, x.y *= bt, x.z *= bt, x.w *= bt;
+          y.x *= bt, y.y *= bt, y.z *= bt, y.w *= bt;
+          vs = fmaf(__uint_as_float(w.x << 16), y.x, vs);
+          vs = fmaf(__uint_as_float(w.x & 0xffff0000u), y.y, vs);
+          vs = fmaf(__uint_as_float(w.y << 16), y.z, vs);
+          vs = fmaf(__uint_as_float(w.y & 0xffff0000u), y.w, vs);
+          mu = max_nan(mu, max_nan(max_nan(fabsf(x.x), fabsf(x.y)), max_nan(fabsf(x.z), fabsf(x.w))));
+          me = max_nan(me, max_nan(max_nan(fabsf(y.x), fabsf(y.y)), max_nan(fabsf(y.z), fabsf(y.w))));
         }
 #pragma unroll
         for (int off = 1; off < 8; off <<= 1) {
@@ -1296,59 +1277,33 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           if (r < c.rows) a.dbeta[size_t(c.row0 + r) * a.H_v + h] = db;
           vd[r] = vs;
           invU[r] = iu, invE[r] = ie;
+          endU[r] = iu * fac[kFend + r];
         }
         uint16_t* dv = a.dv + (size_t(c.row0 + r) * a.H_v + h) * D + 4 * l8;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          const float *up = u + 4 * j, *ep = e + 4 * j;
+          const float4 x = u[m][j], y = e[m][j];
           if (r < c.rows)
             *reinterpret_cast<uint2*>(dv + 32 * j) =
-                make_uint2(pack_bf16x2(ep[0], ep[1]), pack_bf16x2(ep[2], ep[3]));
+                make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
           const int col = 4 * l8 + 32 * j;
-          const uint32_t at = sw128_offset(r, (col & 63) * 2);
-          uint2 uh, ul;
-          split_f16(up[0] * su, up[1] * su, uh.x, ul.x);
-          split_f16(up[2] * su, up[3] * su, uh.y, ul.y);
-          *reinterpret_cast<uint2*>(smem + L::UH + (col >> 6) * kBlk + at) = uh;
-          *reinterpret_cast<uint2*>(smem + L::UL + (col >> 6) * kBlk + at) = ul;
-          *reinterpret_cast<uint2*>(smem + L::OE + (col >> 6) * 2 * kBlk + kBlk + at) =
-              make_uint2(pack_f16(ep[0] * se, ep[1] * se), pack_f16(ep[2] * se, ep[3] * se));
+          const uint32_t at = (col >> 6) * kBlk + sw128_offset(r, (col & 63) * 2);
+          uint32_t p0, p1, q0, q1;
+          split_f16(x.x * su, x.y * su, p0, q0);
+          split_f16(x.z * su, x.w * su, p1, q1);
+          st_shared_v2(base + L::UH + at, p0, p1);
+          st_shared_v2(base + L::UL + at, q0, q1);
+          st_shared_v2(base + L::OE + (col >> 6) * kBlk + kBlk + at, pack_f16(y.x * se, y.y * se),
+                       pack_f16(y.z * se, y.w * se));
         }
       }
       ready(gU);
-      float ih, id, sd;
-      {
-        float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) m0 = max_nan(m0, hm[x]), m1 = max_nan(m1, hm[8 + x]);
-        const float sh = pow2_scale(m0, &ih);
-        sd = pow2_scale(m1, &id);
-        named_sync(1, kGradsWork);  // everybody has read the rows out of these tiles' place
-        state_tile<D, true, 8>(H, sh, base + L::HH, base + L::HL, [](const auto&, int) {});
-      }
-      ready(gH);
-      // dH', and <H', dH'> on the way
-      {
-        float hh = 0.f;
-        state_tile<D, false, 4>(dH, sd, base + L::DH, 0u, [&](const auto& v, int at) {
-          constexpr int B = sizeof(v) / sizeof(v[0]);
-          float4 x[B];
-#pragma unroll
-          for (int m = 0; m < B; ++m)
-            x[m] = *reinterpret_cast<const float4*>(H1 + at + 4 * m * kGradsWork);
-#pragma unroll
-          for (int m = 0; m < B; ++m)
-            hh += fmaf(v[m].x, x[m].x, v[m].y * x[m].y) + fmaf(v[m].z, x[m].z, v[m].w * x[m].w);
-        });
-        hh = warp_sum(hh);
-        if (lane == 0) red[warp] = hh;
-      }
-      ready(gD);
+      named_sync(1, kGradsRows);  // the rows' scales
       // P and N: lanes 0-63 are rows of P, 64-127 of N
-      float x[16], y[16];
+      float x[32];
       mbar_wait(&bars[gPN], ph, abort_flag, err, 64u);
       tc_fence_after();
-      tmem_ld16(tl + kTPN, x);
+      tmem_ld32(tl + kTPN, x);
       tmem_ld_wait();
       float ip, in;
       {
@@ -1357,108 +1312,108 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         const float2 Gr = Gs[pr];
         const float fr = isn ? -invE[pr] : a.scale * fac[kFinvO];
         float m = 0.f;
-        if (pb > cq) {
-          // below the diagonal blocks: the decay in two factors, split at the end of the
-          // column block
-          const float fe = fr * expdiff(Gr, Gs[16 * cq + 15]);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            x[k] *= fe * (fac[kFend + 16 * cq + k] * invU[16 * cq + k]);
-            m = max_nan(m, fabsf(x[k]));
+        for (int cb = 0; cb < 2; ++cb) {  // 16-column blocks
+          // The decay in two factors, e^{G_r - G_b} e^{G_b - G_s}, split at the last row b of
+          // the column block.  In the diagonal blocks the first one is above 1: where the
+          // block decays by 2^60 or more, each element takes an exponential of its own.
+          const int s0 = 32 * ch + 16 * cb, sb = s0 >> 4;
+          const float2 Gb = Gs[s0 + 15];
+          const bool steep = Gs[s0].x - Gb.x > 60.f;
+          const float fe = pb < sb ? 0.f : fr * expdiff(Gr, Gb);
+          const int last = pb > sb ? 16 : pb < sb ? 0 : pr - s0 + (isn ? 0 : 1);
+          if (pb == sb && steep) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              x[16 * cb + k] = k < last
+                  ? x[16 * cb + k] * (expdiff(Gr, Gs[s0 + k]) * invU[s0 + k] * fr) : 0.f;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              const float4 e4 = *reinterpret_cast<const float4*>(endU + s0 + k);
+              float* y = x + 16 * cb + k;
+              y[0] = k < last ? y[0] * (fe * e4.x) : 0.f;
+              y[1] = k + 1 < last ? y[1] * (fe * e4.y) : 0.f;
+              y[2] = k + 2 < last ? y[2] * (fe * e4.z) : 0.f;
+              y[3] = k + 3 < last ? y[3] * (fe * e4.w) : 0.f;
+            }
           }
-        } else if (pb == cq) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int ps = 16 * cq + k;
-            const bool in_ = ps < pr || (ps == pr && !isn);
-            x[k] = in_ ? x[k] * (expdiff(Gr, Gs[ps]) * invU[ps] * fr) : 0.f;
-            m = max_nan(m, fabsf(x[k]));
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = 0.f;
         }
+        m = max_abs_of(x);
         const uint32_t um = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
         if (lane == 0) atomicMax(&most[isn], um);
-        named_sync(1, kGradsWork);
+        named_sync(1, kGradsRows);
         const float sp = pow2_scale(__uint_as_float(most[0]), &ip);
         const float sn = pow2_scale(__uint_as_float(most[1]), &in);
         const float sc = isn ? sn : sp;
-        uint32_t ph_[8], pl_[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) split_f16(x[2 * k] * sc, x[2 * k + 1] * sc, ph_[k], pl_[k]);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t p[4], q[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t at = sw128_offset(pr, 32 * cq + 16 * k);
-          st_shared_v4(base + (isn ? L::N : L::PH) + at, ph_[4 * k], ph_[4 * k + 1],
-                       ph_[4 * k + 2], ph_[4 * k + 3]);
-          if (!isn)
-            st_shared_v4(base + L::PL + at, pl_[4 * k], pl_[4 * k + 1], pl_[4 * k + 2],
-                         pl_[4 * k + 3]);
+          for (int y = 0; y < 4; ++y)
+            split_f16(x[8 * k + 2 * y] * sc, x[8 * k + 2 * y + 1] * sc, p[y], q[y]);
+          const uint32_t at = sw128_offset(pr, 64 * ch + 16 * k);
+          st_shared_v4(base + (isn ? L::N : L::PH) + at, p[0], p[1], p[2], p[3]);
+          if (!isn) st_shared_v4(base + L::PL + at, q[0], q[1], q[2], q[3]);
         }
       }
       ready(gP);
-      // dq and q . dq: row d_k of this thread, 16 chunk rows
+      // dq, q . dq and dk: row d_k of this thread, 2 x 16 chunk rows
       mbar_wait(&bars[gA12], ph, abort_flag, err, 64u);
-      if (h + 1 < h0 + vpg) load_rows(h + 1);
+      mbar_wait(&bars[gA6], ph, abort_flag, err, 64u);
       mbar_wait(&bars[gA345], ph, abort_flag, err, 64u);
       tc_fence_after();
-      tmem_ld16(tl + kTA1, x);
-      tmem_ld16(tl + kTA3, y);
-      tmem_ld_wait();
       {
+        const float ih = red[16 + 2 * (h & 1)], id = red[17 + 2 * (h & 1)];  // the states' scales
         const float f = a.scale * fac[kFinvO] * ih, fp = ip * fac[kFinvK], iq = fac[kFinvQ];
+        const float fq = ip * fac[kFinvQ], fn = in * fac[kFinvK];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int rr = 16 * cq + k;
-          const float d = fmaf(x[k], f * fac[kFeG + rr], y[k] * fp);
-          dqs[k] += d;
-          float q = 0.f;
-          if (on)
-            q = __half2float(*reinterpret_cast<const __half*>(
-                    smem + L::Q + (dk >> 6) * kBlk + sw128_offset(rr, (dk & 63) * 2))) * d;
-          x[k] = q;
-        }
-        // sum over the 32 lanes, the 16 rows spread over them
+        for (int cb = 0; cb < 2; ++cb) {
+          float x0[16], x1[16], x2[16], x3[16];
+          const int s0 = 32 * ch + 16 * cb;
+          tmem_ld16(tl + kTA1 + 16 * cb, x0);
+          tmem_ld16(tl + kTA3 + 16 * cb, x1);
+          tmem_ld_wait();
 #pragma unroll
-        for (int w = 8; w >= 1; w >>= 1) {
-          const bool up = lane & (2 * w);
-#pragma unroll
-          for (int k = 0; k < w; ++k) {
-            const float send = up ? x[k] : x[k + w];
-            x[k] = (up ? x[k + w] : x[k]) + __shfl_xor_sync(0xffffffffu, send, 2 * w);
+          for (int k = 0; k < 16; ++k) {
+            const float d = fmaf(x0[k], f * fac[kFeG + s0 + k], x1[k] * fp);
+            dqs[16 * cb + k] += d;
+            float q = 0.f;
+            if (on)
+              q = __half2float(*reinterpret_cast<const __half*>(
+                      smem + L::Q + (dk >> 6) * kBlk + sw128_offset(s0 + k, (dk & 63) * 2))) * d;
+            x0[k] = q;
           }
-        }
-        x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
-        if ((lane & 1) == 0) part[qd * kBC + 16 * cq + (lane >> 1)] = x[0] * iq;
-      }
-      // dk
-      tmem_ld16(tl + kTA2, x);
-      tmem_ld16(tl + kTA4, y);
-      tmem_ld_wait();
-      {
-        const float fq = ip * fac[kFinvQ];
+          tmem_ld16(tl + kTA2 + 16 * cb, x1);
+          tmem_ld16(tl + kTA4 + 16 * cb, x2);
+          // sum q . dq over the 32 lanes, the 16 rows spread over them
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int rr = 16 * cq + k;
-          dks[k] += fmaf(y[k], fq, x[k] * (-fac[kFeG + rr] * (invE[rr] * ih)));
-        }
-      }
-      mbar_wait(&bars[gA6], ph, abort_flag, err, 64u);
-      tc_fence_after();
-      tmem_ld16(tl + kTA5, x);
-      tmem_ld16(tl + kTA6, y);
-      tmem_ld_wait();
-      {
-        const float fn = in * fac[kFinvK];
+          for (int w = 8; w >= 1; w >>= 1) {
+            const bool up = lane & (2 * w);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int rr = 16 * cq + k;
-          dks[k] += fmaf(x[k], fn, y[k] * (fac[kFeT + rr] * (invU[rr] * id)));
+            for (int k = 0; k < w; ++k) {
+              const float send = up ? x0[k] : x0[k + w];
+              x0[k] = (up ? x0[k + w] : x0[k]) + __shfl_xor_sync(0xffffffffu, send, 2 * w);
+            }
+          }
+          x0[0] += __shfl_xor_sync(0xffffffffu, x0[0], 1);
+          if ((lane & 1) == 0) part[qd * kBC + s0 + (lane >> 1)] = x0[0] * iq;
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            dks[16 * cb + k] +=
+                fmaf(x2[k], fq, x1[k] * (-fac[kFeG + s0 + k] * (invE[s0 + k] * ih)));
+          tmem_ld16(tl + kTA5 + 16 * cb, x2);
+          tmem_ld16(tl + kTA6 + 16 * cb, x3);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            dks[16 * cb + k] +=
+                fmaf(x2[k], fn, x3[k] * (fac[kFeT + s0 + k] * (invU[s0 + k] * id)));
         }
       }
       tc_fence_before();
-      named_sync(1, kGradsWork);  // part and red
+      named_sync(1, kGradsRows);  // part
       // dg: suffix sums over the rows, two per lane, on top of <H', dH'>
       if (warp == 0) {
         double z[2], run;
@@ -1479,7 +1434,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         }
         double hh = 0.0;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) hh += red[w];
+        for (int w = 0; w < kGradsStates / 32; ++w) hh += red[8 * (h & 1) + w];
         z[0] += run - z[1];
         z[1] = run;
 #pragma unroll
@@ -1488,12 +1443,12 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           if (rr < c.rows) a.dg[size_t(c.row0 + rr) * a.H_v + h] = float(z[k] + hh);
         }
       }
-      named_sync(1, kGradsWork);  // the tiles and factors are rewritten for the next head
+      named_sync(1, kGradsRows);  // what was read here is rewritten for the next head
     }
     if (on) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int rr = 16 * cq + k;
+      for (int k = 0; k < 32; ++k) {
+        const int rr = 32 * ch + k;
         if (rr < c.rows) {
           const size_t at = (size_t(c.row0 + rr) * a.H_k + hk) * D + dk;
           a.dq[at] = __bfloat16_as_ushort(__float2bfloat16_rn(dqs[k]));
@@ -1501,9 +1456,74 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         }
       }
     }
+  } else if (warp < 12) {
+    setmaxnreg_dec<kRegsStates>();
+    const int t = tid - kGradsRows;
+    constexpr int kQuads = D * D / 4 / kGradsStates;  // 32 or 8 a thread
+    for (int h = h0; h < h0 + vpg; ++h) {
+      const uint32_t ph = (h - h0) & 1;
+      const size_t unit = size_t(i) * a.H_v + h;
+      const float* H = a.H + (size_t(i + c.seq) * a.H_v + h) * D * D;
+      const float* H1 = H + size_t(a.H_v) * D * D;
+      const float* dH = a.dH + unit * D * D;
+      if (t == 0) {  // to L2: what is read soon, and the next head's states
+        if (h == h0) prefetch_l2(dH, D * D * 4);
+        prefetch_l2(H1, D * D * 4);
+        if (h + 1 < h0 + vpg) {
+          prefetch_l2(H + D * D, D * D * 4);
+          prefetch_l2(dH + D * D, D * D * 4);
+        }
+      }
+      float sh, sd, ih, id;
+      {
+        const float* hm = a.Hmax + unit * 16;
+        const float4 m0 = *reinterpret_cast<const float4*>(hm), m1 = *reinterpret_cast<const float4*>(hm + 4);
+        const float4 n0 = *reinterpret_cast<const float4*>(hm + 8), n1 = *reinterpret_cast<const float4*>(hm + 12);
+        sh = pow2_scale(max_nan(max_nan(max_nan(m0.x, m0.y), max_nan(m0.z, m0.w)),
+                                max_nan(max_nan(m1.x, m1.y), max_nan(m1.z, m1.w))), &ih);
+        sd = pow2_scale(max_nan(max_nan(max_nan(n0.x, n0.y), max_nan(n0.z, n0.w)),
+                                max_nan(max_nan(n1.x, n1.y), max_nan(n1.z, n1.w))), &id);
+      }
+#pragma unroll
+      for (int q = 0; q < kQuads; q += 16) {
+        constexpr int B = kQuads < 16 ? kQuads : 16;
+        float4 v[B];
+#pragma unroll
+        for (int m = 0; m < B; ++m)
+          v[m] = *reinterpret_cast<const float4*>(H + 4 * (t + (q + m) * kGradsStates));
+        if (q == 0) {
+          // Once the last head's H has been multiplied its tiles are free, and so are the
+          // scales of the head before it: the rows' warps have begun the last head.
+          if (h > h0) mbar_wait(&bars[gA12], ph ^ 1, abort_flag, err, 64u);
+          if (t == 0) red[16 + 2 * (h & 1)] = ih, red[17 + 2 * (h & 1)] = id;
+        }
+        quads_to_tile<D, true, B>(v, t + q * kGradsStates, sh, base + L::HH, base + L::HL);
+      }
+      ready(gH);
+      float hh = 0.f;
+#pragma unroll
+      for (int q = 0; q < kQuads; q += 8) {
+        float4 v[8], y[8];
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          v[m] = *reinterpret_cast<const float4*>(dH + 4 * (t + (q + m) * kGradsStates));
+          y[m] = *reinterpret_cast<const float4*>(H1 + 4 * (t + (q + m) * kGradsStates));
+        }
+        if (q == 0 && h > h0) mbar_wait(&bars[gA6], ph ^ 1, abort_flag, err, 64u);
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+          hh += fmaf(v[m].x, y[m].x, v[m].y * y[m].y) + fmaf(v[m].z, y[m].z, v[m].w * y[m].w);
+        quads_to_tile<D, false, 8>(v, t + q * kGradsStates, sd, base + L::DH, 0u);
+      }
+      hh = warp_sum(hh);
+      if (lane == 0) red[8 * (h & 1) + warp - 8] = hh;
+      ready(gD);
+    }
   } else {
-   if (lane == 0) {
-    // The issuer; it also loads K, Q and each head's dO.
+   setmaxnreg_dec<kRegsIssue>();
+   if (warp == 12 && lane == 0) {
+    // The issuer; it also loads K, Q and each head's dO.  (Its loops stay rolled: an
+    // MMA takes longer than its address, and the warp has few registers.)
     const uint64_t kmaj = make_sdesc_sw128(0, 16, 1024);
     const uint64_t mnmaj = make_sdesc_sw128(0, 8192, 1024);
     constexpr uint32_t id64 = make_idesc_f16(128, 64, 0, 0), id128 = make_idesc_f16(128, 128, 0, 0);
@@ -1535,10 +1555,10 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
            mbar_wait(&bars[gU], ph, abort_flag, err, 128u);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int kk = 0; kk < D / 16; ++kk)
         mma_bf16_ss(tmem + kTPN, tall(oe, kk), flat(ul, kk), id64, kk != 0);
-#pragma unroll
+#pragma unroll 1
       for (int kk = 0; kk < D / 16; ++kk)
         mma_bf16_ss(tmem + kTPN, tall(oe, kk), flat(uh, kk), id64, 1u);
       mma_commit(&bars[gPN]);
@@ -1546,38 +1566,38 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       if (!ok) break;
       tc_fence_after();
       // the low limb first, for dO alone; then both, the second half of the columns fresh
-#pragma unroll
+#pragma unroll 1
       for (int kk = 0; kk < D / 16; ++kk)
         mma_bf16_ss(tmem + kTA1, tall(base + L::HL, kk), tall(oe, kk), id64, kk != 0);
       mma_bf16_ss(tmem + kTA1, tall(base + L::HH, 0), tall(oe, 0), id64, 1u);
       mma_bf16_ss(tmem + kTA2, tall(base + L::HH, 0), tall(oe + kBlk, 0), id64, 0u);
-#pragma unroll
+#pragma unroll 1
       for (int kk = 1; kk < D / 16; ++kk)
         mma_bf16_ss(tmem + kTA1, tall(base + L::HH, kk), tall(oe, kk), id128, 1u);
       mma_commit(&bars[gA12]);
       ok = mbar_wait(&bars[gD], ph, abort_flag, err, 128u);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int kk = 0; kk < D / 16; ++kk)
         mma_bf16_ss(tmem + kTA6, tall(base + L::DH, kk), flat(uh, kk), id64, kk != 0);
       mma_commit(&bars[gA6]);
       ok = mbar_wait(&bars[gP], ph, abort_flag, err, 128u);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA3, rows(base + L::K, kk), flat(base + L::PL, kk), id_a, kk != 0);
-#pragma unroll
+#pragma unroll 1
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA3, rows(base + L::K, kk), flat(base + L::PH, kk), id_a, 1u);
-#pragma unroll
+#pragma unroll 1
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA4, rows(base + L::Q, kk), rows(base + L::PH, kk), id_ab, kk != 0);
-#pragma unroll
+#pragma unroll 1
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA5, rows(base + L::K, kk), flat(base + L::N, kk), id_a, kk != 0);
-#pragma unroll
+#pragma unroll 1
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA5, rows(base + L::K, kk), rows(base + L::N, kk), id_ab, 1u);
       mma_commit(&bars[gA345]);
