@@ -1522,10 +1522,13 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   } else {
    setmaxnreg_dec<kRegsIssue>();
    if (warp == 12 && lane == 0) {
-    // The issuer; it also loads K, Q and each head's dO.  (Its loops stay rolled: an
-    // MMA takes longer than its address, and the warp has few registers.)
-    const uint64_t kmaj = make_sdesc_sw128(0, 16, 1024);
-    const uint64_t mnmaj = make_sdesc_sw128(0, 8192, 1024);
+    // The issuer; it also loads K, Q and each head's dO.
+    // Descriptors: the high word is a constant, the low one an address and the (for the
+    // K-major tiles unused) distance of 64-column blocks.
+    const uint32_t b4 = base >> 4;
+    constexpr uint32_t kKmaj = 1u << 16, kMnmaj = (8192u >> 4) << 16;
+    constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+    auto desc = [&](uint32_t low) { return uint64_t(kHigh) << 32 | low; };
     constexpr uint32_t id64 = make_idesc_f16(128, 64, 0, 0), id128 = make_idesc_f16(128, 128, 0, 0);
     constexpr uint32_t id_a = make_idesc_f16(128, 64, 1, 0);   // A MN-major
     constexpr uint32_t id_ab = make_idesc_f16(128, 64, 1, 1);  // both MN-major
@@ -1539,15 +1542,15 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
                   &bars[gO]);
     load_o(h0);
     int loads = 1;
-    const uint32_t oe = base + L::OE, uh = base + L::UH, ul = base + L::UL;
+    constexpr uint32_t oe = L::OE, uh = L::UH, ul = L::UL;
     // descriptors: tall tiles (128 rows a block of 64 columns) and short ones
     auto tall = [&](uint32_t tile, int kk) {
-      return kmaj + ((tile + (kk >> 2) * 2 * kBlk + (kk & 3) * 32) >> 4);
+      return desc(b4 + (kKmaj | (tile + (kk >> 2) * 2 * kBlk + (kk & 3) * 32) >> 4));
     };
     auto flat = [&](uint32_t tile, int kk) {
-      return kmaj + ((tile + (kk >> 2) * kBlk + (kk & 3) * 32) >> 4);
+      return desc(b4 + (kKmaj | (tile + (kk >> 2) * kBlk + (kk & 3) * 32) >> 4));
     };
-    auto rows = [&](uint32_t tile, int kk) { return mnmaj + ((tile + kk * 2048) >> 4); };
+    auto rows = [&](uint32_t tile, int kk) { return desc(b4 + (kMnmaj | (tile + kk * 2048) >> 4)); };
     bool ok = true;
     for (int h = h0; h < h0 + vpg && ok; ++h) {
       const uint32_t ph = (h - h0) & 1;
@@ -1555,10 +1558,10 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
            mbar_wait(&bars[gU], ph, abort_flag, err, 128u);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll 1
+#pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         mma_bf16_ss(tmem + kTPN, tall(oe, kk), flat(ul, kk), id64, kk != 0);
-#pragma unroll 1
+#pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         mma_bf16_ss(tmem + kTPN, tall(oe, kk), flat(uh, kk), id64, 1u);
       mma_commit(&bars[gPN]);
@@ -1566,40 +1569,40 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       if (!ok) break;
       tc_fence_after();
       // the low limb first, for dO alone; then both, the second half of the columns fresh
-#pragma unroll 1
+#pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + kTA1, tall(base + L::HL, kk), tall(oe, kk), id64, kk != 0);
-      mma_bf16_ss(tmem + kTA1, tall(base + L::HH, 0), tall(oe, 0), id64, 1u);
-      mma_bf16_ss(tmem + kTA2, tall(base + L::HH, 0), tall(oe + kBlk, 0), id64, 0u);
-#pragma unroll 1
+        mma_bf16_ss(tmem + kTA1, tall(L::HL, kk), tall(oe, kk), id64, kk != 0);
+      mma_bf16_ss(tmem + kTA1, tall(L::HH, 0), tall(oe, 0), id64, 1u);
+      mma_bf16_ss(tmem + kTA2, tall(L::HH, 0), tall(oe + kBlk, 0), id64, 0u);
+#pragma unroll
       for (int kk = 1; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + kTA1, tall(base + L::HH, kk), tall(oe, kk), id128, 1u);
+        mma_bf16_ss(tmem + kTA1, tall(L::HH, kk), tall(oe, kk), id128, 1u);
       mma_commit(&bars[gA12]);
       ok = mbar_wait(&bars[gD], ph, abort_flag, err, 128u);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll 1
+#pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + kTA6, tall(base + L::DH, kk), flat(uh, kk), id64, kk != 0);
+        mma_bf16_ss(tmem + kTA6, tall(L::DH, kk), flat(uh, kk), id64, kk != 0);
       mma_commit(&bars[gA6]);
       ok = mbar_wait(&bars[gP], ph, abort_flag, err, 128u);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll 1
+#pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA3, rows(base + L::K, kk), flat(base + L::PL, kk), id_a, kk != 0);
-#pragma unroll 1
+        mma_bf16_ss(tmem + kTA3, rows(L::K, kk), flat(L::PL, kk), id_a, kk != 0);
+#pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA3, rows(base + L::K, kk), flat(base + L::PH, kk), id_a, 1u);
-#pragma unroll 1
+        mma_bf16_ss(tmem + kTA3, rows(L::K, kk), flat(L::PH, kk), id_a, 1u);
+#pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA4, rows(base + L::Q, kk), rows(base + L::PH, kk), id_ab, kk != 0);
-#pragma unroll 1
+        mma_bf16_ss(tmem + kTA4, rows(L::Q, kk), rows(L::PH, kk), id_ab, kk != 0);
+#pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA5, rows(base + L::K, kk), flat(base + L::N, kk), id_a, kk != 0);
-#pragma unroll 1
+        mma_bf16_ss(tmem + kTA5, rows(L::K, kk), flat(L::N, kk), id_a, kk != 0);
+#pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA5, rows(base + L::K, kk), rows(base + L::N, kk), id_ab, 1u);
+        mma_bf16_ss(tmem + kTA5, rows(L::K, kk), rows(L::N, kk), id_ab, 1u);
       mma_commit(&bars[gA345]);
       if (h + 1 < h0 + vpg) {  // dO's last reader is done
         ok = mbar_wait(&bars[gA12], ph, abort_flag, err, 128u);
