@@ -188,6 +188,24 @@ __device__ __forceinline__ void cp_async_block(uint32_t dst, const uint8_t* src,
   for (int x = threadIdx.x * 16; x < bytes; x += THREADS * 16) cp_async16(dst + x, src + x);
 }
 
+// Two f32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*reinterpret_cast<uint64_t*>(&d))
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<uint64_t*>(&d))
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -628,7 +646,9 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
 // operands) needed four times the instructions and 6.2 us a chunk.
 // ---------------------------------------------------------------------------
 
-constexpr int kScanThreads = 320;
+constexpr int kScanThreads = 384;
+// Registers after re-allocation: 256 x 208 + 128 x 88 is the launch's 384 x 168.
+constexpr uint32_t kRegsScan = 208, kRegsFeed = 88;
 constexpr int kScanSync = 288;  // the state warps and the issuer
 
 __device__ uint32_t g_err_backward;
@@ -639,7 +659,7 @@ __host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, int a_mn, in
 }
 
 enum { kTX0 = 0, kTX1 = 64, kTH0 = 128, kTH1 = 256, kTA = 384 };  // tensor memory columns
-enum { bKF = 0, bKE = 2, bEF = 4, bQE, bYF, bYE, bSF, bSE, bX, bQ, bS, bH, bDrain, kBars };
+enum { bKF = 0, bKE = 2, bEF = 4, bQE, bYF, bYE, bSF, bSE, bX, bQ, bS, bH, bOut, bDrain, kBars };
 
 template <int D, bool back>
 struct ScanSmem {
@@ -650,7 +670,8 @@ struct ScanSmem {
   static constexpr int Q = Y + kBC * D * (back ? 4 : 2);
   static constexpr int GO = Q + (back ? kTile : 0);  // two limbs, M = 128 rows each
   // The state on its way out: its slices, 64 bytes apart from a multiple of all
-  // banks, so that the two slices of a warp do not collide.
+  // banks, so that the two slices of a warp do not collide.  Then, in the same
+  // place, u or E.
   static constexpr int kSlice = D * 64, kStep = kSlice + 64;
   static constexpr int St = GO + (back ? 2 * kTile + (D == 64 ? kBlk : 0) : 0);
   static constexpr int Fac = St + D / 16 * kStep;  // two buffers
@@ -667,7 +688,10 @@ __device__ __forceinline__ void limbs_to_tmem(const float (&x)[N], float s, uint
                                               uint32_t lo) {
   uint32_t h[N / 2], l[N / 2];
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) split_f16(x[2 * i] * s, x[2 * i + 1] * s, h[i], l[i]);
+  for (int i = 0; i < N / 2; ++i) {
+    const float2 y = mul2(make_float2(x[2 * i], x[2 * i + 1]), both(s));
+    split_f16(y.x, y.y, h[i], l[i]);
+  }
   if constexpr (N == 64) {
     tmem_st32u(hi, h);
     tmem_st32u(lo, l);
@@ -729,8 +753,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
   auto chunk_of = [&](int t) { return c0 + (back ? n - 1 - t : t); };
 
   if (warp < 8) {
+    setmaxnreg_inc<kRegsScan>();
     const int hh = warp >> 2, dv = 32 * (warp & 3) + lane;
-    const bool on = dv < D;
+    const bool on = D == 128 || dv < D;
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);  // this warp's TMEM lanes
     float* inv_h = reinterpret_cast<float*>(smem + L::Inv);        // [2][128] each
     float *inv_x = inv_h + 256, *inv_w = inv_x + 256;
@@ -772,7 +797,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
         limbs_to_tmem(st, s, tl + kTA + NK / 2 * hh, tl + kTA + 64 + NK / 2 * hh);
       }
       tc_fence_before();
-      if (tid == 0) tma_store_wait_read<0>();  // the last state has left its buffer
+      if (tid == 0) tma_store_wait_read<0>();  // the last u has left the state's buffer
       if (!named_all(1, kScanSync, ok)) break;
       {
         stage_state();
@@ -790,34 +815,32 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
         tmem_ld32(tl + kTX0 + 32 * hh, y0);
         tmem_ld32(tl + kTX1 + 32 * hh, y1);
         tmem_ld_wait();
-        const float ik = fac[kFinvK], i0 = inv_h[dv] * ik, i1 = inv_h[128 + dv] * ik;
+        const float ik = back ? fac[kFinvK] : -fac[kFinvK];
+        const float i0 = inv_h[dv] * ik, i1 = inv_h[128 + dv] * ik;
         const float* fr = fac + (back ? kFeT : kFeG) + 32 * hh;
 #pragma unroll
-        for (int r = 0; r < 32; r += 4) {
-          const float4 f4 = *reinterpret_cast<const float4*>(fr + r);
-          const float f[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float kh = fmaf(y0[r + e], i0, y1[r + e] * i1);
-            const int at = (32 * hh + r + e) * D + dv;
-            float v = 0.f;
-            if (back) {
-              if (on) v = reinterpret_cast<const float*>(smem + L::Y)[at];
-              x[r + e] = fmaf(f[e], kh, v);
-            } else {
-              if (on) v = bf16f(reinterpret_cast<const uint16_t*>(smem + L::Y)[at]);
-              x[r + e] = fmaf(-f[e], kh, v);
-            }
-          }
+        for (int r = 0; r < 32; r += 2) {
+          float2 f = *reinterpret_cast<const float2*>(fr + r), v = make_float2(0.f, 0.f);
+          const int at = (32 * hh + r) * D + dv;
+          if (back && on)
+            v = make_float2(reinterpret_cast<const float*>(smem + L::Y)[at],
+                            reinterpret_cast<const float*>(smem + L::Y)[at + D]);
+          if (!back && on)
+            v = make_float2(bf16f(reinterpret_cast<const uint16_t*>(smem + L::Y)[at]),
+                            bf16f(reinterpret_cast<const uint16_t*>(smem + L::Y)[at + D]));
+          const float2 kh = fma2(make_float2(y0[r], y0[r + 1]), both(i0),
+                                 mul2(make_float2(y1[r], y1[r + 1]), both(i1)));
+          const float2 d = fma2(f, kh, v);
+          x[r] = d.x, x[r + 1] = d.y;
         }
       }
       {
         float z[32], inv;
 #pragma unroll
-        for (int r = 0; r < 32; r += 4) {
-          const float4 f4 = *reinterpret_cast<const float4*>(fac + kFbeta + 32 * hh + r);
-          z[r] = x[r] * f4.x, z[r + 1] = x[r + 1] * f4.y;
-          z[r + 2] = x[r + 2] * f4.z, z[r + 3] = x[r + 3] * f4.w;
+        for (int r = 0; r < 32; r += 2) {
+          const float2 d = mul2(make_float2(x[r], x[r + 1]),
+                                *reinterpret_cast<const float2*>(fac + kFbeta + 32 * hh + r));
+          z[r] = d.x, z[r + 1] = d.y;
         }
         const float s = pow2_scale(max_abs_of(z), &inv);
         inv_x[128 * hh + dv] = inv;
@@ -840,7 +863,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
           tmem_ld32(tl + kTH0 + NK * hh + p, y);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) st[p + e] = fmaf(eC, st[p + e], y[e] * f);
+          for (int e = 0; e < 32; e += 2) {
+            const float2 d = fma2(both(eC), make_float2(st[p + e], st[p + e + 1]),
+                                  mul2(make_float2(y[e], y[e + 1]), both(f)));
+            st[p + e] = d.x, st[p + e + 1] = d.y;
+          }
         }
       }
       // 3. u = X - (beta X) S^T, E = Y - (beta Y) S
@@ -854,14 +881,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
         const float is = -fac[kFinvS], i0 = inv_x[dv] * is, i1 = inv_x[128 + dv] * is;
         const float* fr = fac + (back ? kFbG : kFbT) + 32 * hh;
 #pragma unroll
-        for (int r = 0; r < 32; r += 4) {
-          const float4 f4 = *reinterpret_cast<const float4*>(fr + r);
-          const float f[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[r + e] += fmaf(y0[r + e], i0, y1[r + e] * i1);
-            y0[r + e] = x[r + e] * f[e];
-          }
+        for (int r = 0; r < 32; r += 2) {
+          const float2 d = fma2(make_float2(y0[r], y0[r + 1]), both(i0),
+                                fma2(make_float2(y1[r], y1[r + 1]), both(i1),
+                                     make_float2(x[r], x[r + 1])));
+          x[r] = d.x, x[r + 1] = d.y;
+          const float2 w = mul2(d, *reinterpret_cast<const float2*>(fr + r));
+          y0[r] = w.x, y0[r + 1] = w.y;
         }
         float inv;
         const float s = pow2_scale(max_abs_of(y0), &inv);
@@ -872,10 +898,21 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
       const float ik = back ? -fac[kFinvK] : fac[kFinvK];  // (the factors go with K's buffer)
       if (!named_all(1, kScanSync, ok)) break;
       // 4. u or E out, while the product runs; the next state
+      if (tid == 0) {
+        tma_store_wait_read<0>();  // the state has left
+        mbar_arrive(&bars[bOut]);
+      }
+      ok = mbar_wait(&bars[bOut], t & 1, abort_flag, err, 1u) && ok;
       if (on) {
-        float* out = (back ? a.E : a.u) + (unit * kBC + 32 * hh) * D + dv;
+        float* out = reinterpret_cast<float*>(smem + L::St) + 32 * hh * D + dv;
 #pragma unroll
         for (int r = 0; r < 32; ++r) out[r * D] = x[r];
+      }
+      fence_proxy_async_smem();
+      named_sync(2, 256);
+      if (tid == 0) {
+        bulk_store_s2g((back ? a.E : a.u) + unit * kBC * D, smem + L::St, kBC * D * 4);
+        tma_store_commit();
       }
       const float i0 = inv_w[dv] * ik, i1 = inv_w[128 + dv] * ik;
       ok = mbar_wait(&bars[bH], t & 1, abort_flag, err, 2u) && ok;
@@ -887,9 +924,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
         tmem_ld32(tl + kTH1 + NK * hh + p, y1);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float d = fmaf(y0[e], i0, y1[e] * i1);
-          st[p + e] = back ? st[p + e] + d : fmaf(eC, st[p + e], d);
+        for (int e = 0; e < 32; e += 2) {
+          float2 d = make_float2(st[p + e], st[p + e + 1]);
+          if (!back) d = mul2(d, both(eC));
+          d = fma2(make_float2(y0[e], y0[e + 1]), both(i0),
+                   fma2(make_float2(y1[e], y1[e + 1]), both(i1), d));
+          st[p + e] = d.x, st[p + e + 1] = d.y;
         }
       }
     }
@@ -906,7 +946,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
       for (int x = 0; x < NK; ++x) a.dh0[head + size_t(NK * hh + x) * D + dv] = st[x];
     }
     tc_fence_before();
-  } else if (warp == 8) {
+  } else {
+   setmaxnreg_dec<kRegsFeed>();
+   if (warp == 8) {
     // Loads, in the order in which the chain frees their buffers.
     const int seq_lo = max(a.cu[b], 0), seq_hi = min(a.cu[b + 1], a.total_tokens);
     bool ok = true;
@@ -970,7 +1012,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
     if (ts >= 0) mbar_wait(&bars[bSF], ts & 1, nullptr, err, 8u);
     cp_async_wait<0>();
     __syncwarp();
-  } else {
+   } else if (warp == 9) {
     const bool leader = lane == 0;
     const uint64_t kmaj = make_sdesc_sw128(0, 16, 1024);    // K-major operands
     const uint64_t mnmaj = make_sdesc_sw128(0, 8192, 1024);  // MN-major, 64-element blocks apart
@@ -978,16 +1020,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
     constexpr uint32_t id_s = make_idesc_f16(128, 64, 0, back ? 1 : 0);
     constexpr uint32_t id_h = make_idesc_f16(128, D, 0, 1);
     constexpr uint32_t id_q = make_idesc_f16(128, D, 1, 1);
-    bool left = false;
     for (int t = 0; t < n; ++t) {
       const uint32_t k4 = (base + L::K + (t & 1) * L::kTile) >> 4;
       bool ok = true;
       if (leader) ok = mbar_wait(&bars[bKF + (t & 1)], (t >> 1) & 1, abort_flag, err, 16u);
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!named_all(1, kScanSync, ok)) {
-        left = true;
-        break;
-      }
+      if (!named_all(1, kScanSync, ok)) break;
       if (leader) {
         tc_fence_after();
 #pragma unroll
@@ -1019,10 +1057,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
         ok = mbar_wait(&bars[bSF], t & 1, abort_flag, err, 16u) && ok;
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!named_all(1, kScanSync, ok)) {
-        left = true;
-        break;
-      }
+      if (!named_all(1, kScanSync, ok)) break;
       if (leader) {
         tc_fence_after();
         const uint32_t s4 = (base + L::S) >> 4;
@@ -1039,10 +1074,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
         mma_commit(&bars[bSE]);
       }
       __syncwarp();
-      if (!named_all(1, kScanSync, true)) {
-        left = true;
-        break;
-      }
+      if (!named_all(1, kScanSync, true)) break;
       if (leader) {
         tc_fence_after();
 #pragma unroll
@@ -1056,12 +1088,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
       }
       __syncwarp();
     }
-    (void)left;
     if (leader) {  // every MMA this thread issued has completed
       mma_commit(&bars[bDrain]);
       mbar_wait(&bars[bDrain], 0, nullptr, err, 32u);
     }
     __syncwarp();
+   }
   }
   __syncthreads();
   tc_fence_after();
