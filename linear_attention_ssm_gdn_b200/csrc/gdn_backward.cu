@@ -70,8 +70,8 @@ struct BwdArgs {
   float* Y0;           // [chunk][H_v][64][D] scale (Q K^T * D)^T dO
   float* fac;          // [chunk][H_v][kFac]
   float2* G;           // [chunk][H_v][64] cumulative gates / ln 2, high and low part
-  float* u;            // [chunk][H_v][64][D]
-  float* E;            // [chunk][H_v][64][D]
+  float* u;            // [chunk][H_v][D / 32][64][32]
+  float* E;            // [chunk][H_v][D / 32][64][32]
   float* H;            // [chunk + sequence][H_v][D / 16][D][16] entry states, then the final one
   float* dH;           // [chunk][H_v][D / 16][D][16] gradient of the exit state
   float* Hmax;         // [chunk][H_v][2][8] largest |H| and |dH| of each scan warp's part
@@ -659,7 +659,7 @@ __host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N, int a_mn, in
 }
 
 enum { kTX0 = 0, kTX1 = 64, kTH0 = 128, kTH1 = 256, kTA = 384 };  // tensor memory columns
-enum { bKF = 0, bKE = 2, bEF = 4, bQE, bYF, bYE, bSF, bSE, bX, bQ, bS, bH, bOut, bDrain, kBars };
+enum { bKF = 0, bKE = 2, bEF = 4, bQE, bYF, bYE, bSF, bSE, bX, bQ, bS, bH, bDrain, kBars };
 
 template <int D, bool back>
 struct ScanSmem {
@@ -670,11 +670,13 @@ struct ScanSmem {
   static constexpr int Q = Y + kBC * D * (back ? 4 : 2);
   static constexpr int GO = Q + (back ? kTile : 0);  // two limbs, M = 128 rows each
   // The state on its way out: its slices, 64 bytes apart from a multiple of all
-  // banks, so that the two slices of a warp do not collide.  Then, in the same
-  // place, u or E.
-  static constexpr int kSlice = D * 64, kStep = kSlice + 64;
+  // banks, so that the two slices of a warp do not collide.  Every warp sends its own
+  // part, two runs of kRun bytes, and then, from the first one's place, its part of u
+  // or E (4 KB; D = 64 has a place of its own for that).
+  static constexpr int kStep = D * 64 + 64, kRun = D / 2 * 64;
   static constexpr int St = GO + (back ? 2 * kTile + (D == 64 ? kBlk : 0) : 0);
-  static constexpr int Fac = St + D / 16 * kStep;  // two buffers
+  static constexpr int U = St + D / 16 * kStep;
+  static constexpr int Fac = U + (D == 64 ? 8 * 4096 : 0);  // two buffers
   static constexpr int Inv = Fac + 2 * kFac * 4;   // [3][2][128] inverse row scales
   static constexpr int Bars = Inv + 3 * 2 * 128 * 4;
   static constexpr int kUsed = Bars + kBars * 8 + 16 + 1024;  // 1024: alignment of the base
@@ -767,20 +769,25 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
       for (int i = 0; i < NK; ++i)
         st[i] = init != nullptr && on ? init[head + size_t(NK * hh + i) * D + dv] : 0.f;
     }
-    // where (dv, dk = NK hh) is in a state: slice, and place in its rows of 16
-    float* out_st = reinterpret_cast<float*>(smem + L::St + (dv >> 4) * L::kStep) + NK * hh * 16 +
-                    (dv & 15);
-    auto stage_state = [&] {
+    // The warp's part of a state: its lanes' rows of two slices, d_k from NK hh.
+    const int slice = 2 * (warp & 3);
+    uint8_t* run = smem + L::St + slice * L::kStep + hh * L::kRun;
+    float* out_st = reinterpret_cast<float*>(run + (lane >> 4) * L::kStep) + (lane & 15);
+    auto send_state = [&](float* to) {
+      if (lane == 0) tma_store_wait_read<0>();  // what the warp sent last
+      __syncwarp();
       if (on) {
 #pragma unroll
         for (int x = 0; x < NK; ++x) out_st[x * 16] = st[x];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          float* p = to + slice * D * 16 + hh * NK * 16;
+          bulk_store_s2g(p, run, L::kRun);
+          bulk_store_s2g(p + D * 16, run + L::kStep, L::kRun);
+          tma_store_commit();
+        }
       }
-      fence_proxy_async_smem();
-    };
-    auto send_state = [&](float* to) {  // one thread, once every warp has staged its part
-      for (int x = 0; x < D / 16; ++x)
-        bulk_store_s2g(to + x * D * 16, smem + L::St + x * L::kStep, L::kSlice);
-      tma_store_commit();
     };
     bool ok = true;
     int t = 0;
@@ -797,10 +804,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
         limbs_to_tmem(st, s, tl + kTA + NK / 2 * hh, tl + kTA + 64 + NK / 2 * hh);
       }
       tc_fence_before();
-      if (tid == 0) tma_store_wait_read<0>();  // the last u has left the state's buffer
       if (!named_all(1, kScanSync, ok)) break;
       {
-        stage_state();
+        send_state(back ? a.dH + unit * D * D : a.H + (size_t(i + b) * a.H_v + h) * D * D);
         const float wm = warp_max(on ? most : 0.f);
         if (lane == 0) a.Hmax[(unit * 2 + back) * 8 + warp] = wm;
       }
@@ -848,10 +854,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
       }
       tc_fence_before();
       if (!named_all(1, kScanSync, ok)) break;
-      if (tid == 0) {
-        mbar_arrive(&bars[bYE]);
-        send_state(back ? a.dH + unit * D * D : a.H + (size_t(i + b) * a.H_v + h) * D * D);
-      }
+      if (tid == 0) mbar_arrive(&bars[bYE]);
       const float eC = fac[kFeC];
       if constexpr (back) {  // e^{G_C} dH' + (scale e^G dO)^T Q
         ok = mbar_wait(&bars[bQ], t & 1, abort_flag, err, 2u) && ok;
@@ -898,21 +901,20 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
       const float ik = back ? -fac[kFinvK] : fac[kFinvK];  // (the factors go with K's buffer)
       if (!named_all(1, kScanSync, ok)) break;
       // 4. u or E out, while the product runs; the next state
-      if (tid == 0) {
-        tma_store_wait_read<0>();  // the state has left
-        mbar_arrive(&bars[bOut]);
-      }
-      ok = mbar_wait(&bars[bOut], t & 1, abort_flag, err, 1u) && ok;
+      if (lane == 0) tma_store_wait_read<0>();
+      __syncwarp();
       if (on) {
-        float* out = reinterpret_cast<float*>(smem + L::St) + 32 * hh * D + dv;
+        uint8_t* place = D == 128 ? run : smem + L::U + warp * 4096;
+        float* out = reinterpret_cast<float*>(place) + lane;
 #pragma unroll
-        for (int r = 0; r < 32; ++r) out[r * D] = x[r];
-      }
-      fence_proxy_async_smem();
-      named_sync(2, 256);
-      if (tid == 0) {
-        bulk_store_s2g((back ? a.E : a.u) + unit * kBC * D, smem + L::St, kBC * D * 4);
-        tma_store_commit();
+        for (int r = 0; r < 32; ++r) out[r * 32] = x[r];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_store_s2g((back ? a.E : a.u) + unit * kBC * D + (warp & 3) * kBC * 32 + hh * 32 * 32,
+                         place, 4096);
+          tma_store_commit();
+        }
       }
       const float i0 = inv_w[dv] * ik, i1 = inv_w[128 + dv] * ik;
       ok = mbar_wait(&bars[bH], t & 1, abort_flag, err, 2u) && ok;
@@ -933,14 +935,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
         }
       }
     }
-    if constexpr (!back) {  // the final state; the barrier is the state warps' own
-      if (tid == 0) tma_store_wait_read<0>();
-      named_sync(2, 256);
-      stage_state();
-      named_sync(2, 256);
-      if (tid == 0) send_state(a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D);
-    }
-    if (tid == 0) tma_store_wait_all<0>();
+    if constexpr (!back) send_state(a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D);
+    if (lane == 0) tma_store_wait_all<0>();
+    __syncwarp();
     if (back && on && a.dh0 != nullptr) {
 #pragma unroll
       for (int x = 0; x < NK; ++x) a.dh0[head + size_t(NK * hh + x) * D + dv] = st[x];
@@ -1257,13 +1254,13 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int r = 8 * warp + 4 * m + (lane >> 3);
-        const float* up = a.u + (unit * kBC + r) * D + 4 * l8;
-        const float* ep = a.E + (unit * kBC + r) * D + 4 * l8;
+        const float* up = a.u + unit * kBC * D + r * 32 + 4 * l8;
+        const float* ep = a.E + unit * kBC * D + r * 32 + 4 * l8;
         const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + h * D + 4 * l8;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          u[m][j] = *reinterpret_cast<const float4*>(up + 32 * j);
-          e[m][j] = *reinterpret_cast<const float4*>(ep + 32 * j);
+          u[m][j] = *reinterpret_cast<const float4*>(up + kBC * 32 * j);
+          e[m][j] = *reinterpret_cast<const float4*>(ep + kBC * 32 * j);
           vw[m][j] = make_uint2(0u, 0u);
           if (r < c.rows) vw[m][j] = *reinterpret_cast<const uint2*>(vp + 32 * j);
         }
