@@ -63,6 +63,7 @@ struct BwdArgs {
   int32_t* cu_chunks;  // [num_seqs + 1]
   int32_t* chunk_seq;  // [max_chunks]
   int max_chunks;
+  int sms;             // SMs of the device
   uint8_t* KQ;         // [chunk][H_k] f16 tiles of K, then of Q
   uint8_t* O;          // [chunk][H_v] f16 tile of dO
   uint8_t* GO;         // [chunk][H_v] scale e^G dO, high and low tile
@@ -229,7 +230,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // ---------------------------------------------------------------------------
 // Prep: per (chunk, value head), what neither scan's state enters: the f16
-// tiles of K, Q and dO, the gate factors, M and S.
+// tiles of K, Q, dO and e^G dO, the gate factors, Y0 = scale M^T dO and S.
 //
 // K K^T and Q K^T are one pass of MMAs each (exact operands).  With L_b the
 // diagonal 16 x 16 blocks of B diag(beta), S by block rows:
@@ -360,92 +361,33 @@ __device__ __forceinline__ void block_product(float (&acc)[2][4], const float* A
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) {
   using L = PrepSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float2 Gs[kBC];
   __shared__ float bs[kBC], eGs[kBC];
-  __shared__ uint32_t most[6];  // K, Q, dO, M, S, e^G dO
-  const int i = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ uint32_t most[6];  // K, Q; by head: dO, M, S, e^G dO
+  const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
-  const int vpg = a.H_v / a.H_k, hk = h / vpg;
-  const size_t unit = size_t(i) * a.H_v + h;
+  const int vpg = a.H_v / a.H_k, h0 = blockIdx.y * heads, hk = h0 / vpg;
   const uint32_t base = smem_u32(smem);
-  float* fac = a.fac + unit * kFac;
-  uint8_t* kq = h % vpg == 0 ? a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile : nullptr;
-  if (tid < 6) most[tid] = 0;
+  if (tid < 2) most[tid] = 0;
   __syncthreads();
-  TileIn<D> ot;
+  float invk, invq;
   {
     TileIn<D> kt, qt;
     kt.load(a.k + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows, &most[0]);
     qt.load(a.q + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows, &most[1]);
-    ot.load(a.dout + (size_t(c.row0) * a.H_v + h) * D, size_t(a.H_v) * D, c.rows, &most[2]);
-    if (warp == 0) {  // two rows per lane; 64-bit sums
-      double x[2];
-      float bt[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 2 * lane + e;
-        float gv = 0.f;
-        bt[e] = 0.f;
-        if (r < c.rows) {
-          gv = a.g[size_t(c.row0 + r) * a.gb_stride + h];
-          bt[e] = a.beta[size_t(c.row0 + r) * a.gb_stride + h];
-        }
-        x[e] = (gv < kGateFloor ? kGateFloor : gv) * 1.4426950408889634;
-        bs[r] = bt[e];
-      }
-      x[1] += x[0];
-      double run = x[1];
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, run, off);
-        if (lane >= off) run += y;
-      }
-      const double total = __shfl_sync(0xffffffffu, run, 31);
-      x[0] += run - x[1];
-      x[1] = run;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float hi = float(x[e]);
-        const float2 G = make_float2(hi, float(x[e] - double(hi)));
-        Gs[2 * lane + e] = G;
-        a.G[unit * kBC + 2 * lane + e] = G;
-        const double end = __shfl_sync(0xffffffffu, x[1], lane | 7);
-        fac[kFend + 2 * lane + e] = exp2f(float(end - x[e]));
-        const float eG = exp2f(G.x + G.y), eT = exp2f(float(total - x[e]));
-        fac[kFeG + 2 * lane + e] = eG;
-        eGs[2 * lane + e] = a.scale * eG;
-        fac[kFeT + 2 * lane + e] = eT;
-        fac[kFbeta + 2 * lane + e] = bt[e];
-        fac[kFbT + 2 * lane + e] = bt[e] * eT;
-        fac[kFbG + 2 * lane + e] = bt[e] * eG;
-      }
-      if (lane == 0) fac[kFeC] = exp2f(float(total));
-    }
     __syncthreads();
-    float inv;
-    float s = pow2_scale(__uint_as_float(most[0]), &inv);
-    if (tid == 0) fac[kFinvK] = inv;
-    kt.store(s, base + L::K, kq);
-    s = pow2_scale(__uint_as_float(most[1]), &inv);
-    if (tid == 0) fac[kFinvQ] = inv;
-    qt.store(s, base + L::Q, kq != nullptr ? kq + L::kTile : nullptr);
-    s = pow2_scale(__uint_as_float(most[2]), &inv);
-    if (tid == 0) fac[kFinvO] = inv;
-    ot.store(s, 0, a.O + unit * L::kTile);
-    ot.most_scaled(eGs, &most[5]);
+    uint8_t* kq = h0 % vpg == 0 ? a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile : nullptr;
+    kt.store(pow2_scale(__uint_as_float(most[0]), &invk), base + L::K, kq);
+    qt.store(pow2_scale(__uint_as_float(most[1]), &invq), base + L::Q,
+             kq != nullptr ? kq + L::kTile : nullptr);
   }
   __syncthreads();
-  {
-    float inv;
-    const float s = pow2_scale(__uint_as_float(most[5]), &inv);
-    if (tid == 0) fac[kFinvGO] = inv;
-    ot.store_limbs(eGs, s, a.GO + unit * 2 * L::kTile);
-  }
-  // K K^T and Q K^T: warp = 16 rows, every other 16-column block up to the diagonal
+  // K K^T and Q K^T, for all the heads: warp = 16 rows, every other 16-column block up
+  // to the diagonal
   const int rb = warp >> 1, par = warp & 1, g8 = lane >> 2, t2 = 2 * (lane & 3);
   float kk_[4][4] = {}, qk[4][4] = {};
 #pragma unroll
@@ -467,33 +409,84 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
   float* B = reinterpret_cast<float*>(smem + L::B);
   float* S = reinterpret_cast<float*>(smem + L::S);
   float* T = reinterpret_cast<float*>(smem + L::T);
-  float invk, invq;
-  pow2_scale(__uint_as_float(most[0]), &invk);
-  pow2_scale(__uint_as_float(most[1]), &invq);
-  float big = 0.f;
+  for (int h = h0; h < h0 + heads; ++h) {
+  const size_t unit = size_t(i) * a.H_v + h;
+  float* fac = a.fac + unit * kFac;
+  if (tid >= 2 && tid < 6) most[tid] = 0;
+  __syncthreads();  // the last head's (or K and Q's) shared memory is free
+  TileIn<D> ot;
+  ot.load(a.dout + (size_t(c.row0) * a.H_v + h) * D, size_t(a.H_v) * D, c.rows, &most[2]);
+  if (warp == 0) {  // two rows per lane; 64-bit sums
+    double x[2];
+    float bt[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * lane + e;
+      float gv = 0.f;
+      bt[e] = 0.f;
+      if (r < c.rows) {
+        gv = a.g[size_t(c.row0 + r) * a.gb_stride + h];
+        bt[e] = a.beta[size_t(c.row0 + r) * a.gb_stride + h];
+      }
+      x[e] = (gv < kGateFloor ? kGateFloor : gv) * 1.4426950408889634;
+      bs[r] = bt[e];
+    }
+    x[1] += x[0];
+    double run = x[1];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, run, off);
+      if (lane >= off) run += y;
+    }
+    const double total = __shfl_sync(0xffffffffu, run, 31);
+    x[0] += run - x[1];
+    x[1] = run;
+    const double end = __shfl_sync(0xffffffffu, x[1], lane | 7);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float hi = float(x[e]);
+      const float2 G = make_float2(hi, float(x[e] - double(hi)));
+      Gs[2 * lane + e] = G;
+      a.G[unit * kBC + 2 * lane + e] = G;
+      const float eG = exp2f(G.x + G.y), eT = exp2f(float(total - x[e]));
+      fac[kFend + 2 * lane + e] = exp2f(float(end - x[e]));
+      fac[kFeG + 2 * lane + e] = eG;
+      eGs[2 * lane + e] = a.scale * eG;
+      fac[kFeT + 2 * lane + e] = eT;
+      fac[kFbeta + 2 * lane + e] = bt[e];
+      fac[kFbT + 2 * lane + e] = bt[e] * eT;
+      fac[kFbG + 2 * lane + e] = bt[e] * eG;
+    }
+    if (lane == 0) fac[kFeC] = exp2f(float(total));
+  }
+  __syncthreads();
+  float invo;
+  ot.store(pow2_scale(__uint_as_float(most[2]), &invo), base, a.O + unit * L::kTile);
+  ot.most_scaled(eGs, &most[5]);
+  float big = 0.f, m_[4][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int s0 = 32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2;
     if (2 * (j >> 1) + par <= rb) {
+      float b_[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = 16 * rb + g8 + (e >> 1) * 8, s = s0 + (e & 1);
         const float d = s <= r ? expdiff(Gs[r], Gs[s]) * invk : 0.f;
-        kk_[j][e] = s < r ? kk_[j][e] * invk * d : 0.f;
-        qk[j][e] = s <= r ? qk[j][e] * invq * d : 0.f;
-        big = max_nan(big, fabsf(qk[j][e]));
+        b_[e] = s < r ? kk_[j][e] * invk * d : 0.f;
+        m_[j][e] = s <= r ? qk[j][e] * invq * d : 0.f;
+        big = max_nan(big, fabsf(m_[j][e]));
       }
 #pragma unroll
       for (int e = 0; e < 4; e += 2)
         *reinterpret_cast<float2*>(&B[(16 * rb + g8 + (e >> 1) * 8) * kBT + s0]) =
-            make_float2(kk_[j][e], kk_[j][e + 1]);
+            make_float2(b_[e], b_[e + 1]);
     }
   }
   big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
   if (lane == 0) atomicMax(&most[3], __float_as_uint(big));
-  __syncthreads();  // B; the K and Q tiles are free from here
-  float invm, invo;
-  ot.store(pow2_scale(__uint_as_float(most[2]), &invo), base, nullptr);
+  __syncthreads();  // B, the largest values
+  float invm;
   {
     const float sc = pow2_scale(__uint_as_float(most[3]), &invm);
 #pragma unroll
@@ -502,60 +495,39 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           uint32_t hi, lo;
-          split_f16(qk[j][e] * sc, qk[j][e + 1] * sc, hi, lo);
+          split_f16(m_[j][e] * sc, m_[j][e + 1] * sc, hi, lo);
           const uint32_t at = sw128_offset(16 * rb + g8 + (e >> 1) * 8,
                                            (32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2) * 2);
           *reinterpret_cast<uint32_t*>(smem + L::M + at) = hi;
           *reinterpret_cast<uint32_t*>(smem + L::M + kBlk + at) = lo;
         }
+    float invgo;
+    const float sg = pow2_scale(__uint_as_float(most[5]), &invgo);
+    ot.store_limbs(eGs, sg, a.GO + unit * 2 * L::kTile);
+    if (tid == 0)
+      fac[kFinvK] = invk, fac[kFinvQ] = invq, fac[kFinvO] = invo, fac[kFinvGO] = invgo;
   }
-  // The inverses of I + L_b: thread = (block, column), forward substitution
-  if (tid < kBC) {
-    const int b = tid >> 4, j = tid & 15;
-    float x[16];
+  __syncthreads();  // M and dO
+  if (warp < 4) {
+    // The inverses of I + L_b: thread = (block, column), forward substitution
+    if (tid < kBC) {
+      const int b = tid >> 4, j = tid & 15;
+      float x[16];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      float y = r == j ? 1.f : 0.f;
+      for (int r = 0; r < 16; ++r) {
+        float y = r == j ? 1.f : 0.f;
 #pragma unroll
-      for (int q = 0; q < r; ++q)
-        y = fmaf(-B[(16 * b + r) * kBT + 16 * b + q], x[q], y);
-      T[(b * 16 + r) * 20 + j] = y;
-      x[r] = y * bs[16 * b + r];  // L_b's columns carry beta
-    }
-  }
-  __syncthreads();
-  // Y0 = scale M^T dO: warp = 16 rows s, half of the columns; k-steps from the diagonal
-  {
-    const int mt = warp & 3, c0 = (warp >> 2) * (D / 2);
-    float y[D / 16][4] = {};
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-      if (kk >= mt) {
-        uint32_t ah[4], al[4];
-        ldsm4t(ah, piece<true>(base + L::M, 16 * kk, 16 * mt));
-        ldsm4t(al, piece<true>(base + L::M + kBlk, 16 * kk, 16 * mt));
-#pragma unroll
-        for (int np = 0; np < D / 32; ++np) {
-          uint32_t bv[4];
-          ldsm4t(bv, piece<false>(base, 16 * kk, c0 + 16 * np));
-          mma16(y[2 * np], al, bv[0], bv[1]);
-          mma16(y[2 * np + 1], al, bv[2], bv[3]);
-          mma16(y[2 * np], ah, bv[0], bv[1]);
-          mma16(y[2 * np + 1], ah, bv[2], bv[3]);
-        }
+        for (int q = 0; q < r; ++q)
+          y = fmaf(-B[(16 * b + r) * kBT + 16 * b + q], x[q], y);
+        T[(b * 16 + r) * 20 + j] = y;
+        x[r] = y * bs[16 * b + r];  // L_b's columns carry beta
       }
-    const float f = a.scale * invm * invo;
-    float* out = a.Y0 + (unit * kBC + 16 * mt + g8) * D + c0 + t2;
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; e += 2)
-        *reinterpret_cast<float2*>(out + (e >> 1) * 8 * D + 8 * n) =
-            make_float2(y[n][e] * f, y[n][e + 1] * f);
-  }
-  for (int b = 0; b < 4; ++b) {
-    if (warp <= b) {  // block (b, j = warp)
-      const int j = warp;
+    }
+    named_sync(1, 128);
+    // Block column j = warp of S, from its diagonal block down: nothing of another
+    // column enters it
+    const int j = warp;
+    for (int b = j; b < 4; ++b) {
       float acc[2][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
@@ -586,8 +558,39 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
         }
       }
     }
-    __syncthreads();
+  } else {
+    // Meanwhile Y0 = scale M^T dO: warp = 16 rows s; k-steps from the diagonal
+    const int mt = warp & 3;
+    const float f = a.scale * invm * invo;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+      float y[4][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        if (kk >= mt) {
+          uint32_t ah[4], al[4];
+          ldsm4t(ah, piece<true>(base + L::M, 16 * kk, 16 * mt));
+          ldsm4t(al, piece<true>(base + L::M + kBlk, 16 * kk, 16 * mt));
+#pragma unroll
+          for (int np = 0; np < 2; ++np) {
+            uint32_t bv[4];
+            ldsm4t(bv, piece<false>(base, 16 * kk, c0 + 16 * np));
+            mma16(y[2 * np], al, bv[0], bv[1]);
+            mma16(y[2 * np + 1], al, bv[2], bv[3]);
+            mma16(y[2 * np], ah, bv[0], bv[1]);
+            mma16(y[2 * np + 1], ah, bv[2], bv[3]);
+          }
+        }
+      float* out = a.Y0 + (unit * kBC + 16 * mt + g8) * D + c0 + t2;
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+          *reinterpret_cast<float2*>(out + (e >> 1) * 8 * D + 8 * n) =
+              make_float2(y[n][e] * f, y[n][e + 1] * f);
+    }
   }
+  __syncthreads();
   // S as limbs: warp = 16 rows, half of the columns; zeros above the diagonal blocks
   float2 sv[8];
   big = 0.f;
@@ -619,6 +622,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a) {
   uint4* out = reinterpret_cast<uint4*>(a.S + unit * 2 * kBlk);
 #pragma unroll
   for (int x = tid; x < 2 * kBlk / 16; x += 256) out[x] = reinterpret_cast<const uint4*>(smem)[x];
+  }  // heads
 }
 
 // ---------------------------------------------------------------------------
@@ -1698,7 +1702,11 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D, false>, kMax, fwd)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D, true>, kMax, back)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(bwd_grads_kernel<D>, kMax, grads)) != cudaSuccess) return e;
-  bwd_prep_kernel<D><<<dim3(a.max_chunks, a.H_v), 256, prep, s>>>(a);
+  // The value heads that share a key head in one CTA (their K K^T and Q K^T are made
+  // once), unless that leaves SMs without a CTA: then every head has its own.
+  const int vpg = a.H_v / a.H_k;
+  const int heads = (long long)a.max_chunks * a.H_k >= 2 * a.sms ? vpg : 1;
+  bwd_prep_kernel<D><<<dim3(a.max_chunks, a.H_v / heads), 256, prep, s>>>(a, heads);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const unsigned scans = unsigned(a.num_seqs) * a.H_v;
   bwd_scan_kernel<D, true><<<scans, kScanThreads, back, s>>>(a);
@@ -1736,6 +1744,7 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t s) {
   a.h0 = c.h0, a.dhT = c.dhT;
   a.dq = c.dq, a.dk = c.dk, a.dv = c.dv, a.dg = c.dg, a.dbeta = c.dbeta, a.dh0 = c.dh0;
   a.scale = c.scale;
+  a.sms = sm_count();
   TablesCall t = {};
   t.cu_in = c.cu_seqlens;
   t.num_seqs = c.num_seqs;
