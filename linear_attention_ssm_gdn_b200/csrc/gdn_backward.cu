@@ -241,26 +241,29 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // ---------------------------------------------------------------------------
 
 // 64 x D bf16 rows (row stride in elements) as an f16 tile: loads, finds the
-// largest value of the tile (into *most, a shared word that was zero) ...
+// largest value of the tile (into *most, a shared word that was zero), ...
 template <int D>
 struct TileIn {
   uint4 x[D / 32];
-  __device__ __forceinline__ void load(const uint16_t* src, size_t stride, int rows,
-                                       uint32_t* most) {
-    uint32_t m = 0;
+  __device__ __forceinline__ void fetch(const uint16_t* src, size_t stride, int rows) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const int p = threadIdx.x + 256 * i, r = p / (D / 8), c = p % (D / 8);
       x[i] = make_uint4(0, 0, 0, 0);
       if (r < rows) x[i] = *reinterpret_cast<const uint4*>(src + size_t(r) * stride + 8 * c);
+    }
+  }
+  __device__ __forceinline__ void largest(uint32_t* most) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
       m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
                                __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
-    }
     m = max(m >> 16, m & 0xffffu);
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) atomicMax(most, m << 16);
   }
-  // ... and stores the scaled tile to shared (0: not) and global memory (NULL: not).
+  // and stores the scaled tile to shared (0: not) and global memory (NULL: not).
   __device__ __forceinline__ void store(float s, uint32_t tile, uint8_t* out) const {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -276,21 +279,7 @@ struct TileIn {
       if (out != nullptr) *reinterpret_cast<uint4*>(out + at) = make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
-  // The largest |f[row] x| of the tile, and f[row] x as two limb tiles.
-  __device__ __forceinline__ void most_scaled(const float* f, uint32_t* most) const {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const float fr = f[(threadIdx.x + 256 * i) / (D / 8)];
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        m = max_nan(m, max_nan(fabsf(__uint_as_float(w[j] << 16) * fr),
-                               fabsf(__uint_as_float(w[j] & 0xffff0000u) * fr)));
-    }
-    const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    if ((threadIdx.x & 31) == 0) atomicMax(most, u);
-  }
+  // f[row] x as two limb tiles.
   __device__ __forceinline__ void store_limbs(const float* f, float s, uint8_t* out) const {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -336,10 +325,12 @@ __device__ __forceinline__ void mma8_tf32(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // acc (16 x 16, two tiles) += A (16 x 16, row length la) diag(f) B (16 x 16, row length kBT),
-// with `negate` minus it; f may be NULL (ones).
+// with `negate` minus it; f may be NULL (ones).  The low limbs' products have sums of
+// their own: two short chains instead of a long one.
 __device__ __forceinline__ void block_product(float (&acc)[2][4], const float* A, int la,
                                               const float* f, const float* Bm, bool negate) {
   const int lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
+  float low[2][4] = {};
 #pragma unroll
   for (int k0 = 0; k0 < 16; k0 += 8) {
     float x[4] = {A[g8 * la + k0 + t], A[(g8 + 8) * la + k0 + t], A[g8 * la + k0 + t + 4],
@@ -353,10 +344,75 @@ __device__ __forceinline__ void block_product(float (&acc)[2][4], const float* A
       uint32_t h0, l0, h1, l1;
       split_tf32(Bm[(k0 + t) * kBT + 8 * n + g8], h0, l0);
       split_tf32(Bm[(k0 + t + 4) * kBT + 8 * n + g8], h1, l1);
-      mma8_tf32(acc[n], al, h0, h1);
-      mma8_tf32(acc[n], ah, l0, l1);
+      mma8_tf32(low[n], al, h0, h1);
       mma8_tf32(acc[n], ah, h0, h1);
+      mma8_tf32(low[n], ah, l0, l1);
     }
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] += low[n][e];
+}
+
+// The gates of head h: 64-bit sums, two rows per lane of one warp, into shared memory
+// (gs: largest scale e^G) and the unit's factors.
+struct GateRows {
+  float2 G[kBC];
+  float beta[kBC], eG[kBC];  // eG: scale e^G
+  float most;                // the largest |scale e^G|
+};
+__device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c, size_t unit, int h,
+                                           GateRows* s) {
+  const int lane = threadIdx.x & 31;
+  float* fac = a.fac + unit * kFac;
+  double x[2];
+  float bt[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = 2 * lane + e;
+    float gv = 0.f;
+    bt[e] = 0.f;
+    if (r < c.rows) {
+      gv = a.g[size_t(c.row0 + r) * a.gb_stride + h];
+      bt[e] = a.beta[size_t(c.row0 + r) * a.gb_stride + h];
+    }
+    x[e] = (gv < kGateFloor ? kGateFloor : gv) * 1.4426950408889634;
+    s->beta[r] = bt[e];
+  }
+  x[1] += x[0];
+  double run = x[1];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, run, off);
+    if (lane >= off) run += y;
+  }
+  const double total = __shfl_sync(0xffffffffu, run, 31);
+  x[0] += run - x[1];
+  x[1] = run;
+  const double end = __shfl_sync(0xffffffffu, x[1], lane | 7);
+  float most = 0.f;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = 2 * lane + e;
+    const float hi = float(x[e]);
+    const float2 G = make_float2(hi, float(x[e] - double(hi)));
+    s->G[r] = G;
+    a.G[unit * kBC + r] = G;
+    const float eG = exp2f(G.x + G.y), eT = exp2f(float(total - x[e]));
+    s->eG[r] = a.scale * eG;
+    most = max_nan(most, fabsf(a.scale * eG));
+    fac[kFend + r] = exp2f(float(end - x[e]));
+    fac[kFeG + r] = eG;
+    fac[kFeT + r] = eT;
+    fac[kFbeta + r] = bt[e];
+    fac[kFbT + r] = bt[e] * eT;
+    fac[kFbG + r] = bt[e] * eG;
+  }
+  most = warp_max(most);
+  if (lane == 0) {
+    fac[kFeC] = exp2f(float(total));
+    s->most = most;
   }
 }
 
@@ -364,21 +420,27 @@ template <int D>
 __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) {
   using L = PrepSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ float2 Gs[kBC];
-  __shared__ float bs[kBC], eGs[kBC];
-  __shared__ uint32_t most[6];  // K, Q; by head: dO, M, S, e^G dO
+  __shared__ GateRows gates[2];  // by the head's parity
+  __shared__ uint32_t most[5];   // K, Q; by head: dO, M, S
   const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
   const int vpg = a.H_v / a.H_k, h0 = blockIdx.y * heads, hk = h0 / vpg;
   const uint32_t base = smem_u32(smem);
+  const size_t unit0 = size_t(i) * a.H_v;
+  auto dout = [&](int h) { return a.dout + (size_t(c.row0) * a.H_v + h) * D; };
   if (tid < 2) most[tid] = 0;
   __syncthreads();
   float invk, invq;
+  TileIn<D> ot;
   {
     TileIn<D> kt, qt;
-    kt.load(a.k + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows, &most[0]);
-    qt.load(a.q + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows, &most[1]);
+    kt.fetch(a.k + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows);
+    qt.fetch(a.q + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows);
+    ot.fetch(dout(h0), size_t(a.H_v) * D, c.rows);
+    if (warp == 7) make_gates(a, c, unit0 + h0, h0, &gates[h0 & 1]);
+    kt.largest(&most[0]);
+    qt.largest(&most[1]);
     __syncthreads();
     uint8_t* kq = h0 % vpg == 0 ? a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile : nullptr;
     kt.store(pow2_scale(__uint_as_float(most[0]), &invk), base + L::K, kq);
@@ -406,141 +468,134 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
         mma16(qk[2 * j + 1], aq, bv[2], bv[3]);
       }
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) kk_[j][e] *= invk * invk, qk[j][e] *= invk * invq;
   float* B = reinterpret_cast<float*>(smem + L::B);
   float* S = reinterpret_cast<float*>(smem + L::S);
   float* T = reinterpret_cast<float*>(smem + L::T);
   for (int h = h0; h < h0 + heads; ++h) {
-  const size_t unit = size_t(i) * a.H_v + h;
-  float* fac = a.fac + unit * kFac;
-  if (tid >= 2 && tid < 6) most[tid] = 0;
-  __syncthreads();  // the last head's (or K and Q's) shared memory is free
-  TileIn<D> ot;
-  ot.load(a.dout + (size_t(c.row0) * a.H_v + h) * D, size_t(a.H_v) * D, c.rows, &most[2]);
-  if (warp == 0) {  // two rows per lane; 64-bit sums
-    double x[2];
-    float bt[2];
+    const size_t unit = unit0 + h;
+    const GateRows& gr = gates[h & 1];
+    const float* bs = gr.beta;
+    if (tid >= 2 && tid < 5) most[tid] = 0;
+    if (tid == 0) tma_store_wait_read<0>();  // the last head's S has left
+    __syncthreads();  // the last head's (or K and Q's) shared memory is free
+    // B and M
+    ot.largest(&most[2]);
+    float big = 0.f, m_[4][4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 2 * lane + e;
-      float gv = 0.f;
-      bt[e] = 0.f;
-      if (r < c.rows) {
-        gv = a.g[size_t(c.row0 + r) * a.gb_stride + h];
-        bt[e] = a.beta[size_t(c.row0 + r) * a.gb_stride + h];
-      }
-      x[e] = (gv < kGateFloor ? kGateFloor : gv) * 1.4426950408889634;
-      bs[r] = bt[e];
-    }
-    x[1] += x[0];
-    double run = x[1];
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, run, off);
-      if (lane >= off) run += y;
-    }
-    const double total = __shfl_sync(0xffffffffu, run, 31);
-    x[0] += run - x[1];
-    x[1] = run;
-    const double end = __shfl_sync(0xffffffffu, x[1], lane | 7);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float hi = float(x[e]);
-      const float2 G = make_float2(hi, float(x[e] - double(hi)));
-      Gs[2 * lane + e] = G;
-      a.G[unit * kBC + 2 * lane + e] = G;
-      const float eG = exp2f(G.x + G.y), eT = exp2f(float(total - x[e]));
-      fac[kFend + 2 * lane + e] = exp2f(float(end - x[e]));
-      fac[kFeG + 2 * lane + e] = eG;
-      eGs[2 * lane + e] = a.scale * eG;
-      fac[kFeT + 2 * lane + e] = eT;
-      fac[kFbeta + 2 * lane + e] = bt[e];
-      fac[kFbT + 2 * lane + e] = bt[e] * eT;
-      fac[kFbG + 2 * lane + e] = bt[e] * eG;
-    }
-    if (lane == 0) fac[kFeC] = exp2f(float(total));
-  }
-  __syncthreads();
-  float invo;
-  ot.store(pow2_scale(__uint_as_float(most[2]), &invo), base, a.O + unit * L::kTile);
-  ot.most_scaled(eGs, &most[5]);
-  float big = 0.f, m_[4][4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int s0 = 32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2;
-    if (2 * (j >> 1) + par <= rb) {
-      float b_[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 16 * rb + g8 + (e >> 1) * 8, s = s0 + (e & 1);
-        const float d = s <= r ? expdiff(Gs[r], Gs[s]) * invk : 0.f;
-        b_[e] = s < r ? kk_[j][e] * invk * d : 0.f;
-        m_[j][e] = s <= r ? qk[j][e] * invq * d : 0.f;
-        big = max_nan(big, fabsf(m_[j][e]));
-      }
-#pragma unroll
-      for (int e = 0; e < 4; e += 2)
-        *reinterpret_cast<float2*>(&B[(16 * rb + g8 + (e >> 1) * 8) * kBT + s0]) =
-            make_float2(b_[e], b_[e + 1]);
-    }
-  }
-  big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-  if (lane == 0) atomicMax(&most[3], __float_as_uint(big));
-  __syncthreads();  // B, the largest values
-  float invm;
-  {
-    const float sc = pow2_scale(__uint_as_float(most[3]), &invm);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (2 * (j >> 1) + par <= rb)
+    for (int j = 0; j < 4; ++j) {
+      const int s0 = 32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2;
+      if (2 * (j >> 1) + par <= rb) {
+        const float2 G0 = gr.G[s0], G1 = gr.G[s0 + 1];
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-          uint32_t hi, lo;
-          split_f16(m_[j][e] * sc, m_[j][e + 1] * sc, hi, lo);
-          const uint32_t at = sw128_offset(16 * rb + g8 + (e >> 1) * 8,
-                                           (32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2) * 2);
-          *reinterpret_cast<uint32_t*>(smem + L::M + at) = hi;
-          *reinterpret_cast<uint32_t*>(smem + L::M + kBlk + at) = lo;
+          const int r = 16 * rb + g8 + (e >> 1) * 8;
+          const float2 Gr = gr.G[r];
+          const float d0 = s0 <= r ? expdiff(Gr, G0) : 0.f;
+          const float d1 = s0 + 1 <= r ? expdiff(Gr, G1) : 0.f;
+          *reinterpret_cast<float2*>(&B[r * kBT + s0]) =
+              make_float2(s0 < r ? kk_[j][e] * d0 : 0.f, s0 + 1 < r ? kk_[j][e + 1] * d1 : 0.f);
+          m_[j][e] = s0 <= r ? qk[j][e] * d0 : 0.f;
+          m_[j][e + 1] = s0 + 1 <= r ? qk[j][e + 1] * d1 : 0.f;
+          big = max_nan(big, max_nan(fabsf(m_[j][e]), fabsf(m_[j][e + 1])));
         }
-    float invgo;
-    const float sg = pow2_scale(__uint_as_float(most[5]), &invgo);
-    ot.store_limbs(eGs, sg, a.GO + unit * 2 * L::kTile);
-    if (tid == 0)
-      fac[kFinvK] = invk, fac[kFinvQ] = invq, fac[kFinvO] = invo, fac[kFinvGO] = invgo;
-  }
-  __syncthreads();  // M and dO
-  if (warp < 4) {
-    // The inverses of I + L_b: thread = (block, column), forward substitution
-    if (tid < kBC) {
-      const int b = tid >> 4, j = tid & 15;
-      float x[16];
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float y = r == j ? 1.f : 0.f;
-#pragma unroll
-        for (int q = 0; q < r; ++q)
-          y = fmaf(-B[(16 * b + r) * kBT + 16 * b + q], x[q], y);
-        T[(b * 16 + r) * 20 + j] = y;
-        x[r] = y * bs[16 * b + r];  // L_b's columns carry beta
       }
     }
-    named_sync(1, 128);
-    // Block column j = warp of S, from its diagonal block down: nothing of another
-    // column enters it
-    const int j = warp;
-    for (int b = j; b < 4; ++b) {
-      float acc[2][4];
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    if (lane == 0) atomicMax(&most[3], __float_as_uint(big));
+    __syncthreads();  // B, the largest values
+    // M, dO and scale e^G dO as tiles
+    float invm, invo;
+    {
+      const float sc = pow2_scale(__uint_as_float(most[3]), &invm);
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int j = 0; j < 4; ++j)
+        if (2 * (j >> 1) + par <= rb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[n][e] = B[(16 * b + g8 + (e >> 1) * 8) * kBT + 16 * j + 8 * n + t2 + (e & 1)];
-      for (int cc = j; cc < b; ++cc)
-        block_product(acc, B + 16 * b * kBT + 16 * cc, kBT, bs + 16 * cc,
-                      S + 16 * cc * kBT + 16 * j, true);
-      // the right-hand side, then (I + L_b)^-1 times it, both in this block's place
-      float* out = S + 16 * b * kBT + 16 * j;
+          for (int e = 0; e < 4; e += 2) {
+            uint32_t hi, lo;
+            split_f16(m_[j][e] * sc, m_[j][e + 1] * sc, hi, lo);
+            const uint32_t at = sw128_offset(16 * rb + g8 + (e >> 1) * 8,
+                                             (32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2) * 2);
+            *reinterpret_cast<uint32_t*>(smem + L::M + at) = hi;
+            *reinterpret_cast<uint32_t*>(smem + L::M + kBlk + at) = lo;
+          }
+      ot.store(pow2_scale(__uint_as_float(most[2]), &invo), base, a.O + unit * L::kTile);
+      // (scaled for the product of the largest dO and the largest scale e^G)
+      float invgo;
+      const float sg = pow2_scale(__uint_as_float(most[2]) * gr.most, &invgo);
+      ot.store_limbs(gr.eG, sg, a.GO + unit * 2 * L::kTile);
+      if (tid == 0) {
+        float* fac = a.fac + unit * kFac;
+        fac[kFinvK] = invk, fac[kFinvQ] = invq, fac[kFinvO] = invo, fac[kFinvGO] = invgo;
+      }
+    }
+    __syncthreads();  // M and dO
+    if (h + 1 < h0 + heads) ot.fetch(dout(h + 1), size_t(a.H_v) * D, c.rows);
+    if (warp < 4) {
+      // The inverses of I + L_b: thread = (block, column), forward substitution
+      if (tid < kBC) {
+        const int b = tid >> 4, j = tid & 15;
+        float x[16];
 #pragma unroll
-      for (int round = 0; round < 2; ++round) {
+        for (int r = 0; r < 16; ++r) {
+          const float* row = B + (16 * b + r) * kBT + 16 * b;
+          float y0 = r == j ? 1.f : 0.f, y1 = 0.f;
+#pragma unroll
+          for (int q = 0; q < r; q += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(row + q);
+            y0 = fmaf(-w.x, x[q], y0);
+            if (q + 1 < r) y1 = fmaf(-w.y, x[q + 1], y1);
+            if (q + 2 < r) y0 = fmaf(-w.z, x[q + 2], y0);
+            if (q + 3 < r) y1 = fmaf(-w.w, x[q + 3], y1);
+          }
+          y0 += y1;
+          T[(b * 16 + r) * 20 + j] = y0;
+          x[r] = y0 * bs[16 * b + r];  // L_b's columns carry beta
+        }
+      }
+      named_sync(1, 128);
+      // (I + L_b)^-1 B_bj in B's place: warp = block row b and, for the short rows, some
+      // of the long ones' blocks
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        // warp 0: (0,0) (3,0) (2,0); 1: (1,0) (1,1) (3,1); 2: (2,1) (2,2); 3: (3,2) (3,3)
+        const int code = warp == 0 ? 0x20'30'00 >> (8 * m) : warp == 1 ? 0x31'11'10 >> (8 * m)
+                         : warp == 2 ? 0xff'22'21 >> (8 * m) : 0xff'33'32 >> (8 * m);
+        const int b = (code >> 4) & 15, j = code & 15;
+        if (b > 3) break;
+        float* at = B + 16 * b * kBT + 16 * j;
+        float acc[2][4] = {};
+        block_product(acc, T + b * 16 * 20, 20, nullptr, at, false);
+        __syncwarp();
+        float* s_at = S + 16 * b * kBT + 16 * j;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const int o = (g8 + (e >> 1) * 8) * kBT + 8 * n + t2;
+            const float2 v = make_float2(acc[n][e], acc[n][e + 1]);
+            *reinterpret_cast<float2*>(&at[o]) = v;
+            if (b == j) *reinterpret_cast<float2*>(&s_at[o]) = v;  // S's diagonal blocks
+          }
+      }
+      named_sync(1, 128);
+      // Block column j = warp of S, downwards: nothing of another column enters it
+      const int j = warp;
+      for (int b = j + 1; b < 4; ++b) {
+        float acc[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[n][e] = B[(16 * b + g8 + (e >> 1) * 8) * kBT + 16 * j + 8 * n + t2 + (e & 1)];
+        for (int cc = j; cc < b; ++cc)
+          block_product(acc, B + 16 * b * kBT + 16 * cc, kBT, bs + 16 * cc,
+                        S + 16 * cc * kBT + 16 * j, true);
+        float* out = S + 16 * b * kBT + 16 * j;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -548,81 +603,76 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
             *reinterpret_cast<float2*>(&out[(g8 + (e >> 1) * 8) * kBT + 8 * n + t2]) =
                 make_float2(acc[n][e], acc[n][e + 1]);
         __syncwarp();
-        if (round == 0) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-          block_product(acc, T + b * 16 * 20, 20, nullptr, out, false);
-          __syncwarp();
-        }
       }
-    }
-  } else {
-    // Meanwhile Y0 = scale M^T dO: warp = 16 rows s; k-steps from the diagonal
-    const int mt = warp & 3;
-    const float f = a.scale * invm * invo;
+    } else {
+      // Meanwhile Y0 = scale M^T dO: warp = 16 rows s; k-steps from the diagonal
+      const int mt = warp & 3;
+      const float f = a.scale * invm * invo;
 #pragma unroll 1
-    for (int c0 = 0; c0 < D; c0 += 32) {
-      float y[4][4] = {};
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        float y[4][4] = {};
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        if (kk >= mt) {
-          uint32_t ah[4], al[4];
-          ldsm4t(ah, piece<true>(base + L::M, 16 * kk, 16 * mt));
-          ldsm4t(al, piece<true>(base + L::M + kBlk, 16 * kk, 16 * mt));
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk >= mt) {
+            uint32_t ah[4], al[4];
+            ldsm4t(ah, piece<true>(base + L::M, 16 * kk, 16 * mt));
+            ldsm4t(al, piece<true>(base + L::M + kBlk, 16 * kk, 16 * mt));
 #pragma unroll
-          for (int np = 0; np < 2; ++np) {
-            uint32_t bv[4];
-            ldsm4t(bv, piece<false>(base, 16 * kk, c0 + 16 * np));
-            mma16(y[2 * np], al, bv[0], bv[1]);
-            mma16(y[2 * np + 1], al, bv[2], bv[3]);
-            mma16(y[2 * np], ah, bv[0], bv[1]);
-            mma16(y[2 * np + 1], ah, bv[2], bv[3]);
+            for (int np = 0; np < 2; ++np) {
+              uint32_t bv[4];
+              ldsm4t(bv, piece<false>(base, 16 * kk, c0 + 16 * np));
+              mma16(y[2 * np], al, bv[0], bv[1]);
+              mma16(y[2 * np + 1], al, bv[2], bv[3]);
+              mma16(y[2 * np], ah, bv[0], bv[1]);
+              mma16(y[2 * np + 1], ah, bv[2], bv[3]);
+            }
           }
-        }
-      float* out = a.Y0 + (unit * kBC + 16 * mt + g8) * D + c0 + t2;
+        float* out = a.Y0 + (unit * kBC + 16 * mt + g8) * D + c0 + t2;
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; e += 2)
-          *reinterpret_cast<float2*>(out + (e >> 1) * 8 * D + 8 * n) =
-              make_float2(y[n][e] * f, y[n][e + 1] * f);
+          for (int e = 0; e < 4; e += 2)
+            *reinterpret_cast<float2*>(out + (e >> 1) * 8 * D + 8 * n) =
+                make_float2(y[n][e] * f, y[n][e + 1] * f);
+      }
+      if (warp == 7 && h + 1 < h0 + heads) make_gates(a, c, unit + 1, h + 1, &gates[(h + 1) & 1]);
     }
-  }
-  __syncthreads();
-  // S as limbs: warp = 16 rows, half of the columns; zeros above the diagonal blocks
-  float2 sv[8];
-  big = 0.f;
-#pragma unroll
-  for (int m = 0; m < 8; ++m) {
-    const int r = 16 * rb + g8 + 8 * (m & 1), s = 32 * par + 8 * (m >> 1) + t2;
-    sv[m] = make_float2(0.f, 0.f);
-    if (2 * par + (m >> 2) <= rb) sv[m] = *reinterpret_cast<const float2*>(&S[r * kBT + s]);
-    big = max_nan(big, max_nan(fabsf(sv[m].x), fabsf(sv[m].y)));
-  }
-  big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-  if (lane == 0) atomicMax(&most[4], __float_as_uint(big));
-  __syncthreads();
-  {
-    float inv;
-    const float sc = pow2_scale(__uint_as_float(most[4]), &inv);
-    if (tid == 0) fac[kFinvS] = inv;
+    __syncthreads();
+    // S as limbs: warp = 16 rows, half of the columns; zeros above the diagonal blocks
+    float2 sv[8];
+    big = 0.f;
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
       const int r = 16 * rb + g8 + 8 * (m & 1), s = 32 * par + 8 * (m >> 1) + t2;
-      uint32_t hi, lo;
-      split_f16(sv[m].x * sc, sv[m].y * sc, hi, lo);
-      const uint32_t at = sw128_offset(r, 2 * s);
-      *reinterpret_cast<uint32_t*>(smem + at) = hi;
-      *reinterpret_cast<uint32_t*>(smem + kBlk + at) = lo;
+      sv[m] = make_float2(0.f, 0.f);
+      if (2 * par + (m >> 2) <= rb) sv[m] = *reinterpret_cast<const float2*>(&S[r * kBT + s]);
+      big = max_nan(big, max_nan(fabsf(sv[m].x), fabsf(sv[m].y)));
+    }
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    if (lane == 0) atomicMax(&most[4], __float_as_uint(big));
+    __syncthreads();
+    {
+      float inv;
+      const float sc = pow2_scale(__uint_as_float(most[4]), &inv);
+      if (tid == 0) a.fac[unit * kFac + kFinvS] = inv;
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const int r = 16 * rb + g8 + 8 * (m & 1), s = 32 * par + 8 * (m >> 1) + t2;
+        uint32_t hi, lo;
+        split_f16(sv[m].x * sc, sv[m].y * sc, hi, lo);
+        const uint32_t at = sw128_offset(r, 2 * s);
+        *reinterpret_cast<uint32_t*>(smem + at) = hi;
+        *reinterpret_cast<uint32_t*>(smem + kBlk + at) = lo;
+      }
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      bulk_store_s2g(a.S + unit * 2 * kBlk, smem, 2 * kBlk);
+      tma_store_commit();
     }
   }
-  __syncthreads();
-  uint4* out = reinterpret_cast<uint4*>(a.S + unit * 2 * kBlk);
-#pragma unroll
-  for (int x = tid; x < 2 * kBlk / 16; x += 256) out[x] = reinterpret_cast<const uint4*>(smem)[x];
-  }  // heads
+  if (tid == 0) tma_store_wait_all<0>();
 }
 
 // ---------------------------------------------------------------------------
