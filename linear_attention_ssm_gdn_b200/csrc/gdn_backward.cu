@@ -311,11 +311,11 @@ struct PrepSmem {
   static constexpr int kBytes = T + 4 * 16 * 20 * 4;
 };
 
-// x as two TF32 limbs.
+// x as two TF32 limbs: the upper 19 bits of x rounded (half away from zero), and the
+// rest, of which the MMA reads the upper 19 bits.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-  const float rest = x - __uint_as_float(hi);
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma8_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
@@ -360,6 +360,7 @@ __device__ __forceinline__ void block_product(float (&acc)[2][4], const float* A
 struct GateRows {
   float2 G[kBC];
   float beta[kBC], eG[kBC];  // eG: scale e^G
+  float end[kBC];            // e^{G_b - G}, b the last row of the 16-row block
   float most;                // the largest |scale e^G|
 };
 __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c, size_t unit, int h,
@@ -402,7 +403,8 @@ __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c,
     const float eG = exp2f(G.x + G.y), eT = exp2f(float(total - x[e]));
     s->eG[r] = a.scale * eG;
     most = max_nan(most, fabsf(a.scale * eG));
-    fac[kFend + r] = exp2f(float(end - x[e]));
+    s->end[r] = exp2f(float(end - x[e]));
+    fac[kFend + r] = s->end[r];
     fac[kFeG + r] = eG;
     fac[kFeT + r] = eT;
     fac[kFbeta + r] = bt[e];
@@ -489,13 +491,25 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
     for (int j = 0; j < 4; ++j) {
       const int s0 = 32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2;
       if (2 * (j >> 1) + par <= rb) {
-        const float2 G0 = gr.G[s0], G1 = gr.G[s0 + 1];
+        // The decay in two factors, e^{G_r - G_b} e^{G_b - G_s}, split at the last row b of
+        // the column block.  In the diagonal blocks the first one is above 1: where the
+        // block decays by 2^60 or more, each element takes an exponential of its own.
+        const float2 Gb = gr.G[s0 | 15];
+        const bool own = (s0 >> 4) == rb && gr.G[s0 & ~15].x - Gb.x > 60.f;
+        const float2 f = *reinterpret_cast<const float2*>(&gr.end[s0]);
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const int r = 16 * rb + g8 + (e >> 1) * 8;
           const float2 Gr = gr.G[r];
-          const float d0 = s0 <= r ? expdiff(Gr, G0) : 0.f;
-          const float d1 = s0 + 1 <= r ? expdiff(Gr, G1) : 0.f;
+          float d0, d1;
+          if (own) {
+            d0 = s0 <= r ? expdiff(Gr, gr.G[s0]) : 0.f;
+            d1 = s0 + 1 <= r ? expdiff(Gr, gr.G[s0 + 1]) : 0.f;
+          } else {
+            const float d = expdiff(Gr, Gb);
+            d0 = s0 <= r ? d * f.x : 0.f;
+            d1 = s0 + 1 <= r ? d * f.y : 0.f;
+          }
           *reinterpret_cast<float2*>(&B[r * kBT + s0]) =
               make_float2(s0 < r ? kk_[j][e] * d0 : 0.f, s0 + 1 < r ? kk_[j][e + 1] * d1 : 0.f);
           m_[j][e] = s0 <= r ? qk[j][e] * d0 : 0.f;
@@ -539,7 +553,7 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
       // The inverses of I + L_b: thread = (block, column), forward substitution
       if (tid < kBC) {
         const int b = tid >> 4, j = tid & 15;
-        float x[16];
+        float x[16], t[16];  // beta times the column, and the column
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const float* row = B + (16 * b + r) * kBT + 16 * b;
@@ -552,10 +566,11 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
             if (q + 2 < r) y0 = fmaf(-w.z, x[q + 2], y0);
             if (q + 3 < r) y1 = fmaf(-w.w, x[q + 3], y1);
           }
-          y0 += y1;
-          T[(b * 16 + r) * 20 + j] = y0;
-          x[r] = y0 * bs[16 * b + r];  // L_b's columns carry beta
+          t[r] = y0 + y1;
+          x[r] = t[r] * bs[16 * b + r];  // L_b's columns carry beta
         }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) T[(b * 16 + r) * 20 + j] = t[r];
       }
       named_sync(1, 128);
       // (I + L_b)^-1 B_bj in B's place: warp = block row b and, for the short rows, some
