@@ -73,18 +73,30 @@ def _gates(g: torch.Tensor, beta: torch.Tensor, rows: int, H_v: int) -> int:
     return int(g.stride(0)) if rows > 1 else H_v
 
 
-def _launch_on(device, stream):
-    """The device and stream a call runs on: a context that makes `device` (the
-    tensors' own, whichever is current) and `stream` current, so that what the
-    call allocates belongs to the stream that uses it, and the stream's handle.
-    With the current device's current stream there is nothing to switch."""
+def _expect(t: torch.Tensor, dtype, shape, name: str):
+    """_dense, with one quick look at tensors that are as they should be."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        _dense(t, dtype, shape, name)
+
+
+def _current(device, stream):
+    """The handle of the stream to launch on where nothing has to be switched for
+    it: no stream is given and `device` is the current one; else None."""
     if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(), torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
+
+
+@contextlib.contextmanager
+def _switched(device, stream):
+    """Makes `device` (the tensors' own) and `stream` current, so that what the call
+    allocates belongs to the stream that uses it; yields the stream's handle."""
     if stream is None:
         stream = torch.cuda.current_stream(device)
     elif not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return torch.cuda.stream(stream), stream.cuda_stream
+    with torch.cuda.stream(stream):
+        yield stream.cuda_stream
 
 
 def _same_device(device, *tensors):
@@ -302,6 +314,19 @@ def gdn_flag_clear(engaged_flag, stream=None):
 def _qkv(q, k, v, g, beta):
     """Checks of packed rows q, k [R, H_k, d], v [R, H_v, d] bf16, g, beta [R, H_v]
     f32; returns (R, H_k, H_v, d_k, d_v, qk_stride, v_stride, gb_stride)."""
+    bf16, f32 = torch.bfloat16, torch.float32
+    if q.dtype is bf16 and k.dtype is bf16 and v.dtype is bf16 and g.dtype is f32 and \
+            beta.dtype is f32 and q.dim() == 3 and v.dim() == 3 and q.is_cuda:
+        # the common case in one look: every layout as it should be
+        R, H_k, d_k = shape = q.shape
+        Rv, H_v, d_v = v.shape
+        sq, sv, sg = q.stride(), v.stride(), g.stride()
+        if Rv == R > 0 and k.shape == shape and sq[2] == 1 and sq[1] == d_k and k.stride() == sq and \
+                sv[2] == 1 and sv[1] == d_v and g.shape == beta.shape == (R, H_v) and \
+                sg[1] == 1 and beta.stride() == sg:
+            if R == 1:  # the row stride of a single row means nothing
+                return 1, H_k, H_v, d_k, d_v, H_k * d_k, H_v * d_v, H_v
+            return R, H_k, H_v, d_k, d_v, sq[0], sv[0], sg[0]
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need(t, torch.bfloat16, n)
     if q.dim() != 3 or v.dim() != 3 or v.shape[0] != q.shape[0]:
@@ -327,26 +352,30 @@ def gdn_decode(h_table, q, k, v, g, beta, cu_seqlens=None, o=None, scale=1.0, st
     h_table: int64 CUDA tensor [batch] of state pointers (0 = padding sequence);
     cu_seqlens: int32 [batch + 1] row offsets, or None for one row per sequence.
     Returns o [rows, H_v, d] bf16 (rows of no sequence are not written)."""
-    lib = _lib.load()
-    _dense(h_table, torch.int64, (h_table.shape[0],), "h_table")
+    _need(h_table, torch.int64, "h_table")
     R, H_k, H_v, d_k, d_v, qk_stride, v_stride, gb_stride = _qkv(q, k, v, g, beta)
+    device = q.device
+    handle = _current(device, stream)
+    if handle is None:
+        with _switched(device, stream) as handle:
+            return gdn_decode(h_table, q, k, v, g, beta, cu_seqlens, o, scale)
     batch = h_table.shape[0]
+    _expect(h_table, torch.int64, (batch,), "h_table")
     if cu_seqlens is not None:
-        _dense(cu_seqlens, torch.int32, (batch + 1,), "cu_seqlens")
+        _expect(cu_seqlens, torch.int32, (batch + 1,), "cu_seqlens")
     elif R != batch:
         raise ValueError("q/k/v must hold one row per sequence without cu_seqlens")
-    device = q.device
-    if o is not None:
-        _dense(o, torch.bfloat16, (R, H_v, d_v), "o")
+    if o is None:
+        o = torch.empty(R, H_v, d_v, dtype=torch.bfloat16, device=device)
+    else:
+        _expect(o, torch.bfloat16, (R, H_v, d_v), "o")
     _same_device(device, h_table, k, v, g, beta, cu_seqlens, o)
-    on, handle = _launch_on(device, stream)
-    with on:
-        if o is None:
-            o = torch.empty(R, H_v, d_v, dtype=torch.bfloat16, device=device)
-        rc = lib.gdn_decode(_ptr(h_table), _ptr(q), _ptr(k), qk_stride, _ptr(v), v_stride,
-                            _ptr(g), _ptr(beta), gb_stride, _ptr(cu_seqlens), _ptr(o), batch, R,
-                            H_k, H_v, d_k, d_v, float(scale), handle)
-    _lib.check("gdn_decode", rc)
+    rc = _lib.load().gdn_decode(
+        h_table.data_ptr(), q.data_ptr(), k.data_ptr(), qk_stride, v.data_ptr(), v_stride,
+        g.data_ptr(), beta.data_ptr(), gb_stride, _ptr(cu_seqlens), o.data_ptr(), batch, R, H_k,
+        H_v, d_k, d_v, scale, handle)
+    if rc:
+        _lib.check("gdn_decode", rc)
     return o
 
 
@@ -363,59 +392,65 @@ def gdn_state_tables(lens, slots=None, pool=None, out=None, total_rows=None, fla
     of lens) sizes the maps.  With neither row map, total_rows bounds the
     offsets (default: no bound).  flag: int32 word, GDN_FLAG_ERROR is OR-ed in
     on a bad length or slot or where the maps are too short."""
-    lib = _lib.load()
     n = lens.shape[0]
-    _dense(lens, torch.int32, (n,), "lens")
+    _expect(lens, torch.int32, (n,), "lens")
     device = lens.device
+    handle = _current(device, stream)
+    if handle is None:
+        with _switched(device, stream) as handle:
+            return gdn_state_tables(lens, slots, pool, out, total_rows, flag)
     slot_floats = num_slots = 0
     if (slots is None) != (pool is None):
         raise ValueError("slots and pool must both be given or both be left out")
     if slots is not None:
-        _dense(slots, torch.int32, (n,), "slots")
+        _expect(slots, torch.int32, (n,), "slots")
         _need(pool, torch.float32, "pool")
+        if pool.dim() != 4:
+            raise ValueError("pool: expected [slots, H_v, d, d]")
         num_slots = pool.shape[0]
-        if pool.dim() != 4 or (num_slots and not pool[0].is_contiguous()):
+        slot_floats, s1, s2, s3 = pool.stride()
+        if (s1, s2, s3) != (pool.shape[2] * pool.shape[3], pool.shape[3], 1):
             raise ValueError("pool: expected [slots, H_v, d, d] with dense slots")
-        slot_floats = int(pool.stride(0))
     if flag is not None:
         _need(flag, torch.int32, "flag")
-    if out is None and total_rows is None:
-        raise ValueError("total_rows sizes the maps where out is not given")
-    on, handle = _launch_on(device, stream)
-    with on:
-        if out is None:
-            def ints(m):
-                return torch.empty(m, dtype=torch.int32, device=device)
-            out = {"cu_seqlens": ints(n + 1), "row_seq": ints(total_rows),
-                   "cu_chunks": ints(n + 1), "chunk_seq": ints(total_rows // 64 + n)}
-            if slots is not None:
-                out["row_slot"] = ints(total_rows)
-                out["h_table"] = torch.empty(n, dtype=torch.int64, device=device)
-        t = [out.get(x) for x in ("cu_seqlens", "cu_chunks", "row_seq", "row_slot", "chunk_seq")]
-        cu_seqlens, cu_chunks, row_seq, row_slot, chunk_seq = t
-        h_table = out.get("h_table")
-        for x, name in ((cu_seqlens, "cu_seqlens"), (cu_chunks, "cu_chunks")):
-            if x is not None:
-                _dense(x, torch.int32, (n + 1,), name)
-        for x, name in ((row_seq, "row_seq"), (row_slot, "row_slot"), (chunk_seq, "chunk_seq")):
-            if x is not None:
-                _dense(x, torch.int32, (x.shape[0],), name)
-        if (slots is None) != (h_table is None) or (slots is None and row_slot is not None):
-            raise ValueError("h_table belongs to slots and pool, row_slot needs them")
-        if h_table is not None:
-            _dense(h_table, torch.int64, (n,), "h_table")
-        _same_device(device, slots, pool, flag, h_table, *t)
-        rows = [x.shape[0] for x in (row_seq, row_slot) if x is not None]
-        if len(set(rows)) > 1:
-            raise ValueError("row_seq and row_slot must have one length")
-        unbounded = 0x7FFFFFFE
-        row_cap = rows[0] if rows else unbounded if total_rows is None else int(total_rows)
-        chunk_cap = unbounded if chunk_seq is None else chunk_seq.shape[0]
-        rc = lib.gdn_state_tables(_ptr(lens), _ptr(slots), n, _ptr(pool), slot_floats, num_slots,
-                                  _ptr(cu_seqlens), _ptr(h_table), _ptr(row_seq),
-                                  _ptr(row_slot), row_cap, _ptr(cu_chunks), _ptr(chunk_seq),
-                                  chunk_cap, _ptr(flag), handle)
-    _lib.check("gdn_state_tables", rc)
+    if out is None:
+        if total_rows is None:
+            raise ValueError("total_rows sizes the maps where out is not given")
+
+        def ints(m):
+            return torch.empty(m, dtype=torch.int32, device=device)
+        out = {"cu_seqlens": ints(n + 1), "row_seq": ints(total_rows),
+               "cu_chunks": ints(n + 1), "chunk_seq": ints(total_rows // 64 + n)}
+        if slots is not None:
+            out["row_slot"] = ints(total_rows)
+            out["h_table"] = torch.empty(n, dtype=torch.int64, device=device)
+    cu_seqlens, cu_chunks, row_seq, row_slot, chunk_seq, h_table = t = [
+        out.get(x) for x in ("cu_seqlens", "cu_chunks", "row_seq", "row_slot", "chunk_seq",
+                             "h_table")]
+    for x, name in ((cu_seqlens, "cu_seqlens"), (cu_chunks, "cu_chunks")):
+        if x is not None:
+            _expect(x, torch.int32, (n + 1,), name)
+    for x, name in ((row_seq, "row_seq"), (row_slot, "row_slot"), (chunk_seq, "chunk_seq")):
+        if x is not None:
+            _expect(x, torch.int32, (x.shape[0],), name)
+    if (slots is None) != (h_table is None) or (slots is None and row_slot is not None):
+        raise ValueError("h_table belongs to slots and pool, row_slot needs them")
+    if h_table is not None:
+        _expect(h_table, torch.int64, (n,), "h_table")
+    if row_seq is not None and row_slot is not None and row_seq.shape != row_slot.shape:
+        raise ValueError("row_seq and row_slot must have one length")
+    _same_device(device, slots, pool, flag, *t)
+    rows = row_slot if row_seq is None else row_seq
+    unbounded = 0x7FFFFFFE
+    row_cap = rows.shape[0] if rows is not None else \
+        unbounded if total_rows is None else int(total_rows)
+    chunk_cap = unbounded if chunk_seq is None else chunk_seq.shape[0]
+    rc = _lib.load().gdn_state_tables(
+        lens.data_ptr(), _ptr(slots), n, _ptr(pool), slot_floats, num_slots, _ptr(cu_seqlens),
+        _ptr(h_table), _ptr(row_seq), _ptr(row_slot), row_cap, _ptr(cu_chunks), _ptr(chunk_seq),
+        chunk_cap, _ptr(flag), handle)
+    if rc:
+        _lib.check("gdn_state_tables", rc)
     return out
 
 
@@ -429,36 +464,41 @@ def gdn_chunk_backward(q, k, v, g, beta, cu_seqlens, do, h0=None, dhT=None, dh0=
     """Gradients of gdn_chunk_prefill(q, k, v, g, beta, cu_seqlens, h0) from do
     [T, H_v, d] bf16 and dhT [N, H_v, d, d] f32 (None = zeros).  Returns (dq, dk,
     dv, dg, dbeta, dh0); dh0 is None unless h0 or a dh0 buffer is given."""
-    lib = _lib.load()
     T, H_k, H_v, d_k, d_v, qk_stride, v_stride, gb_stride = _qkv(q, k, v, g, beta)
-    _dense(cu_seqlens, torch.int32, (cu_seqlens.shape[0],), "cu_seqlens")
+    device = q.device
+    handle = _current(device, stream)
+    if handle is None:
+        with _switched(device, stream) as handle:
+            return gdn_chunk_backward(q, k, v, g, beta, cu_seqlens, do, h0, dhT, dh0, scale,
+                                      workspace)
+    _expect(cu_seqlens, torch.int32, (cu_seqlens.shape[0],), "cu_seqlens")
     N = cu_seqlens.shape[0] - 1
-    _dense(do, torch.bfloat16, (T, H_v, d_v), "do")
+    _expect(do, torch.bfloat16, (T, H_v, d_v), "do")
     for t, n in ((h0, "h0"), (dhT, "dhT"), (dh0, "dh0")):
         if t is not None:
-            _dense(t, torch.float32, (N, H_v, d_k, d_v), n)
-    device = q.device
+            _expect(t, torch.float32, (N, H_v, d_k, d_v), n)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
     _same_device(device, k, v, g, beta, cu_seqlens, do, h0, dhT, dh0, workspace)
-    on, handle = _launch_on(device, stream)
-    with on:
-        dq = torch.empty(T, H_k, d_k, dtype=torch.bfloat16, device=device)
-        dk = torch.empty_like(dq)
-        dv = torch.empty(T, H_v, d_v, dtype=torch.bfloat16, device=device)
-        dg = torch.empty(T, H_v, dtype=torch.float32, device=device)
-        dbeta = torch.empty_like(dg)
-        if dh0 is None and h0 is not None:
-            dh0 = torch.empty(N, H_v, d_k, d_v, dtype=torch.float32, device=device)
-        if workspace is None:
-            need = int(lib.gdn_chunk_backward_workspace_bytes(T, N, H_k, H_v, d_k, d_v))
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        rc = lib.gdn_chunk_backward(
-            _ptr(q), _ptr(k), qk_stride, _ptr(v), v_stride, _ptr(g), _ptr(beta), gb_stride,
-            _ptr(cu_seqlens), N, T, _ptr(h0), _ptr(do), _ptr(dhT), _ptr(dq), _ptr(dk), _ptr(dv),
-            _ptr(dg), _ptr(dbeta), _ptr(dh0), H_k, H_v, d_k, d_v, float(scale), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), handle)
-    _lib.check("gdn_chunk_backward", rc)
+    lib = _lib.load()
+    dq = torch.empty(T, H_k, d_k, dtype=torch.bfloat16, device=device)
+    dk = torch.empty_like(dq)
+    dv = torch.empty(T, H_v, d_v, dtype=torch.bfloat16, device=device)
+    dg = torch.empty(T, H_v, dtype=torch.float32, device=device)
+    dbeta = torch.empty_like(dg)
+    if dh0 is None and h0 is not None:
+        dh0 = torch.empty(N, H_v, d_k, d_v, dtype=torch.float32, device=device)
+    if workspace is None:
+        need = lib.gdn_chunk_backward_workspace_bytes(T, N, H_k, H_v, d_k, d_v)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    rc = lib.gdn_chunk_backward(
+        q.data_ptr(), k.data_ptr(), qk_stride, v.data_ptr(), v_stride, g.data_ptr(),
+        beta.data_ptr(), gb_stride, cu_seqlens.data_ptr(), N, T, _ptr(h0), do.data_ptr(),
+        _ptr(dhT), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(),
+        _ptr(dh0), H_k, H_v, d_k, d_v, scale, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), handle)
+    if rc:
+        _lib.check("gdn_chunk_backward", rc)
     return dq, dk, dv, dg, dbeta, dh0
 
 
