@@ -15,7 +15,8 @@
 //   dq = scale e^G (dO H^T) + P K,
 //   dk = P^T Q + (N + N^T) K - e^G (beta E) H^T + e^{G_C-G} (beta u) dH'^T,
 //   dg_r = <H', dH'> + sum_{s >= r} (q_s . dq_s - v_s . dv_s),
-// the last because e^{G_r} enters only by scaling q_r up and v_r down.
+// the last because e^{G_r} enters only by scaling q_r up and v_r down (and 0 for the
+// first row of a chunk that begins with a zero state).
 //
 // Gates reach the exponentials as differences of 64-bit cumulative sums (in base
 // 2: exp2f is the shorter function), kept as two floats: a strong decay early in
@@ -1283,7 +1284,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   float* endU = invE + kBC;         // invU e^{G_b - G}
   float* part = endU + kBC;         // [4][64] q . dq of each 32 rows d_k
   float* vd = part + 4 * kBC;       // [64] v . dv
-  float* red = vd + kBC;            // by the head's parity: [2][8] <H', dH'>, [2][2] 1 / scale of H, dH'
+  float* red = vd + kBC;            // by the head's parity: [2][8] <H', dH'>, [2][2] 1 / scale of H, dH', [2] H = 0
   // this warp's part of a tile is written: the issuer may use it
   auto ready = [&](int b) {
     fence_proxy_async_smem();
@@ -1538,7 +1539,9 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int rr = 63 - (2 * lane + k);
-          if (rr < c.rows) a.dg[size_t(c.row0 + rr) * a.H_v + h] = float(z[k] + hh);
+          // a zero entry state's decay does nothing: 0, not the rounding of the sum
+          const bool none = rr == 0 && red[20 + (h & 1)] != 0.f;
+          if (rr < c.rows) a.dg[size_t(c.row0 + rr) * a.H_v + h] = none ? 0.f : float(z[k] + hh);
         }
       }
       named_sync(1, kGradsRows);  // what was read here is rewritten for the next head
@@ -1572,13 +1575,14 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           prefetch_l2(dH + D * D, D * D * 4);
         }
       }
-      float sh, sd, ih, id;
+      float sh, sd, ih, id, most;
       {
         const float* hm = a.Hmax + unit * 16;
         const float4 m0 = *reinterpret_cast<const float4*>(hm), m1 = *reinterpret_cast<const float4*>(hm + 4);
         const float4 n0 = *reinterpret_cast<const float4*>(hm + 8), n1 = *reinterpret_cast<const float4*>(hm + 12);
-        sh = pow2_scale(max_nan(max_nan(max_nan(m0.x, m0.y), max_nan(m0.z, m0.w)),
-                                max_nan(max_nan(m1.x, m1.y), max_nan(m1.z, m1.w))), &ih);
+        most = max_nan(max_nan(max_nan(m0.x, m0.y), max_nan(m0.z, m0.w)),
+                       max_nan(max_nan(m1.x, m1.y), max_nan(m1.z, m1.w)));
+        sh = pow2_scale(most, &ih);
         sd = pow2_scale(max_nan(max_nan(max_nan(n0.x, n0.y), max_nan(n0.z, n0.w)),
                                 max_nan(max_nan(n1.x, n1.y), max_nan(n1.z, n1.w))), &id);
       }
@@ -1593,7 +1597,10 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           // Once the last head's H has been multiplied its tiles are free, and so are the
           // scales of the head before it: the rows' warps have begun the last head.
           if (h > h0) mbar_wait(&bars[gA12], ph ^ 1, abort_flag, err, 64u);
-          if (t == 0) red[16 + 2 * (h & 1)] = ih, red[17 + 2 * (h & 1)] = id;
+          if (t == 0) {
+            red[16 + 2 * (h & 1)] = ih, red[17 + 2 * (h & 1)] = id;
+            red[20 + (h & 1)] = most == 0.f;
+          }
         }
         quads_to_tile<D, true, B>(v, t + q * kGradsStates, sh, base + L::HH, base + L::HL);
       }

@@ -72,6 +72,19 @@ def test_without_states(d):
     _check(lens, got, rows, do, None, None)
 
 
+@pytest.mark.parametrize("h0", [None, "zeros"])
+@pytest.mark.parametrize("lens", [[1], [1, 0, 1], [3, 70]])
+def test_gate_of_a_zero_state_has_no_gradient(lens, h0):
+    """The first row decays a state that is zero: its gate's gradient is 0 exactly."""
+    rows, do, _, dhT = _case(lens, 1, 2, 64, seed=24)
+    h0 = None if h0 is None else torch.zeros(len(lens), 2, 64, 64)
+    dg = _run(lens, rows, do, h0, dhT)[3]
+    first = [x for x, n in zip(R.offsets(lens), lens) if n]
+    assert not dg[first].any()
+    want = R.backward(*rows, lens, do, h0, dhT)[3]
+    assert R.rel(dg, want) <= R.F32_REL
+
+
 def test_only_one_of_the_state_arguments():
     lens = [70]
     rows, do, h0, dhT = _case(lens, 1, 2, 64, seed=6)
