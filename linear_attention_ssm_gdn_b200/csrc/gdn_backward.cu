@@ -77,6 +77,7 @@ struct BwdArgs {
   float* H;            // [chunk + sequence][H_v][D / 16][D][16] entry states, then the final one
   float* dH;           // [chunk][H_v][D / 16][D][16] gradient of the exit state
   float* Hmax;         // [chunk][H_v][2][8] largest |H| and |dH| of each scan warp's part
+  float* h0dh0;        // [sequence][H_v][8] <h0, dh0>, each scan warp's part
 };
 
 // Per-unit factors: of each row e^G, e^{G_C - G}, beta, the products beta
@@ -147,6 +148,15 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// c += A B with a rounded sum: the MMA's own accumulation truncates, and over the
+// steps of a long product the losses have one sign and add up.
+__device__ __forceinline__ void add_mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  float p[4] = {};
+  mma16(p, a, b0, b1);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c[e] += p[e];
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -465,10 +475,10 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
       if (2 * j + par <= rb) {
         uint32_t bv[4];
         ldsm4(bv, piece<true>(base + L::K, 16 * (2 * j + par), 16 * kk));
-        mma16(kk_[2 * j], ak, bv[0], bv[1]);
-        mma16(kk_[2 * j + 1], ak, bv[2], bv[3]);
-        mma16(qk[2 * j], aq, bv[0], bv[1]);
-        mma16(qk[2 * j + 1], aq, bv[2], bv[3]);
+        add_mma16(kk_[2 * j], ak, bv[0], bv[1]);
+        add_mma16(kk_[2 * j + 1], ak, bv[2], bv[3]);
+        add_mma16(qk[2 * j], aq, bv[0], bv[1]);
+        add_mma16(qk[2 * j + 1], aq, bv[2], bv[3]);
       }
   }
 #pragma unroll
@@ -637,10 +647,13 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
             for (int np = 0; np < 2; ++np) {
               uint32_t bv[4];
               ldsm4t(bv, piece<false>(base, 16 * kk, c0 + 16 * np));
-              mma16(y[2 * np], al, bv[0], bv[1]);
-              mma16(y[2 * np + 1], al, bv[2], bv[3]);
-              mma16(y[2 * np], ah, bv[0], bv[1]);
-              mma16(y[2 * np + 1], ah, bv[2], bv[3]);
+              float p0[4] = {}, p1[4] = {};
+              mma16(p0, al, bv[0], bv[1]);
+              mma16(p1, al, bv[2], bv[3]);
+              mma16(p0, ah, bv[0], bv[1]);
+              mma16(p1, ah, bv[2], bv[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[2 * np][e] += p0[e], y[2 * np + 1][e] += p1[e];
             }
           }
         float* out = a.Y0 + (unit * kBC + 16 * mt + g8) * D + c0 + t2;
@@ -1008,6 +1021,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
     if constexpr (!back) send_state(a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D);
     if (lane == 0) tma_store_wait_all<0>();
     __syncwarp();
+    if (back && a.h0 != nullptr && n > 0) {  // the gradient of the first row's gate
+      float s = 0.f;
+#pragma unroll
+      for (int x = 0; x < NK; ++x)
+        s = on ? fmaf(a.h0[head + size_t(NK * hh + x) * D + dv], st[x], s) : 0.f;
+      s = warp_sum(s);
+      if (lane == 0) a.h0dh0[(size_t(b) * a.H_v + h) * 8 + warp] = s;
+    }
     if (back && on && a.dh0 != nullptr) {
 #pragma unroll
       for (int x = 0; x < NK; ++x) a.dh0[head + size_t(NK * hh + x) * D + dv] = st[x];
@@ -1221,7 +1242,8 @@ constexpr int kGradsRows = 256, kGradsStates = 128, kGradsThreads = 512;
 // Registers after re-allocation: 128 (2 x 176 + 112 + 48) is the launch's 512 x 128.
 constexpr uint32_t kRegsRows = 176, kRegsStates = 112, kRegsIssue = 48;
 enum { gO = 0, gU, gH, gP, gD, gPN, gA12, gA345, gA6, gDrain, kGradsBars };
-enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA4 = 256, kTA5 = 320, kTA6 = 384 };
+enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA4 = 256, kTA5 = 320, kTA6 = 384,
+       kTPN2 = kTA3 };  // P and N's second half over d_v: read before A3 is made
 
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -1402,8 +1424,14 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       float x[32];
       mbar_wait(&bars[gPN], ph, abort_flag, err, 64u);
       tc_fence_after();
-      tmem_ld32(tl + kTPN, x);
-      tmem_ld_wait();
+      {
+        float y[32];
+        tmem_ld32(tl + kTPN, x);
+        tmem_ld32(tl + kTPN2, y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] += y[k];
+      }
       float ip, in;
       {
         const bool isn = qd >= 2;
@@ -1534,14 +1562,28 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         double hh = 0.0;
 #pragma unroll
         for (int w = 0; w < kGradsStates / 32; ++w) hh += red[8 * (h & 1) + w];
-        z[0] += run - z[1];
-        z[1] = run;
+        z[0] += run - z[1] + hh;
+        z[1] = run + hh;
+        // The chunk's first row has a second value, <H, e^{-G} dH> with the entry state:
+        // 0 for a zero state, <h0, dh0> for the sequence's first chunk.  What the sums miss of
+        // it they have gathered over the rows: it is shared out along them.
+        const float* first = a.h0dh0 + (size_t(c.seq) * a.H_v + h) * 8;
+        const bool zero = red[20 + (h & 1)] != 0.f;
+        if (zero || (a.h0 != nullptr && i == a.cu_chunks[c.seq])) {
+          double miss = -__shfl_sync(0xffffffffu, z[1], 31);
+          if (!zero) {
+            for (int w = 0; w < 8; ++w) miss += first[w];
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int rr = 63 - (2 * lane + k);
+            if (rr < c.rows) z[k] += rr == 0 ? miss : miss * double(c.rows - rr) / double(c.rows);
+          }
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int rr = 63 - (2 * lane + k);
-          // a zero entry state's decay does nothing: 0, not the rounding of the sum
-          const bool none = rr == 0 && red[20 + (h & 1)] != 0.f;
-          if (rr < c.rows) a.dg[size_t(c.row0 + rr) * a.H_v + h] = none ? 0.f : float(z[k] + hh);
+          if (rr < c.rows) a.dg[size_t(c.row0 + rr) * a.H_v + h] = float(z[k]);
         }
       }
       named_sync(1, kGradsRows);  // what was read here is rewritten for the next head
@@ -1665,10 +1707,11 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + kTPN, tall(oe, kk), flat(ul, kk), id64, kk != 0);
+        mma_bf16_ss(tmem + (kk < D / 32 ? kTPN : kTPN2), tall(oe, kk), flat(ul, kk), id64,
+                    kk % (D / 32) != 0);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + kTPN, tall(oe, kk), flat(uh, kk), id64, 1u);
+        mma_bf16_ss(tmem + (kk < D / 32 ? kTPN : kTPN2), tall(oe, kk), flat(uh, kk), id64, 1u);
       mma_commit(&bars[gPN]);
       ok = mbar_wait(&bars[gH], ph, abort_flag, err, 128u);
       if (!ok) break;
@@ -1761,6 +1804,7 @@ size_t layout(BwdArgs* a, char* base, int total_tokens, int num_seqs, int H_k, i
   a->H = reinterpret_cast<float*>(take((mc + num_seqs) * size_t(H_v) * D * D * 4));
   a->dH = reinterpret_cast<float*>(take(units * D * D * 4));
   a->Hmax = reinterpret_cast<float*>(take(units * 2 * 8 * 4));
+  a->h0dh0 = reinterpret_cast<float*>(take(size_t(num_seqs) * H_v * 8 * 4));
   return at;
 }
 
