@@ -61,7 +61,9 @@ __global__ void __launch_bounds__(kDecThreads)
                   int total_rows, int H_k, int H_v, float scale) {
   constexpr int RPT = D / kGroups;  // state rows per thread
   constexpr int SLICES = D / kCols;
-  __shared__ float part[2][kDecThreads / 32][2 * kCols + 1];  // double-buffered over rows
+  // double-buffered over rows
+  __shared__ __align__(16) float part[2][kDecThreads / 32][2 * kCols];
+  __shared__ __align__(16) float part_kq[2][kDecThreads / 32];
   const int slice = blockIdx.x % SLICES;
   const int unit = blockIdx.x / SLICES;
   const int h = unit % H_v, b = unit / H_v;
@@ -83,9 +85,12 @@ __global__ void __launch_bounds__(kDecThreads)
     return;
   }
   float* H = base + size_t(h) * D * D + size_t(grp * RPT) * D + col;
-  float4 st[RPT];
+  float2 st[RPT][2];
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) st[i] = *reinterpret_cast<const float4*>(H + i * D);
+  for (int i = 0; i < RPT; ++i) {
+    const float4 x = *reinterpret_cast<const float4*>(H + i * D);
+    st[i][0] = make_float2(x.x, x.y), st[i][1] = make_float2(x.z, x.w);
+  }
 
   const uint16_t* kp = k + size_t(row) * qk_stride + hk * D + grp * RPT;
   const uint16_t* qp = q + size_t(row) * qk_stride + hk * D + grp * RPT;
@@ -100,70 +105,66 @@ __global__ void __launch_bounds__(kDecThreads)
       kp += qk_stride, qp += qk_stride, vp += v_stride, gp += gb_stride, bp += gb_stride;
       next.load(kp, qp, vp, gp, bp);
     }
-    float p[4] = {0.f, 0.f, 0.f, 0.f}, s[4] = {0.f, 0.f, 0.f, 0.f}, kq = 0.f;
+    float2 p0{}, p1{}, s0{}, s1{};  // of the thread's columns 0, 1 and 2, 3
+    float kq = 0.f;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const float ki = i & 1 ? bf16_hi(cur.k[i / 2]) : bf16_lo(cur.k[i / 2]);
       const float qi = i & 1 ? bf16_hi(cur.q[i / 2]) : bf16_lo(cur.q[i / 2]);
-      p[0] = fmaf(st[i].x, ki, p[0]), s[0] = fmaf(st[i].x, qi, s[0]);
-      p[1] = fmaf(st[i].y, ki, p[1]), s[1] = fmaf(st[i].y, qi, s[1]);
-      p[2] = fmaf(st[i].z, ki, p[2]), s[2] = fmaf(st[i].z, qi, s[2]);
-      p[3] = fmaf(st[i].w, ki, p[3]), s[3] = fmaf(st[i].w, qi, s[3]);
+      p0 = fma2(st[i][0], both(ki), p0), p1 = fma2(st[i][1], both(ki), p1);
+      s0 = fma2(st[i][0], both(qi), s0), s1 = fma2(st[i][1], both(qi), s1);
       kq = fmaf(ki, qi, kq);
     }
-    // the warp's four row groups, then the four warps
-#pragma unroll
-    for (int off = kQuads; off < 32; off <<= 1) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        p[c] += __shfl_xor_sync(0xffffffffu, p[c], off);
-        s[c] += __shfl_xor_sync(0xffffffffu, s[c], off);
-      }
-      kq += __shfl_xor_sync(0xffffffffu, kq, off);
-    }
-    if (lane < kQuads) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        part[buf][warp][4 * lane + c] = p[c];
-        part[buf][warp][kCols + 4 * lane + c] = s[c];
-      }
-      if (lane == 0) part[buf][warp][2 * kCols] = kq;
-    }
+    // The warp's four row groups, the values spread over them: upper half s, lower half p,
+    // then two columns each.
+    const bool up = lane & 16, right = lane & 8;
+    float2 a0 = up ? s0 : p0, a1 = up ? s1 : p1;
+    const float2 b0 = up ? p0 : s0, b1 = up ? p1 : s1;
+    a0 = add2(a0, make_float2(__shfl_xor_sync(0xffffffffu, b0.x, 16),
+                              __shfl_xor_sync(0xffffffffu, b0.y, 16)));
+    a1 = add2(a1, make_float2(__shfl_xor_sync(0xffffffffu, b1.x, 16),
+                              __shfl_xor_sync(0xffffffffu, b1.y, 16)));
+    const float2 mine = right ? a1 : a0, other = right ? a0 : a1;
+    *reinterpret_cast<float2*>(&part[buf][warp][(up ? kCols : 0) + 4 * quad + (right ? 2 : 0)]) =
+        add2(mine, make_float2(__shfl_xor_sync(0xffffffffu, other.x, 8),
+                               __shfl_xor_sync(0xffffffffu, other.y, 8)));
+    kq += __shfl_xor_sync(0xffffffffu, kq, 8);
+    kq += __shfl_xor_sync(0xffffffffu, kq, 16);
+    if (lane == 0) part_kq[buf][warp] = kq;
     // One barrier per row: the buffer written now is read again two rows on.
     __syncthreads();
-    kq = 0.f;
+    const float4 kq4 = *reinterpret_cast<const float4*>(part_kq[buf]);
+    kq = (kq4.x + kq4.y) + (kq4.z + kq4.w);
+    p0 = p1 = s0 = s1 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kDecThreads / 32; ++w) kq += part[buf][w][2 * kCols];
-    const float a = expf(cur.g), vv[4] = {bf16_lo(cur.v.x), bf16_hi(cur.v.x), bf16_lo(cur.v.y),
-                                          bf16_hi(cur.v.y)};
-    float u[4], out[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float pc = 0.f, sc = 0.f;
-#pragma unroll
-      for (int w = 0; w < kDecThreads / 32; ++w) {
-        pc += part[buf][w][4 * quad + c];
-        sc += part[buf][w][kCols + 4 * quad + c];
-      }
-      u[c] = cur.beta * (vv[c] - a * pc);
-      out[c] = scale * fmaf(kq, u[c], a * sc);
+    for (int w = 0; w < kDecThreads / 32; ++w) {
+      const float4 x = *reinterpret_cast<const float4*>(&part[buf][w][4 * quad]);
+      const float4 y = *reinterpret_cast<const float4*>(&part[buf][w][kCols + 4 * quad]);
+      p0 = add2(p0, make_float2(x.x, x.y)), p1 = add2(p1, make_float2(x.z, x.w));
+      s0 = add2(s0, make_float2(y.x, y.y)), s1 = add2(s1, make_float2(y.z, y.w));
     }
-    if (grp == 0)
-      *reinterpret_cast<uint2*>(orow) =
-          make_uint2(pack_bf16x2(out[0], out[1]), pack_bf16x2(out[2], out[3]));
+    const float a = expf(cur.g);
+    const float2 beta2 = both(cur.beta);
+    const float2 u0 = mul2(beta2, fma2(both(-a), p0, make_float2(bf16_lo(cur.v.x), bf16_hi(cur.v.x))));
+    const float2 u1 = mul2(beta2, fma2(both(-a), p1, make_float2(bf16_lo(cur.v.y), bf16_hi(cur.v.y))));
+    if (grp == 0) {
+      const float2 x = mul2(both(scale), fma2(both(kq), u0, mul2(both(a), s0)));
+      const float2 y = mul2(both(scale), fma2(both(kq), u1, mul2(both(a), s1)));
+      *reinterpret_cast<uint2*>(orow) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(y.x, y.y));
+    }
     orow += size_t(H_v) * D;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const float ki = i & 1 ? bf16_hi(cur.k[i / 2]) : bf16_lo(cur.k[i / 2]);
-      st[i].x = fmaf(ki, u[0], a * st[i].x);
-      st[i].y = fmaf(ki, u[1], a * st[i].y);
-      st[i].z = fmaf(ki, u[2], a * st[i].z);
-      st[i].w = fmaf(ki, u[3], a * st[i].w);
+      st[i][0] = fma2(both(ki), u0, mul2(both(a), st[i][0]));
+      st[i][1] = fma2(both(ki), u1, mul2(both(a), st[i][1]));
     }
     cur = next;
   }
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) *reinterpret_cast<float4*>(H + i * D) = st[i];
+  for (int i = 0; i < RPT; ++i)
+    *reinterpret_cast<float4*>(H + i * D) =
+        make_float4(st[i][0].x, st[i][0].y, st[i][1].x, st[i][1].y);
 }
 
 cudaError_t launch_decode(float* const* h_table, const uint16_t* q, const uint16_t* k,
