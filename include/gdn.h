@@ -353,11 +353,11 @@ int gdn_flag_clear(uint32_t* engaged_flag, gdn_stream_t stream);
  *   o          [total_rows, H_v, d_v] bf16 contiguous
  * Supported: d_k == d_v in {64, 128}, H_v % H_k == 0.
  * Errors: GDN_ERR_NULL (h_table, q, k, v, g, beta or o NULL; a call without
- * sequences or rows may leave theirs out), GDN_ERR_SHAPE (also batch < 0, total_rows < 0, no cu_seqlens with total_rows != batch, or
- * more than 2^31 - 1 CTAs: batch * H_v * d / 32), GDN_ERR_STRIDE,
- * GDN_ERR_ALIGN (q, k, v or o not 16-byte aligned, or qk_stride, v_stride not
- * multiples of 8), GDN_ERR_CUDA.  batch == 0 or total_rows == 0 launches
- * nothing.
+ * sequences or rows may leave theirs out), GDN_ERR_SHAPE (also batch < 0,
+ * total_rows < 0, no cu_seqlens with total_rows != batch, or more than 2^31 - 1
+ * CTAs: batch * H_v * d / 32), GDN_ERR_STRIDE, GDN_ERR_ALIGN (q, k, v or o not
+ * 16-byte aligned, or qk_stride, v_stride not multiples of 8), GDN_ERR_CUDA.
+ * batch == 0 or total_rows == 0 launches nothing.
  * ------------------------------------------------------------------------ */
 int gdn_decode(float* const* h_table, const uint16_t* q, const uint16_t* k, int qk_stride,
                const uint16_t* v, int v_stride, const float* g, const float* beta,

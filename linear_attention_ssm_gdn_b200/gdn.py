@@ -95,6 +95,8 @@ def _switched(device, stream):
         stream = torch.cuda.current_stream(device)
     elif not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
     with torch.cuda.stream(stream):
         yield stream.cuda_stream
 

@@ -1,12 +1,15 @@
 """Host-only checks of gdn_decode, gdn_state_tables and gdn_chunk_backward: their
 guards refuse bad arguments with the named error before anything is launched,
 empty calls succeed, and the binding refuses tensors it cannot pass on."""
+import types
+
 import pytest
 import torch
 
 import linear_attention_ssm_gdn_b200 as gdn
 from linear_attention_ssm_gdn_b200 import _lib
 from linear_attention_ssm_gdn_b200.build import build
+from linear_attention_ssm_gdn_b200.gdn import _switched
 
 P = 0x10000  # fake, aligned device address: never reached behind a refusing guard
 NULL = None
@@ -118,3 +121,10 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         gdn.gdn_chunk_backward(q, q, v, g, g, z(2, dtype=torch.int32), v)
     with pytest.raises(TypeError, match="q"):
         gdn.gdn_chunk_backward(q.float(), q, v, g, g, z(2, dtype=torch.int32), v)
+
+
+def test_a_stream_of_another_device_is_refused():
+    stream = types.SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream"):
+        with _switched(torch.device("cuda", 0), stream):
+            pass
