@@ -1181,7 +1181,9 @@ cudaError_t take_err_backward(uint32_t* out) {
 
 // ---------------------------------------------------------------------------
 // Grads: one CTA per (chunk, key head), the value heads of the group one after
-// another, so that the shared dq and dk are summed in registers, in one order.
+// another, so that the shared dq and dk are summed in registers, in one order.  (A call
+// of few chunks has a CTA per value head instead; the CTAs of a key head are a cluster
+// and sum through each other's shared memory.)
 //
 // All products are transposed, M = 128 rows d_k (or, for P and N, the rows of dO
 // above those of beta E), so that two of them share an MMA where they share an
@@ -1256,7 +1258,7 @@ __device__ __forceinline__ void quads_to_tile(const float4 (&v)[B], int q0, floa
 }
 
 template <int D>
-__global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) {
+__global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a, int heads) {
   using L = GradsSmem<D>;
   constexpr int J = D / 32;         // quads of a row per lane in the row pass
   extern __shared__ uint8_t smem_raw[];
@@ -1267,11 +1269,10 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kGradsBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* err = &g_err_backward;
-  const int i = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, warp = int(warp_id_sync()),
-            lane = tid & 31;
+  const int i = blockIdx.x, tid = threadIdx.x, warp = int(warp_id_sync()), lane = tid & 31;
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
-  const int vpg = a.H_v / a.H_k, h0 = hk * vpg;
+  const int vpg = a.H_v / a.H_k, h0 = blockIdx.y * heads, hk = h0 / vpg;
   if (tid == 0) {
     for (int b = 0; b < kGradsBars; ++b)
       mbar_init(&bars[b], b == gU || b == gP ? kGradsRows / 32 : b == gH || b == gD ? kGradsStates / 32 : 1);
@@ -1316,7 +1317,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     };
     float dqs[32] = {}, dks[32] = {};
     load_head(h0);
-    for (int h = h0; h < h0 + vpg; ++h) {
+    for (int h = h0; h < h0 + heads; ++h) {
       const uint32_t ph = (h - h0) & 1;
       const size_t unit = size_t(i) * a.H_v + h;
       const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (h & 1) * kFac;
@@ -1340,13 +1341,13 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         }
       }
       if (tid < 2) most[tid] = 0;
-      if (tid == 0 && h + 1 < h0 + vpg) {
+      if (tid == 0 && h + 1 < h0 + heads) {
         prefetch_l2(a.u + (unit + 1) * kBC * D, kBC * D * 4);
         prefetch_l2(a.E + (unit + 1) * kBC * D, kBC * D * 4);
       }
       cp_async_wait<0>();  // the factors
       named_sync(1, kGradsRows);
-      if (h + 1 < h0 + vpg) load_head(h + 1);
+      if (h + 1 < h0 + heads) load_head(h + 1);
       // dv, dbeta, v . dv, and the f16 tiles of u and E
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
@@ -1570,22 +1571,43 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       }
       named_sync(1, kGradsRows);  // what was read here is rewritten for the next head
     }
-    if (on) {
+    const size_t out = (size_t(c.row0 + 32 * ch) * a.H_k + hk) * D + dk;
+    const int outs = min(32, c.rows - 32 * ch);
+    if (heads < vpg) {
+      // One head a CTA, the key head's CTAs a cluster: each sums every vpg-th row of all of
+      // them, in the heads' order.  (H has been multiplied: its tiles are free.)
+      float* mine = reinterpret_cast<float*>(smem + L::HH) + ch * D + dk;
+      if (on) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const int rr = 32 * ch + k;
-        if (rr < c.rows) {
-          const size_t at = (size_t(c.row0 + rr) * a.H_k + hk) * D + dk;
-          a.dq[at] = __bfloat16_as_ushort(__float2bfloat16_rn(dqs[k]));
-          a.dk[at] = __bfloat16_as_ushort(__float2bfloat16_rn(dks[k]));
+        for (int k = 0; k < 32; ++k) {
+          mine[4 * k * D] = dqs[k];
+          mine[(4 * k + 2) * D] = dks[k];
         }
       }
+      cluster_sync();
+      for (int k = int(cluster_ctarank()); on && k < outs; k += vpg) {
+        float x = 0.f, y = 0.f;
+        for (int w = 0; w < vpg; ++w) {
+          const uint32_t from = mapa_shared(smem_u32(mine + 4 * k * D), w);
+          x += ld_cluster_f32(from), y += ld_cluster_f32(from + 2 * D * 4);
+        }
+        a.dq[out + size_t(k) * a.H_k * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+        a.dk[out + size_t(k) * a.H_k * D] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+      }
+      cluster_sync();  // the others have read
+    } else if (on) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (k < outs) {
+          a.dq[out + size_t(k) * a.H_k * D] = __bfloat16_as_ushort(__float2bfloat16_rn(dqs[k]));
+          a.dk[out + size_t(k) * a.H_k * D] = __bfloat16_as_ushort(__float2bfloat16_rn(dks[k]));
+        }
     }
   } else if (warp < 12) {
     setmaxnreg_dec<kRegsStates>();
     const int t = tid - kGradsRows;
     constexpr int kQuads = D * D / 4 / kGradsStates;  // 32 or 8 a thread
-    for (int h = h0; h < h0 + vpg; ++h) {
+    for (int h = h0; h < h0 + heads; ++h) {
       const uint32_t ph = (h - h0) & 1;
       const size_t unit = size_t(i) * a.H_v + h;
       const float* H = a.H + (size_t(i + c.seq) * a.H_v + h) * D * D;
@@ -1594,7 +1616,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       if (t == 0) {  // to L2: what is read soon, and the next head's states
         if (h == h0) prefetch_l2(dH, D * D * 4);
         prefetch_l2(H1, D * D * 4);
-        if (h + 1 < h0 + vpg) {
+        if (h + 1 < h0 + heads) {
           prefetch_l2(H + D * D, D * D * 4);
           prefetch_l2(dH + D * D, D * D * 4);
         }
@@ -1648,13 +1670,15 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       if (lane == 0) red[8 * (h & 1) + warp - 8] = hh;
       ready(gD);
     }
+    if (heads < vpg) cluster_sync(), cluster_sync();
   } else {
    setmaxnreg_dec<kRegsIssue>();
    if (warp == 12 && lane == 0) {
     // The issuer; it also loads K, Q and each head's dO.
     // Descriptors: the high word is a constant, the low one an address and the (for the
     // K-major tiles unused) distance of 64-column blocks.
-    const uint32_t b4 = base >> 4;
+    // (In a cluster the address has the CTA's rank above its low 18 bits.)
+    const uint32_t b4 = (base & 0x3ffffu) >> 4;
     constexpr uint32_t kKmaj = 1u << 16, kMnmaj = (8192u >> 4) << 16;
     constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
     auto desc = [&](uint32_t low) { return uint64_t(kHigh) << 32 | low; };
@@ -1681,7 +1705,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     };
     auto rows = [&](uint32_t tile, int kk) { return desc(b4 + (kMnmaj | (tile + kk * 2048) >> 4)); };
     bool ok = true;
-    for (int h = h0; h < h0 + vpg && ok; ++h) {
+    for (int h = h0; h < h0 + heads && ok; ++h) {
       const uint32_t ph = (h - h0) & 1;
       ok = mbar_wait(&bars[gO], ph, abort_flag, err, 128u) &&
            mbar_wait(&bars[gU], ph, abort_flag, err, 128u);
@@ -1734,7 +1758,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA5, rows(L::K, kk), rows(L::N, kk), id_ab, 1u);
       mma_commit(&bars[gA345]);
-      if (h + 1 < h0 + vpg) {  // dO's last reader is done
+      if (h + 1 < h0 + heads) {  // dO's last reader is done
         ok = mbar_wait(&bars[gA12], ph, abort_flag, err, 128u);
         if (!ok) break;
         mbar_arrive_expect_tx(&bars[gO], L::kTile);
@@ -1747,6 +1771,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     mbar_wait(&bars[gO], (loads - 1) & 1, nullptr, err, 32u);
    }
    __syncwarp();
+   if (heads < vpg) cluster_sync(), cluster_sync();
   }
   __syncthreads();
   tc_fence_after();
@@ -1820,8 +1845,20 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   cfg.attrs = &beside;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, bwd_scan_kernel<D, false>, a)) != cudaSuccess) return e;
-  bwd_grads_kernel<D><<<dim3(a.max_chunks, a.H_k), kGradsThreads, grads, s>>>(a);
-  return cudaGetLastError();
+  // Few chunks: one head a CTA, the key head's CTAs joined in clusters, where they all run
+  // at once (one chunk of 48 heads in threes: 68.3 -> 53.9 us a call; 21 chunks of 6 heads:
+  // 109 -> 98).  Where they cannot (clusters of three leave SMs free, so even 24 chunks of 6
+  // heads may need a second wave) they lose: 24 chunks 148 -> 153 us, 47 chunks 253 -> 278.
+  const bool split = vpg > 1 && vpg <= 8 && (long long)a.max_chunks * a.H_v <= a.sms;
+  cudaLaunchAttribute join;
+  join.id = cudaLaunchAttributeClusterDimension;
+  join.val.clusterDim.x = join.val.clusterDim.z = 1;
+  join.val.clusterDim.y = split ? vpg : 1;
+  cfg.gridDim = dim3(a.max_chunks, split ? a.H_v : a.H_k);
+  cfg.blockDim = dim3(kGradsThreads);
+  cfg.dynamicSmemBytes = grads;
+  cfg.attrs = &join;
+  return cudaLaunchKernelEx(&cfg, bwd_grads_kernel<D>, a, split ? 1 : vpg);
 }
 
 }  // namespace
