@@ -1257,8 +1257,8 @@ __device__ __forceinline__ void quads_to_tile(const float4 (&v)[B], int q0, floa
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a, int heads) {
+template <int D, bool split>
+__global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) {
   using L = GradsSmem<D>;
   constexpr int J = D / 32;         // quads of a row per lane in the row pass
   extern __shared__ uint8_t smem_raw[];
@@ -1272,7 +1272,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a, 
   const int i = blockIdx.x, tid = threadIdx.x, warp = int(warp_id_sync()), lane = tid & 31;
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
-  const int vpg = a.H_v / a.H_k, h0 = blockIdx.y * heads, hk = h0 / vpg;
+  const int vpg = a.H_v / a.H_k, heads = split ? 1 : vpg;
+  const int hk = split ? blockIdx.y / vpg : blockIdx.y, h0 = split ? blockIdx.y : hk * vpg;
   if (tid == 0) {
     for (int b = 0; b < kGradsBars; ++b)
       mbar_init(&bars[b], b == gU || b == gP ? kGradsRows / 32 : b == gH || b == gD ? kGradsStates / 32 : 1);
@@ -1571,9 +1572,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a, 
       }
       named_sync(1, kGradsRows);  // what was read here is rewritten for the next head
     }
-    const size_t out = (size_t(c.row0 + 32 * ch) * a.H_k + hk) * D + dk;
-    const int outs = min(32, c.rows - 32 * ch);
-    if (heads < vpg) {
+    if constexpr (split) {
       // One head a CTA, the key head's CTAs a cluster: each sums every vpg-th row of all of
       // them, in the heads' order.  (H has been multiplied: its tiles are free.)
       float* mine = reinterpret_cast<float*>(smem + L::HH) + ch * D + dk;
@@ -1585,23 +1584,27 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a, 
         }
       }
       cluster_sync();
-      for (int k = int(cluster_ctarank()); on && k < outs; k += vpg) {
+      for (int k = int(cluster_ctarank()); on && k < min(32, c.rows - 32 * ch); k += vpg) {
         float x = 0.f, y = 0.f;
         for (int w = 0; w < vpg; ++w) {
           const uint32_t from = mapa_shared(smem_u32(mine + 4 * k * D), w);
           x += ld_cluster_f32(from), y += ld_cluster_f32(from + 2 * D * 4);
         }
-        a.dq[out + size_t(k) * a.H_k * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-        a.dk[out + size_t(k) * a.H_k * D] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+        const size_t at = (size_t(c.row0 + 32 * ch + k) * a.H_k + hk) * D + dk;
+        a.dq[at] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+        a.dk[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
       }
       cluster_sync();  // the others have read
     } else if (on) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (k < outs) {
-          a.dq[out + size_t(k) * a.H_k * D] = __bfloat16_as_ushort(__float2bfloat16_rn(dqs[k]));
-          a.dk[out + size_t(k) * a.H_k * D] = __bfloat16_as_ushort(__float2bfloat16_rn(dks[k]));
+      for (int k = 0; k < 32; ++k) {
+        const int rr = 32 * ch + k;
+        if (rr < c.rows) {
+          const size_t at = (size_t(c.row0 + rr) * a.H_k + hk) * D + dk;
+          a.dq[at] = __bfloat16_as_ushort(__float2bfloat16_rn(dqs[k]));
+          a.dk[at] = __bfloat16_as_ushort(__float2bfloat16_rn(dks[k]));
         }
+      }
     }
   } else if (warp < 12) {
     setmaxnreg_dec<kRegsStates>();
@@ -1670,7 +1673,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a, 
       if (lane == 0) red[8 * (h & 1) + warp - 8] = hh;
       ready(gD);
     }
-    if (heads < vpg) cluster_sync(), cluster_sync();
+    if constexpr (split) cluster_sync(), cluster_sync();
   } else {
    setmaxnreg_dec<kRegsIssue>();
    if (warp == 12 && lane == 0) {
@@ -1771,7 +1774,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a, 
     mbar_wait(&bars[gO], (loads - 1) & 1, nullptr, err, 32u);
    }
    __syncwarp();
-   if (heads < vpg) cluster_sync(), cluster_sync();
+   if constexpr (split) cluster_sync(), cluster_sync();
   }
   __syncthreads();
   tc_fence_after();
@@ -1824,7 +1827,6 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   if ((e = cudaFuncSetAttribute(bwd_prep_kernel<D>, kMax, prep)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D, false>, kMax, fwd)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D, true>, kMax, back)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(bwd_grads_kernel<D>, kMax, grads)) != cudaSuccess) return e;
   // The value heads that share a key head in one CTA (their K K^T and Q K^T are made
   // once), unless that leaves SMs without a CTA: then every head has its own.
   const int vpg = a.H_v / a.H_k;
@@ -1858,7 +1860,9 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(kGradsThreads);
   cfg.dynamicSmemBytes = grads;
   cfg.attrs = &join;
-  return cudaLaunchKernelEx(&cfg, bwd_grads_kernel<D>, a, split ? 1 : vpg);
+  const auto last = split ? bwd_grads_kernel<D, true> : bwd_grads_kernel<D, false>;
+  if ((e = cudaFuncSetAttribute(last, kMax, grads)) != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&cfg, last, a);
 }
 
 }  // namespace
