@@ -418,6 +418,8 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
   __shared__ GateRows gates[2];  // by the head's parity
   __shared__ uint32_t most[5];   // K, Q; by head: dO, M, S
   const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_wait();
+  grid_launch_next();
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
   const int vpg = a.H_v / a.H_k, h0 = blockIdx.y * heads, hk = h0 / vpg;
@@ -791,7 +793,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
   uint32_t* err = &g_err_backward;
   const int tid = threadIdx.x, warp = int(warp_id_sync()), lane = tid & 31;
   const int h = blockIdx.x % a.H_v, order = blockIdx.x / a.H_v, hk = h / (a.H_v / a.H_k);
-  if constexpr (back) asm volatile("griddepcontrol.launch_dependents;");
 
   // Long sequences first: the order-th longest (for up to 64 of them).
   if (tid == 0) {
@@ -802,6 +803,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
   }
   if (warp == 0) tmem_alloc(tmem_slot, 512);
   __syncthreads();
+  if constexpr (back) grid_wait();  // (then the forward scan may start: it need not wait)
+  grid_launch_next();
   if (a.num_seqs <= 64 && tid < a.num_seqs) {
     const int len = a.cu[tid + 1] - a.cu[tid];
     int rank = 0;
@@ -1169,7 +1172,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
   // This grid ends after the other scan's: what follows reads both.
-  if constexpr (!back) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (!back) grid_wait();
 }
 
 cudaError_t take_err_backward(uint32_t* out) {
@@ -1270,8 +1273,6 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* err = &g_err_backward;
   const int i = blockIdx.x, tid = threadIdx.x, warp = int(warp_id_sync()), lane = tid & 31;
-  if (i >= a.cu_chunks[a.num_seqs]) return;
-  const ChunkRows c = chunk_rows(a, i);
   const int vpg = a.H_v / a.H_k, heads = split ? 1 : vpg;
   const int hk = split ? blockIdx.y / vpg : blockIdx.y, h0 = split ? blockIdx.y : hk * vpg;
   if (tid == 0) {
@@ -1280,6 +1281,9 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     *abort_flag = 0;
     fence_barrier_init();
   }
+  grid_wait();
+  if (i >= a.cu_chunks[a.num_seqs]) return;
+  const ChunkRows c = chunk_rows(a, i);
   if (warp == 0) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
@@ -1831,35 +1835,36 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   // once), unless that leaves SMs without a CTA: then every head has its own.
   const int vpg = a.H_v / a.H_k;
   const int heads = (long long)a.max_chunks * a.H_k >= 2 * a.sms ? vpg : 1;
-  bwd_prep_kernel<D><<<dim3(a.max_chunks, a.H_v / heads), 256, prep, s>>>(a, heads);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const unsigned scans = unsigned(a.num_seqs) * a.H_v;
-  bwd_scan_kernel<D, true><<<scans, kScanThreads, back, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchAttribute beside;
-  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  beside.val.programmaticStreamSerializationAllowed = 1;
+  // Each kernel is launched while the one before it ends, and waits for its results itself.
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(scans);
-  cfg.blockDim = dim3(kScanThreads);
-  cfg.dynamicSmemBytes = fwd;
   cfg.stream = s;
-  cfg.attrs = &beside;
+  cfg.attrs = attrs;
   cfg.numAttrs = 1;
+  cfg.gridDim = dim3(a.max_chunks, a.H_v / heads);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = prep;
+  if ((e = cudaLaunchKernelEx(&cfg, bwd_prep_kernel<D>, a, heads)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(unsigned(a.num_seqs) * a.H_v);
+  cfg.blockDim = dim3(kScanThreads);
+  cfg.dynamicSmemBytes = back;
+  if ((e = cudaLaunchKernelEx(&cfg, bwd_scan_kernel<D, true>, a)) != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = fwd;
   if ((e = cudaLaunchKernelEx(&cfg, bwd_scan_kernel<D, false>, a)) != cudaSuccess) return e;
   // Few chunks: one head a CTA, the key head's CTAs joined in clusters, where they all run
   // at once (one chunk of 48 heads in threes: 68.3 -> 53.9 us a call; 21 chunks of 6 heads:
   // 109 -> 98).  Where they cannot (clusters of three leave SMs free, so even 24 chunks of 6
   // heads may need a second wave) they lose: 24 chunks 148 -> 153 us, 47 chunks 253 -> 278.
   const bool split = vpg > 1 && vpg <= 8 && (long long)a.max_chunks * a.H_v <= a.sms;
-  cudaLaunchAttribute join;
-  join.id = cudaLaunchAttributeClusterDimension;
-  join.val.clusterDim.x = join.val.clusterDim.z = 1;
-  join.val.clusterDim.y = split ? vpg : 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = attrs[1].val.clusterDim.z = 1;
+  attrs[1].val.clusterDim.y = vpg;
+  if (split) cfg.numAttrs = 2;
   cfg.gridDim = dim3(a.max_chunks, split ? a.H_v : a.H_k);
   cfg.blockDim = dim3(kGradsThreads);
   cfg.dynamicSmemBytes = grads;
-  cfg.attrs = &join;
   const auto last = split ? bwd_grads_kernel<D, true> : bwd_grads_kernel<D, false>;
   if ((e = cudaFuncSetAttribute(last, kMax, grads)) != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, last, a);

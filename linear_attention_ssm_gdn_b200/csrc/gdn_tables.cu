@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(TablesCall c) {
   __shared__ int32_t slot_of[kTile];
   __shared__ uint32_t sums[2][kTabThreads / 32];
   const int tid = threadIdx.x;
+  grid_launch_next();
   const uint32_t row_top = uint32_t(c.row_capacity) + 1u;
   const uint32_t chunk_top = uint32_t(c.chunk_capacity) + 1u;
   // this CTA's range of map positions
