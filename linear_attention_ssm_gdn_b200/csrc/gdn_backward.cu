@@ -1685,7 +1685,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     // Descriptors: the high word is a constant, the low one an address and the (for the
     // K-major tiles unused) distance of 64-column blocks.
     // (In a cluster the address has the CTA's rank above its low 18 bits.)
-    const uint32_t b4 = (base & 0x3ffffu) >> 4;
+    const uint32_t b4 = (split ? base & 0x3ffffu : base) >> 4;
     constexpr uint32_t kKmaj = 1u << 16, kMnmaj = (8192u >> 4) << 16;
     constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
     auto desc = [&](uint32_t low) { return uint64_t(kHigh) << 32 | low; };
