@@ -391,7 +391,7 @@ def gdn_state_tables(lens, slots=None, pool=None, out=None, total_rows=None, fla
     such a dict to write into, any of its keys left out (a table that is not in
     it is not made); its row and chunk maps may be longer than the step and
     keep what they hold behind it.  Without `out`, total_rows (at least the sum
-    of lens) sizes the maps.  With neither row map, total_rows bounds the
+    of lens) sizes the maps, and the int32 tables are parts of one allocation.  With neither row map, total_rows bounds the
     offsets (default: no bound).  flag: int32 word, GDN_FLAG_ERROR is OR-ed in
     on a bad length or slot or where the maps are too short."""
     n = lens.shape[0]
@@ -418,29 +418,35 @@ def gdn_state_tables(lens, slots=None, pool=None, out=None, total_rows=None, fla
     if out is None:
         if total_rows is None:
             raise ValueError("total_rows sizes the maps where out is not given")
-
-        def ints(m):
-            return torch.empty(m, dtype=torch.int32, device=device)
-        out = {"cu_seqlens": ints(n + 1), "row_seq": ints(total_rows),
-               "cu_chunks": ints(n + 1), "chunk_seq": ints(total_rows // 64 + n)}
-        if slots is not None:
-            out["row_slot"] = ints(total_rows)
-            out["h_table"] = torch.empty(n, dtype=torch.int64, device=device)
-    cu_seqlens, cu_chunks, row_seq, row_slot, chunk_seq, h_table = t = [
-        out.get(x) for x in ("cu_seqlens", "cu_chunks", "row_seq", "row_slot", "chunk_seq",
-                             "h_table")]
-    for x, name in ((cu_seqlens, "cu_seqlens"), (cu_chunks, "cu_chunks")):
-        if x is not None:
-            _expect(x, torch.int32, (n + 1,), name)
-    for x, name in ((row_seq, "row_seq"), (row_slot, "row_slot"), (chunk_seq, "chunk_seq")):
-        if x is not None:
-            _expect(x, torch.int32, (x.shape[0],), name)
-    if (slots is None) != (h_table is None) or (slots is None and row_slot is not None):
-        raise ValueError("h_table belongs to slots and pool, row_slot needs them")
-    if h_table is not None:
-        _expect(h_table, torch.int64, (n,), "h_table")
-    if row_seq is not None and row_slot is not None and row_seq.shape != row_slot.shape:
-        raise ValueError("row_seq and row_slot must have one length")
+        t = ()
+        chunks = total_rows // 64 + n
+        sizes = (n + 1, n + 1, total_rows, chunks, 0 if slots is None else total_rows)
+        cu_seqlens, cu_chunks, row_seq, chunk_seq, row_slot = torch.empty(
+            sum(sizes), dtype=torch.int32, device=device).split(sizes)
+        out = {"cu_seqlens": cu_seqlens, "row_seq": row_seq, "cu_chunks": cu_chunks,
+               "chunk_seq": chunk_seq}
+        h_table = None
+        if slots is None:
+            row_slot = None
+        else:
+            h_table = torch.empty(n, dtype=torch.int64, device=device)
+            out["row_slot"], out["h_table"] = row_slot, h_table
+    else:
+        cu_seqlens, cu_chunks, row_seq, row_slot, chunk_seq, h_table = t = [
+            out.get(x) for x in ("cu_seqlens", "cu_chunks", "row_seq", "row_slot", "chunk_seq",
+                                 "h_table")]
+        for x, name in ((cu_seqlens, "cu_seqlens"), (cu_chunks, "cu_chunks")):
+            if x is not None:
+                _expect(x, torch.int32, (n + 1,), name)
+        for x, name in ((row_seq, "row_seq"), (row_slot, "row_slot"), (chunk_seq, "chunk_seq")):
+            if x is not None:
+                _expect(x, torch.int32, (x.shape[0],), name)
+        if (slots is None) != (h_table is None) or (slots is None and row_slot is not None):
+            raise ValueError("h_table belongs to slots and pool, row_slot needs them")
+        if h_table is not None:
+            _expect(h_table, torch.int64, (n,), "h_table")
+        if row_seq is not None and row_slot is not None and row_seq.shape != row_slot.shape:
+            raise ValueError("row_seq and row_slot must have one length")
     _same_device(device, slots, pool, flag, *t)
     rows = row_slot if row_seq is None else row_seq
     unbounded = 0x7FFFFFFE
