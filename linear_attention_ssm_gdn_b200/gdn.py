@@ -391,9 +391,10 @@ def gdn_state_tables(lens, slots=None, pool=None, out=None, total_rows=None, fla
     such a dict to write into, any of its keys left out (a table that is not in
     it is not made); its row and chunk maps may be longer than the step and
     keep what they hold behind it.  Without `out`, total_rows (at least the sum
-    of lens) sizes the maps, and the int32 tables are parts of one allocation.  With neither row map, total_rows bounds the
-    offsets (default: no bound).  flag: int32 word, GDN_FLAG_ERROR is OR-ed in
-    on a bad length or slot or where the maps are too short."""
+    of lens) sizes the maps, and the int32 tables share one allocation.  With
+    neither row map, total_rows bounds the offsets (default: no bound).  flag:
+    int32 word, GDN_FLAG_ERROR is OR-ed in on a bad length or slot or where the
+    maps are too short."""
     n = lens.shape[0]
     _expect(lens, torch.int32, (n,), "lens")
     device = lens.device
