@@ -64,6 +64,19 @@ def test_shared_key_heads(heads):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads", [(2, 4), (1, 3), (1, 8), (1, 9)])
+@pytest.mark.parametrize("lens", [[1], [33, 0, 2], [64, 65], [700, 1500]])
+def test_value_heads_apart_and_in_turn(lens, heads, d):
+    """Few chunks take a CTA per value head, summed in clusters of up to 8; many, or more
+    value heads a key head, take them in turn."""
+    case = _case(lens, *heads, d, seed=sum(lens) + sum(heads))
+    got = _run(lens, *case, scale=0.5)
+    _check(lens, got, *case, scale=0.5)
+    again = _run(lens, *case, scale=0.5)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_without_states(d):
     lens = [130, 5]
     rows, do, _, _ = _case(lens, 2, 4, d, seed=5)
