@@ -106,6 +106,37 @@ __device__ __forceinline__ ChunkRows chunk_rows(const BwdArgs& a, int i) {
   return c;
 }
 
+// The same without the map, for up to 32 sequences, by a whole warp; *chunks gets the
+// number of chunks.  `write`: this warp writes the map (chunk 0's warp the offsets), which
+// holds what gdn_state_tables would write there.
+constexpr int kFewSeqs = 32;
+__device__ __forceinline__ ChunkRows map_chunk(const BwdArgs& a, int i, bool write, int* chunks) {
+  const int lane = threadIdx.x & 31, n = a.num_seqs;
+  int lo = 0, hi = 0;
+  if (lane < n) lo = a.cu[lane], hi = a.cu[lane + 1];
+  const int own = min(int((unsigned(max(hi - lo, 0)) + kBC - 1) / kBC), a.max_chunks + 1);
+  int end = own;  // (32 times max_chunks stays below 2^31)
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, end, off);
+    if (lane >= off) end += x;
+  }
+  const int first = end - own;
+  *chunks = min(__shfl_sync(0xffffffffu, end, 31), a.max_chunks);
+  ChunkRows c;
+  c.seq = 31 - __clz(__ballot_sync(0xffffffffu, lane < n && first <= i));
+  lo = max(__shfl_sync(0xffffffffu, lo, c.seq), 0);
+  hi = min(__shfl_sync(0xffffffffu, hi, c.seq), a.total_tokens);
+  c.row0 = lo + kBC * (i - __shfl_sync(0xffffffffu, first, c.seq));
+  c.rows = max(0, min(kBC, hi - c.row0));
+  if (write) {
+    if (i == 0 && lane < n) a.cu_chunks[lane] = min(first, a.max_chunks);
+    if (i == 0 && lane == 0) a.cu_chunks[n] = *chunks;
+    if (i < *chunks && lane == 0) a.chunk_seq[i] = c.seq;
+  }
+  return c;
+}
+
 // ---------------------------------------------------------------------------
 // Limbs, fragments, MMAs
 // ---------------------------------------------------------------------------
@@ -421,8 +452,15 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
   const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_wait();
   grid_launch_next();
-  if (i >= a.cu_chunks[a.num_seqs]) return;
-  const ChunkRows c = chunk_rows(a, i);
+  ChunkRows c;
+  if (a.num_seqs <= kFewSeqs) {
+    int chunks;
+    c = map_chunk(a, i, blockIdx.y == 0 && warp == 0, &chunks);
+    if (i >= chunks) return;
+  } else {
+    if (i >= a.cu_chunks[a.num_seqs]) return;
+    c = chunk_rows(a, i);
+  }
   const int vpg = a.H_v / a.H_k, h0 = blockIdx.y * heads, hk = h0 / vpg;
   const uint32_t base = smem_u32(smem);
   const size_t unit0 = size_t(i) * a.H_v;
@@ -1285,7 +1323,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     *abort_flag = 0;
     fence_barrier_init();
   }
-  grid_wait();
+  // The first kernel has completed: the backward scan waited for it before it let the
+  // forward one start, which let this one start.  What the scans write is waited for below.
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
   if (warp == 0) tmem_alloc(tmem_slot, 512);
@@ -1326,6 +1365,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     };
     float dqs[32] = {}, dks[32] = {};
     load_head(h0);
+    grid_wait();
     for (int h = h0; h < h0 + heads; ++h) {
       const uint32_t ph = (h - h0) & 1;
       const size_t unit = size_t(i) * a.H_v + h;
@@ -1618,6 +1658,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     setmaxnreg_dec<kRegsStates>();
     const int t = tid - kGradsRows;
     constexpr int kQuads = D * D / 4 / kGradsStates;  // 32 or 8 a thread
+    grid_wait();
     for (int h = h0; h < h0 + heads; ++h) {
       const uint32_t ph = (h - h0) & 1;
       const size_t unit = size_t(i) * a.H_v + h;
@@ -1846,11 +1887,12 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;
   cfg.attrs = attrs;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.num_seqs <= kFewSeqs ? 0 : 1;  // (the call's first kernel waits for all)
   cfg.gridDim = dim3(a.max_chunks, a.H_v / heads);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = prep;
   if ((e = cudaLaunchKernelEx(&cfg, bwd_prep_kernel<D>, a, heads)) != cudaSuccess) return e;
+  cfg.numAttrs = 1;
   cfg.gridDim = dim3(unsigned(a.num_seqs) * a.H_v);
   cfg.blockDim = dim3(kScanThreads);
   cfg.dynamicSmemBytes = back;
@@ -1893,15 +1935,20 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t s) {
   a.dq = c.dq, a.dk = c.dk, a.dv = c.dv, a.dg = c.dg, a.dbeta = c.dbeta, a.dh0 = c.dh0;
   a.scale = c.scale;
   a.sms = sm_count();
-  TablesCall t = {};
-  t.cu_in = c.cu_seqlens;
-  t.num_seqs = c.num_seqs;
-  t.row_capacity = c.total_tokens;
-  t.cu_chunks = a.cu_chunks;
-  t.chunk_seq = a.chunk_seq;
-  t.chunk_capacity = a.max_chunks;
-  cudaError_t e = launch_tables(t, s);
-  if (e != cudaSuccess) return e;
+  // Up to 32 sequences (a lane each): the first kernel finds its chunks itself, one launch
+  // less.  With the last kernel's early start, 256 rows at d = 64: 45.0 -> 38.6 us a call,
+  // seven sequences of 1100 rows: 92.9 -> 90.1.
+  if (c.num_seqs > kFewSeqs) {
+    TablesCall t = {};
+    t.cu_in = c.cu_seqlens;
+    t.num_seqs = c.num_seqs;
+    t.row_capacity = c.total_tokens;
+    t.cu_chunks = a.cu_chunks;
+    t.chunk_seq = a.chunk_seq;
+    t.chunk_capacity = a.max_chunks;
+    const cudaError_t e = launch_tables(t, s);
+    if (e != cudaSuccess) return e;
+  }
   return c.D == 128 ? run<128>(a, s) : run<64>(a, s);
 }
 
