@@ -1271,7 +1271,7 @@ constexpr int kGradsRows = 256, kGradsStates = 128, kGradsThreads = 512;
 // Registers after re-allocation: 128 (2 x 176 + 112 + 48) is the launch's 512 x 128.
 constexpr uint32_t kRegsRows = 176, kRegsStates = 112, kRegsIssue = 48;
 enum { gO = 0, gU, gH, gP, gD, gPN, gA12, gA345, gA6, gDrain, kGradsBars };
-enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA4 = 256, kTA5 = 320, kTA6 = 384,
+enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA5 = 256, kTA4 = 320, kTA6 = 384,
        kTPN2 = kTA3 };  // P and N's second half over d_v: read before A3 is made
 
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
@@ -1736,6 +1736,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     auto desc = [&](uint32_t low) { return uint64_t(kHigh) << 32 | low; };
     constexpr uint32_t id64 = make_idesc_f16(128, 64, 0, 0), id128 = make_idesc_f16(128, 128, 0, 0);
     constexpr uint32_t id_a = make_idesc_f16(128, 64, 1, 0);   // A MN-major
+    constexpr uint32_t id_a128 = make_idesc_f16(128, 128, 1, 0);
     constexpr uint32_t id_ab = make_idesc_f16(128, 64, 1, 1);  // both MN-major
     auto load_o = [&](int h) {
       const uint8_t* src = a.O + (size_t(i) * a.H_v + h) * L::kTile;
@@ -1794,18 +1795,16 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       ok = mbar_wait(&bars[gP], ph, abort_flag, err, 128u);
       if (!ok) break;
       tc_fence_after();
+      // the low limb of P and N are one tile of 128 rows, A3 and A5 side by side
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA3, rows(L::K, kk), flat(L::PL, kk), id_a, kk != 0);
+        mma_bf16_ss(tmem + kTA3, rows(L::K, kk), flat(L::PL, kk), id_a128, kk != 0);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA3, rows(L::K, kk), flat(L::PH, kk), id_a, 1u);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA4, rows(L::Q, kk), rows(L::PH, kk), id_ab, kk != 0);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA5, rows(L::K, kk), flat(L::N, kk), id_a, kk != 0);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA5, rows(L::K, kk), rows(L::N, kk), id_ab, 1u);
