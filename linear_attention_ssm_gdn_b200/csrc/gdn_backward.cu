@@ -1239,7 +1239,7 @@ cudaError_t take_err_backward(uint32_t* out) {
 // Row factors that differ within a product are applied to its result.
 //   warps 0-7: rows u and E to tiles, the masks of P and N, the sums dq, dk, dg;
 //   warps 8-11: states to tiles and <H', dH'>, as far as a head ahead;
-//   warp 12: one thread loads K, Q, dO and issues the MMAs.
+//   warp 12: one thread loads K, Q, dO and issues the MMAs; warp 13: dg.
 // Bound by the first eight warps' instructions and the latency of the states'
 // loads; the two groups overlap: 305 us at 4576 rows, 48 heads.  (All 16 warps in step
 // took 320 us, 24 warps 345 us, the same products as warp-level MMAs 400 us.)
@@ -1395,7 +1395,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         prefetch_l2(a.E + (unit + 1) * kBC * D, kBC * D * 4);
       }
       cp_async_wait<0>();  // the factors
-      named_sync(1, kGradsRows);
+      named_sync(3, kGradsRows + 32);  // (warp 13 has read the last head's part and vd)
       if (h + 1 < h0 + heads) load_head(h + 1);
       // dv, dbeta, v . dv, and the f16 tiles of u and E
 #pragma unroll
@@ -1572,53 +1572,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         }
       }
       tc_fence_before();
-      named_sync(1, kGradsRows);  // part
-      // dg: suffix sums over the rows, two per lane, on top of <H', dH'>
-      if (warp == 0) {
-        double z[2], run;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int rr = 63 - (2 * lane + k);
-          float sum = 0.f;
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) sum += part[w * kBC + rr];
-          z[k] = rr < c.rows ? double(sum) - double(vd[rr]) : 0.0;
-        }
-        z[1] += z[0];
-        run = z[1];
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const double w = __shfl_up_sync(0xffffffffu, run, off);
-          if (lane >= off) run += w;
-        }
-        double hh = 0.0;
-#pragma unroll
-        for (int w = 0; w < kGradsStates / 32; ++w) hh += red[8 * (h & 1) + w];
-        z[0] += run - z[1] + hh;
-        z[1] = run + hh;
-        // The chunk's first row has a second value, <H, e^{-G} dH> with the entry state:
-        // 0 for a zero state, <h0, dh0> for the sequence's first chunk.  What the sums miss of
-        // it they have gathered over the rows: it is shared out along them.
-        const float* first = a.h0dh0 + (size_t(c.seq) * a.H_v + h) * 8;
-        const bool zero = red[20 + (h & 1)] != 0.f;
-        if (zero || (a.h0 != nullptr && i == a.cu_chunks[c.seq])) {
-          double miss = -__shfl_sync(0xffffffffu, z[1], 31);
-          if (!zero) {
-            for (int w = 0; w < 8; ++w) miss += first[w];
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int rr = 63 - (2 * lane + k);
-            if (rr < c.rows) z[k] += rr == 0 ? miss : miss * double(c.rows - rr) / double(c.rows);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int rr = 63 - (2 * lane + k);
-          if (rr < c.rows) a.dg[size_t(c.row0 + rr) * a.H_v + h] = float(z[k]);
-        }
-      }
-      named_sync(1, kGradsRows);  // what was read here is rewritten for the next head
+      named_sync(2, kGradsRows + 32);  // part is there, with vd: warp 13 sums dg
     }
     if constexpr (split) {
       // One head a CTA, the key head's CTAs a cluster: each sums every vpg-th row of all of
@@ -1820,6 +1774,55 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     mma_commit(&bars[gDrain]);
     mbar_wait(&bars[gDrain], 0, nullptr, err, 32u);
     mbar_wait(&bars[gO], (loads - 1) & 1, nullptr, err, 32u);
+   } else if (warp == 13) {
+    grid_wait();
+    for (int h = h0; h < h0 + heads; ++h) {
+      named_sync(3, kGradsRows + 32);
+      named_sync(2, kGradsRows + 32);
+      // dg: suffix sums over the rows, two per lane, on top of <H', dH'>
+      double z[2], run;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int rr = 63 - (2 * lane + k);
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) sum += part[w * kBC + rr];
+        z[k] = rr < c.rows ? double(sum) - double(vd[rr]) : 0.0;
+      }
+      z[1] += z[0];
+      run = z[1];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const double w = __shfl_up_sync(0xffffffffu, run, off);
+        if (lane >= off) run += w;
+      }
+      double hh = 0.0;
+#pragma unroll
+      for (int w = 0; w < kGradsStates / 32; ++w) hh += red[8 * (h & 1) + w];
+      z[0] += run - z[1] + hh;
+      z[1] = run + hh;
+      // The chunk's first row has a second value, <H, e^{-G} dH> with the entry state:
+      // 0 for a zero state, <h0, dh0> for the sequence's first chunk.  What the sums miss of
+      // it they have gathered over the rows: it is shared out along them.
+      const float* first = a.h0dh0 + (size_t(c.seq) * a.H_v + h) * 8;
+      const bool zero = red[20 + (h & 1)] != 0.f;
+      if (zero || (a.h0 != nullptr && i == a.cu_chunks[c.seq])) {
+        double miss = -__shfl_sync(0xffffffffu, z[1], 31);
+        if (!zero) {
+          for (int w = 0; w < 8; ++w) miss += first[w];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int rr = 63 - (2 * lane + k);
+          if (rr < c.rows) z[k] += rr == 0 ? miss : miss * double(c.rows - rr) / double(c.rows);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int rr = 63 - (2 * lane + k);
+        if (rr < c.rows) a.dg[size_t(c.row0 + rr) * a.H_v + h] = float(z[k]);
+      }
+    }
    }
    __syncwarp();
    if constexpr (split) cluster_sync(), cluster_sync();
