@@ -1278,11 +1278,11 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-// B quads (float4) of a state into a tall f16 tile (and, with LO, their low limbs
+// B quads (float4, the first of v) of a state into a tall f16 tile (and, with LO, their low limbs
 // into a second one): quad q of the state is thread q's, so a warp loads 512
 // contiguous bytes.
 template <int D, bool LO, int B>
-__device__ __forceinline__ void quads_to_tile(const float4 (&v)[B], int q0, float s, uint32_t hi,
+__device__ __forceinline__ void quads_to_tile(const float4 (&v)[8], int q0, float s, uint32_t hi,
                                               uint32_t lo) {
 #pragma unroll
   for (int m = 0; m < B; ++m) {
@@ -1611,40 +1611,54 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   } else if (warp < 12) {
     setmaxnreg_dec<kRegsStates>();
     const int t = tid - kGradsRows;
+    // Two buffers of quads: while one is worked on, the other one's loads are in flight,
+    // across the heads too.
     constexpr int kQuads = D * D / 4 / kGradsStates;  // 32 or 8 a thread
+    constexpr int kBatch = D / 16;                    // H's, 8 or 4; 4 of dH with 4 of H'
+    const size_t unit = size_t(i) * a.H_v + h0;
+    const float* H = a.H + (size_t(i + c.seq) * a.H_v + h0) * D * D;
+    const float* H1 = H + size_t(a.H_v) * D * D;
+    const float* dH = a.dH + unit * D * D;
+    const float* hm = a.Hmax + unit * 16 + (lane & 15);
+    float4 x[8], y[8];
+    auto load_h = [&](float4 (&v)[8], const float* from, int q) {
+#pragma unroll
+      for (int m = 0; m < kBatch; ++m)
+        v[m] = *reinterpret_cast<const float4*>(from + 4 * (t + (q + m) * kGradsStates));
+    };
+    auto load_d = [&](float4 (&v)[8], int q) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        v[m] = *reinterpret_cast<const float4*>(dH + 4 * (t + (q + m) * kGradsStates));
+        v[4 + m] = *reinterpret_cast<const float4*>(H1 + 4 * (t + (q + m) * kGradsStates));
+      }
+    };
     grid_wait();
-    for (int h = h0; h < h0 + heads; ++h) {
+    float largest = *hm;  // lanes 0-7: |H| of a scan warp's part, 8-15: |dH|
+    load_h(x, H, 0);
+    for (int h = h0; h < h0 + heads; ++h, H += D * D, H1 += D * D, dH += D * D, hm += 16) {
       const uint32_t ph = (h - h0) & 1;
-      const size_t unit = size_t(i) * a.H_v + h;
-      const float* H = a.H + (size_t(i + c.seq) * a.H_v + h) * D * D;
-      const float* H1 = H + size_t(a.H_v) * D * D;
-      const float* dH = a.dH + unit * D * D;
+      const bool more = h + 1 < h0 + heads;
       if (t == 0) {  // to L2: what is read soon, and the next head's states
         if (h == h0) prefetch_l2(dH, D * D * 4);
         prefetch_l2(H1, D * D * 4);
-        if (h + 1 < h0 + heads) {
+        if (more) {
           prefetch_l2(H + D * D, D * D * 4);
           prefetch_l2(dH + D * D, D * D * 4);
         }
       }
-      float sh, sd, ih, id, most;
-      {
-        const float* hm = a.Hmax + unit * 16;
-        const float4 m0 = *reinterpret_cast<const float4*>(hm), m1 = *reinterpret_cast<const float4*>(hm + 4);
-        const float4 n0 = *reinterpret_cast<const float4*>(hm + 8), n1 = *reinterpret_cast<const float4*>(hm + 12);
-        most = max_nan(max_nan(max_nan(m0.x, m0.y), max_nan(m0.z, m0.w)),
-                       max_nan(max_nan(m1.x, m1.y), max_nan(m1.z, m1.w)));
-        sh = pow2_scale(most, &ih);
-        sd = pow2_scale(max_nan(max_nan(max_nan(n0.x, n0.y), max_nan(n0.z, n0.w)),
-                                max_nan(max_nan(n1.x, n1.y), max_nan(n1.z, n1.w))), &id);
-      }
 #pragma unroll
-      for (int q = 0; q < kQuads; q += 16) {
-        constexpr int B = kQuads < 16 ? kQuads : 16;
-        float4 v[B];
+      for (int off = 1; off < 8; off <<= 1)
+        largest = max_nan(largest, __shfl_xor_sync(0xffffffffu, largest, off));
+      float ih, id;
+      const float most = __shfl_sync(0xffffffffu, largest, 0), sh = pow2_scale(most, &ih);
+      const float sd = pow2_scale(__shfl_sync(0xffffffffu, largest, 8), &id);
+      auto tile_h = [&](const float4 (&v)[8], int q) {
+        quads_to_tile<D, true, kBatch>(v, t + q * kGradsStates, sh, base + L::HH, base + L::HL);
+      };
 #pragma unroll
-        for (int m = 0; m < B; ++m)
-          v[m] = *reinterpret_cast<const float4*>(H + 4 * (t + (q + m) * kGradsStates));
+      for (int q = 0; q < kQuads; q += 2 * kBatch) {
+        load_h(y, H, q + kBatch);
         if (q == 0) {
           // Once the last head's H has been multiplied its tiles are free, and so are the
           // scales of the head before it: the rows' warps have begun the last head.
@@ -1654,23 +1668,34 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
             red[20 + (h & 1)] = most == 0.f;
           }
         }
-        quads_to_tile<D, true, B>(v, t + q * kGradsStates, sh, base + L::HH, base + L::HL);
+        tile_h(x, q);
+        if (q + 2 * kBatch < kQuads)
+          load_h(x, H, q + 2 * kBatch);
+        else
+          load_d(x, 0);
+        tile_h(y, q + kBatch);
       }
       ready(gH);
       float hh = 0.f;
+      auto tile_d = [&](const float4 (&v)[8], int q) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          hh += fmaf(v[m].x, v[4 + m].x, v[m].y * v[4 + m].y) +
+                fmaf(v[m].z, v[4 + m].z, v[m].w * v[4 + m].w);
+        quads_to_tile<D, false, 4>(v, t + q * kGradsStates, sd, base + L::DH, 0u);
+      };
 #pragma unroll
       for (int q = 0; q < kQuads; q += 8) {
-        float4 v[8], y[8];
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          v[m] = *reinterpret_cast<const float4*>(dH + 4 * (t + (q + m) * kGradsStates));
-          y[m] = *reinterpret_cast<const float4*>(H1 + 4 * (t + (q + m) * kGradsStates));
-        }
+        load_d(y, q + 4);
         if (q == 0 && h > h0) mbar_wait(&bars[gA6], ph ^ 1, abort_flag, err, 64u);
-#pragma unroll
-        for (int m = 0; m < 8; ++m)
-          hh += fmaf(v[m].x, y[m].x, v[m].y * y[m].y) + fmaf(v[m].z, y[m].z, v[m].w * y[m].w);
-        quads_to_tile<D, false, 8>(v, t + q * kGradsStates, sd, base + L::DH, 0u);
+        tile_d(x, q);
+        if (q + 8 < kQuads) {
+          load_d(x, q + 8);
+        } else if (more) {
+          largest = hm[16];
+          load_h(x, H + D * D, 0);
+        }
+        tile_d(y, q + 4);
       }
       hh = warp_sum(hh);
       if (lane == 0) red[8 * (h & 1) + warp - 8] = hh;
