@@ -1260,7 +1260,7 @@ struct GradsSmem {
   static constexpr int Fac = N + kBlk;           // two buffers of the unit's factors
   static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
   static constexpr int F = G + 2 * kBC * 8;      // floats from here
-  static constexpr int kFloats = 3 * kBC + 4 * kBC + kBC + 24;
+  static constexpr int kFloats = 11 * kBC + 40;
   static constexpr int Bars = F + kFloats * 4;
   static constexpr int kUsed = Bars + 16 * 8 + 16 + 1024;
   // More than half of an SM's: all of its tensor memory goes to one CTA.
@@ -1270,9 +1270,9 @@ struct GradsSmem {
 constexpr int kGradsRows = 256, kGradsStates = 128, kGradsThreads = 512;
 // Registers after re-allocation: 128 (2 x 176 + 112 + 48) is the launch's 512 x 128.
 constexpr uint32_t kRegsRows = 176, kRegsStates = 112, kRegsIssue = 48;
-enum { gO = 0, gU, gH, gP, gD, gPN, gA12, gA345, gA6, gDrain, kGradsBars };
+enum { gO = 0, gU, gH, gP, gD, gPN, gA12, gA345, gA6, gE, gDrain, kGradsBars };
 enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA5 = 256, kTA4 = 320, kTA6 = 384,
-       kTPN2 = kTA3 };  // P and N's second half over d_v: read before A3 is made
+       kTPN2 = 448 };  // (P and N's second half over d_v)
 
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -1319,7 +1319,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   const int hk = split ? blockIdx.y / vpg : blockIdx.y, h0 = split ? blockIdx.y : hk * vpg;
   if (tid == 0) {
     for (int b = 0; b < kGradsBars; ++b)
-      mbar_init(&bars[b], b == gU || b == gP ? kGradsRows / 32 : b == gH || b == gD ? kGradsStates / 32 : 1);
+      mbar_init(&bars[b], b == gU || b == gP || b == gE ? kGradsRows / 32 : b == gH || b == gD ? kGradsStates / 32 : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -1332,12 +1332,13 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  float* invU = reinterpret_cast<float*>(smem + L::F);
-  float* invE = invU + kBC;
-  float* endU = invE + kBC;         // invU e^{G_b - G}
+  float* invU2 = reinterpret_cast<float*>(smem + L::F);  // [2][64], by the head's parity
+  float* invE2 = invU2 + 2 * kBC;   // [2][64]
+  float* endU = invE2 + 2 * kBC;    // invU e^{G_b - G}
   float* part = endU + kBC;         // [4][64] q . dq of each 32 rows d_k
-  float* vd = part + 4 * kBC;       // [64] v . dv
-  float* red = vd + kBC;            // by the head's parity: [2][8] <H', dH'>, [2][2] 1 / scale of H, dH', [2] H = 0
+  float* vd2 = part + 4 * kBC;      // [2][64] v . dv
+  // by the head's number: [4][8] <H', dH'>, [2][2] 1 / scale of H, dH', [4] H = 0
+  float* red = vd2 + 2 * kBC;
   // this warp's part of a tile is written: the issuer may use it
   auto ready = [&](int b) {
     fence_proxy_async_smem();
@@ -1366,164 +1367,185 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     float dqs[32] = {}, dks[32] = {};
     load_head(h0);
     grid_wait();
-    for (int h = h0; h < h0 + heads; ++h) {
+    // Head h's masks, the next head's rows (while h's last products run), then h's results
+    // (while the next head's P and N are multiplied).
+    for (int h = h0 - 1; h < h0 + heads; ++h) {
+      const bool on_head = h >= h0, more = h + 1 < h0 + heads;
       const uint32_t ph = (h - h0) & 1;
-      const size_t unit = size_t(i) * a.H_v + h;
       const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (h & 1) * kFac;
       const float2* Gs = reinterpret_cast<const float2*>(smem + L::G) + (h & 1) * kBC;
-      // Rows 8 w .. 8 w + 7 in two halves, 8 lanes a row, 4 J columns a lane.
-      const int l8 = lane & 7;
-      float4 u[2][J], e[2][J];
-      uint2 vw[2][J];
+      const float *invU = invU2 + kBC * (h & 1), *invE = invE2 + kBC * (h & 1);
+      float ip = 0.f, in = 0.f;
+      if (on_head) {
+        if (tid < 2) most[tid] = 0;
+        named_sync(1, kGradsRows);  // the rows' scales; the last head's factors are free
+        if (more) load_head(h + 1);
+        // P and N: lanes 0-63 are rows of P, 64-127 of N
+        float x[32];
+        mbar_wait(&bars[gPN], ph, abort_flag, err, 64u);
+        tc_fence_after();
+        {
+          float y[32];
+          tmem_ld32(tl + kTPN, x);
+          tmem_ld32(tl + kTPN2, y);
+          tmem_ld_wait();
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int r = 8 * warp + 4 * m + (lane >> 3);
-        const float* up = a.u + unit * kBC * D + r * 32 + 4 * l8;
-        const float* ep = a.E + unit * kBC * D + r * 32 + 4 * l8;
-        const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + h * D + 4 * l8;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          u[m][j] = *reinterpret_cast<const float4*>(up + kBC * 32 * j);
-          e[m][j] = *reinterpret_cast<const float4*>(ep + kBC * 32 * j);
-          vw[m][j] = make_uint2(0u, 0u);
-          if (r < c.rows) vw[m][j] = *reinterpret_cast<const uint2*>(vp + 32 * j);
+          for (int k = 0; k < 32; ++k) x[k] += y[k];
         }
-      }
-      if (tid < 2) most[tid] = 0;
-      if (tid == 0 && h + 1 < h0 + heads) {
-        prefetch_l2(a.u + (unit + 1) * kBC * D, kBC * D * 4);
-        prefetch_l2(a.E + (unit + 1) * kBC * D, kBC * D * 4);
-      }
-      cp_async_wait<0>();  // the factors
-      named_sync(3, kGradsRows + 32);  // (warp 13 has read the last head's part and vd)
-      if (h + 1 < h0 + heads) load_head(h + 1);
-      // dv, dbeta, v . dv, and the f16 tiles of u and E
+        {
+          const bool isn = qd >= 2;
+          const int pr = dk & 63, pb = pr >> 4;
+          const float2 Gr = Gs[pr];
+          const float fr = isn ? -invE[pr] : a.scale * fac[kFinvO];
+          float m = 0.f;
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int r = 8 * warp + 4 * m + (lane >> 3);
-        const float bt = fac[kFbeta + r];
-        float db = 0.f, vs = 0.f, mu = 0.f, me = 0.f;
+          for (int cb = 0; cb < 2; ++cb) {  // 16-column blocks
+            // The decay in two factors, e^{G_r - G_b} e^{G_b - G_s}, split at the last row b of
+            // the column block.  In the diagonal blocks the first one is above 1: where the
+            // block decays by 2^60 or more, each element takes an exponential of its own.
+            const int s0 = 32 * ch + 16 * cb, sb = s0 >> 4;
+            const float2 Gb = Gs[s0 + 15];
+            const bool steep = Gs[s0].x - Gb.x > 60.f;
+            const float fe = pb < sb ? 0.f : fr * expdiff(Gr, Gb);
+            const int last = pb > sb ? 16 : pb < sb ? 0 : pr - s0 + (isn ? 0 : 1);
+            if (pb == sb && steep) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          float4 &x = u[m][j], &y = e[m][j];
-          const uint2 w = vw[m][j];
-          db = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, db))));
-          x.x *= bt, x.y *= bt, x.z *= bt, x.w *= bt;
-          y.x *= bt, y.y *= bt, y.z *= bt, y.w *= bt;
-          vs = fmaf(__uint_as_float(w.x << 16), y.x, vs);
-          vs = fmaf(__uint_as_float(w.x & 0xffff0000u), y.y, vs);
-          vs = fmaf(__uint_as_float(w.y << 16), y.z, vs);
-          vs = fmaf(__uint_as_float(w.y & 0xffff0000u), y.w, vs);
-          mu = max_nan(mu, max_nan(max_nan(fabsf(x.x), fabsf(x.y)), max_nan(fabsf(x.z), fabsf(x.w))));
-          me = max_nan(me, max_nan(max_nan(fabsf(y.x), fabsf(y.y)), max_nan(fabsf(y.z), fabsf(y.w))));
-        }
+              for (int k = 0; k < 16; ++k)
+                x[16 * cb + k] = k < last
+                    ? x[16 * cb + k] * (expdiff(Gr, Gs[s0 + k]) * invU[s0 + k] * fr) : 0.f;
+            } else {
 #pragma unroll
-        for (int off = 1; off < 8; off <<= 1) {
-          db += __shfl_xor_sync(0xffffffffu, db, off);
-          vs += __shfl_xor_sync(0xffffffffu, vs, off);
-          mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
-          me = fmaxf(me, __shfl_xor_sync(0xffffffffu, me, off));
-        }
-        float iu, ie;
-        const float su = pow2_scale(mu, &iu), se = pow2_scale(me, &ie);
-        if (l8 == 0) {
-          if (r < c.rows) a.dbeta[size_t(c.row0 + r) * a.H_v + h] = db;
-          vd[r] = vs;
-          invU[r] = iu, invE[r] = ie;
-          endU[r] = iu * fac[kFend + r];
-        }
-        uint16_t* dv = a.dv + (size_t(c.row0 + r) * a.H_v + h) * D + 4 * l8;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const float4 x = u[m][j], y = e[m][j];
-          if (r < c.rows)
-            *reinterpret_cast<uint2*>(dv + 32 * j) =
-                make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-          const int col = 4 * l8 + 32 * j;
-          const uint32_t at = (col >> 6) * kBlk + sw128_offset(r, (col & 63) * 2);
-          uint32_t p0, p1, q0, q1;
-          split_f16(x.x * su, x.y * su, p0, q0);
-          split_f16(x.z * su, x.w * su, p1, q1);
-          st_shared_v2(base + L::UH + at, p0, p1);
-          st_shared_v2(base + L::UL + at, q0, q1);
-          st_shared_v2(base + L::OE + (col >> 6) * kBlk + kBlk + at, pack_f16(y.x * se, y.y * se),
-                       pack_f16(y.z * se, y.w * se));
-        }
-      }
-      ready(gU);
-      named_sync(1, kGradsRows);  // the rows' scales
-      // P and N: lanes 0-63 are rows of P, 64-127 of N
-      float x[32];
-      mbar_wait(&bars[gPN], ph, abort_flag, err, 64u);
-      tc_fence_after();
-      {
-        float y[32];
-        tmem_ld32(tl + kTPN, x);
-        tmem_ld32(tl + kTPN2, y);
-        tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] += y[k];
-      }
-      float ip, in;
-      {
-        const bool isn = qd >= 2;
-        const int pr = dk & 63, pb = pr >> 4;
-        const float2 Gr = Gs[pr];
-        const float fr = isn ? -invE[pr] : a.scale * fac[kFinvO];
-        float m = 0.f;
-#pragma unroll
-        for (int cb = 0; cb < 2; ++cb) {  // 16-column blocks
-          // The decay in two factors, e^{G_r - G_b} e^{G_b - G_s}, split at the last row b of
-          // the column block.  In the diagonal blocks the first one is above 1: where the
-          // block decays by 2^60 or more, each element takes an exponential of its own.
-          const int s0 = 32 * ch + 16 * cb, sb = s0 >> 4;
-          const float2 Gb = Gs[s0 + 15];
-          const bool steep = Gs[s0].x - Gb.x > 60.f;
-          const float fe = pb < sb ? 0.f : fr * expdiff(Gr, Gb);
-          const int last = pb > sb ? 16 : pb < sb ? 0 : pr - s0 + (isn ? 0 : 1);
-          if (pb == sb && steep) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              x[16 * cb + k] = k < last
-                  ? x[16 * cb + k] * (expdiff(Gr, Gs[s0 + k]) * invU[s0 + k] * fr) : 0.f;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float4 e4 = *reinterpret_cast<const float4*>(endU + s0 + k);
-              float* y = x + 16 * cb + k;
-              y[0] = k < last ? y[0] * (fe * e4.x) : 0.f;
-              y[1] = k + 1 < last ? y[1] * (fe * e4.y) : 0.f;
-              y[2] = k + 2 < last ? y[2] * (fe * e4.z) : 0.f;
-              y[3] = k + 3 < last ? y[3] * (fe * e4.w) : 0.f;
+              for (int k = 0; k < 16; k += 4) {
+                const float4 e4 = *reinterpret_cast<const float4*>(endU + s0 + k);
+                float* y = x + 16 * cb + k;
+                y[0] = k < last ? y[0] * (fe * e4.x) : 0.f;
+                y[1] = k + 1 < last ? y[1] * (fe * e4.y) : 0.f;
+                y[2] = k + 2 < last ? y[2] * (fe * e4.z) : 0.f;
+                y[3] = k + 3 < last ? y[3] * (fe * e4.w) : 0.f;
+              }
             }
           }
-        }
-        m = max_abs_of(x);
-        const uint32_t um = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-        if (lane == 0) atomicMax(&most[isn], um);
-        named_sync(1, kGradsRows);
-        const float sp = pow2_scale(__uint_as_float(most[0]), &ip);
-        const float sn = pow2_scale(__uint_as_float(most[1]), &in);
-        const float sc = isn ? sn : sp;
+          m = max_abs_of(x);
+          const uint32_t um = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+          if (lane == 0) atomicMax(&most[isn], um);
+          named_sync(1, kGradsRows);
+          const float sp = pow2_scale(__uint_as_float(most[0]), &ip);
+          const float sn = pow2_scale(__uint_as_float(most[1]), &in);
+          const float sc = isn ? sn : sp;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t p[4], q[4];
+          for (int k = 0; k < 4; ++k) {
+            uint32_t p[4], q[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            split_f16(x[8 * k + 2 * y] * sc, x[8 * k + 2 * y + 1] * sc, p[y], q[y]);
-          const uint32_t at = sw128_offset(pr, 64 * ch + 16 * k);
-          st_shared_v4(base + (isn ? L::N : L::PH) + at, p[0], p[1], p[2], p[3]);
-          if (!isn) st_shared_v4(base + L::PL + at, q[0], q[1], q[2], q[3]);
+            for (int y = 0; y < 4; ++y)
+              split_f16(x[8 * k + 2 * y] * sc, x[8 * k + 2 * y + 1] * sc, p[y], q[y]);
+            const uint32_t at = sw128_offset(pr, 64 * ch + 16 * k);
+            st_shared_v4(base + (isn ? L::N : L::PH) + at, p[0], p[1], p[2], p[3]);
+            if (!isn) st_shared_v4(base + L::PL + at, q[0], q[1], q[2], q[3]);
+          }
         }
+        ready(gP);
       }
-      ready(gP);
+      if (more) {
+        const int n = h + 1;
+        const size_t unit = size_t(i) * a.H_v + n;
+        const float* fan = reinterpret_cast<const float*>(smem + L::Fac) + (n & 1) * kFac;
+        // Rows 8 w .. 8 w + 7 in two halves, 8 lanes a row, 4 J columns a lane.
+        const int l8 = lane & 7;
+        float4 u[2][J], e[2][J];
+        uint2 vw[2][J];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int r = 8 * warp + 4 * m + (lane >> 3);
+          const float* up = a.u + unit * kBC * D + r * 32 + 4 * l8;
+          const float* ep = a.E + unit * kBC * D + r * 32 + 4 * l8;
+          const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + n * D + 4 * l8;
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            u[m][j] = *reinterpret_cast<const float4*>(up + kBC * 32 * j);
+            e[m][j] = *reinterpret_cast<const float4*>(ep + kBC * 32 * j);
+            vw[m][j] = make_uint2(0u, 0u);
+            if (r < c.rows) vw[m][j] = *reinterpret_cast<const uint2*>(vp + 32 * j);
+          }
+        }
+        if (tid == 0 && n + 1 < h0 + heads) {
+          prefetch_l2(a.u + (unit + 1) * kBC * D, kBC * D * 4);
+          prefetch_l2(a.E + (unit + 1) * kBC * D, kBC * D * 4);
+        }
+        cp_async_wait<0>();  // the factors
+        // Every row warp is here, and warp 13 has read the part and vd of the head before h.
+        if (on_head)
+          named_sync(3, kGradsRows + 32);
+        else
+          named_sync(1, kGradsRows);
+        if (on_head) {  // the products that read u and E are done
+          mbar_wait(&bars[gA12], ph, abort_flag, err, 64u);
+          mbar_wait(&bars[gA6], ph, abort_flag, err, 64u);
+        }
+        // dv, dbeta, v . dv, and the f16 tiles of u and E
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int r = 8 * warp + 4 * m + (lane >> 3);
+          const float bt = fan[kFbeta + r];
+          float db = 0.f, vs = 0.f, mu = 0.f, me = 0.f;
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            float4 &x = u[m][j], &y = e[m][j];
+            const uint2 w = vw[m][j];
+            db = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, db))));
+            x.x *= bt, x.y *= bt, x.z *= bt, x.w *= bt;
+            y.x *= bt, y.y *= bt, y.z *= bt, y.w *= bt;
+            vs = fmaf(__uint_as_float(w.x << 16), y.x, vs);
+            vs = fmaf(__uint_as_float(w.x & 0xffff0000u), y.y, vs);
+            vs = fmaf(__uint_as_float(w.y << 16), y.z, vs);
+            vs = fmaf(__uint_as_float(w.y & 0xffff0000u), y.w, vs);
+            mu = max_nan(mu, max_nan(max_nan(fabsf(x.x), fabsf(x.y)), max_nan(fabsf(x.z), fabsf(x.w))));
+            me = max_nan(me, max_nan(max_nan(fabsf(y.x), fabsf(y.y)), max_nan(fabsf(y.z), fabsf(y.w))));
+          }
+#pragma unroll
+          for (int off = 1; off < 8; off <<= 1) {
+            db += __shfl_xor_sync(0xffffffffu, db, off);
+            vs += __shfl_xor_sync(0xffffffffu, vs, off);
+            mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
+            me = fmaxf(me, __shfl_xor_sync(0xffffffffu, me, off));
+          }
+          float iu, ie;
+          const float su = pow2_scale(mu, &iu), se = pow2_scale(me, &ie);
+          if (l8 == 0) {
+            if (r < c.rows) a.dbeta[size_t(c.row0 + r) * a.H_v + n] = db;
+            vd2[kBC * (n & 1) + r] = vs;
+            invU2[kBC * (n & 1) + r] = iu, invE2[kBC * (n & 1) + r] = ie;
+            endU[r] = iu * fan[kFend + r];
+          }
+          uint16_t* dv = a.dv + (size_t(c.row0 + r) * a.H_v + n) * D + 4 * l8;
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const float4 x = u[m][j], y = e[m][j];
+            if (r < c.rows)
+              *reinterpret_cast<uint2*>(dv + 32 * j) =
+                  make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+            const int col = 4 * l8 + 32 * j;
+            const uint32_t at = (col >> 6) * kBlk + sw128_offset(r, (col & 63) * 2);
+            uint32_t p0, p1, q0, q1;
+            split_f16(x.x * su, x.y * su, p0, q0);
+            split_f16(x.z * su, x.w * su, p1, q1);
+            st_shared_v2(base + L::UH + at, p0, p1);
+            st_shared_v2(base + L::UL + at, q0, q1);
+            st_shared_v2(base + L::OE + (col >> 6) * kBlk + kBlk + at, pack_f16(y.x * se, y.y * se),
+                         pack_f16(y.z * se, y.w * se));
+          }
+        }
+        ready(gU);
+      } else {
+        named_sync(3, kGradsRows + 32);
+      }
+      if (!on_head) continue;
       // dq, q . dq and dk: row d_k of this thread, 2 x 16 chunk rows
       mbar_wait(&bars[gA12], ph, abort_flag, err, 64u);
       mbar_wait(&bars[gA6], ph, abort_flag, err, 64u);
       mbar_wait(&bars[gA345], ph, abort_flag, err, 64u);
       tc_fence_after();
       {
-        const float ih = red[16 + 2 * (h & 1)], id = red[17 + 2 * (h & 1)];  // the states' scales
+        const float ih = red[32 + 2 * (h & 1)], id = red[33 + 2 * (h & 1)];  // the states' scales
         const float f = a.scale * fac[kFinvO] * ih, fp = ip * fac[kFinvK], iq = fac[kFinvQ];
         const float fq = ip * fac[kFinvQ], fn = in * fac[kFinvK];
 #pragma unroll
@@ -1571,7 +1593,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
                 fmaf(x2[k], fn, x3[k] * (fac[kFeT + s0 + k] * (invU[s0 + k] * id)));
         }
       }
-      tc_fence_before();
+      ready(gE);
       named_sync(2, kGradsRows + 32);  // part is there, with vd: warp 13 sums dg
     }
     if constexpr (split) {
@@ -1664,8 +1686,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           // scales of the head before it: the rows' warps have begun the last head.
           if (h > h0) mbar_wait(&bars[gA12], ph ^ 1, abort_flag, err, 64u);
           if (t == 0) {
-            red[16 + 2 * (h & 1)] = ih, red[17 + 2 * (h & 1)] = id;
-            red[20 + (h & 1)] = most == 0.f;
+            red[32 + 2 * (h & 1)] = ih, red[33 + 2 * (h & 1)] = id;
+            red[36 + (h & 3)] = most == 0.f;
           }
         }
         tile_h(x, q);
@@ -1698,7 +1720,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         tile_d(y, q + 4);
       }
       hh = warp_sum(hh);
-      if (lane == 0) red[8 * (h & 1) + warp - 8] = hh;
+      if (lane == 0) red[8 * (h & 3) + warp - 8] = hh;
       ready(gD);
     }
     if constexpr (split) cluster_sync(), cluster_sync();
@@ -1752,6 +1774,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         mma_bf16_ss(tmem + (kk < D / 32 ? kTPN : kTPN2), tall(oe, kk), flat(uh, kk), id64, 1u);
       mma_commit(&bars[gPN]);
       ok = mbar_wait(&bars[gH], ph, abort_flag, err, 128u);
+      // (the rows' warps have read the last head's sums)
+      if (h > h0) ok = mbar_wait(&bars[gE], ph ^ 1, abort_flag, err, 128u) && ok;
       if (!ok) break;
       tc_fence_after();
       // the low limb first, for dO alone; then both, the second half of the columns fresh
@@ -1771,6 +1795,13 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       for (int kk = 0; kk < D / 16; ++kk)
         mma_bf16_ss(tmem + kTA6, tall(L::DH, kk), flat(uh, kk), id64, kk != 0);
       mma_commit(&bars[gA6]);
+      if (h + 1 < h0 + heads) {  // dO's last reader is done
+        ok = mbar_wait(&bars[gA12], ph, abort_flag, err, 128u);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&bars[gO], L::kTile);
+        load_o(h + 1);
+        ++loads;
+      }
       ok = mbar_wait(&bars[gP], ph, abort_flag, err, 128u);
       if (!ok) break;
       tc_fence_after();
@@ -1788,13 +1819,6 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA5, rows(L::K, kk), rows(L::N, kk), id_ab, 1u);
       mma_commit(&bars[gA345]);
-      if (h + 1 < h0 + heads) {  // dO's last reader is done
-        ok = mbar_wait(&bars[gA12], ph, abort_flag, err, 128u);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&bars[gO], L::kTile);
-        load_o(h + 1);
-        ++loads;
-      }
     }
     mma_commit(&bars[gDrain]);
     mbar_wait(&bars[gDrain], 0, nullptr, err, 32u);
@@ -1812,7 +1836,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) sum += part[w * kBC + rr];
-        z[k] = rr < c.rows ? double(sum) - double(vd[rr]) : 0.0;
+        z[k] = rr < c.rows ? double(sum) - double(vd2[kBC * (h & 1) + rr]) : 0.0;
       }
       z[1] += z[0];
       run = z[1];
@@ -1823,14 +1847,14 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       }
       double hh = 0.0;
 #pragma unroll
-      for (int w = 0; w < kGradsStates / 32; ++w) hh += red[8 * (h & 1) + w];
+      for (int w = 0; w < kGradsStates / 32; ++w) hh += red[8 * (h & 3) + w];
       z[0] += run - z[1] + hh;
       z[1] = run + hh;
       // The chunk's first row has a second value, <H, e^{-G} dH> with the entry state:
       // 0 for a zero state, <h0, dh0> for the sequence's first chunk.  What the sums miss of
       // it they have gathered over the rows: it is shared out along them.
       const float* first = a.h0dh0 + (size_t(c.seq) * a.H_v + h) * 8;
-      const bool zero = red[20 + (h & 1)] != 0.f;
+      const bool zero = red[36 + (h & 3)] != 0.f;
       if (zero || (a.h0 != nullptr && i == a.cu_chunks[c.seq])) {
         double miss = -__shfl_sync(0xffffffffu, z[1], 31);
         if (!zero) {
