@@ -1240,9 +1240,14 @@ cudaError_t take_err_backward(uint32_t* out) {
 //   warps 0-7: rows u and E to tiles, the masks of P and N, the sums dq, dk, dg;
 //   warps 8-11: states to tiles and <H', dH'>, as far as a head ahead;
 //   warp 12: one thread loads K, Q, dO and issues the MMAs; warp 13: dg.
-// Bound by the first eight warps' instructions and the latency of the states'
-// loads; the two groups overlap: 305 us at 4576 rows, 48 heads.  (All 16 warps in step
-// took 320 us, 24 warps 345 us, the same products as warp-level MMAs 400 us.)
+// A head's rows are staged while the products of the head before it run, and its P and N
+// are multiplied while those warps sum that head's dq and dk.
+// Bound by the latency of the states' loads: 287 us at 4576 rows, 48 heads, 220 if a
+// head's states came for nothing.  Two batches of them are in flight or at work (one at a
+// time: 305 us; four smaller ones 300, single quads 345: a wait for one load is a wait for
+// those issued with it), and they pass by the L1 cache, of which the shared memory leaves
+// some 20 KB (through it: 296 us).  (All 16 warps in step took 320 us, 24 warps 345 us, the
+// same products as warp-level MMAs 400 us.)
 // P and N have two accumulators, a half of d_v each, summed with rounding: the tensor
 // cores' accumulation truncates, and dg sums what it loses over the rows.
 // ---------------------------------------------------------------------------
@@ -1461,8 +1466,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + n * D + 4 * l8;
 #pragma unroll
           for (int j = 0; j < J; ++j) {
-            u[m][j] = *reinterpret_cast<const float4*>(up + kBC * 32 * j);
-            e[m][j] = *reinterpret_cast<const float4*>(ep + kBC * 32 * j);
+            u[m][j] = __ldcg(reinterpret_cast<const float4*>(up + kBC * 32 * j));
+            e[m][j] = __ldcg(reinterpret_cast<const float4*>(ep + kBC * 32 * j));
             vw[m][j] = make_uint2(0u, 0u);
             if (r < c.rows) vw[m][j] = *reinterpret_cast<const uint2*>(vp + 32 * j);
           }
@@ -1646,13 +1651,14 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     auto load_h = [&](float4 (&v)[8], const float* from, int q) {
 #pragma unroll
       for (int m = 0; m < kBatch; ++m)
-        v[m] = *reinterpret_cast<const float4*>(from + 4 * (t + (q + m) * kGradsStates));
+        v[m] = __ldcg(reinterpret_cast<const float4*>(from + 4 * (t + (q + m) * kGradsStates)));
     };
     auto load_d = [&](float4 (&v)[8], int q) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        v[m] = *reinterpret_cast<const float4*>(dH + 4 * (t + (q + m) * kGradsStates));
-        v[4 + m] = *reinterpret_cast<const float4*>(H1 + 4 * (t + (q + m) * kGradsStates));
+        const int at = 4 * (t + (q + m) * kGradsStates);
+        v[m] = __ldcg(reinterpret_cast<const float4*>(dH + at));
+        v[4 + m] = __ldcg(reinterpret_cast<const float4*>(H1 + at));
       }
     };
     grid_wait();
