@@ -209,6 +209,47 @@ def test_strided_views_and_rows_behind_the_last_sequence():
     _check(lens, [x[:T] for x in got[:5]] + [got[5]], rows, do, h0, dhT)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [-0.7, 0.0, 1e-20, 3e4])
+def test_scales(scale, d):
+    lens = [70, 3, 130]
+    case = _case(lens, 1, 2, d, seed=24)
+    _check(lens, _run(lens, *case, scale=scale), *case, scale=scale)
+
+
+def test_first_offset_above_zero():
+    """Rows before the first sequence belong to none, as those behind the last."""
+    lens, spare = [70, 0, 33], 9
+    rows, do, h0, dhT = _case(lens, 2, 4, 128, seed=25)
+
+    def padded(x):
+        nan = torch.full((spare, *x.shape[1:]), float("nan"), dtype=x.dtype)
+        return torch.cat([nan, x, nan]).to(DEV)
+
+    cu = torch.tensor([spare + x for x in R.offsets(lens)], dtype=torch.int32, device=DEV)
+    got = gdn_chunk_backward(*[padded(x) for x in rows], cu, padded(do), h0=h0.to(DEV),
+                             dhT=dhT.to(DEV))
+    _check(lens, [x[spare:-spare] for x in got[:5]] + [got[5]], rows, do, h0, dhT)
+
+
+def test_nan_stays_in_its_sequence():
+    lens = [70, 130, 64]
+    rows, do, h0, dhT = _case(lens, 2, 4, 128, seed=26)
+    want = _run(lens, rows, do, h0, dhT)
+    rows[2][100, 1, 5] = float("nan")
+    got = _run(lens, rows, do, h0, dhT)
+    for x, y in zip(got[:5], want):
+        assert torch.equal(x[:70], y[:70]) and torch.equal(x[200:], y[200:])
+    assert torch.isnan(got[1][70:200]).any()
+
+
+def test_negative_beta():
+    lens = [300]
+    case = _case(lens, 2, 2, 128, seed=27)
+    case[0][4] = case[0][4] * 2 - 1
+    _check(lens, _run(lens, *case), *case)
+
+
 def test_many_chunks_and_the_same_bits_twice():
     lens = [2000, 333]
     case = _case(lens, 2, 4, 128, seed=14)
@@ -216,6 +257,13 @@ def test_many_chunks_and_the_same_bits_twice():
     for x, y in zip(a, b):
         assert torch.equal(x, y)
     _check(lens, a, *case)
+
+
+@pytest.mark.parametrize("n", [32, 33, 64, 65])
+def test_numbers_of_sequences(n):
+    lens = [(7 * i * i) % 150 for i in range(n)]
+    case = _case(lens, 1, 3, 64, seed=n)
+    _check(lens, _run(lens, *case), *case)
 
 
 def test_many_sequences():
