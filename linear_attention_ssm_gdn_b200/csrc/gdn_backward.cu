@@ -728,10 +728,9 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
 }
 
 // ---------------------------------------------------------------------------
-// Scans: one CTA per (sequence, value head, direction); the two directions are two
-// kernels that run at the same time (programmatic dependent launch, the backward
-// one, with the longer chain, first): 283 us for both at 4576 rows, 48 heads, 3.9 us a
-// chunk.
+// Scans: one CTA per (sequence, value head, direction), both directions in one launch
+// (the backward one, with the longer chain, first): about 330 us at 4576 rows, 48 heads,
+// 4.6 us a chunk.
 //
 // H^T [dv][dk] is held by 8 state warps, thread (dv, half of d_k), 64 f32
 // registers at D = 128.  Per chunk three products, M = 128 (dv), A from tensor
@@ -819,8 +818,9 @@ __device__ __forceinline__ float max_abs_of(const float (&x)[N]) {
   return max_nan(m0, m1);
 }
 
+// The CTA `at` of one direction.
 template <int D, bool back>
-__global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
+__device__ __forceinline__ void scan(const BwdArgs& a, int at) {
   using L = ScanSmem<D, back>;
   constexpr int NK = D / 2;   // d_k columns of a thread
   extern __shared__ uint8_t smem_raw[];
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* err = &g_err_backward;
   const int tid = threadIdx.x, warp = int(warp_id_sync()), lane = tid & 31;
-  const int h = blockIdx.x % a.H_v, order = blockIdx.x / a.H_v, hk = h / (a.H_v / a.H_k);
+  const int h = at % a.H_v, order = at / a.H_v, hk = h / (a.H_v / a.H_k);
 
   // Long sequences first: the order-th longest (for up to 64 of them).
   if (tid == 0) {
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
   }
   if (warp == 0) tmem_alloc(tmem_slot, 512);
   __syncthreads();
-  if constexpr (back) grid_wait();  // (then the forward scan may start: it need not wait)
+  grid_wait();
   grid_launch_next();
   if (a.num_seqs <= 64 && tid < a.num_seqs) {
     const int len = a.cu[tid + 1] - a.cu[tid];
@@ -935,13 +935,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
 #pragma unroll
         for (int r = 0; r < 32; r += 2) {
           float2 f = *reinterpret_cast<const float2*>(fr + r), v = make_float2(0.f, 0.f);
-          const int at = (32 * hh + r) * D + dv;
+          const int y = (32 * hh + r) * D + dv;
           if (back && on)
-            v = make_float2(reinterpret_cast<const float*>(smem + L::Y)[at],
-                            reinterpret_cast<const float*>(smem + L::Y)[at + D]);
+            v = make_float2(reinterpret_cast<const float*>(smem + L::Y)[y],
+                            reinterpret_cast<const float*>(smem + L::Y)[y + D]);
           if (!back && on)
-            v = make_float2(bf16f(reinterpret_cast<const uint16_t*>(smem + L::Y)[at]),
-                            bf16f(reinterpret_cast<const uint16_t*>(smem + L::Y)[at + D]));
+            v = make_float2(bf16f(reinterpret_cast<const uint16_t*>(smem + L::Y)[y]),
+                            bf16f(reinterpret_cast<const uint16_t*>(smem + L::Y)[y + D]));
           const float2 kh = fma2(make_float2(y0[r], y0[r + 1]), both(i0),
                                  mul2(make_float2(y1[r], y1[r + 1]), both(i1)));
           const float2 d = fma2(f, kh, v);
@@ -1211,8 +1211,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
-  // This grid ends after the other scan's: what follows reads both.
-  if constexpr (!back) grid_wait();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kScanThreads, 1) bwd_scan_kernel(BwdArgs a) {
+  const int half = gridDim.x / 2;
+  if (int(blockIdx.x) < half)
+    scan<D, true>(a, blockIdx.x);
+  else
+    scan<D, false>(a, blockIdx.x - half);
 }
 
 cudaError_t take_err_backward(uint32_t* out) {
@@ -1328,8 +1335,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     *abort_flag = 0;
     fence_barrier_init();
   }
-  // The first kernel has completed: the backward scan waited for it before it let the
-  // forward one start, which let this one start.  What the scans write is waited for below.
+  // Every CTA waits, those without a chunk too: this grid's end is the call's.
+  grid_wait();
   if (i >= a.cu_chunks[a.num_seqs]) return;
   const ChunkRows c = chunk_rows(a, i);
   if (warp == 0) tmem_alloc(tmem_slot, 512);
@@ -1371,7 +1378,6 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     };
     float dqs[32] = {}, dks[32] = {};
     load_head(h0);
-    grid_wait();
     // Head h's masks, the next head's rows (while h's last products run), then h's results
     // (while the next head's P and N are multiplied).
     for (int h = h0 - 1; h < h0 + heads; ++h) {
@@ -1661,7 +1667,6 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         v[4 + m] = __ldcg(reinterpret_cast<const float4*>(H1 + at));
       }
     };
-    grid_wait();
     float largest = *hm;  // lanes 0-7: |H| of a scan warp's part, 8-15: |dH|
     load_h(x, H, 0);
     for (int h = h0; h < h0 + heads; ++h, H += D * D, H1 += D * D, dH += D * D, hm += 16) {
@@ -1830,7 +1835,6 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     mbar_wait(&bars[gDrain], 0, nullptr, err, 32u);
     mbar_wait(&bars[gO], (loads - 1) & 1, nullptr, err, 32u);
    } else if (warp == 13) {
-    grid_wait();
     for (int h = h0; h < h0 + heads; ++h) {
       named_sync(3, kGradsRows + 32);
       named_sync(2, kGradsRows + 32);
@@ -1926,18 +1930,19 @@ size_t layout(BwdArgs* a, char* base, int total_tokens, int num_seqs, int H_k, i
 
 template <int D>
 cudaError_t run(const BwdArgs& a, cudaStream_t s) {
-  constexpr int prep = PrepSmem<D>::kBytes, fwd = ScanSmem<D, false>::kBytes,
-                back = ScanSmem<D, true>::kBytes, grads = GradsSmem<D>::kBytes;
+  constexpr int prep = PrepSmem<D>::kBytes, grads = GradsSmem<D>::kBytes;
+  constexpr int scans = ScanSmem<D, true>::kBytes > ScanSmem<D, false>::kBytes
+                            ? ScanSmem<D, true>::kBytes : ScanSmem<D, false>::kBytes;
   cudaError_t e;
   const auto kMax = cudaFuncAttributeMaxDynamicSharedMemorySize;
   if ((e = cudaFuncSetAttribute(bwd_prep_kernel<D>, kMax, prep)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D, false>, kMax, fwd)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D, true>, kMax, back)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(bwd_scan_kernel<D>, kMax, scans)) != cudaSuccess) return e;
   // The value heads that share a key head in one CTA (their K K^T and Q K^T are made
   // once), unless that leaves SMs without a CTA: then every head has its own.
   const int vpg = a.H_v / a.H_k;
   const int heads = (long long)a.max_chunks * a.H_k >= 2 * a.sms ? vpg : 1;
-  // Each kernel is launched while the one before it ends, and waits for its results itself.
+  // Each kernel is launched while the one before it ends, and all of its CTAs wait for that
+  // one's end themselves, before they read anything.
   cudaLaunchAttribute attrs[2];
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attrs[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1950,12 +1955,10 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   cfg.dynamicSmemBytes = prep;
   if ((e = cudaLaunchKernelEx(&cfg, bwd_prep_kernel<D>, a, heads)) != cudaSuccess) return e;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(unsigned(a.num_seqs) * a.H_v);
+  cfg.gridDim = dim3(2u * a.num_seqs * a.H_v);
   cfg.blockDim = dim3(kScanThreads);
-  cfg.dynamicSmemBytes = back;
-  if ((e = cudaLaunchKernelEx(&cfg, bwd_scan_kernel<D, true>, a)) != cudaSuccess) return e;
-  cfg.dynamicSmemBytes = fwd;
-  if ((e = cudaLaunchKernelEx(&cfg, bwd_scan_kernel<D, false>, a)) != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = scans;
+  if ((e = cudaLaunchKernelEx(&cfg, bwd_scan_kernel<D>, a)) != cudaSuccess) return e;
   // Few chunks: one head a CTA, the key head's CTAs joined in clusters, where they all run
   // at once (one chunk of 48 heads in threes: 68.3 -> 53.9 us a call; 21 chunks of 6 heads:
   // 109 -> 98).  Where they cannot (clusters of three leave SMs free, so even 24 chunks of 6
