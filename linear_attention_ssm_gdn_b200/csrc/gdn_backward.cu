@@ -67,10 +67,12 @@ struct BwdArgs {
   int sms;             // SMs of the device
   uint8_t* KQ;         // [chunk][H_k] f16 tiles of K, then of Q
   uint8_t* O;          // [chunk][H_v] f16 tile of dO
-  uint8_t* GO;         // [chunk][H_v] scale e^G dO, high and low tile
-  uint8_t* S;          // [chunk][H_v] S, high and low block
+  uint8_t* GO;         // [chunk][H_v] scale e^G dO, high and low tile, a scale per column
+  uint8_t* S;          // [chunk][H_v] S below its diagonal blocks, high and low block
   float* Y0;           // [chunk][H_v][64][D] scale (Q K^T * D)^T dO
   float* fac;          // [chunk][H_v][kFac]
+  float* ff;           // [chunk][H_v][kFwdFac] factors and diagonal blocks for the forward scan
+  float* fb;           // [chunk][H_v][kBackFac] ... and for the backward one
   float2* G;           // [chunk][H_v][64] cumulative gates / ln 2, high and low part
   float* u;            // [chunk][H_v][D / 32][64][32]
   float* E;            // [chunk][H_v][D / 32][64][32]
@@ -80,12 +82,25 @@ struct BwdArgs {
   float* h0dh0;        // [sequence][H_v][8] <h0, dh0>, each scan warp's part
 };
 
-// Per-unit factors: of each row e^G, e^{G_C - G}, beta, the products beta
-// e^{G_C - G} and beta e^G, and e^{G_b - G} with b the last row of its 16-row
-// block; then scalars.
-enum { kFeG = 0, kFeT = kBC, kFbeta = 2 * kBC, kFbT = 3 * kBC, kFbG = 4 * kBC,
-       kFend = 5 * kBC, kFeC = 6 * kBC, kFinvK, kFinvQ, kFinvO, kFinvS, kFinvGO };
-constexpr int kFac = 6 * kBC + 8;
+// Per-unit factors for the gradients: of each row e^G, e^{G_C - G}, beta and e^{G_b - G}
+// with b the last row of its 16-row block; then scalars.
+enum { kFeG = 0, kFeT = kBC, kFbeta = 2 * kBC, kFend = 3 * kBC, kFinvK = 4 * kBC, kFinvQ, kFinvO };
+constexpr int kFac = 4 * kBC + 4;
+
+// For a scan: what scales the rows of its three products (kSx: the state times K^T; kSin:
+// X or Y into the product with S; kSw: u or E into the product with K), what scales that
+// with S where it leaves it (kSout: minus the scale of each row and block, see s_out), e^{G_C},
+// and minus the diagonal blocks of S times beta, f32: of block b element (r, s) at
+// 256 b + 16 s + r for the forward scan, 256 b + 16 r + s for the backward one.  The
+// backward scan also has the inverse scales of GO's columns.
+enum { kSx = 0, kSin = kBC, kSw = 2 * kBC, kSout = 3 * kBC, kSeC = 3 * kBC + 96,
+       kSdiag = 3 * kBC + 100, kScol = kSdiag + 1024 };
+constexpr int kFwdFac = kScol, kBackFac = kScol + 128;
+// Where the scale of row i of a product with S is that comes from k-block j: the forward scan's
+// k-block j reaches the rows of the blocks behind it, the backward scan's those before it.
+__host__ __device__ constexpr int s_out(bool back, int j, int i) {
+  return kSout + (back ? 8 * j * (j - 1) + i : j == 0 ? i - 16 : j == 1 ? 48 + i - 32 : 80 + i - 48);
+}
 
 __device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(uint32_t(x) << 16); }
 __device__ __forceinline__ float expdiff(float2 a, float2 b) {
@@ -150,6 +165,11 @@ __device__ __forceinline__ float pow2_scale(float largest, float* inverse) {
   return __uint_as_float((268u - e) << 23);
 }
 
+// 2^e, 0 below the smallest normal number.
+__device__ __forceinline__ float pow2(int e) {
+  return __uint_as_float(uint32_t(min(max(e + 127, 0), 254)) << 23);
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -171,6 +191,26 @@ __device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32
   lo = pack_f16(x, y);
 }
 
+// a and b as three bf16 limbs, 24 bits of any f32: no scale is needed.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&limb)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    limb[i] = pack_bf16(a, b);
+    a -= __uint_as_float(limb[i] << 16), b -= __uint_as_float(limb[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ void mma16_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                           uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                       uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -256,6 +296,15 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // Prep: per (chunk, value head), what neither scan's state enters: the f16
 // tiles of K, Q, dO and e^G dO, the gate factors, Y0 = scale M^T dO and S.
 //
+// A chunk's decays span any range, and what they make small can be all there is: where only
+// the last row has an output gradient, E_s is e^{G_63 - G_s} times something of size 1.  So no
+// scale is shared by elements that a decay sets apart.  M has bf16 limbs, which need no scale.
+// S meets its operands block by block: the diagonal blocks in f32 on the CUDA cores, element
+// (r, s) of block (a, b) below them, e^{G_r - G_s} times something of size 1, as limbs of
+// S 2^-(from_r + to_s) under a scale of the block, where 2^from_r and 2^to_s are e^{G_r - G_a} and
+// e^{G_b - G_s} (a the first row of its block, b the last one of the other) to the nearest power
+// of two.  The scan puts them on its operand or its result, whichever has that row.
+//
 // K K^T and Q K^T are one pass of MMAs each (exact operands).  With L_b the
 // diagonal 16 x 16 blocks of B diag(beta), S by block rows:
 //   S_bj = (I + L_b)^-1 (B_bj - sum over j <= c < b of B_bc (diag(beta) S)_cj).
@@ -304,18 +353,57 @@ struct TileIn {
       if (out != nullptr) *reinterpret_cast<uint4*>(out + at) = make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
-  // f[row] x as two limb tiles.
-  __device__ __forceinline__ void store_limbs(const float* f, float s, uint8_t* out) const {
+  // as it is, to shared memory
+  __device__ __forceinline__ void store_raw(uint32_t tile) const {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const int p = threadIdx.x + 256 * i, r = p / (D / 8), c = 8 * (p % (D / 8));
+      st_shared_v4(tile + (c >> 6) * kBlk + sw128_offset(r, (c & 63) * 2), x[i].x, x[i].y, x[i].z,
+                   x[i].w);
+    }
+  }
+  // The largest finite |f[row] x| of each column into most[D], words that were zero.  (A NaN or
+  // an infinity reaches its own column's results whatever its scale.)
+  __device__ __forceinline__ void largest_of_columns(const float* f, uint32_t* most) const {
+    uint32_t m[8] = {};
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const float fr = f[(threadIdx.x + 256 * i) / (D / 8)];
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = __float_as_uint(__uint_as_float(w[j] << 16) * fr) & 0x7fffffffu;
+        const uint32_t b = __float_as_uint(__uint_as_float(w[j] & 0xffff0000u) * fr) & 0x7fffffffu;
+        m[2 * j] = max(m[2 * j], a < 0x7f800000u ? a : 0u);
+        m[2 * j + 1] = max(m[2 * j + 1], b < 0x7f800000u ? b : 0u);
+      }
+    }
+    // the warp's rows: lanes D / 8 apart have the same columns
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+      for (int off = D / 8; off < 32; off <<= 1)
+        m[j] = max(m[j], __shfl_xor_sync(0xffffffffu, m[j], off));
+      if ((threadIdx.x & 31) < D / 8) atomicMax(&most[8 * (threadIdx.x % (D / 8)) + j], m[j]);
+    }
+  }
+  // f[row] x as two limb tiles, a scale per column.
+  __device__ __forceinline__ void store_limbs(const float* f, const uint32_t* most,
+                                              uint8_t* out) const {
+    const int c = 8 * (threadIdx.x % (D / 8));
+    float s[8], inv;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = pow2_scale(__uint_as_float(most[c + j]), &inv);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int r = (threadIdx.x + 256 * i) / (D / 8);
       const float fr = f[r];
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       uint32_t h[4], l[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        split_f16(__uint_as_float(w[j] << 16) * fr * s,
-                  __uint_as_float(w[j] & 0xffff0000u) * fr * s, h[j], l[j]);
+        split_f16(__uint_as_float(w[j] << 16) * fr * s[2 * j],
+                  __uint_as_float(w[j] & 0xffff0000u) * fr * s[2 * j + 1], h[j], l[j]);
       const uint32_t at = (c >> 6) * kBlk + sw128_offset(r, (c & 63) * 2);
       *reinterpret_cast<uint4*>(out + at) = make_uint4(h[0], h[1], h[2], h[3]);
       *reinterpret_cast<uint4*>(out + D / 64 * kBlk + at) = make_uint4(l[0], l[1], l[2], l[3]);
@@ -329,8 +417,8 @@ template <int D>
 struct PrepSmem {
   static constexpr int kTile = D / 64 * kBlk;
   static constexpr int K = 0, Q = kTile;       // f16 tiles; later dO, then the limbs of S
-  static constexpr int M = 2 * kBlk;           // later, over Q: the limbs of M
-  static constexpr int B = 2 * kTile > 4 * kBlk ? 2 * kTile : 4 * kBlk;
+  static constexpr int M = 2 * kBlk;           // later, over Q: the three limbs of M
+  static constexpr int B = 5 * kBlk;
   static constexpr int S = B + kBC * kBT * 4;
   static constexpr int T = S + kBC * kBT * 4;  // [4][16][20] the diagonal blocks' inverses
   static constexpr int kBytes = T + 4 * 16 * 20 * 4;
@@ -380,18 +468,20 @@ __device__ __forceinline__ void block_product(float (&acc)[2][4], const float* A
     for (int e = 0; e < 4; ++e) acc[n][e] += low[n][e];
 }
 
+constexpr int kFold = 96;  // the largest power of two that moves between S and its operand
+
 // The gates of head h: 64-bit sums, two rows per lane of one warp, into shared memory
 // (gs: largest scale e^G) and the unit's factors.
 struct GateRows {
   float2 G[kBC];
-  float beta[kBC], eG[kBC];  // eG: scale e^G
+  float beta[kBC], eG[kBC];  // eG: scale e^G / scale of Q
   float end[kBC];            // e^{G_b - G}, b the last row of the 16-row block
-  float most;                // the largest |scale e^G|
+  int from[kBC], to[kBC];    // e^{G - G_a}, a the block's first row, and e^{G_b - G}: nearest 2^x
 };
 __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c, size_t unit, int h,
-                                           GateRows* s) {
+                                           float invk, float invq, GateRows* s) {
   const int lane = threadIdx.x & 31;
-  float* fac = a.fac + unit * kFac;
+  float *fac = a.fac + unit * kFac, *ff = a.ff + unit * kFwdFac, *fb = a.fb + unit * kBackFac;
   double x[2];
   float bt[2];
 #pragma unroll
@@ -417,7 +507,7 @@ __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c,
   x[0] += run - x[1];
   x[1] = run;
   const double end = __shfl_sync(0xffffffffu, x[1], lane | 7);
-  float most = 0.f;
+  const double begin = __shfl_sync(0xffffffffu, x[0], lane & 24);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int r = 2 * lane + e;
@@ -426,21 +516,22 @@ __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c,
     s->G[r] = G;
     a.G[unit * kBC + r] = G;
     const float eG = exp2f(G.x + G.y), eT = exp2f(float(total - x[e]));
-    s->eG[r] = a.scale * eG;
-    most = max_nan(most, fabsf(a.scale * eG));
+    s->eG[r] = a.scale * eG * invq;
     s->end[r] = exp2f(float(end - x[e]));
+    s->from[r] = max(-kFold, min(kFold, __float2int_rn(float(x[e] - begin))));
+    s->to[r] = max(-kFold, min(kFold, __float2int_rn(float(end - x[e]))));
     fac[kFend + r] = s->end[r];
     fac[kFeG + r] = eG;
     fac[kFeT + r] = eT;
     fac[kFbeta + r] = bt[e];
-    fac[kFbT + r] = bt[e] * eT;
-    fac[kFbG + r] = bt[e] * eG;
+    ff[kSx + r] = -eG * invk;
+    ff[kSin + r] = bt[e] * pow2(s->to[r]);
+    ff[kSw + r] = bt[e] * eT * invk;
+    fb[kSx + r] = eT * invk;
+    fb[kSin + r] = bt[e] * pow2(s->from[r]);
+    fb[kSw + r] = -bt[e] * eG * invk;
   }
-  most = warp_max(most);
-  if (lane == 0) {
-    fac[kFeC] = exp2f(float(total));
-    s->most = most;
-  }
+  if (lane == 0) ff[kSeC] = fb[kSeC] = exp2f(float(total));
 }
 
 template <int D>
@@ -448,7 +539,8 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
   using L = PrepSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ GateRows gates[2];  // by the head's parity
-  __shared__ uint32_t most[5];   // K, Q; by head: dO, M, S
+  __shared__ uint32_t most[3];   // K, Q; by head: dO
+  __shared__ uint32_t cols[D];   // by head: columns of scale e^G dO / scale of Q
   const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_wait();
   grid_launch_next();
@@ -474,7 +566,6 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
     kt.fetch(a.k + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows);
     qt.fetch(a.q + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows);
     ot.fetch(dout(h0), size_t(a.H_v) * D, c.rows);
-    if (warp == 7) make_gates(a, c, unit0 + h0, h0, &gates[h0 & 1]);
     kt.largest(&most[0]);
     qt.largest(&most[1]);
     __syncthreads();
@@ -483,6 +574,7 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
     qt.store(pow2_scale(__uint_as_float(most[1]), &invq), base + L::Q,
              kq != nullptr ? kq + L::kTile : nullptr);
   }
+  if (warp == 7) make_gates(a, c, unit0 + h0, h0, invk, invq, &gates[h0 & 1]);
   __syncthreads();
   // K K^T and Q K^T, for all the heads: warp = 16 rows, every other 16-column block up
   // to the diagonal
@@ -515,12 +607,14 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
     const size_t unit = unit0 + h;
     const GateRows& gr = gates[h & 1];
     const float* bs = gr.beta;
-    if (tid >= 2 && tid < 5) most[tid] = 0;
+    if (tid == 0) most[2] = 0;
+    if (tid >= 128 && tid < 128 + D) cols[tid - 128] = 0;
     if (tid == 0) tma_store_wait_read<0>();  // the last head's S has left
     __syncthreads();  // the last head's (or K and Q's) shared memory is free
     // B and M
     ot.largest(&most[2]);
-    float big = 0.f, m_[4][4];
+    ot.largest_of_columns(gr.eG, cols);
+    float m_[4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int s0 = 32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2;
@@ -548,37 +642,36 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
               make_float2(s0 < r ? kk_[j][e] * d0 : 0.f, s0 + 1 < r ? kk_[j][e + 1] * d1 : 0.f);
           m_[j][e] = s0 <= r ? qk[j][e] * d0 : 0.f;
           m_[j][e + 1] = s0 + 1 <= r ? qk[j][e + 1] * d1 : 0.f;
-          big = max_nan(big, max_nan(fabsf(m_[j][e]), fabsf(m_[j][e + 1])));
         }
       }
     }
-    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-    if (lane == 0) atomicMax(&most[3], __float_as_uint(big));
     __syncthreads();  // B, the largest values
     // M, dO and scale e^G dO as tiles
-    float invm, invo;
     {
-      const float sc = pow2_scale(__uint_as_float(most[3]), &invm);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (2 * (j >> 1) + par <= rb)
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
-            uint32_t hi, lo;
-            split_f16(m_[j][e] * sc, m_[j][e + 1] * sc, hi, lo);
+            uint32_t limb[3];
+            split_bf16(m_[j][e], m_[j][e + 1], limb);
             const uint32_t at = sw128_offset(16 * rb + g8 + (e >> 1) * 8,
                                              (32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2) * 2);
-            *reinterpret_cast<uint32_t*>(smem + L::M + at) = hi;
-            *reinterpret_cast<uint32_t*>(smem + L::M + kBlk + at) = lo;
+#pragma unroll
+            for (int x = 0; x < 3; ++x)
+              *reinterpret_cast<uint32_t*>(smem + L::M + x * kBlk + at) = limb[x];
           }
-      ot.store(pow2_scale(__uint_as_float(most[2]), &invo), base, a.O + unit * L::kTile);
-      // (scaled for the product of the largest dO and the largest scale e^G)
-      float invgo;
-      const float sg = pow2_scale(__uint_as_float(most[2]) * gr.most, &invgo);
-      ot.store_limbs(gr.eG, sg, a.GO + unit * 2 * L::kTile);
+      float invo, inv;
+      ot.store_raw(base);
+      ot.store(pow2_scale(__uint_as_float(most[2]), &invo), 0, a.O + unit * L::kTile);
+      ot.store_limbs(gr.eG, cols, a.GO + unit * 2 * L::kTile);
+      if (tid < D) {
+        pow2_scale(__uint_as_float(cols[tid]), &inv);
+        a.fb[unit * kBackFac + kScol + tid] = inv;
+      }
       if (tid == 0) {
         float* fac = a.fac + unit * kFac;
-        fac[kFinvK] = invk, fac[kFinvQ] = invq, fac[kFinvO] = invo, fac[kFinvGO] = invgo;
+        fac[kFinvK] = invk, fac[kFinvQ] = invq, fac[kFinvO] = invo;
       }
     }
     __syncthreads();  // M and dO
@@ -656,25 +749,26 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
     } else {
       // Meanwhile Y0 = scale M^T dO: warp = 16 rows s; k-steps from the diagonal
       const int mt = warp & 3;
-      const float f = a.scale * invm * invo;
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         float y[4][4] = {};
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           if (kk >= mt) {
-            uint32_t ah[4], al[4];
-            ldsm4t(ah, piece<true>(base + L::M, 16 * kk, 16 * mt));
-            ldsm4t(al, piece<true>(base + L::M + kBlk, 16 * kk, 16 * mt));
+            uint32_t am[3][4];
+#pragma unroll
+            for (int x = 0; x < 3; ++x)
+              ldsm4t(am[x], piece<true>(base + L::M + x * kBlk, 16 * kk, 16 * mt));
 #pragma unroll
             for (int np = 0; np < 2; ++np) {
               uint32_t bv[4];
               ldsm4t(bv, piece<false>(base, 16 * kk, c0 + 16 * np));
               float p0[4] = {}, p1[4] = {};
-              mma16(p0, al, bv[0], bv[1]);
-              mma16(p1, al, bv[2], bv[3]);
-              mma16(p0, ah, bv[0], bv[1]);
-              mma16(p1, ah, bv[2], bv[3]);
+#pragma unroll
+              for (int x = 2; x >= 0; --x) {
+                mma16_bf16(p0, am[x], bv[0], bv[1]);
+                mma16_bf16(p1, am[x], bv[2], bv[3]);
+              }
 #pragma unroll
               for (int e = 0; e < 4; ++e) y[2 * np][e] += p0[e], y[2 * np + 1][e] += p1[e];
             }
@@ -685,36 +779,71 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
 #pragma unroll
           for (int e = 0; e < 4; e += 2)
             *reinterpret_cast<float2*>(out + (e >> 1) * 8 * D + 8 * n) =
-                make_float2(y[n][e] * f, y[n][e + 1] * f);
+                make_float2(y[n][e] * a.scale, y[n][e + 1] * a.scale);
       }
-      if (warp == 7 && h + 1 < h0 + heads) make_gates(a, c, unit + 1, h + 1, &gates[(h + 1) & 1]);
+      if (warp == 7 && h + 1 < h0 + heads)
+        make_gates(a, c, unit + 1, h + 1, invk, invq, &gates[(h + 1) & 1]);
     }
     __syncthreads();
-    // S as limbs: warp = 16 rows, half of the columns; zeros above the diagonal blocks
-    float2 sv[8];
-    big = 0.f;
+    // S to its places: warp = 16 rows, half of the columns, two blocks
+    float *ff = a.ff + unit * kFwdFac, *fb = a.fb + unit * kBackFac;
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const int r = 16 * rb + g8 + 8 * (m & 1), s = 32 * par + 8 * (m >> 1) + t2;
-      sv[m] = make_float2(0.f, 0.f);
-      if (2 * par + (m >> 2) <= rb) sv[m] = *reinterpret_cast<const float2*>(&S[r * kBT + s]);
-      big = max_nan(big, max_nan(fabsf(sv[m].x), fabsf(sv[m].y)));
-    }
-    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-    if (lane == 0) atomicMax(&most[4], __float_as_uint(big));
-    __syncthreads();
-    {
-      float inv;
-      const float sc = pow2_scale(__uint_as_float(most[4]), &inv);
-      if (tid == 0) a.fac[unit * kFac + kFinvS] = inv;
+    for (int jj = 0; jj < 2; ++jj) {
+      const int cb = 2 * par + jj, s0 = 16 * cb + t2;
+      if (cb == rb) {
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        const int r = 16 * rb + g8 + 8 * (m & 1), s = 32 * par + 8 * (m >> 1) + t2;
-        uint32_t hi, lo;
-        split_f16(sv[m].x * sc, sv[m].y * sc, hi, lo);
-        const uint32_t at = sw128_offset(r, 2 * s);
-        *reinterpret_cast<uint32_t*>(smem + at) = hi;
-        *reinterpret_cast<uint32_t*>(smem + kBlk + at) = lo;
+        for (int m = 0; m < 4; ++m) {
+          const int r = 16 * rb + g8 + 8 * (m & 1), s = s0 + 8 * (m >> 1);
+          const float2 v = *reinterpret_cast<const float2*>(&S[r * kBT + s]);
+          float* f = ff + kSdiag + 256 * rb + (s & 15) * 16 + (r & 15);
+          f[0] = -v.x * bs[s], f[16] = -v.y * bs[s + 1];
+          *reinterpret_cast<float2*>(fb + kSdiag + 256 * rb + (r & 15) * 16 + (s & 15)) =
+              make_float2(-v.x * bs[r], -v.y * bs[r]);
+        }
+      } else if (cb < rb) {
+        float2 v[4];
+        int fold[4][2], most_e = -1 << 20;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int r = 16 * rb + g8 + 8 * (m & 1), s = s0 + 8 * (m >> 1);
+          v[m] = *reinterpret_cast<const float2*>(&S[r * kBT + s]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = e ? v[m].y : v[m].x;
+            const int ex = (__float_as_uint(x) >> 23) & 255;
+            fold[m][e] = gr.from[r] + gr.to[s + e];
+            if (x != 0.f && ex < 255) most_e = max(most_e, ex - fold[m][e]);
+          }
+        }
+        most_e = __reduce_max_sync(0xffffffffu, most_e);
+        if (most_e == -1 << 20) most_e = 127;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int r = 16 * rb + g8 + 8 * (m & 1), s = s0 + 8 * (m >> 1);
+          float x[2] = {v[m].x, v[m].y};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // the largest to [2^14, 2^15); in two steps, none overflows
+            const int up = max(-252, min(252, 141 - most_e - fold[m][e]));
+            x[e] = x[e] * pow2(up >> 1) * pow2(up - (up >> 1));
+          }
+          uint32_t hi, lo;
+          split_f16(x[0], x[1], hi, lo);
+          const uint32_t at = sw128_offset(r, 2 * s);
+          *reinterpret_cast<uint32_t*>(smem + at) = hi;
+          *reinterpret_cast<uint32_t*>(smem + kBlk + at) = lo;
+        }
+        if (lane < 16) {
+          const int r = 16 * rb + lane, s = 16 * cb + lane;
+          ff[s_out(false, cb, r)] = -pow2(most_e - 141 + gr.from[r]);
+          fb[s_out(true, rb, s)] = -pow2(most_e - 141 + gr.to[s]);
+        }
+      } else {  // (read by MMAs whose results are not)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t at = sw128_offset(16 * rb + g8 + 8 * (m & 1), 2 * (s0 + 8 * (m >> 1)));
+          *reinterpret_cast<uint32_t*>(smem + at) = 0;
+          *reinterpret_cast<uint32_t*>(smem + kBlk + at) = 0;
+        }
       }
     }
     fence_proxy_async_smem();
@@ -736,9 +865,9 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
 // registers at D = 128.  Per chunk three products, M = 128 (dv), A from tensor
 // memory (the limbs that the state warps write), B the chunk's tiles:
 //   1. H^T K^T -> X (or Y), 2. (beta X)^T S^T -> u (or S: E), 3. (f u)^T K -> H'.
-// A row's limbs have one scale per half (its thread's own maximum), so no warp
-// waits for another one's maximum: the halves go to accumulators of their own,
-// summed when they are read.  The backward scan also has (scale e^G dO)^T Q, from
+// A row's limbs have one scale per half (its thread's own maximum; for product 2, whose rows
+// decays set apart, per 16 rows), so no warp waits for another one's maximum: the parts go to
+// accumulators of their own, summed when they are read.  The backward scan also has (scale e^G dO)^T Q, from
 // tiles made before, between products 1 and 2.
 //   warps 0-7: state; warp 8: loads (bulk copies into buffers freed by the
 //   products that read them); warp 9: one thread issues the MMAs after the state
@@ -782,22 +911,24 @@ struct ScanSmem {
   static constexpr int kStep = D * 64 + 64, kRun = D / 2 * 64;
   static constexpr int St = GO + (back ? 2 * kTile + (D == 64 ? kBlk : 0) : 0);
   static constexpr int U = St + D / 16 * kStep;
+  static constexpr int kFactors = back ? kBackFac : kFwdFac;
   static constexpr int Fac = U + (D == 64 ? 8 * 4096 : 0);  // two buffers
-  static constexpr int Inv = Fac + 2 * kFac * 4;   // [3][2][128] inverse row scales
-  static constexpr int Bars = Inv + 3 * 2 * 128 * 4;
+  static constexpr int Inv = Fac + 2 * kFactors * 4;   // [8][128] inverse row scales
+  static constexpr int Bars = Inv + 8 * 128 * 4;
   static constexpr int kUsed = Bars + kBars * 8 + 16 + 1024;  // 1024: alignment of the base
   // More than half of an SM's: all of its tensor memory goes to one CTA.
   static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
 };
 
-// N floats times s as limbs: hi to TMEM columns `hi`, lo to `lo` (N / 2 each).
+// N floats as limbs, the first half times s0, the second times s1: hi to TMEM columns `hi`, lo
+// to `lo` (N / 2 each).
 template <int N>
-__device__ __forceinline__ void limbs_to_tmem(const float (&x)[N], float s, uint32_t hi,
+__device__ __forceinline__ void limbs_to_tmem(const float (&x)[N], float s0, float s1, uint32_t hi,
                                               uint32_t lo) {
   uint32_t h[N / 2], l[N / 2];
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) {
-    const float2 y = mul2(make_float2(x[2 * i], x[2 * i + 1]), both(s));
+    const float2 y = mul2(make_float2(x[2 * i], x[2 * i + 1]), both(i < N / 4 ? s0 : s1));
     split_f16(y.x, y.y, h[i], l[i]);
   }
   if constexpr (N == 64) {
@@ -867,8 +998,8 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
     const int hh = warp >> 2, dv = 32 * (warp & 3) + lane;
     const bool on = D == 128 || dv < D;
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);  // this warp's TMEM lanes
-    float* inv_h = reinterpret_cast<float*>(smem + L::Inv);        // [2][128] each
-    float *inv_x = inv_h + 256, *inv_w = inv_x + 256;
+    float* inv_h = reinterpret_cast<float*>(smem + L::Inv);        // [2][128]
+    float *inv_x = inv_h + 256, *inv_w = inv_x + 512;              // [4][128], [2][128]
     const size_t head = (size_t(b) * a.H_v + h) * D * D;
     float st[NK];
     {
@@ -902,14 +1033,14 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
     for (; t < n; ++t) {
       const int i = chunk_of(t);
       const size_t unit = size_t(i) * a.H_v + h;
-      const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (t & 1) * kFac;
+      const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (t & 1) * L::kFactors;
       // 1. the state's limbs
       const float most = max_abs_of(st);
       {
         float inv;
         const float s = pow2_scale(most, &inv);
         inv_h[128 * hh + dv] = inv;
-        limbs_to_tmem(st, s, tl + kTA + NK / 2 * hh, tl + kTA + 64 + NK / 2 * hh);
+        limbs_to_tmem(st, s, s, tl + kTA + NK / 2 * hh, tl + kTA + 64 + NK / 2 * hh);
       }
       tc_fence_before();
       if (!named_all(1, kScanSync, ok)) break;
@@ -929,9 +1060,8 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
         tmem_ld32(tl + kTX0 + 32 * hh, y0);
         tmem_ld32(tl + kTX1 + 32 * hh, y1);
         tmem_ld_wait();
-        const float ik = back ? fac[kFinvK] : -fac[kFinvK];
-        const float i0 = inv_h[dv] * ik, i1 = inv_h[128 + dv] * ik;
-        const float* fr = fac + (back ? kFeT : kFeG) + 32 * hh;
+        const float i0 = inv_h[dv], i1 = inv_h[128 + dv];
+        const float* fr = fac + kSx + 32 * hh;
 #pragma unroll
         for (int r = 0; r < 32; r += 2) {
           float2 f = *reinterpret_cast<const float2*>(fr + r), v = make_float2(0.f, 0.f);
@@ -948,26 +1078,53 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
           x[r] = d.x, x[r + 1] = d.y;
         }
       }
-      {
-        float z[32], inv;
+      {  // into the product with S: a scale of its own for each 16 rows, a k-step
+        float z[32], m[2], inv[2], sc[2];
 #pragma unroll
-        for (int r = 0; r < 32; r += 2) {
-          const float2 d = mul2(make_float2(x[r], x[r + 1]),
-                                *reinterpret_cast<const float2*>(fac + kFbeta + 32 * hh + r));
-          z[r] = d.x, z[r + 1] = d.y;
+        for (int j = 0; j < 2; ++j) {
+          float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+          for (int r = 16 * j; r < 16 * j + 16; r += 2) {
+            const float2 d = mul2(make_float2(x[r], x[r + 1]),
+                                  *reinterpret_cast<const float2*>(fac + kSin + 32 * hh + r));
+            z[r] = d.x, z[r + 1] = d.y;
+            m0 = max_nan(m0, fabsf(d.x)), m1 = max_nan(m1, fabsf(d.y));
+          }
+          m[j] = max_nan(m0, m1);
+          sc[j] = pow2_scale(m[j], &inv[j]);
+          inv_x[128 * (2 * hh + j) + dv] = inv[j];
         }
-        const float s = pow2_scale(max_abs_of(z), &inv);
-        inv_x[128 * hh + dv] = inv;
-        limbs_to_tmem(z, s, tl + kTA + 16 * hh, tl + kTA + 32 + 16 * hh);
+        limbs_to_tmem(z, sc[0], sc[1], tl + kTA + 16 * hh, tl + kTA + 32 + 16 * hh);
       }
       tc_fence_before();
       if (!named_all(1, kScanSync, ok)) break;
       if (tid == 0) mbar_arrive(&bars[bYE]);
-      const float eC = fac[kFeC];
+      // The diagonal blocks' share, while that product runs.  In the order in which no row is
+      // changed that a later one needs.
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float4* w4 = reinterpret_cast<const float4*>(fac + kSdiag + 256 * (2 * hh + j));
+        float* xj = x + 16 * j;
+#pragma unroll
+        for (int gg = 0; gg < 4; ++gg) {
+          const int g = back ? gg : 3 - gg;
+          float2 a0 = make_float2(xj[4 * g], xj[4 * g + 1]);
+          float2 a1 = make_float2(xj[4 * g + 2], xj[4 * g + 3]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (back ? i > 4 * g : i < 4 * g + 3) {
+              const float4 w = w4[4 * i + g];
+              a0 = fma2(make_float2(w.x, w.y), both(xj[i]), a0);
+              a1 = fma2(make_float2(w.z, w.w), both(xj[i]), a1);
+            }
+          xj[4 * g] = a0.x, xj[4 * g + 1] = a0.y, xj[4 * g + 2] = a1.x, xj[4 * g + 3] = a1.y;
+        }
+      }
+      const float eC = fac[kSeC];
       if constexpr (back) {  // e^{G_C} dH' + (scale e^G dO)^T Q
         ok = mbar_wait(&bars[bQ], t & 1, abort_flag, err, 2u) && ok;
         tc_fence_after();
-        const float f = fac[kFinvGO] * fac[kFinvQ];
+        const float f = fac[kScol + (D == 128 ? dv : dv & 63)];
 #pragma unroll
         for (int p = 0; p < NK; p += 32) {
           float y[32];
@@ -981,32 +1138,50 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
           }
         }
       }
-      // 3. u = X - (beta X) S^T, E = Y - (beta Y) S
+      // 3. u = X - (beta X) S^T, E = Y - (beta Y) S: the other blocks' share, by k-block
       ok = mbar_wait(&bars[bS], t & 1, abort_flag, err, 2u) && ok;
       tc_fence_after();
       {
-        float y0[32], y1[32];
-        tmem_ld32(tl + kTX0 + 32 * hh, y0);
-        tmem_ld32(tl + kTX1 + 32 * hh, y1);
-        tmem_ld_wait();
-        const float is = -fac[kFinvS], i0 = inv_x[dv] * is, i1 = inv_x[128 + dv] * is;
-        const float* fr = fac + (back ? kFbG : kFbT) + 32 * hh;
+        // rows i0 .. of this thread's x from k-block j, whose sums begin at column `col`
+        auto add = [&](int j, int row, int col, auto& y) {
+          constexpr int n = sizeof(y) / sizeof(float);
+          if constexpr (n == 32)
+            tmem_ld32(tl + col, y);
+          else
+            tmem_ld16(tl + col, y);
+          tmem_ld_wait();
+          const float inv = inv_x[128 * j + dv];
+          const float* out = fac + s_out(back, j, 32 * hh + row);
+#pragma unroll
+          for (int r = 0; r < n; r += 2) {
+            const float2 f = mul2(both(inv), *reinterpret_cast<const float2*>(out + r));
+            const float2 d = fma2(make_float2(y[r], y[r + 1]), f,
+                                  make_float2(x[row + r], x[row + r + 1]));
+            x[row + r] = d.x, x[row + r + 1] = d.y;
+          }
+        };
+        float y16[16], y32[32];
+        if (back ? hh == 0 : hh == 1) {
+          add(back ? 2 : 0, 0, back ? kTX1 : kTX0 + 16, y32);
+          add(back ? 3 : 1, 0, back ? kTH1 : kTX0 + 48, y32);
+          add(back ? 1 : 2, back ? 0 : 16, back ? kTX0 : kTX0 + 80, y16);
+        } else {
+          add(back ? 3 : 0, back ? 0 : 16, back ? kTH1 + 32 : kTX0, y16);
+        }
+      }
+      {
+        float w[32], inv;
 #pragma unroll
         for (int r = 0; r < 32; r += 2) {
-          const float2 d = fma2(make_float2(y0[r], y0[r + 1]), both(i0),
-                                fma2(make_float2(y1[r], y1[r + 1]), both(i1),
-                                     make_float2(x[r], x[r + 1])));
-          x[r] = d.x, x[r + 1] = d.y;
-          const float2 w = mul2(d, *reinterpret_cast<const float2*>(fr + r));
-          y0[r] = w.x, y0[r + 1] = w.y;
+          const float2 d = mul2(make_float2(x[r], x[r + 1]),
+                                *reinterpret_cast<const float2*>(fac + kSw + 32 * hh + r));
+          w[r] = d.x, w[r + 1] = d.y;
         }
-        float inv;
-        const float s = pow2_scale(max_abs_of(y0), &inv);
+        const float s = pow2_scale(max_abs_of(w), &inv);
         inv_w[128 * hh + dv] = inv;
-        limbs_to_tmem(y0, s, tl + kTA + 64 + 16 * hh, tl + kTA + 96 + 16 * hh);
+        limbs_to_tmem(w, s, s, tl + kTA + 64 + 16 * hh, tl + kTA + 96 + 16 * hh);
       }
       tc_fence_before();
-      const float ik = back ? -fac[kFinvK] : fac[kFinvK];  // (the factors go with K's buffer)
       if (!named_all(1, kScanSync, ok)) break;
       // 4. u or E out, while the product runs; the next state
       if (lane == 0) tma_store_wait_read<0>();
@@ -1024,7 +1199,7 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
           tma_store_commit();
         }
       }
-      const float i0 = inv_w[dv] * ik, i1 = inv_w[128 + dv] * ik;
+      const float i0 = inv_w[dv], i1 = inv_w[128 + dv];
       ok = mbar_wait(&bars[bH], t & 1, abort_flag, err, 2u) && ok;
       tc_fence_after();
 #pragma unroll
@@ -1073,9 +1248,10 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
       if (t >= 2) ok = mbar_wait(&bars[bKE + (t & 1)], ((t >> 1) & 1) ^ 1, abort_flag, err, 4u);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&bars[bKF + (t & 1)], L::kTile + kFac * 4);
+        mbar_arrive_expect_tx(&bars[bKF + (t & 1)], L::kTile + L::kFactors * 4);
         bulk_load_g2s(smem + L::K + (t & 1) * L::kTile, kq, L::kTile, &bars[bKF + (t & 1)]);
-        bulk_load_g2s(smem + L::Fac + (t & 1) * kFac * 4, a.fac + unit * kFac, kFac * 4,
+        bulk_load_g2s(smem + L::Fac + (t & 1) * L::kFactors * 4,
+                      (back ? a.fb : a.ff) + unit * L::kFactors, L::kFactors * 4,
                       &bars[bKF + (t & 1)]);
       }
       tk = t;
@@ -1130,7 +1306,6 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
     const uint64_t kmaj = make_sdesc_sw128(0, 16, 1024);    // K-major operands
     const uint64_t mnmaj = make_sdesc_sw128(0, 8192, 1024);  // MN-major, 64-element blocks apart
     constexpr uint32_t id_x = make_idesc_f16(128, 64, 0, 0);
-    constexpr uint32_t id_s = make_idesc_f16(128, 64, 0, back ? 1 : 0);
     constexpr uint32_t id_h = make_idesc_f16(128, D, 0, 1);
     constexpr uint32_t id_q = make_idesc_f16(128, D, 1, 1);
     for (int t = 0; t < n; ++t) {
@@ -1174,15 +1349,21 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
       if (leader) {
         tc_fence_after();
         const uint32_t s4 = (base + L::S) >> 4;
+        // By k-block j, in sums of their own: the rows of the blocks behind it, or (the tile being
+        // read along its columns, whole) those of all blocks, of which the ones before it count.
         // (x low) S high, (x high) S low, (x high) S high
 #pragma unroll
         for (int q = 0; q < 3; ++q)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_ts(tmem + (kk >> 1 ? kTX1 : kTX0), tmem + kTA + (q == 0 ? 32 : 0) + 8 * kk,
-                        (back ? mnmaj + (s4 + (q == 1 ? kBlk >> 4 : 0) + 128 * kk)
-                              : kmaj + (s4 + (q == 1 ? kBlk >> 4 : 0) + 2 * kk)),
-                        id_s, q != 0 || (kk & 1) != 0);
+          for (int jj = 0; jj < 3; ++jj) {
+            const int j = back ? jj + 1 : jj;
+            const uint32_t to = back ? (j == 1 ? kTX0 : j == 2 ? kTX1 : kTH1)
+                                     : kTX0 + (j == 0 ? 0 : j == 1 ? 48 : 80);
+            const uint32_t at = s4 + (q == 1 ? kBlk >> 4 : 0);
+            mma_bf16_ts(tmem + to, tmem + kTA + (q == 0 ? 32 : 0) + 8 * j,
+                        back ? mnmaj + (at + 128 * j) : kmaj + (at + 128 * (j + 1) + 2 * j),
+                        make_idesc_f16(128, back ? 64 : 48 - 16 * j, 0, back ? 1 : 0), q != 0);
+          }
         mma_commit(&bars[bS]);
         mma_commit(&bars[bSE]);
       }
@@ -1918,6 +2099,8 @@ size_t layout(BwdArgs* a, char* base, int total_tokens, int num_seqs, int H_k, i
   a->S = reinterpret_cast<uint8_t*>(take(units * 2 * kBlk));
   a->Y0 = reinterpret_cast<float*>(take(units * kBC * D * 4));
   a->fac = reinterpret_cast<float*>(take(units * kFac * 4));
+  a->ff = reinterpret_cast<float*>(take(units * kFwdFac * 4));
+  a->fb = reinterpret_cast<float*>(take(units * kBackFac * 4));
   a->G = reinterpret_cast<float2*>(take(units * kBC * 8));
   a->u = reinterpret_cast<float*>(take(units * kBC * D * 4));
   a->E = reinterpret_cast<float*>(take(units * kBC * D * 4));

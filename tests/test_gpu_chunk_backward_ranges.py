@@ -5,7 +5,7 @@ import torch
 import operator_reference as R
 from linear_attention_ssm_gdn_b200 import (debug_device_errors, gdn_chunk_backward,
                                            gdn_chunk_backward_workspace_bytes)
-from test_gpu_chunk_backward import DEV, _case
+from test_gpu_chunk_backward import DEV, NAMES, _case
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,60 @@ def test_a_captured_call_replayed_without_rows():
                 assert torch.equal(x, y)
         else:
             assert torch.equal(copy, dhT)
+
+
+@pytest.mark.parametrize("rise", [20.0, 70.0])
+@pytest.mark.parametrize("fall", [5.0, 120.0, 1e4])
+def test_gates_that_rise_and_then_fall(rise, fall):
+    """A rise within the documented bound, and within the same 16 rows a fall far below where it
+    began: no decay of a pair of rows overflows, though those to the block's end differ by more
+    than f32 holds."""
+    lens, d = [100], 64
+    rows, do, h0, dhT = _case(lens, 1, 2, d, seed=3)
+    rows[3].fill_(-0.01)
+    rows[3][20], rows[3][26] = rise, -fall
+    rows[2][:20] *= 2.0 ** -60  # what the rise enlarges
+    h0 = h0 * 2.0 ** -60
+    dev = [x.to(DEV) for x in rows]
+    cu = torch.tensor([0, 100], dtype=torch.int32, device=DEV)
+    got = gdn_chunk_backward(*dev, cu, do.to(DEV), h0=h0.to(DEV), dhT=dhT.to(DEV))
+    want = R.backward(*dev, lens, do.to(DEV), h0.to(DEV), dhT.to(DEV))
+    for name, x, y in zip(NAMES, got, want):
+        assert torch.isfinite(x).all(), name
+        if name != "dg":
+            assert R.rel(x, y) <= (R.BF16_REL if name in NAMES[:3] else 0) + R.F32_REL, name
+
+
+def _row_errors(x, y):
+    """Of each row (all heads): 2-norm of the difference over that of y."""
+    x, y = x.double().flatten(1), y.flatten(1)
+    return ((x - y).norm(dim=1) / y.norm(dim=1)).max()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gate, rows_", [(-0.3, 64), (-0.5, 64), (-1.0, 64), (-0.3, 200), (-2.0, 40)])
+@pytest.mark.parametrize("what", ["last row", "final state", "first row of v"])
+def test_masked_gradients_behind_strong_decays(what, gate, rows_, d):
+    """All that reaches the chunk's first rows comes through its decays (of e^-19 to e^-80, f32's
+    range is e^-87): every row is as near to its own size as where nothing decays."""
+    lens = [rows_]
+    rows, do, h0, dhT = _case(lens, 1, 2, d, seed=4)
+    rows[3].fill_(gate)
+    rows[3][::5] *= 0.7  # (not the same for all)
+    if what == "final state":
+        do = torch.zeros_like(do)
+    else:
+        do[:-1] = 0
+        dhT = torch.zeros_like(dhT)
+    if what == "first row of v":  # the forward scan's counterpart
+        rows[2][1:] = 0
+        h0 = torch.zeros_like(h0)
+    dev = [x.to(DEV) for x in rows]
+    cu = torch.tensor([0, rows_], dtype=torch.int32, device=DEV)
+    got = gdn_chunk_backward(*dev, cu, do.to(DEV), h0=h0.to(DEV), dhT=dhT.to(DEV))
+    want = R.backward(*dev, lens, do.to(DEV), h0.to(DEV), dhT.to(DEV))
+    errs = {"dv": _row_errors(got[2], want[2]), "dh0": R.rel(got[5], want[5]),
+            "dbeta": R.rel(got[4], want[4])}
+    print(errs)
+    assert errs["dv"] <= R.BF16_REL + R.F32_REL
+    assert errs["dh0"] <= R.F32_REL and errs["dbeta"] <= R.F32_REL
