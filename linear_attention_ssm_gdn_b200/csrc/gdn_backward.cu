@@ -106,6 +106,14 @@ __device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(uint
 __device__ __forceinline__ float expdiff(float2 a, float2 b) {
   return exp2f((a.x - b.x) + (a.y - b.y));
 }
+// The decay e^{G_r - G_s} for s <= r as two factors, e^{G_r - G_b} e^{G_b - G_s} with b the last row
+// of column s's 16-row block, takes one exponential a row and block.  The first factor is above
+// 1 where r comes before b, and the second one where gates rise from s to b, both far out of f32's
+// range for gates that are steep enough: then each pair of rows takes an exponential of its own.
+__device__ __forceinline__ bool steep(float2 Gr, float2 Gb) {
+  const float x = Gr.x - Gb.x;
+  return x > 60.f || x < -100.f;
+}
 
 // The rows of chunk i: sequence, first row, number of rows (0 where the row
 // offsets are inconsistent).
@@ -619,18 +627,14 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
     for (int j = 0; j < 4; ++j) {
       const int s0 = 32 * (j >> 1) + 16 * par + 8 * (j & 1) + t2;
       if (2 * (j >> 1) + par <= rb) {
-        // The decay in two factors, e^{G_r - G_b} e^{G_b - G_s}, split at the last row b of
-        // the column block.  In the diagonal blocks the first one is above 1: where the
-        // block decays by 2^60 or more, each element takes an exponential of its own.
-        const float2 Gb = gr.G[s0 | 15];
-        const bool own = (s0 >> 4) == rb && gr.G[s0 & ~15].x - Gb.x > 60.f;
+        const float2 Gb = gr.G[s0 | 15];  // the decay in two factors, see steep()
         const float2 f = *reinterpret_cast<const float2*>(&gr.end[s0]);
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const int r = 16 * rb + g8 + (e >> 1) * 8;
           const float2 Gr = gr.G[r];
           float d0, d1;
-          if (own) {
+          if (steep(Gr, Gb)) {
             d0 = s0 <= r ? expdiff(Gr, gr.G[s0]) : 0.f;
             d1 = s0 + 1 <= r ? expdiff(Gr, gr.G[s0 + 1]) : 0.f;
           } else {
@@ -1592,15 +1596,11 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           float m = 0.f;
 #pragma unroll
           for (int cb = 0; cb < 2; ++cb) {  // 16-column blocks
-            // The decay in two factors, e^{G_r - G_b} e^{G_b - G_s}, split at the last row b of
-            // the column block.  In the diagonal blocks the first one is above 1: where the
-            // block decays by 2^60 or more, each element takes an exponential of its own.
             const int s0 = 32 * ch + 16 * cb, sb = s0 >> 4;
-            const float2 Gb = Gs[s0 + 15];
-            const bool steep = Gs[s0].x - Gb.x > 60.f;
+            const float2 Gb = Gs[s0 + 15];  // the decay in two factors, see steep()
             const float fe = pb < sb ? 0.f : fr * expdiff(Gr, Gb);
             const int last = pb > sb ? 16 : pb < sb ? 0 : pr - s0 + (isn ? 0 : 1);
-            if (pb == sb && steep) {
+            if (pb >= sb && steep(Gr, Gb)) {
 #pragma unroll
               for (int k = 0; k < 16; ++k)
                 x[16 * cb + k] = k < last

@@ -109,3 +109,27 @@ def test_masked_gradients_behind_strong_decays(what, gate, rows_, d):
     print(errs)
     assert errs["dv"] <= R.BF16_REL + R.F32_REL
     assert errs["dh0"] <= R.F32_REL and errs["dbeta"] <= R.F32_REL
+
+
+@pytest.mark.parametrize("rise, fall, where", [(70.0, 90.0, 26), (70.0, 75.0, 26), (70.0, 110.0, 40)])
+def test_a_rise_and_a_fall_beyond_f32_between_them(rise, fall, where):
+    """From the top of the rise to the end of the fall it is e^-75 to e^-110: what f32 no longer
+    holds (below e^-87) is lost on the way back to the first rows, in any form in 32 bits, but
+    nothing overflows, and the rows from the fall on are right."""
+    lens, d = [100], 64
+    rows, do, h0, dhT = _case(lens, 1, 2, d, seed=5)
+    rows[3].fill_(-0.01)
+    rows[3][20], rows[3][where] = rise, -fall
+    rows[2][:20] *= 2.0 ** -60
+    h0 = h0 * 2.0 ** -60
+    do[:where] = 0
+    dev = [x.to(DEV) for x in rows]
+    cu = torch.tensor([0, 100], dtype=torch.int32, device=DEV)
+    got = gdn_chunk_backward(*dev, cu, do.to(DEV), h0=h0.to(DEV), dhT=dhT.to(DEV))
+    want = R.backward(*dev, lens, do.to(DEV), h0.to(DEV), dhT.to(DEV))
+    for name, x, y in zip(NAMES, got, want):
+        assert torch.isfinite(x).all(), name
+        if name in ("dv", "dbeta"):
+            assert R.rel(x[where:], y[where:]) <= (R.BF16_REL if name == "dv" else 0) + R.F32_REL
+    if fall < 87:
+        assert R.rel(got[5], want[5]) <= R.F32_REL
