@@ -29,8 +29,8 @@
 // that puts the largest value of its row or tile just below 2^15: 22 bits, or
 // 2^-40 of the largest value, whichever is coarser.  bf16 inputs are exact in
 // one limb under such a scale.  exact x f32 takes 2 MMAs, f32 x f32 takes 3
-// (lo x lo is below the f32 rounding).  What reaches only dq or dk, which are
-// rounded to bf16 (2^-9), takes one limb (2^-12).
+// (lo x lo is below the f32 rounding).  Only beta E has a single limb (2^-12) in
+// one product, N.
 //
 // The scans and the gradients run on tcgen05; the first kernel, whose products are
 // small and triangular, on warp-level MMAs.
@@ -1423,14 +1423,14 @@ cudaError_t take_err_backward(uint32_t* out) {
 // All products are transposed, M = 128 rows d_k (or, for P and N, the rows of dO
 // above those of beta E), so that two of them share an MMA where they share an
 // operand:
-//   [P; N]       = [dO; beta E] (beta u)^T           K = d_v, two limbs of u
-//   [A1 | A2]    = H [dO; beta E]^T                  K = d_v, low limb of H for dO only
-//   A3           = P K (two limbs),  A4 = P^T Q,  A5 = N K + N^T K   K = 64
-//   A6           = dH' (beta u)^T                    K = d_v
+//   [P; N]       = [dO; beta E] (beta u)^T           K = d_v
+//   [A1 | A2]    = H [dO; beta E]^T                  K = d_v, by halves
+//   A3           = P K,  A4 = P^T Q,  A5 = N K + N^T K   K = 64
+//   A6           = dH' (beta u)^T                    K = d_v, by halves
 //   dq = scale e^G A1 + A3,  dk = A4 + A5 - e^G A2 + e^{G_C - G} A6.
 // Row factors that differ within a product are applied to its result.
 //   warps 0-7: rows u and E to tiles, the masks of P and N, the sums dq, dk, dg;
-//   warps 8-11: states to tiles and <H', dH'>, as far as a head ahead;
+//   warps 8-11: states to tiles, in two slots, and <H', dH'>;
 //   warp 12: one thread loads K, Q, dO and issues the MMAs; warp 13: dg.
 // A head's rows are staged while the products of the head before it run, and its P and N
 // are multiplied while those warps sum that head's dq and dk.
@@ -1447,14 +1447,14 @@ cudaError_t take_err_backward(uint32_t* out) {
 template <int D>
 struct GradsSmem {
   static constexpr int kTile = D / 64 * kBlk;
-  static constexpr int kTall = 2 * kTile;        // 128 rows
   static constexpr int K = 0, Q = kTile;         // f16 tiles of the chunk
-  static constexpr int OE = 2 * kTile + (D == 64 ? kBlk : 0);  // dO over beta E, 128 rows
-  static constexpr int UH = OE + kTall, UL = UH + kTile;       // beta u, two limbs
-  static constexpr int HH = UL + kTile, HL = HH + kTall;       // H, two limbs
-  static constexpr int DH = HL + kTall;          // dH'
-  static constexpr int PH = DH + kTall, PL = PH + kBlk, N = PL + kBlk;
-  static constexpr int Fac = N + kBlk;           // two buffers of the unit's factors
+  // dO, beta E high and beta E low, for each 64 columns one over the other
+  static constexpr int OE = 2 * kTile + (D == 64 ? kBlk : 0), kOE = 3 * kBlk;
+  static constexpr int UH = OE + D / 64 * kOE, UL = UH + kTile;  // beta u, two limbs
+  // Two slots for 64 columns (d_v) of H or dH' with 128 rows: high limb, low limb
+  static constexpr int H = UL + kTile, kSlot = 4 * kBlk;
+  static constexpr int PL = H + 2 * kSlot, NL = PL + kBlk, PH = NL + kBlk, NH = PH + kBlk;
+  static constexpr int Fac = NH + kBlk;          // two buffers of the unit's factors
   static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
   static constexpr int F = G + 2 * kBC * 8;      // floats from here
   static constexpr int kFloats = 11 * kBC + 40;
@@ -1467,7 +1467,7 @@ struct GradsSmem {
 constexpr int kGradsRows = 256, kGradsStates = 128, kGradsThreads = 512;
 // Registers after re-allocation: 128 (2 x 176 + 112 + 48) is the launch's 512 x 128.
 constexpr uint32_t kRegsRows = 176, kRegsStates = 112, kRegsIssue = 48;
-enum { gO = 0, gU, gH, gP, gD, gPN, gA12, gA345, gA6, gE, gDrain, kGradsBars };
+enum { gO = 0, gU, gFull, gFree = gFull + 2, gP = gFree + 2, gPN, gA12, gA345, gA6, gE, gDrain, kGradsBars };
 enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA5 = 256, kTA4 = 320, kTA6 = 384,
        kTPN2 = 448 };  // (P and N's second half over d_v)
 
@@ -1475,27 +1475,19 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-// B quads (float4, the first of v) of a state into a tall f16 tile (and, with LO, their low limbs
-// into a second one): quad q of the state is thread q's, so a warp loads 512
-// contiguous bytes.
-template <int D, bool LO, int B>
-__device__ __forceinline__ void quads_to_tile(const float4 (&v)[8], int q0, float s, uint32_t hi,
-                                              uint32_t lo) {
+// B quads (float4, the first of v) of 64 columns of a state into a slot's tiles: quad q is thread
+// q's, so a warp loads 512 contiguous bytes.
+template <int D, int B>
+__device__ __forceinline__ void quads_to_slot(const float4 (&v)[8], int q0, float s, uint32_t slot) {
 #pragma unroll
   for (int m = 0; m < B; ++m) {
-    const int x = q0 + m * kGradsStates;  // slice, d_k, quad
-    const int dk = (x >> 2) % D, col = x / (4 * D) * 16 + (x & 3) * 4;
-    const uint32_t to = (col >> 6) * 2 * kBlk + sw128_offset(dk, (col & 63) * 2);
+    const int x = q0 + m * kGradsStates;  // slice of 16 columns, d_k, quad
+    const uint32_t to = slot + sw128_offset((x >> 2) % D, (x / (4 * D) * 16 + (x & 3) * 4) * 2);
     uint32_t h0, h1, l0, l1;
-    if constexpr (LO) {
-      split_f16(v[m].x * s, v[m].y * s, h0, l0);
-      split_f16(v[m].z * s, v[m].w * s, h1, l1);
-      st_shared_v2(lo + to, l0, l1);
-    } else {
-      h0 = pack_f16(v[m].x * s, v[m].y * s);
-      h1 = pack_f16(v[m].z * s, v[m].w * s);
-    }
-    st_shared_v2(hi + to, h0, h1);
+    split_f16(v[m].x * s, v[m].y * s, h0, l0);
+    split_f16(v[m].z * s, v[m].w * s, h1, l1);
+    st_shared_v2(to, h0, h1);
+    st_shared_v2(to + 2 * kBlk, l0, l1);
   }
 }
 
@@ -1516,7 +1508,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   const int hk = split ? blockIdx.y / vpg : blockIdx.y, h0 = split ? blockIdx.y : hk * vpg;
   if (tid == 0) {
     for (int b = 0; b < kGradsBars; ++b)
-      mbar_init(&bars[b], b == gU || b == gP || b == gE ? kGradsRows / 32 : b == gH || b == gD ? kGradsStates / 32 : 1);
+      mbar_init(&bars[b], b == gU || b == gP || b == gE ? kGradsRows / 32 : b == gFull || b == gFull + 1 ? kGradsStates / 32 : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -1631,8 +1623,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
             for (int y = 0; y < 4; ++y)
               split_f16(x[8 * k + 2 * y] * sc, x[8 * k + 2 * y + 1] * sc, p[y], q[y]);
             const uint32_t at = sw128_offset(pr, 64 * ch + 16 * k);
-            st_shared_v4(base + (isn ? L::N : L::PH) + at, p[0], p[1], p[2], p[3]);
-            if (!isn) st_shared_v4(base + L::PL + at, q[0], q[1], q[2], q[3]);
+            st_shared_v4(base + (isn ? L::NH : L::PH) + at, p[0], p[1], p[2], p[3]);
+            st_shared_v4(base + (isn ? L::NL : L::PL) + at, q[0], q[1], q[2], q[3]);
           }
         }
         ready(gP);
@@ -1722,8 +1714,11 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
             split_f16(x.z * su, x.w * su, p1, q1);
             st_shared_v2(base + L::UH + at, p0, p1);
             st_shared_v2(base + L::UL + at, q0, q1);
-            st_shared_v2(base + L::OE + (col >> 6) * kBlk + kBlk + at, pack_f16(y.x * se, y.y * se),
-                         pack_f16(y.z * se, y.w * se));
+            split_f16(y.x * se, y.y * se, p0, q0);
+            split_f16(y.z * se, y.w * se, p1, q1);
+            const uint32_t e_at = base + L::OE + (col >> 6) * (L::kOE - kBlk) + kBlk + at;
+            st_shared_v2(e_at, p0, p1);
+            st_shared_v2(e_at + kBlk, q0, q1);
           }
         }
         ready(gU);
@@ -1790,8 +1785,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     }
     if constexpr (split) {
       // One head a CTA, the key head's CTAs a cluster: each sums every vpg-th row of all of
-      // them, in the heads' order.  (H has been multiplied: its tiles are free.)
-      float* mine = reinterpret_cast<float*>(smem + L::HH) + ch * D + dk;
+      // them, in the heads' order.  (The states have been multiplied: their slots are free.)
+      float* mine = reinterpret_cast<float*>(smem + L::H) + ch * D + dk;
       if (on) {
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
@@ -1827,31 +1822,41 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     const int t = tid - kGradsRows;
     // Two buffers of quads: while one is worked on, the other one's loads are in flight,
     // across the heads too.
-    constexpr int kQuads = D * D / 4 / kGradsStates;  // 32 or 8 a thread
-    constexpr int kBatch = D / 16;                    // H's, 8 or 4; 4 of dH with 4 of H'
+    constexpr int kHalves = D / 64;                   // of d_v
+    constexpr int kQuads = D * 16 / kGradsStates;     // of a half: 16 or 8 a thread
+    constexpr int kBatch = kQuads / 2;                // H's; 4 of dH' with 4 of H'
     const size_t unit = size_t(i) * a.H_v + h0;
     const float* H = a.H + (size_t(i + c.seq) * a.H_v + h0) * D * D;
     const float* H1 = H + size_t(a.H_v) * D * D;
     const float* dH = a.dH + unit * D * D;
     const float* hm = a.Hmax + unit * 16 + (lane & 15);
     float4 x[8], y[8];
-    auto load_h = [&](float4 (&v)[8], const float* from, int q) {
+    auto load_h = [&](float4 (&v)[8], const float* from, int half, int q) {
 #pragma unroll
       for (int m = 0; m < kBatch; ++m)
-        v[m] = __ldcg(reinterpret_cast<const float4*>(from + 4 * (t + (q + m) * kGradsStates)));
+        v[m] = __ldcg(reinterpret_cast<const float4*>(
+            from + half * 64 * D + 4 * (t + (q + m) * kGradsStates)));
     };
-    auto load_d = [&](float4 (&v)[8], int q) {
+    auto load_d = [&](float4 (&v)[8], int half, int q) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const int at = 4 * (t + (q + m) * kGradsStates);
+        const int at = half * 64 * D + 4 * (t + (q + m) * kGradsStates);
         v[m] = __ldcg(reinterpret_cast<const float4*>(dH + at));
         v[4 + m] = __ldcg(reinterpret_cast<const float4*>(H1 + at));
       }
     };
+    int fills = 0;  // slot fills & 1 is next
+    auto slot_free = [&]() {  // what was there has been multiplied
+      if (fills >= 2)
+        mbar_wait(&bars[gFree + (fills & 1)], (fills >> 1 & 1) ^ 1, abort_flag, err, 64u);
+    };
+    auto slot_full = [&]() {
+      ready(gFull + (fills & 1));
+      ++fills;
+    };
     float largest = *hm;  // lanes 0-7: |H| of a scan warp's part, 8-15: |dH|
-    load_h(x, H, 0);
+    load_h(x, H, 0, 0);
     for (int h = h0; h < h0 + heads; ++h, H += D * D, H1 += D * D, dH += D * D, hm += 16) {
-      const uint32_t ph = (h - h0) & 1;
       const bool more = h + 1 < h0 + heads;
       if (t == 0) {  // to L2: what is read soon, and the next head's states
         if (h == h0) prefetch_l2(dH, D * D * 4);
@@ -1867,53 +1872,58 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       float ih, id;
       const float most = __shfl_sync(0xffffffffu, largest, 0), sh = pow2_scale(most, &ih);
       const float sd = pow2_scale(__shfl_sync(0xffffffffu, largest, 8), &id);
-      auto tile_h = [&](const float4 (&v)[8], int q) {
-        quads_to_tile<D, true, kBatch>(v, t + q * kGradsStates, sh, base + L::HH, base + L::HL);
-      };
 #pragma unroll
-      for (int q = 0; q < kQuads; q += 2 * kBatch) {
-        load_h(y, H, q + kBatch);
-        if (q == 0) {
-          // Once the last head's H has been multiplied its tiles are free, and so are the
-          // scales of the head before it: the rows' warps have begun the last head.
-          if (h > h0) mbar_wait(&bars[gA12], ph ^ 1, abort_flag, err, 64u);
-          if (t == 0) {
-            red[32 + 2 * (h & 1)] = ih, red[33 + 2 * (h & 1)] = id;
-            red[36 + (h & 3)] = most == 0.f;
-          }
+      for (int half = 0; half < kHalves; ++half) {
+        const uint32_t slot = base + L::H + (fills & 1) * L::kSlot;
+        load_h(y, H, half, kBatch);
+        slot_free();
+        // (A product of the last head has freed the slot, so the rows' warps are done with the
+        // head before it, whose scales were here.)
+        if (half == 0 && t == 0) {
+          red[32 + 2 * (h & 1)] = ih, red[33 + 2 * (h & 1)] = id;
+          red[36 + (h & 3)] = most == 0.f;
         }
-        tile_h(x, q);
-        if (q + 2 * kBatch < kQuads)
-          load_h(x, H, q + 2 * kBatch);
+        quads_to_slot<D, kBatch>(x, t, sh, slot);
+        if (half + 1 < kHalves)
+          load_h(x, H, half + 1, 0);
         else
-          load_d(x, 0);
-        tile_h(y, q + kBatch);
+          load_d(x, 0, 0);
+        quads_to_slot<D, kBatch>(y, t + kBatch * kGradsStates, sh, slot);
+        slot_full();
       }
-      ready(gH);
       float hh = 0.f;
-      auto tile_d = [&](const float4 (&v)[8], int q) {
+      auto dot = [&](const float4 (&v)[8]) {
 #pragma unroll
         for (int m = 0; m < 4; ++m)
           hh += fmaf(v[m].x, v[4 + m].x, v[m].y * v[4 + m].y) +
                 fmaf(v[m].z, v[4 + m].z, v[m].w * v[4 + m].w);
-        quads_to_tile<D, false, 4>(v, t + q * kGradsStates, sd, base + L::DH, 0u);
       };
 #pragma unroll
-      for (int q = 0; q < kQuads; q += 8) {
-        load_d(y, q + 4);
-        if (q == 0 && h > h0) mbar_wait(&bars[gA6], ph ^ 1, abort_flag, err, 64u);
-        tile_d(x, q);
-        if (q + 8 < kQuads) {
-          load_d(x, q + 8);
-        } else if (more) {
-          largest = hm[16];
-          load_h(x, H + D * D, 0);
+      for (int half = 0; half < kHalves; ++half) {
+        const uint32_t slot = base + L::H + (fills & 1) * L::kSlot;
+#pragma unroll
+        for (int q = 0; q < kQuads; q += 8) {
+          load_d(y, half, q + 4);
+          if (q == 0) slot_free();
+          dot(x);
+          quads_to_slot<D, 4>(x, t + q * kGradsStates, sd, slot);
+          if (q + 8 < kQuads) {
+            load_d(x, half, q + 8);
+          } else if (half + 1 < kHalves) {
+            load_d(x, half + 1, 0);
+          } else if (more) {
+            largest = hm[16];
+            load_h(x, H + D * D, 0, 0);
+          }
+          dot(y);
+          quads_to_slot<D, 4>(y, t + (q + 4) * kGradsStates, sd, slot);
         }
-        tile_d(y, q + 4);
+        if (half + 1 == kHalves) {
+          hh = warp_sum(hh);
+          if (lane == 0) red[8 * (h & 3) + warp - 8] = hh;
+        }
+        slot_full();
       }
-      hh = warp_sum(hh);
-      if (lane == 0) red[8 * (h & 3) + warp - 8] = hh;
-      ready(gD);
     }
     if constexpr (split) cluster_sync(), cluster_sync();
   } else {
@@ -1928,29 +1938,32 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
     auto desc = [&](uint32_t low) { return uint64_t(kHigh) << 32 | low; };
     constexpr uint32_t id64 = make_idesc_f16(128, 64, 0, 0), id128 = make_idesc_f16(128, 128, 0, 0);
-    constexpr uint32_t id_a = make_idesc_f16(128, 64, 1, 0);   // A MN-major
-    constexpr uint32_t id_a128 = make_idesc_f16(128, 128, 1, 0);
+    constexpr uint32_t id_a128 = make_idesc_f16(128, 128, 1, 0);  // A MN-major
     constexpr uint32_t id_ab = make_idesc_f16(128, 64, 1, 1);  // both MN-major
     auto load_o = [&](int h) {
       const uint8_t* src = a.O + (size_t(i) * a.H_v + h) * L::kTile;
       for (int x = 0; x < D / 64; ++x)
-        bulk_load_g2s(smem + L::OE + x * 2 * kBlk, src + x * kBlk, kBlk, &bars[gO]);
+        bulk_load_g2s(smem + L::OE + x * L::kOE, src + x * kBlk, kBlk, &bars[gO]);
     };
     mbar_arrive_expect_tx(&bars[gO], 3 * L::kTile);
     bulk_load_g2s(smem + L::K, a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile, 2 * L::kTile,
                   &bars[gO]);
     load_o(h0);
     int loads = 1;
-    constexpr uint32_t oe = L::OE, uh = L::UH, ul = L::UL;
-    // descriptors: tall tiles (128 rows a block of 64 columns) and short ones
-    auto tall = [&](uint32_t tile, int kk) {
-      return desc(b4 + (kKmaj | (tile + (kk >> 2) * 2 * kBlk + (kk & 3) * 32) >> 4));
+    constexpr uint32_t oe = L::OE, el = L::OE + 2 * kBlk, uh = L::UH, ul = L::UL;
+    // descriptors: dO and beta E, a slot (64 columns), 64 rows, and those along their columns
+    auto out = [&](uint32_t tile, int kk) {
+      return desc(b4 + (kKmaj | (tile + (kk >> 2) * L::kOE + (kk & 3) * 32) >> 4));
+    };
+    auto slot = [&](int fill, int limb, int kk) {
+      return desc(b4 + (kKmaj | (L::H + (fill & 1) * L::kSlot + limb * 2 * kBlk + (kk & 3) * 32) >> 4));
     };
     auto flat = [&](uint32_t tile, int kk) {
       return desc(b4 + (kKmaj | (tile + (kk >> 2) * kBlk + (kk & 3) * 32) >> 4));
     };
     auto rows = [&](uint32_t tile, int kk) { return desc(b4 + (kMnmaj | (tile + kk * 2048) >> 4)); };
     bool ok = true;
+    int fills = 0;
     for (int h = h0; h < h0 + heads && ok; ++h) {
       const uint32_t ph = (h - h0) & 1;
       ok = mbar_wait(&bars[gO], ph, abort_flag, err, 128u) &&
@@ -1959,33 +1972,47 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + (kk < D / 32 ? kTPN : kTPN2), tall(oe, kk), flat(ul, kk), id64,
+        mma_bf16_ss(tmem + (kk < D / 32 ? kTPN : kTPN2), out(oe, kk), flat(ul, kk), id64,
                     kk % (D / 32) != 0);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + (kk < D / 32 ? kTPN : kTPN2), tall(oe, kk), flat(uh, kk), id64, 1u);
+        mma_bf16_ss(tmem + (kk < D / 32 ? kTPN : kTPN2), out(oe, kk), flat(uh, kk), id64, 1u);
       mma_commit(&bars[gPN]);
-      ok = mbar_wait(&bars[gH], ph, abort_flag, err, 128u);
       // (the rows' warps have read the last head's sums)
-      if (h > h0) ok = mbar_wait(&bars[gE], ph ^ 1, abort_flag, err, 128u) && ok;
+      if (h > h0) ok = mbar_wait(&bars[gE], ph ^ 1, abort_flag, err, 128u);
       if (!ok) break;
-      tc_fence_after();
-      // the low limb first, for dO alone; then both, the second half of the columns fresh
+#pragma unroll 1
+      for (int k0 = 0; k0 < D / 16 && ok; k0 += 4, ++fills) {  // by halves of d_v
+        ok = mbar_wait(&bars[gFull + (fills & 1)], fills >> 1 & 1, abort_flag, err, 128u);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + kTA1, tall(L::HL, kk), tall(oe, kk), id64, kk != 0);
-      mma_bf16_ss(tmem + kTA1, tall(L::HH, 0), tall(oe, 0), id64, 1u);
-      mma_bf16_ss(tmem + kTA2, tall(L::HH, 0), tall(oe + kBlk, 0), id64, 0u);
+        for (int kk = 0; kk < 4; ++kk)
+          mma_bf16_ss(tmem + kTA1, slot(fills, 1, kk), out(oe, k0 + kk), id128, k0 + kk != 0);
 #pragma unroll
-      for (int kk = 1; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + kTA1, tall(L::HH, kk), tall(oe, kk), id128, 1u);
+        for (int kk = 0; kk < 4; ++kk)
+          mma_bf16_ss(tmem + kTA2, slot(fills, 0, kk), out(el, k0 + kk), id64, 1u);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_bf16_ss(tmem + kTA1, slot(fills, 0, kk), out(oe, k0 + kk), id128, 1u);
+        mma_commit(&bars[gFree + (fills & 1)]);
+      }
+      if (!ok) break;
       mma_commit(&bars[gA12]);
-      ok = mbar_wait(&bars[gD], ph, abort_flag, err, 128u);
-      if (!ok) break;
-      tc_fence_after();
+#pragma unroll 1
+      for (int k0 = 0; k0 < D / 16 && ok; k0 += 4, ++fills) {
+        ok = mbar_wait(&bars[gFull + (fills & 1)], fills >> 1 & 1, abort_flag, err, 128u);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + kTA6, tall(L::DH, kk), flat(uh, kk), id64, kk != 0);
+        for (int x = 0; x < 3; ++x)  // low x high, high x low, high x high
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_ss(tmem + kTA6, slot(fills, x == 0, kk), flat(x == 1 ? ul : uh, k0 + kk), id64,
+                        k0 + kk + x != 0);
+        mma_commit(&bars[gFree + (fills & 1)]);
+      }
+      if (!ok) break;
       mma_commit(&bars[gA6]);
       if (h + 1 < h0 + heads) {  // dO's last reader is done
         ok = mbar_wait(&bars[gA12], ph, abort_flag, err, 128u);
@@ -1997,19 +2024,20 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       ok = mbar_wait(&bars[gP], ph, abort_flag, err, 128u);
       if (!ok) break;
       tc_fence_after();
-      // the low limb of P and N are one tile of 128 rows, A3 and A5 side by side
+      // a limb of P and that of N are one tile of 128 rows, A3 and A5 side by side
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA3, rows(L::K, kk), flat(L::PL, kk), id_a128, kk != 0);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA3, rows(L::K, kk), flat(L::PH, kk), id_a, 1u);
+        mma_bf16_ss(tmem + kTA3, rows(L::K, kk), flat(L::PH, kk), id_a128, 1u);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA4, rows(L::Q, kk), rows(L::PH, kk), id_ab, kk != 0);
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA5, rows(L::K, kk), rows(L::N, kk), id_ab, 1u);
+        for (int kk = 0; kk < 4; ++kk) {
+          mma_bf16_ss(tmem + kTA4, rows(L::Q, kk), rows(x ? L::PH : L::PL, kk), id_ab, kk + x != 0);
+          mma_bf16_ss(tmem + kTA5, rows(L::K, kk), rows(x ? L::NH : L::NL, kk), id_ab, 1u);
+        }
       mma_commit(&bars[gA345]);
     }
     mma_commit(&bars[gDrain]);

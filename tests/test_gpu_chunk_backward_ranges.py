@@ -133,3 +133,23 @@ def test_a_rise_and_a_fall_beyond_f32_between_them(rise, fall, where):
             assert R.rel(x[where:], y[where:]) <= (R.BF16_REL if name == "dv" else 0) + R.F32_REL
     if fall < 87:
         assert R.rel(got[5], want[5]) <= R.F32_REL
+
+
+@pytest.mark.parametrize("heads", [(2, 2), (1, 3)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rounded_once(d, heads):
+    """dq, dk and dv are the exact gradients rounded to bf16, but for elements that the f32
+    arithmetic moves over the middle of two neighbours.  An error of e times the tensor's
+    root mean square r moves an element x, whose neighbours are at least 2^-8 |x| apart, with
+    probability 2 e r / (2^-8 |x|) at most; over normally distributed x (1 / |x| cut off where that
+    is 1) this is about 2^9 e (0.8 ln(1 / (2^9 e)) + 1), 4.6 % for e = F32_REL.  One operand of 11
+    bits (e = 1.4e-4, the root mean square of its rounding) gives 22 %."""
+    lens = [300, 70]
+    case = _case(lens, *heads, d, seed=6)
+    rows, do, h0, dhT = case
+    cu = torch.tensor(R.offsets(lens), dtype=torch.int32, device=DEV)
+    dev = [x.to(DEV) for x in rows]
+    got = gdn_chunk_backward(*dev, cu, do.to(DEV), h0=h0.to(DEV), dhT=dhT.to(DEV))
+    want = R.backward(*dev, lens, do.to(DEV), h0.to(DEV), dhT.to(DEV))
+    other = [float((x != y.to(torch.bfloat16)).double().mean()) for x, y in zip(got[:3], want)]
+    assert max(other) <= 0.046
