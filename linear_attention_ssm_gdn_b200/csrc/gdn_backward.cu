@@ -29,8 +29,9 @@
 // that puts the largest value of its row or tile just below 2^15: 22 bits, or
 // 2^-40 of the largest value, whichever is coarser.  bf16 inputs are exact in
 // one limb under such a scale.  exact x f32 takes 2 MMAs, f32 x f32 takes 3
-// (lo x lo is below the f32 rounding).  Only beta E has a single limb (2^-12) in
-// one product, N.
+// (lo x lo is below the f32 rounding).  Where no scale would do (M, P and N, whose
+// elements decays set apart along rows and columns) the limbs are bf16, three of them,
+// or two in dk, which is rounded to bf16 itself (2^-17 against 2^-9).
 //
 // The scans and the gradients run on tcgen05; the first kernel, whose products are
 // small and triangular, on warp-level MMAs.
@@ -65,8 +66,8 @@ struct BwdArgs {
   int32_t* chunk_seq;  // [max_chunks]
   int max_chunks;
   int sms;             // SMs of the device
-  uint8_t* KQ;         // [chunk][H_k] f16 tiles of K, then of Q
-  uint8_t* O;          // [chunk][H_v] f16 tile of dO
+  uint8_t* KQ;         // [chunk][H_k] f16 tiles of K, then of Q, a scale per row
+  uint8_t* O;          // [chunk][H_v] f16 tile of dO, a scale per row
   uint8_t* GO;         // [chunk][H_v] scale e^G dO, high and low tile, a scale per column
   uint8_t* S;          // [chunk][H_v] S below its diagonal blocks, high and low block
   float* Y0;           // [chunk][H_v][64][D] scale (Q K^T * D)^T dO
@@ -82,10 +83,10 @@ struct BwdArgs {
   float* h0dh0;        // [sequence][H_v][8] <h0, dh0>, each scan warp's part
 };
 
-// Per-unit factors for the gradients: of each row e^G, e^{G_C - G}, beta and e^{G_b - G}
-// with b the last row of its 16-row block; then scalars.
-enum { kFeG = 0, kFeT = kBC, kFbeta = 2 * kBC, kFend = 3 * kBC, kFinvK = 4 * kBC, kFinvQ, kFinvO };
-constexpr int kFac = 4 * kBC + 4;
+// Per-unit factors for the gradients: of each row e^G, e^{G_C - G}, beta, e^{G_b - G} with b
+// the last row of its 16-row block, and scale times the inverse scale of dO's row.
+enum { kFeG = 0, kFeT = kBC, kFbeta = 2 * kBC, kFend = 3 * kBC, kFo = 4 * kBC };
+constexpr int kFac = 5 * kBC;
 
 // For a scan: what scales the rows of its three products (kSx: the state times K^T; kSin:
 // X or Y into the product with S; kSw: u or E into the product with K), what scales that
@@ -219,20 +220,12 @@ __device__ __forceinline__ void mma16_bf16(float (&c)[4], const uint32_t (&a)[4]
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                      uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // c += A B with a rounded sum: the MMA's own accumulation truncates, and over the
 // steps of a long product the losses have one sign and add up.
 __device__ __forceinline__ void add_mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
   float p[4] = {};
-  mma16(p, a, b0, b1);
+  mma16_bf16(p, a, b0, b1);
 #pragma unroll
   for (int e = 0; e < 4; ++e) c[e] += p[e];
 }
@@ -308,10 +301,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // the last row has an output gradient, E_s is e^{G_63 - G_s} times something of size 1.  So no
 // scale is shared by elements that a decay sets apart.  M has bf16 limbs, which need no scale.
 // S meets its operands block by block: the diagonal blocks in f32 on the CUDA cores, element
-// (r, s) of block (a, b) below them, e^{G_r - G_s} times something of size 1, as limbs of
-// S 2^-(from_r + to_s) under a scale of the block, where 2^from_r and 2^to_s are e^{G_r - G_a} and
-// e^{G_b - G_s} (a the first row of its block, b the last one of the other) to the nearest power
-// of two.  The scan puts them on its operand or its result, whichever has that row.
+// (r, s) of block (a, b) below them, e^{G_r - G_s} |k_r| |k_s| times something of size 1, as limbs
+// of S 2^-(from_r + to_s) under a scale of the block, where 2^from_r and 2^to_s are e^{G_r - G_a} |k_r|
+// and e^{G_b - G_s} |k_s| (a the first row of its block, b the last one of the other) to the nearest
+// power of two or two.  The scan puts them on its operand or its result, whichever has that row.
 //
 // K K^T and Q K^T are one pass of MMAs each (exact operands).  With L_b the
 // diagonal 16 x 16 blocks of B diag(beta), S by block rows:
@@ -322,8 +315,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // 140 then).  132 us at 4576 rows, 16 key and 48 value heads, d = 128: 0.38 GB written.
 // ---------------------------------------------------------------------------
 
-// 64 x D bf16 rows (row stride in elements) as an f16 tile: loads, finds the
-// largest value of the tile (into *most, a shared word that was zero), ...
+// 64 x D bf16 rows (row stride in elements) and the tiles that are made of them.
 template <int D>
 struct TileIn {
   uint4 x[D / 32];
@@ -335,21 +327,20 @@ struct TileIn {
       if (r < rows) x[i] = *reinterpret_cast<const uint4*>(src + size_t(r) * stride + 8 * c);
     }
   }
-  __device__ __forceinline__ void largest(uint32_t* most) const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                               __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
-    m = max(m >> 16, m & 0xffffu);
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) atomicMax(most, m << 16);
-  }
-  // and stores the scaled tile to shared (0: not) and global memory (NULL: not).
-  __device__ __forceinline__ void store(float s, uint32_t tile, uint8_t* out) const {
+  // As f16, each row times a power of two of its own, to global memory (NULL: not); the inverse
+  // scales times f to inv[64].
+  __device__ __forceinline__ void store(uint8_t* out, float f, float* inv) const {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const int p = threadIdx.x + 256 * i, r = p / (D / 8), c = 8 * (p % (D / 8));
+      uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                            __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+#pragma unroll
+      for (int off = 1; off < D / 8; off <<= 1)  // the row's lanes
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+      float is;
+      const float s = pow2_scale(__uint_as_float(max(m >> 16, m & 0xffffu) << 16), &is);
+      if (c == 0) inv[r] = is * f;
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       uint32_t h[4];
 #pragma unroll
@@ -357,7 +348,6 @@ struct TileIn {
         h[j] = pack_f16(__uint_as_float(w[j] << 16) * s,
                         __uint_as_float(w[j] & 0xffff0000u) * s);
       const uint32_t at = (c >> 6) * kBlk + sw128_offset(r, (c & 63) * 2);
-      if (tile != 0) st_shared_v4(tile + at, h[0], h[1], h[2], h[3]);
       if (out != nullptr) *reinterpret_cast<uint4*>(out + at) = make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
@@ -424,7 +414,7 @@ constexpr int kBT = 68;  // row length of the f32 squares (16-byte rows, 4 banks
 template <int D>
 struct PrepSmem {
   static constexpr int kTile = D / 64 * kBlk;
-  static constexpr int K = 0, Q = kTile;       // f16 tiles; later dO, then the limbs of S
+  static constexpr int K = 0, Q = kTile;       // bf16 tiles; later dO, then the limbs of S
   static constexpr int M = 2 * kBlk;           // later, over Q: the three limbs of M
   static constexpr int B = 5 * kBlk;
   static constexpr int S = B + kBC * kBT * 4;
@@ -484,10 +474,12 @@ struct GateRows {
   float2 G[kBC];
   float beta[kBC], eG[kBC];  // eG: scale e^G / scale of Q
   float end[kBC];            // e^{G_b - G}, b the last row of the 16-row block
-  int from[kBC], to[kBC];    // e^{G - G_a}, a the block's first row, and e^{G_b - G}: nearest 2^x
+  // The nearest 2^x of e^{G - G_a}, a the block's first row, and of e^{G_b - G}, each times the
+  // size of k.
+  int from[kBC], to[kBC];
 };
 __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c, size_t unit, int h,
-                                           float invk, float invq, GateRows* s) {
+                                           const float* invk, const float* invq, GateRows* s) {
   const int lane = threadIdx.x & 31;
   float *fac = a.fac + unit * kFac, *ff = a.ff + unit * kFwdFac, *fb = a.fb + unit * kBackFac;
   double x[2];
@@ -524,20 +516,21 @@ __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c,
     s->G[r] = G;
     a.G[unit * kBC + r] = G;
     const float eG = exp2f(G.x + G.y), eT = exp2f(float(total - x[e]));
-    s->eG[r] = a.scale * eG * invq;
+    s->eG[r] = a.scale * eG * invq[r];
     s->end[r] = exp2f(float(end - x[e]));
-    s->from[r] = max(-kFold, min(kFold, __float2int_rn(float(x[e] - begin))));
-    s->to[r] = max(-kFold, min(kFold, __float2int_rn(float(end - x[e]))));
+    const int size = int(__float_as_uint(invk[r]) >> 23) - 112;  // (the largest of k: 2^size)
+    s->from[r] = max(-kFold, min(kFold, __float2int_rn(float(x[e] - begin)) + size));
+    s->to[r] = max(-kFold, min(kFold, __float2int_rn(float(end - x[e])) + size));
     fac[kFend + r] = s->end[r];
     fac[kFeG + r] = eG;
     fac[kFeT + r] = eT;
     fac[kFbeta + r] = bt[e];
-    ff[kSx + r] = -eG * invk;
+    ff[kSx + r] = -eG * invk[r];
     ff[kSin + r] = bt[e] * pow2(s->to[r]);
-    ff[kSw + r] = bt[e] * eT * invk;
-    fb[kSx + r] = eT * invk;
+    ff[kSw + r] = bt[e] * eT * invk[r];
+    fb[kSx + r] = eT * invk[r];
     fb[kSin + r] = bt[e] * pow2(s->from[r]);
-    fb[kSw + r] = -bt[e] * eG * invk;
+    fb[kSw + r] = -bt[e] * eG * invk[r];
   }
   if (lane == 0) ff[kSeC] = fb[kSeC] = exp2f(float(total));
 }
@@ -547,8 +540,8 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
   using L = PrepSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ GateRows gates[2];  // by the head's parity
-  __shared__ uint32_t most[3];   // K, Q; by head: dO
-  __shared__ uint32_t cols[D];   // by head: columns of scale e^G dO / scale of Q
+  __shared__ float invk[kBC], invq[kBC];  // inverse scales of K's and Q's rows
+  __shared__ uint32_t cols[D];   // by head: columns of scale e^G dO / scale of Q's row
   const int i = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_wait();
   grid_launch_next();
@@ -565,25 +558,20 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
   const uint32_t base = smem_u32(smem);
   const size_t unit0 = size_t(i) * a.H_v;
   auto dout = [&](int h) { return a.dout + (size_t(c.row0) * a.H_v + h) * D; };
-  if (tid < 2) most[tid] = 0;
-  __syncthreads();
-  float invk, invq;
   TileIn<D> ot;
   {
     TileIn<D> kt, qt;
     kt.fetch(a.k + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows);
     qt.fetch(a.q + size_t(c.row0) * a.qk_stride + hk * D, a.qk_stride, c.rows);
     ot.fetch(dout(h0), size_t(a.H_v) * D, c.rows);
-    kt.largest(&most[0]);
-    qt.largest(&most[1]);
-    __syncthreads();
     uint8_t* kq = h0 % vpg == 0 ? a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile : nullptr;
-    kt.store(pow2_scale(__uint_as_float(most[0]), &invk), base + L::K, kq);
-    qt.store(pow2_scale(__uint_as_float(most[1]), &invq), base + L::Q,
-             kq != nullptr ? kq + L::kTile : nullptr);
+    kt.store_raw(base + L::K);
+    qt.store_raw(base + L::Q);
+    kt.store(kq, 1.f, invk);
+    qt.store(kq != nullptr ? kq + L::kTile : nullptr, 1.f, invq);
   }
-  if (warp == 7) make_gates(a, c, unit0 + h0, h0, invk, invq, &gates[h0 & 1]);
   __syncthreads();
+  if (warp == 7) make_gates(a, c, unit0 + h0, h0, invk, invq, &gates[h0 & 1]);
   // K K^T and Q K^T, for all the heads: warp = 16 rows, every other 16-column block up
   // to the diagonal
   const int rb = warp >> 1, par = warp & 1, g8 = lane >> 2, t2 = 2 * (lane & 3);
@@ -604,10 +592,6 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
         add_mma16(qk[2 * j + 1], aq, bv[2], bv[3]);
       }
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) kk_[j][e] *= invk * invk, qk[j][e] *= invk * invq;
   float* B = reinterpret_cast<float*>(smem + L::B);
   float* S = reinterpret_cast<float*>(smem + L::S);
   float* T = reinterpret_cast<float*>(smem + L::T);
@@ -615,12 +599,10 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
     const size_t unit = unit0 + h;
     const GateRows& gr = gates[h & 1];
     const float* bs = gr.beta;
-    if (tid == 0) most[2] = 0;
     if (tid >= 128 && tid < 128 + D) cols[tid - 128] = 0;
     if (tid == 0) tma_store_wait_read<0>();  // the last head's S has left
     __syncthreads();  // the last head's (or K and Q's) shared memory is free
     // B and M
-    ot.largest(&most[2]);
     ot.largest_of_columns(gr.eG, cols);
     float m_[4][4];
 #pragma unroll
@@ -665,17 +647,13 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
             for (int x = 0; x < 3; ++x)
               *reinterpret_cast<uint32_t*>(smem + L::M + x * kBlk + at) = limb[x];
           }
-      float invo, inv;
       ot.store_raw(base);
-      ot.store(pow2_scale(__uint_as_float(most[2]), &invo), 0, a.O + unit * L::kTile);
+      ot.store(a.O + unit * L::kTile, a.scale, a.fac + unit * kFac + kFo);
       ot.store_limbs(gr.eG, cols, a.GO + unit * 2 * L::kTile);
       if (tid < D) {
+        float inv;
         pow2_scale(__uint_as_float(cols[tid]), &inv);
         a.fb[unit * kBackFac + kScol + tid] = inv;
-      }
-      if (tid == 0) {
-        float* fac = a.fac + unit * kFac;
-        fac[kFinvK] = invk, fac[kFinvQ] = invq, fac[kFinvO] = invo;
       }
     }
     __syncthreads();  // M and dO
@@ -1425,9 +1403,9 @@ cudaError_t take_err_backward(uint32_t* out) {
 // operand:
 //   [P; N]       = [dO; beta E] (beta u)^T           K = d_v
 //   [A1 | A2]    = H [dO; beta E]^T                  K = d_v, by halves
-//   A3           = P K,  A4 = P^T Q,  A5 = N K + N^T K   K = 64
+//   A3           = P K,  A4 = P^T Q + N K + N^T K    K = 64
 //   A6           = dH' (beta u)^T                    K = d_v, by halves
-//   dq = scale e^G A1 + A3,  dk = A4 + A5 - e^G A2 + e^{G_C - G} A6.
+//   dq = scale e^G A1 + A3,  dk = A4 - e^G A2 + e^{G_C - G} A6.
 // Row factors that differ within a product are applied to its result.
 //   warps 0-7: rows u and E to tiles, the masks of P and N, the sums dq, dk, dg;
 //   warps 8-11: states to tiles, in two slots, and <H', dH'>;
@@ -1447,13 +1425,16 @@ cudaError_t take_err_backward(uint32_t* out) {
 template <int D>
 struct GradsSmem {
   static constexpr int kTile = D / 64 * kBlk;
-  static constexpr int K = 0, Q = kTile;         // f16 tiles of the chunk
-  // dO, beta E high and beta E low, for each 64 columns one over the other
-  static constexpr int OE = 2 * kTile + (D == 64 ? kBlk : 0), kOE = 3 * kBlk;
+  // Q and K as they are (bf16), for each 64 columns one over the other
+  static constexpr int QK = 0, kQK = 2 * kBlk;
+  // dO, beta E high and beta E low, likewise
+  static constexpr int OE = D / 64 * kQK, kOE = 3 * kBlk;
   static constexpr int UH = OE + D / 64 * kOE, UL = UH + kTile;  // beta u, two limbs
   // Two slots for 64 columns (d_v) of H or dH' with 128 rows: high limb, low limb
   static constexpr int H = UL + kTile, kSlot = 4 * kBlk;
-  static constexpr int PL = H + 2 * kSlot, NL = PL + kBlk, PH = NL + kBlk, NH = PH + kBlk;
+  // bf16 limbs of P (high, middle, low) and N (high, middle)
+  static constexpr int PL = H + 2 * kSlot, PM = PL + kBlk, NM = PM + kBlk, PH = NM + kBlk,
+                       NH = PH + kBlk;
   static constexpr int Fac = NH + kBlk;          // two buffers of the unit's factors
   static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
   static constexpr int F = G + 2 * kBC * 8;      // floats from here
@@ -1467,9 +1448,9 @@ struct GradsSmem {
 constexpr int kGradsRows = 256, kGradsStates = 128, kGradsThreads = 512;
 // Registers after re-allocation: 128 (2 x 176 + 112 + 48) is the launch's 512 x 128.
 constexpr uint32_t kRegsRows = 176, kRegsStates = 112, kRegsIssue = 48;
-enum { gO = 0, gU, gFull, gFree = gFull + 2, gP = gFree + 2, gPN, gA12, gA345, gA6, gE, gDrain, kGradsBars };
-enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA5 = 256, kTA4 = 320, kTA6 = 384,
-       kTPN2 = 448 };  // (P and N's second half over d_v)
+enum { gO = 0, gQK, gU, gFull, gFree = gFull + 2, gP = gFree + 2, gPN, gA12, gA345, gA6, gE, gDrain, kGradsBars };
+enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA4 = 256, kTEL = 320, kTA6 = 384,
+       kTPN2 = 448 };  // (kTEL: beta E's low limb in N; kTPN2: P and N's second half over d_v)
 
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -1496,7 +1477,6 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   using L = GradsSmem<D>;
   constexpr int J = D / 32;         // quads of a row per lane in the row pass
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint32_t most[2];      // P, N
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::Bars);
@@ -1508,7 +1488,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   const int hk = split ? blockIdx.y / vpg : blockIdx.y, h0 = split ? blockIdx.y : hk * vpg;
   if (tid == 0) {
     for (int b = 0; b < kGradsBars; ++b)
-      mbar_init(&bars[b], b == gU || b == gP || b == gE ? kGradsRows / 32 : b == gFull || b == gFull + 1 ? kGradsStates / 32 : 1);
+      mbar_init(&bars[b], b == gQK ? 2 : b == gU || b == gP || b == gE ? kGradsRows / 32 : b == gFull || b == gFull + 1 ? kGradsStates / 32 : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -1563,9 +1543,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (h & 1) * kFac;
       const float2* Gs = reinterpret_cast<const float2*>(smem + L::G) + (h & 1) * kBC;
       const float *invU = invU2 + kBC * (h & 1), *invE = invE2 + kBC * (h & 1);
-      float ip = 0.f, in = 0.f;
       if (on_head) {
-        if (tid < 2) most[tid] = 0;
         named_sync(1, kGradsRows);  // the rows' scales; the last head's factors are free
         if (more) load_head(h + 1);
         // P and N: lanes 0-63 are rows of P, 64-127 of N
@@ -1579,13 +1557,18 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] += y[k];
+          if (qd >= 2) {
+            tmem_ld32(tl + kTEL, y);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] += y[k];
+          }
         }
         {
           const bool isn = qd >= 2;
           const int pr = dk & 63, pb = pr >> 4;
           const float2 Gr = Gs[pr];
-          const float fr = isn ? -invE[pr] : a.scale * fac[kFinvO];
-          float m = 0.f;
+          const float fr = isn ? -invE[pr] : fac[kFo + pr];
 #pragma unroll
           for (int cb = 0; cb < 2; ++cb) {  // 16-column blocks
             const int s0 = 32 * ch + 16 * cb, sb = s0 >> 4;
@@ -1609,22 +1592,18 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
               }
             }
           }
-          m = max_abs_of(x);
-          const uint32_t um = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-          if (lane == 0) atomicMax(&most[isn], um);
-          named_sync(1, kGradsRows);
-          const float sp = pow2_scale(__uint_as_float(most[0]), &ip);
-          const float sn = pow2_scale(__uint_as_float(most[1]), &in);
-          const float sc = isn ? sn : sp;
+          // bf16 limbs: decays set the elements of a row as well as those of a column apart, and
+          // the tiles are multiplied along both, so no scale would do
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t p[4], q[4];
+            uint32_t w[4][3];
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              split_f16(x[8 * k + 2 * y] * sc, x[8 * k + 2 * y + 1] * sc, p[y], q[y]);
-            const uint32_t at = sw128_offset(pr, 64 * ch + 16 * k);
-            st_shared_v4(base + (isn ? L::NH : L::PH) + at, p[0], p[1], p[2], p[3]);
-            st_shared_v4(base + (isn ? L::NL : L::PL) + at, q[0], q[1], q[2], q[3]);
+              split_bf16(x[8 * k + 2 * y], x[8 * k + 2 * y + 1], w[y]);
+            const uint32_t at = base + sw128_offset(pr, 64 * ch + 16 * k);
+            st_shared_v4(at + (isn ? L::NH : L::PH), w[0][0], w[1][0], w[2][0], w[3][0]);
+            st_shared_v4(at + (isn ? L::NM : L::PM), w[0][1], w[1][1], w[2][1], w[3][1]);
+            if (!isn) st_shared_v4(at + L::PL, w[0][2], w[1][2], w[2][2], w[3][2]);
           }
         }
         ready(gP);
@@ -1733,8 +1712,6 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       tc_fence_after();
       {
         const float ih = red[32 + 2 * (h & 1)], id = red[33 + 2 * (h & 1)];  // the states' scales
-        const float f = a.scale * fac[kFinvO] * ih, fp = ip * fac[kFinvK], iq = fac[kFinvQ];
-        const float fq = ip * fac[kFinvQ], fn = in * fac[kFinvK];
 #pragma unroll
         for (int cb = 0; cb < 2; ++cb) {
           float x0[16], x1[16], x2[16], x3[16];
@@ -1744,12 +1721,12 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float d = fmaf(x0[k], f * fac[kFeG + s0 + k], x1[k] * fp);
+            const float d = fmaf(x0[k], fac[kFeG + s0 + k] * (fac[kFo + s0 + k] * ih), x1[k]);
             dqs[16 * cb + k] += d;
             float q = 0.f;
             if (on)
-              q = __half2float(*reinterpret_cast<const __half*>(
-                      smem + L::Q + (dk >> 6) * kBlk + sw128_offset(s0 + k, (dk & 63) * 2))) * d;
+              q = bf16f(*reinterpret_cast<const uint16_t*>(
+                      smem + L::QK + (dk >> 6) * L::kQK + sw128_offset(s0 + k, (dk & 63) * 2))) * d;
             x0[k] = q;
           }
           tmem_ld16(tl + kTA2 + 16 * cb, x1);
@@ -1765,19 +1742,18 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
             }
           }
           x0[0] += __shfl_xor_sync(0xffffffffu, x0[0], 1);
-          if ((lane & 1) == 0) part[qd * kBC + s0 + (lane >> 1)] = x0[0] * iq;
+          if ((lane & 1) == 0) part[qd * kBC + s0 + (lane >> 1)] = x0[0];
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             dks[16 * cb + k] +=
-                fmaf(x2[k], fq, x1[k] * (-fac[kFeG + s0 + k] * (invE[s0 + k] * ih)));
-          tmem_ld16(tl + kTA5 + 16 * cb, x2);
+                fmaf(x1[k], -fac[kFeG + s0 + k] * (invE[s0 + k] * ih), x2[k]);
           tmem_ld16(tl + kTA6 + 16 * cb, x3);
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             dks[16 * cb + k] +=
-                fmaf(x2[k], fn, x3[k] * (fac[kFeT + s0 + k] * (invU[s0 + k] * id)));
+                x3[k] * (fac[kFeT + s0 + k] * (invU[s0 + k] * id));
         }
       }
       ready(gE);
@@ -1929,28 +1905,28 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   } else {
    setmaxnreg_dec<kRegsIssue>();
    if (warp == 12 && lane == 0) {
-    // The issuer; it also loads K, Q and each head's dO.
+    // The issuer; it also loads each head's dO.
     // Descriptors: the high word is a constant, the low one an address and the (for the
     // K-major tiles unused) distance of 64-column blocks.
     // (In a cluster the address has the CTA's rank above its low 18 bits.)
     const uint32_t b4 = (split ? base & 0x3ffffu : base) >> 4;
-    constexpr uint32_t kKmaj = 1u << 16, kMnmaj = (8192u >> 4) << 16;
+    constexpr uint32_t kKmaj = 1u << 16, kMnmaj = (uint32_t(L::kQK) >> 4) << 16;
     constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
     auto desc = [&](uint32_t low) { return uint64_t(kHigh) << 32 | low; };
     constexpr uint32_t id64 = make_idesc_f16(128, 64, 0, 0), id128 = make_idesc_f16(128, 128, 0, 0);
-    constexpr uint32_t id_a128 = make_idesc_f16(128, 128, 1, 0);  // A MN-major
-    constexpr uint32_t id_ab = make_idesc_f16(128, 64, 1, 1);  // both MN-major
+    constexpr uint32_t id_a = make_idesc_bf16(128, 64, 1, 0);  // A MN-major
+    constexpr uint32_t id_a128 = make_idesc_bf16(128, 128, 1, 0);
+    constexpr uint32_t id_ab = make_idesc_bf16(128, 64, 1, 1);  // both MN-major
     auto load_o = [&](int h) {
       const uint8_t* src = a.O + (size_t(i) * a.H_v + h) * L::kTile;
       for (int x = 0; x < D / 64; ++x)
         bulk_load_g2s(smem + L::OE + x * L::kOE, src + x * kBlk, kBlk, &bars[gO]);
     };
-    mbar_arrive_expect_tx(&bars[gO], 3 * L::kTile);
-    bulk_load_g2s(smem + L::K, a.KQ + (size_t(i) * a.H_k + hk) * 2 * L::kTile, 2 * L::kTile,
-                  &bars[gO]);
+    mbar_arrive_expect_tx(&bars[gO], L::kTile);
     load_o(h0);
     int loads = 1;
     constexpr uint32_t oe = L::OE, el = L::OE + 2 * kBlk, uh = L::UH, ul = L::UL;
+    constexpr uint32_t tq = L::QK, tk = L::QK + kBlk;
     // descriptors: dO and beta E, a slot (64 columns), 64 rows, and those along their columns
     auto out = [&](uint32_t tile, int kk) {
       return desc(b4 + (kKmaj | (tile + (kk >> 2) * L::kOE + (kk & 3) * 32) >> 4));
@@ -1977,6 +1953,10 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         mma_bf16_ss(tmem + (kk < D / 32 ? kTPN : kTPN2), out(oe, kk), flat(uh, kk), id64, 1u);
+      // (rows 64 to 127 of this one: beta E's low limb)
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_bf16_ss(tmem + kTEL, out(oe + kBlk, kk), flat(uh, kk), id64, kk != 0);
       mma_commit(&bars[gPN]);
       // (the rows' warps have read the last head's sums)
       if (h > h0) ok = mbar_wait(&bars[gE], ph ^ 1, abort_flag, err, 128u);
@@ -2024,25 +2004,42 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       ok = mbar_wait(&bars[gP], ph, abort_flag, err, 128u);
       if (!ok) break;
       tc_fence_after();
-      // a limb of P and that of N are one tile of 128 rows, A3 and A5 side by side
+      if (h == h0) ok = mbar_wait(&bars[gQK], 0, abort_flag, err, 128u);
+      if (!ok) break;
+      tc_fence_after();
+      // A limb of P and that of N are one tile of 128 rows, A3 and A4 side by side.
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA3, rows(L::K, kk), flat(L::PL, kk), id_a128, kk != 0);
+        mma_bf16_ss(tmem + kTA3, rows(tk, kk), flat(L::PM, kk), id_a128, kk != 0);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA3, rows(L::K, kk), flat(L::PH, kk), id_a128, 1u);
+        mma_bf16_ss(tmem + kTA3, rows(tk, kk), flat(L::PL, kk), id_a, 1u);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ss(tmem + kTA3, rows(tk, kk), flat(L::PH, kk), id_a128, 1u);
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          mma_bf16_ss(tmem + kTA4, rows(L::Q, kk), rows(x ? L::PH : L::PL, kk), id_ab, kk + x != 0);
-          mma_bf16_ss(tmem + kTA5, rows(L::K, kk), rows(x ? L::NH : L::NL, kk), id_ab, 1u);
+          mma_bf16_ss(tmem + kTA4, rows(tq, kk), rows(x ? L::PH : L::PM, kk), id_ab, 1u);
+          mma_bf16_ss(tmem + kTA4, rows(tk, kk), rows(x ? L::NH : L::NM, kk), id_ab, 1u);
         }
       mma_commit(&bars[gA345]);
     }
     mma_commit(&bars[gDrain]);
     mbar_wait(&bars[gDrain], 0, nullptr, err, 32u);
     mbar_wait(&bars[gO], (loads - 1) & 1, nullptr, err, 32u);
+   } else if (warp >= 14) {  // Q and K
+    const uint16_t* src = (warp == 14 ? a.q : a.k) + hk * D;
+    const uint32_t to = base + L::QK + (warp == 14 ? 0 : kBlk);
+    for (int y = lane; y < kBC * D / 8; y += 32) {
+      const int r = y / (D / 8), col = 8 * (y % (D / 8));
+      cp_async16(to + (col >> 6) * L::kQK + sw128_offset(r, (col & 63) * 2),
+                 r < c.rows ? src + size_t(c.row0 + r) * a.qk_stride + col : src, r < c.rows);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    ready(gQK);
    } else if (warp == 13) {
     for (int h = h0; h < h0 + heads; ++h) {
       named_sync(3, kGradsRows + 32);
