@@ -14,9 +14,13 @@
 //   N = -strictly lower ((beta E) (beta u)^T) * D,
 //   dq = scale e^G (dO H^T) + P K,
 //   dk = P^T Q + (N + N^T) K - e^G (beta E) H^T + e^{G_C-G} (beta u) dH'^T,
-//   dg_r = <H', dH'> + sum_{s >= r} (q_s . dq_s - v_s . dv_s),
-// the last because e^{G_r} enters only by scaling q_r up and v_r down.  The first row of
-// a sequence has a second value, <h0, dh0>, and that of a chunk with a zero state has 0.
+//   dg_r = e^{G_C} <H, dH'> + sum_{t >= r} a_t + sum_{s < r} b_s + sum_{s < r <= t} W_ts  with
+//   a_t = e^{G_t} (scale q_t . H dO_t - k_t . H beta E_t),  b_s = e^{G_C-G_s} k_s . dH' beta u_s,
+//   W_ts = P_ts q_t . k_s + N_ts k_t . k_s:
+// what row r's gate decays is all that lies before it, H and the rows s < r, and it decays it for
+// all behind, dH' and the rows t >= r.  Every term has the gate's own decay in it, so a strong one
+// costs dg no accuracy.  (As sum_{s >= r} (q_s . dq_s - v_s . dv_s) + <H', dH'>, which needs no W, dg
+// is the small rest of large terms where decays are strong.)
 //
 // Gates reach the exponentials as differences of 64-bit cumulative sums (in base
 // 2: exp2f is the shorter function), kept as two floats: a strong decay early in
@@ -77,16 +81,15 @@ struct BwdArgs {
   float2* G;           // [chunk][H_v][64] cumulative gates / ln 2, high and low part
   float* u;            // [chunk][H_v][D / 32][64][32]
   float* E;            // [chunk][H_v][D / 32][64][32]
-  float* H;            // [chunk + sequence][H_v][D / 16][D][16] entry states, then the final one
+  float* H;            // [chunk][H_v][D / 16][D][16] entry states
   float* dH;           // [chunk][H_v][D / 16][D][16] gradient of the exit state
   float* Hmax;         // [chunk][H_v][2][8] largest |H| and |dH| of each scan warp's part
-  float* h0dh0;        // [sequence][H_v][8] <h0, dh0>, each scan warp's part
 };
 
 // Per-unit factors for the gradients: of each row e^G, e^{G_C - G}, beta, e^{G_b - G} with b
-// the last row of its 16-row block, and scale times the inverse scale of dO's row.
-enum { kFeG = 0, kFeT = kBC, kFbeta = 2 * kBC, kFend = 3 * kBC, kFo = 4 * kBC };
-constexpr int kFac = 5 * kBC;
+// the last row of its 16-row block, and scale times the inverse scale of dO's row; e^{G_C}.
+enum { kFeG = 0, kFeT = kBC, kFbeta = 2 * kBC, kFend = 3 * kBC, kFo = 4 * kBC, kFeC = 5 * kBC };
+constexpr int kFac = 5 * kBC + 4;
 
 // For a scan: what scales the rows of its three products (kSx: the state times K^T; kSin:
 // X or Y into the product with S; kSw: u or E into the product with K), what scales that
@@ -532,7 +535,7 @@ __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c,
     fb[kSin + r] = bt[e] * pow2(s->from[r]);
     fb[kSw + r] = -bt[e] * eG * invk[r];
   }
-  if (lane == 0) ff[kSeC] = fb[kSeC] = exp2f(float(total));
+  if (lane == 0) fac[kFeC] = ff[kSeC] = fb[kSeC] = exp2f(float(total));
 }
 
 template <int D>
@@ -1027,7 +1030,7 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
       tc_fence_before();
       if (!named_all(1, kScanSync, ok)) break;
       {
-        send_state(back ? a.dH + unit * D * D : a.H + (size_t(i + b) * a.H_v + h) * D * D);
+        send_state((back ? a.dH : a.H) + unit * D * D);
         const float wm = warp_max(on ? most : 0.f);
         if (lane == 0) a.Hmax[(unit * 2 + back) * 8 + warp] = wm;
       }
@@ -1200,17 +1203,8 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
         }
       }
     }
-    if constexpr (!back) send_state(a.H + (size_t(c0 + n + b) * a.H_v + h) * D * D);
     if (lane == 0) tma_store_wait_all<0>();
     __syncwarp();
-    if (back && a.h0 != nullptr && n > 0) {  // the gradient of the first row's gate
-      float s = 0.f;
-#pragma unroll
-      for (int x = 0; x < NK; ++x)
-        s = on ? fmaf(a.h0[head + size_t(NK * hh + x) * D + dv], st[x], s) : 0.f;
-      s = warp_sum(s);
-      if (lane == 0) a.h0dh0[(size_t(b) * a.H_v + h) * 8 + warp] = s;
-    }
     if (back && on && a.dh0 != nullptr) {
 #pragma unroll
       for (int x = 0; x < NK; ++x) a.dh0[head + size_t(NK * hh + x) * D + dv] = st[x];
@@ -1401,25 +1395,24 @@ cudaError_t take_err_backward(uint32_t* out) {
 // All products are transposed, M = 128 rows d_k (or, for P and N, the rows of dO
 // above those of beta E), so that two of them share an MMA where they share an
 // operand:
+//   [Q; K] K^T, once
 //   [P; N]       = [dO; beta E] (beta u)^T           K = d_v
 //   [A1 | A2]    = H [dO; beta E]^T                  K = d_v, by halves
 //   A3           = P K,  A4 = P^T Q + N K + N^T K    K = 64
 //   A6           = dH' (beta u)^T                    K = d_v, by halves
 //   dq = scale e^G A1 + A3,  dk = A4 - e^G A2 + e^{G_C - G} A6.
 // Row factors that differ within a product are applied to its result.
-//   warps 0-7: rows u and E to tiles, the masks of P and N, the sums dq, dk, dg;
-//   warps 8-11: states to tiles, in two slots, and <H', dH'>;
-//   warp 12: one thread loads K, Q, dO and issues the MMAs; warp 13: dg.
-// A head's rows are staged while the products of the head before it run, and its P and N
-// are multiplied while those warps sum that head's dq and dk.
+//   warps 0-7: rows u and E to tiles, the masks of P and N, the sums dq, dk and those of dg;
+//   warps 8-11: states to tiles, in two slots, and <H, dH'>;
+//   warp 12: one thread loads dO and issues the MMAs; warp 13: dg; warps 14, 15: Q and K.
+// Between a head's products and sums the row warps stage the next head's rows, as soon as the
+// products that read the last ones are done, so that the slots are free again early.
 // Bound by the latency of the states' loads: 287 us at 4576 rows, 48 heads, 220 if a
 // head's states came for nothing.  Two batches of them are in flight or at work (one at a
 // time: 305 us; four smaller ones 300, single quads 345: a wait for one load is a wait for
 // those issued with it), and they pass by the L1 cache, of which the shared memory leaves
 // some 20 KB (through it: 296 us).  (All 16 warps in step took 320 us, 24 warps 345 us, the
 // same products as warp-level MMAs 400 us.)
-// P and N have two accumulators, a half of d_v each, summed with rounding: the tensor
-// cores' accumulation truncates, and dg sums what it loses over the rows.
 // ---------------------------------------------------------------------------
 
 template <int D>
@@ -1438,7 +1431,7 @@ struct GradsSmem {
   static constexpr int Fac = NH + kBlk;          // two buffers of the unit's factors
   static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
   static constexpr int F = G + 2 * kBC * 8;      // floats from here
-  static constexpr int kFloats = 11 * kBC + 40;
+  static constexpr int kFloats = 5 * kBC + 12 * kBC + kBC + 40;
   static constexpr int Bars = F + kFloats * 4;
   static constexpr int kUsed = Bars + 16 * 8 + 16 + 1024;
   // More than half of an SM's: all of its tensor memory goes to one CTA.
@@ -1450,7 +1443,26 @@ constexpr int kGradsRows = 256, kGradsStates = 128, kGradsThreads = 512;
 constexpr uint32_t kRegsRows = 176, kRegsStates = 112, kRegsIssue = 48;
 enum { gO = 0, gQK, gU, gFull, gFree = gFull + 2, gP = gFree + 2, gPN, gA12, gA345, gA6, gE, gDrain, kGradsBars };
 enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA4 = 256, kTEL = 320, kTA6 = 384,
-       kTPN2 = 448 };  // (kTEL: beta E's low limb in N; kTPN2: P and N's second half over d_v)
+       kTQK = 448 };  // (kTEL: beta E's low limb in N)
+
+// Sums over the warp's lanes of N values each: lane l gets that of value l / (32 / N).
+template <int N>
+__device__ __forceinline__ float sum_over_lanes(float (&x)[N]) {
+  constexpr int step = 32 / N;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int w = N / 2; w >= 1; w >>= 1) {
+    const bool up = lane & (step * w);
+#pragma unroll
+    for (int k = 0; k < w; ++k) {
+      const float send = up ? x[k] : x[k + w];
+      x[k] = (up ? x[k + w] : x[k]) + __shfl_xor_sync(0xffffffffu, send, step * w);
+    }
+  }
+#pragma unroll
+  for (int w = step / 2; w >= 1; w >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], w);
+  return x[0];
+}
 
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -1504,10 +1516,12 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   float* invU2 = reinterpret_cast<float*>(smem + L::F);  // [2][64], by the head's parity
   float* invE2 = invU2 + 2 * kBC;   // [2][64]
   float* endU = invE2 + 2 * kBC;    // invU e^{G_b - G}
-  float* part = endU + kBC;         // [4][64] q . dq of each 32 rows d_k
-  float* vd2 = part + 4 * kBC;      // [2][64] v . dv
-  // by the head's number: [4][8] <H', dH'>, [2][2] 1 / scale of H, dH', [4] H = 0
-  float* red = vd2 + 2 * kBC;
+  // for dg, of the 32 rows d_k or t of each warp: a_t and b_s, W's sums over t with s before the
+  // column; [2][32] W of P's and N's rows 32 .. summed over the columns before 32
+  float *part_a = endU + kBC, *part_b = part_a + 4 * kBC, *part_w = part_b + 4 * kBC;
+  float* row_w = part_w + 4 * kBC;
+  // by the head's number: [4][8] <H, dH'>, [2][2] 1 / scale of H, dH'
+  float* red = row_w + kBC;
   // this warp's part of a tile is written: the issuer may use it
   auto ready = [&](int b) {
     fence_proxy_async_smem();
@@ -1535,8 +1549,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     };
     float dqs[32] = {}, dks[32] = {};
     load_head(h0);
-    // Head h's masks, the next head's rows (while h's last products run), then h's results
-    // (while the next head's P and N are multiplied).
+    // Head h's masks and the sums over d_v, the next head's rows, then h's other sums (while the
+    // next head's P and N are multiplied).
     for (int h = h0 - 1; h < h0 + heads; ++h) {
       const bool on_head = h >= h0, more = h + 1 < h0 + heads;
       const uint32_t ph = (h - h0) & 1;
@@ -1544,7 +1558,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       const float2* Gs = reinterpret_cast<const float2*>(smem + L::G) + (h & 1) * kBC;
       const float *invU = invU2 + kBC * (h & 1), *invE = invE2 + kBC * (h & 1);
       if (on_head) {
-        named_sync(1, kGradsRows);  // the rows' scales; the last head's factors are free
+        // the rows' scales are there, the last head's factors and its parts of dg free
+        named_sync(3, kGradsRows + 32);
         if (more) load_head(h + 1);
         // P and N: lanes 0-63 are rows of P, 64-127 of N
         float x[32];
@@ -1553,10 +1568,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         {
           float y[32];
           tmem_ld32(tl + kTPN, x);
-          tmem_ld32(tl + kTPN2, y);
           tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] += y[k];
           if (qd >= 2) {
             tmem_ld32(tl + kTEL, y);
             tmem_ld_wait();
@@ -1607,6 +1619,65 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           }
         }
         ready(gP);
+        // W, and what of it crosses each row of this half: 0 where t comes before the columns
+        if (ch <= (qd & 1)) {
+#pragma unroll
+          for (int cb = 0; cb < 2; ++cb) {
+            float y[16];
+            tmem_ld16(tl + kTQK + 16 * cb, y);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k)  // (P's diagonal crosses none)
+              x[16 * cb + k] *= 32 * ch + 16 * cb + k == (dk & 63) ? 0.f : y[k];
+          }
+          float run = 0.f;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {  // of the columns before k, for t >= k
+            const float w = x[k];
+            x[k] = ch < (qd & 1) || k <= lane ? run : 0.f;
+            run += w;
+          }
+          if (ch < (qd & 1)) row_w[32 * (qd >> 1) + lane] = run;
+          part_w[qd * kBC + 32 * ch + lane] = sum_over_lanes(x);
+        }
+        // dq, dk and dg, what comes from the states: row d_k of this thread, 2 x 16 chunk rows
+        mbar_wait(&bars[gA12], ph, abort_flag, err, 64u);
+        mbar_wait(&bars[gA6], ph, abort_flag, err, 64u);
+        tc_fence_after();
+        const float ih = red[32 + 2 * (h & 1)], id = red[33 + 2 * (h & 1)];  // the states' scales
+#pragma unroll
+        for (int cb = 0; cb < 2; ++cb) {
+          float x0[16], x1[16], x2[16];
+          const int s0 = 32 * ch + 16 * cb;
+          tmem_ld16(tl + kTA1 + 16 * cb, x0);
+          tmem_ld16(tl + kTA2 + 16 * cb, x1);
+          tmem_ld16(tl + kTA6 + 16 * cb, x2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int r = s0 + k;
+            const float eg = fac[kFeG + r] * ih;
+            const float dq = x0[k] * (eg * fac[kFo + r]), dkh = x1[k] * (eg * invE[r]);
+            const float dkd = x2[k] * (fac[kFeT + r] * (invU[r] * id));
+            dqs[16 * cb + k] += dq;
+            dks[16 * cb + k] += dkd - dkh;
+            float qv = 0.f, kv = 0.f;
+            if (on) {
+              const uint8_t* at = smem + L::QK + (dk >> 6) * L::kQK + sw128_offset(r, (dk & 63) * 2);
+              qv = bf16f(*reinterpret_cast<const uint16_t*>(at));
+              kv = bf16f(*reinterpret_cast<const uint16_t*>(at + kBlk));
+            }
+            x0[k] = fmaf(qv, dq, -(kv * dkh));
+            x1[k] = kv * dkd;
+          }
+          const float sa = sum_over_lanes(x0), sb = sum_over_lanes(x1);
+          if ((lane & 1) == 0) {
+            part_a[qd * kBC + s0 + (lane >> 1)] = sa;
+            part_b[qd * kBC + s0 + (lane >> 1)] = sb;
+          }
+        }
+        ready(gE);
+        named_arrive(2, kGradsRows + 32);  // warp 13 sums dg
       }
       if (more) {
         const int n = h + 1;
@@ -1615,19 +1686,15 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         // Rows 8 w .. 8 w + 7 in two halves, 8 lanes a row, 4 J columns a lane.
         const int l8 = lane & 7;
         float4 u[2][J], e[2][J];
-        uint2 vw[2][J];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const int r = 8 * warp + 4 * m + (lane >> 3);
           const float* up = a.u + unit * kBC * D + r * 32 + 4 * l8;
           const float* ep = a.E + unit * kBC * D + r * 32 + 4 * l8;
-          const uint16_t* vp = a.v + size_t(c.row0 + r) * a.v_stride + n * D + 4 * l8;
 #pragma unroll
           for (int j = 0; j < J; ++j) {
             u[m][j] = __ldcg(reinterpret_cast<const float4*>(up + kBC * 32 * j));
             e[m][j] = __ldcg(reinterpret_cast<const float4*>(ep + kBC * 32 * j));
-            vw[m][j] = make_uint2(0u, 0u);
-            if (r < c.rows) vw[m][j] = *reinterpret_cast<const uint2*>(vp + 32 * j);
           }
         }
         if (tid == 0 && n + 1 < h0 + heads) {
@@ -1635,39 +1702,25 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           prefetch_l2(a.E + (unit + 1) * kBC * D, kBC * D * 4);
         }
         cp_async_wait<0>();  // the factors
-        // Every row warp is here, and warp 13 has read the part and vd of the head before h.
-        if (on_head)
-          named_sync(3, kGradsRows + 32);
-        else
-          named_sync(1, kGradsRows);
-        if (on_head) {  // the products that read u and E are done
-          mbar_wait(&bars[gA12], ph, abort_flag, err, 64u);
-          mbar_wait(&bars[gA6], ph, abort_flag, err, 64u);
-        }
-        // dv, dbeta, v . dv, and the f16 tiles of u and E
+        named_sync(1, kGradsRows);  // ... are there, and every row warp is done with the last tiles
+        // dv, dbeta, and the f16 tiles of u and E
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const int r = 8 * warp + 4 * m + (lane >> 3);
           const float bt = fan[kFbeta + r];
-          float db = 0.f, vs = 0.f, mu = 0.f, me = 0.f;
+          float db = 0.f, mu = 0.f, me = 0.f;
 #pragma unroll
           for (int j = 0; j < J; ++j) {
             float4 &x = u[m][j], &y = e[m][j];
-            const uint2 w = vw[m][j];
             db = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, db))));
             x.x *= bt, x.y *= bt, x.z *= bt, x.w *= bt;
             y.x *= bt, y.y *= bt, y.z *= bt, y.w *= bt;
-            vs = fmaf(__uint_as_float(w.x << 16), y.x, vs);
-            vs = fmaf(__uint_as_float(w.x & 0xffff0000u), y.y, vs);
-            vs = fmaf(__uint_as_float(w.y << 16), y.z, vs);
-            vs = fmaf(__uint_as_float(w.y & 0xffff0000u), y.w, vs);
             mu = max_nan(mu, max_nan(max_nan(fabsf(x.x), fabsf(x.y)), max_nan(fabsf(x.z), fabsf(x.w))));
             me = max_nan(me, max_nan(max_nan(fabsf(y.x), fabsf(y.y)), max_nan(fabsf(y.z), fabsf(y.w))));
           }
 #pragma unroll
           for (int off = 1; off < 8; off <<= 1) {
             db += __shfl_xor_sync(0xffffffffu, db, off);
-            vs += __shfl_xor_sync(0xffffffffu, vs, off);
             mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
             me = fmaxf(me, __shfl_xor_sync(0xffffffffu, me, off));
           }
@@ -1675,7 +1728,6 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           const float su = pow2_scale(mu, &iu), se = pow2_scale(me, &ie);
           if (l8 == 0) {
             if (r < c.rows) a.dbeta[size_t(c.row0 + r) * a.H_v + n] = db;
-            vd2[kBC * (n & 1) + r] = vs;
             invU2[kBC * (n & 1) + r] = iu, invE2[kBC * (n & 1) + r] = ie;
             endU[r] = iu * fan[kFend + r];
           }
@@ -1701,63 +1753,20 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           }
         }
         ready(gU);
-      } else {
-        named_sync(3, kGradsRows + 32);
       }
       if (!on_head) continue;
-      // dq, q . dq and dk: row d_k of this thread, 2 x 16 chunk rows
-      mbar_wait(&bars[gA12], ph, abort_flag, err, 64u);
-      mbar_wait(&bars[gA6], ph, abort_flag, err, 64u);
+      // and what comes from the chunk's own rows
       mbar_wait(&bars[gA345], ph, abort_flag, err, 64u);
       tc_fence_after();
-      {
-        const float ih = red[32 + 2 * (h & 1)], id = red[33 + 2 * (h & 1)];  // the states' scales
 #pragma unroll
-        for (int cb = 0; cb < 2; ++cb) {
-          float x0[16], x1[16], x2[16], x3[16];
-          const int s0 = 32 * ch + 16 * cb;
-          tmem_ld16(tl + kTA1 + 16 * cb, x0);
-          tmem_ld16(tl + kTA3 + 16 * cb, x1);
-          tmem_ld_wait();
+      for (int cb = 0; cb < 2; ++cb) {
+        float x0[16], x1[16];
+        tmem_ld16(tl + kTA3 + 16 * cb, x0);
+        tmem_ld16(tl + kTA4 + 16 * cb, x1);
+        tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float d = fmaf(x0[k], fac[kFeG + s0 + k] * (fac[kFo + s0 + k] * ih), x1[k]);
-            dqs[16 * cb + k] += d;
-            float q = 0.f;
-            if (on)
-              q = bf16f(*reinterpret_cast<const uint16_t*>(
-                      smem + L::QK + (dk >> 6) * L::kQK + sw128_offset(s0 + k, (dk & 63) * 2))) * d;
-            x0[k] = q;
-          }
-          tmem_ld16(tl + kTA2 + 16 * cb, x1);
-          tmem_ld16(tl + kTA4 + 16 * cb, x2);
-          // sum q . dq over the 32 lanes, the 16 rows spread over them
-#pragma unroll
-          for (int w = 8; w >= 1; w >>= 1) {
-            const bool up = lane & (2 * w);
-#pragma unroll
-            for (int k = 0; k < w; ++k) {
-              const float send = up ? x0[k] : x0[k + w];
-              x0[k] = (up ? x0[k + w] : x0[k]) + __shfl_xor_sync(0xffffffffu, send, 2 * w);
-            }
-          }
-          x0[0] += __shfl_xor_sync(0xffffffffu, x0[0], 1);
-          if ((lane & 1) == 0) part[qd * kBC + s0 + (lane >> 1)] = x0[0];
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            dks[16 * cb + k] +=
-                fmaf(x1[k], -fac[kFeG + s0 + k] * (invE[s0 + k] * ih), x2[k]);
-          tmem_ld16(tl + kTA6 + 16 * cb, x3);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            dks[16 * cb + k] +=
-                x3[k] * (fac[kFeT + s0 + k] * (invU[s0 + k] * id));
-        }
+        for (int k = 0; k < 16; ++k) dqs[16 * cb + k] += x0[k], dks[16 * cb + k] += x1[k];
       }
-      ready(gE);
-      named_sync(2, kGradsRows + 32);  // part is there, with vd: warp 13 sums dg
     }
     if constexpr (split) {
       // One head a CTA, the key head's CTAs a cluster: each sums every vpg-th row of all of
@@ -1800,10 +1809,9 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     // across the heads too.
     constexpr int kHalves = D / 64;                   // of d_v
     constexpr int kQuads = D * 16 / kGradsStates;     // of a half: 16 or 8 a thread
-    constexpr int kBatch = kQuads / 2;                // H's; 4 of dH' with 4 of H'
+    constexpr int kBatch = kQuads / 2;                // H's; 4 of dH' with 4 of H
     const size_t unit = size_t(i) * a.H_v + h0;
-    const float* H = a.H + (size_t(i + c.seq) * a.H_v + h0) * D * D;
-    const float* H1 = H + size_t(a.H_v) * D * D;
+    const float* H = a.H + unit * D * D;
     const float* dH = a.dH + unit * D * D;
     const float* hm = a.Hmax + unit * 16 + (lane & 15);
     float4 x[8], y[8];
@@ -1818,7 +1826,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       for (int m = 0; m < 4; ++m) {
         const int at = half * 64 * D + 4 * (t + (q + m) * kGradsStates);
         v[m] = __ldcg(reinterpret_cast<const float4*>(dH + at));
-        v[4 + m] = __ldcg(reinterpret_cast<const float4*>(H1 + at));
+        v[4 + m] = __ldcg(reinterpret_cast<const float4*>(H + at));
       }
     };
     int fills = 0;  // slot fills & 1 is next
@@ -1832,11 +1840,10 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     };
     float largest = *hm;  // lanes 0-7: |H| of a scan warp's part, 8-15: |dH|
     load_h(x, H, 0, 0);
-    for (int h = h0; h < h0 + heads; ++h, H += D * D, H1 += D * D, dH += D * D, hm += 16) {
+    for (int h = h0; h < h0 + heads; ++h, H += D * D, dH += D * D, hm += 16) {
       const bool more = h + 1 < h0 + heads;
       if (t == 0) {  // to L2: what is read soon, and the next head's states
         if (h == h0) prefetch_l2(dH, D * D * 4);
-        prefetch_l2(H1, D * D * 4);
         if (more) {
           prefetch_l2(H + D * D, D * D * 4);
           prefetch_l2(dH + D * D, D * D * 4);
@@ -1846,7 +1853,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       for (int off = 1; off < 8; off <<= 1)
         largest = max_nan(largest, __shfl_xor_sync(0xffffffffu, largest, off));
       float ih, id;
-      const float most = __shfl_sync(0xffffffffu, largest, 0), sh = pow2_scale(most, &ih);
+      const float sh = pow2_scale(__shfl_sync(0xffffffffu, largest, 0), &ih);
       const float sd = pow2_scale(__shfl_sync(0xffffffffu, largest, 8), &id);
 #pragma unroll
       for (int half = 0; half < kHalves; ++half) {
@@ -1857,7 +1864,6 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
         // head before it, whose scales were here.)
         if (half == 0 && t == 0) {
           red[32 + 2 * (h & 1)] = ih, red[33 + 2 * (h & 1)] = id;
-          red[36 + (h & 3)] = most == 0.f;
         }
         quads_to_slot<D, kBatch>(x, t, sh, slot);
         if (half + 1 < kHalves)
@@ -1914,6 +1920,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
     auto desc = [&](uint32_t low) { return uint64_t(kHigh) << 32 | low; };
     constexpr uint32_t id64 = make_idesc_f16(128, 64, 0, 0), id128 = make_idesc_f16(128, 128, 0, 0);
+    constexpr uint32_t id_qk = make_idesc_bf16(128, 64, 0, 0);
     constexpr uint32_t id_a = make_idesc_bf16(128, 64, 1, 0);  // A MN-major
     constexpr uint32_t id_a128 = make_idesc_bf16(128, 128, 1, 0);
     constexpr uint32_t id_ab = make_idesc_bf16(128, 64, 1, 1);  // both MN-major
@@ -1927,9 +1934,12 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     int loads = 1;
     constexpr uint32_t oe = L::OE, el = L::OE + 2 * kBlk, uh = L::UH, ul = L::UL;
     constexpr uint32_t tq = L::QK, tk = L::QK + kBlk;
-    // descriptors: dO and beta E, a slot (64 columns), 64 rows, and those along their columns
+    // descriptors: dO and beta E, Q and K, a slot (64 columns), 64 rows, and those along their columns
     auto out = [&](uint32_t tile, int kk) {
       return desc(b4 + (kKmaj | (tile + (kk >> 2) * L::kOE + (kk & 3) * 32) >> 4));
+    };
+    auto both_qk = [&](uint32_t tile, int kk) {
+      return desc(b4 + (kKmaj | (tile + (kk >> 2) * L::kQK + (kk & 3) * 32) >> 4));
     };
     auto slot = [&](int fill, int limb, int kk) {
       return desc(b4 + (kKmaj | (L::H + (fill & 1) * L::kSlot + limb * 2 * kBlk + (kk & 3) * 32) >> 4));
@@ -1940,6 +1950,11 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     auto rows = [&](uint32_t tile, int kk) { return desc(b4 + (kMnmaj | (tile + kk * 2048) >> 4)); };
     bool ok = true;
     int fills = 0;
+    ok = mbar_wait(&bars[gQK], 0, abort_flag, err, 128u);
+    tc_fence_after();
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      mma_bf16_ss(tmem + kTQK, both_qk(tq, kk), both_qk(tk, kk), id_qk, kk != 0);
     for (int h = h0; h < h0 + heads && ok; ++h) {
       const uint32_t ph = (h - h0) & 1;
       ok = mbar_wait(&bars[gO], ph, abort_flag, err, 128u) &&
@@ -1948,11 +1963,10 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + (kk < D / 32 ? kTPN : kTPN2), out(oe, kk), flat(ul, kk), id64,
-                    kk % (D / 32) != 0);
+        mma_bf16_ss(tmem + kTPN, out(oe, kk), flat(ul, kk), id64, kk != 0);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16_ss(tmem + (kk < D / 32 ? kTPN : kTPN2), out(oe, kk), flat(uh, kk), id64, 1u);
+        mma_bf16_ss(tmem + kTPN, out(oe, kk), flat(uh, kk), id64, 1u);
       // (rows 64 to 127 of this one: beta E's low limb)
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
@@ -2004,9 +2018,6 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       ok = mbar_wait(&bars[gP], ph, abort_flag, err, 128u);
       if (!ok) break;
       tc_fence_after();
-      if (h == h0) ok = mbar_wait(&bars[gQK], 0, abort_flag, err, 128u);
-      if (!ok) break;
-      tc_fence_after();
       // A limb of P and that of N are one tile of 128 rows, A3 and A4 side by side.
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
@@ -2044,48 +2055,49 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     for (int h = h0; h < h0 + heads; ++h) {
       named_sync(3, kGradsRows + 32);
       named_sync(2, kGradsRows + 32);
-      // dg: suffix sums over the rows, two per lane, on top of <H', dH'>
-      double z[2], run;
+      // Two rows a lane, 2 l and 2 l + 1: sums of a from the row on, of b before it, and of W; of
+      // row_w, for the rows 32 .., from the row on.
+      double up[2], down[2], far[2], own[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int rr = 63 - (2 * lane + k);
-        float sum = 0.f;
+        const int r = 2 * lane + k;
+        float sa = 0.f, sb = 0.f, sw = 0.f;
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) sum += part[w * kBC + rr];
-        z[k] = rr < c.rows ? double(sum) - double(vd2[kBC * (h & 1) + rr]) : 0.0;
+        for (int w = 0; w < D / 32; ++w) sa += part_a[w * kBC + r], sb += part_b[w * kBC + r];
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (r < 32 || w & 1) sw += part_w[w * kBC + r];
+        up[k] = sa, down[k] = sb, own[k] = sw;
+        far[k] = r < 32 ? 0.0 : double(row_w[r - 32]) + double(row_w[r]);
       }
-      z[1] += z[0];
-      run = z[1];
+      double run_a = up[0] + up[1], run_f = far[0] + far[1], run_b = down[0] + down[1];
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const double w = __shfl_up_sync(0xffffffffu, run, off);
-        if (lane >= off) run += w;
+        const double wa = __shfl_down_sync(0xffffffffu, run_a, off);
+        const double wf = __shfl_down_sync(0xffffffffu, run_f, off);
+        const double wb = __shfl_up_sync(0xffffffffu, run_b, off);
+        if (lane + off < 32) run_a += wa, run_f += wf;
+        if (lane >= off) run_b += wb;
       }
+      // (the sums before and behind the lane's rows as sums, not as differences: nothing cancels)
+      double next_a = __shfl_down_sync(0xffffffffu, run_a, 1);
+      double next_f = __shfl_down_sync(0xffffffffu, run_f, 1);
+      double prev_b = __shfl_up_sync(0xffffffffu, run_b, 1);
+      if (lane == 31) next_a = next_f = 0.0;
+      if (lane == 0) prev_b = 0.0;
+      const float* fac = reinterpret_cast<const float*>(smem + L::Fac) + (h & 1) * kFac;
       double hh = 0.0;
 #pragma unroll
       for (int w = 0; w < kGradsStates / 32; ++w) hh += red[8 * (h & 3) + w];
-      z[0] += run - z[1] + hh;
-      z[1] = run + hh;
-      // The chunk's first row has a second value, <H, e^{-G} dH> with the entry state:
-      // 0 for a zero state, <h0, dh0> for the sequence's first chunk.  What the sums miss of
-      // it they have gathered over the rows: it is shared out along them.
-      const float* first = a.h0dh0 + (size_t(c.seq) * a.H_v + h) * 8;
-      const bool zero = red[36 + (h & 3)] != 0.f;
-      if (zero || (a.h0 != nullptr && i == a.cu_chunks[c.seq])) {
-        double miss = -__shfl_sync(0xffffffffu, z[1], 31);
-        if (!zero) {
-          for (int w = 0; w < 8; ++w) miss += first[w];
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int rr = 63 - (2 * lane + k);
-          if (rr < c.rows) z[k] += rr == 0 ? miss : miss * double(c.rows - rr) / double(c.rows);
-        }
-      }
+      hh *= fac[kFeC];
+      const double z[2] = {hh + (next_a + up[1] + up[0]) + prev_b + own[0] +
+                               (lane < 16 ? 0.0 : next_f + far[1] + far[0]),
+                           hh + (next_a + up[1]) + (prev_b + down[0]) + own[1] +
+                               (lane < 16 ? 0.0 : next_f + far[1])};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int rr = 63 - (2 * lane + k);
-        if (rr < c.rows) a.dg[size_t(c.row0 + rr) * a.H_v + h] = float(z[k]);
+        const int r = 2 * lane + k;
+        if (r < c.rows) a.dg[size_t(c.row0 + r) * a.H_v + h] = float(z[k]);
       }
     }
    }
@@ -2129,10 +2141,9 @@ size_t layout(BwdArgs* a, char* base, int total_tokens, int num_seqs, int H_k, i
   a->G = reinterpret_cast<float2*>(take(units * kBC * 8));
   a->u = reinterpret_cast<float*>(take(units * kBC * D * 4));
   a->E = reinterpret_cast<float*>(take(units * kBC * D * 4));
-  a->H = reinterpret_cast<float*>(take((mc + num_seqs) * size_t(H_v) * D * D * 4));
+  a->H = reinterpret_cast<float*>(take(units * D * D * 4));
   a->dH = reinterpret_cast<float*>(take(units * D * D * 4));
   a->Hmax = reinterpret_cast<float*>(take(units * 2 * 8 * 4));
-  a->h0dh0 = reinterpret_cast<float*>(take(size_t(num_seqs) * H_v * 8 * 4));
   return at;
 }
 

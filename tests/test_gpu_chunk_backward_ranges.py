@@ -187,3 +187,37 @@ def test_a_bad_output_gradient_stays_in_its_row_of_dq(value, d):
     got = gdn_chunk_backward(*dev, cu, do.to(DEV), h0=h0.to(DEV), dhT=dhT.to(DEV))[0]
     assert torch.equal(got[:40], want[:40]) and torch.equal(got[41:], want[41:])
     assert not torch.isfinite(got[40]).all() or value == 3e38
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shift", [0.0, -1.0, -3.0, -5.0, -8.0, -30.0])
+def test_gate_gradients_under_decays(shift, d):
+    """dg_r has the decay e^g_r itself: its accuracy is relative to that, however strong it is."""
+    lens = [150, 7]
+    rows, do, h0, dhT = _case(lens, 1, 2, d, seed=9)
+    rows[3] += shift
+    dev = [x.to(DEV) for x in rows]
+    cu = torch.tensor(R.offsets(lens), dtype=torch.int32, device=DEV)
+    got = gdn_chunk_backward(*dev, cu, do.to(DEV), h0=h0.to(DEV), dhT=dhT.to(DEV))[3]
+    want = R.backward(*dev, lens, do.to(DEV), h0.to(DEV), dhT.to(DEV))[3]
+    print(R.rel(got, want))
+    assert R.rel(got, want) <= R.F32_REL
+    # against e^g as well: with gates of many sizes the norm alone shows the weakest
+    size = rows[3].double().exp().to(DEV)
+    assert R.rel(got.double() / size, want / size) <= R.F32_REL
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cut", [1, 15, 16, 31, 32, 33, 47, 63, 64, 100])
+def test_one_strong_gate(cut, d):
+    """One row forgets nearly everything: its dg is e^-25 of its neighbours'."""
+    lens = [130]
+    rows, do, h0, dhT = _case(lens, 1, 2, d, seed=10)
+    rows[3][cut] = -25.0
+    dev = [x.to(DEV) for x in rows]
+    cu = torch.tensor(R.offsets(lens), dtype=torch.int32, device=DEV)
+    got = gdn_chunk_backward(*dev, cu, do.to(DEV), h0=h0.to(DEV), dhT=dhT.to(DEV))[3]
+    want = R.backward(*dev, lens, do.to(DEV), h0.to(DEV), dhT.to(DEV))[3]
+    assert R.rel(got, want) <= R.F32_REL
+    # a single sum of some 10^4 products, which may cancel to a tenth of their size
+    assert R.rel(got[cut], want[cut]) <= 10 * R.F32_REL
