@@ -1397,13 +1397,13 @@ cudaError_t take_err_backward(uint32_t* out) {
 // operand:
 //   [Q; K] K^T, once
 //   [P; N]       = [dO; beta E] (beta u)^T           K = d_v
-//   [A1 | A2]    = H [dO; beta E]^T                  K = d_v, by halves
-//   A3           = P K,  A4 = P^T Q + N K + N^T K    K = 64
+//   [A1 | A2]    = H [dO; beta E]^T                  K = d_v, by halves, in turn with
 //   A6           = dH' (beta u)^T                    K = d_v, by halves
+//   A3           = P K,  A4 = P^T Q + N K + N^T K    K = 64
 //   dq = scale e^G A1 + A3,  dk = A4 - e^G A2 + e^{G_C - G} A6.
 // Row factors that differ within a product are applied to its result.
 //   warps 0-7: rows u and E to tiles, the masks of P and N, the sums dq, dk and those of dg;
-//   warps 8-11: states to tiles, in two slots, and <H, dH'>;
+//   warps 8-11: states to limbs, in two slots, and <H, dH'>;
 //   warp 12: one thread loads dO and issues the MMAs; warp 13: dg; warps 14, 15: Q and K.
 // Between a head's products and sums the row warps stage the next head's rows, as soon as the
 // products that read the last ones are done, so that the slots are free again early.
@@ -1423,7 +1423,8 @@ struct GradsSmem {
   // dO, beta E high and beta E low, likewise
   static constexpr int OE = D / 64 * kQK, kOE = 3 * kBlk;
   static constexpr int UH = OE + D / 64 * kOE, UL = UH + kTile;  // beta u, two limbs
-  // Two slots for 64 columns (d_v) of H or dH' with 128 rows: high limb, low limb
+  // Slots for 64 columns (d_v) of H and of dH', as they are (f32, slices of 16 columns), then
+  // in the same place as limbs with 128 rows, high and low
   static constexpr int H = UL + kTile, kSlot = 4 * kBlk;
   // bf16 limbs of P (high, middle, low) and N (high, middle)
   static constexpr int PL = H + 2 * kSlot, PM = PL + kBlk, NM = PM + kBlk, PH = NM + kBlk,
@@ -1441,7 +1442,8 @@ struct GradsSmem {
 constexpr int kGradsRows = 256, kGradsStates = 128, kGradsThreads = 512;
 // Registers after re-allocation: 128 (2 x 176 + 112 + 48) is the launch's 512 x 128.
 constexpr uint32_t kRegsRows = 176, kRegsStates = 112, kRegsIssue = 48;
-enum { gO = 0, gQK, gU, gFull, gFree = gFull + 2, gP = gFree + 2, gPN, gA12, gA345, gA6, gE, gDrain, kGradsBars };
+enum { gO = 0, gQK, gU, gLand, gFull = gLand + 2, gFree = gFull + 2, gP = gFree + 2, gPN, gStates,
+       gA34, gE, gDrain, kGradsBars };
 enum { kTPN = 0, kTA1 = 64, kTA2 = 128, kTA3 = 192, kTA4 = 256, kTEL = 320, kTA6 = 384,
        kTQK = 448 };  // (kTEL: beta E's low limb in N)
 
@@ -1468,20 +1470,11 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-// B quads (float4, the first of v) of 64 columns of a state into a slot's tiles: quad q is thread
-// q's, so a warp loads 512 contiguous bytes.
-template <int D, int B>
-__device__ __forceinline__ void quads_to_slot(const float4 (&v)[8], int q0, float s, uint32_t slot) {
-#pragma unroll
-  for (int m = 0; m < B; ++m) {
-    const int x = q0 + m * kGradsStates;  // slice of 16 columns, d_k, quad
-    const uint32_t to = slot + sw128_offset((x >> 2) % D, (x / (4 * D) * 16 + (x & 3) * 4) * 2);
-    uint32_t h0, h1, l0, l1;
-    split_f16(v[m].x * s, v[m].y * s, h0, l0);
-    split_f16(v[m].z * s, v[m].w * s, h1, l1);
-    st_shared_v2(to, h0, h1);
-    st_shared_v2(to + 2 * kBlk, l0, l1);
-  }
+// Quad q of 64 columns of a state (slice of 16 columns, d_k, quad): where its limbs are in the
+// slot's tile.
+template <int D>
+__device__ __forceinline__ uint32_t quad_place(int q) {
+  return sw128_offset((q >> 2) % D, (q / (4 * D) * 16 + (q & 3) * 4) * 2);
 }
 
 template <int D, bool split>
@@ -1641,8 +1634,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           part_w[qd * kBC + 32 * ch + lane] = sum_over_lanes(x);
         }
         // dq, dk and dg, what comes from the states: row d_k of this thread, 2 x 16 chunk rows
-        mbar_wait(&bars[gA12], ph, abort_flag, err, 64u);
-        mbar_wait(&bars[gA6], ph, abort_flag, err, 64u);
+        mbar_wait(&bars[gStates], ph, abort_flag, err, 64u);
         tc_fence_after();
         const float ih = red[32 + 2 * (h & 1)], id = red[33 + 2 * (h & 1)];  // the states' scales
 #pragma unroll
@@ -1756,7 +1748,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       }
       if (!on_head) continue;
       // and what comes from the chunk's own rows
-      mbar_wait(&bars[gA345], ph, abort_flag, err, 64u);
+      mbar_wait(&bars[gA34], ph, abort_flag, err, 64u);
       tc_fence_after();
 #pragma unroll
       for (int cb = 0; cb < 2; ++cb) {
@@ -1805,108 +1797,93 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   } else if (warp < 12) {
     setmaxnreg_dec<kRegsStates>();
     const int t = tid - kGradsRows;
-    // Two buffers of quads: while one is worked on, the other one's loads are in flight,
-    // across the heads too.
-    constexpr int kHalves = D / 64;                   // of d_v
-    constexpr int kQuads = D * 16 / kGradsStates;     // of a half: 16 or 8 a thread
-    constexpr int kBatch = kQuads / 2;                // H's; 4 of dH' with 4 of H
+    // By halves of d_v: H's f32 values come to its slot by a bulk copy, those of dH' to the other,
+    // and are turned into limbs there.  The next half's copies start when both have been multiplied.
+    constexpr int kHalves = D / 64, kBytes = 64 * D * 4;
+    constexpr int kQuads = kBytes / 16 / kGradsStates;  // 16 or 8 a thread
     const size_t unit = size_t(i) * a.H_v + h0;
-    const float* H = a.H + unit * D * D;
-    const float* dH = a.dH + unit * D * D;
+    const uint32_t slot_h = base + L::H, slot_d = slot_h + L::kSlot;
+    auto load = [&](int p) {  // the p-th half of the CTA's states
+      const size_t at = unit * D * D + size_t(p) * 64 * D;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        mbar_arrive_expect_tx(&bars[gLand + x], kBytes);
+        bulk_load_g2s(smem + L::H + x * L::kSlot, (x ? a.dH : a.H) + at, kBytes, &bars[gLand + x]);
+      }
+    };
     const float* hm = a.Hmax + unit * 16 + (lane & 15);
-    float4 x[8], y[8];
-    auto load_h = [&](float4 (&v)[8], const float* from, int half, int q) {
-#pragma unroll
-      for (int m = 0; m < kBatch; ++m)
-        v[m] = __ldcg(reinterpret_cast<const float4*>(
-            from + half * 64 * D + 4 * (t + (q + m) * kGradsStates)));
-    };
-    auto load_d = [&](float4 (&v)[8], int half, int q) {
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int at = half * 64 * D + 4 * (t + (q + m) * kGradsStates);
-        v[m] = __ldcg(reinterpret_cast<const float4*>(dH + at));
-        v[4 + m] = __ldcg(reinterpret_cast<const float4*>(H + at));
-      }
-    };
-    int fills = 0;  // slot fills & 1 is next
-    auto slot_free = [&]() {  // what was there has been multiplied
-      if (fills >= 2)
-        mbar_wait(&bars[gFree + (fills & 1)], (fills >> 1 & 1) ^ 1, abort_flag, err, 64u);
-    };
-    auto slot_full = [&]() {
-      ready(gFull + (fills & 1));
-      ++fills;
-    };
     float largest = *hm;  // lanes 0-7: |H| of a scan warp's part, 8-15: |dH|
-    load_h(x, H, 0, 0);
-    for (int h = h0; h < h0 + heads; ++h, H += D * D, dH += D * D, hm += 16) {
-      const bool more = h + 1 < h0 + heads;
-      if (t == 0) {  // to L2: what is read soon, and the next head's states
-        if (h == h0) prefetch_l2(dH, D * D * 4);
-        if (more) {
-          prefetch_l2(H + D * D, D * D * 4);
-          prefetch_l2(dH + D * D, D * D * 4);
-        }
-      }
+    if (t == 0) load(0);
+    int p = 0, loads = 1;
+    const int halves = heads * kHalves;
+    bool ok = true;
+    for (int h = h0; h < h0 + heads; ++h, hm += 16) {
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1)
         largest = max_nan(largest, __shfl_xor_sync(0xffffffffu, largest, off));
       float ih, id;
       const float sh = pow2_scale(__shfl_sync(0xffffffffu, largest, 0), &ih);
       const float sd = pow2_scale(__shfl_sync(0xffffffffu, largest, 8), &id);
-#pragma unroll
-      for (int half = 0; half < kHalves; ++half) {
-        const uint32_t slot = base + L::H + (fills & 1) * L::kSlot;
-        load_h(y, H, half, kBatch);
-        slot_free();
-        // (A product of the last head has freed the slot, so the rows' warps are done with the
-        // head before it, whose scales were here.)
-        if (half == 0 && t == 0) {
-          red[32 + 2 * (h & 1)] = ih, red[33 + 2 * (h & 1)] = id;
-        }
-        quads_to_slot<D, kBatch>(x, t, sh, slot);
-        if (half + 1 < kHalves)
-          load_h(x, H, half + 1, 0);
-        else
-          load_d(x, 0, 0);
-        quads_to_slot<D, kBatch>(y, t + kBatch * kGradsStates, sh, slot);
-        slot_full();
-      }
+      if (h + 1 < h0 + heads) largest = hm[16];
       float hh = 0.f;
-      auto dot = [&](const float4 (&v)[8]) {
+#pragma unroll 1
+      for (int half = 0; half < kHalves; ++half, ++p) {
+        if (t == 0 && p + 1 < halves) {  // the next half to L2
+          prefetch_l2(a.H + unit * D * D + size_t(p + 1) * 64 * D, kBytes);
+          prefetch_l2(a.dH + unit * D * D + size_t(p + 1) * 64 * D, kBytes);
+        }
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-          hh += fmaf(v[m].x, v[4 + m].x, v[m].y * v[4 + m].y) +
-                fmaf(v[m].z, v[4 + m].z, v[m].w * v[4 + m].w);
-      };
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t slot = x ? slot_d : slot_h;
+          float4 v[kQuads];
+          ok = mbar_wait(&bars[gLand + x], p & 1, abort_flag, err, 64u) && ok;
 #pragma unroll
-      for (int half = 0; half < kHalves; ++half) {
-        const uint32_t slot = base + L::H + (fills & 1) * L::kSlot;
+          for (int m = 0; m < kQuads; ++m)
+            v[m] = *reinterpret_cast<const float4*>(smem + L::H + x * L::kSlot +
+                                                    16 * (t + m * kGradsStates));
+          if (x) {  // <H, dH'>, H from its limbs
 #pragma unroll
-        for (int q = 0; q < kQuads; q += 8) {
-          load_d(y, half, q + 4);
-          if (q == 0) slot_free();
-          dot(x);
-          quads_to_slot<D, 4>(x, t + q * kGradsStates, sd, slot);
-          if (q + 8 < kQuads) {
-            load_d(x, half, q + 8);
-          } else if (half + 1 < kHalves) {
-            load_d(x, half + 1, 0);
-          } else if (more) {
-            largest = hm[16];
-            load_h(x, H + D * D, 0, 0);
+            for (int m = 0; m < kQuads; ++m) {
+              const uint32_t at = L::H + quad_place<D>(t + m * kGradsStates);
+              const uint2 hi = *reinterpret_cast<const uint2*>(smem + at);
+              const uint2 lo = *reinterpret_cast<const uint2*>(smem + at + 2 * kBlk);
+              const float2 a0 = add2(unpack_f16(hi.x), unpack_f16(lo.x));
+              const float2 a1 = add2(unpack_f16(hi.y), unpack_f16(lo.y));
+              hh += fmaf(a0.x, v[m].x, a0.y * v[m].y) + fmaf(a1.x, v[m].z, a1.y * v[m].w);
+            }
           }
-          dot(y);
-          quads_to_slot<D, 4>(y, t + (q + 4) * kGradsStates, sd, slot);
+          named_sync(4, kGradsStates);  // all have read
+          const float s = x ? sd : sh;
+#pragma unroll
+          for (int m = 0; m < kQuads; ++m) {
+            const uint32_t to = slot + quad_place<D>(t + m * kGradsStates);
+            uint32_t p0, p1, q0, q1;
+            split_f16(v[m].x * s, v[m].y * s, p0, q0);
+            split_f16(v[m].z * s, v[m].w * s, p1, q1);
+            st_shared_v2(to, p0, p1);
+            st_shared_v2(to + 2 * kBlk, q0, q1);
+          }
+          if (x == 0 && half == 0 && t == 0) {
+            // (The last head's states have been multiplied, so the rows' warps are done with the
+            // head before it, whose scales were here.)
+            red[32 + 2 * (h & 1)] = ih, red[33 + 2 * (h & 1)] = id;
+          }
+          if (x && half + 1 == kHalves) {
+            hh = warp_sum(hh) * ih;
+            if (lane == 0) red[8 * (h & 3) + warp - 8] = hh;
+          }
+          ready(gFull + x);
         }
-        if (half + 1 == kHalves) {
-          hh = warp_sum(hh);
-          if (lane == 0) red[8 * (h & 3) + warp - 8] = hh;
+        if (t == 0 && p + 1 < halves) {  // (the second one: every warp has passed its fence)
+          ok = mbar_wait(&bars[gFree], p & 1, abort_flag, err, 64u) && ok;
+          ok = mbar_wait(&bars[gFree + 1], p & 1, abort_flag, err, 64u) && ok;
+          if (ok) load(p + 1), ++loads;
         }
-        slot_full();
+        __syncwarp();
       }
     }
+    if (t == 0)  // nothing may still be landing in shared memory at exit
+      for (int x = 0; x < 2; ++x) mbar_wait(&bars[gLand + x], (loads - 1) & 1, nullptr, err, 32u);
     if constexpr (split) cluster_sync(), cluster_sync();
   } else {
    setmaxnreg_dec<kRegsIssue>();
@@ -1915,7 +1892,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     // Descriptors: the high word is a constant, the low one an address and the (for the
     // K-major tiles unused) distance of 64-column blocks.
     // (In a cluster the address has the CTA's rank above its low 18 bits.)
-    const uint32_t b4 = (split ? base & 0x3ffffu : base) >> 4;
+    uint32_t b4 = (split ? base & 0x3ffffu : base) >> 4;
     constexpr uint32_t kKmaj = 1u << 16, kMnmaj = (uint32_t(L::kQK) >> 4) << 16;
     constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
     auto desc = [&](uint32_t low) { return uint64_t(kHigh) << 32 | low; };
@@ -1941,15 +1918,15 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     auto both_qk = [&](uint32_t tile, int kk) {
       return desc(b4 + (kKmaj | (tile + (kk >> 2) * L::kQK + (kk & 3) * 32) >> 4));
     };
-    auto slot = [&](int fill, int limb, int kk) {
-      return desc(b4 + (kKmaj | (L::H + (fill & 1) * L::kSlot + limb * 2 * kBlk + (kk & 3) * 32) >> 4));
+    auto slot = [&](int x, int limb, int kk) {
+      return desc(b4 + (kKmaj | (L::H + x * L::kSlot + limb * 2 * kBlk + (kk & 3) * 32) >> 4));
     };
     auto flat = [&](uint32_t tile, int kk) {
       return desc(b4 + (kKmaj | (tile + (kk >> 2) * kBlk + (kk & 3) * 32) >> 4));
     };
     auto rows = [&](uint32_t tile, int kk) { return desc(b4 + (kMnmaj | (tile + kk * 2048) >> 4)); };
     bool ok = true;
-    int fills = 0;
+    int p = 0;  // halves of states
     ok = mbar_wait(&bars[gQK], 0, abort_flag, err, 128u);
     tc_fence_after();
 #pragma unroll
@@ -1957,6 +1934,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       mma_bf16_ss(tmem + kTQK, both_qk(tq, kk), both_qk(tk, kk), id_qk, kk != 0);
     for (int h = h0; h < h0 + heads && ok; ++h) {
       const uint32_t ph = (h - h0) & 1;
+      asm volatile("" : "+r"(b4));  // (a hundred descriptors are made where they are needed, not kept)
       ok = mbar_wait(&bars[gO], ph, abort_flag, err, 128u) &&
            mbar_wait(&bars[gU], ph, abort_flag, err, 128u);
       if (!ok) break;
@@ -1976,40 +1954,36 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       if (h > h0) ok = mbar_wait(&bars[gE], ph ^ 1, abort_flag, err, 128u);
       if (!ok) break;
 #pragma unroll 1
-      for (int k0 = 0; k0 < D / 16 && ok; k0 += 4, ++fills) {  // by halves of d_v
-        ok = mbar_wait(&bars[gFull + (fills & 1)], fills >> 1 & 1, abort_flag, err, 128u);
+      for (int k0 = 0; k0 < D / 16; k0 += 4, ++p) {  // by halves of d_v
+        asm volatile("" : "+r"(b4));
+        ok = mbar_wait(&bars[gFull], p & 1, abort_flag, err, 128u);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_bf16_ss(tmem + kTA1, slot(fills, 1, kk), out(oe, k0 + kk), id128, k0 + kk != 0);
+          mma_bf16_ss(tmem + kTA1, slot(0, 1, kk), out(oe, k0 + kk), id128, k0 + kk != 0);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_bf16_ss(tmem + kTA2, slot(fills, 0, kk), out(el, k0 + kk), id64, 1u);
+          mma_bf16_ss(tmem + kTA2, slot(0, 0, kk), out(el, k0 + kk), id64, 1u);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_bf16_ss(tmem + kTA1, slot(fills, 0, kk), out(oe, k0 + kk), id128, 1u);
-        mma_commit(&bars[gFree + (fills & 1)]);
-      }
-      if (!ok) break;
-      mma_commit(&bars[gA12]);
-#pragma unroll 1
-      for (int k0 = 0; k0 < D / 16 && ok; k0 += 4, ++fills) {
-        ok = mbar_wait(&bars[gFull + (fills & 1)], fills >> 1 & 1, abort_flag, err, 128u);
+          mma_bf16_ss(tmem + kTA1, slot(0, 0, kk), out(oe, k0 + kk), id128, 1u);
+        mma_commit(&bars[gFree]);
+        ok = mbar_wait(&bars[gFull + 1], p & 1, abort_flag, err, 128u);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int x = 0; x < 3; ++x)  // low x high, high x low, high x high
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_ss(tmem + kTA6, slot(fills, x == 0, kk), flat(x == 1 ? ul : uh, k0 + kk), id64,
+            mma_bf16_ss(tmem + kTA6, slot(1, x == 0, kk), flat(x == 1 ? ul : uh, k0 + kk), id64,
                         k0 + kk + x != 0);
-        mma_commit(&bars[gFree + (fills & 1)]);
+        mma_commit(&bars[gFree + 1]);
       }
       if (!ok) break;
-      mma_commit(&bars[gA6]);
+      mma_commit(&bars[gStates]);
       if (h + 1 < h0 + heads) {  // dO's last reader is done
-        ok = mbar_wait(&bars[gA12], ph, abort_flag, err, 128u);
+        ok = mbar_wait(&bars[gStates], ph, abort_flag, err, 128u);
         if (!ok) break;
         mbar_arrive_expect_tx(&bars[gO], L::kTile);
         load_o(h + 1);
@@ -2035,7 +2009,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           mma_bf16_ss(tmem + kTA4, rows(tq, kk), rows(x ? L::PH : L::PM, kk), id_ab, 1u);
           mma_bf16_ss(tmem + kTA4, rows(tk, kk), rows(x ? L::NH : L::NM, kk), id_ab, 1u);
         }
-      mma_commit(&bars[gA345]);
+      mma_commit(&bars[gA34]);
     }
     mma_commit(&bars[gDrain]);
     mbar_wait(&bars[gDrain], 0, nullptr, err, 32u);
