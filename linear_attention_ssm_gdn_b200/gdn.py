@@ -353,7 +353,8 @@ def gdn_decode(h_table, q, k, v, g, beta, cu_seqlens=None, o=None, scale=1.0, st
     """The recurrent form: each sequence's state takes its new rows in place.
     h_table: int64 CUDA tensor [batch] of state pointers (0 = padding sequence);
     cu_seqlens: int32 [batch + 1] row offsets, or None for one row per sequence.
-    Returns o [rows, H_v, d] bf16 (rows of no sequence are not written)."""
+    Returns o [rows, H_v, d] bf16; rows of no sequence are not written: they keep what a
+    given `o` holds, and hold anything in a new one."""
     _need(h_table, torch.int64, "h_table")
     R, H_k, H_v, d_k, d_v, qk_stride, v_stride, gb_stride = _qkv(q, k, v, g, beta)
     device = q.device
@@ -469,17 +470,22 @@ def gdn_chunk_backward_workspace_bytes(total_tokens, num_seqs, H_k, H_v, d_k, d_
 
 
 def gdn_chunk_backward(q, k, v, g, beta, cu_seqlens, do, h0=None, dhT=None, dh0=None, scale=1.0,
-                       workspace=None, stream=None):
+                       workspace=None, stream=None, dq=None, dk=None, dv=None, dg=None,
+                       dbeta=None):
     """Gradients of gdn_chunk_prefill(q, k, v, g, beta, cu_seqlens, h0) from do
     [T, H_v, d] bf16 and dhT [N, H_v, d, d] f32 (None = zeros).  Returns (dq, dk,
-    dv, dg, dbeta, dh0); dh0 is None unless h0 or a dh0 buffer is given."""
+    dv, dg, dbeta, dh0), in the buffers that are given for them; dh0 is None unless
+    h0 or a dh0 buffer is given.  Rows of no sequence are not written: they keep what
+    a given buffer holds, and hold anything in a new one.  So where a batch has such rows
+    (padding) and their gradients are read, give buffers, zeroed once.  `workspace` is
+    allocated by the call unless it is given."""
     T, H_k, H_v, d_k, d_v, qk_stride, v_stride, gb_stride = _qkv(q, k, v, g, beta)
     device = q.device
     handle = _current(device, stream)
     if handle is None:
         with _switched(device, stream) as handle:
             return gdn_chunk_backward(q, k, v, g, beta, cu_seqlens, do, h0, dhT, dh0, scale,
-                                      workspace)
+                                      workspace, None, dq, dk, dv, dg, dbeta)
     _expect(cu_seqlens, torch.int32, (cu_seqlens.shape[0],), "cu_seqlens")
     N = cu_seqlens.shape[0] - 1
     _expect(do, torch.bfloat16, (T, H_v, d_v), "do")
@@ -490,11 +496,19 @@ def gdn_chunk_backward(q, k, v, g, beta, cu_seqlens, do, h0=None, dhT=None, dh0=
         raise ValueError("workspace: must be contiguous")
     _same_device(device, k, v, g, beta, cu_seqlens, do, h0, dhT, dh0, workspace)
     lib = _lib.load()
-    dq = torch.empty(T, H_k, d_k, dtype=torch.bfloat16, device=device)
-    dk = torch.empty_like(dq)
-    dv = torch.empty(T, H_v, d_v, dtype=torch.bfloat16, device=device)
-    dg = torch.empty(T, H_v, dtype=torch.float32, device=device)
-    dbeta = torch.empty_like(dg)
+
+    def gradient(t, name, dtype, *shape):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        _expect(t, dtype, shape, name)
+        _same_device(device, t)
+        return t
+
+    dq = gradient(dq, "dq", torch.bfloat16, T, H_k, d_k)
+    dk = gradient(dk, "dk", torch.bfloat16, T, H_k, d_k)
+    dv = gradient(dv, "dv", torch.bfloat16, T, H_v, d_v)
+    dg = gradient(dg, "dg", torch.float32, T, H_v)
+    dbeta = gradient(dbeta, "dbeta", torch.float32, T, H_v)
     if dh0 is None and h0 is not None:
         dh0 = torch.empty(N, H_v, d_k, d_v, dtype=torch.float32, device=device)
     if workspace is None:

@@ -221,3 +221,40 @@ def test_one_strong_gate(cut, d):
     assert R.rel(got, want) <= R.F32_REL
     # a single sum of some 10^4 products, which may cancel to a tenth of their size
     assert R.rel(got[cut], want[cut]) <= 10 * R.F32_REL
+
+
+@pytest.mark.parametrize("given", [("dq", "dk", "dv", "dg", "dbeta"), ("dk", "dg")])
+def test_gradients_into_given_buffers(given):
+    """Rows before, between and behind the sequences keep what the buffers hold."""
+    lens, spare, d = [70, 0, 33], 5, 64
+    rows, do, h0, dhT = _case(lens, 2, 4, d, seed=11)
+    T = sum(lens) + 2 * spare
+    dev = [torch.cat([x[:spare], x, x[:spare]]).to(DEV) for x in (*rows, do)]
+    cu = torch.tensor([spare + x for x in R.offsets(lens)], dtype=torch.int32, device=DEV)
+    shapes = {"dq": (T, 2, d), "dk": (T, 2, d), "dv": (T, 4, d), "dg": (T, 4), "dbeta": (T, 4)}
+    bufs = {n: torch.full(shapes[n], 7.0, device=DEV,
+                          dtype=torch.bfloat16 if n in NAMES[:3] else torch.float32) for n in given}
+    got = gdn_chunk_backward(*dev[:5], cu, dev[5], h0=h0.to(DEV), dhT=dhT.to(DEV), **bufs)
+    want = gdn_chunk_backward(*[x[spare:-spare].contiguous() for x in dev[:5]],
+                              (cu - spare).contiguous(), dev[5][spare:-spare].contiguous(),
+                              h0=h0.to(DEV), dhT=dhT.to(DEV))
+    for name, x, y in zip(NAMES, got, want):
+        if name != "dh0":
+            assert torch.equal(x[spare:-spare], y), name
+        if name in bufs:
+            assert x is bufs[name]
+            assert (x[:spare] == 7).all() and (x[-spare:] == 7).all()
+
+
+def test_refused_buffers():
+    rows, do, _, _ = _case([4], 1, 2, 64, seed=12)
+    dev = [x.to(DEV) for x in rows]
+    cu = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    good = gdn_chunk_backward(*dev, cu, do.to(DEV))
+    for name, x in zip(NAMES[:5], good):
+        with pytest.raises(ValueError, match=name):
+            gdn_chunk_backward(*dev, cu, do.to(DEV), **{name: x[:3]})
+        with pytest.raises(TypeError, match=name):
+            gdn_chunk_backward(*dev, cu, do.to(DEV), **{name: x.double()})
+        with pytest.raises(ValueError, match=name):
+            gdn_chunk_backward(*dev, cu, do.to(DEV), **{name: x.cpu()})
