@@ -164,10 +164,13 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(TablesCall c) {
 }
 
 cudaError_t launch_tables(const TablesCall& c, cudaStream_t s) {
-  // One CTA per 2048 map positions, at most one per SM: more would only repeat
-  // the sums.
-  const long long span = c.row_capacity > c.chunk_capacity ? c.row_capacity : c.chunk_capacity;
-  long long grid = (span + 2047) / 2048;
+  // One CTA per 2048 positions of the maps that are made and per tile of lengths, at most one
+  // per SM: more would only repeat the sums.
+  const long long rows = c.row_seq != nullptr || c.row_slot != nullptr ? c.row_capacity : 0;
+  const long long chunks = c.chunk_seq != nullptr ? c.chunk_capacity : 0;
+  const long long tiles = (c.num_seqs + (long long)kTile - 1) / kTile;
+  long long grid = ((rows > chunks ? rows : chunks) + 2047) / 2048;
+  if (grid < tiles) grid = tiles;
   if (grid > sm_count()) grid = sm_count();
   if (grid < 1) grid = 1;
   tables_kernel<<<unsigned(grid), kTabThreads, 0, s>>>(c);
