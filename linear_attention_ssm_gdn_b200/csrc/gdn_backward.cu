@@ -94,16 +94,16 @@ constexpr int kFac = 5 * kBC + 4;
 // For a scan: what scales the rows of its three products (kSx: the state times K^T; kSin:
 // X or Y into the product with S; kSw: u or E into the product with K), what scales that
 // with S where it leaves it (kSout: minus the scale of each row and block, see s_out), e^{G_C},
-// and minus the diagonal blocks of S times beta, f32: of block b element (r, s) at
-// 256 b + 16 s + r for the forward scan, 256 b + 16 r + s for the backward one.  The
-// backward scan also has the inverse scales of GO's columns.
-enum { kSx = 0, kSin = kBC, kSw = 2 * kBC, kSout = 3 * kBC, kSeC = 3 * kBC + 96,
-       kSdiag = 3 * kBC + 100, kScol = kSdiag + 1024 };
+// whether the diagonal blocks are apart, and then minus those blocks times beta, f32: of block b
+// element (r, s) at 256 b + 16 s + r for the forward scan, 256 b + 16 r + s for the backward one.
+// The backward scan also has the inverse scales of GO's columns.
+enum { kSx = 0, kSin = kBC, kSw = 2 * kBC, kSout = 3 * kBC, kSeC = 3 * kBC + 160, kSapart,
+       kSdiag = kSeC + 4, kScol = kSdiag + 1024 };
 constexpr int kFwdFac = kScol, kBackFac = kScol + 128;
 // Where the scale of row i of a product with S is that comes from k-block j: the forward scan's
-// k-block j reaches the rows of the blocks behind it, the backward scan's those before it.
+// k-block j reaches the rows from its own on, the backward scan's those up to its own.
 __host__ __device__ constexpr int s_out(bool back, int j, int i) {
-  return kSout + (back ? 8 * j * (j - 1) + i : j == 0 ? i - 16 : j == 1 ? 48 + i - 32 : 80 + i - 48);
+  return kSout + (back ? 8 * j * (j + 1) + i : i + 8 * j * (7 - j));
 }
 
 __device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(uint32_t(x) << 16); }
@@ -303,11 +303,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // A chunk's decays span any range, and what they make small can be all there is: where only
 // the last row has an output gradient, E_s is e^{G_63 - G_s} times something of size 1.  So no
 // scale is shared by elements that a decay sets apart.  M has bf16 limbs, which need no scale.
-// S meets its operands block by block: the diagonal blocks in f32 on the CUDA cores, element
-// (r, s) of block (a, b) below them, e^{G_r - G_s} |k_r| |k_s| times something of size 1, as limbs
-// of S 2^-(from_r + to_s) under a scale of the block, where 2^from_r and 2^to_s are e^{G_r - G_a} |k_r|
-// and e^{G_b - G_s} |k_s| (a the first row of its block, b the last one of the other) to the nearest
-// power of two or two.  The scan puts them on its operand or its result, whichever has that row.
+// S meets its operands block by block: element (r, s) of block (a, b), e^{G_r - G_s} |k_r| |k_s|
+// times something of size 1, as limbs of S 2^-(from_r + to_s) under a scale of the block, where
+// 2^from_r and 2^to_s are e^{G_r - G_a} |k_r| and e^{G_b - G_s} |k_s| (a the first row of its block,
+// b the last one of the other) to the nearest power of two or two.  The scan puts them on its
+// operand or its result, whichever has that row.  Within a diagonal block these are of no use
+// (r and s share it), so where its rows are far apart it is f32, on the CUDA cores.
 //
 // K K^T and Q K^T are one pass of MMAs each (exact operands).  With L_b the
 // diagonal 16 x 16 blocks of B diag(beta), S by block rows:
@@ -469,6 +470,10 @@ __device__ __forceinline__ void block_product(float (&acc)[2][4], const float* A
     for (int e = 0; e < 4; ++e) acc[n][e] += low[n][e];
 }
 
+// S's diagonal blocks are f32, on the CUDA cores, where a block's rows differ by more than this
+// power of two: limbs leave 2^(kApart - 40) of a row's own size. (Such chunks take about 1100
+// cycles more of a scan's 8000.)
+constexpr float kApart = 14.f;
 constexpr int kFold = 96;  // the largest power of two that moves between S and its operand
 
 // The gates of head h: 64-bit sums, two rows per lane of one warp, into shared memory
@@ -480,6 +485,7 @@ struct GateRows {
   // The nearest 2^x of e^{G - G_a}, a the block's first row, and of e^{G_b - G}, each times the
   // size of k.
   int from[kBC], to[kBC];
+  bool apart;                // the diagonal blocks of S keep out of the limbs
 };
 __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c, size_t unit, int h,
                                            const float* invk, const float* invq, GateRows* s) {
@@ -506,6 +512,29 @@ __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c,
     const double y = __shfl_up_sync(0xffffffffu, run, off);
     if (lane >= off) run += y;
   }
+  // How far the rows of a 16-row block are apart, in powers of two (k = 0 has no part in S)
+  float range;
+  {
+    float hi[2] = {-INFINITY, -INFINITY}, lo[2] = {INFINITY, INFINITY};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float size = float(int(__float_as_uint(invk[2 * lane + e]) >> 23));
+      if (size > 2.f) {
+        const float G = float(e ? run : run - x[1] + x[0]);
+        hi[0] = max_nan(hi[0], G), lo[0] = -max_nan(-lo[0], -G);
+        hi[1] = fmaxf(hi[1], size), lo[1] = fminf(lo[1], size);
+      }
+    }
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        hi[v] = max_nan(hi[v], __shfl_xor_sync(0xffffffffu, hi[v], off));
+        lo[v] = -max_nan(-lo[v], -__shfl_xor_sync(0xffffffffu, lo[v], off));
+      }
+    range = hi[0] - lo[0] + (hi[1] - lo[1]);
+  }
+  const bool apart = __any_sync(0xffffffffu, !(range <= kApart));
   const double total = __shfl_sync(0xffffffffu, run, 31);
   x[0] += run - x[1];
   x[1] = run;
@@ -535,7 +564,11 @@ __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c,
     fb[kSin + r] = bt[e] * pow2(s->from[r]);
     fb[kSw + r] = -bt[e] * eG * invk[r];
   }
-  if (lane == 0) fac[kFeC] = ff[kSeC] = fb[kSeC] = exp2f(float(total));
+  if (lane == 0) {
+    fac[kFeC] = ff[kSeC] = fb[kSeC] = exp2f(float(total));
+    ff[kSapart] = fb[kSapart] = apart ? 1.f : 0.f;
+    s->apart = apart;
+  }
 }
 
 template <int D>
@@ -775,7 +808,7 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
 #pragma unroll
     for (int jj = 0; jj < 2; ++jj) {
       const int cb = 2 * par + jj, s0 = 16 * cb + t2;
-      if (cb == rb) {
+      if (cb == rb && gr.apart) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const int r = 16 * rb + g8 + 8 * (m & 1), s = s0 + 8 * (m >> 1);
@@ -784,8 +817,13 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
           f[0] = -v.x * bs[s], f[16] = -v.y * bs[s + 1];
           *reinterpret_cast<float2*>(fb + kSdiag + 256 * rb + (r & 15) * 16 + (s & 15)) =
               make_float2(-v.x * bs[r], -v.y * bs[r]);
+          const uint32_t at = sw128_offset(r, 2 * s);
+          *reinterpret_cast<uint32_t*>(smem + at) = 0;
+          *reinterpret_cast<uint32_t*>(smem + kBlk + at) = 0;
         }
-      } else if (cb < rb) {
+        if (lane < 16)
+          ff[s_out(false, cb, 16 * rb + lane)] = fb[s_out(true, rb, 16 * cb + lane)] = 0.f;
+      } else if (cb <= rb) {
         float2 v[4];
         int fold[4][2], most_e = -1 << 20;
 #pragma unroll
@@ -867,8 +905,8 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
 // ---------------------------------------------------------------------------
 
 constexpr int kScanThreads = 384;
-// Registers after re-allocation: 256 x 208 + 128 x 88 is the launch's 384 x 168.
-constexpr uint32_t kRegsScan = 208, kRegsFeed = 88;
+// Registers after re-allocation: 256 x 232 + 128 x 40 is the launch's 384 x 168.
+constexpr uint32_t kRegsScan = 232, kRegsFeed = 40;
 constexpr int kScanSync = 288;  // the state warps and the issuer
 
 __device__ uint32_t g_err_backward;
@@ -1084,8 +1122,9 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
       tc_fence_before();
       if (!named_all(1, kScanSync, ok)) break;
       if (tid == 0) mbar_arrive(&bars[bYE]);
-      // The diagonal blocks' share, while that product runs.  In the order in which no row is
-      // changed that a later one needs.
+      // The diagonal blocks' share where they are apart, while that product runs.  In the order in
+      // which no row is changed that a later one needs.
+      if (fac[kSapart] != 0.f)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float4* w4 = reinterpret_cast<const float4*>(fac + kSdiag + 256 * (2 * hh + j));
@@ -1123,35 +1162,40 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
           }
         }
       }
-      // 3. u = X - (beta X) S^T, E = Y - (beta Y) S: the other blocks' share, by k-block
+      // 3. u = X - (beta X) S^T, E = Y - (beta Y) S, by k-block
       ok = mbar_wait(&bars[bS], t & 1, abort_flag, err, 2u) && ok;
       tc_fence_after();
       {
-        // rows i0 .. of this thread's x from k-block j, whose sums begin at column `col`
-        auto add = [&](int j, int row, int col, auto& y) {
-          constexpr int n = sizeof(y) / sizeof(float);
-          if constexpr (n == 32)
-            tmem_ld32(tl + col, y);
-          else
-            tmem_ld16(tl + col, y);
-          tmem_ld_wait();
+        // rows `row` .. of this thread's x from k-block j
+        auto add = [&](int j, int row, const auto& y) {
           const float inv = inv_x[128 * j + dv];
           const float* out = fac + s_out(back, j, 32 * hh + row);
 #pragma unroll
-          for (int r = 0; r < n; r += 2) {
+          for (int r = 0; r < int(sizeof(y) / sizeof(float)); r += 2) {
             const float2 f = mul2(both(inv), *reinterpret_cast<const float2*>(out + r));
             const float2 d = fma2(make_float2(y[r], y[r + 1]), f,
                                   make_float2(x[row + r], x[row + r + 1]));
             x[row + r] = d.x, x[row + r + 1] = d.y;
           }
         };
-        float y16[16], y32[32];
+        float y0[32], y1[32], y2[16];
         if (back ? hh == 0 : hh == 1) {
-          add(back ? 2 : 0, 0, back ? kTX1 : kTX0 + 16, y32);
-          add(back ? 3 : 1, 0, back ? kTH1 : kTX0 + 48, y32);
-          add(back ? 1 : 2, back ? 0 : 16, back ? kTX0 : kTX0 + 80, y16);
+          tmem_ld32(tl + (back ? kTX1 : kTX0 + 32), y0);
+          tmem_ld32(tl + (back ? kTH1 : kTX1 + 16), y1);
+          tmem_ld_wait();
+          add(back ? 1 : 0, 0, y0);
+          tmem_ld32(tl + (back ? kTH1 + 64 : kTH1), y0);
+          tmem_ld16(tl + (back ? kTX0 : kTH1 + 32), y2);
+          add(back ? 2 : 1, 0, y1);
+          tmem_ld_wait();
+          add(back ? 3 : 2, 0, y0);
+          add(back ? 0 : 3, back ? 0 : 16, y2);
         } else {
-          add(back ? 3 : 0, back ? 0 : 16, back ? kTH1 + 32 : kTX0, y16);
+          tmem_ld32(tl + (back ? kTH1 + 96 : kTX0), y0);
+          tmem_ld16(tl + (back ? kTH1 + 32 : kTX1), y2);
+          tmem_ld_wait();
+          add(back ? 3 : 0, 0, y0);
+          add(back ? 2 : 1, back ? 0 : 16, y2);
         }
       }
       {
@@ -1284,8 +1328,10 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
     constexpr uint32_t id_x = make_idesc_f16(128, 64, 0, 0);
     constexpr uint32_t id_h = make_idesc_f16(128, D, 0, 1);
     constexpr uint32_t id_q = make_idesc_f16(128, D, 1, 1);
+    uint32_t b4 = base >> 4;
     for (int t = 0; t < n; ++t) {
-      const uint32_t k4 = (base + L::K + (t & 1) * L::kTile) >> 4;
+      asm volatile("" : "+r"(b4));  // (descriptors are made where they are needed, not kept)
+      const uint32_t k4 = b4 + ((L::K + (t & 1) * L::kTile) >> 4);
       bool ok = true;
       if (leader) ok = mbar_wait(&bars[bKF + (t & 1)], (t >> 1) & 1, abort_flag, err, 16u);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -1311,8 +1357,8 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 mma_bf16_ss(tmem + kTH0,
-                            mnmaj + (((base + L::GO + limb * L::kTile) >> 4) + 128 * kk),
-                            mnmaj + (((base + L::Q) >> 4) + 128 * kk), id_q,
+                            mnmaj + (b4 + ((L::GO + limb * L::kTile) >> 4) + 128 * kk),
+                            mnmaj + (b4 + (L::Q >> 4) + 128 * kk), id_q,
                             limb == 0 || kk != 0);
           }
           mma_commit(&bars[bQ]);
@@ -1324,21 +1370,19 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
       if (!named_all(1, kScanSync, ok)) break;
       if (leader) {
         tc_fence_after();
-        const uint32_t s4 = (base + L::S) >> 4;
-        // By k-block j, in sums of their own: the rows of the blocks behind it, or (the tile being
-        // read along its columns, whole) those of all blocks, of which the ones before it count.
+        const uint32_t s4 = b4 + (L::S >> 4);
+        // By k-block j, in sums of their own: the rows from it on, or (the tile being read along
+        // its columns, whole) those of all blocks, of which the ones up to it count.
         // (x low) S high, (x high) S low, (x high) S high
 #pragma unroll
         for (int q = 0; q < 3; ++q)
 #pragma unroll
-          for (int jj = 0; jj < 3; ++jj) {
-            const int j = back ? jj + 1 : jj;
-            const uint32_t to = back ? (j == 1 ? kTX0 : j == 2 ? kTX1 : kTH1)
-                                     : kTX0 + (j == 0 ? 0 : j == 1 ? 48 : 80);
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t to = j == 0 ? kTX0 : j == 1 ? kTX1 : j == 2 ? kTH1 : kTH1 + (back ? 64 : 32);
             const uint32_t at = s4 + (q == 1 ? kBlk >> 4 : 0);
             mma_bf16_ts(tmem + to, tmem + kTA + (q == 0 ? 32 : 0) + 8 * j,
-                        back ? mnmaj + (at + 128 * j) : kmaj + (at + 128 * (j + 1) + 2 * j),
-                        make_idesc_f16(128, back ? 64 : 48 - 16 * j, 0, back ? 1 : 0), q != 0);
+                        back ? mnmaj + (at + 128 * j) : kmaj + (at + 128 * j + 2 * j),
+                        make_idesc_f16(128, back ? 64 : 64 - 16 * j, 0, back ? 1 : 0), q != 0);
           }
         mma_commit(&bars[bS]);
         mma_commit(&bars[bSE]);
