@@ -34,8 +34,8 @@
 // 2^-40 of the largest value, whichever is coarser.  bf16 inputs are exact in
 // one limb under such a scale.  exact x f32 takes 2 MMAs, f32 x f32 takes 3
 // (lo x lo is below the f32 rounding).  Where no scale would do (M, P and N, whose
-// elements decays set apart along rows and columns) the limbs are bf16, three of them,
-// or two in dk, which is rounded to bf16 itself (2^-17 against 2^-9).
+// elements decays set apart along rows and columns) the limbs are bf16, three of them for M,
+// two for P and N, which reach only dq and dk, rounded to bf16 themselves (2^-17 against 2^-9).
 //
 // The scans and the gradients run on tcgen05; the first kernel, whose products are
 // small and triangular, on warp-level MMAs.
@@ -203,14 +203,15 @@ __device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32
   lo = pack_f16(x, y);
 }
 
-// a and b as three bf16 limbs, 24 bits of any f32: no scale is needed.
+// a and b as N bf16 limbs, 8 bits each of any f32: no scale is needed.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&limb)[3]) {
+template <int N>
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&limb)[N]) {
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < N; ++i) {
     limb[i] = pack_bf16(a, b);
     a -= __uint_as_float(limb[i] << 16), b -= __uint_as_float(limb[i] & 0xffff0000u);
   }
@@ -1470,9 +1471,8 @@ struct GradsSmem {
   // Slots for 64 columns (d_v) of H and of dH', as they are (f32, slices of 16 columns), then
   // in the same place as limbs with 128 rows, high and low
   static constexpr int H = UL + kTile, kSlot = 4 * kBlk;
-  // bf16 limbs of P (high, middle, low) and N (high, middle)
-  static constexpr int PL = H + 2 * kSlot, PM = PL + kBlk, NM = PM + kBlk, PH = NM + kBlk,
-                       NH = PH + kBlk;
+  // bf16 limbs of P and N
+  static constexpr int PL = H + 2 * kSlot, NL = PL + kBlk, PH = NL + kBlk, NH = PH + kBlk;
   static constexpr int Fac = NH + kBlk;          // two buffers of the unit's factors
   static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
   static constexpr int F = G + 2 * kBC * 8;      // floats from here
@@ -1645,14 +1645,13 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           // the tiles are multiplied along both, so no scale would do
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t w[4][3];
+            uint32_t w[4][2];
 #pragma unroll
             for (int y = 0; y < 4; ++y)
               split_bf16(x[8 * k + 2 * y], x[8 * k + 2 * y + 1], w[y]);
             const uint32_t at = base + sw128_offset(pr, 64 * ch + 16 * k);
             st_shared_v4(at + (isn ? L::NH : L::PH), w[0][0], w[1][0], w[2][0], w[3][0]);
-            st_shared_v4(at + (isn ? L::NM : L::PM), w[0][1], w[1][1], w[2][1], w[3][1]);
-            if (!isn) st_shared_v4(at + L::PL, w[0][2], w[1][2], w[2][2], w[3][2]);
+            st_shared_v4(at + (isn ? L::NL : L::PL), w[0][1], w[1][1], w[2][1], w[3][1]);
           }
         }
         ready(gP);
@@ -1842,23 +1841,23 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     setmaxnreg_dec<kRegsStates>();
     const int t = tid - kGradsRows;
     // By halves of d_v: H's f32 values come to its slot by a bulk copy, those of dH' to the other,
-    // and are turned into limbs there.  The next half's copies start when both have been multiplied.
+    // and are turned into limbs there.  The next half's copy to a slot starts when that has been
+    // multiplied.
     constexpr int kHalves = D / 64, kBytes = 64 * D * 4;
     constexpr int kQuads = kBytes / 16 / kGradsStates;  // 16 or 8 a thread
     const size_t unit = size_t(i) * a.H_v + h0;
     const uint32_t slot_h = base + L::H, slot_d = slot_h + L::kSlot;
-    auto load = [&](int p) {  // the p-th half of the CTA's states
-      const size_t at = unit * D * D + size_t(p) * 64 * D;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        mbar_arrive_expect_tx(&bars[gLand + x], kBytes);
-        bulk_load_g2s(smem + L::H + x * L::kSlot, (x ? a.dH : a.H) + at, kBytes, &bars[gLand + x]);
-      }
+    int loads[2] = {};
+    auto load = [&](int p, int x) {  // the p-th half of the CTA's states H or dH'
+      mbar_arrive_expect_tx(&bars[gLand + x], kBytes);
+      bulk_load_g2s(smem + L::H + x * L::kSlot,
+                    (x ? a.dH : a.H) + unit * D * D + size_t(p) * 64 * D, kBytes, &bars[gLand + x]);
+      ++loads[x];
     };
     const float* hm = a.Hmax + unit * 16 + (lane & 15);
     float largest = *hm;  // lanes 0-7: |H| of a scan warp's part, 8-15: |dH|
-    if (t == 0) load(0);
-    int p = 0, loads = 1;
+    if (t == 0) load(0, 0), load(0, 1);
+    int p = 0;
     const int halves = heads * kHalves;
     bool ok = true;
     for (int h = h0; h < h0 + heads; ++h, hm += 16) {
@@ -1896,7 +1895,9 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
               hh += fmaf(a0.x, v[m].x, a0.y * v[m].y) + fmaf(a1.x, v[m].z, a1.y * v[m].w);
             }
           }
-          named_sync(4, kGradsStates);  // all have read
+          if (x) fence_proxy_async_smem();  // H's limbs have been read: before a copy comes there
+          named_sync(4, kGradsStates);      // all have read
+          if (x && t == 0 && p + 1 < halves && mbar_test_wait(&bars[gFree], p & 1)) load(p + 1, 0);
           const float s = x ? sd : sh;
 #pragma unroll
           for (int m = 0; m < kQuads; ++m) {
@@ -1918,16 +1919,19 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           }
           ready(gFull + x);
         }
-        if (t == 0 && p + 1 < halves) {  // (the second one: every warp has passed its fence)
-          ok = mbar_wait(&bars[gFree], p & 1, abort_flag, err, 64u) && ok;
-          ok = mbar_wait(&bars[gFree + 1], p & 1, abort_flag, err, 64u) && ok;
-          if (ok) load(p + 1), ++loads;
+        if (t == 0 && p + 1 < halves) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (loads[x] == p + 1) {
+              ok = mbar_wait(&bars[gFree + x], p & 1, abort_flag, err, 64u) && ok;
+              if (ok) load(p + 1, x);
+            }
         }
         __syncwarp();
       }
     }
     if (t == 0)  // nothing may still be landing in shared memory at exit
-      for (int x = 0; x < 2; ++x) mbar_wait(&bars[gLand + x], (loads - 1) & 1, nullptr, err, 32u);
+      for (int x = 0; x < 2; ++x) mbar_wait(&bars[gLand + x], (loads[x] - 1) & 1, nullptr, err, 32u);
     if constexpr (split) cluster_sync(), cluster_sync();
   } else {
    setmaxnreg_dec<kRegsIssue>();
@@ -1942,8 +1946,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
     auto desc = [&](uint32_t low) { return uint64_t(kHigh) << 32 | low; };
     constexpr uint32_t id64 = make_idesc_f16(128, 64, 0, 0), id128 = make_idesc_f16(128, 128, 0, 0);
     constexpr uint32_t id_qk = make_idesc_bf16(128, 64, 0, 0);
-    constexpr uint32_t id_a = make_idesc_bf16(128, 64, 1, 0);  // A MN-major
-    constexpr uint32_t id_a128 = make_idesc_bf16(128, 128, 1, 0);
+    constexpr uint32_t id_a128 = make_idesc_bf16(128, 128, 1, 0);  // A MN-major
     constexpr uint32_t id_ab = make_idesc_bf16(128, 64, 1, 1);  // both MN-major
     auto load_o = [&](int h) {
       const uint8_t* src = a.O + (size_t(i) * a.H_v + h) * L::kTile;
@@ -2039,10 +2042,7 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       // A limb of P and that of N are one tile of 128 rows, A3 and A4 side by side.
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA3, rows(tk, kk), flat(L::PM, kk), id_a128, kk != 0);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_bf16_ss(tmem + kTA3, rows(tk, kk), flat(L::PL, kk), id_a, 1u);
+        mma_bf16_ss(tmem + kTA3, rows(tk, kk), flat(L::PL, kk), id_a128, kk != 0);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
         mma_bf16_ss(tmem + kTA3, rows(tk, kk), flat(L::PH, kk), id_a128, 1u);
@@ -2050,8 +2050,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          mma_bf16_ss(tmem + kTA4, rows(tq, kk), rows(x ? L::PH : L::PM, kk), id_ab, 1u);
-          mma_bf16_ss(tmem + kTA4, rows(tk, kk), rows(x ? L::NH : L::NM, kk), id_ab, 1u);
+          mma_bf16_ss(tmem + kTA4, rows(tq, kk), rows(x ? L::PH : L::PL, kk), id_ab, 1u);
+          mma_bf16_ss(tmem + kTA4, rows(tk, kk), rows(x ? L::NH : L::NL, kk), id_ab, 1u);
         }
       mma_commit(&bars[gA34]);
     }
