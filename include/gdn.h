@@ -349,7 +349,8 @@ int gdn_flag_clear(uint32_t* engaged_flag, gdn_stream_t stream);
  *              Offsets are clamped to 0..total_rows on the device; o rows that
  *              belong to no sequence are left as they were
  *   q, k       [total_rows, qk_stride] bf16; v [total_rows, v_stride] bf16;
- *              g, beta [total_rows, gb_stride] f32 (g = -inf forgets the state)
+ *              g, beta [total_rows, gb_stride] f32 (below g = -104 e^g is 0: the state
+ *              is forgotten, whatever it holds)
  *   o          [total_rows, H_v, d_v] bf16 contiguous
  * Supported: d_k == d_v in {64, 128}, H_v % H_k == 0.
  * Errors: GDN_ERR_NULL (h_table, q, k, v, g, beta or o NULL; a call without

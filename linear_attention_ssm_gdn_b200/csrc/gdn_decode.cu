@@ -113,6 +113,10 @@ __global__ void __launch_bounds__(kDecThreads, 6)
       kp += qk_stride, qp += qk_stride, vp += v_stride, gp += gb_stride, bp += gb_stride;
       next.load(kp, qp, vp, gp, bp);
     }
+    if (cur.g < -104.f) {  // e^g is 0: the state is forgotten, whatever it holds (0 times NaN is NaN)
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) st[i][0] = st[i][1] = make_float2(0.f, 0.f);
+    }
     float2 p0{}, p1{}, s0{}, s1{};  // of the thread's columns 0, 1 and 2, 3
     float kq = 0.f;
 #pragma unroll
