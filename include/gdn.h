@@ -410,9 +410,11 @@ int gdn_state_tables(const int32_t* lens, const int32_t* slots, int num_seqs, fl
  * Given the gradients dout of the outputs and dhT of the final states of
  *     (o, hT) = gdn_chunk_prefill(q, k, v, g, beta, h0),
  * the gradients of every input.  Nothing of the forward call is kept: the
- * chunk states are recomputed here, to f32 accuracy (dg, dbeta and dh0 are
- * the exact function's gradients to about 1e-6 relative, dq, dk and dv are
- * rounded once, to bf16).  No atomics: the same inputs give the same bits.
+ * chunk states are recomputed here, to f32 accuracy.  dg, dbeta and dh0 are
+ * the exact function's gradients to about 1e-6 relative, under strong decays
+ * too; dq, dk and dv are rounded to bf16 once, from sums that are within 1e-5
+ * of each row's own size.  No atomics in the sums: the same inputs give the
+ * same bits.
  *
  *   q, k, v, g, beta, strides, cu_seqlens, num_seqs, total_tokens, h0, heads,
  *   scale      as for gdn_chunk_prefill (h0 NULL = zeros); the same bound on
@@ -425,10 +427,19 @@ int gdn_state_tables(const int32_t* lens, const int32_t* slots, int num_seqs, fl
  *   dv         [T, H_v, d_v] bf16 contiguous
  *   dg, dbeta  [T, H_v] f32 contiguous
  *   dh0        [num_seqs, H_v, d_k, d_v] f32, or NULL (not wanted); may equal
- *              dhT.  An empty sequence's dh0 is its dhT
+ *              dhT, must not overlap another input.  An empty sequence's dh0 is
+ *              its dhT
  *   workspace  >= gdn_chunk_backward_workspace_bytes() bytes, 256-byte aligned,
- *              no two calls in flight at once may share it
- * Rows that belong to no sequence (behind cu[num_seqs]) are left as they were.
+ *              no two calls in flight at once may share it.  It holds what the
+ *              chunks of all heads need at once, about 315 KiB a chunk of 64 rows
+ *              and value head at d = 128, half of that at 64 (4576 tokens x 48
+ *              heads: 1.03 GiB, 24,674 tokens: 5.6 GiB, 131,072 tokens: 29 GiB),
+ *              and nothing between calls.  A batch too large for it can be passed
+ *              in parts: sequences do not depend on one another, and a long one
+ *              can be cut at any row, last part first, with its state there as h0
+ *              and one part's dh0 as the dhT of the part before
+ * Rows that belong to no sequence (before cu[0], behind cu[num_seqs]) are left
+ * as they were.
  * Supported: d_k == d_v in {64, 128}; H_v % H_k == 0, H_v <= 65535.
  * Errors: as for gdn_chunk_prefill, over the buffers above (GDN_ERR_NULL: q, k,
  * v, g, beta, cu_seqlens, dout, dq, dk, dv, dg or dbeta NULL; with

@@ -30,9 +30,10 @@
 // to f32 accuracy; a single bf16 or f16 operand would cost three digits.  Every
 // product runs on the tensor cores in f16 with f32 sums, each f32 operand as
 // two f16 limbs (hi = f16(x s), lo = f16(x s - hi)) under a power-of-two scale s
-// that puts the largest value of its row or tile just below 2^15: 22 bits, or
-// 2^-40 of the largest value, whichever is coarser.  bf16 inputs are exact in
-// one limb under such a scale.  exact x f32 takes 2 MMAs, f32 x f32 takes 3
+// that puts the largest value of what shares it in [2^14, 2^15): 22 bits, or
+// 2^-40 of the largest value, whichever is coarser.  Only what enters the same sums
+// shares one: a row, a column, a state (a head's entry state or its gradient).  A row
+// of bf16 inputs is exact in one limb under its scale.  exact x f32 takes 2 MMAs, f32 x f32 takes 3
 // (lo x lo is below the f32 rounding).  Where no scale would do (M, P and N, whose
 // elements decays set apart along rows and columns) the limbs are bf16, three of them for M,
 // two for P and N, which reach only dq and dk, rounded to bf16 themselves (2^-17 against 2^-9).
@@ -316,8 +317,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 //   S_bj = (I + L_b)^-1 (B_bj - sum over j <= c < b of B_bc (diag(beta) S)_cj).
 // The four inverses are solved side by side in f32 on the CUDA cores (a thread a
 // column); the block products are TF32 MMAs in two limbs each (22 bits).  Bound
-// by latency and the writes; two CTAs an SM hide some of it (three spill: 176 us against
-// 140 then).  132 us at 4576 rows, 16 key and 48 value heads, d = 128: 0.38 GB written.
+// by latency and the writes; two CTAs an SM hide some of it (three spill).  164 us at 4576
+// rows, 16 key and 48 value heads, d = 128: 0.42 GB written.
 // ---------------------------------------------------------------------------
 
 // 64 x D bf16 rows (row stride in elements) and the tiles that are made of them.
@@ -882,8 +883,7 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
 
 // ---------------------------------------------------------------------------
 // Scans: one CTA per (sequence, value head, direction), both directions in one launch
-// (the backward one, with the longer chain, first): about 330 us at 4576 rows, 48 heads,
-// 4.6 us a chunk.
+// (the backward one first): 304 us at 4576 rows, 48 heads, 4.2 us a chunk.
 //
 // H^T [dv][dk] is held by 8 state warps, thread (dv, half of d_k), 64 f32
 // registers at D = 128.  Per chunk three products, M = 128 (dv), A from tensor
@@ -891,18 +891,19 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
 //   1. H^T K^T -> X (or Y), 2. (beta X)^T S^T -> u (or S: E), 3. (f u)^T K -> H'.
 // A row's limbs have one scale per half (its thread's own maximum; for product 2, whose rows
 // decays set apart, per 16 rows), so no warp waits for another one's maximum: the parts go to
-// accumulators of their own, summed when they are read.  The backward scan also has (scale e^G dO)^T Q, from
-// tiles made before, between products 1 and 2.
+// accumulators of their own, summed when they are read.  The backward scan also has
+// (scale e^G dO)^T Q, from tiles made before, between products 1 and 2.
 //   warps 0-7: state; warp 8: loads (bulk copies into buffers freed by the
 //   products that read them); warp 9: one thread issues the MMAs after the state
 //   warps' barrier.
 // Low limbs are multiplied first: the f32 accumulator then rounds against small
 // sums while it holds them.  D = 64 runs the same code with half of the rows idle.
 //
-// Bound by the chain: per chunk 16 + 12 + 8 MMAs (55 to 68 cycles each), about
-// 1200 instructions a state warp between them, and three hand-overs each way.
-// The warp-level form of this scan (two warps per 16 columns, state fragments as A
-// operands) needed four times the instructions and 6.2 us a chunk.
+// Bound by the chain, about 8000 cycles a chunk: 16 + 12 + 8 MMAs (55 to 68 cycles each) take
+// 2300 of them, the state warps' 1400 instructions between them most of the rest (limbs 800,
+// the state on its way out 1500, X and its limbs 900, u or E and its limbs 1400), with three
+// hand-overs each way.  The diagonal blocks, where they are apart, take 1100 more: their
+// coefficients are broadcast from shared memory, four a load.
 // ---------------------------------------------------------------------------
 
 constexpr int kScanThreads = 384;
@@ -1452,12 +1453,10 @@ cudaError_t take_err_backward(uint32_t* out) {
 //   warp 12: one thread loads dO and issues the MMAs; warp 13: dg; warps 14, 15: Q and K.
 // Between a head's products and sums the row warps stage the next head's rows, as soon as the
 // products that read the last ones are done, so that the slots are free again early.
-// Bound by the latency of the states' loads: 287 us at 4576 rows, 48 heads, 220 if a
-// head's states came for nothing.  Two batches of them are in flight or at work (one at a
-// time: 305 us; four smaller ones 300, single quads 345: a wait for one load is a wait for
-// those issued with it), and they pass by the L1 cache, of which the shared memory leaves
-// some 20 KB (through it: 296 us).  (All 16 warps in step took 320 us, 24 warps 345 us, the
-// same products as warp-level MMAs 400 us.)
+// 324 us at 4576 rows, 48 heads.  Bound by the latency of a head's steps, each of which waits for
+// another group's (issue slots 36 % used, tensor pipe 16 %, barriers and loads the stalls).  The
+// states' values come to the slots by bulk copies and become limbs in place: with loads through
+// registers, two batches in flight, the call took 55 us more.
 // ---------------------------------------------------------------------------
 
 template <int D>
@@ -2196,10 +2195,10 @@ cudaError_t run(const BwdArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(kScanThreads);
   cfg.dynamicSmemBytes = scans;
   if ((e = cudaLaunchKernelEx(&cfg, bwd_scan_kernel<D>, a)) != cudaSuccess) return e;
-  // Few chunks: one head a CTA, the key head's CTAs joined in clusters, where they all run
-  // at once (one chunk of 48 heads in threes: 68.3 -> 53.9 us a call; 21 chunks of 6 heads:
-  // 109 -> 98).  Where they cannot (clusters of three leave SMs free, so even 24 chunks of 6
-  // heads may need a second wave) they lose: 24 chunks 148 -> 153 us, 47 chunks 253 -> 278.
+  // Few chunks: one head a CTA, the key head's CTAs joined in clusters, while there is an SM for
+  // each (one chunk of 48 heads in threes: 65.9 -> 48.0 us a call; 18 chunks of 6 heads: 118 -> 102;
+  // at the rule's edge, where clusters of three leave SMs free and a second wave may come, 24 chunks
+  // of 6 heads 163 -> 161, 12 of 12 heads 113.8 -> 113.0).
   const bool split = vpg > 1 && vpg <= 8 && (long long)a.max_chunks * a.H_v <= a.sms;
   attrs[1].id = cudaLaunchAttributeClusterDimension;
   attrs[1].val.clusterDim.x = attrs[1].val.clusterDim.z = 1;
@@ -2232,9 +2231,7 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t s) {
   a.dq = c.dq, a.dk = c.dk, a.dv = c.dv, a.dg = c.dg, a.dbeta = c.dbeta, a.dh0 = c.dh0;
   a.scale = c.scale;
   a.sms = sm_count();
-  // Up to 32 sequences (a lane each): the first kernel finds its chunks itself, one launch
-  // less.  With the last kernel's early start, 256 rows at d = 64: 45.0 -> 38.6 us a call,
-  // seven sequences of 1100 rows: 92.9 -> 90.1.
+  // Up to 32 sequences (a lane each): the first kernel finds its chunks itself, one launch less.
   if (c.num_seqs > kFewSeqs) {
     TablesCall t = {};
     t.cu_in = c.cu_seqlens;

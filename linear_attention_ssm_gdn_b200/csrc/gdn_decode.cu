@@ -14,10 +14,11 @@
 // state row.  Small CTAs keep many loads in flight per SM and give 4 CTAs per
 // head to a call with one sequence.
 //
-// Measured (48 heads, D = 128, one row each): 64 sequences 58.8 us, 6.9 TB/s of state
-// moved, 256 sequences 240 us, 6.7 TB/s.  Sequences of 0 to 6 rows (37 x 32 heads) take
-// 34 us for 148 MB: there the rows' instructions and their barrier bound it, so the
-// arithmetic is packed, two f32 per instruction (44 us of the call before, 37 since).
+// Measured (48 heads, D = 128, one row each): 64 sequences 64 us a call (404 MB, 6.3 TB/s),
+// 256 sequences 240 us (6.7 TB/s).  37 sequences of 0 to 6 rows (32 heads; 31 with rows, 132 MB)
+// take 35 us, 34 of them the kernel: there issue slots are 55 % used and the stalls are those of
+// the rows' reductions (shuffles and shared memory) before those of loads, so the arithmetic is
+// packed, two f32 per instruction (44 us of the call before).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -57,8 +58,8 @@ struct DecodeRow {
 };
 
 // Six CTAs an SM: with the compiler's own choice of registers (96, five CTAs) 64 x 48 heads
-// take 59.5 us and 256 x 48 244 us, with eight CTAs (spills) 70 us the first; the rows of
-// 37 x 32 heads take 34 us instead of 32.
+// took 66.9 us a call instead of 66.0 and 256 x 48 251 instead of 248, with eight CTAs (spills)
+// 70 us the first; the rows of 37 x 32 heads take 34 us of kernel instead of 32.
 template <int D>
 __global__ void __launch_bounds__(kDecThreads, 6)
     decode_kernel(float* const* __restrict__ h_table, const uint16_t* __restrict__ q,

@@ -258,3 +258,24 @@ def test_refused_buffers():
             gdn_chunk_backward(*dev, cu, do.to(DEV), **{name: x.double()})
         with pytest.raises(ValueError, match=name):
             gdn_chunk_backward(*dev, cu, do.to(DEV), **{name: x.cpu()})
+
+
+@pytest.mark.parametrize("cut", [64, 100])
+def test_a_sequence_in_two_parts(cut):
+    """Last part first, its dh0 as the first part's dhT, the state between them as its h0."""
+    lens, d = [230], 128
+    rows, do, h0, dhT = _case(lens, 1, 2, d, seed=13)
+    dev, do, h0, dhT = [x.to(DEV) for x in rows], do.to(DEV), h0.to(DEV), dhT.to(DEV)
+    want = R.backward(*dev, lens, do, h0, dhT)
+    between = R.forward(*[x[:cut] for x in dev], [cut], h0)[1].float()
+
+    def part(rows, do, h0, dhT):
+        cu = torch.tensor([0, do.shape[0]], dtype=torch.int32, device=DEV)
+        return gdn_chunk_backward(*rows, cu, do, h0=h0, dhT=dhT)
+
+    last = part([x[cut:] for x in dev], do[cut:], between, dhT)
+    first = part([x[:cut] for x in dev], do[:cut], h0, last[5])
+    for name, a, b, y in zip(NAMES, first, last, want):
+        x = a if name == "dh0" else torch.cat([a, b])
+        # (a part's h0 and dhT are rounded to f32 once more: 2^-24 each)
+        assert R.rel(x, y) <= (R.BF16_REL if name in NAMES[:3] else 0) + R.F32_REL, name
