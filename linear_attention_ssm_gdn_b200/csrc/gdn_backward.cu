@@ -74,10 +74,10 @@ struct BwdArgs {
   uint8_t* KQ;         // [chunk][H_k] f16 tiles of K, then of Q, a scale per row
   uint8_t* O;          // [chunk][H_v] f16 tile of dO, a scale per row
   uint8_t* GO;         // [chunk][H_v] scale e^G dO, high and low tile, a scale per column
-  uint8_t* S;          // [chunk][H_v] S below its diagonal blocks, high and low block
+  uint8_t* S;          // [chunk][H_v] -S, three limbs
   float* Y0;           // [chunk][H_v][64][D] scale (Q K^T * D)^T dO
   float* fac;          // [chunk][H_v][kFac]
-  float* ff;           // [chunk][H_v][kFwdFac] factors and diagonal blocks for the forward scan
+  float* ff;           // [chunk][H_v][kFwdFac] factors for the forward scan
   float* fb;           // [chunk][H_v][kBackFac] ... and for the backward one
   float2* G;           // [chunk][H_v][64] cumulative gates / ln 2, high and low part
   float* u;            // [chunk][H_v][D / 32][64][32]
@@ -93,19 +93,10 @@ enum { kFeG = 0, kFeT = kBC, kFbeta = 2 * kBC, kFend = 3 * kBC, kFo = 4 * kBC, k
 constexpr int kFac = 5 * kBC + 4;
 
 // For a scan: what scales the rows of its three products (kSx: the state times K^T; kSin:
-// X or Y into the product with S; kSw: u or E into the product with K), what scales that
-// with S where it leaves it (kSout: minus the scale of each row and block, see s_out), e^{G_C},
-// whether the diagonal blocks are apart, and then minus those blocks times beta, f32: of block b
-// element (r, s) at 256 b + 16 s + r for the forward scan, 256 b + 16 r + s for the backward one.
-// The backward scan also has the inverse scales of GO's columns.
-enum { kSx = 0, kSin = kBC, kSw = 2 * kBC, kSout = 3 * kBC, kSeC = 3 * kBC + 160, kSapart,
-       kSdiag = kSeC + 4, kScol = kSdiag + 1024 };
+// X or Y into the product with S; kSw: u or E into the product with K) and e^{G_C}.  The
+// backward scan also has the inverse scales of GO's columns.
+enum { kSx = 0, kSin = kBC, kSw = 2 * kBC, kSeC = 3 * kBC, kScol = kSeC + 4 };
 constexpr int kFwdFac = kScol, kBackFac = kScol + 128;
-// Where the scale of row i of a product with S is that comes from k-block j: the forward scan's
-// k-block j reaches the rows from its own on, the backward scan's those up to its own.
-__host__ __device__ constexpr int s_out(bool back, int j, int i) {
-  return kSout + (back ? 8 * j * (j + 1) + i : i + 8 * j * (7 - j));
-}
 
 __device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(uint32_t(x) << 16); }
 __device__ __forceinline__ float expdiff(float2 a, float2 b) {
@@ -176,11 +167,6 @@ __device__ __forceinline__ float pow2_scale(float largest, float* inverse) {
   const uint32_t e = max(__float_as_uint(largest) >> 23, 16u);
   *inverse = __uint_as_float((e - 14u) << 23);
   return __uint_as_float((268u - e) << 23);
-}
-
-// 2^e, 0 below the smallest normal number.
-__device__ __forceinline__ float pow2(int e) {
-  return __uint_as_float(uint32_t(min(max(e + 127, 0), 254)) << 23);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
@@ -303,14 +289,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // tiles of K, Q, dO and e^G dO, the gate factors, Y0 = scale M^T dO and S.
 //
 // A chunk's decays span any range, and what they make small can be all there is: where only
-// the last row has an output gradient, E_s is e^{G_63 - G_s} times something of size 1.  So no
-// scale is shared by elements that a decay sets apart.  M has bf16 limbs, which need no scale.
-// S meets its operands block by block: element (r, s) of block (a, b), e^{G_r - G_s} |k_r| |k_s|
-// times something of size 1, as limbs of S 2^-(from_r + to_s) under a scale of the block, where
-// 2^from_r and 2^to_s are e^{G_r - G_a} |k_r| and e^{G_b - G_s} |k_s| (a the first row of its block,
-// b the last one of the other) to the nearest power of two or two.  The scan puts them on its
-// operand or its result, whichever has that row.  Within a diagonal block these are of no use
-// (r and s share it), so where its rows are far apart it is f32, on the CUDA cores.
+// the last row has an output gradient, E_s is e^{G_63 - G_s} times something of size 1.  So S
+// and M, whose elements they set apart along rows and columns, have three bf16 limbs each,
+// which need no scale, and so has what S is multiplied with.
 //
 // K K^T and Q K^T are one pass of MMAs each (exact operands).  With L_b the
 // diagonal 16 x 16 blocks of B diag(beta), S by block rows:
@@ -420,7 +401,7 @@ constexpr int kBT = 68;  // row length of the f32 squares (16-byte rows, 4 banks
 template <int D>
 struct PrepSmem {
   static constexpr int kTile = D / 64 * kBlk;
-  static constexpr int K = 0, Q = kTile;       // bf16 tiles; later dO, then the limbs of S
+  static constexpr int K = 0, Q = kTile;       // bf16 tiles; later dO; then from 0 on S's limbs
   static constexpr int M = 2 * kBlk;           // later, over Q: the three limbs of M
   static constexpr int B = 5 * kBlk;
   static constexpr int S = B + kBC * kBT * 4;
@@ -472,22 +453,12 @@ __device__ __forceinline__ void block_product(float (&acc)[2][4], const float* A
     for (int e = 0; e < 4; ++e) acc[n][e] += low[n][e];
 }
 
-// S's diagonal blocks are f32, on the CUDA cores, where a block's rows differ by more than this
-// power of two: limbs leave 2^(kApart - 40) of a row's own size. (Such chunks take about 1100
-// cycles more of a scan's 8000.)
-constexpr float kApart = 14.f;
-constexpr int kFold = 96;  // the largest power of two that moves between S and its operand
-
 // The gates of head h: 64-bit sums, two rows per lane of one warp, into shared memory
 // (gs: largest scale e^G) and the unit's factors.
 struct GateRows {
   float2 G[kBC];
   float beta[kBC], eG[kBC];  // eG: scale e^G / scale of Q
   float end[kBC];            // e^{G_b - G}, b the last row of the 16-row block
-  // The nearest 2^x of e^{G - G_a}, a the block's first row, and of e^{G_b - G}, each times the
-  // size of k.
-  int from[kBC], to[kBC];
-  bool apart;                // the diagonal blocks of S keep out of the limbs
 };
 __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c, size_t unit, int h,
                                            const float* invk, const float* invq, GateRows* s) {
@@ -514,34 +485,10 @@ __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c,
     const double y = __shfl_up_sync(0xffffffffu, run, off);
     if (lane >= off) run += y;
   }
-  // How far the rows of a 16-row block are apart, in powers of two (k = 0 has no part in S)
-  float range;
-  {
-    float hi[2] = {-INFINITY, -INFINITY}, lo[2] = {INFINITY, INFINITY};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float size = float(int(__float_as_uint(invk[2 * lane + e]) >> 23));
-      if (size > 2.f) {
-        const float G = float(e ? run : run - x[1] + x[0]);
-        hi[0] = max_nan(hi[0], G), lo[0] = -max_nan(-lo[0], -G);
-        hi[1] = fmaxf(hi[1], size), lo[1] = fminf(lo[1], size);
-      }
-    }
-#pragma unroll
-    for (int off = 1; off < 8; off <<= 1)
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        hi[v] = max_nan(hi[v], __shfl_xor_sync(0xffffffffu, hi[v], off));
-        lo[v] = -max_nan(-lo[v], -__shfl_xor_sync(0xffffffffu, lo[v], off));
-      }
-    range = hi[0] - lo[0] + (hi[1] - lo[1]);
-  }
-  const bool apart = __any_sync(0xffffffffu, !(range <= kApart));
   const double total = __shfl_sync(0xffffffffu, run, 31);
   x[0] += run - x[1];
   x[1] = run;
   const double end = __shfl_sync(0xffffffffu, x[1], lane | 7);
-  const double begin = __shfl_sync(0xffffffffu, x[0], lane & 24);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int r = 2 * lane + e;
@@ -552,25 +499,18 @@ __device__ __forceinline__ void make_gates(const BwdArgs& a, const ChunkRows& c,
     const float eG = exp2f(G.x + G.y), eT = exp2f(float(total - x[e]));
     s->eG[r] = a.scale * eG * invq[r];
     s->end[r] = exp2f(float(end - x[e]));
-    const int size = int(__float_as_uint(invk[r]) >> 23) - 112;  // (the largest of k: 2^size)
-    s->from[r] = max(-kFold, min(kFold, __float2int_rn(float(x[e] - begin)) + size));
-    s->to[r] = max(-kFold, min(kFold, __float2int_rn(float(end - x[e])) + size));
     fac[kFend + r] = s->end[r];
     fac[kFeG + r] = eG;
     fac[kFeT + r] = eT;
     fac[kFbeta + r] = bt[e];
     ff[kSx + r] = -eG * invk[r];
-    ff[kSin + r] = bt[e] * pow2(s->to[r]);
+    ff[kSin + r] = bt[e];
     ff[kSw + r] = bt[e] * eT * invk[r];
     fb[kSx + r] = eT * invk[r];
-    fb[kSin + r] = bt[e] * pow2(s->from[r]);
+    fb[kSin + r] = bt[e];
     fb[kSw + r] = -bt[e] * eG * invk[r];
   }
-  if (lane == 0) {
-    fac[kFeC] = ff[kSeC] = fb[kSeC] = exp2f(float(total));
-    ff[kSapart] = fb[kSapart] = apart ? 1.f : 0.f;
-    s->apart = apart;
-  }
+  if (lane == 0) fac[kFeC] = ff[kSeC] = fb[kSeC] = exp2f(float(total));
 }
 
 template <int D>
@@ -805,76 +745,22 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
         make_gates(a, c, unit + 1, h + 1, invk, invq, &gates[(h + 1) & 1]);
     }
     __syncthreads();
-    // S to its places: warp = 16 rows, half of the columns, two blocks
-    float *ff = a.ff + unit * kFwdFac, *fb = a.fb + unit * kBackFac;
+    // -S as limbs: warp = 16 rows, half of the columns; zeros above the diagonal blocks
 #pragma unroll
-    for (int jj = 0; jj < 2; ++jj) {
-      const int cb = 2 * par + jj, s0 = 16 * cb + t2;
-      if (cb == rb && gr.apart) {
+    for (int m = 0; m < 8; ++m) {
+      const int r = 16 * rb + g8 + 8 * (m & 1), s = 32 * par + 8 * (m >> 1) + t2;
+      float2 v = make_float2(0.f, 0.f);
+      if (2 * par + (m >> 2) <= rb) v = *reinterpret_cast<const float2*>(&S[r * kBT + s]);
+      uint32_t limb[3];
+      split_bf16(-v.x, -v.y, limb);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int r = 16 * rb + g8 + 8 * (m & 1), s = s0 + 8 * (m >> 1);
-          const float2 v = *reinterpret_cast<const float2*>(&S[r * kBT + s]);
-          float* f = ff + kSdiag + 256 * rb + (s & 15) * 16 + (r & 15);
-          f[0] = -v.x * bs[s], f[16] = -v.y * bs[s + 1];
-          *reinterpret_cast<float2*>(fb + kSdiag + 256 * rb + (r & 15) * 16 + (s & 15)) =
-              make_float2(-v.x * bs[r], -v.y * bs[r]);
-          const uint32_t at = sw128_offset(r, 2 * s);
-          *reinterpret_cast<uint32_t*>(smem + at) = 0;
-          *reinterpret_cast<uint32_t*>(smem + kBlk + at) = 0;
-        }
-        if (lane < 16)
-          ff[s_out(false, cb, 16 * rb + lane)] = fb[s_out(true, rb, 16 * cb + lane)] = 0.f;
-      } else if (cb <= rb) {
-        float2 v[4];
-        int fold[4][2], most_e = -1 << 20;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int r = 16 * rb + g8 + 8 * (m & 1), s = s0 + 8 * (m >> 1);
-          v[m] = *reinterpret_cast<const float2*>(&S[r * kBT + s]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = e ? v[m].y : v[m].x;
-            const int ex = (__float_as_uint(x) >> 23) & 255;
-            fold[m][e] = gr.from[r] + gr.to[s + e];
-            if (x != 0.f && ex < 255) most_e = max(most_e, ex - fold[m][e]);
-          }
-        }
-        most_e = __reduce_max_sync(0xffffffffu, most_e);
-        if (most_e == -1 << 20) most_e = 127;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int r = 16 * rb + g8 + 8 * (m & 1), s = s0 + 8 * (m >> 1);
-          float x[2] = {v[m].x, v[m].y};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // the largest to [2^14, 2^15); in two steps, none overflows
-            const int up = max(-252, min(252, 141 - most_e - fold[m][e]));
-            x[e] = x[e] * pow2(up >> 1) * pow2(up - (up >> 1));
-          }
-          uint32_t hi, lo;
-          split_f16(x[0], x[1], hi, lo);
-          const uint32_t at = sw128_offset(r, 2 * s);
-          *reinterpret_cast<uint32_t*>(smem + at) = hi;
-          *reinterpret_cast<uint32_t*>(smem + kBlk + at) = lo;
-        }
-        if (lane < 16) {
-          const int r = 16 * rb + lane, s = 16 * cb + lane;
-          ff[s_out(false, cb, r)] = -pow2(most_e - 141 + gr.from[r]);
-          fb[s_out(true, rb, s)] = -pow2(most_e - 141 + gr.to[s]);
-        }
-      } else {  // (read by MMAs whose results are not)
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const uint32_t at = sw128_offset(16 * rb + g8 + 8 * (m & 1), 2 * (s0 + 8 * (m >> 1)));
-          *reinterpret_cast<uint32_t*>(smem + at) = 0;
-          *reinterpret_cast<uint32_t*>(smem + kBlk + at) = 0;
-        }
-      }
+      for (int x = 0; x < 3; ++x)
+        *reinterpret_cast<uint32_t*>(smem + x * kBlk + sw128_offset(r, 2 * s)) = limb[x];
     }
     fence_proxy_async_smem();
     __syncthreads();
     if (tid == 0) {
-      bulk_store_s2g(a.S + unit * 2 * kBlk, smem, 2 * kBlk);
+      bulk_store_s2g(a.S + unit * 3 * kBlk, smem, 3 * kBlk);
       tma_store_commit();
     }
   }
@@ -889,9 +775,10 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
 // registers at D = 128.  Per chunk three products, M = 128 (dv), A from tensor
 // memory (the limbs that the state warps write), B the chunk's tiles:
 //   1. H^T K^T -> X (or Y), 2. (beta X)^T S^T -> u (or S: E), 3. (f u)^T K -> H'.
-// A row's limbs have one scale per half (its thread's own maximum; for product 2, whose rows
-// decays set apart, per 16 rows), so no warp waits for another one's maximum: the parts go to
-// accumulators of their own, summed when they are read.  The backward scan also has
+// The limbs of products 1 and 3 are f16, a row's under one scale per half (its thread's own
+// maximum, with the factors of the rows in it), so no warp waits for another one's maximum: the
+// halves go to accumulators of their own, summed when they are read.  Product 2, whose results
+// decays set apart, has three bf16 limbs on both sides.  The backward scan also has
 // (scale e^G dO)^T Q, from tiles made before, between products 1 and 2.
 //   warps 0-7: state; warp 8: loads (bulk copies into buffers freed by the
 //   products that read them); warp 9: one thread issues the MMAs after the state
@@ -902,8 +789,7 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
 // Bound by the chain, about 8000 cycles a chunk: 16 + 12 + 8 MMAs (55 to 68 cycles each) take
 // 2300 of them, the state warps' 1400 instructions between them most of the rest (limbs 800,
 // the state on its way out 1500, X and its limbs 900, u or E and its limbs 1400), with three
-// hand-overs each way.  The diagonal blocks, where they are apart, take 1100 more: their
-// coefficients are broadcast from shared memory, four a load.
+// hand-overs each way.
 // ---------------------------------------------------------------------------
 
 constexpr int kScanThreads = 384;
@@ -925,8 +811,8 @@ template <int D, bool back>
 struct ScanSmem {
   static constexpr int kTile = D / 64 * kBlk;
   static constexpr int K = 0;                      // two buffers
-  static constexpr int S = 2 * kTile;              // S high, low
-  static constexpr int Y = S + 2 * kBlk;           // Y0 (f32) or V (bf16), [64][D]
+  static constexpr int S = 2 * kTile;              // -S, three limbs
+  static constexpr int Y = S + 3 * kBlk;           // Y0 (f32) or V (bf16), [64][D]
   static constexpr int Q = Y + kBC * D * (back ? 4 : 2);
   static constexpr int GO = Q + (back ? kTile : 0);  // two limbs, M = 128 rows each
   // The state on its way out: its slices, 64 bytes apart from a multiple of all
@@ -938,22 +824,21 @@ struct ScanSmem {
   static constexpr int U = St + D / 16 * kStep;
   static constexpr int kFactors = back ? kBackFac : kFwdFac;
   static constexpr int Fac = U + (D == 64 ? 8 * 4096 : 0);  // two buffers
-  static constexpr int Inv = Fac + 2 * kFactors * 4;   // [8][128] inverse row scales
-  static constexpr int Bars = Inv + 8 * 128 * 4;
+  static constexpr int Inv = Fac + 2 * kFactors * 4;   // [2][2][128] inverse row scales
+  static constexpr int Bars = Inv + 4 * 128 * 4;
   static constexpr int kUsed = Bars + kBars * 8 + 16 + 1024;  // 1024: alignment of the base
   // More than half of an SM's: all of its tensor memory goes to one CTA.
   static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
 };
 
-// N floats as limbs, the first half times s0, the second times s1: hi to TMEM columns `hi`, lo
-// to `lo` (N / 2 each).
+// N floats times s as f16 limbs: hi to TMEM columns `hi`, lo to `lo` (N / 2 each).
 template <int N>
-__device__ __forceinline__ void limbs_to_tmem(const float (&x)[N], float s0, float s1, uint32_t hi,
+__device__ __forceinline__ void limbs_to_tmem(const float (&x)[N], float s, uint32_t hi,
                                               uint32_t lo) {
   uint32_t h[N / 2], l[N / 2];
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) {
-    const float2 y = mul2(make_float2(x[2 * i], x[2 * i + 1]), both(i < N / 4 ? s0 : s1));
+    const float2 y = mul2(make_float2(x[2 * i], x[2 * i + 1]), both(s));
     split_f16(y.x, y.y, h[i], l[i]);
   }
   if constexpr (N == 64) {
@@ -1024,7 +909,7 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
     const bool on = D == 128 || dv < D;
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);  // this warp's TMEM lanes
     float* inv_h = reinterpret_cast<float*>(smem + L::Inv);        // [2][128]
-    float *inv_x = inv_h + 256, *inv_w = inv_x + 512;              // [4][128], [2][128]
+    float* inv_w = inv_h + 256;                                    // [2][128]
     const size_t head = (size_t(b) * a.H_v + h) * D * D;
     float st[NK];
     {
@@ -1065,7 +950,7 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
         float inv;
         const float s = pow2_scale(most, &inv);
         inv_h[128 * hh + dv] = inv;
-        limbs_to_tmem(st, s, s, tl + kTA + NK / 2 * hh, tl + kTA + 64 + NK / 2 * hh);
+        limbs_to_tmem(st, s, tl + kTA + NK / 2 * hh, tl + kTA + 64 + NK / 2 * hh);
       }
       tc_fence_before();
       if (!named_all(1, kScanSync, ok)) break;
@@ -1103,49 +988,24 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
           x[r] = d.x, x[r + 1] = d.y;
         }
       }
-      {  // into the product with S: a scale of its own for each 16 rows, a k-step
-        float z[32], m[2], inv[2], sc[2];
+      {  // into the product with S, whose rows decays set apart: bf16 limbs
+        uint32_t z[3][16];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float m0 = 0.f, m1 = 0.f;
+        for (int r = 0; r < 32; r += 2) {
+          const float2 d = mul2(make_float2(x[r], x[r + 1]),
+                                *reinterpret_cast<const float2*>(fac + kSin + 32 * hh + r));
+          uint32_t limb[3];
+          split_bf16(d.x, d.y, limb);
 #pragma unroll
-          for (int r = 16 * j; r < 16 * j + 16; r += 2) {
-            const float2 d = mul2(make_float2(x[r], x[r + 1]),
-                                  *reinterpret_cast<const float2*>(fac + kSin + 32 * hh + r));
-            z[r] = d.x, z[r + 1] = d.y;
-            m0 = max_nan(m0, fabsf(d.x)), m1 = max_nan(m1, fabsf(d.y));
-          }
-          m[j] = max_nan(m0, m1);
-          sc[j] = pow2_scale(m[j], &inv[j]);
-          inv_x[128 * (2 * hh + j) + dv] = inv[j];
+          for (int l = 0; l < 3; ++l) z[l][r / 2] = limb[l];
         }
-        limbs_to_tmem(z, sc[0], sc[1], tl + kTA + 16 * hh, tl + kTA + 32 + 16 * hh);
+#pragma unroll
+        for (int l = 0; l < 3; ++l) tmem_st16u(tl + kTA + 32 * l + 16 * hh, z[l]);
+        tmem_st_wait();
       }
       tc_fence_before();
       if (!named_all(1, kScanSync, ok)) break;
       if (tid == 0) mbar_arrive(&bars[bYE]);
-      // The diagonal blocks' share where they are apart, while that product runs.  In the order in
-      // which no row is changed that a later one needs.
-      if (fac[kSapart] != 0.f)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float4* w4 = reinterpret_cast<const float4*>(fac + kSdiag + 256 * (2 * hh + j));
-        float* xj = x + 16 * j;
-#pragma unroll
-        for (int gg = 0; gg < 4; ++gg) {
-          const int g = back ? gg : 3 - gg;
-          float2 a0 = make_float2(xj[4 * g], xj[4 * g + 1]);
-          float2 a1 = make_float2(xj[4 * g + 2], xj[4 * g + 3]);
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (back ? i > 4 * g : i < 4 * g + 3) {
-              const float4 w = w4[4 * i + g];
-              a0 = fma2(make_float2(w.x, w.y), both(xj[i]), a0);
-              a1 = fma2(make_float2(w.z, w.w), both(xj[i]), a1);
-            }
-          xj[4 * g] = a0.x, xj[4 * g + 1] = a0.y, xj[4 * g + 2] = a1.x, xj[4 * g + 3] = a1.y;
-        }
-      }
       const float eC = fac[kSeC];
       if constexpr (back) {  // e^{G_C} dH' + (scale e^G dO)^T Q
         ok = mbar_wait(&bars[bQ], t & 1, abort_flag, err, 2u) && ok;
@@ -1164,40 +1024,19 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
           }
         }
       }
-      // 3. u = X - (beta X) S^T, E = Y - (beta Y) S, by k-block
+      // 3. u = X - (beta X) S^T, E = Y - (beta Y) S
       ok = mbar_wait(&bars[bS], t & 1, abort_flag, err, 2u) && ok;
       tc_fence_after();
       {
-        // rows `row` .. of this thread's x from k-block j
-        auto add = [&](int j, int row, const auto& y) {
-          const float inv = inv_x[128 * j + dv];
-          const float* out = fac + s_out(back, j, 32 * hh + row);
+        float y0[32], y1[32];
+        tmem_ld32(tl + kTX0 + 32 * hh, y0);
+        tmem_ld32(tl + kTX1 + 32 * hh, y1);
+        tmem_ld_wait();
 #pragma unroll
-          for (int r = 0; r < int(sizeof(y) / sizeof(float)); r += 2) {
-            const float2 f = mul2(both(inv), *reinterpret_cast<const float2*>(out + r));
-            const float2 d = fma2(make_float2(y[r], y[r + 1]), f,
-                                  make_float2(x[row + r], x[row + r + 1]));
-            x[row + r] = d.x, x[row + r + 1] = d.y;
-          }
-        };
-        float y0[32], y1[32], y2[16];
-        if (back ? hh == 0 : hh == 1) {
-          tmem_ld32(tl + (back ? kTX1 : kTX0 + 32), y0);
-          tmem_ld32(tl + (back ? kTH1 : kTX1 + 16), y1);
-          tmem_ld_wait();
-          add(back ? 1 : 0, 0, y0);
-          tmem_ld32(tl + (back ? kTH1 + 64 : kTH1), y0);
-          tmem_ld16(tl + (back ? kTX0 : kTH1 + 32), y2);
-          add(back ? 2 : 1, 0, y1);
-          tmem_ld_wait();
-          add(back ? 3 : 2, 0, y0);
-          add(back ? 0 : 3, back ? 0 : 16, y2);
-        } else {
-          tmem_ld32(tl + (back ? kTH1 + 96 : kTX0), y0);
-          tmem_ld16(tl + (back ? kTH1 + 32 : kTX1), y2);
-          tmem_ld_wait();
-          add(back ? 3 : 0, 0, y0);
-          add(back ? 2 : 1, back ? 0 : 16, y2);
+        for (int r = 0; r < 32; r += 2) {
+          const float2 d = add2(make_float2(x[r], x[r + 1]),
+                                add2(make_float2(y0[r], y0[r + 1]), make_float2(y1[r], y1[r + 1])));
+          x[r] = d.x, x[r + 1] = d.y;
         }
       }
       {
@@ -1210,7 +1049,7 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
         }
         const float s = pow2_scale(max_abs_of(w), &inv);
         inv_w[128 * hh + dv] = inv;
-        limbs_to_tmem(w, s, s, tl + kTA + 64 + 16 * hh, tl + kTA + 96 + 16 * hh);
+        limbs_to_tmem(w, s, tl + kTA + 64 + 16 * hh, tl + kTA + 96 + 16 * hh);
       }
       tc_fence_before();
       if (!named_all(1, kScanSync, ok)) break;
@@ -1310,8 +1149,8 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
       if (t >= 1) ok = mbar_wait(&bars[bSE], (t - 1) & 1, abort_flag, err, 4u);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&bars[bSF], 2 * kBlk);
-        bulk_load_g2s(smem + L::S, a.S + unit * 2 * kBlk, 2 * kBlk, &bars[bSF]);
+        mbar_arrive_expect_tx(&bars[bSF], 3 * kBlk);
+        bulk_load_g2s(smem + L::S, a.S + unit * 3 * kBlk, 3 * kBlk, &bars[bSF]);
       }
       ts = t;
     }
@@ -1328,6 +1167,7 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
     const uint64_t kmaj = make_sdesc_sw128(0, 16, 1024);    // K-major operands
     const uint64_t mnmaj = make_sdesc_sw128(0, 8192, 1024);  // MN-major, 64-element blocks apart
     constexpr uint32_t id_x = make_idesc_f16(128, 64, 0, 0);
+    constexpr uint32_t id_s = make_idesc_bf16(128, 64, 0, back ? 1 : 0);
     constexpr uint32_t id_h = make_idesc_f16(128, D, 0, 1);
     constexpr uint32_t id_q = make_idesc_f16(128, D, 1, 1);
     uint32_t b4 = base >> 4;
@@ -1373,18 +1213,16 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
       if (leader) {
         tc_fence_after();
         const uint32_t s4 = b4 + (L::S >> 4);
-        // By k-block j, in sums of their own: the rows from it on, or (the tile being read along
-        // its columns, whole) those of all blocks, of which the ones up to it count.
-        // (x low) S high, (x high) S low, (x high) S high
+        // limb pairs from the smallest on, without those below 2^-24; the rows' halves apart
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
+        for (int q = 0; q < 6; ++q)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t to = j == 0 ? kTX0 : j == 1 ? kTX1 : j == 2 ? kTH1 : kTH1 + (back ? 64 : 32);
-            const uint32_t at = s4 + (q == 1 ? kBlk >> 4 : 0);
-            mma_bf16_ts(tmem + to, tmem + kTA + (q == 0 ? 32 : 0) + 8 * j,
-                        back ? mnmaj + (at + 128 * j) : kmaj + (at + 128 * j + 2 * j),
-                        make_idesc_f16(128, back ? 64 : 64 - 16 * j, 0, back ? 1 : 0), q != 0);
+          for (int kk = 0; kk < 4; ++kk) {
+            const int lx = q == 0 ? 2 : q == 2 || q == 3 ? 1 : 0, ls = q == 1 ? 2 : q == 2 || q == 4 ? 1 : 0;
+            const uint32_t at = s4 + ls * (kBlk >> 4);
+            mma_bf16_ts(tmem + (kk >> 1 ? kTX1 : kTX0), tmem + kTA + 32 * lx + 8 * kk,
+                        back ? mnmaj + (at + 128 * kk) : kmaj + (at + 2 * kk), id_s,
+                        q != 0 || (kk & 1) != 0);
           }
         mma_commit(&bars[bS]);
         mma_commit(&bars[bSE]);
@@ -1475,7 +1313,7 @@ struct GradsSmem {
   static constexpr int Fac = NH + kBlk;          // two buffers of the unit's factors
   static constexpr int G = Fac + 2 * kFac * 4;   // two buffers of the cumulative gates
   static constexpr int F = G + 2 * kBC * 8;      // floats from here
-  static constexpr int kFloats = 5 * kBC + 12 * kBC + kBC + 40;
+  static constexpr int kFloats = 4 * kBC + 12 * kBC + kBC + 40;
   static constexpr int Bars = F + kFloats * 4;
   static constexpr int kUsed = Bars + 16 * 8 + 16 + 1024;
   // More than half of an SM's: all of its tensor memory goes to one CTA.
@@ -1551,10 +1389,9 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
   const uint32_t tmem = *tmem_slot;
   float* invU2 = reinterpret_cast<float*>(smem + L::F);  // [2][64], by the head's parity
   float* invE2 = invU2 + 2 * kBC;   // [2][64]
-  float* endU = invE2 + 2 * kBC;    // invU e^{G_b - G}
   // for dg, of the 32 rows d_k or t of each warp: a_t and b_s, W's sums over t with s before the
   // column; [2][32] W of P's and N's rows 32 .. summed over the columns before 32
-  float *part_a = endU + kBC, *part_b = part_a + 4 * kBC, *part_w = part_b + 4 * kBC;
+  float *part_a = invE2 + 2 * kBC, *part_b = part_a + 4 * kBC, *part_w = part_b + 4 * kBC;
   float* row_w = part_w + 4 * kBC;
   // by the head's number: [4][8] <H, dH'>, [2][2] 1 / scale of H, dH'
   float* red = row_w + kBC;
@@ -1627,16 +1464,18 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
 #pragma unroll
               for (int k = 0; k < 16; ++k)
                 x[16 * cb + k] = k < last
-                    ? x[16 * cb + k] * (expdiff(Gr, Gs[s0 + k]) * invU[s0 + k] * fr) : 0.f;
+                    ? x[16 * cb + k] * invU[s0 + k] * (expdiff(Gr, Gs[s0 + k]) * fr) : 0.f;
             } else {
 #pragma unroll
               for (int k = 0; k < 16; k += 4) {
-                const float4 e4 = *reinterpret_cast<const float4*>(endU + s0 + k);
+                // (the decay's two factors first: either of them may be out of range with 1 / scale)
+                const float4 e4 = *reinterpret_cast<const float4*>(fac + kFend + s0 + k);
+                const float4 u4 = *reinterpret_cast<const float4*>(invU + s0 + k);
                 float* y = x + 16 * cb + k;
-                y[0] = k < last ? y[0] * (fe * e4.x) : 0.f;
-                y[1] = k + 1 < last ? y[1] * (fe * e4.y) : 0.f;
-                y[2] = k + 2 < last ? y[2] * (fe * e4.z) : 0.f;
-                y[3] = k + 3 < last ? y[3] * (fe * e4.w) : 0.f;
+                y[0] = k < last ? y[0] * u4.x * (fe * e4.x) : 0.f;
+                y[1] = k + 1 < last ? y[1] * u4.y * (fe * e4.y) : 0.f;
+                y[2] = k + 2 < last ? y[2] * u4.z * (fe * e4.z) : 0.f;
+                y[3] = k + 3 < last ? y[3] * u4.w * (fe * e4.w) : 0.f;
               }
             }
           }
@@ -1691,8 +1530,8 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           for (int k = 0; k < 16; ++k) {
             const int r = s0 + k;
             const float eg = fac[kFeG + r] * ih;
-            const float dq = x0[k] * (eg * fac[kFo + r]), dkh = x1[k] * (eg * invE[r]);
-            const float dkd = x2[k] * (fac[kFeT + r] * (invU[r] * id));
+            const float dq = x0[k] * fac[kFo + r] * eg, dkh = x1[k] * invE[r] * eg;
+            const float dkd = x2[k] * invU[r] * (fac[kFeT + r] * id);
             dqs[16 * cb + k] += dq;
             dks[16 * cb + k] += dkd - dkh;
             float qv = 0.f, kv = 0.f;
@@ -1763,7 +1602,6 @@ __global__ void __launch_bounds__(kGradsThreads, 1) bwd_grads_kernel(BwdArgs a) 
           if (l8 == 0) {
             if (r < c.rows) a.dbeta[size_t(c.row0 + r) * a.H_v + n] = db;
             invU2[kBC * (n & 1) + r] = iu, invE2[kBC * (n & 1) + r] = ie;
-            endU[r] = iu * fan[kFend + r];
           }
           uint16_t* dv = a.dv + (size_t(c.row0 + r) * a.H_v + n) * D + 4 * l8;
 #pragma unroll
@@ -2150,7 +1988,7 @@ size_t layout(BwdArgs* a, char* base, int total_tokens, int num_seqs, int H_k, i
   a->KQ = reinterpret_cast<uint8_t*>(take(mc * H_k * 2 * tile));
   a->O = reinterpret_cast<uint8_t*>(take(units * tile));
   a->GO = reinterpret_cast<uint8_t*>(take(units * 2 * tile));
-  a->S = reinterpret_cast<uint8_t*>(take(units * 2 * kBlk));
+  a->S = reinterpret_cast<uint8_t*>(take(units * 3 * kBlk));
   a->Y0 = reinterpret_cast<float*>(take(units * kBC * D * 4));
   a->fac = reinterpret_cast<float*>(take(units * kFac * 4));
   a->ff = reinterpret_cast<float*>(take(units * kFwdFac * 4));

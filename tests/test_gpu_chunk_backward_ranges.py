@@ -279,3 +279,33 @@ def test_a_sequence_in_two_parts(cut):
         x = a if name == "dh0" else torch.cat([a, b])
         # (a part's h0 and dhT are rounded to f32 once more: 2^-24 each)
         assert R.rel(x, y) <= (R.BF16_REL if name in NAMES[:3] else 0) + R.F32_REL, name
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gates, keys, what", [(0.0, 0, "values"), (-0.1, 0, "values"),
+                                               (-3.0, -10, "values"), (0.0, 2, "queries")])
+def test_rows_that_data_sets_apart(what, gates, keys, d):
+    """Ordinary gates, but most rows have no value (the rows behind the last one that has live on
+    what decays left of it) or hardly any query: a 16-row block holds rows 2^-35 and less of its
+    largest, and each keeps its own accuracy.  (dbeta: the product of two vectors that may cancel
+    to a hundredth.)"""
+    lens = [128, 65]
+    rows, do, _, _ = _case(lens, 2, 2, d, seed=14)
+    rows[3] += gates
+    rows[1] = rows[1] * 2.0 ** keys
+    rows[4] = rows[4] * 2.0 ** (-2 * max(0, keys))
+    if what == "values":
+        rows[2][6:54] = rows[2][58:99] = rows[2][130:] = 0
+        if keys == 0:
+            rows[2][6:99] = 0
+    else:
+        rows[0][[62, 126, 127, 189, 190, 191, 192]] *= 2.0 ** -35
+    dev = [x.to(DEV) for x in rows]
+    cu = torch.tensor(R.offsets(lens), dtype=torch.int32, device=DEV)
+    got = gdn_chunk_backward(*dev, cu, do.to(DEV))
+    want = R.backward(*dev, lens, do.to(DEV))
+    for name, x, y in zip(NAMES[:5], got, want):
+        keep = y.double().flatten(1).norm(dim=1) > 1e-28  # (what f32 has digits for on the way there)
+        tol = R.BF16_REL + 8 * R.F32_REL if name in NAMES[:3] else 100 * R.F32_REL
+        if name != "dg":
+            assert _row_errors(x[keep], y[keep]) <= tol, name
