@@ -922,18 +922,22 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
     const int slice = 2 * (warp & 3);
     uint8_t* run = smem + L::St + slice * L::kStep + hh * L::kRun;
     float* out_st = reinterpret_cast<float*>(run + (lane >> 4) * L::kStep) + (lane & 15);
-    auto send_state = [&](float* to) {
-      if (lane == 0) tma_store_wait_read<0>();  // what the warp sent last
-      __syncwarp();
+    // In two halves of the rows d_k, while products 1 and 2 run.
+    auto send_state = [&](float* to, int half) {
+      if (half == 0) {
+        if (lane == 0) tma_store_wait_read<0>();  // what the warp sent last
+        __syncwarp();
+      }
       if (on) {
 #pragma unroll
-        for (int x = 0; x < NK; ++x) out_st[x * 16] = st[x];
+        for (int x = 0; x < NK / 2; ++x) out_st[(half * NK / 2 + x) * 16] = st[half * NK / 2 + x];
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          float* p = to + slice * D * 16 + hh * NK * 16;
-          bulk_store_s2g(p, run, L::kRun);
-          bulk_store_s2g(p + D * 16, run + L::kStep, L::kRun);
+          float* p = to + slice * D * 16 + (hh * NK + half * NK / 2) * 16;
+          const uint8_t* from = run + half * L::kRun / 2;
+          bulk_store_s2g(p, from, L::kRun / 2);
+          bulk_store_s2g(p + D * 16, from + L::kStep, L::kRun / 2);
           tma_store_commit();
         }
       }
@@ -955,7 +959,7 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
       tc_fence_before();
       if (!named_all(1, kScanSync, ok)) break;
       {
-        send_state((back ? a.dH : a.H) + unit * D * D);
+        send_state((back ? a.dH : a.H) + unit * D * D, 0);
         const float wm = warp_max(on ? most : 0.f);
         if (lane == 0) a.Hmax[(unit * 2 + back) * 8 + warp] = wm;
       }
@@ -1006,6 +1010,7 @@ __device__ __forceinline__ void scan(const BwdArgs& a, int at) {
       tc_fence_before();
       if (!named_all(1, kScanSync, ok)) break;
       if (tid == 0) mbar_arrive(&bars[bYE]);
+      send_state((back ? a.dH : a.H) + unit * D * D, 1);
       const float eC = fac[kSeC];
       if constexpr (back) {  // e^{G_C} dH' + (scale e^G dO)^T Q
         ok = mbar_wait(&bars[bQ], t & 1, abort_flag, err, 2u) && ok;
