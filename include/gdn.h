@@ -413,7 +413,7 @@ int gdn_state_tables(const int32_t* lens, const int32_t* slots, int num_seqs, fl
  * chunk states are recomputed here, to f32 accuracy.  dg, dbeta and dh0 are
  * the exact function's gradients to about 1e-6 relative, under strong decays
  * too; dq, dk and dv are rounded to bf16 once, from sums that are within 1e-5
- * of each row's own size.  No atomics in the sums: the same inputs give the
+ * of the size of each row's own terms.  No atomics in the sums: the same inputs give the
  * same bits.
  *
  *   q, k, v, g, beta, strides, cu_seqlens, num_seqs, total_tokens, h0, heads,
@@ -431,9 +431,9 @@ int gdn_state_tables(const int32_t* lens, const int32_t* slots, int num_seqs, fl
  *              its dhT
  *   workspace  >= gdn_chunk_backward_workspace_bytes() bytes, 256-byte aligned,
  *              no two calls in flight at once may share it.  It holds what the
- *              chunks of all heads need at once, about 315 KiB a chunk of 64 rows
+ *              chunks of all heads need at once, about 313 KiB a chunk of 64 rows
  *              and value head at d = 128, half of that at 64 (4576 tokens x 48
- *              heads: 1.03 GiB, 24,674 tokens: 5.6 GiB, 131,072 tokens: 29 GiB),
+ *              heads: 1.02 GiB, 24,674 tokens: 5.6 GiB, 131,072 tokens: 29 GiB),
  *              and nothing between calls.  A batch too large for it can be passed
  *              in parts: sequences do not depend on one another, and a long one
  *              can be cut at any row, last part first, with its state there as h0

@@ -34,9 +34,10 @@
 // 2^-40 of the largest value, whichever is coarser.  Only what enters the same sums
 // shares one: a row, a column, a state (a head's entry state or its gradient).  A row
 // of bf16 inputs is exact in one limb under its scale.  exact x f32 takes 2 MMAs, f32 x f32 takes 3
-// (lo x lo is below the f32 rounding).  Where no scale would do (M, P and N, whose
-// elements decays set apart along rows and columns) the limbs are bf16, three of them for M,
-// two for P and N, which reach only dq and dk, rounded to bf16 themselves (2^-17 against 2^-9).
+// (lo x lo is below the f32 rounding).  Where no scale would do (S, M, P and N, whose elements
+// decays set apart along rows and columns, and what S is multiplied with) the limbs are bf16: three
+// of them, f32's own 24 bits, six MMAs with another such operand; two for P and N, which reach only
+// dq and dk, rounded to bf16 themselves (2^-17 of a row's terms against 2^-9 of the row).
 //
 // The scans and the gradients run on tcgen05; the first kernel, whose products are
 // small and triangular, on warp-level MMAs.
@@ -298,8 +299,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 //   S_bj = (I + L_b)^-1 (B_bj - sum over j <= c < b of B_bc (diag(beta) S)_cj).
 // The four inverses are solved side by side in f32 on the CUDA cores (a thread a
 // column); the block products are TF32 MMAs in two limbs each (22 bits).  Bound
-// by latency and the writes; two CTAs an SM hide some of it (three spill).  164 us at 4576
-// rows, 16 key and 48 value heads, d = 128: 0.42 GB written.
+// by latency and the writes; two CTAs an SM hide some of it (three spill).  160 us at 4576
+// rows, 16 key and 48 value heads, d = 128: 0.41 GB written.
 // ---------------------------------------------------------------------------
 
 // 64 x D bf16 rows (row stride in elements) and the tiles that are made of them.
@@ -769,7 +770,7 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
 
 // ---------------------------------------------------------------------------
 // Scans: one CTA per (sequence, value head, direction), both directions in one launch
-// (the backward one first): 304 us at 4576 rows, 48 heads, 4.2 us a chunk.
+// (the backward one first): 286 us at 4576 rows, 48 heads, 4.0 us a chunk.
 //
 // H^T [dv][dk] is held by 8 state warps, thread (dv, half of d_k), 64 f32
 // registers at D = 128.  Per chunk three products, M = 128 (dv), A from tensor
@@ -786,10 +787,10 @@ __global__ void __launch_bounds__(256, 2) bwd_prep_kernel(BwdArgs a, int heads) 
 // Low limbs are multiplied first: the f32 accumulator then rounds against small
 // sums while it holds them.  D = 64 runs the same code with half of the rows idle.
 //
-// Bound by the chain, about 8000 cycles a chunk: 16 + 12 + 8 MMAs (55 to 68 cycles each) take
-// 2300 of them, the state warps' 1400 instructions between them most of the rest (limbs 800,
-// the state on its way out 1500, X and its limbs 900, u or E and its limbs 1400), with three
-// hand-overs each way.
+// Bound by the chain, about 7800 cycles a chunk: 16 + 24 + 8 MMAs (about 58 cycles each) take
+// 2900 of them, what the state warps do between them (limbs of the state 800, X and its limbs
+// 900, u or E and its limbs 900, their way out 600, the new state 450) and the hand-overs, three
+// each way, the rest.  The state's way out (1400) runs beside the first two products.
 // ---------------------------------------------------------------------------
 
 constexpr int kScanThreads = 384;
@@ -1296,8 +1297,8 @@ cudaError_t take_err_backward(uint32_t* out) {
 //   warp 12: one thread loads dO and issues the MMAs; warp 13: dg; warps 14, 15: Q and K.
 // Between a head's products and sums the row warps stage the next head's rows, as soon as the
 // products that read the last ones are done, so that the slots are free again early.
-// 324 us at 4576 rows, 48 heads.  Bound by the latency of a head's steps, each of which waits for
-// another group's (issue slots 36 % used, tensor pipe 16 %, barriers and loads the stalls).  The
+// 336 us at 4576 rows, 48 heads.  Bound by the latency of a head's steps, each of which waits for
+// another group's (issue slots 36 % used, tensor pipe 15 %, barriers and loads the stalls).  The
 // states' values come to the slots by bulk copies and become limbs in place: with loads through
 // registers, two batches in flight, the call took 55 us more.
 // ---------------------------------------------------------------------------
