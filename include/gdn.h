@@ -412,9 +412,10 @@ int gdn_state_tables(const int32_t* lens, const int32_t* slots, int num_seqs, fl
  * the gradients of every input.  Nothing of the forward call is kept: the
  * chunk states are recomputed here, to f32 accuracy.  dg, dbeta and dh0 are
  * the exact function's gradients to about 1e-6 relative, under strong decays
- * too (a recurrence that grows, beta |k|^2 far above 2, multiplies that); dq, dk and dv are rounded to bf16 once, from sums that are within 1e-5
- * of the size of each row's own terms.  No atomics in the sums: the same inputs give the
- * same bits.
+ * too (a recurrence that grows, beta |k|^2 far above 2, multiplies that); dq,
+ * dk and dv are rounded to bf16 once, from sums that are within 1e-5 of the
+ * size of each row's own terms.  No atomics in the sums: the same inputs give
+ * the same bits.
  *
  *   q, k, v, g, beta, strides, cu_seqlens, num_seqs, total_tokens, h0, heads,
  *   scale      as for gdn_chunk_prefill (h0 NULL = zeros); the same bound on
